@@ -191,8 +191,8 @@ def _prepare_plan(c, seed):
          "slots": torch.zeros(T, dtype=torch.int32, device=DEV), "taken": torch.zeros(c["B"], dtype=torch.int32, device=DEV)}
     if own:
         from barrier_free_message_gb300 import sfar
-        one = torch.zeros((2, pool, 1, P, 64), dtype=F8, device=DEV)
-        s["kv"] = sfar.SfarKv(one, one, *[torch.ones((2, pool, 1), device=DEV) for _ in range(2)], q_heads=1)
+        caches = [torch.zeros((2, pool, 1, P, 64), dtype=F8, device=DEV) for _ in range(2)]
+        s["kv"] = sfar.SfarKv(*caches, *[torch.ones((2, pool, 1), device=DEV) for _ in range(2)], q_heads=1)
     return s
 
 
