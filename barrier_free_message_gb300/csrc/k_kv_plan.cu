@@ -1,0 +1,242 @@
+// k_kv_plan.cu -- block tables, slot map and token offsets of a step, built on
+// the GPU from the requests' lengths.
+//
+// Request b goes from len to len' = max(0, len + delta) tokens and so from
+// have = ceil(len / P) to want = ceil(len' / P) pages.  Three exclusive sums
+// over the requests place everything: of the pages that are lacking (where in
+// the ring of free pages a request's begin), of the pages given back (where
+// behind the free ones they go) and of the new tokens (the rows of the step).
+// Free pages leave the ring at its head and return behind its tail, so what
+// is read and what is written never meet, in whatever order the CTAs work.
+//
+// Latency-bound: a few KB.  One launch of one cluster; every CTA forms the
+// sums over all requests itself (they fit its shared memory), so that the
+// CTAs exchange nothing, and takes its share of the outputs.  The one cluster
+// barrier, between the reads of the lengths and the ring's state and the
+// writes of the new ones, lets both be updated in place.
+#include <cooperative_groups.h>
+
+#include "sfar_kv_args.h"
+#include "sfar_prims.cuh"
+#include "sfar_kv_device.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+constexpr int kThreads = SFAR_PLAN_THREADS, kWarps = kThreads / 32;
+
+struct Sums {
+    long long need, back, count;
+};
+
+__device__ __forceinline__ long long up(long long v, int shift) { return (v + (1ll << shift) - 1) >> shift; }
+
+// inclusive sums over the CTA; *total gets the CTA's
+__device__ __forceinline__ Sums block_scan(Sums v, Sums *total, Sums *warp_sums)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long a = __shfl_up_sync(SFAR_FULL, v.need, d), b = __shfl_up_sync(SFAR_FULL, v.back, d),
+                        c = __shfl_up_sync(SFAR_FULL, v.count, d);
+        if (lane >= d) {
+            v.need += a;
+            v.back += b;
+            v.count += c;
+        }
+    }
+    if (lane == 31)
+        warp_sums[warp] = v;
+    __syncthreads();
+    Sums before = {0, 0, 0}, all = {0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const Sums s = warp_sums[w];
+        if (w < warp) {
+            before.need += s.need;
+            before.back += s.back;
+            before.count += s.count;
+        }
+        all.need += s.need;
+        all.back += s.back;
+        all.count += s.count;
+    }
+    __syncthreads();
+    *total = all;
+    v.need += before.need;
+    v.back += before.back;
+    v.count += before.count;
+    return v;
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(SFAR_PLAN_THREADS) k_kv_plan(const __grid_constant__ SfarKvPlanArgs a)
+{
+    extern __shared__ int mem[];
+    int *s_start = mem;                     // [B + 1] first row of a request's new tokens, at most T
+    int *s_len = s_start + a.B + 1;         // [B] tokens held before
+    int *s_new = s_len + a.B;               // [B] tokens held after (before, if refused)
+    int *s_off = s_new + a.B;               // [B] ring offset of its pages taken or given back; -1 refused
+    __shared__ Sums warp_sums[kWarps];
+    __shared__ int s_used;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int shift = a.shift;
+    const int crank = blockIdx.x, csize = gridDim.x;
+    if (tid == 0)
+        s_used = 0;
+    pdl_wait();
+
+    int head = a.state[0], freec = a.state[1];
+    if (head < 0 || head >= a.pages || freec < 0 || freec > a.pages) {
+        if (tid == 0 && crank == 0)
+            sfar_kv_fault(a.ctl, 0, SFAR_KV_BAD_RING);
+        head = 0;
+        freec = 0;
+    }
+    const long long most = min((long long)a.W << shift, (long long)INT_MAX);
+    Sums carry = {0, 0, 0};
+    for (int base = 0; base < a.B; base += kThreads) {
+        const int i = base + tid;
+        long long len = 0, after = 0;
+        int d = 0;
+        Sums v = {0, 0, 0};
+        bool fits = true;
+        if (i < a.B) {
+            len = a.lens[i];
+            d = a.delta[i];
+            if (len < 0 || len > most) {
+                if (crank == 0)
+                    sfar_kv_fault(a.ctl, i, SFAR_KV_BAD_LENGTH);
+                len = len < 0 ? 0 : most;
+            }
+            after = max(0ll, len + d);
+            const long long have = up(len, shift), want = up(after, shift);
+            fits = after <= most;
+            v.need = d > 0 && fits ? want - have : 0;
+            v.back = d < 0 ? have - want : 0;
+            v.count = max(d, 0);
+        }
+        Sums all;
+        Sums t = block_scan(v, &all, warp_sums);
+        t.need += carry.need;
+        t.back += carry.back;
+        t.count += carry.count;
+        carry.need += all.need;
+        carry.back += all.back;
+        carry.count += all.count;
+        const bool ok = d <= 0 || (fits && (v.need == 0 || t.need <= freec));
+        const int upto = ok && v.need > 0 ? (int)t.need : 0;
+        const int best = __reduce_max_sync(SFAR_FULL, upto);
+        if (lane == 0 && best > 0)
+            atomicMax(&s_used, best);
+        if (i < a.B) {
+            s_start[i] = (int)min(t.count - v.count, (long long)a.T);
+            s_len[i] = (int)len;
+            s_new[i] = (int)(ok ? after : len);
+            s_off[i] = !ok ? -1 : v.need > 0 ? (int)(t.need - v.need) : (int)min(t.back - v.back, (long long)a.pages);
+        }
+    }
+    if (tid == 0) {
+        s_start[a.B] = (int)min(carry.count, (long long)a.T);
+        if (crank == 0 && carry.count > a.T)
+            sfar_kv_fault(a.ctl, a.B, SFAR_KV_BAD_TOKENS);
+    }
+    // every CTA has read the lengths and the state; from here on they may change
+    cg::this_cluster().sync();
+
+    const int used = s_used;
+    const unsigned pages = (unsigned)a.pages;
+    auto ring_at = [&](unsigned i) {       // the free page i places behind the head
+        unsigned p = (unsigned)head + i;
+        return p >= pages ? p - pages : p;
+    };
+    for (int i = crank * kThreads + tid; i < a.B; i += csize * kThreads) {
+        a.lens_out[i] = s_new[i];
+        a.taken[i] = s_off[i] >= 0;
+        a.starts[i] = s_start[i];
+    }
+    if (crank == 0 && tid == 0) {
+        a.starts[a.B] = s_start[a.B];
+        long long left = (long long)freec - used + carry.back;
+        if (left > a.pages) {
+            sfar_kv_fault(a.ctl, 0, SFAR_KV_BAD_RING);
+            left = a.pages;
+        }
+        a.state_out[0] = (int)ring_at((unsigned)used);
+        a.state_out[1] = (int)left;
+    }
+    // table entries of new pages, ring entries of pages given back: a warp per request
+    for (int b = crank * kWarps + (tid >> 5); b < a.B; b += csize * kWarps) {
+        const int off = s_off[b];
+        if (off < 0)
+            continue;
+        const int have = (int)up(s_len[b], shift), want = (int)up(s_new[b], shift);
+        int *row = a.table + (size_t)b * a.W;
+        for (int j = have + lane; j < want; j += 32) {
+            int p = a.ring[ring_at((unsigned)(off + j - have))];
+            if ((unsigned)p >= pages) {
+                sfar_kv_fault(a.ctl, b, SFAR_KV_BAD_PAGE);
+                p = -1;
+            }
+            row[j] = p;
+        }
+        for (int j = want + lane; j < have; j += 32) {
+            const long long at = (long long)off + j - want;
+            if (at >= (long long)a.pages - freec)
+                continue;                   // more than the pool has: recorded above
+            const int p = row[j];
+            if ((unsigned)p >= pages)
+                sfar_kv_fault(a.ctl, b, SFAR_KV_BAD_PAGE);
+            unsigned to = (unsigned)head + (unsigned)freec;
+            to = (to >= pages ? to - pages : to) + (unsigned)at;
+            a.ring[to >= pages ? to - pages : to] = p;
+        }
+    }
+    // slots: a thread finds its first token's request and walks on from there
+    const int total = s_start[a.B];
+    for (long long t0 = 4ll * (crank * kThreads + tid); t0 < a.T; t0 += 4ll * csize * kThreads) {
+        int out[4];
+        int b = 0;
+        if (t0 < total) {
+            int lo = 0, hi = a.B;           // the last b with starts[b] <= t0
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (s_start[mid] <= t0)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            b = lo;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const long long t = t0 + e;
+            int slot = -1;
+            if (t < total) {
+                while (t >= s_start[b + 1])
+                    ++b;
+                const int off = s_off[b];
+                if (off >= 0) {
+                    const int len = s_len[b], pos = len + (int)(t - s_start[b]);
+                    const int j = pos >> shift, have = (int)up(len, shift);
+                    const int p = j < have ? a.table[(size_t)b * a.W + j] : a.ring[ring_at((unsigned)(off + j - have))];
+                    if ((unsigned)p < pages)
+                        slot = (p << shift) + (pos & ((1 << shift) - 1));
+                    else
+                        sfar_kv_fault(a.ctl, b, SFAR_KV_BAD_PAGE);
+                }
+            }
+            out[e] = slot;
+        }
+        if (t0 + 4 <= a.T && ((uintptr_t)a.slots & 15u) == 0) {
+            *reinterpret_cast<int4 *>(a.slots + t0) = make_int4(out[0], out[1], out[2], out[3]);
+        } else {
+            for (int e = 0; e < 4 && t0 + e < a.T; ++e)
+                a.slots[t0 + e] = out[e];
+        }
+    }
+}
+
+const void *sfar_kernel_kv_plan() { return (const void *)k_kv_plan; }

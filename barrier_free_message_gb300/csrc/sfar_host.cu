@@ -23,6 +23,7 @@
 #include "sfar_fused.h"
 #include "sfar_gemv.h"
 #include "sfar_internal.h"
+#include "sfar_kv_args.h"
 #include "sfar_test.h"
 
 namespace {
@@ -217,6 +218,10 @@ static sfar_status launch_knob(sfar *h, int which, unsigned long long value, con
     }
     return SFAR_OK;
 }
+
+SfarView sfar_view(const sfar *h) { return SfarView{h->R, h->dt, h->dev, h->sms, h->mode, h->ctl}; }
+
+void sfar_set_last_error(int status) { g_last_error = (sfar_status)status; }
 
 extern "C" {
 
@@ -1048,6 +1053,8 @@ static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
     }();
     return fn;
 }
+
+void *sfar_tensor_map_encoder() { return reinterpret_cast<void *>(tensor_map_encoder()); }
 
 sfar_status sfar_rowpar_gemv(sfar_t *h, const void *const x[], const void *const w[], void *const y[], size_t k,
                              size_t hidden, size_t prefetch_rows, sfar_stream_t s)

@@ -1,0 +1,76 @@
+// sfar_kv_args.h -- kernel parameters of the paged 8-bit cache's operators and of
+// the 8-bit projection.
+#pragma once
+#include <cuda.h>
+
+#include "sfar_internal.h"
+
+// What the translation units beside the AllReduce's need of a handle.
+struct SfarView {
+    int R, dt, dev, sms, mode;
+    SfarCtl *ctl;
+};
+struct sfar;
+SfarView sfar_view(const sfar *h);
+// sets what sfar_last_error reports
+void sfar_set_last_error(int status);
+// The driver's cuTensorMapEncodeTiled (PFN_cuTensorMapEncodeTiled_v12000), or NULL.
+extern "C" void *sfar_tensor_map_encoder();
+
+struct SfarKvPlanArgs {
+    const int *lens, *delta;
+    int *table, *ring;
+    const int *state;
+    int *lens_out, *state_out, *starts, *slots, *taken;
+    SfarCtl *ctl;
+    int B, W, T, shift, pages;      // requests, table width, token rows, log2 page_tokens, pool
+};
+
+struct SfarKvAppendArgs {
+    const uint16_t *x[2][SFAR_MAX_R];       // new keys, values
+    uint8_t *cache[2][SFAR_MAX_R];
+    float *scale[2][SFAR_MAX_R];
+    const int *slots;
+    SfarCtl *ctl;
+    long long ts[2], hs[2];                 // strides of a token and of a head, elements
+    int T, H, R, shift, pages, window;      // window: tokens per CTA
+};
+
+struct SfarAttnArgs {
+    const uint8_t *k[SFAR_MAX_R], *v[SFAR_MAX_R];
+    const float *ks[SFAR_MAX_R], *vs[SFAR_MAX_R];
+    const uint16_t *q[SFAR_MAX_R];
+    uint16_t *out[SFAR_MAX_R];
+    const int *table, *lens, *starts;
+    SfarCtl *ctl;
+    long long qts, qhs, ots, ohs;
+    float scale;
+    int R, B, W, T, Hq, Hk, G, shift, pages, window;
+};
+
+struct SfarQuantArgs {
+    const uint16_t *x[SFAR_MAX_R];
+    uint8_t *x8[SFAR_MAX_R];
+    float *sx[SFAR_MAX_R];
+    long long m, k, ldx, ldx8;
+    int R, kb, vec;                         // vec: 16-byte loads and 8-byte stores are aligned
+};
+
+struct SfarGemm8Args {
+    const uint8_t *x8[SFAR_MAX_R], *w8[SFAR_MAX_R];
+    const float *sx[SFAR_MAX_R], *sw[SFAR_MAX_R];
+    uint16_t *y[SFAR_MAX_R];
+    SfarCtl *ctl;
+    long long m, k, n, ldx, ldw;
+    int R;
+};
+
+const void *sfar_kernel_kv_plan();
+const void *sfar_kernel_kv_append(int head_dim);
+const void *sfar_kernel_kv_attn(int head_dim);
+const void *sfar_kernel_quantize();
+const void *sfar_kernel_gemm8();
+
+#define SFAR_PLAN_THREADS 512
+#define SFAR_PLAN_CLUSTER 8
+#define SFAR_APPEND_WARPS 8

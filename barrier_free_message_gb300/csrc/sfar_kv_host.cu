@@ -1,0 +1,418 @@
+// sfar_kv_host.cu -- the C ABI of the paged 8-bit cache (include/sfar_kv.h)
+// and of the 8-bit projection (include/sfar_fp8.h): arguments, handle, launch.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <string.h>
+
+#include <new>
+
+#include "sfar.h"
+#include "sfar_fp8.h"
+#include "sfar_kv.h"
+#include "sfar_kv_args.h"
+#include "sfar_test.h"
+
+struct sfar_kv {
+    int R = 0, Hq = 0, Hk = 0, D = 0, P = 0, shift = 0;
+    size_t pages = 0;
+    int dev = 0, sms = 0;
+    void *cache[2][SFAR_MAX_R] = {};
+    float *scale[2][SFAR_MAX_R] = {};
+    uint8_t *ws = nullptr;
+    SfarCtl *ctl = nullptr;             // at the start of ws
+    SfarCtl *host_ctl = nullptr;
+    cudaStream_t priv = nullptr;
+};
+
+namespace {
+
+size_t ceil_div(size_t x, size_t a) { return (x + a - 1) / a; }
+bool aligned(const void *p, uintptr_t a) { return p && ((uintptr_t)p & (a - 1)) == 0; }
+
+struct Span {
+    uintptr_t lo, hi;
+    Span(const void *p, size_t bytes) : lo((uintptr_t)p), hi((uintptr_t)p + bytes) {}
+    bool meets(const Span &o) const { return lo < o.hi && o.lo < hi; }
+};
+
+// Launches f as a programmatic dependent of the kernel before it on the
+// stream (every kernel here begins with griddepcontrol.wait); plain: without.
+sfar_status launch(int dev, const void *f, dim3 grid, unsigned threads, size_t smem, void *args, sfar_stream_t s, bool plain = false,
+                   unsigned cluster = 1)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = (cudaStream_t)s;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (!plain) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = cluster;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    void *params[] = {args};
+    int cur = -1;
+    cudaGetDevice(&cur);
+    if (cur != dev)
+        cudaSetDevice(dev);
+    const cudaError_t err = cudaLaunchKernelExC(&cfg, f, params);
+    if (cur != dev && cur >= 0)
+        cudaSetDevice(cur);
+    if (err != cudaSuccess) {
+        cudaGetLastError();
+        return SFAR_ERR_CUDA;
+    }
+    return SFAR_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+sfar_kv_t *sfar_kv_create(int R, int q_heads, int kv_heads, int head_dim, int page_tokens, size_t pages,
+                          void *const k_cache[], void *const v_cache[], float *const k_scale[],
+                          float *const v_scale[])
+{
+    auto fail = [](sfar_status st) {
+        sfar_set_last_error(st);
+        return (sfar_kv_t *)nullptr;
+    };
+    if (R < 1 || R > SFAR_MAX_R || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads || q_heads > 65535 ||
+        (head_dim != 64 && head_dim != 128) ||
+        (page_tokens != 16 && page_tokens != 32 && page_tokens != 64 && page_tokens != 128) || pages == 0 ||
+        pages >= (1ull << 31) / (size_t)page_tokens || pages >= (1ull << 31) / (size_t)kv_heads || !k_cache || !v_cache ||
+        !k_scale || !v_scale)
+        return fail(SFAR_ERR_INVALID);
+    const size_t cbytes = pages * (size_t)kv_heads * (size_t)page_tokens * (size_t)head_dim;
+    const size_t sbytes = pages * (size_t)kv_heads * sizeof(float);
+    for (int i = 0; i < 4 * R; ++i) {
+        auto span = [&](int j) {
+            const int r = j >> 2;
+            return j & 2 ? Span(j & 1 ? v_scale[r] : k_scale[r], sbytes) : Span(j & 1 ? v_cache[r] : k_cache[r], cbytes);
+        };
+        if (!aligned((const void *)span(i).lo, i & 2 ? 4 : 16))
+            return fail(SFAR_ERR_INVALID);
+        for (int j = 0; j < i; ++j)
+            if (span(i).meets(span(j)))
+                return fail(SFAR_ERR_INVALID);
+    }
+    int dev = 0, major = 0, minor = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return fail(SFAR_ERR_CUDA);
+    }
+    if (major != 10 || minor != 3)
+        return fail(SFAR_ERR_UNSUPPORTED);
+    sfar_kv *h = new (std::nothrow) sfar_kv();
+    if (!h)
+        return fail(SFAR_ERR_OOM);
+    h->R = R;
+    h->Hq = q_heads;
+    h->Hk = kv_heads;
+    h->D = head_dim;
+    h->P = page_tokens;
+    h->shift = page_tokens == 16 ? 4 : page_tokens == 32 ? 5 : page_tokens == 64 ? 6 : 7;
+    h->pages = pages;
+    h->dev = dev;
+    h->sms = sms;
+    for (int r = 0; r < R; ++r) {
+        h->cache[0][r] = k_cache[r];
+        h->cache[1][r] = v_cache[r];
+        h->scale[0][r] = k_scale[r];
+        h->scale[1][r] = v_scale[r];
+    }
+    if (cudaMalloc(&h->ws, 256) != cudaSuccess) {
+        cudaGetLastError();
+        delete h;
+        return fail(SFAR_ERR_OOM);
+    }
+    h->ctl = reinterpret_cast<SfarCtl *>(h->ws);
+    SfarCtl init;
+    memset(&init, 0, sizeof init);
+    init.timeout_ns = 1000000000ull;
+    init.strag_rank = init.drop_rank = -1;
+    init.f_rank = init.f_cta = init.f_peer = -1;
+    if (cudaMemcpy(h->ctl, &init, sizeof init, cudaMemcpyHostToDevice) != cudaSuccess ||
+        cudaStreamCreateWithFlags(&h->priv, cudaStreamNonBlocking) != cudaSuccess ||
+        cudaMallocHost(&h->host_ctl, sizeof(SfarCtl)) != cudaSuccess ||
+        cudaFuncSetAttribute(sfar_kernel_kv_plan(), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (4 * SFAR_KV_MAX_REQUESTS + 1) * 4) != cudaSuccess) {
+        cudaGetLastError();
+        sfar_kv_destroy(h);
+        return fail(SFAR_ERR_CUDA);
+    }
+    sfar_set_last_error(SFAR_OK);
+    return h;
+}
+
+void sfar_kv_destroy(sfar_kv_t *h)
+{
+    if (!h)
+        return;
+    int cur = -1;
+    cudaGetDevice(&cur);
+    if (cur != h->dev)
+        cudaSetDevice(h->dev);
+    if (h->priv)
+        cudaStreamDestroy(h->priv);
+    if (h->host_ctl)
+        cudaFreeHost(h->host_ctl);
+    if (h->ws)
+        cudaFree(h->ws);
+    if (cur != h->dev && cur >= 0)
+        cudaSetDevice(cur);
+    cudaGetLastError();
+    delete h;
+}
+
+sfar_status sfar_kv_plan(sfar_kv_t *h, const int32_t *lens, const int32_t *delta, int32_t *table, int32_t *ring,
+                         const int32_t *state, int32_t *lens_out, int32_t *state_out, int32_t *starts, int32_t *slots,
+                         int32_t *taken, size_t requests, size_t table_width, size_t tokens, sfar_stream_t s)
+{
+    if (!h || requests == 0 || requests > SFAR_KV_MAX_REQUESTS || table_width == 0 || table_width >= (1ull << 31) ||
+        tokens >= (1ull << 31) || (tokens && !aligned(slots, 4)))
+        return SFAR_ERR_INVALID;
+    const Span spans[] = {Span(lens, requests * 4), Span(delta, requests * 4), Span(table, requests * table_width * 4),
+                          Span(ring, h->pages * 4), Span(state, 8), Span(lens_out, requests * 4), Span(state_out, 8),
+                          Span(starts, requests * 4 + 4), Span(slots, tokens * 4), Span(taken, requests * 4)};
+    const int n = (int)(sizeof spans / sizeof spans[0]);
+    for (int i = 0; i < n; ++i) {
+        if (i != 8 && !aligned((const void *)spans[i].lo, 4))
+            return SFAR_ERR_INVALID;
+        for (int j = 0; j < i; ++j)
+            if (spans[i].meets(spans[j]) && !((i == 5 && j == 0) || (i == 6 && j == 4)))
+                return SFAR_ERR_INVALID;
+    }
+    if ((lens_out != lens && spans[5].meets(spans[0])) || (state_out != state && spans[6].meets(spans[4])))
+        return SFAR_ERR_INVALID;
+    SfarKvPlanArgs a{lens,  delta, table,  ring,          state,            lens_out,    state_out, starts,
+                     slots, taken, h->ctl, (int)requests, (int)table_width, (int)tokens, h->shift,  (int)h->pages};
+    return launch(h->dev, sfar_kernel_kv_plan(), dim3(SFAR_PLAN_CLUSTER), SFAR_PLAN_THREADS, (4 * requests + 1) * 4, &a, s,
+                  false, SFAR_PLAN_CLUSTER);
+}
+
+sfar_status sfar_kv_append(sfar_kv_t *h, const void *const k[], const void *const v[], const int32_t *slots,
+                           size_t tokens, size_t k_token_stride, size_t k_head_stride, size_t v_token_stride,
+                           size_t v_head_stride, sfar_stream_t s)
+{
+    if (!h || !k || !v || tokens >= (1ull << 31) || (tokens && !aligned(slots, 4)) || k_token_stride % 8 ||
+        k_head_stride % 8 || v_token_stride % 8 || v_head_stride % 8)
+        return SFAR_ERR_INVALID;
+    SfarKvAppendArgs a;
+    memset(&a, 0, sizeof a);
+    for (int r = 0; r < h->R; ++r) {
+        if (tokens && (!aligned(k[r], 16) || !aligned(v[r], 16)))
+            return SFAR_ERR_INVALID;
+        a.x[0][r] = static_cast<const uint16_t *>(k[r]);
+        a.x[1][r] = static_cast<const uint16_t *>(v[r]);
+        for (int i = 0; i < 2; ++i) {
+            a.cache[i][r] = static_cast<uint8_t *>(h->cache[i][r]);
+            a.scale[i][r] = h->scale[i][r];
+        }
+    }
+    if (tokens == 0)
+        return SFAR_OK;
+    a.slots = slots;
+    a.ctl = h->ctl;
+    a.ts[0] = (long long)k_token_stride;
+    a.hs[0] = (long long)k_head_stride;
+    a.ts[1] = (long long)v_token_stride;
+    a.hs[1] = (long long)v_head_stride;
+    a.T = (int)tokens;
+    a.H = h->Hk;
+    a.R = h->R;
+    a.shift = h->shift;
+    a.pages = (int)h->pages;
+    // tokens per CTA: one while the grid is below four CTAs per SM, doubling from there
+    const size_t groups = ceil_div(2 * (size_t)h->R * (size_t)h->Hk, SFAR_APPEND_WARPS);
+    a.window = 1;
+    while (a.window < 32 && ceil_div(tokens, (size_t)a.window) * groups > 4 * (size_t)h->sms)
+        a.window *= 2;
+    if (groups > 65535)
+        return SFAR_ERR_INVALID;
+    return launch(h->dev, sfar_kernel_kv_append(h->D), dim3((unsigned)ceil_div(tokens, (size_t)a.window), (unsigned)groups),
+                  32 * SFAR_APPEND_WARPS, 0, &a, s);
+}
+
+sfar_status sfar_kv_attention(sfar_kv_t *h, const void *const q[], void *const out[], const int32_t *table,
+                              const int32_t *lens, const int32_t *starts, size_t requests, size_t table_width,
+                              size_t tokens, size_t q_token_stride, size_t q_head_stride, size_t out_token_stride,
+                              size_t out_head_stride, size_t max_q, float scale, size_t window, sfar_stream_t s)
+{
+    if (!h || !q || !out || requests == 0 || requests > SFAR_KV_MAX_REQUESTS || table_width == 0 ||
+        table_width >= (1ull << 31) || tokens >= (1ull << 31) || !aligned(table, 4) || !aligned(lens, 4) ||
+        !aligned(starts, 4) || q_token_stride % 8 || q_head_stride % 8 || out_token_stride % 8 || out_head_stride % 8 ||
+        !(scale >= 0.f) || isinf(scale))
+        return SFAR_ERR_INVALID;
+    (void)max_q;
+    if (tokens == 0)
+        return SFAR_OK;
+    SfarAttnArgs a;
+    memset(&a, 0, sizeof a);
+    auto extent = [&](size_t ts, size_t hs) { return 2 * ((tokens - 1) * ts + (size_t)(h->Hq - 1) * hs + (size_t)h->D); };
+    const size_t qb = extent(q_token_stride, q_head_stride), ob = extent(out_token_stride, out_head_stride);
+    for (int r = 0; r < h->R; ++r) {
+        if (!aligned(q[r], 16) || !aligned(out[r], 16))
+            return SFAR_ERR_INVALID;
+        a.q[r] = static_cast<const uint16_t *>(q[r]);
+        a.out[r] = static_cast<uint16_t *>(out[r]);
+        a.k[r] = static_cast<const uint8_t *>(h->cache[0][r]);
+        a.v[r] = static_cast<const uint8_t *>(h->cache[1][r]);
+        a.ks[r] = h->scale[0][r];
+        a.vs[r] = h->scale[1][r];
+    }
+    for (int i = 0; i < h->R; ++i)
+        for (int j = 0; j < h->R; ++j)
+            if (Span(out[i], ob).meets(Span(q[j], qb)))
+                return SFAR_ERR_INVALID;
+    a.table = table;
+    a.lens = lens;
+    a.starts = starts;
+    a.ctl = h->ctl;
+    a.qts = (long long)q_token_stride;
+    a.qhs = (long long)q_head_stride;
+    a.ots = (long long)out_token_stride;
+    a.ohs = (long long)out_head_stride;
+    a.scale = scale;
+    a.R = h->R;
+    a.B = (int)requests;
+    a.W = (int)table_width;
+    a.T = (int)tokens;
+    a.Hq = h->Hq;
+    a.Hk = h->Hk;
+    a.G = h->Hq / h->Hk;
+    a.shift = h->shift;
+    a.pages = (int)h->pages;
+    a.window = window >= (1ull << 31) ? 0 : (int)window;
+    return launch(h->dev, sfar_kernel_kv_attn(h->D), dim3((unsigned)ceil_div(tokens * (size_t)h->Hq, 4), (unsigned)h->R), 128, 0,
+                  &a, s);
+}
+
+sfar_status sfar_kv_status_get(sfar_kv_t *h, sfar_fault *info)
+{
+    if (!h)
+        return SFAR_ERR_INVALID;
+    if (cudaMemcpyAsync(h->host_ctl, h->ctl, 32, cudaMemcpyDeviceToHost, h->priv) != cudaSuccess ||
+        cudaStreamSynchronize(h->priv) != cudaSuccess) {
+        cudaGetLastError();
+        return SFAR_ERR_CUDA;
+    }
+    const SfarCtl *c = h->host_ctl;
+    const sfar_status code = (sfar_status)c->status;
+    if (info) {
+        info->code = code;
+        info->rank = code ? c->f_rank : -1;
+        info->cta = code ? c->f_cta : -1;
+        info->peer = code ? c->f_peer : -1;
+        info->epoch = code ? c->f_epoch : 0;
+        info->where = code ? c->f_where : 0;
+    }
+    return code;
+}
+
+sfar_status sfar_kv_reset(sfar_kv_t *h, sfar_stream_t s)
+{
+    if (!h)
+        return SFAR_ERR_INVALID;
+    if (cudaMemsetAsync(h->ctl, 0, 32, (cudaStream_t)s) != cudaSuccess) {
+        cudaGetLastError();
+        return SFAR_ERR_CUDA;
+    }
+    return SFAR_OK;
+}
+
+// ---------------------------------------------------------- 8-bit projection
+sfar_status sfar_quantize_fp8(sfar_t *h, const void *const x[], void *const x8[], float *const sx[], size_t m,
+                              size_t k, size_t ldx, size_t ldx8, sfar_stream_t s)
+{
+    if (!h || !x || !x8 || !sx || m == 0 || k == 0 || m >= (1ull << 31) || k >= (1ull << 31) || ldx < k || ldx8 < k ||
+        ldx >= (1ull << 40) || ldx8 >= (1ull << 40))
+        return SFAR_ERR_INVALID;
+    const SfarView v = sfar_view(h);
+    if (v.dt != SFAR_BF16)
+        return SFAR_ERR_INVALID;
+    SfarQuantArgs a;
+    memset(&a, 0, sizeof a);
+    a.kb = (int)ceil_div(k, SFAR_FP8_BLOCK);
+    a.vec = ldx % 8 == 0 && ldx8 % 8 == 0;
+    const size_t xb = ((m - 1) * ldx + k) * 2, qb = (m - 1) * ldx8 + k, sb = (size_t)a.kb * m * 4;
+    for (int r = 0; r < v.R; ++r) {
+        if (!aligned(x[r], 2) || !x8[r] || !aligned(sx[r], 4))
+            return SFAR_ERR_INVALID;
+        a.vec = a.vec && aligned(x[r], 16) && aligned(x8[r], 8);
+        a.x[r] = static_cast<const uint16_t *>(x[r]);
+        a.x8[r] = static_cast<uint8_t *>(x8[r]);
+        a.sx[r] = sx[r];
+    }
+    for (int i = 0; i < v.R; ++i)
+        for (int j = 0; j < v.R; ++j) {
+            const Span q(x8[i], qb), sc(sx[i], sb), in(x[j], xb);
+            if (q.meets(in) || sc.meets(in) || q.meets(Span(sx[j], sb)) ||
+                (i < j && (q.meets(Span(x8[j], qb)) || sc.meets(Span(sx[j], sb)))))
+                return SFAR_ERR_INVALID;
+        }
+    a.m = (long long)m;
+    a.k = (long long)k;
+    a.ldx = (long long)ldx;
+    a.ldx8 = (long long)ldx8;
+    a.R = v.R;
+    const size_t ctas = ceil_div(m * ceil_div((size_t)a.kb, 2), 8), most = ceil_div(16 * (size_t)v.sms, (size_t)v.R);
+    return launch(v.dev, sfar_kernel_quantize(), dim3((unsigned)(ctas < most ? ctas : most), (unsigned)v.R), 256, 0, &a, s,
+                  v.mode == SFAR_LAUNCH_PLAIN);
+}
+
+sfar_status sfar_rowpar_gemm_fp8(sfar_t *h, const void *const x8[], const float *const sx[], const void *const w8[],
+                                 const float *const sw[], void *const y[], size_t m, size_t k, size_t hidden,
+                                 size_t ldx8, size_t ldw, sfar_stream_t s)
+{
+    if (!h || !x8 || !sx || !w8 || !sw || !y || m == 0 || k == 0 || hidden == 0 || m >= (1ull << 31) ||
+        k >= (1ull << 31) || hidden >= (1ull << 31) || ldx8 < k || ldw < k || ldx8 % 16 || ldw % 16 ||
+        ldx8 >= (1ull << 40) || ldw >= (1ull << 40))
+        return SFAR_ERR_INVALID;
+    const SfarView v = sfar_view(h);
+    if (v.dt != SFAR_BF16)
+        return SFAR_ERR_INVALID;
+    SfarGemm8Args a;
+    memset(&a, 0, sizeof a);
+    const size_t kb = ceil_div(k, SFAR_FP8_BLOCK), nb = ceil_div(hidden, SFAR_FP8_BLOCK);
+    const size_t xb = (m - 1) * ldx8 + k, wb = (hidden - 1) * ldw + k, yb = m * hidden * 2;
+    for (int r = 0; r < v.R; ++r) {
+        if (!aligned(x8[r], 16) || !aligned(w8[r], 16) || !aligned(sx[r], 4) || !aligned(sw[r], 4) || !aligned(y[r], 2))
+            return SFAR_ERR_INVALID;
+        a.x8[r] = static_cast<const uint8_t *>(x8[r]);
+        a.w8[r] = static_cast<const uint8_t *>(w8[r]);
+        a.sx[r] = sx[r];
+        a.sw[r] = sw[r];
+        a.y[r] = static_cast<uint16_t *>(y[r]);
+    }
+    for (int i = 0; i < v.R; ++i) {
+        const Span out(y[i], yb);
+        for (int j = 0; j < v.R; ++j)
+            if (out.meets(Span(x8[j], xb)) || out.meets(Span(w8[j], wb)) || out.meets(Span(sx[j], kb * m * 4)) ||
+                out.meets(Span(sw[j], nb * kb * 4)) || (i < j && out.meets(Span(y[j], yb))))
+                return SFAR_ERR_INVALID;
+    }
+    a.ctl = v.ctl;
+    a.m = (long long)m;
+    a.k = (long long)k;
+    a.n = (long long)hidden;
+    a.ldx = (long long)ldx8;
+    a.ldw = (long long)ldw;
+    a.R = v.R;
+    return launch(v.dev, sfar_kernel_gemm8(), dim3((unsigned)ceil_div(hidden, 64), (unsigned)ceil_div(m, 16), (unsigned)v.R), 256, 0,
+                  &a, s, v.mode == SFAR_LAUNCH_PLAIN);
+}
+
+}  // extern "C"

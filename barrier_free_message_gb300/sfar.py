@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libsfar (``include/sfar.h``, ``include/sfar_test.h``).
+"""Thin ctypes binding of libsfar (``include/sfar.h``, ``include/sfar_decode.h``,
+``include/sfar_kv.h``, ``include/sfar_fp8.h``, ``include/sfar_test.h``).
 
 Argument marshalling only: every step of the AllReduce runs in the library's
 CUDA kernels.  The functions keep the C names; pointers are plain integers
@@ -28,7 +29,8 @@ MODES = {"serial": SFAR_LAUNCH_SERIAL, "overlap": SFAR_LAUNCH_OVERLAP, "plain": 
          "cooperative": SFAR_LAUNCH_COOPERATIVE}
 WAIT_NAMES = {1: "done", 2: "ll", 3: "sentinel", 4: "ready", 5: "bottom", 6: "ll128", 7: "rs", 8: "ag",
               9: "arrive", 10: "complete", 11: "copy", 12: "counter",
-              13: "cluster"}
+              13: "cluster",
+              32: "page", 33: "length", 34: "slot", 35: "tokens", 36: "ring"}
 
 
 class SfarFault(ctypes.Structure):
@@ -83,6 +85,16 @@ _SIGS = [
     ("sfar_test_set_fused_path", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int]),
     ("sfar_test_query_fused_path", ctypes.c_int, [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_size_t,
                                                   ctypes.POINTER(ctypes.c_int)]),
+    ("sfar_quantize_fp8", ctypes.c_int, [ctypes.c_void_p] * 4 + [ctypes.c_size_t] * 4 + [ctypes.c_void_p]),
+    ("sfar_rowpar_gemm_fp8", ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_size_t] * 5 + [ctypes.c_void_p]),
+    ("sfar_kv_create", ctypes.c_void_p, [ctypes.c_int] * 5 + [ctypes.c_size_t] + [ctypes.c_void_p] * 4),
+    ("sfar_kv_destroy", None, [ctypes.c_void_p]),
+    ("sfar_kv_plan", ctypes.c_int, [ctypes.c_void_p] * 11 + [ctypes.c_size_t] * 3 + [ctypes.c_void_p]),
+    ("sfar_kv_append", ctypes.c_int, [ctypes.c_void_p] * 4 + [ctypes.c_size_t] * 5 + [ctypes.c_void_p]),
+    ("sfar_kv_attention", ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_size_t] * 8 +
+     [ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p]),
+    ("sfar_kv_status_get", ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(SfarFault)]),
+    ("sfar_kv_reset", ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     ("sfar_probe_empty", ctypes.c_int, [ctypes.c_void_p]),
     ("sfar_probe_pingpong", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                            ctypes.c_void_p, ctypes.c_void_p]),
@@ -124,6 +136,50 @@ def _stream(stream):
 
 def _ptr_array(ptrs):
     return (ctypes.c_void_p * len(ptrs))(*[int(p) for p in ptrs])
+
+
+def _rank_ptrs(x, R, what):
+    """A pointer per rank: of a list of R tensors, or of the slices of one [R, ...] tensor."""
+    if isinstance(x, (list, tuple)):
+        if len(x) != R:
+            raise ValueError(f"{what}: need {R} tensors, one per rank")
+        return (ctypes.c_void_p * R)(*[t.data_ptr() for t in x])
+    if x.shape[0] != R:
+        raise ValueError(f"{what}: need [{R}, ...], a slice per rank")
+    base, step = x.data_ptr(), x.stride(0) * x.element_size()
+    return (ctypes.c_void_p * R)(*range(base, base + R * step, step)) if step else (ctypes.c_void_p * R)(*[base] * R)
+
+
+def _rank_form(x, ndim, what, *dtypes):
+    """Rank 0's tensor, after the checks that hold for every rank: dimensions, type, the same strides, unit
+    stride along the last dimension."""
+    if isinstance(x, (list, tuple)):
+        t = x[0]
+        for o in x[1:]:
+            if o.shape != t.shape or o.stride() != t.stride() or o.dtype != t.dtype:
+                raise ValueError(f"{what}: the ranks' tensors differ in shape, strides or type")
+    else:
+        t = x[0]
+    if t.dim() != ndim or str(t.dtype) not in dtypes:
+        raise ValueError(f"{what}: need {ndim} dimensions of {' or '.join(dtypes)} per rank")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    return t
+
+
+_BF16, _FP32, _INT32 = "torch.bfloat16", "torch.float32", "torch.int32"
+_BYTES = ("torch.float8_e4m3fn", "torch.uint8")
+
+
+def _strides(t):
+    """Strides of the two leading dimensions; 0 where there is one entry only, whatever torch keeps there."""
+    return tuple(t.stride(i) if t.shape[i] > 1 else 0 for i in (0, 1))
+
+
+def _int32(t, shape, what):
+    if tuple(t.shape) != shape or str(t.dtype) != _INT32 or not t.is_contiguous():
+        raise ValueError(f"{what}: need a contiguous int32 tensor of shape {list(shape)}")
+    return t.data_ptr()
 
 
 def _check(code, what):
@@ -306,6 +362,39 @@ class Sfar:
                                 [t.data_ptr() for t in y], k, hidden, prefetch_rows, stream)
         _check(code, "sfar_rowpar_gemv")
 
+    def quantize_fp8(self, x, x8, sx, stream=None) -> None:
+        """x: [m, k] bf16 per rank -> x8: [m, k] e4m3 and sx: [ceil(k / 128), m] fp32 per rank (lists of R
+        tensors, or one tensor [R, ...] each; rows of x and x8 may be strided)."""
+        t, o, c = _rank_form(x, 2, "x", _BF16), _rank_form(x8, 2, "x8", *_BYTES), _rank_form(sx, 2, "sx", _FP32)
+        m, k = t.shape
+        if o.shape != t.shape or tuple(c.shape) != ((k + 127) // 128, m) or not c.is_contiguous():
+            raise ValueError("quantize_fp8: x8 must be [m, k], sx a contiguous [ceil(k / 128), m]")
+        R = self.R
+        code = lib().sfar_quantize_fp8(self.h, _rank_ptrs(x, R, "x"), _rank_ptrs(x8, R, "x8"), _rank_ptrs(sx, R, "sx"),
+                                       m, k, t.stride(0) if m > 1 else (k + 15) // 16 * 16,
+                                       o.stride(0) if m > 1 else (k + 15) // 16 * 16, _stream(stream))
+        _check(code, "sfar_quantize_fp8")
+
+    def rowpar_gemm_fp8(self, x8, sx, w8, sw, y, stream=None) -> None:
+        """x8 [m, k], sx [ceil(k / 128), m] (as quantize_fp8 gives them), w8 [hidden, k] e4m3 and sw
+        [ceil(hidden / 128), ceil(k / 128)] fp32 -> y [m, hidden] bf16, per rank (lists of R tensors, or one
+        tensor [R, ...] each; rows of x8 and w8 may be strided by multiples of 16)."""
+        tx, tw, ty = _rank_form(x8, 2, "x8", *_BYTES), _rank_form(w8, 2, "w8", *_BYTES), _rank_form(y, 2, "y", _BF16)
+        cx, cw = _rank_form(sx, 2, "sx", _FP32), _rank_form(sw, 2, "sw", _FP32)
+        m, k = tx.shape
+        n, kb = tw.shape[0], (k + 127) // 128
+        if tw.shape[1] != k or tuple(ty.shape) != (m, n) or tuple(cx.shape) != (kb, m) or \
+                tuple(cw.shape) != ((n + 127) // 128, kb) or not (ty.is_contiguous() and cx.is_contiguous() and
+                                                                  cw.is_contiguous()):
+            raise ValueError("rowpar_gemm_fp8: need x8 [m, k], w8 [hidden, k], contiguous sx [ceil(k / 128), m], "
+                             "sw [ceil(hidden / 128), ceil(k / 128)] and y [m, hidden]")
+        R, up = self.R, (k + 15) // 16 * 16
+        code = lib().sfar_rowpar_gemm_fp8(self.h, _rank_ptrs(x8, R, "x8"), _rank_ptrs(sx, R, "sx"),
+                                          _rank_ptrs(w8, R, "w8"), _rank_ptrs(sw, R, "sw"), _rank_ptrs(y, R, "y"),
+                                          m, k, n, tx.stride(0) if m > 1 else up, tw.stride(0) if n > 1 else up,
+                                          _stream(stream))
+        _check(code, "sfar_rowpar_gemm_fp8")
+
     def status(self):
         return sfar_status_get(self.h)
 
@@ -321,6 +410,94 @@ class Sfar:
     def close(self) -> None:
         if self.h:
             sfar_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class SfarKv:
+    """A paged key/value cache in e4m3 with a scale for each page and head, for R simulated ranks
+    (``include/sfar_kv.h``).
+
+    ``k_cache``, ``v_cache``: [pages, kv_heads, page_tokens, head_dim] e4m3 (or its bytes) per rank; ``k_scale``,
+    ``v_scale``: [pages, kv_heads] fp32 per rank -- lists of R contiguous tensors, or one tensor [R, ...] each.
+    The tensors stay the caller's and are kept alive by this object.
+    """
+
+    def __init__(self, k_cache, v_cache, k_scale, v_scale, q_heads: int):
+        self.h = None
+        R = len(k_cache)
+        k, v = _rank_form(k_cache, 4, "k_cache", *_BYTES), _rank_form(v_cache, 4, "v_cache", *_BYTES)
+        ks, vs = _rank_form(k_scale, 2, "k_scale", _FP32), _rank_form(v_scale, 2, "v_scale", _FP32)
+        if v.shape != k.shape or ks.shape != k.shape[:2] or vs.shape != k.shape[:2] or \
+                not all(t.is_contiguous() for t in (k, v, ks, vs)):
+            raise ValueError("SfarKv: need contiguous caches [pages, kv_heads, page_tokens, head_dim] and scales "
+                             "[pages, kv_heads]")
+        self.R, self.q_heads = R, q_heads
+        self.pages, self.kv_heads, self.page_tokens, self.head_dim = k.shape
+        self.tensors = (k_cache, v_cache, k_scale, v_scale)
+        h = lib().sfar_kv_create(R, q_heads, self.kv_heads, self.head_dim, self.page_tokens, self.pages,
+                                 _rank_ptrs(k_cache, R, "k_cache"), _rank_ptrs(v_cache, R, "v_cache"),
+                                 _rank_ptrs(k_scale, R, "k_scale"), _rank_ptrs(v_scale, R, "v_scale"))
+        if not h:
+            raise SfarError(lib().sfar_last_error(), "sfar_kv_create")
+        self.h = h
+
+    def plan(self, lens, delta, table, ring, state, lens_out, state_out, starts, slots, taken, stream=None) -> None:
+        """Pages, slots and offsets of a step from the requests' lengths; every tensor int32.  lens, delta,
+        lens_out, taken: [requests]; table: [requests, width]; ring: [pages]; state, state_out: [2]; starts:
+        [requests + 1]; slots: [tokens].  lens_out may be lens, state_out may be state."""
+        B = lens.shape[0]
+        W, T = table.shape[1], slots.shape[0]
+        code = lib().sfar_kv_plan(self.h, _int32(lens, (B,), "lens"), _int32(delta, (B,), "delta"),
+                                  _int32(table, (B, W), "table"), _int32(ring, (self.pages,), "ring"),
+                                  _int32(state, (2,), "state"), _int32(lens_out, (B,), "lens_out"),
+                                  _int32(state_out, (2,), "state_out"), _int32(starts, (B + 1,), "starts"),
+                                  _int32(slots, (T,), "slots"), _int32(taken, (B,), "taken"), B, W, T, _stream(stream))
+        _check(code, "sfar_kv_plan")
+
+    def append(self, k, v, slots, stream=None) -> None:
+        """k, v: [tokens, kv_heads, head_dim] bf16 per rank (token and head strides multiples of 8); slots: [tokens]."""
+        tk, tv = _rank_form(k, 3, "k", _BF16), _rank_form(v, 3, "v", _BF16)
+        T = slots.shape[0]
+        shape = (T, self.kv_heads, self.head_dim)
+        if tuple(tk.shape) != shape or tuple(tv.shape) != shape:
+            raise ValueError(f"append: need k and v of shape {list(shape)} per rank")
+        code = lib().sfar_kv_append(self.h, _rank_ptrs(k, self.R, "k"), _rank_ptrs(v, self.R, "v"),
+                                    _int32(slots, (T,), "slots"), T, *_strides(tk), *_strides(tv),
+                                    _stream(stream))
+        _check(code, "sfar_kv_append")
+
+    def attention(self, q, out, table, lens, starts, max_q: int, scale=None, window: int = 0, stream=None) -> None:
+        """q, out: [tokens, q_heads, head_dim] bf16 per rank (token and head strides multiples of 8); table:
+        [requests, width], lens: [requests], starts: [requests + 1].  scale: 1 / sqrt(head_dim) if None."""
+        tq, to = _rank_form(q, 3, "q", _BF16), _rank_form(out, 3, "out", _BF16)
+        if tuple(tq.shape[1:]) != (self.q_heads, self.head_dim) or to.shape != tq.shape:
+            raise ValueError(f"attention: need q and out of shape [tokens, {self.q_heads}, {self.head_dim}] per rank")
+        B, W = table.shape
+        if scale is None:
+            scale = self.head_dim ** -0.5
+        code = lib().sfar_kv_attention(self.h, _rank_ptrs(q, self.R, "q"), _rank_ptrs(out, self.R, "out"),
+                                       _int32(table, (B, W), "table"), _int32(lens, (B,), "lens"),
+                                       _int32(starts, (B + 1,), "starts"), B, W, tq.shape[0], *_strides(tq),
+                                       *_strides(to), max_q, scale, window, _stream(stream))
+        _check(code, "sfar_kv_attention")
+
+    def status(self):
+        f = SfarFault()
+        code = lib().sfar_kv_status_get(self.h, ctypes.byref(f))
+        return code, f
+
+    def reset(self, stream=None) -> None:
+        _check(lib().sfar_kv_reset(self.h, _stream(stream)), "sfar_kv_reset")
+
+    def close(self) -> None:
+        if self.h:
+            lib().sfar_kv_destroy(self.h)
             self.h = None
 
     def __del__(self):
