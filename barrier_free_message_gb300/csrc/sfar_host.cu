@@ -388,6 +388,8 @@ sfar_t *sfar_create(int R, size_t max_bytes, sfar_dtype dt)
         cudaFuncSetAttribute(sfar_kernel_gemv(), cudaFuncAttributeMaxDynamicSharedMemorySize, SFAR_GEMV_SMEM) !=
             cudaSuccess)
         st = SFAR_ERR_UNSUPPORTED;
+    if (st == SFAR_OK && sfar_fp8_prepare() != 0)
+        st = SFAR_ERR_UNSUPPORTED;
     // co-residency: every CTA of a call must be resident at once (ranks wait
     // on each other), so K is capped by the occupancy of each variant
     for (int p = 0; p < SFAR_NUM_PROTOS && st == SFAR_OK; ++p) {

@@ -57,19 +57,25 @@ struct SfarQuantArgs {
 };
 
 struct SfarGemm8Args {
-    const uint8_t *x8[SFAR_MAX_R], *w8[SFAR_MAX_R];
+    // x8 and w8 of every rank as 2-D tensor maps: k bytes (innermost) by rows,
+    // boxes of 128 bytes x the tile's tokens (x) or 128 rows (w), 128-byte
+    // swizzle, zeros outside
+    alignas(64) CUtensorMap xmap[SFAR_MAX_R];
+    alignas(64) CUtensorMap wmap[SFAR_MAX_R];
     const float *sx[SFAR_MAX_R], *sw[SFAR_MAX_R];
     uint16_t *y[SFAR_MAX_R];
     SfarCtl *ctl;
-    long long m, k, n, ldx, ldw;
-    int R;
+    long long m, n;
+    int R, kb, tiles_m, tiles_n, vec;       // vec: rows of y are 16-byte aligned
 };
 
 const void *sfar_kernel_kv_plan();
 const void *sfar_kernel_kv_append(int head_dim);
 const void *sfar_kernel_kv_attn(int head_dim);
 const void *sfar_kernel_quantize();
-const void *sfar_kernel_gemm8();
+const void *sfar_kernel_gemm8(int tokens, int *threads, int *smem);
+// once per device: what the 8-bit projection's kernels need of it; 0 or a cudaError_t
+int sfar_fp8_prepare();
 
 #define SFAR_PLAN_THREADS 512
 #define SFAR_PLAN_CLUSTER 8

@@ -1,5 +1,7 @@
 // sfar_kv_host.cu -- the C ABI of the paged 8-bit cache (include/sfar_kv.h)
 // and of the 8-bit projection (include/sfar_fp8.h): arguments, handle, launch.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <string.h>
@@ -28,6 +30,10 @@ namespace {
 
 size_t ceil_div(size_t x, size_t a) { return (x + a - 1) / a; }
 bool aligned(const void *p, uintptr_t a) { return p && ((uintptr_t)p & (a - 1)) == 0; }
+
+// Up to this many tokens the projection runs with outputs along the tensor
+// core's lanes (weights read once, HBM-bound), beyond it with tokens there.
+const size_t kFewTokens = 256;
 
 struct Span {
     uintptr_t lo, hi;
@@ -384,18 +390,21 @@ sfar_status sfar_rowpar_gemm_fp8(sfar_t *h, const void *const x8[], const float 
     const SfarView v = sfar_view(h);
     if (v.dt != SFAR_BF16)
         return SFAR_ERR_INVALID;
-    SfarGemm8Args a;
-    memset(&a, 0, sizeof a);
+    const PFN_cuTensorMapEncodeTiled_v12000 encode =
+        reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(sfar_tensor_map_encoder());
+    if (!encode)
+        return SFAR_ERR_UNSUPPORTED;
     const size_t kb = ceil_div(k, SFAR_FP8_BLOCK), nb = ceil_div(hidden, SFAR_FP8_BLOCK);
     const size_t xb = (m - 1) * ldx8 + k, wb = (hidden - 1) * ldw + k, yb = m * hidden * 2;
+    SfarGemm8Args a;
+    a.vec = hidden % 8 == 0;
     for (int r = 0; r < v.R; ++r) {
         if (!aligned(x8[r], 16) || !aligned(w8[r], 16) || !aligned(sx[r], 4) || !aligned(sw[r], 4) || !aligned(y[r], 2))
             return SFAR_ERR_INVALID;
-        a.x8[r] = static_cast<const uint8_t *>(x8[r]);
-        a.w8[r] = static_cast<const uint8_t *>(w8[r]);
         a.sx[r] = sx[r];
         a.sw[r] = sw[r];
         a.y[r] = static_cast<uint16_t *>(y[r]);
+        a.vec = a.vec && aligned(y[r], 16);
     }
     for (int i = 0; i < v.R; ++i) {
         const Span out(y[i], yb);
@@ -404,15 +413,42 @@ sfar_status sfar_rowpar_gemm_fp8(sfar_t *h, const void *const x8[], const float 
                 out.meets(Span(sw[j], nb * kb * 4)) || (i < j && out.meets(Span(y[j], yb))))
                 return SFAR_ERR_INVALID;
     }
+    const int few = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : m <= kFewTokens ? 128 : 0;
+    const cuuint32_t unit[2] = {1, 1}, wbox[2] = {SFAR_FP8_BLOCK, 128}, xbox[2] = {SFAR_FP8_BLOCK, few ? (cuuint32_t)few : 128u};
+    auto map = [&](CUtensorMap *to, const void *p, size_t rows, size_t ld, const cuuint32_t *box) {
+        const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld};
+        return encode(to, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), dims, strides, box, unit,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    for (int r = 0; r < v.R; ++r)
+        if (!map(&a.xmap[r], x8[r], m, ldx8, xbox) || !map(&a.wmap[r], w8[r], hidden, ldw, wbox))
+            return SFAR_ERR_INVALID;
     a.ctl = v.ctl;
     a.m = (long long)m;
-    a.k = (long long)k;
     a.n = (long long)hidden;
-    a.ldx = (long long)ldx8;
-    a.ldw = (long long)ldw;
     a.R = v.R;
-    return launch(v.dev, sfar_kernel_gemm8(), dim3((unsigned)ceil_div(hidden, 64), (unsigned)ceil_div(m, 16), (unsigned)v.R), 256, 0,
-                  &a, s, v.mode == SFAR_LAUNCH_PLAIN);
+    a.kb = (int)kb;
+    a.tiles_m = (int)ceil_div(m, few ? (size_t)few : 256);
+    a.tiles_n = (int)ceil_div(hidden, few ? 128 : 256);
+    const size_t tiles = (size_t)v.R * (size_t)a.tiles_m * (size_t)a.tiles_n;
+    const size_t slots = few ? (size_t)v.sms : (size_t)v.sms / 2;
+    const size_t grid = (tiles < slots ? tiles : slots) * (few ? 1 : 2);
+    int threads = 0, smem = 0;
+    const void *f = sfar_kernel_gemm8(few, &threads, &smem);
+    return launch(v.dev, f, dim3((unsigned)grid), (unsigned)threads, (size_t)smem, &a, s, v.mode == SFAR_LAUNCH_PLAIN);
 }
 
 }  // extern "C"
+
+int sfar_fp8_prepare()
+{
+    for (int few : {16, 32, 64, 128, 0}) {
+        int threads = 0, smem = 0;
+        const void *f = sfar_kernel_gemm8(few, &threads, &smem);
+        const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess)
+            return (int)e;
+    }
+    return 0;
+}
