@@ -37,11 +37,16 @@ struct SfarKvAppendArgs {
 };
 
 struct SfarAttnArgs {
-    const uint8_t *k[SFAR_MAX_R], *v[SFAR_MAX_R];
+    // caches of every rank as 3-D tensor maps: head_dim bytes (innermost) by
+    // page_tokens by pages * kv_heads, a box of up to SFAR_ATTN_TILE tokens
+    alignas(64) CUtensorMap kmap[SFAR_MAX_R];
+    alignas(64) CUtensorMap vmap[SFAR_MAX_R];
     const float *ks[SFAR_MAX_R], *vs[SFAR_MAX_R];
     const uint16_t *q[SFAR_MAX_R];
     uint16_t *out[SFAR_MAX_R];
     const int *table, *lens, *starts;
+    float *part;                            // partial results, two per CTA: [2 * grid][16][D + 4]
+    int *arrived;                           // [grid] parts of the row tile that began in a CTA; 0 between calls
     SfarCtl *ctl;
     long long qts, qhs, ots, ohs;
     float scale;
@@ -71,7 +76,7 @@ struct SfarGemm8Args {
 
 const void *sfar_kernel_kv_plan();
 const void *sfar_kernel_kv_append(int head_dim);
-const void *sfar_kernel_kv_attn(int head_dim);
+const void *sfar_kernel_kv_attn(int head_dim, int *threads, int *smem);
 const void *sfar_kernel_quantize();
 const void *sfar_kernel_gemm8(int tokens, int *threads, int *smem);
 // once per device: what the 8-bit projection's kernels need of it; 0 or a cudaError_t
@@ -80,3 +85,6 @@ int sfar_fp8_prepare();
 #define SFAR_PLAN_THREADS 512
 #define SFAR_PLAN_CLUSTER 8
 #define SFAR_APPEND_WARPS 8
+#define SFAR_ATTN_TILE 64
+#define SFAR_ATTN_STAGES 4
+#define SFAR_ATTN_CTAS 2                    // per SM

@@ -22,8 +22,11 @@ struct sfar_kv {
     float *scale[2][SFAR_MAX_R] = {};
     uint8_t *ws = nullptr;
     SfarCtl *ctl = nullptr;             // at the start of ws
+    float *part = nullptr;              // attention: partial results and their counters, in ws
+    int *arrived = nullptr;
     SfarCtl *host_ctl = nullptr;
     cudaStream_t priv = nullptr;
+    CUtensorMap map[2][SFAR_MAX_R];     // the caches as the attention's copies see them
 };
 
 namespace {
@@ -139,18 +142,40 @@ sfar_kv_t *sfar_kv_create(int R, int q_heads, int kv_heads, int head_dim, int pa
         h->scale[0][r] = k_scale[r];
         h->scale[1][r] = v_scale[r];
     }
-    if (cudaMalloc(&h->ws, 256) != cudaSuccess) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode =
+        reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(sfar_tensor_map_encoder());
+    const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)page_tokens, (cuuint64_t)(pages * (size_t)kv_heads)};
+    const cuuint64_t strides[2] = {(cuuint64_t)head_dim, (cuuint64_t)head_dim * (cuuint64_t)page_tokens};
+    const cuuint32_t unit[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {(cuuint32_t)head_dim, (cuuint32_t)(page_tokens < SFAR_ATTN_TILE ? page_tokens : SFAR_ATTN_TILE), 1};
+    for (int i = 0; i < 2 * R; ++i)
+        if (!encode || encode(&h->map[i & 1][i >> 1], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, h->cache[i & 1][i >> 1], dims, strides, box, unit,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
+            delete h;
+            return fail(encode ? SFAR_ERR_INVALID : SFAR_ERR_UNSUPPORTED);
+        }
+    const size_t ctas = (size_t)sms * SFAR_ATTN_CTAS;
+    const size_t o_arrived = 256, o_part = (o_arrived + ctas * 4 + 255) / 256 * 256;
+    const size_t bytes = o_part + ctas * 2 * 16 * ((size_t)head_dim + 4) * 4;
+    if (cudaMalloc(&h->ws, bytes) != cudaSuccess) {
         cudaGetLastError();
         delete h;
         return fail(SFAR_ERR_OOM);
     }
     h->ctl = reinterpret_cast<SfarCtl *>(h->ws);
+    h->arrived = reinterpret_cast<int *>(h->ws + o_arrived);
+    h->part = reinterpret_cast<float *>(h->ws + o_part);
     SfarCtl init;
     memset(&init, 0, sizeof init);
     init.timeout_ns = 1000000000ull;
     init.strag_rank = init.drop_rank = -1;
     init.f_rank = init.f_cta = init.f_peer = -1;
-    if (cudaMemcpy(h->ctl, &init, sizeof init, cudaMemcpyHostToDevice) != cudaSuccess ||
+    int threads = 0, smem = 0;
+    const void *attn = sfar_kernel_kv_attn(head_dim, &threads, &smem);
+    if (cudaMemset(h->ws, 0, bytes) != cudaSuccess ||
+        cudaMemcpy(h->ctl, &init, sizeof init, cudaMemcpyHostToDevice) != cudaSuccess ||
+        cudaFuncSetAttribute(attn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem + (SFAR_KV_MAX_REQUESTS + 1) * 4) != cudaSuccess ||
         cudaStreamCreateWithFlags(&h->priv, cudaStreamNonBlocking) != cudaSuccess ||
         cudaMallocHost(&h->host_ctl, sizeof(SfarCtl)) != cudaSuccess ||
         cudaFuncSetAttribute(sfar_kernel_kv_plan(), cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -266,7 +291,8 @@ sfar_status sfar_kv_attention(sfar_kv_t *h, const void *const q[], void *const o
     if (tokens == 0)
         return SFAR_OK;
     SfarAttnArgs a;
-    memset(&a, 0, sizeof a);
+    memcpy(a.kmap, h->map[0], sizeof a.kmap);
+    memcpy(a.vmap, h->map[1], sizeof a.vmap);
     auto extent = [&](size_t ts, size_t hs) { return 2 * ((tokens - 1) * ts + (size_t)(h->Hq - 1) * hs + (size_t)h->D); };
     const size_t qb = extent(q_token_stride, q_head_stride), ob = extent(out_token_stride, out_head_stride);
     for (int r = 0; r < h->R; ++r) {
@@ -274,8 +300,6 @@ sfar_status sfar_kv_attention(sfar_kv_t *h, const void *const q[], void *const o
             return SFAR_ERR_INVALID;
         a.q[r] = static_cast<const uint16_t *>(q[r]);
         a.out[r] = static_cast<uint16_t *>(out[r]);
-        a.k[r] = static_cast<const uint8_t *>(h->cache[0][r]);
-        a.v[r] = static_cast<const uint8_t *>(h->cache[1][r]);
         a.ks[r] = h->scale[0][r];
         a.vs[r] = h->scale[1][r];
     }
@@ -287,6 +311,8 @@ sfar_status sfar_kv_attention(sfar_kv_t *h, const void *const q[], void *const o
     a.lens = lens;
     a.starts = starts;
     a.ctl = h->ctl;
+    a.part = h->part;
+    a.arrived = h->arrived;
     a.qts = (long long)q_token_stride;
     a.qhs = (long long)q_head_stride;
     a.ots = (long long)out_token_stride;
@@ -302,8 +328,9 @@ sfar_status sfar_kv_attention(sfar_kv_t *h, const void *const q[], void *const o
     a.shift = h->shift;
     a.pages = (int)h->pages;
     a.window = window >= (1ull << 31) ? 0 : (int)window;
-    return launch(h->dev, sfar_kernel_kv_attn(h->D), dim3((unsigned)ceil_div(tokens * (size_t)h->Hq, 4), (unsigned)h->R), 128, 0,
-                  &a, s);
+    int threads = 0, smem = 0;
+    const void *f = sfar_kernel_kv_attn(h->D, &threads, &smem);
+    return launch(h->dev, f, dim3((unsigned)(h->sms * SFAR_ATTN_CTAS)), (unsigned)threads, (size_t)smem + (requests + 1) * 4, &a, s);
 }
 
 sfar_status sfar_kv_status_get(sfar_kv_t *h, sfar_fault *info)
