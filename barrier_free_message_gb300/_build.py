@@ -19,8 +19,8 @@ LIB = os.path.join(OUT_DIR, "libsfar.so")
 
 SOURCES = ["sfar_host.cu", "k_ll.cu", "k_ll128.cu", "k_sentinel.cu", "k_db.cu", "k_twoshot.cu", "k_twoshot_sent.cu", "k_tma.cu",
            "k_atomic.cu", "k_fused.cu", "k_fused8.cu", "k_fused_ts.cu", "k_gemv.cu",
-           "k_misc.cu", "sfar_noalloc.cu", "k_kv_plan.cu", "k_kv_append.cu", "k_kv_attn.cu", "k_quant8.cu", "k_gemm8.cu",
-           "sfar_kv_host.cu"]
+           "k_misc.cu", "sfar_noalloc.cu", "k_kv_plan.cu", "k_kv_append.cu", "k_kv_attn.cu",
+           "k_kv_prompt.cu", "k_quant8.cu", "k_gemm8.cu", "sfar_kv_host.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", *ARCH, "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

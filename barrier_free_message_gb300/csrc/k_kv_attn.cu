@@ -33,8 +33,7 @@
 // rows), four consumer warps of 16 tokens of each tile with running states of
 // their own, joined through shared memory once per piece of 16 rows.
 #include "sfar_e4m3.cuh"
-#include "sfar_kv_args.h"
-#include "sfar_kv_device.cuh"
+#include "sfar_attn.cuh"
 #include "sfar_tc.cuh"
 
 namespace {
@@ -43,7 +42,6 @@ constexpr int kTile = SFAR_ATTN_TILE;              // cached tokens per stage
 constexpr int kConsumers = 4, kThreads = 32 * (kConsumers + 1);
 constexpr int kStages = SFAR_ATTN_STAGES;
 constexpr int kRows = 16;
-constexpr float kLift = 6.f;                       // log2 by which a score may pass the running maximum
 
 // Shared memory of a CTA, after the prefix sums.
 template <int D> struct Lay {
@@ -63,24 +61,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float lg2(float x)
-{
-    float y;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t half2_of(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a)
 {
@@ -110,36 +90,6 @@ template <int D> __device__ __forceinline__ int token_of(int n)
     return D == 128 ? n : (int)((0x65742130u >> (4 * n)) & 7u);
 }
 
-// Parts of a row's softmax, joined: the references first, then the parts in
-// their order.  o = sum of weights * values, relative to 2^wtop; sum relative
-// to 2^top.
-template <int E> struct State {
-    float top = -INFINITY, wtop = -INFINITY, sum = 0.f, o[E] = {};
-    __device__ __forceinline__ void reference(float t, float w)
-    {
-        top = fmaxf(top, t);
-        wtop = fmaxf(wtop, w);
-    }
-    // adds a part's sum; returns what its o is to be multiplied by
-    __device__ __forceinline__ float add(float t, float s, float w)
-    {
-        sum += t == -INFINITY ? s : ex2(t - top) * s;         // s is 0 then, or NaN
-        return w == -INFINITY ? 1.f : ex2(w - wtop);          // o is 0 then, or NaN
-    }
-    __device__ __forceinline__ void add4(int e, float by, const float4 &v)
-    {
-        o[e] += by * v.x;
-        o[e + 1] += by * v.y;
-        o[e + 2] += by * v.z;
-        o[e + 3] += by * v.w;
-    }
-    // 0 for a row that attends to nothing
-    __device__ __forceinline__ float factor() const
-    {
-        return sum == 0.f ? 0.f : wtop == -INFINITY ? 1.f / sum : ex2(wtop - top) / sum;
-    }
-};
-
 // One piece: 16 rows of a request and a run of its tiles.
 struct Piece {
     int plane, b, rt;           // rank * Hk + head; request; row tile
@@ -151,14 +101,6 @@ struct Piece {
 struct Work {
     const uint32_t *upto;       // [B + 1] prefix sums of the requests' units, per plane
     const SfarAttnArgs &a;
-    __device__ __forceinline__ void request(int b, int &len, int &count, int &first) const
-    {
-        const long long most = min((long long)a.W << a.shift, (long long)INT_MAX);
-        len = (int)max(0ll, min((long long)a.lens[b], most));
-        const int s = a.starts[b], e = a.starts[b + 1];
-        first = s;
-        count = s < 0 || e < s || e > a.T ? 0 : e - s;
-    }
     // tiles that some row of the request attends to (at least one: rows of nothing are written too)
     __device__ __forceinline__ void range(int len, int count, int &begin, int &all) const
     {
@@ -181,7 +123,7 @@ struct Work {
                 hi = mid;
         }
         p.b = lo;
-        request(lo, p.len, p.count, p.first);
+        sfar_attn_request(a, lo, p.len, p.count, p.first);
         range(p.len, p.count, p.begin, p.all);
         const uint32_t w = v - upto[lo];
         p.rt = (int)(w / (uint32_t)p.all);
@@ -236,15 +178,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_attn(const __grid_constant__
         uint32_t v = 0;
         if (b < a.B) {
             int len, count, first, begin, all;
-            work.request(b, len, count, first);
+            sfar_attn_request(a, b, len, count, first);
             work.range(len, count, begin, all);
             v = (uint32_t)(((long long)count * a.G + kRows - 1) / kRows) * (uint32_t)all;
-            if (blockIdx.x == 0) {
-                if (a.lens[b] != len)
-                    sfar_kv_fault(a.ctl, b, SFAR_KV_BAD_LENGTH);
-                if (a.starts[b + 1] - first != count || first < 0)
-                    sfar_kv_fault(a.ctl, b, SFAR_KV_BAD_TOKENS);
-            }
+            if (blockIdx.x == 0)
+                sfar_attn_check(a, b, len, count, first);
         }
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -268,14 +206,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_attn(const __grid_constant__
         __syncthreads();
     }
 
-    // rows past the last request
-    for (long long i = (long long)blockIdx.x * kThreads + tid; i < (long long)(a.T - max(0, min(a.starts[a.B], a.T))) * a.Hq * a.R;
-         i += (long long)gridDim.x * kThreads) {
-        const int h = (int)(i % a.Hq), r = (int)(i / a.Hq % a.R);
-        uint16_t *dst = a.out[r] + (a.T - 1 - i / a.Hq / a.R) * a.ots + h * a.ohs;
-        for (int e = 0; e < D; e += 8)
-            st_v4(dst + e, make_uint4(0, 0, 0, 0));
-    }
+    sfar_attn_padding<D>(a);
 
     const long long U = (long long)carry * a.R * a.Hk;
     const long long N = min((long long)gridDim.x, U);
@@ -472,8 +403,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_attn(const __grid_constant__
                 now[i] = fmaxf(now[i], __shfl_xor_sync(SFAR_FULL, now[i], 1));
                 now[i] = fmaxf(now[i], __shfl_xor_sync(SFAR_FULL, now[i], 2));
             }
-            const bool move = now[0] > top[0] + kLift || now[1] > top[1] + kLift || now[0] + lvs > wtop[0] + kLift ||
-                              now[1] + lvs > wtop[1] + kLift;
+            const bool move = now[0] > top[0] + kAttnLift || now[1] > top[1] + kAttnLift || now[0] + lvs > wtop[0] + kAttnLift ||
+                              now[1] + lvs > wtop[1] + kAttnLift;
             if (__any_sync(SFAR_FULL, move)) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -600,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_attn(const __grid_constant__
         consumers_sync();
         constexpr int kE = D / 8;                  // elements of one row per thread: 8 threads a row
         const int row = tid >> 3, col = (tid & 7) * kE;
-        State<kE> all;
+        SfarAttnState<kE> all;
         for (int w = 0; w < kConsumers; ++w)
             all.reference(s_ml[0][w][row], s_ml[2][w][row]);
 #pragma unroll
@@ -639,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_attn(const __grid_constant__
             write = s_last;
             if (write && row < rows) {
                 __threadfence();
-                all = State<kE>();
+                all = SfarAttnState<kE>();
 #pragma unroll 8
                 for (long long c = c0; c <= c1; ++c) {
                     const float4 m = __ldcg(reinterpret_cast<const float4 *>(slot(c, c == c0) + kRows * D + row * 4));

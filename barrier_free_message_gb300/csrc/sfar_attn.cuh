@@ -1,0 +1,85 @@
+// sfar_attn.cuh -- what the two attention kernels share.
+#pragma once
+#include "sfar_kv_args.h"
+#include "sfar_kv_device.cuh"
+#include "sfar_tc.cuh"
+
+constexpr float kAttnLift = 6.f;       // log2 by which a score or weight may pass its running reference
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lg2(float x)
+{
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Request b: its context, how many new tokens it has and the row of the first.
+__device__ __forceinline__ void sfar_attn_request(const SfarAttnArgs &a, int b, int &len, int &count, int &first)
+{
+    const long long most = min((long long)a.W << a.shift, (long long)INT_MAX - 1024);
+    len = (int)max(0ll, min((long long)a.lens[b], most));
+    const int s = a.starts[b], e = a.starts[b + 1];
+    first = s;
+    count = s < 0 || e < s || e > a.T ? 0 : e - s;
+}
+// Records what sfar_attn_request had to correct.
+__device__ __forceinline__ void sfar_attn_check(const SfarAttnArgs &a, int b, int len, int count, int first)
+{
+    if (a.lens[b] != len)
+        sfar_kv_fault(a.ctl, b, SFAR_KV_BAD_LENGTH);
+    if (first < 0 || a.starts[b + 1] - first != count)
+        sfar_kv_fault(a.ctl, b, SFAR_KV_BAD_TOKENS);
+}
+// Zeros for the rows past the last request, by the whole grid.
+template <int D> __device__ __forceinline__ void sfar_attn_padding(const SfarAttnArgs &a)
+{
+    const long long rows = (long long)(a.T - max(0, min(a.starts[a.B], a.T))) * a.Hq * a.R;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < rows; i += (long long)gridDim.x * blockDim.x) {
+        const int h = (int)(i % a.Hq), r = (int)(i / a.Hq % a.R);
+        uint16_t *dst = a.out[r] + (a.T - 1 - i / a.Hq / a.R) * a.ots + h * a.ohs;
+        for (int e = 0; e < D; e += 8)
+            st_v4(dst + e, make_uint4(0, 0, 0, 0));
+    }
+}
+
+// Parts of a row's softmax, joined: the references first, then the parts in
+// their order.  o = sum of weights * values, relative to 2^wtop; sum relative
+// to 2^top.
+template <int E> struct SfarAttnState {
+    float top = -INFINITY, wtop = -INFINITY, sum = 0.f, o[E] = {};
+    __device__ __forceinline__ void reference(float t, float w)
+    {
+        top = fmaxf(top, t);
+        wtop = fmaxf(wtop, w);
+    }
+    // adds a part's sum; returns what its o is to be multiplied by
+    __device__ __forceinline__ float add(float t, float s, float w)
+    {
+        sum += t == -INFINITY ? s : ex2(t - top) * s;         // s is 0 then, or NaN
+        return w == -INFINITY ? 1.f : ex2(w - wtop);          // o is 0 then, or NaN
+    }
+    __device__ __forceinline__ void add4(int e, float by, const float4 &v)
+    {
+        o[e] += by * v.x;
+        o[e + 1] += by * v.y;
+        o[e + 2] += by * v.z;
+        o[e + 3] += by * v.w;
+    }
+    // 0 for a row that attends to nothing
+    __device__ __forceinline__ float factor() const
+    {
+        return sum == 0.f ? 0.f : wtop == -INFINITY ? 1.f / sum : ex2(wtop - top) / sum;
+    }
+};

@@ -41,11 +41,12 @@ struct SfarAttnArgs {
     // page_tokens by pages * kv_heads, a box of up to SFAR_ATTN_TILE tokens
     alignas(64) CUtensorMap kmap[SFAR_MAX_R];
     alignas(64) CUtensorMap vmap[SFAR_MAX_R];
+    const uint8_t *v[SFAR_MAX_R];           // the value caches
     const float *ks[SFAR_MAX_R], *vs[SFAR_MAX_R];
     const uint16_t *q[SFAR_MAX_R];
     uint16_t *out[SFAR_MAX_R];
     const int *table, *lens, *starts;
-    float *part;                            // partial results, two per CTA: [2 * grid][16][D + 4]
+    float *part;                            // partial results, two per CTA
     int *arrived;                           // [grid] parts of the row tile that began in a CTA; 0 between calls
     SfarCtl *ctl;
     long long qts, qhs, ots, ohs;
@@ -77,6 +78,7 @@ struct SfarGemm8Args {
 const void *sfar_kernel_kv_plan();
 const void *sfar_kernel_kv_append(int head_dim);
 const void *sfar_kernel_kv_attn(int head_dim, int *threads, int *smem);
+const void *sfar_kernel_kv_prompt(int head_dim, int *threads, int *smem);
 const void *sfar_kernel_quantize();
 const void *sfar_kernel_gemm8(int tokens, int *threads, int *smem);
 // once per device: what the 8-bit projection's kernels need of it; 0 or a cudaError_t
@@ -88,3 +90,5 @@ int sfar_fp8_prepare();
 #define SFAR_ATTN_TILE 64
 #define SFAR_ATTN_STAGES 4
 #define SFAR_ATTN_CTAS 2                    // per SM
+#define SFAR_PROMPT_ROWS 256
+#define SFAR_PROMPT_REQUESTS 4096           // whose prefix sums fit beside the prompt kernel's tiles

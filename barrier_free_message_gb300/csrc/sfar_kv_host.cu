@@ -38,6 +38,10 @@ bool aligned(const void *p, uintptr_t a) { return p && ((uintptr_t)p & (a - 1)) 
 // core's lanes (weights read once, HBM-bound), beyond it with tokens there.
 const size_t kFewTokens = 256;
 
+// Up to this many query rows (new tokens x query heads per key head) of the
+// longest request the attention runs 16 rows at a time, beyond it 256.
+const size_t kFewRows = 32;
+
 struct Span {
     uintptr_t lo, hi;
     Span(const void *p, size_t bytes) : lo((uintptr_t)p), hi((uintptr_t)p + bytes) {}
@@ -157,7 +161,8 @@ sfar_kv_t *sfar_kv_create(int R, int q_heads, int kv_heads, int head_dim, int pa
         }
     const size_t ctas = (size_t)sms * SFAR_ATTN_CTAS;
     const size_t o_arrived = 256, o_part = (o_arrived + ctas * 4 + 255) / 256 * 256;
-    const size_t bytes = o_part + ctas * 2 * 16 * ((size_t)head_dim + 4) * 4;
+    const size_t few = ctas * 2 * 16, many = (size_t)sms * 2 * SFAR_PROMPT_ROWS;     // rows of partial results
+    const size_t bytes = o_part + (few > many ? few : many) * ((size_t)head_dim + 4) * 4;
     if (cudaMalloc(&h->ws, bytes) != cudaSuccess) {
         cudaGetLastError();
         delete h;
@@ -173,7 +178,10 @@ sfar_kv_t *sfar_kv_create(int R, int q_heads, int kv_heads, int head_dim, int pa
     init.f_rank = init.f_cta = init.f_peer = -1;
     int threads = 0, smem = 0;
     const void *attn = sfar_kernel_kv_attn(head_dim, &threads, &smem);
+    int pthreads = 0, psmem = 0;
+    const void *prompt = sfar_kernel_kv_prompt(head_dim, &pthreads, &psmem);
     if (cudaMemset(h->ws, 0, bytes) != cudaSuccess ||
+        cudaFuncSetAttribute(prompt, cudaFuncAttributeMaxDynamicSharedMemorySize, psmem + (SFAR_PROMPT_REQUESTS + 1) * 4) != cudaSuccess ||
         cudaMemcpy(h->ctl, &init, sizeof init, cudaMemcpyHostToDevice) != cudaSuccess ||
         cudaFuncSetAttribute(attn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem + (SFAR_KV_MAX_REQUESTS + 1) * 4) != cudaSuccess ||
         cudaStreamCreateWithFlags(&h->priv, cudaStreamNonBlocking) != cudaSuccess ||
@@ -287,7 +295,6 @@ sfar_status sfar_kv_attention(sfar_kv_t *h, const void *const q[], void *const o
         !aligned(starts, 4) || q_token_stride % 8 || q_head_stride % 8 || out_token_stride % 8 || out_head_stride % 8 ||
         !(scale >= 0.f) || isinf(scale))
         return SFAR_ERR_INVALID;
-    (void)max_q;
     if (tokens == 0)
         return SFAR_OK;
     SfarAttnArgs a;
@@ -300,6 +307,7 @@ sfar_status sfar_kv_attention(sfar_kv_t *h, const void *const q[], void *const o
             return SFAR_ERR_INVALID;
         a.q[r] = static_cast<const uint16_t *>(q[r]);
         a.out[r] = static_cast<uint16_t *>(out[r]);
+        a.v[r] = static_cast<const uint8_t *>(h->cache[1][r]);
         a.ks[r] = h->scale[0][r];
         a.vs[r] = h->scale[1][r];
     }
@@ -329,6 +337,10 @@ sfar_status sfar_kv_attention(sfar_kv_t *h, const void *const q[], void *const o
     a.pages = (int)h->pages;
     a.window = window >= (1ull << 31) ? 0 : (int)window;
     int threads = 0, smem = 0;
+    if (max_q * (size_t)a.G > kFewRows && requests <= SFAR_PROMPT_REQUESTS) {
+        const void *f = sfar_kernel_kv_prompt(h->D, &threads, &smem);
+        return launch(h->dev, f, dim3((unsigned)h->sms), (unsigned)threads, (size_t)smem + (requests + 1) * 4, &a, s);
+    }
     const void *f = sfar_kernel_kv_attn(h->D, &threads, &smem);
     return launch(h->dev, f, dim3((unsigned)(h->sms * SFAR_ATTN_CTAS)), (unsigned)threads, (size_t)smem + (requests + 1) * 4, &a, s);
 }

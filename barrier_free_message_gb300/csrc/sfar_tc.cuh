@@ -188,6 +188,14 @@ __device__ __forceinline__ void ld32(uint32_t (&v)[32], uint32_t addr)
         : "r"(addr));
 }
 #undef SFAR_R4
+__device__ __forceinline__ void st16(uint32_t addr, const uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
 
 // ---------------------------------------------------------------- tensor core
 // Shared-memory descriptor of a K-major operand whose rows are 128 bytes with
@@ -196,6 +204,18 @@ __device__ __forceinline__ void ld32(uint32_t (&v)[32], uint32_t addr)
 __device__ __forceinline__ uint64_t desc_k128(uint32_t addr)
 {
     return (uint64_t)((addr & 0x3ffffu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+// The same for rows of D bytes (64 with the 64-byte swizzle, or 128).
+template <int D> __device__ __forceinline__ uint64_t desc_k(uint32_t addr)
+{
+    return D == 128 ? desc_k128(addr)
+                    : (uint64_t)((addr & 0x3ffffu) >> 4) | (1ull << 16) | (32ull << 32) | (1ull << 46) | (4ull << 61);
+}
+// N-major operand of 16-bit elements: rows of 64 elements (128 bytes, 128-byte
+// swizzle), one per K index; the next 64 elements of N `block` bytes on.
+__device__ __forceinline__ uint64_t desc_n128(uint32_t addr, uint32_t block)
+{
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(block >> 4) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
 // Instruction descriptor: binary32 accumulator, both operands K-major e4m3.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24); }
@@ -213,6 +233,14 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
                      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
                      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
                      : "memory");
+}
+// binary16 (or bf16, by idesc), the first operand in tensor memory
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+                 : "memory");
 }
 // arrives on bar when every MMA issued so far by this thread is complete
 __device__ __forceinline__ void commit(uint32_t bar)
@@ -250,6 +278,12 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
 {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
