@@ -7,18 +7,21 @@
 //
 // Operands.  Keys are used as they lie in the cache, e4m3; the query row,
 // scaled by a power of two to a largest magnitude in [128, 256), is split into
-// two e4m3 numbers: the nearest, and what is left.  bf16's 8 significant bits
-// are 4 + 4, so the split is exact down to 2^-9 of the row's largest element
-// and off by at most 2^-18 of it below; two e4m3 products cost what one
-// binary16 product would, and the keys need no conversion.  Values are widened
-// to binary16 (exact) by a warpgroup of its own, once for the 256 rows that
+// two e4m3 numbers: the leading 4 of bf16's 8 significant bits, and the other
+// 4.  The split is exact for elements down to 2^-9 of the row's largest and
+// off by at most 2^-17 of that below; two e4m3 products cost what one binary16
+// product would, and the keys need no conversion.  Values are widened
+// to binary16 (exact) by two warps, once for the 256 rows that
 // share them; the weights are rounded to binary16 and are the operand in
-// tensor memory, in the place of the scores they come from.
+// tensor memory, in the place of the scores they come from.  One running
+// reference serves weights and sum, the weights' (score times value scale), and
+// the sum is of weight / value scale: two value scales of one request may be
+// up to 2^100 apart.
 //
 // A CTA takes 256 rows as two tiles of 128, each with a softmax warpgroup (a
 // thread per row: no shuffles).  The tensor core alternates: while it runs
 // O_B += W_B V and S_B = Q_B K' of one tile, the other's softmax works.  Warp
-// 12 copies tiles (TMA), one thread of warp 13 issues the MMAs.  The
+// 12   The
 // accumulator is rescaled, in tensor memory, only when a reference moves.
 //
 // Work: as in k_kv_attn.cu the tiles of all (rank, key head, request, 256
@@ -32,7 +35,8 @@ namespace {
 
 constexpr int kTile = 128;                         // cached tokens per step
 constexpr int kRows = SFAR_PROMPT_ROWS;            // query rows per CTA: two tiles of 128
-constexpr int kThreads = 512;
+constexpr int kThreads = 384;                      // 8 softmax warps, kWiden that widen values, one copies, one issues
+constexpr int kWiden = 2, kCopyWarp = 8 + kWiden, kMmaWarp = kCopyWarp + 1;
 constexpr int kKStages = 3, kVStages = 2, kHStages = 2, kMeta = 4;
 
 template <int D> struct Lay {
@@ -41,8 +45,11 @@ template <int D> struct Lay {
     static constexpr int kBytes = oQ + 4 * kQ;     // queries: two tiles, nearest and rest
 };
 struct Meta {                                      // of a step
-    float ks[kTile / 16], lvs[kTile / 16], sign[kTile / 16];   // each 16 tokens: key scale, log2 and sign of the value scale
-    int bad;                                       // bit i: tokens 16 i .. are on no page of the pool
+    float ks[kTile / 16], lvs[kTile / 16], ivs[kTile / 16];    // each 16 tokens: key scale, log2 of the value scale and its inverse
+    // bit i: tokens 16 i .. are on no page of the pool; 8: a key scale is negative; 16 + i: tokens' value scale is 0
+    // (1 is put for it, and zeros for the values); 24 + i: it is negative (its magnitude is put, and -v for the values)
+    uint32_t odd;
+    int pad[3];
 };
 enum Bar {                                         // barriers, by index
     kKFull = 0,
@@ -57,7 +64,7 @@ enum Bar {                                         // barriers, by index
     kOFull = kPFull + 2,
     kOEmpty = kOFull + 2,
     kQFull = kOEmpty + 2,
-    kDrain = kQFull + 1,
+    kDrain = kQFull + 2,
     kBars = kDrain + 1
 };
 
@@ -129,7 +136,29 @@ struct Work {
     }
 };
 
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// 0xff for each byte that is a NaN of e4m3
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+// Sixteen e4m3 as binary16 to two 16-byte chunks of a swizzled row (the second
+// one's place differs in bit 4); flip: the second half first.
+__device__ __forceinline__ void widen(unsigned char *to, int flip, const uint4 &v)
+{
+    const uint4 lo = make_uint4(cvt_f16x2_e4m3(v.x), cvt_f16x2_e4m3(v.x >> 16), cvt_f16x2_e4m3(v.y), cvt_f16x2_e4m3(v.y >> 16));
+    const uint4 hi = make_uint4(cvt_f16x2_e4m3(v.z), cvt_f16x2_e4m3(v.z >> 16), cvt_f16x2_e4m3(v.w), cvt_f16x2_e4m3(v.w >> 16));
+    *reinterpret_cast<uint4 *>(to) = flip ? hi : lo;
+    *reinterpret_cast<uint4 *>((uintptr_t)to ^ 16) = flip ? lo : hi;
+}
+// the largest of 16 values, NaN left out unless all are
+__device__ __forceinline__ float max16(const uint32_t *v)
+{
+    float m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        m[i] = fmaxf(fmaxf(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])),
+                     fmaxf(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+// the four warps of a tile's softmax
+__device__ __forceinline__ void tile_sync(int x) { asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory"); }
 
 }  // namespace
 
@@ -139,9 +168,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
     using L = Lay<D>;
     extern __shared__ __align__(1024) unsigned char dyn[];
     __shared__ __align__(8) unsigned long long bars[kBars];
-    __shared__ Meta meta[kMeta];
+    __shared__ __align__(16) Meta meta[kMeta];
     __shared__ uint32_t s_warp[kThreads / 32], s_tmem;
-    __shared__ int s_last, s_nan[2];               // first and last context token of this piece whose value holds a NaN
+    __shared__ int s_last[2], s_nan[2][2];         // by the piece's parity: first and last context token whose value holds a NaN
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t mem = (tc::smem(dyn) + 1023u) & ~1023u;
     unsigned char *gen = dyn + (mem - tc::smem(dyn));
@@ -151,17 +180,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
 
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i) {
-            const bool four = (i >= kVEmpty && i < kVEmpty + kVStages) || (i >= kHFull && i < kHFull + kHStages) ||
-                              (i >= kPFull && i < kPFull + 2) || (i >= kOEmpty && i < kOEmpty + 2);
-            tc::bar_init(bar(i), i == kQFull ? 8 : four ? 4 : 1);
+            const bool widen = (i >= kVEmpty && i < kVEmpty + kVStages) || (i >= kHFull && i < kHFull + kHStages);
+            const bool four = (i >= kPFull && i < kPFull + 2) || (i >= kOEmpty && i < kDrain);
+            tc::bar_init(bar(i), four ? 4 : widen ? kWiden : 1);
         }
         tc::bar_fence_init();
         tc::fence_async();
         upto[0] = 0;
-        s_nan[0] = INT_MAX;
-        s_nan[1] = -1;
+        s_nan[0][0] = INT_MAX;
+        s_nan[0][1] = -1;
     }
-    if (warp == 13)
+    if (warp == kMmaWarp)
         tc::tmem_alloc<1>(tc::smem(&s_tmem), 512);
     pdl_wait();
     const unsigned long long limit = ld_relaxed_u64(&a.ctl->timeout_ns);
@@ -209,17 +238,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
     const long long U = (long long)carry * a.R * a.Hk;
     const long long N = min((long long)gridDim.x, U);
     const long long u0 = blockIdx.x < N ? blockIdx.x * U / N : 0, u1 = blockIdx.x < N ? (blockIdx.x + 1) * U / N : 0;
-    bool dead = false;                             // a wait gave up
 
     if (warp < 8) {
         // -------------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        bool dead = false;                         // a wait gave up: go on without waiting
         const int x = warp >> 2;                   // which tile of rows
         const int rho = x * 128 + (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
         const uint32_t tS = tmem + x * 256 + lanes, tO = tS + 128;
         tc::Ring<kMeta> ms;
         uint32_t sphase = 0, ophase = 0;
+        int odd_piece = 0;
         for (long long u = u0; u < u1;) {
             const Piece p = work.at(u, u1);
             const int r = p.plane / a.Hk, hk = p.plane % a.Hk;
@@ -229,13 +258,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             const bool row = rho < rows;
             float f = 0.f;
             if (mine) {
-                // this thread's query row, split, K-major with the swizzle of its row length
+                // this thread's query row, split, K-major with the swizzle of its length: the leading 4 bits of
+                // every element and the other 4
                 const uint16_t *src = a.q[r] + (long long)(p.first + (row ? n / a.G : 0)) * a.qts + (long long)(hk * a.G + n % a.G) * a.qhs;
                 uint32_t m = 0;
-#pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 v = row ? ld_nc_v4(src + c * 8) : make_uint4(0, 0, 0, 0);
-                    m = sfar_max_abs2(sfar_max_abs2(sfar_max_abs2(sfar_max_abs2(m, v.x), v.y), v.z), v.w);
+                {
+                    uint4 v[D / 8];
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c)
+                        v[c] = row ? ld_nc_v4(src + c * 8) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c)
+                        m = sfar_max_abs2(sfar_max_abs2(sfar_max_abs2(sfar_max_abs2(m, v[c].x), v[c].y), v[c].z), v[c].w);
                 }
                 m = sfar_max_half(m);
                 const bool special = m >= 0x7f80u;
@@ -243,141 +277,157 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                 const float up = sfar_exp2i(7 - e);
                 f = a.scale * 1.4426950408889634f * sfar_exp2i(max(e - 7, -126));
                 const int lrow = rho & 127;
-#pragma unroll 2
+#pragma unroll 1
                 for (int c = 0; c < D / 16; ++c) {
-                    uint32_t hi[4], lo[4];
+                    const uint4 v0 = row ? ld_nc_v4(src + c * 16) : make_uint4(0, 0, 0, 0);
+                    const uint4 v1 = row ? ld_nc_v4(src + c * 16 + 8) : make_uint4(0, 0, 0, 0);
+                    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+                    uint32_t ph[8], pl[8];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint4 v = row ? ld_nc_v4(src + c * 16 + h * 8) : make_uint4(0, 0, 0, 0);
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    for (int y = 0; y < 8; ++y) {
+                        const float x0 = bf16_lo(w[y]) * up, x1 = bf16_hi(w[y]) * up;
+                        const float h0 = __uint_as_float(__float_as_uint(x0) & 0xfff00000u), h1 = __uint_as_float(__float_as_uint(x1) & 0xfff00000u);
+                        ph[y] = cvt_e4m3x2(h0, h1);
+                        pl[y] = cvt_e4m3x2(x0 - h0, x1 - h1);
+                    }
+                    if (special) {                 // infinities would saturate: NaN
 #pragma unroll
-                        for (int i = 0; i < 4; i += 2) {
-                            uint32_t ph[2], pl[2];
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const float x0 = bf16_lo(w[i + y]) * up, x1 = bf16_hi(w[i + y]) * up;
-                                ph[y] = cvt_e4m3x2(x0, x1);
-                                const float2 b = e4m3x2_to_float2(ph[y]);
-                                pl[y] = cvt_e4m3x2(x0 - b.x, x1 - b.y);
-                                if (special) {     // infinities would saturate: NaN
-                                    if ((w[i + y] & 0x7f80u) == 0x7f80u)
-                                        ph[y] |= 0x7fu;
-                                    if ((w[i + y] & 0x7f800000u) == 0x7f800000u)
-                                        ph[y] |= 0x7f00u;
-                                }
-                            }
-                            hi[2 * h + i / 2] = ph[0] | ph[1] << 16;
-                            lo[2 * h + i / 2] = pl[0] | pl[1] << 16;
+                        for (int y = 0; y < 8; ++y) {
+                            if ((w[y] & 0x7f80u) == 0x7f80u)
+                                ph[y] |= 0x7fu;
+                            if ((w[y] & 0x7f800000u) == 0x7f800000u)
+                                ph[y] |= 0x7f00u;
                         }
                     }
                     const int chunk = D == 128 ? c ^ (lrow & 7) : c ^ ((lrow >> 1) & 3);
                     unsigned char *dst = gen + L::oQ + x * 2 * L::kQ + lrow * D + chunk * 16;
-                    *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(dst + L::kQ) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(ph[0] | ph[1] << 16, ph[2] | ph[3] << 16, ph[4] | ph[5] << 16, ph[6] | ph[7] << 16);
+                    *reinterpret_cast<uint4 *>(dst + L::kQ) = make_uint4(pl[0] | pl[1] << 16, pl[2] | pl[3] << 16, pl[4] | pl[5] << 16, pl[6] | pl[7] << 16);
                 }
                 tc::fence_async();
+                __syncwarp();
+                if (lane == 0)
+                    tc::bar_arrive(bar(kQFull + x));
             }
-            __syncwarp();
-            if (lane == 0)
-                tc::bar_arrive(bar(kQFull));
             const int pos = p.len - p.count + n / a.G;
             const int hi = row ? min(p.len, pos + 1) : INT_MAX, lo = row && a.window ? max(0, pos - a.window + 1) : 0;
             // tiles that every row of this warp sees whole
             const int all_from = __reduce_max_sync(SFAR_FULL, lo), all_to = min(p.len, __reduce_min_sync(SFAR_FULL, hi));
-            // log2 references: of the scores (sum), of the weights (o)
-            float top = -INFINITY, wtop = -INFINITY, sum = 0.f;
+            // log2 reference of the weights; sum: of weight / value scale
+            float wtop = -INFINITY, sum = 0.f;
             for (int k = 0; mine && k < p.tiles; ++k) {
                 const int j0 = (p.tile0 + k) * kTile;
                 dead = dead || !tc::bar_wait(bar(kMFull + ms.slot), ms.phase, limit);
                 const Meta &m = meta[ms.slot];
-                float c[8];
+                float c[8], lvs[8], ivs[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    c[i] = f * m.ks[i];
+                for (int i = 0; i < 8; i += 4) {
+                    const float4 y = *reinterpret_cast<const float4 *>(m.ks + i), z = *reinterpret_cast<const float4 *>(m.lvs + i),
+                                 w = *reinterpret_cast<const float4 *>(m.ivs + i);
+                    c[i] = f * y.x, c[i + 1] = f * y.y, c[i + 2] = f * y.z, c[i + 3] = f * y.w;
+                    lvs[i] = z.x, lvs[i + 1] = z.y, lvs[i + 2] = z.z, lvs[i + 3] = z.w;
+                    ivs[i] = w.x, ivs[i + 1] = w.y, ivs[i + 2] = w.z, ivs[i + 3] = w.w;
+                }
+                const uint32_t odd = m.odd & 0x1ffu;
+                const bool edge = j0 < all_from || j0 + kTile > all_to || odd;
                 dead = dead || !tc::bar_wait(bar(kSFull + x), sphase, limit);
                 sphase ^= 1u;
                 tc::fence_after();
-                uint32_t s[4][32];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    tc::ld32(s[i], tS + 32 * i);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    tc::wait_ld(s[i]);
-                const bool edge = j0 < all_from || j0 + kTile > all_to || m.bad;
                 if (edge) {
+                    // scaled here, -inf where the row does not see the token, and put back
+#pragma unroll 1
+                    for (int i = 0; i < kTile; i += 16) {
+                        uint32_t v[16];
+                        tc::ld16(v, tS + i);
+                        tc::wait_ld(v);
+                        const float by = f * m.ks[i >> 4];
+                        const int from = odd >> (i >> 4) & 1 ? kTile : lo - j0 - i, to = min(hi, p.len) - j0 - i;
 #pragma unroll
-                    for (int i = 0; i < 128; ++i) {
-                        const int j = j0 + i;
-                        const bool see = j >= lo && j < hi && j < p.len && !(m.bad >> (i >> 4) & 1);
-                        s[i >> 5][i & 31] = __float_as_uint(see ? __uint_as_float(s[i >> 5][i & 31]) * c[i >> 4] : -INFINITY);
+                        for (int e = 0; e < 16; ++e)
+                            v[e] = __float_as_uint(e >= from && e < to ? __uint_as_float(v[e]) * by : -INFINITY);
+                        tc::st16(tS + i, v);
                     }
+                    tc::wait_st();
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         c[i] = 1.f;
                 }
-                float now = -INFINITY, wnow = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float g = __uint_as_float(s[i >> 1][16 * (i & 1)]);
-                    if (c[i] >= 0.f) {
-#pragma unroll
-                        for (int e = 1; e < 16; ++e)
-                            g = fmaxf(g, __uint_as_float(s[i >> 1][16 * (i & 1) + e]));
-                    } else {
-#pragma unroll
-                        for (int e = 1; e < 16; ++e)
-                            g = fminf(g, __uint_as_float(s[i >> 1][16 * (i & 1) + e]));
-                    }
-                    g *= c[i];
-                    now = fmaxf(now, g);
-                    wnow = fmaxf(wnow, g + m.lvs[i]);
-                }
-                const bool move = now > top + kAttnLift || wnow > wtop + kAttnLift;
-                if (__any_sync(SFAR_FULL, move)) {
-                    const float next = fmaxf(top, now), wnext = fmaxf(wtop, wnow);
-                    const float keep = wtop == -INFINITY ? 1.f : ex2(wtop - wnext);      // o is 0 then, or NaN
-                    sum *= top == -INFINITY ? 1.f : ex2(top - next);
-                    top = next;
-                    wtop = wnext;
-                    if (k > 0) {
-                        // the scores' barrier says that the products before are complete
+                // The weights are formed against the reference as it stands.  Only if they come out large (or there is
+                // none yet) is the tile's largest looked for, the reference moved and the weights formed again.
+                uint32_t w[64];
+                float tile;
+                bool look = __any_sync(SFAR_FULL, wtop == -INFINITY);
 #pragma unroll 1
-                        for (int i = 0; i < D; i += 16) {
-                            uint32_t o[16];
-                            tc::ld16(o, tO + i);
-                            tc::wait_ld(o);
+                for (bool looked = false;; looked = true) {
+                    if (look) {
+                        float now = -INFINITY;
+#pragma unroll 1
+                        for (int i = 0; i < kTile; i += 16) {
+                            uint32_t v[16];
+                            tc::ld16(v, tS + i);
+                            tc::wait_ld(v);
+                            now = fmaxf(now, max16(v) * (edge ? 1.f : f * m.ks[i >> 4]) + m.lvs[i >> 4]);
+                        }
+                        const float next = fmaxf(wtop, now);
+                        const float keep = wtop == -INFINITY ? 1.f : ex2(wtop - next);   // o is 0 then, or NaN
+                        sum *= keep;
+                        wtop = next;
+                        if (k > 0) {
+                            // the scores' barrier says that the products before are complete
+#pragma unroll 1
+                            for (int i = 0; i < D; i += 16) {
+                                uint32_t o[16];
+                                tc::ld16(o, tO + i);
+                                tc::wait_ld(o);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-                            tc::st16(tO + i, o);
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                                tc::st16(tO + i, o);
+                            }
                         }
                     }
-                }
-                const float ref = top == -INFINITY ? 0.f : top;
-                const uint64_t nref = tc::pack2(-ref, -ref);
-                uint64_t add = 0ull;
+                    const float ref = wtop == -INFINITY ? 0.f : wtop;
+                    uint32_t s[2][32];
+                    tile = 0.f;
+                    float more = 0.f;
+                    tc::ld32(s[0], tS);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t w[16];
+                    for (int i = 0; i < 4; ++i) {
+                        tc::wait_ld(s[i & 1]);
+                        if (i < 3)
+                            tc::ld32(s[(i + 1) & 1], tS + 32 * (i + 1));
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int gi = 2 * i + h;
-                        const float by = m.sign[gi] * (wtop == -INFINITY ? 0.f : ex2(ref + m.lvs[gi] - wtop));
-                        const uint64_t c2 = tc::pack2(c[gi], c[gi]), by2 = tc::pack2(by, by);
+                        for (int h = 0; h < 2; ++h) {
+                            const int gi = 2 * i + h;
+                            const uint64_t c2 = tc::pack2(c[gi], c[gi]), off = tc::pack2(lvs[gi] - ref, lvs[gi] - ref);
+                            uint64_t add = 0ull;
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const float2 y = tc::unpack2(tc::fma2(tc::pack2u(s[i][16 * h + e], s[i][16 * h + e + 1]), c2, nref));
-                            const uint64_t pp = tc::pack2(ex2(y.x), ex2(y.y));
-                            add = tc::add2(add, pp);
-                            const float2 z = tc::unpack2(tc::mul2(pp, by2));
-                            w[8 * h + e / 2] = half2_of(z.x, z.y);
+                            for (int e = 0; e < 16; e += 2) {
+                                const float2 y = tc::unpack2(tc::fma2(tc::pack2u(s[i & 1][16 * h + e], s[i & 1][16 * h + e + 1]), c2, off));
+                                const float a0 = ex2(y.x), a1 = ex2(y.y);
+                                add = tc::add2(add, tc::pack2(a0, a1));
+                                w[16 * i + 8 * h + e / 2] = half2_of(a0, a1);
+                            }
+                            const float2 y = tc::unpack2(add);
+                            tile += y.x + y.y;
+                            more = fmaf(y.x + y.y, ivs[gi], more);
                         }
                     }
-                    tc::st16(tS + 16 * i, w);
+                    // a tile's weights of up to 2^14 in all: none leaves binary16's range
+                    look = __any_sync(SFAR_FULL, !(tile <= 16384.f));
+                    if (!look || looked) {
+                        sum += more;
+                        break;
+                    }
                 }
-                const float2 y = tc::unpack2(add);
-                sum += y.x + y.y;
+#pragma unroll
+                for (int i = 0; i < 64; i += 16) {
+                    uint32_t part[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        part[e] = w[i + e];
+                    tc::st16(tS + i, part);
+                }
                 tc::wait_st();
                 tc::fence_before();
                 __syncwarp();
@@ -397,17 +447,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             const bool part = p.tiles < p.all;
             const long long from = u - (p.tile0 - p.begin), to = from + p.all;
             const long long c0 = ((from + 1) * N - 1) / U, c1 = (to * N - 1) / U;
-            // [element / 4][row] and the references last, so that neighbouring rows are neighbours
+            // [element / 4][row] and the reference last, so that neighbouring rows are neighbours
             auto slot = [&](long long cta, int which) {
                 return reinterpret_cast<float4 *>(a.part) + ((size_t)cta * 2 + which) * (kRows * (D / 4 + 1));
             };
             float4 *dst = slot(blockIdx.x, p.tile0 == p.begin ? 1 : 0);
-            SfarAttnState<4> mineS;
-            mineS.reference(top, wtop);
-            mineS.add(top, sum, wtop);
-            const float inv = mineS.factor();
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;         // 0: the row attends to nothing
             uint16_t *out = a.out[r] + (long long)(p.first + n / a.G) * a.ots + (long long)(hk * a.G + n % a.G) * a.ohs;
-            const bool poisoned = s_nan[1] >= 0;
+            const int *nan = s_nan[odd_piece];
+            odd_piece ^= 1;
             if (mine) {
 #pragma unroll 1
                 for (int i = 0; i < D; i += 16) {
@@ -418,9 +466,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
                         v[e] = __uint_as_float(o[e]);
-                    if (poisoned && row && !dead) {
+                    if (nan[1] >= 0 && row && !dead) {
                         // values that were NaN and taken out: put back for the rows that see them
-                        const int from_j = max(max(lo, s_nan[0]), p.tile0 * kTile), to_j = min(min(hi, s_nan[1] + 1), (p.tile0 + p.tiles) * kTile);
+                        const int from_j = max(max(lo, nan[0]), p.tile0 * kTile), to_j = min(min(hi, nan[1] + 1), (p.tile0 + p.tiles) * kTile);
                         for (int j = from_j; j < to_j; ++j) {
                             const int page = a.table[(size_t)p.b * a.W + (j >> a.shift)];
                             if ((unsigned)page >= (unsigned)a.pages)
@@ -451,53 +499,58 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                 if (lane == 0)
                     tc::bar_arrive(bar(kOEmpty + x));
                 if (part && row)
-                    __stcg(dst + D / 4 * kRows + rho, make_float4(top, sum, wtop, 0.f));
+                    __stcg(dst + D / 4 * kRows + rho, make_float4(wtop, sum, wtop, 0.f));
             }
-            softmax_sync();                        // every row has been left in the workspace, every thread has read s_nan
-            if (tid == 0) {
-                s_nan[0] = INT_MAX;                // the next piece's values are converted after its queries are in place
-                s_nan[1] = -1;
-            }
-            if (part) {
+            if (mine && part) {
+                // the last of the row tile's CTAs joins its parts in order; the two tiles of rows separately
                 __threadfence();
-                softmax_sync();
-                if (tid == 0) {
-                    const int done = atomicAdd(a.arrived + c0, 1);
-                    s_last = done == (int)(c1 - c0);
-                    if (s_last)
-                        a.arrived[c0] = 0;         // for the next call
+                tile_sync(x);
+                if ((tid & 127) == 0) {
+                    int *arrived = a.arrived + 2 * c0 + x;
+                    const int done = atomicAdd(arrived, 1);
+                    s_last[x] = done == (int)(c1 - c0);
+                    if (s_last[x])
+                        *arrived = 0;              // for the next call
                 }
-                softmax_sync();
-                if (s_last && row) {
+                tile_sync(x);
+                if (s_last[x] && row) {
                     __threadfence();
                     SfarAttnState<4> st;
+#pragma unroll 4
                     for (long long cta = c0; cta <= c1; ++cta) {
                         const float4 t = __ldcg(slot(cta, cta == c0) + D / 4 * kRows + rho);
                         st.reference(t.x, t.z);
                     }
+#pragma unroll 4
                     for (long long cta = c0; cta <= c1; ++cta) {
                         const float4 t = __ldcg(slot(cta, cta == c0) + D / 4 * kRows + rho);
                         st.add(t.x, t.y, t.z);
                     }
                     const float by = st.factor();
 #pragma unroll 1
-                    for (int i = 0; i < D; i += 8) {
-                        float v[8] = {};
+                    for (int i = 0; i < D; i += 32) {
+                        float v[32] = {};
+#pragma unroll 1
                         for (long long cta = c0; cta <= c1; ++cta) {
                             const float4 *src = slot(cta, cta == c0) + rho;
-                            const float4 t = __ldcg(src + D / 4 * kRows), y = __ldcg(src + i / 4 * kRows), z = __ldcg(src + (i / 4 + 1) * kRows);
+                            const float4 t = __ldcg(src + D / 4 * kRows);
+                            float4 y[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                y[e] = __ldcg(src + (i / 4 + e) * kRows);
                             const float w = t.z == -INFINITY ? 1.f : ex2(t.z - st.wtop);
-                            v[0] += w * y.x;
-                            v[1] += w * y.y;
-                            v[2] += w * y.z;
-                            v[3] += w * y.w;
-                            v[4] += w * z.x;
-                            v[5] += w * z.y;
-                            v[6] += w * z.z;
-                            v[7] += w * z.w;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                v[4 * e] += w * y[e].x;
+                                v[4 * e + 1] += w * y[e].y;
+                                v[4 * e + 2] += w * y[e].z;
+                                v[4 * e + 3] += w * y[e].w;
+                            }
                         }
-                        st_v4(out + i, make_uint4(tc::bf16x2(v[0] * by, v[1] * by), tc::bf16x2(v[2] * by, v[3] * by),
-                                                  tc::bf16x2(v[4] * by, v[5] * by), tc::bf16x2(v[6] * by, v[7] * by)));
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            st_v4(out + i + e, make_uint4(tc::bf16x2(v[e] * by, v[e + 1] * by), tc::bf16x2(v[e + 2] * by, v[e + 3] * by),
+                                                          tc::bf16x2(v[e + 4] * by, v[e + 5] * by), tc::bf16x2(v[e + 6] * by, v[e + 7] * by)));
                     }
                 }
             }
@@ -506,59 +559,83 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
         if (dead && lane == 0)
             sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (warp < 12) {
+        if (warp < kCopyWarp) {
             // --------------------------------------- values: e4m3 -> binary16
             tc::Ring<kVStages> vs;
             tc::Ring<kHStages> hs;
             tc::Ring<kMeta> ms;
             const int ct = tid - 256;
-            uint32_t qphase = 0;
+            // this thread's 16-byte chunk c of tokens ct / kC, + 32 kWiden / kC, ...: the swizzle's bits of a token repeat
+            constexpr int kC = D / 16, kSteps = kTile * kC / (32 * kWiden), kFrom = 32 * kWiden * 16, kTo = 32 * kWiden / kC * 128;
+            static_assert((32 * kWiden / kC) % 8 == 0 && kSteps % 4 == 0, "a step keeps the swizzle");
+            const int tok0 = ct / kC, c = ct % kC;
+            const int from = tok0 * D + ((D == 128 ? c ^ (tok0 & 7) : c ^ ((tok0 >> 1) & 3)) << 4);
+            // 64 elements (128 bytes) of a token to a row, swizzled; the second 64 in a block of their own.  The two
+            // halves of a chunk go to chunks 2 (c & 3) and + 1; c & 4 takes them in the other order, so that 8 lanes
+            // meet in no bank.
+            const int at = 2 * (c & 3) + (c >> 2 & 1);
+            const int to = (c >> 2) * (kTile * 128) + tok0 * 128 + ((at ^ (tok0 & 7)) << 4), flip = c >> 2 & 1;
+            bool dead = false;
+            uint32_t qphase = 0, ophase = 0;
+            int before = 0;                        // rows of the piece before
             for (long long u = u0; u < u1;) {
                 const Piece p = work.at(u, u1);
-                // the queries of a piece are in place once the piece before has been written out
+                // the first tile's queries are in place once the piece before has been written out
                 dead = dead || !tc::bar_wait(bar(kQFull), qphase, limit);
+                if (before > 128) {                // the second tile of rows of the piece before, if it had one
+                    dead = dead || !tc::bar_wait(bar(kOEmpty + 1), ophase, limit);
+                    ophase ^= 1u;
+                }
+                before = min(kRows, p.count * a.G - p.rt * kRows);
+                int *nan = s_nan[qphase];
                 qphase ^= 1u;
+                if (ct == 0) {                     // of the piece before, for the piece after
+                    s_nan[qphase][0] = INT_MAX;
+                    s_nan[qphase][1] = -1;
+                }
+                // tiles that every row of the piece sees whole
+                const int pos0 = p.len - p.count + p.rt * kRows / a.G;
+                const int pos1 = p.len - p.count + min(p.count - 1, (p.rt * kRows + kRows - 1) / a.G);
+                const int all_from = a.window ? max(0, pos1 - a.window + 1) : 0, all_to = min(p.len, pos0 + 1);
                 for (int k = 0; k < p.tiles; ++k) {
                     const int j0 = (p.tile0 + k) * kTile;
                     dead = dead || !tc::bar_wait(bar(kMFull + ms.slot), ms.phase, limit);
-                    const int bad = meta[ms.slot].bad;
+                    const uint32_t odd = meta[ms.slot].odd & ~0x100u;
                     dead = dead || !tc::bar_wait(bar(kVFull + vs.slot), vs.phase, limit) ||
                            !tc::bar_wait(bar(kHEmpty + hs.slot), hs.phase ^ 1u, limit);
-                    const unsigned char *src = gen + L::oV + vs.slot * L::kK;
-                    unsigned char *dst = gen + L::oH + hs.slot * L::kH;
-                    constexpr int kC = D / 16;     // 16-byte chunks of a token
-#pragma unroll 2
-                    for (int i = ct; i < kTile * kC; i += 128) {
-                        const int tok = i / kC, c = i % kC, j = j0 + tok;
-                        const int from = D == 128 ? c ^ (tok & 7) : c ^ ((tok >> 1) & 3);
-                        uint4 v = *reinterpret_cast<const uint4 *>(src + tok * D + from * 16);
-                        if (j >= p.len || (bad >> (tok >> 4) & 1))
-                            v = make_uint4(0, 0, 0, 0);
-                        uint32_t *w = &v.x;
-                        uint32_t is = 0;
+                    const unsigned char *src = gen + L::oV + vs.slot * L::kK + from;
+                    unsigned char *dst = gen + L::oH + hs.slot * L::kH + to;
+                    if (j0 >= all_from && j0 + kTile <= all_to && !odd) {
+#pragma unroll 1
+                        for (int n = 0; n < kSteps; n += 4) {
+                            uint4 v[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            is |= (w[e] & 0x7f7f7f7fu) + 0x01010101u;
-                        if (is & 0x80808080u) {
-                            // NaN reaches only the rows that see the token: taken out here, put back at the end
+                            for (int b = 0; b < 4; ++b)
+                                v[b] = *reinterpret_cast<const uint4 *>(src + (n + b) * kFrom);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                w[e] &= ~__vcmpeq4(w[e] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                            atomicMin(&s_nan[0], j);
-                            atomicMax(&s_nan[1], j);
+                            for (int b = 0; b < 4; ++b)
+                                widen(dst + (n + b) * kTo, flip, v[b]);
                         }
-                        uint32_t h[8];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            h[2 * e] = cvt_f16x2_e4m3(w[e]);
-                            h[2 * e + 1] = cvt_f16x2_e4m3(w[e] >> 16);
+                    } else {
+                        // some row does not see some token: places that hold none are zeros, and a NaN, which
+                        // would reach every row, is taken out here and put back at the end
+#pragma unroll 1
+                        for (int n = 0; n < kSteps; ++n) {
+                            const int tok = ct / kC + n * (32 * kWiden / kC);
+                            uint4 v = *reinterpret_cast<const uint4 *>(src + n * kFrom);
+                            const int g = tok >> 4;
+                            if (j0 + tok >= p.len || ((odd | odd >> 16) >> g & 1))
+                                v = make_uint4(0, 0, 0, 0);
+                            if (odd >> (24 + g) & 1)
+                                v = make_uint4(v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u);
+                            const uint4 is = make_uint4(nan_bytes(v.x), nan_bytes(v.y), nan_bytes(v.z), nan_bytes(v.w));
+                            if (is.x | is.y | is.z | is.w) {
+                                v = make_uint4(v.x & ~is.x, v.y & ~is.y, v.z & ~is.z, v.w & ~is.w);
+                                atomicMin(&nan[0], j0 + tok);
+                                atomicMax(&nan[1], j0 + tok);
+                            }
+                            widen(dst + n * kTo, flip, v);
                         }
-                        // 64 elements (128 bytes) of a token to a row, swizzled; the second 64 in a block of their own
-                        unsigned char *to = dst + (c >> 2) * (kTile * 128) + tok * 128;
-                        const int at = 2 * (c & 3);
-                        *reinterpret_cast<uint4 *>(to + ((at ^ (tok & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-                        *reinterpret_cast<uint4 *>(to + (((at + 1) ^ (tok & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
                     }
                     tc::fence_async();
                     __syncwarp();
@@ -572,12 +649,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                 }
                 u += p.tiles;
             }
-        } else if (warp == 12) {
+        } else if (warp == kCopyWarp) {
             // ------------------------------------------------------------ copies
             tc::Ring<kKStages> kr;
             tc::Ring<kVStages> vr;
             tc::Ring<kMeta> ms;
             uint32_t issued = 0;
+            bool dead = false;
             const uint64_t often = tc::evict_last();
             const int per = min(1 << a.shift, SFAR_ATTN_TILE), boxes = kTile / per;   // tokens of one copy
             for (long long u = u0; u < u1 && !dead;) {
@@ -609,15 +687,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                     __syncwarp();
                     const int of = lane * 16 / per;                      // the copy that 16 tokens lie in
                     const float k16 = __shfl_sync(SFAR_FULL, ks, of & 31), v16 = __shfl_sync(SFAR_FULL, vs, of & 31);
-                    const unsigned none = __ballot_sync(SFAR_FULL, lane < kTile / 16 && !(any >> (of & 31) & 1u));
+                    const bool sixteen = lane < kTile / 16, there = any >> (of & 31) & 1u;
+                    const uint32_t none = __ballot_sync(SFAR_FULL, sixteen && !there), minus = __ballot_sync(SFAR_FULL, sixteen && v16 < 0.f);
+                    const uint32_t zero = __ballot_sync(SFAR_FULL, sixteen && there && v16 == 0.f);
+                    const bool negative = __any_sync(SFAR_FULL, ks < 0.f);
                     Meta &m = meta[ms.slot];
-                    if (lane < kTile / 16) {
+                    if (sixteen) {
+                        const float v = v16 == 0.f ? 1.f : fabsf(v16);
                         m.ks[lane] = k16;
-                        m.lvs[lane] = lg2(fabsf(v16));
-                        m.sign[lane] = copysignf(1.f, v16);
+                        m.lvs[lane] = lg2(v);
+                        m.ivs[lane] = 1.f / v;
                     }
                     if (lane == 0)
-                        m.bad = (int)none;
+                        m.odd = none | (negative ? 256u : 0u) | zero << 16 | minus << 24;
                     __syncwarp();
                     if (lane == 0) {
                         tc::bar_arrive(bar(kMFull + ms.slot));
@@ -647,20 +729,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                 for (uint32_t i = issued - min(issued, (uint32_t)kVStages); i < issued; ++i)
                     tc::bar_wait(bar(kVFull + i % kVStages), (i / kVStages) & 1u, limit);
             }
-        } else if (warp == 13) {
+        } else {
             // -------------------------------------------------------------- MMAs
             constexpr uint32_t idS = tc::idesc_e4m3(128, kTile);
             // binary16 weights in tensor memory times values with the head contiguous (N-major)
             constexpr uint32_t idO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);
             tc::Ring<kKStages> kr;
             tc::Ring<kHStages> hr;
-            uint32_t qphase = 0, pphase[2] = {0, 0}, ofree[2] = {1, 1};
+            bool dead = false;
+            uint32_t qphase[2] = {0, 0}, pphase[2] = {0, 0}, ofree[2] = {1, 1};
             for (long long u = u0; u < u1 && !dead;) {
                 const Piece p = work.at(u, u1);
                 const int tiles = min(kRows, p.count * a.G - p.rt * kRows) > 128 ? 2 : 1;
-                if (lane == 0) {
-                    dead = !tc::bar_wait(bar(kQFull), qphase, limit);
-                    tc::fence_after();
+                if (tc::elect_one()) {             // the same lane every time: the rings stay in its registers
                     for (int k = 0; k <= p.tiles && !dead; ++k) {
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
@@ -691,12 +772,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                                     tc::commit(bar(kOFull + x));
                             }
                             if (k < p.tiles) {
-                                if (x == 0) {
-                                    dead = !tc::bar_wait(bar(kKFull + kr.slot), kr.phase, limit);
-                                    if (dead)
-                                        continue;
-                                    tc::fence_after();
+                                if (k == 0) {
+                                    dead = !tc::bar_wait(bar(kQFull + x), qphase[x], limit);
+                                    qphase[x] ^= 1u;
                                 }
+                                if (x == 0)
+                                    dead = dead || !tc::bar_wait(bar(kKFull + kr.slot), kr.phase, limit);
+                                if (dead)
+                                    continue;
+                                tc::fence_after();
                                 const uint64_t dk = tc::desc_k<D>(mem + L::oK + kr.slot * L::kK);
                                 const uint64_t dq = tc::desc_k<D>(mem + L::oQ + x * 2 * L::kQ);
 #pragma unroll
@@ -713,12 +797,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                             }
                         }
                     }
-                    qphase ^= 1u;
                 }
                 dead = __any_sync(SFAR_FULL, dead);
                 u += p.tiles;
             }
-            if (lane == 0) {
+            if (tc::elect_one()) {
                 if (dead)
                     sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
                 // every MMA and every arrival it causes is done before the CTA leaves
@@ -730,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
     __syncwarp();
     tc::fence_before();
     __syncthreads();
-    if (warp == 13)
+    if (warp == kMmaWarp)
         tc::tmem_free<1>(tmem, 512);
 }
 

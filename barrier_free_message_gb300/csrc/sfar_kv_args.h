@@ -47,7 +47,7 @@ struct SfarAttnArgs {
     uint16_t *out[SFAR_MAX_R];
     const int *table, *lens, *starts;
     float *part;                            // partial results, two per CTA
-    int *arrived;                           // [grid] parts of the row tile that began in a CTA; 0 between calls
+    int *arrived;                           // [2 * grid] parts of the row tile that began in a CTA; 0 between calls
     SfarCtl *ctl;
     long long qts, qhs, ots, ohs;
     float scale;

@@ -160,7 +160,7 @@ sfar_kv_t *sfar_kv_create(int R, int q_heads, int kv_heads, int head_dim, int pa
             return fail(encode ? SFAR_ERR_INVALID : SFAR_ERR_UNSUPPORTED);
         }
     const size_t ctas = (size_t)sms * SFAR_ATTN_CTAS;
-    const size_t o_arrived = 256, o_part = (o_arrived + ctas * 4 + 255) / 256 * 256;
+    const size_t o_arrived = 256, o_part = (o_arrived + ctas * 8 + 255) / 256 * 256;
     const size_t few = ctas * 2 * 16, many = (size_t)sms * 2 * SFAR_PROMPT_ROWS;     // rows of partial results
     const size_t bytes = o_part + (few > many ? few : many) * ((size_t)head_dim + 4) * 4;
     if (cudaMalloc(&h->ws, bytes) != cudaSuccess) {
