@@ -18,8 +18,8 @@
 // the sum is of weight / value scale: two value scales of one request may be
 // up to 2^100 apart.
 //
-// A CTA takes 256 rows as two tiles of 128, each with a softmax warpgroup (a
-// thread per row: no shuffles).  The tensor core alternates: while it runs
+// A CTA takes 256 rows as two tiles of 128, each with eight softmax warps (two
+// threads per row, a half of its columns each: no shuffles).  The tensor core alternates: while it runs
 // O_B += W_B V and S_B = Q_B K' of one tile, the other's softmax works.  Warp
 // 12   The
 // accumulator is rescaled, in tensor memory, only when a reference moves.
@@ -35,8 +35,10 @@ namespace {
 
 constexpr int kTile = 128;                         // cached tokens per step
 constexpr int kRows = SFAR_PROMPT_ROWS;            // query rows per CTA: two tiles of 128
-constexpr int kThreads = 384;                      // 8 softmax warps, kWiden that widen values, one copies, one issues
-constexpr int kWiden = 2, kCopyWarp = 8 + kWiden, kMmaWarp = kCopyWarp + 1;
+constexpr int kSoft = 16;                          // softmax warps
+constexpr int kWiden = 2, kCopyWarp = kSoft + kWiden, kMmaWarp = kCopyWarp + 1;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kOver = 6;                           // what a row tile costs beside its tiles, in tiles
 constexpr int kKStages = 3, kVStages = 2, kHStages = 2, kMeta = 4;
 
 template <int D> struct Lay {
@@ -70,8 +72,10 @@ enum Bar {                                         // barriers, by index
 
 // One piece: 256 rows of a request and a run of its tiles.
 struct Piece {
+    long long at;               // its first place on the line
     int plane, b, rt;           // rank * Hk + head; request; row tile
-    int tile0, tiles;           // first tile of this piece (in tiles of the context), how many
+    int tile0, tiles;           // first tile of this piece (in tiles of the context), how many (may be none)
+    int units;                  // places on the line: tiles, and the row tile's kOver if they are this piece's
     int begin, all;             // first tile of the whole row tile, and its count
     int len, count, first;      // context, new tokens, row of the first new token
 };
@@ -93,6 +97,7 @@ struct Work {
     {
         const int lane = threadIdx.x & 31;
         Piece p;
+        p.at = u;
         const uint32_t S = upto[a.B];
         p.plane = (int)(u / S);
         const uint32_t v = (uint32_t)(u - (long long)p.plane * S);
@@ -113,7 +118,7 @@ struct Work {
             int begin = 0, all = 0;
             if (rt0 + lane < n)
                 range(p.len, p.count, rt0 + lane, begin, all);
-            uint32_t sum = (uint32_t)all;
+            uint32_t sum = rt0 + lane < n ? (uint32_t)all + kOver : 0u;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const uint32_t o = __shfl_up_sync(SFAR_FULL, sum, d);
@@ -126,13 +131,25 @@ struct Work {
                 p.rt = rt0 + l;
                 p.begin = __shfl_sync(SFAR_FULL, begin, l);
                 p.all = __shfl_sync(SFAR_FULL, all, l);
-                const int k = (int)(w - (__shfl_sync(SFAR_FULL, sum, l) - (uint32_t)p.all));
+                const int k = (int)(w - (__shfl_sync(SFAR_FULL, sum, l) - (uint32_t)(p.all + kOver)));
                 p.tile0 = p.begin + k;
-                p.tiles = (int)min((long long)(p.all - k), end - u);
+                p.units = (int)min((long long)(p.all + kOver - k), end - u);
+                p.tiles = max(0, min(p.units, p.all - k));
                 return p;
             }
             w -= __shfl_sync(SFAR_FULL, sum, 31);
         }
+    }
+    // the next piece with tiles from place u on, and u past it; false: none before `end`
+    __device__ __forceinline__ bool take(long long &u, long long end, Piece &p) const
+    {
+        while (u < end) {
+            p = at(u, end);
+            u += p.units;
+            if (p.tiles > 0)
+                return true;
+        }
+        return false;
     }
 };
 
@@ -147,6 +164,18 @@ __device__ __forceinline__ void widen(unsigned char *to, int flip, const uint4 &
     *reinterpret_cast<uint4 *>(to) = flip ? hi : lo;
     *reinterpret_cast<uint4 *>((uintptr_t)to ^ 16) = flip ? lo : hi;
 }
+// 32 bytes of a row of the result: one store if they are aligned to it
+__device__ __forceinline__ void st32(uint16_t *p, const uint32_t (&v)[8])
+{
+    if (((uintptr_t)p & 31) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+                     "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        st_v4(p, make_uint4(v[0], v[1], v[2], v[3]));
+        st_v4(p + 8, make_uint4(v[4], v[5], v[6], v[7]));
+    }
+}
 // the largest of 16 values, NaN left out unless all are
 __device__ __forceinline__ float max16(const uint32_t *v)
 {
@@ -157,8 +186,18 @@ __device__ __forceinline__ float max16(const uint32_t *v)
                      fmaxf(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
     return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
-// the four warps of a tile's softmax
-__device__ __forceinline__ void tile_sync(int x) { asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory"); }
+// The eight warps of a tile's softmax; the two warps that share 32 rows.
+__device__ __forceinline__ void tile_sync(int x) { asm volatile("bar.sync %0, 256;" ::"r"(1 + x) : "memory"); }
+__device__ __forceinline__ void pair_sync(int pair) { asm volatile("bar.sync %0, 64;" ::"r"(3 + pair) : "memory"); }
+__device__ __forceinline__ bool pair_any(int pair, bool v)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\tbar.red.or.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"(3 + pair), "r"((uint32_t)v)
+                 : "memory");
+    return r != 0;
+}
 
 }  // namespace
 
@@ -170,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
     __shared__ __align__(8) unsigned long long bars[kBars];
     __shared__ __align__(16) Meta meta[kMeta];
     __shared__ uint32_t s_warp[kThreads / 32], s_tmem;
+    __shared__ float s_row[2][2][128];             // [tile][half]: what the two threads of a row tell each other
     __shared__ int s_last[2], s_nan[2][2];         // by the piece's parity: first and last context token whose value holds a NaN
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t mem = (tc::smem(dyn) + 1023u) & ~1023u;
@@ -181,8 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i) {
             const bool widen = (i >= kVEmpty && i < kVEmpty + kVStages) || (i >= kHFull && i < kHFull + kHStages);
-            const bool four = (i >= kPFull && i < kPFull + 2) || (i >= kOEmpty && i < kDrain);
-            tc::bar_init(bar(i), four ? 4 : widen ? kWiden : 1);
+            const bool eight = (i >= kPFull && i < kPFull + 2) || (i >= kOEmpty && i < kDrain);
+            tc::bar_init(bar(i), eight ? kSoft / 2 : widen ? kWiden : 1);
         }
         tc::bar_fence_init();
         tc::fence_async();
@@ -209,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             for (int rt = lane; rt < n; rt += 32) {
                 int begin, all;
                 work.range(len, count, rt, begin, all);
-                v += (uint32_t)all;
+                v += (uint32_t)(all + kOver);
             }
             v = __reduce_add_sync(SFAR_FULL, v);
             if (blockIdx.x == 0 && lane == 0)
@@ -239,18 +279,46 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
     const long long N = min((long long)gridDim.x, U);
     const long long u0 = blockIdx.x < N ? blockIdx.x * U / N : 0, u1 = blockIdx.x < N ? (blockIdx.x + 1) * U / N : 0;
 
-    if (warp < 8) {
+    if (warp < kSoft) {
         // -------------------------------------------------------------- softmax
         bool dead = false;                         // a wait gave up: go on without waiting
-        const int x = warp >> 2;                   // which tile of rows
-        const int rho = x * 128 + (warp & 3) * 32 + lane;
+        // two threads to a row of scores, and of the accumulator: the first half of the columns and the second
+        const int x = warp >> 3, half = warp >> 2 & 1, pair = x * 4 + (warp & 3);
+        const int lrow = (warp & 3) * 32 + lane, rho = x * 128 + lrow;
         const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
-        const uint32_t tS = tmem + x * 256 + lanes, tO = tS + 128;
+        const uint32_t tS = tmem + x * 256 + 64 * half + lanes, tO = tmem + x * 256 + 128 + D / 2 * half + lanes;
+        float *told = &s_row[x][half][lrow], *other = &s_row[x][half ^ 1][lrow];
+        unsigned char *qs = gen + L::oQ + x * 2 * L::kQ;             // this tile's queries: as they are, then split
         tc::Ring<kMeta> ms;
         uint32_t sphase = 0, ophase = 0;
         int odd_piece = 0;
-        for (long long u = u0; u < u1;) {
-            const Piece p = work.at(u, u1);
+        // a piece's query rows into shared memory, as they are: 256 (D = 128) or 128 bytes to a row
+        auto fetch = [&](const Piece &p) {
+            const int r = p.plane / a.Hk, hk = p.plane % a.Hk, rows = min(kRows, p.count * a.G - p.rt * kRows);
+            if (rows <= x * 128)
+                return;
+            // lane i < 16: where the warp's row i comes from
+            const int mine = x * 128 + (warp & 7) * 16 + (lane & 15), n = p.rt * kRows + mine;
+            const uint16_t *src = a.q[r];
+            if (mine < rows)
+                src += (long long)(p.first + n / a.G) * a.qts + (long long)(hk * a.G + n % a.G) * a.qhs;
+            constexpr int kC = D / 8;
+#pragma unroll 4
+            for (int i = 0; i < 16 * kC; i += 32) {
+                const int row = (i + lane) / kC, c = (i + lane) % kC;
+                const uint16_t *from = reinterpret_cast<const uint16_t *>(__shfl_sync(SFAR_FULL, (unsigned long long)src, row));
+                const int at = (warp & 7) * 16 + row;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem(qs) + at * 2 * D + ((c ^ (at & (kC - 1))) << 4)),
+                             "l"(from + c * 8), "r"(x * 128 + at < rows ? 16u : 0u)
+                             : "memory");
+            }
+        };
+        Piece p;
+        long long u = u0;
+        bool have = work.take(u, u1, p);
+        if (have)
+            fetch(p);
+        while (have) {
             const int r = p.plane / a.Hk, hk = p.plane % a.Hk;
             const int rows = min(kRows, p.count * a.G - p.rt * kRows);
             const bool mine = rows > x * 128;      // the tile has rows
@@ -258,30 +326,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             const bool row = rho < rows;
             float f = 0.f;
             if (mine) {
-                // this thread's query row, split, K-major with the swizzle of its length: the leading 4 bits of
-                // every element and the other 4
-                const uint16_t *src = a.q[r] + (long long)(p.first + (row ? n / a.G : 0)) * a.qts + (long long)(hk * a.G + n % a.G) * a.qhs;
+                // this thread's half of its query row, split, K-major with the swizzle of its length: the leading 4
+                // bits of every element and the other 4
+                constexpr int kC = D / 16;         // its 16-byte chunks
+                uint4 v[kC];
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                tile_sync(x);
                 uint32_t m = 0;
-                {
-                    uint4 v[D / 8];
 #pragma unroll
-                    for (int c = 0; c < D / 8; ++c)
-                        v[c] = row ? ld_nc_v4(src + c * 8) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c)
-                        m = sfar_max_abs2(sfar_max_abs2(sfar_max_abs2(sfar_max_abs2(m, v[c].x), v[c].y), v[c].z), v[c].w);
+                for (int c = 0; c < kC; ++c) {
+                    v[c] = *reinterpret_cast<const uint4 *>(qs + lrow * 2 * D + (((half * kC + c) ^ (lrow & (2 * kC - 1))) << 4));
+                    m = sfar_max_abs2(sfar_max_abs2(sfar_max_abs2(sfar_max_abs2(m, v[c].x), v[c].y), v[c].z), v[c].w);
                 }
                 m = sfar_max_half(m);
+                *told = __uint_as_float(m);
+                tile_sync(x);                      // every row has been read: the split ones go into its place
+                m = max(m, __float_as_uint(*other));
                 const bool special = m >= 0x7f80u;
                 const int e = special ? 127 : max((int)(m >> 7) - 127, -112);
                 const float up = sfar_exp2i(7 - e);
                 f = a.scale * 1.4426950408889634f * sfar_exp2i(max(e - 7, -126));
-                const int lrow = rho & 127;
-#pragma unroll 1
-                for (int c = 0; c < D / 16; ++c) {
-                    const uint4 v0 = row ? ld_nc_v4(src + c * 16) : make_uint4(0, 0, 0, 0);
-                    const uint4 v1 = row ? ld_nc_v4(src + c * 16 + 8) : make_uint4(0, 0, 0, 0);
-                    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+                for (int c = 0; c < kC; c += 2) {
+                    const uint32_t w[8] = {v[c].x, v[c].y, v[c].z, v[c].w, v[c + 1].x, v[c + 1].y, v[c + 1].z, v[c + 1].w};
                     uint32_t ph[8], pl[8];
 #pragma unroll
                     for (int y = 0; y < 8; ++y) {
@@ -299,8 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                                 ph[y] |= 0x7f00u;
                         }
                     }
-                    const int chunk = D == 128 ? c ^ (lrow & 7) : c ^ ((lrow >> 1) & 3);
-                    unsigned char *dst = gen + L::oQ + x * 2 * L::kQ + lrow * D + chunk * 16;
+                    const int at = (half * kC + c) / 2, chunk = D == 128 ? at ^ (lrow & 7) : at ^ ((lrow >> 1) & 3);
+                    unsigned char *dst = qs + lrow * D + chunk * 16;
                     *reinterpret_cast<uint4 *>(dst) = make_uint4(ph[0] | ph[1] << 16, ph[2] | ph[3] << 16, ph[4] | ph[5] << 16, ph[6] | ph[7] << 16);
                     *reinterpret_cast<uint4 *>(dst + L::kQ) = make_uint4(pl[0] | pl[1] << 16, pl[2] | pl[3] << 16, pl[4] | pl[5] << 16, pl[6] | pl[7] << 16);
                 }
@@ -313,35 +380,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             const int hi = row ? min(p.len, pos + 1) : INT_MAX, lo = row && a.window ? max(0, pos - a.window + 1) : 0;
             // tiles that every row of this warp sees whole
             const int all_from = __reduce_max_sync(SFAR_FULL, lo), all_to = min(p.len, __reduce_min_sync(SFAR_FULL, hi));
-            // log2 reference of the weights; sum: of weight / value scale
+            // log2 reference of the row's weights; sum: of this half's weight / value scale
             float wtop = -INFINITY, sum = 0.f;
             for (int k = 0; mine && k < p.tiles; ++k) {
-                const int j0 = (p.tile0 + k) * kTile;
+                const int j0 = (p.tile0 + k) * kTile + 64 * half;
                 dead = dead || !tc::bar_wait(bar(kMFull + ms.slot), ms.phase, limit);
                 const Meta &m = meta[ms.slot];
-                float c[8], lvs[8], ivs[8];
-#pragma unroll
-                for (int i = 0; i < 8; i += 4) {
-                    const float4 y = *reinterpret_cast<const float4 *>(m.ks + i), z = *reinterpret_cast<const float4 *>(m.lvs + i),
-                                 w = *reinterpret_cast<const float4 *>(m.ivs + i);
-                    c[i] = f * y.x, c[i + 1] = f * y.y, c[i + 2] = f * y.z, c[i + 3] = f * y.w;
-                    lvs[i] = z.x, lvs[i + 1] = z.y, lvs[i + 2] = z.z, lvs[i + 3] = z.w;
-                    ivs[i] = w.x, ivs[i + 1] = w.y, ivs[i + 2] = w.z, ivs[i + 3] = w.w;
-                }
-                const uint32_t odd = m.odd & 0x1ffu;
-                const bool edge = j0 < all_from || j0 + kTile > all_to || odd;
+                const float4 ks = *reinterpret_cast<const float4 *>(m.ks + 4 * half), lv = *reinterpret_cast<const float4 *>(m.lvs + 4 * half),
+                             iv = *reinterpret_cast<const float4 *>(m.ivs + 4 * half);
+                float c[4] = {f * ks.x, f * ks.y, f * ks.z, f * ks.w};
+                const float lvs[4] = {lv.x, lv.y, lv.z, lv.w}, ivs[4] = {iv.x, iv.y, iv.z, iv.w};
+                const uint32_t odd = m.odd;
+                const uint32_t none = odd >> (4 * half) & 15u;
+                const bool edge = j0 < all_from || j0 + 64 > all_to || none || (odd & 0x100u);
                 dead = dead || !tc::bar_wait(bar(kSFull + x), sphase, limit);
                 sphase ^= 1u;
                 tc::fence_after();
                 if (edge) {
                     // scaled here, -inf where the row does not see the token, and put back
 #pragma unroll 1
-                    for (int i = 0; i < kTile; i += 16) {
+                    for (int i = 0; i < 64; i += 16) {
                         uint32_t v[16];
                         tc::ld16(v, tS + i);
                         tc::wait_ld(v);
-                        const float by = f * m.ks[i >> 4];
-                        const int from = odd >> (i >> 4) & 1 ? kTile : lo - j0 - i, to = min(hi, p.len) - j0 - i;
+                        const float by = f * m.ks[4 * half + (i >> 4)];
+                        const int from = none >> (i >> 4) & 1 ? 64 : lo - j0 - i, to = min(hi, p.len) - j0 - i;
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
                             v[e] = __float_as_uint(e >= from && e < to ? __uint_as_float(v[e]) * by : -INFINITY);
@@ -349,33 +412,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                     }
                     tc::wait_st();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
+                    for (int i = 0; i < 4; ++i)
                         c[i] = 1.f;
                 }
                 // The weights are formed against the reference as it stands.  Only if they come out large (or there is
-                // none yet) is the tile's largest looked for, the reference moved and the weights formed again.
-                uint32_t w[64];
-                float tile;
-                bool look = __any_sync(SFAR_FULL, wtop == -INFINITY);
+                // none yet) is the row's largest looked for, the reference moved and the weights formed again.
+                uint32_t w[32];
+                bool look = __any_sync(SFAR_FULL, wtop == -INFINITY);          // the same in both warps of a pair
 #pragma unroll 1
                 for (bool looked = false;; looked = true) {
                     if (look) {
                         float now = -INFINITY;
 #pragma unroll 1
-                        for (int i = 0; i < kTile; i += 16) {
+                        for (int i = 0; i < 64; i += 16) {
                             uint32_t v[16];
                             tc::ld16(v, tS + i);
                             tc::wait_ld(v);
-                            now = fmaxf(now, max16(v) * (edge ? 1.f : f * m.ks[i >> 4]) + m.lvs[i >> 4]);
+                            now = fmaxf(now, max16(v) * (edge ? 1.f : f * m.ks[4 * half + (i >> 4)]) + m.lvs[4 * half + (i >> 4)]);
                         }
-                        const float next = fmaxf(wtop, now);
+                        *told = now;
+                        pair_sync(pair);
+                        const float next = fmaxf(wtop, fmaxf(now, *other));
                         const float keep = wtop == -INFINITY ? 1.f : ex2(wtop - next);   // o is 0 then, or NaN
                         sum *= keep;
                         wtop = next;
                         if (k > 0) {
                             // the scores' barrier says that the products before are complete
 #pragma unroll 1
-                            for (int i = 0; i < D; i += 16) {
+                            for (int i = 0; i < D / 2; i += 16) {
                                 uint32_t o[16];
                                 tc::ld16(o, tO + i);
                                 tc::wait_ld(o);
@@ -387,41 +451,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                         }
                     }
                     const float ref = wtop == -INFINITY ? 0.f : wtop;
-                    uint32_t s[2][32];
-                    tile = 0.f;
-                    float more = 0.f;
-                    tc::ld32(s[0], tS);
+                    uint32_t s[2][16];
+                    float tile = 0.f, more = 0.f;
+                    tc::ld16(s[0], tS);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         tc::wait_ld(s[i & 1]);
                         if (i < 3)
-                            tc::ld32(s[(i + 1) & 1], tS + 32 * (i + 1));
+                            tc::ld16(s[(i + 1) & 1], tS + 16 * (i + 1));
+                        const uint64_t c2 = tc::pack2(c[i], c[i]), off = tc::pack2(lvs[i] - ref, lvs[i] - ref);
+                        uint64_t add = 0ull;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int gi = 2 * i + h;
-                            const uint64_t c2 = tc::pack2(c[gi], c[gi]), off = tc::pack2(lvs[gi] - ref, lvs[gi] - ref);
-                            uint64_t add = 0ull;
-#pragma unroll
-                            for (int e = 0; e < 16; e += 2) {
-                                const float2 y = tc::unpack2(tc::fma2(tc::pack2u(s[i & 1][16 * h + e], s[i & 1][16 * h + e + 1]), c2, off));
-                                const float a0 = ex2(y.x), a1 = ex2(y.y);
-                                add = tc::add2(add, tc::pack2(a0, a1));
-                                w[16 * i + 8 * h + e / 2] = half2_of(a0, a1);
-                            }
-                            const float2 y = tc::unpack2(add);
-                            tile += y.x + y.y;
-                            more = fmaf(y.x + y.y, ivs[gi], more);
+                        for (int e = 0; e < 16; e += 2) {
+                            const float2 y = tc::unpack2(tc::fma2(tc::pack2u(s[i & 1][e], s[i & 1][e + 1]), c2, off));
+                            const float a0 = ex2(y.x), a1 = ex2(y.y);
+                            add = tc::add2(add, tc::pack2(a0, a1));
+                            w[8 * i + e / 2] = half2_of(a0, a1);
                         }
+                        const float2 y = tc::unpack2(add);
+                        tile += y.x + y.y;
+                        more = fmaf(y.x + y.y, ivs[i], more);
                     }
                     // a tile's weights of up to 2^14 in all: none leaves binary16's range
-                    look = __any_sync(SFAR_FULL, !(tile <= 16384.f));
+                    look = pair_any(pair, !(tile <= 8192.f));
                     if (!look || looked) {
                         sum += more;
                         break;
                     }
                 }
+                // in the first columns of this half's scores
 #pragma unroll
-                for (int i = 0; i < 64; i += 16) {
+                for (int i = 0; i < 32; i += 16) {
                     uint32_t part[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
@@ -438,14 +498,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             if (!mine)
                 for (int k = 0; k < p.tiles; ++k)
                     ms.next();
+            // the next piece's queries come in while this one is written out: the last scores are complete
+            Piece next;
+            have = work.take(u, u1, next);
+            if (have)
+                fetch(next);
             // --------------------------------------------------------- epilogue
             if (mine) {
+                *told = sum;
+                pair_sync(pair);
+                sum += *other;
                 dead = dead || !tc::bar_wait(bar(kOFull + x), ophase, limit);
                 ophase ^= 1u;
                 tc::fence_after();
             }
             const bool part = p.tiles < p.all;
-            const long long from = u - (p.tile0 - p.begin), to = from + p.all;
+            const long long from = p.at - (p.tile0 - p.begin), to = from + p.all;
             const long long c0 = ((from + 1) * N - 1) / U, c1 = (to * N - 1) / U;
             // [element / 4][row] and the reference last, so that neighbouring rows are neighbours
             auto slot = [&](long long cta, int which) {
@@ -456,9 +524,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             uint16_t *out = a.out[r] + (long long)(p.first + n / a.G) * a.ots + (long long)(hk * a.G + n % a.G) * a.ohs;
             const int *nan = s_nan[odd_piece];
             odd_piece ^= 1;
+            const int d0 = half * (D / 2);
             if (mine) {
 #pragma unroll 1
-                for (int i = 0; i < D; i += 16) {
+                for (int i = 0; i < D / 2; i += 16) {
                     uint32_t o[16];
                     tc::ld16(o, tO + i);
                     tc::wait_ld(o);
@@ -473,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                             const int page = a.table[(size_t)p.b * a.W + (j >> a.shift)];
                             if ((unsigned)page >= (unsigned)a.pages)
                                 continue;
-                            const uint8_t *vp = a.v[r] + (((long long)page * a.Hk + hk << a.shift) + (j & ((1 << a.shift) - 1))) * D + i;
+                            const uint8_t *vp = a.v[r] + (((long long)page * a.Hk + hk << a.shift) + (j & ((1 << a.shift) - 1))) * D + d0 + i;
                             for (int e = 0; e < 16; ++e)
                                 if ((vp[e] & 0x7f) == 0x7f)
                                     for (int z = 0; z < 16; ++z)
@@ -486,26 +555,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                     if (part) {
 #pragma unroll
                         for (int e = 0; e < 16; e += 4)
-                            __stcg(dst + (i + e) / 4 * kRows + rho, make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+                            __stcg(dst + (d0 + i + e) / 4 * kRows + rho, make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
                     } else {
+                        uint32_t b[8];
 #pragma unroll
-                        for (int e = 0; e < 16; e += 8)
-                            st_v4(out + i + e, make_uint4(tc::bf16x2(v[e] * inv, v[e + 1] * inv), tc::bf16x2(v[e + 2] * inv, v[e + 3] * inv),
-                                                          tc::bf16x2(v[e + 4] * inv, v[e + 5] * inv), tc::bf16x2(v[e + 6] * inv, v[e + 7] * inv)));
+                        for (int e = 0; e < 8; ++e)
+                            b[e] = tc::bf16x2(v[2 * e] * inv, v[2 * e + 1] * inv);
+                        st32(out + d0 + i, b);
                     }
                 }
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0)
                     tc::bar_arrive(bar(kOEmpty + x));
-                if (part && row)
+                if (part && row && half == 0)
                     __stcg(dst + D / 4 * kRows + rho, make_float4(wtop, sum, wtop, 0.f));
             }
             if (mine && part) {
                 // the last of the row tile's CTAs joins its parts in order; the two tiles of rows separately
                 __threadfence();
                 tile_sync(x);
-                if ((tid & 127) == 0) {
+                if ((tid & 255) == 0) {
                     int *arrived = a.arrived + 2 * c0 + x;
                     const int done = atomicAdd(arrived, 1);
                     s_last[x] = done == (int)(c1 - c0);
@@ -528,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                     }
                     const float by = st.factor();
 #pragma unroll 1
-                    for (int i = 0; i < D; i += 32) {
+                    for (int i = d0; i < d0 + D / 2; i += 32) {
                         float v[32] = {};
 #pragma unroll 1
                         for (long long cta = c0; cta <= c1; ++cta) {
@@ -548,14 +618,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                             }
                         }
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            st_v4(out + i + e, make_uint4(tc::bf16x2(v[e] * by, v[e + 1] * by), tc::bf16x2(v[e + 2] * by, v[e + 3] * by),
-                                                          tc::bf16x2(v[e + 4] * by, v[e + 5] * by), tc::bf16x2(v[e + 6] * by, v[e + 7] * by)));
+                        for (int h = 0; h < 32; h += 16) {
+                            uint32_t b[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                b[e] = tc::bf16x2(v[h + 2 * e] * by, v[h + 2 * e + 1] * by);
+                            st32(out + i + h, b);
+                        }
                     }
                 }
             }
-            u += p.tiles;
+            p = next;
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         if (dead && lane == 0)
             sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
     } else {
@@ -564,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             tc::Ring<kVStages> vs;
             tc::Ring<kHStages> hs;
             tc::Ring<kMeta> ms;
-            const int ct = tid - 256;
+            const int ct = tid - 32 * kSoft;
             // this thread's 16-byte chunk c of tokens ct / kC, + 32 kWiden / kC, ...: the swizzle's bits of a token repeat
             constexpr int kC = D / 16, kSteps = kTile * kC / (32 * kWiden), kFrom = 32 * kWiden * 16, kTo = 32 * kWiden / kC * 128;
             static_assert((32 * kWiden / kC) % 8 == 0 && kSteps % 4 == 0, "a step keeps the swizzle");
@@ -578,8 +653,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             bool dead = false;
             uint32_t qphase = 0, ophase = 0;
             int before = 0;                        // rows of the piece before
-            for (long long u = u0; u < u1;) {
-                const Piece p = work.at(u, u1);
+            Piece p;
+            for (long long u = u0; work.take(u, u1, p);) {
                 // the first tile's queries are in place once the piece before has been written out
                 dead = dead || !tc::bar_wait(bar(kQFull), qphase, limit);
                 if (before > 128) {                // the second tile of rows of the piece before, if it had one
@@ -647,7 +722,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                     hs.next();
                     ms.next();
                 }
-                u += p.tiles;
             }
         } else if (warp == kCopyWarp) {
             // ------------------------------------------------------------ copies
@@ -658,8 +732,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             bool dead = false;
             const uint64_t often = tc::evict_last();
             const int per = min(1 << a.shift, SFAR_ATTN_TILE), boxes = kTile / per;   // tokens of one copy
-            for (long long u = u0; u < u1 && !dead;) {
-                const Piece p = work.at(u, u1);
+            Piece p;
+            for (long long u = u0; !dead && work.take(u, u1, p);) {
                 const int r = p.plane / a.Hk, hk = p.plane % a.Hk;
                 const int *row = a.table + (size_t)p.b * a.W;
                 for (int k = 0; k < p.tiles; ++k) {
@@ -719,7 +793,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                     vr.next();
                     ms.next();
                 }
-                u += p.tiles;
             }
             if (dead && lane == 0) {
                 sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
@@ -738,8 +811,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             tc::Ring<kHStages> hr;
             bool dead = false;
             uint32_t qphase[2] = {0, 0}, pphase[2] = {0, 0}, ofree[2] = {1, 1};
-            for (long long u = u0; u < u1 && !dead;) {
-                const Piece p = work.at(u, u1);
+            Piece p;
+            for (long long u = u0; !dead && work.take(u, u1, p);) {
                 const int tiles = min(kRows, p.count * a.G - p.rt * kRows) > 128 ? 2 : 1;
                 if (tc::elect_one()) {             // the same lane every time: the rings stay in its registers
                     for (int k = 0; k <= p.tiles && !dead; ++k) {
@@ -763,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                                 const uint64_t dv = tc::desc_n128(mem + L::oH + hr.slot * L::kH, kTile * 128);
 #pragma unroll
                                 for (int i = 0; i < kTile / 16; ++i)
-                                    tc::mma_f16_ts(tO, tS + 8 * i, dv + 128 * i, idO, k > 1 || i > 0);
+                                    tc::mma_f16_ts(tO, tS + (i < 4 ? 8 * i : 32 + 8 * i), dv + 128 * i, idO, k > 1 || i > 0);
                                 if (x == tiles - 1) {
                                     tc::commit(bar(kHEmpty + hr.slot));
                                     hr.next();
@@ -799,7 +872,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                     }
                 }
                 dead = __any_sync(SFAR_FULL, dead);
-                u += p.tiles;
             }
             if (tc::elect_one()) {
                 if (dead)
