@@ -39,7 +39,7 @@ constexpr int kSoft = 16;                          // softmax warps
 constexpr int kWiden = 2, kCopyWarp = kSoft + kWiden, kMmaWarp = kCopyWarp + 1;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kOver = 6;                           // what a row tile costs beside its tiles, in tiles
-constexpr int kKStages = 3, kVStages = 2, kHStages = 2, kMeta = 4;
+constexpr int kKStages = 3, kVStages = 2, kHStages = 2, kMeta = 4, kPieces = 8;
 
 template <int D> struct Lay {
     static constexpr int kK = kTile * D, kH = kTile * D * 2, kQ = 128 * D;
@@ -66,7 +66,9 @@ enum Bar {                                         // barriers, by index
     kOFull = kPFull + 2,
     kOEmpty = kOFull + 2,
     kQFull = kOEmpty + 2,
-    kDrain = kQFull + 2,
+    kPiece = kQFull + 2,
+    kPieceFree = kPiece + kPieces,
+    kDrain = kPieceFree + kPieces,
     kBars = kDrain + 1
 };
 
@@ -188,6 +190,15 @@ __device__ __forceinline__ float max16(const uint32_t *v)
 }
 // The eight warps of a tile's softmax; the two warps that share 32 rows.
 __device__ __forceinline__ void tile_sync(int x) { asm volatile("bar.sync %0, 256;" ::"r"(1 + x) : "memory"); }
+__device__ __forceinline__ bool tile_any(int x, bool v)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\tbar.red.or.pred q, %1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"(1 + x), "r"((uint32_t)v)
+                 : "memory");
+    return r != 0;
+}
 __device__ __forceinline__ void pair_sync(int pair) { asm volatile("bar.sync %0, 64;" ::"r"(3 + pair) : "memory"); }
 __device__ __forceinline__ bool pair_any(int pair, bool v)
 {
@@ -209,8 +220,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
     __shared__ __align__(8) unsigned long long bars[kBars];
     __shared__ __align__(16) Meta meta[kMeta];
     __shared__ uint32_t s_warp[kThreads / 32], s_tmem;
-    __shared__ float s_row[2][2][128];             // [tile][half]: what the two threads of a row tell each other
-    __shared__ int s_last[2], s_nan[2][2];         // by the piece's parity: first and last context token whose value holds a NaN
+    __shared__ Piece s_piece[kPieces];             // what the copying warp has begun with; no tiles: the end
+    __shared__ float s_row[3][2][2][128];          // [what][tile][half]: what the two threads of a row tell each other
+    __shared__ int s_last[2], s_nan[4][2];         // by the piece, modulo 4: first and last context token whose value holds a NaN
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t mem = (tc::smem(dyn) + 1023u) & ~1023u;
     unsigned char *gen = dyn + (mem - tc::smem(dyn));
@@ -221,14 +233,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i) {
             const bool widen = (i >= kVEmpty && i < kVEmpty + kVStages) || (i >= kHFull && i < kHFull + kHStages);
-            const bool eight = (i >= kPFull && i < kPFull + 2) || (i >= kOEmpty && i < kDrain);
-            tc::bar_init(bar(i), eight ? kSoft / 2 : widen ? kWiden : 1);
+            const bool eight = (i >= kPFull && i < kPFull + 2) || (i >= kOEmpty && i < kPiece);
+            tc::bar_init(bar(i), eight ? kSoft / 2 : widen ? kWiden : i >= kPieceFree && i < kDrain ? kSoft + kWiden + 1 : 1);
         }
         tc::bar_fence_init();
         tc::fence_async();
         upto[0] = 0;
-        s_nan[0][0] = INT_MAX;
-        s_nan[0][1] = -1;
+        for (int i = 0; i < 4; ++i) {
+            s_nan[i][0] = INT_MAX;
+            s_nan[i][1] = -1;
+        }
     }
     if (warp == kMmaWarp)
         tc::tmem_alloc<1>(tc::smem(&s_tmem), 512);
@@ -287,16 +301,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
         const int lrow = (warp & 3) * 32 + lane, rho = x * 128 + lrow;
         const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
         const uint32_t tS = tmem + x * 256 + 64 * half + lanes, tO = tmem + x * 256 + 128 + D / 2 * half + lanes;
-        float *told = &s_row[x][half][lrow], *other = &s_row[x][half ^ 1][lrow];
+        auto told = [&](int what) -> float & { return s_row[what][x][half][lrow]; };
+        auto other = [&](int what) { return s_row[what][x][half ^ 1][lrow]; };
         unsigned char *qs = gen + L::oQ + x * 2 * L::kQ;             // this tile's queries: as they are, then split
         tc::Ring<kMeta> ms;
         uint32_t sphase = 0, ophase = 0;
-        int odd_piece = 0;
+        int piece = 0;
         // a piece's query rows into shared memory, as they are: 256 (D = 128) or 128 bytes to a row
         auto fetch = [&](const Piece &p) {
             const int r = p.plane / a.Hk, hk = p.plane % a.Hk, rows = min(kRows, p.count * a.G - p.rt * kRows);
-            if (rows <= x * 128)
-                return;
             // lane i < 16: where the warp's row i comes from
             const int mine = x * 128 + (warp & 7) * 16 + (lane & 15), n = p.rt * kRows + mine;
             const uint16_t *src = a.q[r];
@@ -313,77 +326,90 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                              : "memory");
             }
         };
-        Piece p;
-        long long u = u0;
-        bool have = work.take(u, u1, p);
-        if (have)
-            fetch(p);
-        while (have) {
-            const int r = p.plane / a.Hk, hk = p.plane % a.Hk;
-            const int rows = min(kRows, p.count * a.G - p.rt * kRows);
-            const bool mine = rows > x * 128;      // the tile has rows
-            const int n = p.rt * kRows + rho;      // row of the request
-            const bool row = rho < rows;
-            float f = 0.f;
-            if (mine) {
-                // this thread's half of its query row, split, K-major with the swizzle of its length: the leading 4
-                // bits of every element and the other 4
-                constexpr int kC = D / 16;         // its 16-byte chunks
-                uint4 v[kC];
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                tile_sync(x);
-                uint32_t m = 0;
+        // Its rows, split, K-major with the swizzle of their length: the leading 4 bits of every element and the other
+        // 4.  Returns what takes a product of this thread's row to a score in units of log2.
+        auto split = [&]() {
+            constexpr int kC = D / 16;             // 16-byte chunks of this thread's half of a row
+            uint4 v[kC];
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            tile_sync(x);
+            uint32_t m = 0;
 #pragma unroll
-                for (int c = 0; c < kC; ++c) {
-                    v[c] = *reinterpret_cast<const uint4 *>(qs + lrow * 2 * D + (((half * kC + c) ^ (lrow & (2 * kC - 1))) << 4));
-                    m = sfar_max_abs2(sfar_max_abs2(sfar_max_abs2(sfar_max_abs2(m, v[c].x), v[c].y), v[c].z), v[c].w);
+            for (int c = 0; c < kC; ++c) {
+                v[c] = *reinterpret_cast<const uint4 *>(qs + lrow * 2 * D + (((half * kC + c) ^ (lrow & (2 * kC - 1))) << 4));
+                m = sfar_max_abs2(sfar_max_abs2(sfar_max_abs2(sfar_max_abs2(m, v[c].x), v[c].y), v[c].z), v[c].w);
+            }
+            m = sfar_max_half(m);
+            told(0) = __uint_as_float(m);
+            tile_sync(x);                          // every row has been read: the split ones go into its place
+            m = max(m, __float_as_uint(other(0)));
+            const bool special = m >= 0x7f80u;
+            const int e = special ? 127 : max((int)(m >> 7) - 127, -112);
+            const float up = sfar_exp2i(7 - e);
+#pragma unroll
+            for (int c = 0; c < kC; c += 2) {
+                const uint32_t w[8] = {v[c].x, v[c].y, v[c].z, v[c].w, v[c + 1].x, v[c + 1].y, v[c + 1].z, v[c + 1].w};
+                uint32_t ph[8], pl[8];
+#pragma unroll
+                for (int y = 0; y < 8; ++y) {
+                    const float x0 = bf16_lo(w[y]) * up, x1 = bf16_hi(w[y]) * up;
+                    const float h0 = __uint_as_float(__float_as_uint(x0) & 0xfff00000u), h1 = __uint_as_float(__float_as_uint(x1) & 0xfff00000u);
+                    ph[y] = cvt_e4m3x2(h0, h1);
+                    pl[y] = cvt_e4m3x2(x0 - h0, x1 - h1);
                 }
-                m = sfar_max_half(m);
-                *told = __uint_as_float(m);
-                tile_sync(x);                      // every row has been read: the split ones go into its place
-                m = max(m, __float_as_uint(*other));
-                const bool special = m >= 0x7f80u;
-                const int e = special ? 127 : max((int)(m >> 7) - 127, -112);
-                const float up = sfar_exp2i(7 - e);
-                f = a.scale * 1.4426950408889634f * sfar_exp2i(max(e - 7, -126));
-#pragma unroll
-                for (int c = 0; c < kC; c += 2) {
-                    const uint32_t w[8] = {v[c].x, v[c].y, v[c].z, v[c].w, v[c + 1].x, v[c + 1].y, v[c + 1].z, v[c + 1].w};
-                    uint32_t ph[8], pl[8];
+                if (special) {                     // infinities would saturate: NaN
 #pragma unroll
                     for (int y = 0; y < 8; ++y) {
-                        const float x0 = bf16_lo(w[y]) * up, x1 = bf16_hi(w[y]) * up;
-                        const float h0 = __uint_as_float(__float_as_uint(x0) & 0xfff00000u), h1 = __uint_as_float(__float_as_uint(x1) & 0xfff00000u);
-                        ph[y] = cvt_e4m3x2(h0, h1);
-                        pl[y] = cvt_e4m3x2(x0 - h0, x1 - h1);
+                        if ((w[y] & 0x7f80u) == 0x7f80u)
+                            ph[y] |= 0x7fu;
+                        if ((w[y] & 0x7f800000u) == 0x7f800000u)
+                            ph[y] |= 0x7f00u;
                     }
-                    if (special) {                 // infinities would saturate: NaN
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) {
-                            if ((w[y] & 0x7f80u) == 0x7f80u)
-                                ph[y] |= 0x7fu;
-                            if ((w[y] & 0x7f800000u) == 0x7f800000u)
-                                ph[y] |= 0x7f00u;
-                        }
-                    }
-                    const int at = (half * kC + c) / 2, chunk = D == 128 ? at ^ (lrow & 7) : at ^ ((lrow >> 1) & 3);
-                    unsigned char *dst = qs + lrow * D + chunk * 16;
-                    *reinterpret_cast<uint4 *>(dst) = make_uint4(ph[0] | ph[1] << 16, ph[2] | ph[3] << 16, ph[4] | ph[5] << 16, ph[6] | ph[7] << 16);
-                    *reinterpret_cast<uint4 *>(dst + L::kQ) = make_uint4(pl[0] | pl[1] << 16, pl[2] | pl[3] << 16, pl[4] | pl[5] << 16, pl[6] | pl[7] << 16);
                 }
-                tc::fence_async();
-                __syncwarp();
-                if (lane == 0)
-                    tc::bar_arrive(bar(kQFull + x));
+                const int at = (half * kC + c) / 2, chunk = D == 128 ? at ^ (lrow & 7) : at ^ ((lrow >> 1) & 3);
+                unsigned char *dst = qs + lrow * D + chunk * 16;
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(ph[0] | ph[1] << 16, ph[2] | ph[3] << 16, ph[4] | ph[5] << 16, ph[6] | ph[7] << 16);
+                *reinterpret_cast<uint4 *>(dst + L::kQ) = make_uint4(pl[0] | pl[1] << 16, pl[2] | pl[3] << 16, pl[4] | pl[5] << 16, pl[6] | pl[7] << 16);
             }
-            const int pos = p.len - p.count + n / a.G;
+            tc::fence_async();
+            __syncwarp();
+            if (lane == 0)
+                tc::bar_arrive(bar(kQFull + x));
+            return a.scale * 1.4426950408889634f * sfar_exp2i(max(e - 7, -126));
+        };
+        // The next piece, by all warps of the tile alike (or by none: after a wait that gave up).  It is read where the
+        // copying warp has put it, and given back when it has been written out.
+        tc::Ring<kPieces> ps;
+        auto take = [&](int &at) {
+            dead = dead || !tc::bar_wait(bar(kPiece + ps.slot), ps.phase, limit);
+            const bool none = tile_any(x, dead);
+            at = (int)ps.slot;
+            ps.next();
+            return !none && s_piece[at].tiles > 0;
+        };
+        auto rows_of = [&](const Piece &p) { return min(kRows, p.count * a.G - p.rt * kRows) - x * 128; };   // of this tile
+        int now_at, next_at;
+        bool have = take(now_at);
+        float f = 0.f;
+        if (have && rows_of(s_piece[now_at]) > 0) {
+            fetch(s_piece[now_at]);
+            f = split();
+        }
+        while (have) {
+            const Piece &p = s_piece[now_at];
+            const bool mine = rows_of(p) > 0;      // the tile has rows
+            const int n = p.rt * kRows + rho;      // row of the request
+            const bool row = lrow < rows_of(p);
+            const int tok = n / a.G;
+            const int pos = p.len - p.count + tok;
             const int hi = row ? min(p.len, pos + 1) : INT_MAX, lo = row && a.window ? max(0, pos - a.window + 1) : 0;
             // tiles that every row of this warp sees whole
             const int all_from = __reduce_max_sync(SFAR_FULL, lo), all_to = min(p.len, __reduce_min_sync(SFAR_FULL, hi));
             // log2 reference of the row's weights; sum: of this half's weight / value scale
             float wtop = -INFINITY, sum = 0.f;
-            for (int k = 0; mine && k < p.tiles; ++k) {
-                const int j0 = (p.tile0 + k) * kTile + 64 * half;
+            const int tiles = p.tiles, j00 = p.tile0 * kTile + 64 * half;
+            for (int k = 0; mine && k < tiles; ++k) {
+                const int j0 = j00 + k * kTile;
                 dead = dead || !tc::bar_wait(bar(kMFull + ms.slot), ms.phase, limit);
                 const Meta &m = meta[ms.slot];
                 const float4 ks = *reinterpret_cast<const float4 *>(m.ks + 4 * half), lv = *reinterpret_cast<const float4 *>(m.lvs + 4 * half),
@@ -396,6 +422,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                 dead = dead || !tc::bar_wait(bar(kSFull + x), sphase, limit);
                 sphase ^= 1u;
                 tc::fence_after();
+                if (k == tiles - 1) {
+                    // the last scores of the piece are complete: the next one's queries may come in
+                    have = take(next_at);
+                    if (have && rows_of(s_piece[next_at]) > 0)
+                        fetch(s_piece[next_at]);
+                }
                 if (edge) {
                     // scaled here, -inf where the row does not see the token, and put back
 #pragma unroll 1
@@ -415,78 +447,58 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                     for (int i = 0; i < 4; ++i)
                         c[i] = 1.f;
                 }
-                // The weights are formed against the reference as it stands.  Only if they come out large (or there is
-                // none yet) is the row's largest looked for, the reference moved and the weights formed again.
-                uint32_t w[32];
-                bool look = __any_sync(SFAR_FULL, wtop == -INFINITY);          // the same in both warps of a pair
+                float now;
+                {
+                    uint32_t s[32];
+                    tc::ld32(s, tS);
+                    tc::wait_ld(s);
+                    now = fmaxf(fmaf(max16(s), c[0], lvs[0]), fmaf(max16(s + 16), c[1], lvs[1]));
+                    tc::ld32(s, tS + 32);
+                    tc::wait_ld(s);
+                    now = fmaxf(now, fmaxf(fmaf(max16(s), c[2], lvs[2]), fmaf(max16(s + 16), c[3], lvs[3])));
+                }
+                uint32_t s[2][16];                 // scores are read twice rather than held: registers that spill cost more
+                tc::ld16(s[0], tS);
+                if (pair_any(pair, now > wtop + kAttnLift)) {
+                    told(1) = now;
+                    pair_sync(pair);
+                    const float next = fmaxf(wtop, fmaxf(now, other(1)));
+                    const float keep = wtop == -INFINITY ? 1.f : ex2(wtop - next);   // o is 0 then, or NaN
+                    sum *= keep;
+                    wtop = next;
+                    if (k > 0) {
+                        // the scores' barrier says that the products before are complete
 #pragma unroll 1
-                for (bool looked = false;; looked = true) {
-                    if (look) {
-                        float now = -INFINITY;
-#pragma unroll 1
-                        for (int i = 0; i < 64; i += 16) {
-                            uint32_t v[16];
-                            tc::ld16(v, tS + i);
-                            tc::wait_ld(v);
-                            now = fmaxf(now, max16(v) * (edge ? 1.f : f * m.ks[4 * half + (i >> 4)]) + m.lvs[4 * half + (i >> 4)]);
-                        }
-                        *told = now;
-                        pair_sync(pair);
-                        const float next = fmaxf(wtop, fmaxf(now, *other));
-                        const float keep = wtop == -INFINITY ? 1.f : ex2(wtop - next);   // o is 0 then, or NaN
-                        sum *= keep;
-                        wtop = next;
-                        if (k > 0) {
-                            // the scores' barrier says that the products before are complete
-#pragma unroll 1
-                            for (int i = 0; i < D / 2; i += 16) {
-                                uint32_t o[16];
-                                tc::ld16(o, tO + i);
-                                tc::wait_ld(o);
+                        for (int i = 0; i < D / 2; i += 16) {
+                            uint32_t o[16];
+                            tc::ld16(o, tO + i);
+                            tc::wait_ld(o);
 #pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-                                tc::st16(tO + i, o);
-                            }
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                            tc::st16(tO + i, o);
                         }
-                    }
-                    const float ref = wtop == -INFINITY ? 0.f : wtop;
-                    uint32_t s[2][16];
-                    float tile = 0.f, more = 0.f;
-                    tc::ld16(s[0], tS);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        tc::wait_ld(s[i & 1]);
-                        if (i < 3)
-                            tc::ld16(s[(i + 1) & 1], tS + 16 * (i + 1));
-                        const uint64_t c2 = tc::pack2(c[i], c[i]), off = tc::pack2(lvs[i] - ref, lvs[i] - ref);
-                        uint64_t add = 0ull;
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const float2 y = tc::unpack2(tc::fma2(tc::pack2u(s[i & 1][e], s[i & 1][e + 1]), c2, off));
-                            const float a0 = ex2(y.x), a1 = ex2(y.y);
-                            add = tc::add2(add, tc::pack2(a0, a1));
-                            w[8 * i + e / 2] = half2_of(a0, a1);
-                        }
-                        const float2 y = tc::unpack2(add);
-                        tile += y.x + y.y;
-                        more = fmaf(y.x + y.y, ivs[i], more);
-                    }
-                    // a tile's weights of up to 2^14 in all: none leaves binary16's range
-                    look = pair_any(pair, !(tile <= 8192.f));
-                    if (!look || looked) {
-                        sum += more;
-                        break;
                     }
                 }
-                // in the first columns of this half's scores
+                const float ref = wtop == -INFINITY ? 0.f : wtop;
 #pragma unroll
-                for (int i = 0; i < 32; i += 16) {
-                    uint32_t part[16];
+                for (int i = 0; i < 4; ++i) {
+                    tc::wait_ld(s[i & 1]);
+                    if (i < 3)
+                        tc::ld16(s[(i + 1) & 1], tS + 16 * (i + 1));
+                    uint32_t w[8];
+                    const uint64_t c2 = tc::pack2(c[i], c[i]), off = tc::pack2(lvs[i] - ref, lvs[i] - ref);
+                    uint64_t add = 0ull;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        part[e] = w[i + e];
-                    tc::st16(tS + i, part);
+                    for (int e = 0; e < 16; e += 2) {
+                        const float2 y = tc::unpack2(tc::fma2(tc::pack2u(s[i & 1][e], s[i & 1][e + 1]), c2, off));
+                        const float a0 = ex2(y.x), a1 = ex2(y.y);
+                        add = tc::add2(add, tc::pack2(a0, a1));
+                        w[e / 2] = half2_of(a0, a1);
+                    }
+                    const float2 y = tc::unpack2(add);
+                    sum = fmaf(y.x + y.y, ivs[i], sum);
+                    tc::st8(tS + 8 * i, w);        // over scores that have been read
                 }
                 tc::wait_st();
                 tc::fence_before();
@@ -495,35 +507,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                     tc::bar_arrive(bar(kPFull + x));
                 ms.next();
             }
-            if (!mine)
-                for (int k = 0; k < p.tiles; ++k)
+            if (!mine) {
+                for (int k = 0; k < tiles; ++k)
                     ms.next();
-            // the next piece's queries come in while this one is written out: the last scores are complete
-            Piece next;
-            have = work.take(u, u1, next);
-            if (have)
-                fetch(next);
+                have = take(next_at);
+                if (have && rows_of(s_piece[next_at]) > 0)
+                    fetch(s_piece[next_at]);
+            }
+            // the next queries first, so that their first scores are formed while this piece is written out
+            float fnext = 0.f;
+            if (have && rows_of(s_piece[next_at]) > 0)
+                fnext = split();
             // --------------------------------------------------------- epilogue
             if (mine) {
-                *told = sum;
+                told(2) = sum;
                 pair_sync(pair);
-                sum += *other;
+                sum += other(2);
                 dead = dead || !tc::bar_wait(bar(kOFull + x), ophase, limit);
                 ophase ^= 1u;
                 tc::fence_after();
             }
             const bool part = p.tiles < p.all;
-            const long long from = p.at - (p.tile0 - p.begin), to = from + p.all;
-            const long long c0 = ((from + 1) * N - 1) / U, c1 = (to * N - 1) / U;
             // [element / 4][row] and the reference last, so that neighbouring rows are neighbours
             auto slot = [&](long long cta, int which) {
                 return reinterpret_cast<float4 *>(a.part) + ((size_t)cta * 2 + which) * (kRows * (D / 4 + 1));
             };
             float4 *dst = slot(blockIdx.x, p.tile0 == p.begin ? 1 : 0);
             const float inv = sum == 0.f ? 0.f : 1.f / sum;         // 0: the row attends to nothing
-            uint16_t *out = a.out[r] + (long long)(p.first + n / a.G) * a.ots + (long long)(hk * a.G + n % a.G) * a.ohs;
-            const int *nan = s_nan[odd_piece];
-            odd_piece ^= 1;
+            const int r = p.plane / a.Hk, hk = p.plane % a.Hk;
+            uint16_t *out = a.out[r] + (long long)(p.first + tok) * a.ots + (long long)(hk * a.G + n - tok * a.G) * a.ohs;
+            const int *nan = s_nan[piece++ & 3];
             const int d0 = half * (D / 2);
             if (mine) {
 #pragma unroll 1
@@ -573,6 +586,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             }
             if (mine && part) {
                 // the last of the row tile's CTAs joins its parts in order; the two tiles of rows separately
+                const long long from = p.at - (p.tile0 - p.begin), to = from + p.all;
+                const long long c0 = ((from + 1) * N - 1) / U, c1 = (to * N - 1) / U;
                 __threadfence();
                 tile_sync(x);
                 if ((tid & 255) == 0) {
@@ -628,7 +643,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                     }
                 }
             }
-            p = next;
+            __syncwarp();
+            if (lane == 0)
+                tc::bar_arrive(bar(kPieceFree + now_at));
+            now_at = next_at;
+            f = fnext;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (dead && lane == 0)
@@ -652,22 +671,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             const int to = (c >> 2) * (kTile * 128) + tok0 * 128 + ((at ^ (tok0 & 7)) << 4), flip = c >> 2 & 1;
             bool dead = false;
             uint32_t qphase = 0, ophase = 0;
-            int before = 0;                        // rows of the piece before
-            Piece p;
-            for (long long u = u0; work.take(u, u1, p);) {
-                // the first tile's queries are in place once the piece before has been written out
+            int before = 0, piece = 0;             // rows of the piece before
+            tc::Ring<kPieces> ps;
+            for (;; ps.next()) {
+                dead = __any_sync(SFAR_FULL, dead || !tc::bar_wait(bar(kPiece + ps.slot), ps.phase, limit));
+                if (dead)
+                    break;
+                const Piece p = s_piece[ps.slot];
+                __syncwarp();
+                if (lane == 0)
+                    tc::bar_arrive(bar(kPieceFree + ps.slot));
+                if (p.tiles == 0)
+                    break;
+                // The first rows' queries are in place: they have read the marks of the piece before the last.  Those
+                // are cleared for the piece after the next.
                 dead = dead || !tc::bar_wait(bar(kQFull), qphase, limit);
-                if (before > 128) {                // the second tile of rows of the piece before, if it had one
-                    dead = dead || !tc::bar_wait(bar(kOEmpty + 1), ophase, limit);
-                    ophase ^= 1u;
-                }
-                before = min(kRows, p.count * a.G - p.rt * kRows);
-                int *nan = s_nan[qphase];
                 qphase ^= 1u;
-                if (ct == 0) {                     // of the piece before, for the piece after
-                    s_nan[qphase][0] = INT_MAX;
-                    s_nan[qphase][1] = -1;
+                int *nan = s_nan[piece & 3];
+                if (ct == 0) {
+                    s_nan[(piece + 2) & 3][0] = INT_MAX;
+                    s_nan[(piece + 2) & 3][1] = -1;
                 }
+                ++piece;
                 // tiles that every row of the piece sees whole
                 const int pos0 = p.len - p.count + p.rt * kRows / a.G;
                 const int pos1 = p.len - p.count + min(p.count - 1, (p.rt * kRows + kRows - 1) / a.G);
@@ -712,6 +737,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                             widen(dst + n * kTo, flip, v);
                         }
                     }
+                    if (k == p.tiles - 1) {
+                        // so have the second rows of the piece before, if it had any, at the latest now
+                        if (before > 128) {
+                            dead = dead || !tc::bar_wait(bar(kOEmpty + 1), ophase, limit);
+                            ophase ^= 1u;
+                        }
+                        before = min(kRows, p.count * a.G - p.rt * kRows);
+                    }
                     tc::fence_async();
                     __syncwarp();
                     if (lane == 0) {
@@ -733,7 +766,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             const uint64_t often = tc::evict_last();
             const int per = min(1 << a.shift, SFAR_ATTN_TILE), boxes = kTile / per;   // tokens of one copy
             Piece p;
-            for (long long u = u0; !dead && work.take(u, u1, p);) {
+            tc::Ring<kPieces> ps;
+            for (long long u = u0; !dead; ps.next()) {
+                const bool have = work.take(u, u1, p);
+                if (!tc::bar_wait(bar(kPieceFree + ps.slot), ps.phase ^ 1u, limit)) {
+                    dead = true;
+                    break;
+                }
+                if (!have)
+                    p.tiles = 0;
+                if (lane == 0) {
+                    s_piece[ps.slot] = p;
+                    tc::bar_arrive(bar(kPiece + ps.slot));
+                }
+                if (!have)
+                    break;
                 const int r = p.plane / a.Hk, hk = p.plane % a.Hk;
                 const int *row = a.table + (size_t)p.b * a.W;
                 for (int k = 0; k < p.tiles; ++k) {
@@ -811,8 +858,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             tc::Ring<kHStages> hr;
             bool dead = false;
             uint32_t qphase[2] = {0, 0}, pphase[2] = {0, 0}, ofree[2] = {1, 1};
-            Piece p;
-            for (long long u = u0; !dead && work.take(u, u1, p);) {
+            tc::Ring<kPieces> ps;
+            for (;; ps.next()) {
+                dead = __any_sync(SFAR_FULL, dead || !tc::bar_wait(bar(kPiece + ps.slot), ps.phase, limit));
+                if (dead)
+                    break;
+                const Piece p = s_piece[ps.slot];
+                __syncwarp();
+                if (lane == 0)
+                    tc::bar_arrive(bar(kPieceFree + ps.slot));
+                if (p.tiles == 0)
+                    break;
                 const int tiles = min(kRows, p.count * a.G - p.rt * kRows) > 128 ? 2 : 1;
                 if (tc::elect_one()) {             // the same lane every time: the rings stay in its registers
                     for (int k = 0; k <= p.tiles && !dead; ++k) {

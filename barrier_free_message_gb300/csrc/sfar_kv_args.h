@@ -91,4 +91,4 @@ int sfar_fp8_prepare();
 #define SFAR_ATTN_STAGES 4
 #define SFAR_ATTN_CTAS 2                    // per SM
 #define SFAR_PROMPT_ROWS 256
-#define SFAR_PROMPT_REQUESTS 3584           // whose prefix sums fit beside the prompt kernel's tiles
+#define SFAR_PROMPT_REQUESTS 2048           // whose prefix sums fit beside the prompt kernel's tiles

@@ -197,6 +197,13 @@ __device__ __forceinline__ void st16(uint32_t addr, const uint32_t (&v)[16])
         : "memory");
 }
 
+__device__ __forceinline__ void st8(uint32_t addr, const uint32_t (&v)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // ---------------------------------------------------------------- tensor core
 // Shared-memory descriptor of a K-major operand whose rows are 128 bytes with
 // the 128-byte swizzle (what a TMA box 128 bytes wide writes): groups of 8
