@@ -127,58 +127,91 @@ def strerror(code: int) -> str:
     return _lib.sfar_strerror(code).decode()
 
 
+_current = None
+
+
 def _stream(stream):
-    if stream is None:
+    """The stream's handle; None: torch's current stream of the current device (read without building a Stream
+    object, which costs more than a launch)."""
+    global _current
+    if stream is not None:
+        return int(stream)
+    if _current is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
-    return int(stream)
+        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        if raw is None or device is None or not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
+        _current = lambda: raw(device())                       # noqa: E731
+    return _current()
 
 
 def _ptr_array(ptrs):
     return (ctypes.c_void_p * len(ptrs))(*[int(p) for p in ptrs])
 
 
-def _rank_ptrs(x, R, what):
-    """A pointer per rank: of a list of R tensors, or of the slices of one [R, ...] tensor."""
+_types = None
+
+
+def _torch_types():
+    """(bf16, fp32, int32, types of a byte), once torch is loaded."""
+    global _types
+    if _types is None:
+        import torch
+        _types = ((torch.bfloat16,), (torch.float32,), torch.int32, (torch.float8_e4m3fn, torch.uint8))
+    return _types
+
+
+_forms = {}
+
+
+def _form(dtype, shape, stride, cuda, ndim, dtypes, what):
+    """Checks one rank's shape and strides; returns them, the stride of a dimension of one entry as 0, whatever
+    torch keeps there, and whether they are a contiguous tensor's."""
+    if len(shape) != ndim or dtype not in dtypes:
+        raise ValueError(f"{what}: need {ndim} dimensions of {' or '.join(map(str, dtypes))} per rank")
+    if stride[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    if not cuda:
+        raise ValueError(f"{what}: must be on the GPU")
+    n, dense = 1, True
+    for size, st in zip(reversed(shape), reversed(stride)):
+        dense = dense and (size <= 1 or st == n)
+        n *= size
+    return shape, tuple(st if n > 1 else 0 for n, st in zip(shape, stride)), dense
+
+
+def _ranks(x, R, ndim, dtypes, what):
+    """(array of a pointer per rank, shape, strides, contiguous) of R tensors on the GPU, given as a list or as one
+    tensor [R, ...] whose slices they are: the same shape, strides and type, unit stride along the last dimension."""
     if isinstance(x, (list, tuple)):
         if len(x) != R:
             raise ValueError(f"{what}: need {R} tensors, one per rank")
-        return (ctypes.c_void_p * R)(*[t.data_ptr() for t in x])
-    if x.shape[0] != R:
-        raise ValueError(f"{what}: need [{R}, ...], a slice per rank")
-    base, step = x.data_ptr(), x.stride(0) * x.element_size()
-    return (ctypes.c_void_p * R)(*range(base, base + R * step, step)) if step else (ctypes.c_void_p * R)(*[base] * R)
-
-
-def _rank_form(x, ndim, what, *dtypes):
-    """Rank 0's tensor, after the checks that hold for every rank: dimensions, type, the same strides, unit
-    stride along the last dimension."""
-    if isinstance(x, (list, tuple)):
         t = x[0]
-        for o in x[1:]:
-            if o.shape != t.shape or o.stride() != t.stride() or o.dtype != t.dtype:
+        dtype, shape, stride = t.dtype, t.shape, t.stride()
+        for o in x:
+            if o.shape != shape or o.stride() != stride or o.dtype != dtype:
                 raise ValueError(f"{what}: the ranks' tensors differ in shape, strides or type")
-    else:
-        t = x[0]
-    if t.dim() != ndim or str(t.dtype) not in dtypes:
-        raise ValueError(f"{what}: need {ndim} dimensions of {' or '.join(dtypes)} per rank")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{what}: the last dimension must be contiguous")
-    return t
-
-
-_BF16, _FP32, _INT32 = "torch.bfloat16", "torch.float32", "torch.int32"
-_BYTES = ("torch.float8_e4m3fn", "torch.uint8")
-
-
-def _strides(t):
-    """Strides of the two leading dimensions; 0 where there is one entry only, whatever torch keeps there."""
-    return tuple(t.stride(i) if t.shape[i] > 1 else 0 for i in (0, 1))
+        ptrs = (ctypes.c_void_p * R)(*[o.data_ptr() for o in x])
+        return (ptrs, *_form(dtype, tuple(shape), stride, all(o.is_cuda for o in x), ndim, dtypes, what))
+    # what a shape and its strides come to is worked out once
+    key = (what, R, ndim, x.dtype, x.shape, x.stride(), x.is_cuda)
+    form = _forms.get(key)
+    if form is None:
+        shape, stride = tuple(x.shape), x.stride()
+        if len(shape) == 0 or shape[0] != R:
+            raise ValueError(f"{what}: need [{R}, ...], a slice per rank")
+        if len(_forms) >= 4096:
+            _forms.clear()
+        form = _forms[key] = (ctypes.c_void_p * R, stride[0] * x.element_size(),
+                              *_form(x.dtype, shape[1:], stride[1:], x.is_cuda, ndim, dtypes, what))
+    array, step, shape, stride, dense = form
+    base = x.data_ptr()
+    return array(*range(base, base + R * step, step)) if step else array(*[base] * R), shape, stride, dense
 
 
 def _int32(t, shape, what):
-    if tuple(t.shape) != shape or str(t.dtype) != _INT32 or not t.is_contiguous():
-        raise ValueError(f"{what}: need a contiguous int32 tensor of shape {list(shape)}")
+    if t.dtype is not _torch_types()[2] or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{what}: need a contiguous int32 tensor of shape {list(shape)} on the GPU")
     return t.data_ptr()
 
 
@@ -365,35 +398,38 @@ class Sfar:
     def quantize_fp8(self, x, x8, sx, stream=None) -> None:
         """x: [m, k] bf16 per rank -> x8: [m, k] e4m3 and sx: [ceil(k / 128), m] fp32 per rank (lists of R
         tensors, or one tensor [R, ...] each; rows of x and x8 may be strided)."""
-        t, o, c = _rank_form(x, 2, "x", _BF16), _rank_form(x8, 2, "x8", *_BYTES), _rank_form(sx, 2, "sx", _FP32)
-        m, k = t.shape
-        if o.shape != t.shape or tuple(c.shape) != ((k + 127) // 128, m) or not c.is_contiguous():
-            raise ValueError("quantize_fp8: x8 must be [m, k], sx a contiguous [ceil(k / 128), m]")
+        bf16, fp32, _, byte = _torch_types()
         R = self.R
-        code = lib().sfar_quantize_fp8(self.h, _rank_ptrs(x, R, "x"), _rank_ptrs(x8, R, "x8"), _rank_ptrs(sx, R, "sx"),
-                                       m, k, t.stride(0) if m > 1 else (k + 15) // 16 * 16,
-                                       o.stride(0) if m > 1 else (k + 15) // 16 * 16, _stream(stream))
-        _check(code, "sfar_quantize_fp8")
+        px, shape, st, _ = _ranks(x, R, 2, bf16, "x")
+        po, oshape, ost, _ = _ranks(x8, R, 2, byte, "x8")
+        ps, sshape, _, dense = _ranks(sx, R, 2, fp32, "sx")
+        m, k = shape
+        if oshape != shape or sshape != ((k + 127) // 128, m) or not dense:
+            raise ValueError("quantize_fp8: x8 must be [m, k], sx a contiguous [ceil(k / 128), m]")
+        up = (k + 15) // 16 * 16
+        _check(lib().sfar_quantize_fp8(self.h, px, po, ps, m, k, st[0] or up, ost[0] or up, _stream(stream)),
+               "sfar_quantize_fp8")
 
     def rowpar_gemm_fp8(self, x8, sx, w8, sw, y, stream=None) -> None:
         """x8 [m, k], sx [ceil(k / 128), m] (as quantize_fp8 gives them), w8 [hidden, k] e4m3 and sw
         [ceil(hidden / 128), ceil(k / 128)] fp32 -> y [m, hidden] bf16, per rank (lists of R tensors, or one
         tensor [R, ...] each; rows of x8 and w8 may be strided by multiples of 16)."""
-        tx, tw, ty = _rank_form(x8, 2, "x8", *_BYTES), _rank_form(w8, 2, "w8", *_BYTES), _rank_form(y, 2, "y", _BF16)
-        cx, cw = _rank_form(sx, 2, "sx", _FP32), _rank_form(sw, 2, "sw", _FP32)
-        m, k = tx.shape
-        n, kb = tw.shape[0], (k + 127) // 128
-        if tw.shape[1] != k or tuple(ty.shape) != (m, n) or tuple(cx.shape) != (kb, m) or \
-                tuple(cw.shape) != ((n + 127) // 128, kb) or not (ty.is_contiguous() and cx.is_contiguous() and
-                                                                  cw.is_contiguous()):
+        bf16, fp32, _, byte = _torch_types()
+        R = self.R
+        px, xs, xst, _ = _ranks(x8, R, 2, byte, "x8")
+        pw, ws, wst, _ = _ranks(w8, R, 2, byte, "w8")
+        py, ys, _, dense_y = _ranks(y, R, 2, bf16, "y")
+        pc, cs, _, dense_c = _ranks(sx, R, 2, fp32, "sx")
+        pd, ds, _, dense_d = _ranks(sw, R, 2, fp32, "sw")
+        m, k = xs
+        n, kb = ws[0], (k + 127) // 128
+        if ws[1] != k or ys != (m, n) or cs != (kb, m) or ds != ((n + 127) // 128, kb) or \
+                not (dense_y and dense_c and dense_d):
             raise ValueError("rowpar_gemm_fp8: need x8 [m, k], w8 [hidden, k], contiguous sx [ceil(k / 128), m], "
                              "sw [ceil(hidden / 128), ceil(k / 128)] and y [m, hidden]")
-        R, up = self.R, (k + 15) // 16 * 16
-        code = lib().sfar_rowpar_gemm_fp8(self.h, _rank_ptrs(x8, R, "x8"), _rank_ptrs(sx, R, "sx"),
-                                          _rank_ptrs(w8, R, "w8"), _rank_ptrs(sw, R, "sw"), _rank_ptrs(y, R, "y"),
-                                          m, k, n, tx.stride(0) if m > 1 else up, tw.stride(0) if n > 1 else up,
-                                          _stream(stream))
-        _check(code, "sfar_rowpar_gemm_fp8")
+        up = (k + 15) // 16 * 16
+        _check(lib().sfar_rowpar_gemm_fp8(self.h, px, pc, pw, pd, py, m, k, n, xst[0] or up, wst[0] or up,
+                                          _stream(stream)), "sfar_rowpar_gemm_fp8")
 
     def status(self):
         return sfar_status_get(self.h)
@@ -430,19 +466,20 @@ class SfarKv:
 
     def __init__(self, k_cache, v_cache, k_scale, v_scale, q_heads: int):
         self.h = None
+        _, fp32, _, byte = _torch_types()
         R = len(k_cache)
-        k, v = _rank_form(k_cache, 4, "k_cache", *_BYTES), _rank_form(v_cache, 4, "v_cache", *_BYTES)
-        ks, vs = _rank_form(k_scale, 2, "k_scale", _FP32), _rank_form(v_scale, 2, "v_scale", _FP32)
-        if v.shape != k.shape or ks.shape != k.shape[:2] or vs.shape != k.shape[:2] or \
-                not all(t.is_contiguous() for t in (k, v, ks, vs)):
+        pk, k, _, dense_k = _ranks(k_cache, R, 4, byte, "k_cache")
+        pv, v, _, dense_v = _ranks(v_cache, R, 4, byte, "v_cache")
+        pks, ks, _, dense_ks = _ranks(k_scale, R, 2, fp32, "k_scale")
+        pvs, vs, _, dense_vs = _ranks(v_scale, R, 2, fp32, "v_scale")
+        if v != k or ks != k[:2] or vs != k[:2] or \
+                not (dense_k and dense_v and dense_ks and dense_vs):
             raise ValueError("SfarKv: need contiguous caches [pages, kv_heads, page_tokens, head_dim] and scales "
                              "[pages, kv_heads]")
         self.R, self.q_heads = R, q_heads
-        self.pages, self.kv_heads, self.page_tokens, self.head_dim = k.shape
+        self.pages, self.kv_heads, self.page_tokens, self.head_dim = k
         self.tensors = (k_cache, v_cache, k_scale, v_scale)
-        h = lib().sfar_kv_create(R, q_heads, self.kv_heads, self.head_dim, self.page_tokens, self.pages,
-                                 _rank_ptrs(k_cache, R, "k_cache"), _rank_ptrs(v_cache, R, "v_cache"),
-                                 _rank_ptrs(k_scale, R, "k_scale"), _rank_ptrs(v_scale, R, "v_scale"))
+        h = lib().sfar_kv_create(R, q_heads, self.kv_heads, self.head_dim, self.page_tokens, self.pages, pk, pv, pks, pvs)
         if not h:
             raise SfarError(lib().sfar_last_error(), "sfar_kv_create")
         self.h = h
@@ -462,30 +499,29 @@ class SfarKv:
 
     def append(self, k, v, slots, stream=None) -> None:
         """k, v: [tokens, kv_heads, head_dim] bf16 per rank (token and head strides multiples of 8); slots: [tokens]."""
-        tk, tv = _rank_form(k, 3, "k", _BF16), _rank_form(v, 3, "v", _BF16)
+        bf16 = _torch_types()[0]
+        pk, ks, kst, _ = _ranks(k, self.R, 3, bf16, "k")
+        pv, vs, vst, _ = _ranks(v, self.R, 3, bf16, "v")
         T = slots.shape[0]
-        shape = (T, self.kv_heads, self.head_dim)
-        if tuple(tk.shape) != shape or tuple(tv.shape) != shape:
-            raise ValueError(f"append: need k and v of shape {list(shape)} per rank")
-        code = lib().sfar_kv_append(self.h, _rank_ptrs(k, self.R, "k"), _rank_ptrs(v, self.R, "v"),
-                                    _int32(slots, (T,), "slots"), T, *_strides(tk), *_strides(tv),
-                                    _stream(stream))
-        _check(code, "sfar_kv_append")
+        if ks != (T, self.kv_heads, self.head_dim) or vs != ks:
+            raise ValueError(f"append: need k and v of shape {[T, self.kv_heads, self.head_dim]} per rank")
+        _check(lib().sfar_kv_append(self.h, pk, pv, _int32(slots, (T,), "slots"), T, kst[0], kst[1], vst[0], vst[1],
+                                    _stream(stream)), "sfar_kv_append")
 
     def attention(self, q, out, table, lens, starts, max_q: int, scale=None, window: int = 0, stream=None) -> None:
         """q, out: [tokens, q_heads, head_dim] bf16 per rank (token and head strides multiples of 8); table:
         [requests, width], lens: [requests], starts: [requests + 1].  scale: 1 / sqrt(head_dim) if None."""
-        tq, to = _rank_form(q, 3, "q", _BF16), _rank_form(out, 3, "out", _BF16)
-        if tuple(tq.shape[1:]) != (self.q_heads, self.head_dim) or to.shape != tq.shape:
+        bf16 = _torch_types()[0]
+        pq, qs, qst, _ = _ranks(q, self.R, 3, bf16, "q")
+        po, os_, ost, _ = _ranks(out, self.R, 3, bf16, "out")
+        if qs[1:] != (self.q_heads, self.head_dim) or os_ != qs:
             raise ValueError(f"attention: need q and out of shape [tokens, {self.q_heads}, {self.head_dim}] per rank")
         B, W = table.shape
         if scale is None:
             scale = self.head_dim ** -0.5
-        code = lib().sfar_kv_attention(self.h, _rank_ptrs(q, self.R, "q"), _rank_ptrs(out, self.R, "out"),
-                                       _int32(table, (B, W), "table"), _int32(lens, (B,), "lens"),
-                                       _int32(starts, (B + 1,), "starts"), B, W, tq.shape[0], *_strides(tq),
-                                       *_strides(to), max_q, scale, window, _stream(stream))
-        _check(code, "sfar_kv_attention")
+        _check(lib().sfar_kv_attention(self.h, pq, po, _int32(table, (B, W), "table"), _int32(lens, (B,), "lens"),
+                                       _int32(starts, (B + 1,), "starts"), B, W, qs[0], qst[0], qst[1], ost[0], ost[1],
+                                       max_q, scale, window, _stream(stream)), "sfar_kv_attention")
 
     def status(self):
         f = SfarFault()

@@ -1,6 +1,7 @@
 """The paged 8-bit cache's operators on the GPU against the plain 64-bit
 references of kv_ref: plans and quantised caches bit for bit, attention and
 projection within bounds counted from their roundings."""
+import ctypes
 import random
 
 import pytest
@@ -509,14 +510,18 @@ def test_gemm_nan_stays_in_its_row_and_column():
 
 
 # ----------------------------------------------------------------- refusals
+def rank_ptrs(tensors):
+    return (ctypes.c_void_p * len(tensors))(*[t.data_ptr() for t in tensors])
+
+
 def test_calls_refuse_bad_arguments():
     cpu, dev, kv = fresh(R=2, H=2, D=64, P=16, pages=4, q_heads=4)
     L, z = sfar.lib(), torch.zeros(4096, dtype=torch.int32, device="cuda")
     a = z.data_ptr()
     bf = torch.zeros(2, 4, 4, 64, dtype=torch.bfloat16, device="cuda")
     out = torch.zeros_like(bf)
-    x, o = [(sfar._rank_ptrs(t, 2, "t")) for t in (bf, out)]
-    odd = sfar._rank_ptrs([bf[0].flatten()[1:], bf[1]], 2, "t")
+    x, o = [(rank_ptrs(t)) for t in (bf, out)]
+    odd = rank_ptrs([bf[0].flatten()[1:], bf[1]])
     bad = sfar.SFAR_ERR_INVALID
     at = [a + 256 * i for i in range(10)]
     assert L.sfar_kv_plan(kv.h, *at, 4, 2, 8, None) == 0
@@ -547,8 +552,7 @@ def test_calls_refuse_bad_arguments():
     h = sfar.Sfar(2, 1 << 16, "bf16")
     try:
         f = torch.zeros(2, 8192, device="cuda")
-        s1, s2, b1, b2 = [sfar._rank_ptrs(torch.zeros_like(f), 2, "t") for _ in range(4)]
-        b1, b2, s1, s2 = [sfar._rank_ptrs(f[:, 2048 * i:2048 * i + 2048], 2, "t") for i in range(4)]
+        b1, b2, s1, s2 = [rank_ptrs(f[:, 2048 * i:2048 * i + 2048]) for i in range(4)]
         assert L.sfar_quantize_fp8(fp32.h, b1, b2, s1, 2, 64, 64, 64, None) == bad
         assert L.sfar_rowpar_gemm_fp8(fp32.h, b1, s1, b2, s2, o, 2, 64, 8, 64, 64, None) == bad
         assert L.sfar_quantize_fp8(h.h, b1, b2, s1, 2, 64, 64, 64, None) == 0

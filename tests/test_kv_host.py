@@ -70,7 +70,8 @@ def test_python_layer_refuses_wrong_tensors():
     t = torch.zeros(2, 4, 2, 16, 64, dtype=torch.uint8)
     s = torch.zeros(2, 4, 2)
     for args in ((t.float(), t, s, s), (t, t[:, :, :, :8], s, s), (t, t, s[:, :3], s), (t, t, s, s.double()),
-                 (t[..., ::2], t[..., ::2], s, s), ([t[0], t[1][:3]], t, s, s), (t, t[:1], s, s)):
+                 (t[..., ::2], t[..., ::2], s, s), ([t[0], t[1][:3]], t, s, s), (t, t[:1], s, s),
+                 (t, t, s, s)):                                # on the CPU
         with pytest.raises(ValueError):
             sfar.SfarKv(*args, q_heads=4)
 
