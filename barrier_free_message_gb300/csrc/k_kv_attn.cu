@@ -40,13 +40,12 @@ namespace {
 
 constexpr int kTile = SFAR_ATTN_TILE;              // cached tokens per stage
 constexpr int kConsumers = 4, kThreads = 32 * (kConsumers + 1);
-constexpr int kStages = SFAR_ATTN_STAGES;
-constexpr int kRows = 16;
 
 // Shared memory of a CTA, after the prefix sums.
-template <int D> struct Lay {
+template <int D, int RH> struct Lay {
+    static constexpr int kRows = 8 * RH, kStages = RH == 1 ? 3 : 4;
     static constexpr int kStage = 2 * kTile * D;
-    static constexpr int kRow = D + 16;            // floats of a row in the join buffer, padded against bank conflicts
+    static constexpr int kRow = D + 4;             // floats of a row in the join buffer, padded against bank conflicts
     static constexpr int kJoin = kConsumers * kRows * kRow * 4;
     static constexpr int kQ = kRows * D * 2;
     static constexpr int kBytes = kStages * kStage + kJoin + 2 * kQ;
@@ -56,23 +55,18 @@ struct Meta {                                      // of a stage
     int bad;                                       // bit i: tokens 16 i .. are on no page of the pool
 };
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, const uint32_t (&b)[2])
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a)
+// an 8 x 8 matrix of 16-bit values, a row to four lanes, transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t v)
 {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a)
-{
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -82,9 +76,9 @@ template <int D> __device__ __forceinline__ uint32_t at_chunk(int token, int chu
 {
     return D == 128 ? token * 128 + ((chunk ^ (token & 7)) << 4) : token * 64 + ((chunk ^ ((token >> 1) & 3)) << 4);
 }
-// The token (of 8) that stands in column n of an 8-column fragment.  For
-// 64-byte rows an order in which neither the key loads (rows n, n + 1) nor the
-// value loads (columns 0 2 4 6, then 1 3 5 7) meet in a bank.
+// The token (of 8) that stands at place n of a fragment's 8.  For 64-byte rows
+// an order in which neither the key loads (places n, n + 1) nor the value loads
+// (places 0 2 4 6, then 1 3 5 7) meet in a bank.
 template <int D> __device__ __forceinline__ int token_of(int n)
 {
     return D == 128 ? n : (int)((0x65742130u >> (4 * n)) & 7u);
@@ -98,7 +92,7 @@ struct Piece {
     int len, count, first;      // context, new tokens, row of the first new token
 };
 
-struct Work {
+template <int kRows> struct Work {
     const uint32_t *upto;       // [B + 1] prefix sums of the requests' units, per plane
     const SfarAttnArgs &a;
     // tiles that some row of the request attends to (at least one: rows of nothing are written too)
@@ -112,7 +106,7 @@ struct Work {
     {
         Piece p;
         const uint32_t S = upto[a.B];
-        p.plane = (int)(u / S);
+        p.plane = (int)sfar_div(u, S);
         const uint32_t v = (uint32_t)(u - (long long)p.plane * S);
         int lo = 0, hi = a.B;
         while (hi - lo > 1) {
@@ -136,16 +130,18 @@ struct Work {
 
 }  // namespace
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 2) k_kv_attn(const __grid_constant__ SfarAttnArgs a)
+template <int D, int RH>
+__global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __grid_constant__ SfarAttnArgs a)
 {
-    using L = Lay<D>;
+    using L = Lay<D, RH>;
+    constexpr int kRows = L::kRows, kStages = L::kStages;
     extern __shared__ __align__(1024) unsigned char dyn[];
     __shared__ __align__(8) unsigned long long bars[2 * kStages + 4];
     __shared__ Meta meta[kStages];
+    __shared__ Piece s_piece[kConsumers];          // each warp's, out of its registers
     __shared__ float s_ml[3][kConsumers][kRows];   // running maximum, sum, weight reference
     __shared__ uint32_t s_warp[kThreads / 32];
-    __shared__ int s_last;
+    __shared__ int s_last, s_nan[2][2];            // by the piece's parity: first and last token whose value holds a NaN
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = (tc::smem(dyn) + 1023u) & ~1023u;
     unsigned char *mem = dyn + (base - tc::smem(dyn));
@@ -166,12 +162,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_attn(const __grid_constant__
         tc::bar_fence_init();
         tc::fence_async();
         upto[0] = 0;
+        s_nan[0][0] = INT_MAX;
+        s_nan[0][1] = -1;
     }
     pdl_wait();
     const unsigned long long limit = ld_relaxed_u64(&a.ctl->timeout_ns);
 
     // prefix sums of the requests' units: row tiles x tiles
-    const Work work{upto, a};
+    const Work<kRows> work{upto, a};
     uint32_t carry = 0;
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
         const int b = b0 + tid;
@@ -212,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_attn(const __grid_constant__
     const long long N = min((long long)gridDim.x, U);
     if (blockIdx.x >= N)
         return;
-    const long long u0 = blockIdx.x * U / N, u1 = (blockIdx.x + 1) * U / N;
+    const long long u0 = sfar_div(blockIdx.x * U, N), u1 = sfar_div((blockIdx.x + 1) * U, N);
 
     if (warp == kConsumers) {
         // ------------------------------------------------------------- producer
@@ -306,23 +304,32 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_attn(const __grid_constant__
     tc::Ring<kStages> st;
     tc::Ring<2> qs;
     bool dead = false;                             // a wait gave up: go on without waiting, so that the warps stay together
+    int piece = 0;
     for (long long u = u0; u < u1;) {
-        const Piece p = work.at(u, u1);
+        {
+            const Piece q = work.at(u, u1);
+            __syncwarp();
+            if (lane == 0)
+                s_piece[warp] = q;
+            __syncwarp();
+        }
+        const Piece &p = s_piece[warp];
         const int r = p.plane / a.Hk, hk = p.plane % a.Hk;
         const int rows = min(kRows, p.count * a.G - p.rt * kRows);
-        // the query rows g and g + 8, brought into binary16's range
-        uint32_t q[kK][4];
-        float f[2];
-        int lo[2], hi[2];
+        // The query rows, brought into binary16's range: of each 8, lane (g, t) holds a quarter of row g, and answers for
+        // rows 2 t and 2 t + 1 of the scores.
+        uint32_t q[RH][kK][2];
+        float f[RH][2];
+        int lo[RH][2], hi[RH][2];
         dead = dead || !tc::bar_wait(qfull + 8 * qs.slot, qs.phase, limit);
+        const unsigned char *qrow = mem + kStages * L::kStage + L::kJoin + qs.slot * L::kQ;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int rho = g + 8 * i;
+        for (int i = 0; i < RH; ++i) {
             uint4 v[D / 32];
             uint32_t m = 0;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
-                v[c] = lds128(qbuf + qs.slot * L::kQ + rho * D * 2 + t * (D / 2) + c * 16);
+                v[c] = *reinterpret_cast<const uint4 *>(qrow + (8 * i + g) * D * 2 + t * (D / 2) + c * 16);
                 m = sfar_max_abs2(sfar_max_abs2(sfar_max_abs2(sfar_max_abs2(m, v[c].x), v[c].y), v[c].z), v[c].w);
             }
             m = sfar_max_half(m);
@@ -330,17 +337,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_attn(const __grid_constant__
             m = max(m, __shfl_xor_sync(SFAR_FULL, m, 2));
             const int e = max((int)(m >> 7) - 127, -112);       // largest magnitude below 2^(e + 1)
             const float up = sfar_exp2i(14 - e);
-            f[i] = a.scale * 1.4426950408889634f * sfar_exp2i(max(e - 14, -126));
+            const float mine = a.scale * 1.4426950408889634f * sfar_exp2i(max(e - 14, -126));
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
                 for (int x = 0; x < 4; ++x)       // values 8 c + 2 x, + 1 of the lane's D / 4
-                    q[2 * c + (x >> 1)][2 * (x & 1) + i] = half2_of(bf16_lo(w[x]) * up, bf16_hi(w[x]) * up);
+                    q[i][2 * c + (x >> 1)][x & 1] = half2_of(bf16_lo(w[x]) * up, bf16_hi(w[x]) * up);
             }
-            const int pos = p.len - p.count + (p.rt * kRows + rho) / a.G;
-            hi[i] = rho < rows ? pos + 1 : INT_MAX;
-            lo[i] = rho < rows && a.window ? max(0, pos - a.window + 1) : 0;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int rho = 8 * i + 2 * t + y, pos = p.len - p.count + (p.rt * kRows + rho) / a.G;
+                f[i][y] = __shfl_sync(SFAR_FULL, mine, 4 * (2 * t + y));
+                hi[i][y] = rho < rows ? pos + 1 : INT_MAX;
+                lo[i][y] = rho < rows && a.window ? max(0, pos - a.window + 1) : 0;
+            }
         }
         __syncwarp();
         if (lane == 0)
@@ -350,90 +361,102 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_attn(const __grid_constant__
         const int pos0 = p.len - p.count + p.rt * kRows / a.G, pos1 = p.len - p.count + (p.rt * kRows + rows - 1) / a.G;
         const int all_from = a.window ? max(0, pos1 - a.window + 1) : 0, all_to = pos0 + 1;
 
-        float o[D / 8][4];
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-            o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        float o[RH][D / 16][4] = {};               // o[i][n][2 h + y]: row 8 i + 2 t + y, element (D / 8) g + 2 n + h
         // log2 references: of the scores (sum), of the weights (o)
-        float top[2] = {-INFINITY, -INFINITY}, wtop[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
-        for (int k = 0; k < p.tiles; ++k) {
-            const int j0 = (p.tile0 + k) * kTile;
+        float top[RH][2], wtop[RH][2], sum[RH][2];
+#pragma unroll
+        for (int i = 0; i < 2 * RH; ++i) {
+            top[i >> 1][i & 1] = wtop[i >> 1][i & 1] = -INFINITY;
+            sum[i >> 1][i & 1] = 0.f;
+        }
+        const int j00 = p.tile0 * kTile, j1 = j00 + p.tiles * kTile;
+        for (int j0 = j00; j0 < j1; j0 += kTile) {
             dead = dead || !tc::bar_wait(full + 8 * st.slot, st.phase, limit);
-            const uint32_t kt = ring + st.slot * L::kStage, vt = kt + kTile * D;
+            const unsigned char *kt = mem + st.slot * L::kStage, *vt = kt + kTile * D;
             const Meta &m = meta[st.slot];
             const bool edge = j0 < all_from || j0 + kTile > all_to || m.bad;
             const int c0 = warp * 16;              // this warp's tokens of the tile
-            float s[2][4] = {};
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int tok = c0 + 8 * n + token_of<D>(g);
+            // scores, transposed: x[i][2 h + y] of token g (+ 8 h) and row 8 i + 2 t + y
+            float x[RH][4] = {};
+            {
+                const unsigned char *k0 = kt, *k1 = kt;
+                uint4 ka[D / 64], kb[D / 64];
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
-                    const uint4 w4 = lds128(kt + at_chunk<D>(tok, t * (D / 64) + c));
-                    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+                    ka[c] = *reinterpret_cast<const uint4 *>(k0 + at_chunk<D>(c0 + token_of<D>(g), t * (D / 64) + c));
+                    kb[c] = *reinterpret_cast<const uint4 *>(k1 + at_chunk<D>(c0 + 8 + token_of<D>(g), t * (D / 64) + c));
+                }
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        mma_f16(s[n], q[4 * c + x], cvt_f16x2_e4m3(w[x]), cvt_f16x2_e4m3(w[x] >> 16));
+                for (int c = 0; c < D / 64; ++c) {
+                    const uint32_t w[4] = {ka[c].x, ka[c].y, ka[c].z, ka[c].w}, z[4] = {kb[c].x, kb[c].y, kb[c].z, kb[c].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t a0 = cvt_f16x2_e4m3(w[e]), a1 = cvt_f16x2_e4m3(z[e]), a2 = cvt_f16x2_e4m3(w[e] >> 16),
+                                       a3 = cvt_f16x2_e4m3(z[e] >> 16);
+#pragma unroll
+                        for (int i = 0; i < RH; ++i)
+                            mma_f16(x[i], a0, a1, a2, a3, q[i][4 * c + e]);
+                    }
                 }
             }
             const float ks = m.ks[warp], vs = m.vs[warp];
             const bool gone = (m.bad >> warp) & 1;
-            // scores in units of log2; columns 2 t, 2 t + 1 of either fragment
-            float x[2][4];
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    x[n][e] = s[n][e] * (f[e >> 1] * ks);
-            if (edge) {
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = j0 + c0 + 8 * n + token_of<D>(2 * t + (e & 1));
-                        if (gone || j >= p.len || j < lo[e >> 1] || j >= hi[e >> 1])
-                            x[n][e] = -INFINITY;
-                    }
-            }
             const float lvs = lg2(fabsf(vs));
-            float now[2];
+            bool move = false;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                now[i] = fmaxf(fmaxf(x[0][2 * i], x[0][2 * i + 1]), fmaxf(x[1][2 * i], x[1][2 * i + 1]));
-                now[i] = fmaxf(now[i], __shfl_xor_sync(SFAR_FULL, now[i], 1));
-                now[i] = fmaxf(now[i], __shfl_xor_sync(SFAR_FULL, now[i], 2));
-            }
-            const bool move = now[0] > top[0] + kAttnLift || now[1] > top[1] + kAttnLift || now[0] + lvs > wtop[0] + kAttnLift ||
-                              now[1] + lvs > wtop[1] + kAttnLift;
+            for (int i = 0; i < RH; ++i)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const float by = f[i][y] * ks;   // to units of log2
+                    x[i][y] *= by;
+                    x[i][2 + y] *= by;
+                    if (edge) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int j = j0 + c0 + 8 * h + token_of<D>(g);
+                            if (gone || j >= p.len || j < lo[i][y] || j >= hi[i][y])
+                                x[i][2 * h + y] = -INFINITY;
+                        }
+                    }
+                    const float now = fmaxf(x[i][y], x[i][2 + y]);
+                    move = move || now > top[i][y] + kAttnLift || now + lvs > wtop[i][y] + kAttnLift;
+                }
             if (__any_sync(SFAR_FULL, move)) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float next = fmaxf(top[i], now[i]), wnext = fmaxf(wtop[i], now[i] + lvs);
-                    const float keep = wtop[i] == -INFINITY ? 0.f : ex2(wtop[i] - wnext);
-                    sum[i] *= top[i] == -INFINITY ? 1.f : ex2(top[i] - next);
-                    top[i] = next;
-                    wtop[i] = wnext;
+                for (int i = 0; i < RH; ++i)
 #pragma unroll
-                    for (int n = 0; n < D / 8; ++n) {
-                        o[n][2 * i] *= keep;
-                        o[n][2 * i + 1] *= keep;
+                    for (int y = 0; y < 2; ++y) {
+                        float now = fmaxf(x[i][y], x[i][2 + y]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1)
+                            now = fmaxf(now, __shfl_xor_sync(SFAR_FULL, now, d));
+                        const float next = fmaxf(top[i][y], now), wnext = fmaxf(wtop[i][y], now + lvs);
+                        const float keep = wtop[i][y] == -INFINITY ? 1.f : ex2(wtop[i][y] - wnext);      // o is 0 then, or NaN
+                        sum[i][y] *= top[i][y] == -INFINITY ? 1.f : ex2(top[i][y] - next);
+                        top[i][y] = next;
+                        wtop[i][y] = wnext;
+#pragma unroll
+                        for (int n = 0; n < D / 16; ++n) {
+                            o[i][n][y] *= keep;
+                            o[i][n][2 + y] *= keep;
+                        }
                     }
-                }
             }
-            uint32_t w[4];
+            uint32_t w[RH][2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float ref = top[i] == -INFINITY ? 0.f : top[i];
-                const float by = copysignf(wtop[i] == -INFINITY ? 0.f : ex2(ref + lvs - wtop[i]), vs);
+            for (int i = 0; i < RH; ++i) {
                 float e4[4];
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        e4[2 * n + e] = ex2(x[n][2 * i + e] - ref);
-                sum[i] += (e4[0] + e4[1]) + (e4[2] + e4[3]);
-                w[i] = half2_of(e4[0] * by, e4[1] * by);
-                w[2 + i] = half2_of(e4[2] * by, e4[3] * by);
+                for (int y = 0; y < 2; ++y) {
+                    const float ref = top[i][y] == -INFINITY ? 0.f : top[i][y];
+                    const float by = copysignf(wtop[i][y] == -INFINITY ? 0.f : ex2(ref + lvs - wtop[i][y]), vs);
+                    const float e0 = ex2(x[i][y] - ref), e1 = ex2(x[i][2 + y] - ref);
+                    sum[i][y] += e0 + e1;
+                    e4[y] = e0 * by;
+                    e4[2 + y] = e1 * by;
+                }
+                w[i][0] = transpose8(half2_of(e4[0], e4[1]));
+                w[i][1] = transpose8(half2_of(e4[2], e4[3]));
             }
             // values: rows of the columns 2 t, 2 t + 1 (either fragment), 16 (8) bytes of the head at 16 g (8 g)
             constexpr int kW = D / 32;             // words of a lane's part of a row
@@ -442,31 +465,35 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_attn(const __grid_constant__
             for (int e = 0; e < 4; ++e) {
                 const int tok = c0 + 8 * (e >> 1) + token_of<D>(2 * t + (e & 1));
                 if constexpr (D == 128) {
-                    const uint4 y = lds128(vt + at_chunk<D>(tok, g));
+                    const uint4 y = *reinterpret_cast<const uint4 *>(vt + at_chunk<D>(tok, g));
                     v[e][0] = y.x;
                     v[e][1] = y.y;
                     v[e][2] = y.z;
                     v[e][3] = y.w;
                 } else {
-                    const uint2 y = lds64(vt + at_chunk<D>(tok, g >> 1) + (g & 1) * 8);
+                    const uint2 y = *reinterpret_cast<const uint2 *>(vt + at_chunk<D>(tok, g >> 1) + (g & 1) * 8);
                     v[e][0] = y.x;
                     v[e][1] = y.y;
                 }
             }
-            bool nan = false;
             if (edge) {
-                // a value that some row must not see is taken out; one that is NaN is put back below for the rows that see it
+                // places that hold no token are zeros; a NaN, which would reach every row, is taken out, and put back
+                // when the piece is joined
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int j = j0 + c0 + 8 * (e >> 1) + token_of<D>(2 * t + (e & 1));
-                    const bool off = gone || j >= p.len;
+                    uint32_t any = 0;
 #pragma unroll
                     for (int i = 0; i < kW; ++i) {
-                        if (off)
+                        if (gone || j >= p.len)
                             v[e][i] = 0;
                         const uint32_t is = __vcmpeq4(v[e][i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                        nan = nan || is;
+                        any |= is;
                         v[e][i] &= ~is;
+                    }
+                    if (any) {
+                        atomicMin(&s_nan[piece & 1][0], j);
+                        atomicMax(&s_nan[piece & 1][1], j);
                     }
                 }
             }
@@ -474,29 +501,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_attn(const __grid_constant__
             for (int i = 0; i < kW; ++i) {
                 const uint32_t a01 = __byte_perm(v[0][i], v[1][i], 0x5140), a23 = __byte_perm(v[0][i], v[1][i], 0x7362);
                 const uint32_t b01 = __byte_perm(v[2][i], v[3][i], 0x5140), b23 = __byte_perm(v[2][i], v[3][i], 0x7362);
-                mma_f16(o[4 * i], w, cvt_f16x2_e4m3(a01), cvt_f16x2_e4m3(b01));
-                mma_f16(o[4 * i + 1], w, cvt_f16x2_e4m3(a01 >> 16), cvt_f16x2_e4m3(b01 >> 16));
-                mma_f16(o[4 * i + 2], w, cvt_f16x2_e4m3(a23), cvt_f16x2_e4m3(b23));
-                mma_f16(o[4 * i + 3], w, cvt_f16x2_e4m3(a23 >> 16), cvt_f16x2_e4m3(b23 >> 16));
-            }
-            if (edge && __any_sync(SFAR_FULL, nan)) {
-                // o[n][2 i + e]: row g + 8 i, element (D / 8) (2 t + e) + n of the head
-                for (int n = 0; n < 16 && !gone; ++n) {
-                    const int j = j0 + c0 + n;
+                const uint32_t va[8] = {cvt_f16x2_e4m3(a01), cvt_f16x2_e4m3(a01 >> 16), cvt_f16x2_e4m3(b01), cvt_f16x2_e4m3(b01 >> 16),
+                                        cvt_f16x2_e4m3(a23), cvt_f16x2_e4m3(a23 >> 16), cvt_f16x2_e4m3(b23), cvt_f16x2_e4m3(b23 >> 16)};
 #pragma unroll
-                    for (int d = 0; d < D / 8; ++d)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int at = (D / 8) * (2 * t + e) + d;
-                            uint32_t byte;
-                            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(vt + at_chunk<D>(c0 + n, at >> 4) + (at & 15)));
-                            if ((byte & 0x7f) == 0x7f && j < p.len) {
-                                if (j >= lo[0] && j < hi[0])
-                                    o[d][e] = NAN;
-                                if (j >= lo[1] && j < hi[1])
-                                    o[d][2 + e] = NAN;
-                            }
-                        }
+                for (int r8 = 0; r8 < RH; ++r8) {
+                    mma_f16(o[r8][2 * i], va[0], va[1], va[2], va[3], w[r8]);
+                    mma_f16(o[r8][2 * i + 1], va[4], va[5], va[6], va[7], w[r8]);
                 }
             }
             __syncwarp();
@@ -504,51 +514,69 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_attn(const __grid_constant__
                 tc::bar_arrive(empty + 8 * st.slot);
             st.next();
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            sum[i] += __shfl_xor_sync(SFAR_FULL, sum[i], 1);
-            sum[i] += __shfl_xor_sync(SFAR_FULL, sum[i], 2);
-        }
         // join the warps' states
         consumers_sync();                          // the last piece's has been read
-        if (t == 0)
+        if (tid == 0) {
+            s_nan[(piece + 1) & 1][0] = INT_MAX;
+            s_nan[(piece + 1) & 1][1] = -1;
+        }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                s_ml[0][warp][g + 8 * i] = top[i];
-                s_ml[1][warp][g + 8 * i] = sum[i];
-                s_ml[2][warp][g + 8 * i] = wtop[i];
-            }
+        for (int i = 0; i < RH; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+            for (int y = 0; y < 2; ++y) {
+                float all = sum[i][y];
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int n = 0; n < D / 8; n += 4) {
-                    float *dst = join + (warp * kRows + g + 8 * i) * L::kRow + t * (D / 4 + 4) + e * (D / 8) + n;
-                    *reinterpret_cast<float4 *>(dst) =
-                        make_float4(o[n][2 * i + e], o[n + 1][2 * i + e], o[n + 2][2 * i + e], o[n + 3][2 * i + e]);
+                for (int d = 4; d < 32; d <<= 1)
+                    all += __shfl_xor_sync(SFAR_FULL, all, d);
+                const int rho = 8 * i + 2 * t + y;
+                if (g == 0) {
+                    s_ml[0][warp][rho] = top[i][y];
+                    s_ml[1][warp][rho] = all;
+                    s_ml[2][warp][rho] = wtop[i][y];
                 }
+                float *dst = join + (warp * kRows + rho) * L::kRow + g * (D / 8);
+#pragma unroll
+                for (int n = 0; n < D / 16; n += 2)
+                    *reinterpret_cast<float4 *>(dst + 2 * n) = make_float4(o[i][n][y], o[i][n][2 + y], o[i][n + 1][y], o[i][n + 1][2 + y]);
+            }
         consumers_sync();
-        constexpr int kE = D / 8;                  // elements of one row per thread: 8 threads a row
-        const int row = tid >> 3, col = (tid & 7) * kE;
+        constexpr int kE = RH * D / 16, kT = D / kE;       // elements of one row per thread, threads of a row
+        const int row = tid / kT, col = tid % kT * kE;
         SfarAttnState<kE> all;
         for (int w = 0; w < kConsumers; ++w)
             all.reference(s_ml[0][w][row], s_ml[2][w][row]);
 #pragma unroll
         for (int w = 0; w < kConsumers; ++w) {
             const float by = all.add(s_ml[0][w][row], s_ml[1][w][row], s_ml[2][w][row]);
-            const float *src = join + (w * kRows + row) * L::kRow + col / (D / 4) * (D / 4 + 4) + col % (D / 4);
+            const float *src = join + (w * kRows + row) * L::kRow + col;
 #pragma unroll
             for (int e = 0; e < kE; e += 4)
                 all.add4(e, by, *reinterpret_cast<const float4 *>(src + e));
+        }
+        const int *nan = s_nan[piece++ & 1];
+        if (nan[1] >= 0 && row < rows) {
+            const int n = p.rt * kRows + row, pos = p.len - p.count + n / a.G;
+            const int from = max(max(nan[0], p.tile0 * kTile), a.window ? pos - a.window + 1 : 0);
+            const int to = min(min(nan[1], pos), (p.tile0 + p.tiles) * kTile - 1);
+            for (int j = from; j <= to; ++j) {
+                const int page = a.table[(size_t)p.b * a.W + (j >> a.shift)];
+                if ((unsigned)page >= (unsigned)a.pages)
+                    continue;
+                const uint8_t *vp = a.v[r] + ((((long long)page * a.Hk + hk) << a.shift) + (j & ((1 << a.shift) - 1))) * D + col;
+#pragma unroll
+                for (int e = 0; e < kE; ++e)
+                    if ((vp[e] & 0x7f) == 0x7f)
+                        all.o[e] = NAN;
+            }
         }
         bool write = true;
         if (p.tiles < p.all) {
             // a part: leave it in the workspace; the last of the row tile's CTAs joins them in order
             const long long from = u - (p.tile0 - p.begin), to = from + p.all;
-            const long long c0 = ((from + 1) * N - 1) / U, c1 = (to * N - 1) / U;
+            const int c0 = (int)sfar_div((from + 1) * N - 1, U), c1 = (int)sfar_div(to * N - 1, U);
+
             const int mine = p.tile0 == p.begin ? 1 : 0;
-            auto slot = [&](long long c, int which) { return a.part + ((size_t)c * 2 + which) * (kRows * (D + 4)); };
+            auto slot = [&](int c, int which) { return a.part + ((size_t)c * 2 + which) * (kRows * (D + 4)); };
             float *dst = slot(blockIdx.x, mine);
             if (row < rows) {
 #pragma unroll
@@ -562,22 +590,26 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_attn(const __grid_constant__
             consumers_sync();
             if (tid == 0) {
                 const int done = atomicAdd(a.arrived + c0, 1);
-                s_last = done == (int)(c1 - c0);
+                s_last = done == c1 - c0;
                 if (s_last)
                     a.arrived[c0] = 0;             // for the next call
             }
             consumers_sync();
             write = s_last;
-            if (write && row < rows) {
+            if (write) {
                 __threadfence();
                 all = SfarAttnState<kE>();
-#pragma unroll 8
-                for (long long c = c0; c <= c1; ++c) {
+                const int last = row < rows ? c1 : c0 - 1;
+                // the threads of a row share the references out
+                for (int c = c0 + tid % kT; c <= last; c += kT) {
                     const float4 m = __ldcg(reinterpret_cast<const float4 *>(slot(c, c == c0) + kRows * D + row * 4));
                     all.reference(m.x, m.z);
                 }
+#pragma unroll
+                for (int d = 1; d < kT; d <<= 1)
+                    all.reference(__shfl_xor_sync(SFAR_FULL, all.top, d), __shfl_xor_sync(SFAR_FULL, all.wtop, d));
 #pragma unroll 4
-                for (long long c = c0; c <= c1; ++c) {
+                for (int c = c0; c <= last; ++c) {
                     const float *src = slot(c, c == c0);
                     const float4 m = __ldcg(reinterpret_cast<const float4 *>(src + kRows * D + row * 4));
                     float4 v[kE / 4];
@@ -596,9 +628,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_attn(const __grid_constant__
             const float inv = all.factor();
             uint16_t *dst = a.out[r] + (long long)(p.first + n / a.G) * a.ots + (long long)(hk * a.G + n % a.G) * a.ohs + col;
 #pragma unroll
-            for (int e = 0; e < kE; e += 8)
-                st_v4(dst + e, make_uint4(tc::bf16x2(all.o[e] * inv, all.o[e + 1] * inv), tc::bf16x2(all.o[e + 2] * inv, all.o[e + 3] * inv),
-                                          tc::bf16x2(all.o[e + 4] * inv, all.o[e + 5] * inv), tc::bf16x2(all.o[e + 6] * inv, all.o[e + 7] * inv)));
+            for (int e = 0; e < kE; e += 4)
+                st_v2u32(dst + e, tc::bf16x2(all.o[e] * inv, all.o[e + 1] * inv), tc::bf16x2(all.o[e + 2] * inv, all.o[e + 3] * inv));
         }
         u += p.tiles;
     }
@@ -606,9 +637,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_attn(const __grid_constant__
         sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
 }
 
-const void *sfar_kernel_kv_attn(int head_dim, int *threads, int *smem)
+// rows: 8 or 16 at a time
+const void *sfar_kernel_kv_attn(int head_dim, int rows, int *threads, int *smem)
 {
+#define SFAR_ATTN(D, RH) (*smem = Lay<D, RH>::kBytes + 1024, (const void *)k_kv_attn<D, RH>)
     *threads = kThreads;
-    *smem = (head_dim == 64 ? Lay<64>::kBytes : Lay<128>::kBytes) + 1024;
-    return head_dim == 64 ? (const void *)k_kv_attn<64> : (const void *)k_kv_attn<128>;
+    if (rows == 8)
+        return head_dim == 64 ? SFAR_ATTN(64, 1) : SFAR_ATTN(128, 1);
+    return head_dim == 64 ? SFAR_ATTN(64, 2) : SFAR_ATTN(128, 2);
+#undef SFAR_ATTN
 }

@@ -101,7 +101,7 @@ struct Work {
         Piece p;
         p.at = u;
         const uint32_t S = upto[a.B];
-        p.plane = (int)(u / S);
+        p.plane = (int)sfar_div(u, S);
         const uint32_t v = (uint32_t)(u - (long long)p.plane * S);
         int lo = 0, hi = a.B;
         while (hi - lo > 1) {
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
 
     const long long U = (long long)carry * a.R * a.Hk;
     const long long N = min((long long)gridDim.x, U);
-    const long long u0 = blockIdx.x < N ? blockIdx.x * U / N : 0, u1 = blockIdx.x < N ? (blockIdx.x + 1) * U / N : 0;
+    const long long u0 = blockIdx.x < N ? sfar_div(blockIdx.x * U, N) : 0, u1 = blockIdx.x < N ? sfar_div((blockIdx.x + 1) * U, N) : 0;
 
     if (warp < kSoft) {
         // -------------------------------------------------------------- softmax
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             if (mine && part) {
                 // the last of the row tile's CTAs joins its parts in order; the two tiles of rows separately
                 const long long from = p.at - (p.tile0 - p.begin), to = from + p.all;
-                const long long c0 = ((from + 1) * N - 1) / U, c1 = (to * N - 1) / U;
+                const long long c0 = sfar_div((from + 1) * N - 1, U), c1 = sfar_div(to * N - 1, U);
                 __threadfence();
                 tile_sync(x);
                 if ((tid & 255) == 0) {

@@ -25,6 +25,11 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi)
     return r;
 }
 
+// a / b for a >= 0, b > 0, in 32 bits where they fit (a 64-bit division takes some hundred instructions)
+__device__ __forceinline__ long long sfar_div(long long a, long long b)
+{
+    return (a | b) >> 32 == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
 // Request b: its context, how many new tokens it has and the row of the first.
 __device__ __forceinline__ void sfar_attn_request(const SfarAttnArgs &a, int b, int &len, int &count, int &first)
 {

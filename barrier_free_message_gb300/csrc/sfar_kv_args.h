@@ -77,7 +77,7 @@ struct SfarGemm8Args {
 
 const void *sfar_kernel_kv_plan();
 const void *sfar_kernel_kv_append(int head_dim);
-const void *sfar_kernel_kv_attn(int head_dim, int *threads, int *smem);
+const void *sfar_kernel_kv_attn(int head_dim, int rows, int *threads, int *smem);
 const void *sfar_kernel_kv_prompt(int head_dim, int *threads, int *smem);
 const void *sfar_kernel_quantize();
 const void *sfar_kernel_gemm8(int tokens, int *threads, int *smem);
@@ -88,7 +88,6 @@ int sfar_fp8_prepare();
 #define SFAR_PLAN_CLUSTER 8
 #define SFAR_APPEND_WARPS 8
 #define SFAR_ATTN_TILE 64
-#define SFAR_ATTN_STAGES 4
-#define SFAR_ATTN_CTAS 2                    // per SM
+#define SFAR_ATTN_CTAS(rows) ((rows) == 8 ? 3 : 2)   // per SM
 #define SFAR_PROMPT_ROWS 256
 #define SFAR_PROMPT_REQUESTS 2048           // whose prefix sums fit beside the prompt kernel's tiles

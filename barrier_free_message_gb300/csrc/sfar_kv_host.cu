@@ -159,9 +159,9 @@ sfar_kv_t *sfar_kv_create(int R, int q_heads, int kv_heads, int head_dim, int pa
             delete h;
             return fail(encode ? SFAR_ERR_INVALID : SFAR_ERR_UNSUPPORTED);
         }
-    const size_t ctas = (size_t)sms * SFAR_ATTN_CTAS;
+    const size_t ctas = (size_t)sms * 3;                   // the most CTAs of any of the kernels
     const size_t o_arrived = 256, o_part = (o_arrived + ctas * 8 + 255) / 256 * 256;
-    const size_t few = ctas * 2 * 16, many = (size_t)sms * 2 * SFAR_PROMPT_ROWS;     // rows of partial results
+    const size_t few = (size_t)sms * 2 * 2 * 16, many = (size_t)sms * 2 * SFAR_PROMPT_ROWS;     // rows of partial results
     const size_t bytes = o_part + (few > many ? few : many) * ((size_t)head_dim + 4) * 4;
     if (cudaMalloc(&h->ws, bytes) != cudaSuccess) {
         cudaGetLastError();
@@ -177,13 +177,15 @@ sfar_kv_t *sfar_kv_create(int R, int q_heads, int kv_heads, int head_dim, int pa
     init.strag_rank = init.drop_rank = -1;
     init.f_rank = init.f_cta = init.f_peer = -1;
     int threads = 0, smem = 0;
-    const void *attn = sfar_kernel_kv_attn(head_dim, &threads, &smem);
     int pthreads = 0, psmem = 0;
     const void *prompt = sfar_kernel_kv_prompt(head_dim, &pthreads, &psmem);
     if (cudaMemset(h->ws, 0, bytes) != cudaSuccess ||
         cudaFuncSetAttribute(prompt, cudaFuncAttributeMaxDynamicSharedMemorySize, psmem + (SFAR_PROMPT_REQUESTS + 1) * 4) != cudaSuccess ||
         cudaMemcpy(h->ctl, &init, sizeof init, cudaMemcpyHostToDevice) != cudaSuccess ||
-        cudaFuncSetAttribute(attn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem + (SFAR_KV_MAX_REQUESTS + 1) * 4) != cudaSuccess ||
+        cudaFuncSetAttribute(sfar_kernel_kv_attn(head_dim, 8, &threads, &smem), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem + (SFAR_KV_MAX_REQUESTS + 1) * 4) != cudaSuccess ||
+        cudaFuncSetAttribute(sfar_kernel_kv_attn(head_dim, 16, &threads, &smem), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem + (SFAR_KV_MAX_REQUESTS + 1) * 4) != cudaSuccess ||
         cudaStreamCreateWithFlags(&h->priv, cudaStreamNonBlocking) != cudaSuccess ||
         cudaMallocHost(&h->host_ctl, sizeof(SfarCtl)) != cudaSuccess ||
         cudaFuncSetAttribute(sfar_kernel_kv_plan(), cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -341,8 +343,9 @@ sfar_status sfar_kv_attention(sfar_kv_t *h, const void *const q[], void *const o
         const void *f = sfar_kernel_kv_prompt(h->D, &threads, &smem);
         return launch(h->dev, f, dim3((unsigned)h->sms), (unsigned)threads, (size_t)smem + (requests + 1) * 4, &a, s);
     }
-    const void *f = sfar_kernel_kv_attn(h->D, &threads, &smem);
-    return launch(h->dev, f, dim3((unsigned)(h->sms * SFAR_ATTN_CTAS)), (unsigned)threads, (size_t)smem + (requests + 1) * 4, &a, s);
+    const int rows = max_q * (size_t)a.G <= 8 ? 8 : 16;
+    const void *f = sfar_kernel_kv_attn(h->D, rows, &threads, &smem);
+    return launch(h->dev, f, dim3((unsigned)(h->sms * SFAR_ATTN_CTAS(rows))), (unsigned)threads, (size_t)smem + (requests + 1) * 4, &a, s);
 }
 
 sfar_status sfar_kv_status_get(sfar_kv_t *h, sfar_fault *info)
