@@ -165,6 +165,8 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
         s_nan[0][0] = INT_MAX;
         s_nan[0][1] = -1;
     }
+    if (tid < 2 * a.R)
+        tc::prefetch_map(tid & 1 ? &a.vmap[tid >> 1] : &a.kmap[tid >> 1]);
     pdl_wait();
     const unsigned long long limit = ld_relaxed_u64(&a.ctl->timeout_ns);
 
@@ -204,12 +206,12 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
         __syncthreads();
     }
 
-    sfar_attn_padding<D>(a);
-
     const long long U = (long long)carry * a.R * a.Hk;
     const long long N = min((long long)gridDim.x, U);
-    if (blockIdx.x >= N)
+    if (blockIdx.x >= N) {
+        sfar_attn_padding<D>(a, tid, kThreads);
         return;
+    }
     const long long u0 = sfar_div(blockIdx.x * U, N), u1 = sfar_div((blockIdx.x + 1) * U, N);
 
     if (warp == kConsumers) {
@@ -224,24 +226,27 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
         for (long long u = u0; u < u1 && !gave_up;) {
             const Piece p = work.at(u, u1);
             const int r = p.plane / a.Hk, hk = p.plane % a.Hk;
-            if (!tc::bar_wait(qempty + 8 * qs.slot, qs.phase ^ 1u, limit)) {
-                gave_up = true;
-                break;
-            }
-            for (int i = lane; i < kRows * D / 8; i += 32) {
-                const int rho = i / (D / 8), c = i % (D / 8), row = p.rt * kRows + rho;
-                const int tok = row / a.G;
-                const uint16_t *src = a.q[r];
-                uint32_t bytes = 0;
-                if (tok < p.count) {
-                    src += (long long)(p.first + tok) * a.qts + (long long)(hk * a.G + row % a.G) * a.qhs + c * 8;
-                    bytes = 16;
+            // the piece's query rows, once its first copies are on their way
+            auto fetch = [&]() {
+                if (!tc::bar_wait(qempty + 8 * qs.slot, qs.phase ^ 1u, limit)) {
+                    gave_up = true;
+                    return;
                 }
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(qbuf + qs.slot * L::kQ + i * 16), "l"(src), "r"(bytes)
-                             : "memory");
-            }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(qfull + 8 * qs.slot) : "memory");
-            qs.next();
+                for (int i = lane; i < kRows * D / 8; i += 32) {
+                    const int rho = i / (D / 8), c = i % (D / 8), row = p.rt * kRows + rho;
+                    const int tok = row / a.G;
+                    const uint16_t *src = a.q[r];
+                    uint32_t bytes = 0;
+                    if (tok < p.count) {
+                        src += (long long)(p.first + tok) * a.qts + (long long)(hk * a.G + row % a.G) * a.qhs + c * 8;
+                        bytes = 16;
+                    }
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(qbuf + qs.slot * L::kQ + i * 16), "l"(src), "r"(bytes)
+                                 : "memory");
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(qfull + 8 * qs.slot) : "memory");
+                qs.next();
+            };
             const int *row = a.table + (size_t)p.b * a.W;
             for (int k = 0; k < p.tiles; ++k) {
                 const int j0 = (p.tile0 + k) * kTile;
@@ -268,6 +273,8 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
                     tc::load_3d(dst, &a.kmap[r], 0, j & ((1 << a.shift) - 1), slab, bar, once);
                     tc::load_3d(dst + kTile * D, &a.vmap[r], 0, j & ((1 << a.shift) - 1), slab, bar, once);
                 }
+                if (k == 0)
+                    fetch();
                 const unsigned any = __ballot_sync(SFAR_FULL, go);
                 const int of = lane * 16 / per;                             // the copy that 16 tokens lie in
                 const float k16 = __shfl_sync(SFAR_FULL, ks, of & 31), v16 = __shfl_sync(SFAR_FULL, vs, of & 31);
@@ -586,10 +593,11 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
                 if (col == 0)
                     __stcg(reinterpret_cast<float4 *>(dst + kRows * D + row * 4), make_float4(all.top, all.sum, all.wtop, 0.f));
             }
-            __threadfence();
             consumers_sync();
             if (tid == 0) {
+                __threadfence();                   // of all the CTA's writes: the barrier has ordered them before it
                 const int done = atomicAdd(a.arrived + c0, 1);
+                __threadfence();
                 s_last = done == c1 - c0;
                 if (s_last)
                     a.arrived[c0] = 0;             // for the next call
@@ -597,7 +605,6 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
             consumers_sync();
             write = s_last;
             if (write) {
-                __threadfence();
                 all = SfarAttnState<kE>();
                 const int last = row < rows ? c1 : c0 - 1;
                 // the threads of a row share the references out
@@ -608,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
 #pragma unroll
                 for (int d = 1; d < kT; d <<= 1)
                     all.reference(__shfl_xor_sync(SFAR_FULL, all.top, d), __shfl_xor_sync(SFAR_FULL, all.wtop, d));
-#pragma unroll 4
+#pragma unroll 6
                 for (int c = c0; c <= last; ++c) {
                     const float *src = slot(c, c == c0);
                     const float4 m = __ldcg(reinterpret_cast<const float4 *>(src + kRows * D + row * 4));
@@ -633,6 +640,7 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
         }
         u += p.tiles;
     }
+    sfar_attn_padding<D>(a, tid, 32 * kConsumers);
     if (dead && lane == 0)
         sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
 }

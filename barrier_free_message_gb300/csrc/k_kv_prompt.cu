@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             upto[b + 1] = before;
         __syncthreads();
     }
-    sfar_attn_padding<D>(a);
+    sfar_attn_padding<D>(a, tid, kThreads);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();

@@ -15,7 +15,6 @@ __global__ void __launch_bounds__(256) k_quant8(const __grid_constant__ SfarQuan
     const long long pairs = (a.kb + 1) / 2, units = pairs * a.m;
     const int r = blockIdx.y;
     pdl_wait();
-    pdl_launch_dependents();               // the projection sets itself up meanwhile, and waits for this kernel's end
     const uint16_t *x = a.x[r];
     for (long long u = blockIdx.x * 8ll + (threadIdx.x >> 5); u < units; u += gridDim.x * 8ll) {
         const long long row = u % a.m, b = 2 * (u / a.m) + half;

@@ -47,11 +47,12 @@ __device__ __forceinline__ void sfar_attn_check(const SfarAttnArgs &a, int b, in
     if (first < 0 || a.starts[b + 1] - first != count)
         sfar_kv_fault(a.ctl, b, SFAR_KV_BAD_TOKENS);
 }
-// Zeros for the rows past the last request, by the whole grid.
-template <int D> __device__ __forceinline__ void sfar_attn_padding(const SfarAttnArgs &a)
+// Zeros for the rows past the last request, by the whole grid; this thread is
+// `thread` of the `threads` that its CTA has for it (or of fewer than another's).
+template <int D> __device__ __forceinline__ void sfar_attn_padding(const SfarAttnArgs &a, int thread, int threads)
 {
     const long long rows = (long long)(a.T - max(0, min(a.starts[a.B], a.T))) * a.Hq * a.R;
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < rows; i += (long long)gridDim.x * blockDim.x) {
+    for (long long i = blockIdx.x + (long long)thread * gridDim.x; i < rows; i += (long long)gridDim.x * threads) {
         const int h = (int)(i % a.Hq), r = (int)(i / a.Hq % a.R);
         uint16_t *dst = a.out[r] + (a.T - 1 - i / a.Hq / a.R) * a.ots + h * a.ohs;
         for (int e = 0; e < D; e += 8)
