@@ -32,20 +32,32 @@ __global__ void __launch_bounds__(32 * SFAR_APPEND_WARPS) k_kv_append(const __gr
         return;
     const int kv = plane & 1, h = (plane >> 1) % a.H, r = (plane >> 1) / a.H;
 
-    // the window's runs: a token begins one if it does not continue its neighbour's page
-    const int t_lane = blockIdx.x * a.window + lane;
+    // The window's runs: a token begins one if it does not continue its neighbour's page.  A run may go on past the
+    // window, by less than a page: bit l of goes[w] says that token 32 w + l of the window and what follows continues
+    // the one before it.
+    const int t_base = blockIdx.x * a.window;
+    const int words = 1 + ((P + 31) >> 5);
     int slot = -1;
     bool leads = false;
-    if (lane < a.window && t_lane < a.T) {
-        slot = a.slots[t_lane];
-        if (slot >= 0 && (slot >> a.shift) >= a.pages) {
-            sfar_kv_fault(a.ctl, t_lane, SFAR_KV_BAD_SLOT);
+    uint32_t goes[5];
+    {
+        int s[5], before[5];
+#pragma unroll
+        for (int w = 0; w < 5; ++w) {
+            const int t = t_base + 32 * w + lane;
+            const bool in = w < words && t >= t_base && t < a.T;
+            s[w] = in ? a.slots[t] : -1;
+            before[w] = in && t > 0 ? a.slots[t - 1] : -1;
+        }
+        slot = s[0];
+        if (lane < a.window && t_base + lane < a.T && (slot < -1 || (slot >= 0 && (slot >> a.shift) >= a.pages))) {
+            sfar_kv_fault(a.ctl, t_base + lane, SFAR_KV_BAD_SLOT);
             slot = -1;
         }
-        if (slot >= 0)
-            leads = (slot & (P - 1)) == 0 || t_lane == 0 || a.slots[t_lane - 1] != slot - 1;
-        else if (slot < -1)
-            sfar_kv_fault(a.ctl, t_lane, SFAR_KV_BAD_SLOT);
+#pragma unroll
+        for (int w = 0; w < 5; ++w)
+            goes[w] = __ballot_sync(SFAR_FULL, s[w] >= 0 && s[w] == before[w] + 1 && (s[w] & (P - 1)) != 0 && before[w] >= 0);
+        leads = lane < a.window && slot >= 0 && !(goes[0] >> lane & 1u);
     }
     const uint16_t *src = a.x[kv][r] + (long long)h * a.hs[kv];
     const long long ts = a.ts[kv];
@@ -53,17 +65,19 @@ __global__ void __launch_bounds__(32 * SFAR_APPEND_WARPS) k_kv_append(const __gr
     float *scales = a.scale[kv][r];
     for (unsigned todo = __ballot_sync(SFAR_FULL, leads); todo; todo &= todo - 1) {
         const int from = __ffs(todo) - 1;
-        const int t0 = blockIdx.x * a.window + from;
+        const int t0 = t_base + from;
         const int s0 = __shfl_sync(SFAR_FULL, slot, from);
         const int page = s0 >> a.shift, first = s0 & (P - 1);
         int n = 1;                         // the run's tokens: at most what is left of the page
-        for (int at = 1; at < P - first; at += 32) {
-            const int o = at + lane;
-            const bool more = o < P - first && t0 + o < a.T && a.slots[t0 + o] == s0 + o;
-            const unsigned m = __ballot_sync(SFAR_FULL, more);
-            n += m == SFAR_FULL ? 32 : __ffs(~m) - 1;
-            if (m != SFAR_FULL)
+#pragma unroll
+        for (int w = 0; w < 5; ++w) {
+            // places of word w after `from` that end the run
+            const uint32_t after = w ? SFAR_FULL : from == 31 ? 0u : SFAR_FULL << (from + 1);
+            const uint32_t end = ~goes[w] & after;
+            if (end) {
+                n = 32 * w + __ffs(end) - 1 - from;
                 break;
+            }
         }
         const uint16_t *x = src + (long long)t0 * ts + (lane % kVec) * 8;
         const int tok = lane / kVec;       // of the step's tokens, this lane's
@@ -119,16 +133,22 @@ __global__ void __launch_bounds__(32 * SFAR_APPEND_WARPS) k_kv_append(const __gr
         }
         const SfarInv by(scale);
         uint8_t *dst = base + (long long)(first + tok) * D + (lane % kVec) * 8;
+        auto store = [&](auto how) {
 #pragma unroll
-        for (int i = 0; i < kKeep; ++i)
-            if (i * kTok + tok < n) {
-                const uint2 q = sfar_quantize8(keep[i], by, special);
+            for (int i = 0; i < kKeep; ++i)
+                if (i * kTok + tok < n) {
+                    const uint2 q = sfar_quantize8(keep[i], how, special);
+                    st_v2u32(dst + i * kTok * D, q.x, q.y);
+                }
+            for (int i = kKeep; i * kTok + tok < n; ++i) {
+                const uint2 q = sfar_quantize8(load(i), how, special);
                 st_v2u32(dst + i * kTok * D, q.x, q.y);
             }
-        for (int i = kKeep; i * kTok + tok < n; ++i) {
-            const uint2 q = sfar_quantize8(load(i), by, special);
-            st_v2u32(dst + i * kTok * D, q.x, q.y);
-        }
+        };
+        if (by.pow2)
+            store(by.inv);
+        else
+            store(by);
     }
 }
 

@@ -24,7 +24,8 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kThreads = SFAR_PLAN_THREADS, kWarps = kThreads / 32;
+constexpr int kMostWarps = SFAR_PLAN_THREADS / 32;
+constexpr int kShare = 4;                  // lanes of a request when its pages are written
 
 struct Sums {
     long long need, back, count;
@@ -32,10 +33,9 @@ struct Sums {
 
 __device__ __forceinline__ long long up(long long v, int shift) { return (v + (1ll << shift) - 1) >> shift; }
 
-// inclusive sums over the CTA; *total gets the CTA's
-__device__ __forceinline__ Sums block_scan(Sums v, Sums *total, Sums *warp_sums)
+__device__ __forceinline__ void warp_scan(Sums &v)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const long long a = __shfl_up_sync(SFAR_FULL, v.need, d), b = __shfl_up_sync(SFAR_FULL, v.back, d),
@@ -46,28 +46,33 @@ __device__ __forceinline__ Sums block_scan(Sums v, Sums *total, Sums *warp_sums)
             v.count += c;
         }
     }
+}
+// inclusive sums over the CTA's threads, on top of *carry, which goes on to include them
+__device__ __forceinline__ Sums block_scan(Sums v, Sums *carry, Sums *warp_sums)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (int)blockDim.x >> 5;
+    warp_scan(v);
     if (lane == 31)
         warp_sums[warp] = v;
     __syncthreads();
-    Sums before = {0, 0, 0}, all = {0, 0, 0};
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        const Sums s = warp_sums[w];
-        if (w < warp) {
-            before.need += s.need;
-            before.back += s.back;
-            before.count += s.count;
-        }
-        all.need += s.need;
-        all.back += s.back;
-        all.count += s.count;
+    if (warp == 0) {
+        Sums s = {0, 0, 0};
+        if (lane < warps)
+            s = warp_sums[lane];
+        warp_scan(s);
+        if (lane < warps)
+            warp_sums[lane] = s;
     }
     __syncthreads();
-    *total = all;
-    v.need += before.need;
-    v.back += before.back;
-    v.count += before.count;
-    return v;
+    Sums before = *carry;
+    if (warp > 0) {
+        const Sums s = warp_sums[warp - 1];
+        before = {before.need + s.need, before.back + s.back, before.count + s.count};
+    }
+    const Sums all = warp_sums[warps - 1];
+    *carry = {carry->need + all.need, carry->back + all.back, carry->count + all.count};
+    __syncthreads();
+    return {v.need + before.need, v.back + before.back, v.count + before.count};
 }
 
 }  // namespace
@@ -79,9 +84,9 @@ __global__ void __launch_bounds__(SFAR_PLAN_THREADS) k_kv_plan(const __grid_cons
     int *s_len = s_start + a.B + 1;         // [B] tokens held before
     int *s_new = s_len + a.B;               // [B] tokens held after (before, if refused)
     int *s_off = s_new + a.B;               // [B] ring offset of its pages taken or given back; -1 refused
-    __shared__ Sums warp_sums[kWarps];
+    __shared__ Sums warp_sums[kMostWarps];
     __shared__ int s_used;
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31, kThreads = blockDim.x;
     const int shift = a.shift;
     const int crank = blockIdx.x, csize = gridDim.x;
     if (tid == 0)
@@ -118,14 +123,7 @@ __global__ void __launch_bounds__(SFAR_PLAN_THREADS) k_kv_plan(const __grid_cons
             v.back = d < 0 ? have - want : 0;
             v.count = max(d, 0);
         }
-        Sums all;
-        Sums t = block_scan(v, &all, warp_sums);
-        t.need += carry.need;
-        t.back += carry.back;
-        t.count += carry.count;
-        carry.need += all.need;
-        carry.back += all.back;
-        carry.count += all.count;
+        const Sums t = block_scan(v, &carry, warp_sums);
         const bool ok = d <= 0 || (fits && (v.need == 0 || t.need <= freec));
         const int upto = ok && v.need > 0 ? (int)t.need : 0;
         const int best = __reduce_max_sync(SFAR_FULL, upto);
@@ -167,14 +165,15 @@ __global__ void __launch_bounds__(SFAR_PLAN_THREADS) k_kv_plan(const __grid_cons
         a.state_out[0] = (int)ring_at((unsigned)used);
         a.state_out[1] = (int)left;
     }
-    // table entries of new pages, ring entries of pages given back: a warp per request
-    for (int b = crank * kWarps + (tid >> 5); b < a.B; b += csize * kWarps) {
+    // table entries of new pages, ring entries of pages given back: a few lanes per request (most gain a page or none)
+    const int part = tid % kShare;
+    for (int b = (crank * kThreads + tid) / kShare; b < a.B; b += csize * kThreads / kShare) {
         const int off = s_off[b];
         if (off < 0)
             continue;
         const int have = (int)up(s_len[b], shift), want = (int)up(s_new[b], shift);
         int *row = a.table + (size_t)b * a.W;
-        for (int j = have + lane; j < want; j += 32) {
+        for (int j = have + part; j < want; j += kShare) {
             int p = a.ring[ring_at((unsigned)(off + j - have))];
             if ((unsigned)p >= pages) {
                 sfar_kv_fault(a.ctl, b, SFAR_KV_BAD_PAGE);
@@ -182,7 +181,7 @@ __global__ void __launch_bounds__(SFAR_PLAN_THREADS) k_kv_plan(const __grid_cons
             }
             row[j] = p;
         }
-        for (int j = want + lane; j < have; j += 32) {
+        for (int j = want + part; j < have; j += kShare) {
             const long long at = (long long)off + j - want;
             if (at >= (long long)a.pages - freec)
                 continue;                   // more than the pool has: recorded above
@@ -210,22 +209,29 @@ __global__ void __launch_bounds__(SFAR_PLAN_THREADS) k_kv_plan(const __grid_cons
             }
             b = lo;
         }
+        int last = -1, page = -1;          // neighbours mostly share a page: its number is read once
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const long long t = t0 + e;
             int slot = -1;
             if (t < total) {
-                while (t >= s_start[b + 1])
+                while (t >= s_start[b + 1]) {
                     ++b;
+                    last = -1;
+                }
                 const int off = s_off[b];
                 if (off >= 0) {
                     const int len = s_len[b], pos = len + (int)(t - s_start[b]);
-                    const int j = pos >> shift, have = (int)up(len, shift);
-                    const int p = j < have ? a.table[(size_t)b * a.W + j] : a.ring[ring_at((unsigned)(off + j - have))];
-                    if ((unsigned)p < pages)
-                        slot = (p << shift) + (pos & ((1 << shift) - 1));
-                    else
-                        sfar_kv_fault(a.ctl, b, SFAR_KV_BAD_PAGE);
+                    const int j = pos >> shift;
+                    if (j != last) {
+                        const int have = (int)up(len, shift);
+                        page = j < have ? a.table[(size_t)b * a.W + j] : a.ring[ring_at((unsigned)(off + j - have))];
+                        last = j;
+                        if ((unsigned)page >= pages)
+                            sfar_kv_fault(a.ctl, b, SFAR_KV_BAD_PAGE);
+                    }
+                    if ((unsigned)page < pages)
+                        slot = (page << shift) + (pos & ((1 << shift) - 1));
                 }
             }
             out[e] = slot;

@@ -59,15 +59,18 @@ struct SfarInv {
     __device__ __forceinline__ float operator()(float x) const { return pow2 ? x * inv : __fdiv_rn(x, s); }
 };
 
-// Eight bf16 (one 16-byte vector) as eight e4m3 of x / scale; `special`: some
-// value of the group is infinite or NaN, and such values become NaN.
-__device__ __forceinline__ uint2 sfar_quantize8(const uint4 &v, const SfarInv &by, bool special)
+__device__ __forceinline__ float sfar_times(float by, float x) { return by * x; }
+__device__ __forceinline__ float sfar_times(const SfarInv &by, float x) { return by(x); }
+// Eight bf16 (one 16-byte vector) as eight e4m3 of x / scale (by: the scale's
+// SfarInv, or the inverse of a power of two); `special`: some value of the
+// group is infinite or NaN, and such values become NaN.
+template <class By> __device__ __forceinline__ uint2 sfar_quantize8(const uint4 &v, const By &by, bool special)
 {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t p[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        p[i] = cvt_e4m3x2(by(bf16_lo(w[i])), by(bf16_hi(w[i])));
+        p[i] = cvt_e4m3x2(sfar_times(by, bf16_lo(w[i])), sfar_times(by, bf16_hi(w[i])));
     if (special) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

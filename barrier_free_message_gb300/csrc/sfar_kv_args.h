@@ -84,8 +84,9 @@ const void *sfar_kernel_gemm8(int tokens, int *threads, int *smem);
 // once per device: what the 8-bit projection's kernels need of it; 0 or a cudaError_t
 int sfar_fp8_prepare();
 
-#define SFAR_PLAN_THREADS 512
+#define SFAR_PLAN_THREADS 1024
 #define SFAR_PLAN_CLUSTER 8
+#define SFAR_QUANT_COLS 1024                // columns a warp of the quantisation takes of a row
 #define SFAR_APPEND_WARPS 8
 #define SFAR_ATTN_TILE 64
 #define SFAR_ATTN_CTAS(rows) ((rows) == 8 ? 3 : 2)   // per SM

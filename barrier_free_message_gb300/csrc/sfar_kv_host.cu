@@ -240,7 +240,9 @@ sfar_status sfar_kv_plan(sfar_kv_t *h, const int32_t *lens, const int32_t *delta
         return SFAR_ERR_INVALID;
     SfarKvPlanArgs a{lens,  delta, table,  ring,          state,            lens_out,    state_out, starts,
                      slots, taken, h->ctl, (int)requests, (int)table_width, (int)tokens, h->shift,  (int)h->pages};
-    return launch(h->dev, sfar_kernel_kv_plan(), dim3(SFAR_PLAN_CLUSTER), SFAR_PLAN_THREADS, (4 * requests + 1) * 4, &a, s,
+    // small steps need no more than a warp's worth of sums per scheduler
+    const unsigned threads = requests <= 256 && tokens <= 8192 ? 256 : SFAR_PLAN_THREADS;
+    return launch(h->dev, sfar_kernel_kv_plan(), dim3(SFAR_PLAN_CLUSTER), threads, (4 * requests + 1) * 4, &a, s,
                   false, SFAR_PLAN_CLUSTER);
 }
 
@@ -416,8 +418,10 @@ sfar_status sfar_quantize_fp8(sfar_t *h, const void *const x[], void *const x8[]
     a.ldx = (long long)ldx;
     a.ldx8 = (long long)ldx8;
     a.R = v.R;
-    const size_t ctas = ceil_div(m * ceil_div((size_t)a.kb, 2), 8), most = ceil_div(16 * (size_t)v.sms, (size_t)v.R);
-    return launch(v.dev, sfar_kernel_quantize(), dim3((unsigned)(ctas < most ? ctas : most), (unsigned)v.R), 256, 0, &a, s,
+    const size_t rows = ceil_div(m, 8), cols = ceil_div(k, SFAR_QUANT_COLS);
+    if (cols > 65535)
+        return SFAR_ERR_INVALID;
+    return launch(v.dev, sfar_kernel_quantize(), dim3((unsigned)rows, (unsigned)cols, (unsigned)v.R), 256, 0, &a, s,
                   v.mode == SFAR_LAUNCH_PLAIN);
 }
 
