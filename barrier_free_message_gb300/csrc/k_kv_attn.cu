@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
     const uint32_t base = (tc::smem(dyn) + 1023u) & ~1023u;
     unsigned char *mem = dyn + (base - tc::smem(dyn));
     const uint32_t ring = base, qbuf = base + kStages * L::kStage + L::kJoin;
-    float *join = reinterpret_cast<float *>(mem + kStages * L::kStage);
+    float *joint = reinterpret_cast<float *>(mem + kStages * L::kStage);
     uint32_t *upto = reinterpret_cast<uint32_t *>(mem + L::kBytes);
     const uint32_t full = tc::smem(bars), empty = full + 8 * kStages, qfull = empty + 8 * kStages, qempty = qfull + 16;
 
@@ -165,14 +165,13 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
         s_nan[0][0] = INT_MAX;
         s_nan[0][1] = -1;
     }
-    if (tid < 2 * a.R)
-        tc::prefetch_map(tid & 1 ? &a.vmap[tid >> 1] : &a.kmap[tid >> 1]);
     pdl_wait();
     const unsigned long long limit = ld_relaxed_u64(&a.ctl->timeout_ns);
 
     // prefix sums of the requests' units: row tiles x tiles
     const Work<kRows> work{upto, a};
     uint32_t carry = 0;
+    int row_tiles = 0;                             // this thread's requests'
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
         const int b = b0 + tid;
         uint32_t v = 0;
@@ -180,7 +179,9 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
             int len, count, first, begin, all;
             sfar_attn_request(a, b, len, count, first);
             work.range(len, count, begin, all);
-            v = (uint32_t)(((long long)count * a.G + kRows - 1) / kRows) * (uint32_t)all;
+            const int n = (int)(((long long)count * a.G + kRows - 1) / kRows);
+            v = (uint32_t)n * (uint32_t)all;
+            row_tiles += n;
             if (blockIdx.x == 0)
                 sfar_attn_check(a, b, len, count, first);
         }
@@ -206,8 +207,18 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
         __syncthreads();
     }
 
+    // The line is cut into as many pieces as there are CTAs, but short row tiles are left whole, or in cuts of four tiles:
+    // joining two parts costs what six tiles do (a context of 99 tokens: 8.2 us in two parts, 5.7 in one).
+    row_tiles = __reduce_add_sync(SFAR_FULL, row_tiles);
+    if (lane == 0)
+        s_warp[warp] = (uint32_t)row_tiles;
+    __syncthreads();
+    long long whole = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w)
+        whole += s_warp[w];
     const long long U = (long long)carry * a.R * a.Hk;
-    const long long N = min((long long)gridDim.x, U);
+    const long long N = min(min((long long)gridDim.x, U), max(whole * a.R * a.Hk, U / 4));
     if (blockIdx.x >= N) {
         sfar_attn_padding<D>(a, tid, kThreads);
         return;
@@ -541,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
                     s_ml[1][warp][rho] = all;
                     s_ml[2][warp][rho] = wtop[i][y];
                 }
-                float *dst = join + (warp * kRows + rho) * L::kRow + g * (D / 8);
+                float *dst = joint + (warp * kRows + rho) * L::kRow + g * (D / 8);
 #pragma unroll
                 for (int n = 0; n < D / 16; n += 2)
                     *reinterpret_cast<float4 *>(dst + 2 * n) = make_float4(o[i][n][y], o[i][n][2 + y], o[i][n + 1][y], o[i][n + 1][2 + y]);
@@ -555,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
 #pragma unroll
         for (int w = 0; w < kConsumers; ++w) {
             const float by = all.add(s_ml[0][w][row], s_ml[1][w][row], s_ml[2][w][row]);
-            const float *src = join + (w * kRows + row) * L::kRow + col;
+            const float *src = joint + (w * kRows + row) * L::kRow + col;
 #pragma unroll
             for (int e = 0; e < kE; e += 4)
                 all.add4(e, by, *reinterpret_cast<const float4 *>(src + e));
@@ -578,56 +589,72 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
         }
         bool write = true;
         if (p.tiles < p.all) {
-            // a part: leave it in the workspace; the last of the row tile's CTAs joins them in order
+            // a part: leave it in the workspace, for the last of the row tile's CTAs
             const long long from = u - (p.tile0 - p.begin), to = from + p.all;
             const int c0 = (int)sfar_div((from + 1) * N - 1, U), c1 = (int)sfar_div(to * N - 1, U);
-
-            const int mine = p.tile0 == p.begin ? 1 : 0;
-            auto slot = [&](int c, int which) { return a.part + ((size_t)c * 2 + which) * (kRows * (D + 4)); };
-            float *dst = slot(blockIdx.x, mine);
-            if (row < rows) {
+            SfarJoin join(a, 0, c0, c1, blockIdx.x);
+            auto slot = [&](int c) { return a.part + ((size_t)c * 2 + (c == c0)) * (kRows * (D + 4)); };
+            float *dst = slot(blockIdx.x);
+            for (;;) {
+                __syncwarp();                      // a row's threads have read what its first one now overwrites
+                if (row < rows) {
 #pragma unroll
-                for (int e = 0; e < kE; e += 4)
-                    __stcg(reinterpret_cast<float4 *>(dst + row * D + col + e),
-                           make_float4(all.o[e], all.o[e + 1], all.o[e + 2], all.o[e + 3]));
-                if (col == 0)
-                    __stcg(reinterpret_cast<float4 *>(dst + kRows * D + row * 4), make_float4(all.top, all.sum, all.wtop, 0.f));
-            }
-            consumers_sync();
-            if (tid == 0) {
-                __threadfence();                   // of all the CTA's writes: the barrier has ordered them before it
-                const int done = atomicAdd(a.arrived + c0, 1);
-                __threadfence();
-                s_last = done == c1 - c0;
-                if (s_last)
-                    a.arrived[c0] = 0;             // for the next call
-            }
-            consumers_sync();
-            write = s_last;
-            if (write) {
+                    for (int e = 0; e < kE; e += 4)
+                        __stcg(reinterpret_cast<float4 *>(dst + row * D + col + e),
+                               make_float4(all.o[e], all.o[e + 1], all.o[e + 2], all.o[e + 3]));
+                    if (col == 0)
+                        __stcg(reinterpret_cast<float4 *>(dst + kRows * D + row * 4), make_float4(all.top, all.sum, all.wtop, 0.f));
+                }
+                consumers_sync();
+                if (tid == 0)
+                    s_last = join.last();
+                consumers_sync();
+                write = s_last;
+                if (!write)
+                    break;
                 all = SfarAttnState<kE>();
-                const int last = row < rows ? c1 : c0 - 1;
-                // the threads of a row share the references out
-                for (int c = c0 + tid % kT; c <= last; c += kT) {
-                    const float4 m = __ldcg(reinterpret_cast<const float4 *>(slot(c, c == c0) + kRows * D + row * 4));
-                    all.reference(m.x, m.z);
+                // one pass, a batch of parts in flight (the code is as short as its loads allow: it runs once, from a
+                // cold instruction cache)
+                constexpr int kBatch = 32 / kE;
+                const int last = row < rows ? join.hi : join.lo - 1;
+#pragma unroll 1
+                for (int c = join.lo; c <= last; c += kBatch * join.step) {
+                    float4 m[kBatch], v[kBatch][kE / 4];
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        m[i] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+                        const int from = c + i * join.step;
+                        const float *src = slot(from);
+                        if (from <= last)
+                            m[i] = __ldcg(reinterpret_cast<const float4 *>(src + kRows * D + row * 4));
+#pragma unroll
+                        for (int e = 0; e < kE / 4; ++e) {
+                            v[i][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (from <= last)
+                                v[i][e] = __ldcg(reinterpret_cast<const float4 *>(src + row * D + col + 4 * e));
+                        }
+                    }
+                    SfarAttnState<kE> next;
+                    next.reference(all.top, all.wtop);
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i)
+                        next.reference(m[i].x, m[i].z);
+                    const float keep = next.add(all.top, all.sum, all.wtop);
+#pragma unroll
+                    for (int e = 0; e < kE; ++e)
+                        next.o[e] = all.o[e] * keep;
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const float by = next.add(m[i].x, m[i].y, m[i].z);
+#pragma unroll
+                        for (int e = 0; e < kE / 4; ++e)
+                            next.add4(4 * e, by, v[i][e]);
+                    }
+                    all = next;
                 }
-#pragma unroll
-                for (int d = 1; d < kT; d <<= 1)
-                    all.reference(__shfl_xor_sync(SFAR_FULL, all.top, d), __shfl_xor_sync(SFAR_FULL, all.wtop, d));
-#pragma unroll 6
-                for (int c = c0; c <= last; ++c) {
-                    const float *src = slot(c, c == c0);
-                    const float4 m = __ldcg(reinterpret_cast<const float4 *>(src + kRows * D + row * 4));
-                    float4 v[kE / 4];
-#pragma unroll
-                    for (int e = 0; e < kE; e += 4)
-                        v[e / 4] = __ldcg(reinterpret_cast<const float4 *>(src + row * D + col + e));
-                    const float by = all.add(m.x, m.y, m.z);
-#pragma unroll
-                    for (int e = 0; e < kE; e += 4)
-                        all.add4(e, by, v[e / 4]);
-                }
+                dst = slot(join.lo);
+                if (!join.next(a, 0))
+                    break;
             }
         }
         if (write && row < rows) {

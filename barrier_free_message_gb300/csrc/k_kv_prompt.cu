@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
     // prefix sums of the requests' units
     const Work work{upto, a};
     uint32_t carry = 0;
+    int row_tiles = 0;                             // of this warp's requests
     for (int r0 = 0; r0 < a.B; r0 += kThreads / 32) {
         // a warp per request
         const int b = r0 + warp;
@@ -260,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             int len, count, first;
             sfar_attn_request(a, b, len, count, first);
             const int n = work.row_tiles(count);
+            row_tiles += n;
             for (int rt = lane; rt < n; rt += 32) {
                 int begin, all;
                 work.range(len, count, rt, begin, all);
@@ -289,8 +291,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
     tc::fence_after();
     const uint32_t tmem = s_tmem;
 
+    // as in k_kv_attn.cu, short row tiles are left whole, or in cuts of no less than two row tiles' fixed cost
+    if (lane == 0)
+        s_warp[warp] = (uint32_t)row_tiles;
+    __syncthreads();
+    long long whole = 0;
+    for (int w = 0; w < kThreads / 32; ++w)
+        whole += s_warp[w];
     const long long U = (long long)carry * a.R * a.Hk;
-    const long long N = min((long long)gridDim.x, U);
+    const long long N = min(min((long long)gridDim.x, U), max(whole * a.R * a.Hk, U / (2 * kOver)));
     const long long u0 = blockIdx.x < N ? sfar_div(blockIdx.x * U, N) : 0, u1 = blockIdx.x < N ? sfar_div((blockIdx.x + 1) * U, N) : 0;
 
     if (warp < kSoft) {
@@ -528,11 +537,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                 tc::fence_after();
             }
             const bool part = p.tiles < p.all;
+            const long long from = p.at - (p.tile0 - p.begin), to = from + p.all;
+            const int c0 = part ? (int)sfar_div((from + 1) * N - 1, U) : 0, c1 = part ? (int)sfar_div(to * N - 1, U) : 0;
             // [element / 4][row] and the reference last, so that neighbouring rows are neighbours
-            auto slot = [&](long long cta, int which) {
-                return reinterpret_cast<float4 *>(a.part) + ((size_t)cta * 2 + which) * (kRows * (D / 4 + 1));
+            auto slot = [&](int cta) {
+                return reinterpret_cast<float4 *>(a.part) + ((size_t)cta * 2 + (cta == c0)) * (kRows * (D / 4 + 1)) + rho;
             };
-            float4 *dst = slot(blockIdx.x, p.tile0 == p.begin ? 1 : 0);
+            float4 *dst = slot(blockIdx.x);
             const float inv = sum == 0.f ? 0.f : 1.f / sum;         // 0: the row attends to nothing
             const int r = p.plane / a.Hk, hk = p.plane % a.Hk;
             uint16_t *out = a.out[r] + (long long)(p.first + tok) * a.ots + (long long)(hk * a.G + n - tok * a.G) * a.ohs;
@@ -568,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                     if (part) {
 #pragma unroll
                         for (int e = 0; e < 16; e += 4)
-                            __stcg(dst + (d0 + i + e) / 4 * kRows + rho, make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+                            __stcg(dst + (d0 + i + e) / 4 * kRows, make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
                     } else {
                         uint32_t b[8];
 #pragma unroll
@@ -582,65 +593,72 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                 if (lane == 0)
                     tc::bar_arrive(bar(kOEmpty + x));
                 if (part && row && half == 0)
-                    __stcg(dst + D / 4 * kRows + rho, make_float4(wtop, sum, wtop, 0.f));
+                    __stcg(dst + D / 4 * kRows, make_float4(wtop, sum, wtop, 0.f));
             }
             if (mine && part) {
-                // the last of the row tile's CTAs joins its parts in order; the two tiles of rows separately
-                const long long from = p.at - (p.tile0 - p.begin), to = from + p.all;
-                const long long c0 = sfar_div((from + 1) * N - 1, U), c1 = sfar_div(to * N - 1, U);
-                __threadfence();
-                tile_sync(x);
-                if ((tid & 255) == 0) {
-                    int *arrived = a.arrived + 2 * c0 + x;
-                    const int done = atomicAdd(arrived, 1);
-                    s_last[x] = done == (int)(c1 - c0);
-                    if (s_last[x])
-                        *arrived = 0;              // for the next call
-                }
-                tile_sync(x);
-                if (s_last[x] && row) {
-                    __threadfence();
+                // the last of the row tile's CTAs joins its parts; the two tiles of rows separately
+                SfarJoin join(a, x, c0, c1, blockIdx.x);
+                for (;;) {
+                    tile_sync(x);
+                    if ((tid & 255) == 0)
+                        s_last[x] = join.last();
+                    tile_sync(x);
+                    if (!s_last[x])
+                        break;
+                    // sums first, then the accumulator, 16 columns at a time
                     SfarAttnState<4> st;
+                    const int last = row ? join.hi : join.lo - 1;
 #pragma unroll 4
-                    for (long long cta = c0; cta <= c1; ++cta) {
-                        const float4 t = __ldcg(slot(cta, cta == c0) + D / 4 * kRows + rho);
-                        st.reference(t.x, t.z);
-                    }
-#pragma unroll 4
-                    for (long long cta = c0; cta <= c1; ++cta) {
-                        const float4 t = __ldcg(slot(cta, cta == c0) + D / 4 * kRows + rho);
-                        st.add(t.x, t.y, t.z);
+                    for (int c = join.lo; c <= last; c += join.step) {
+                        const float4 t = __ldcg(slot(c) + D / 4 * kRows);
+                        SfarAttnState<4> next;
+                        next.reference(st.top, st.wtop);
+                        next.reference(t.x, t.z);
+                        next.add(st.top, st.sum, st.wtop);
+                        next.add(t.x, t.y, t.z);
+                        st = next;
                     }
                     const float by = st.factor();
+                    const int lo_part = join.lo, step = join.step;
+                    const bool more = join.next(a, x);
+                    dst = slot(lo_part);
 #pragma unroll 1
-                    for (int i = d0; i < d0 + D / 2; i += 32) {
-                        float v[32] = {};
-#pragma unroll 1
-                        for (long long cta = c0; cta <= c1; ++cta) {
-                            const float4 *src = slot(cta, cta == c0) + rho;
+                    for (int i = d0; row && i < d0 + D / 2; i += 16) {
+                        float v[16] = {};
+#pragma unroll 2
+                        for (int c = lo_part; c <= last; c += step) {
+                            const float4 *src = slot(c);
                             const float4 t = __ldcg(src + D / 4 * kRows);
-                            float4 y[8];
+                            float4 y[4];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
+                            for (int e = 0; e < 4; ++e)
                                 y[e] = __ldcg(src + (i / 4 + e) * kRows);
                             const float w = t.z == -INFINITY ? 1.f : ex2(t.z - st.wtop);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
+                            for (int e = 0; e < 4; ++e) {
                                 v[4 * e] += w * y[e].x;
                                 v[4 * e + 1] += w * y[e].y;
                                 v[4 * e + 2] += w * y[e].z;
                                 v[4 * e + 3] += w * y[e].w;
                             }
                         }
+                        if (more) {
 #pragma unroll
-                        for (int h = 0; h < 32; h += 16) {
+                            for (int e = 0; e < 16; e += 4)
+                                __stcg(dst + (i + e) / 4 * kRows, make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+                        } else {
                             uint32_t b[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                b[e] = tc::bf16x2(v[h + 2 * e] * by, v[h + 2 * e + 1] * by);
-                            st32(out + i + h, b);
+                                b[e] = tc::bf16x2(v[2 * e] * by, v[2 * e + 1] * by);
+                            st32(out + i, b);
                         }
                     }
+                    if (!more)
+                        break;
+                    tile_sync(x);                  // both threads of a row have read the group's references
+                    if (row && half == 0)
+                        __stcg(dst + D / 4 * kRows, make_float4(st.top, st.sum, st.wtop, 0.f));
                 }
             }
             __syncwarp();

@@ -89,3 +89,49 @@ template <int E> struct SfarAttnState {
         return sum == 0.f ? 0.f : wtop == -INFINITY ? 1.f / sum : ex2(wtop - top) / sum;
     }
 };
+
+// How the parts of a row tile that lies in CTAs c0 .. c1 are joined: always in
+// the order of the CTAs, by whichever of them comes last -- of a group of
+// `radix` neighbours, which leaves its result in the place of its first, and
+// then of the groups (one CTA would read 76 parts of 16 rows for 40 us; two
+// levels of 9 take 5).  Up to 8 parts are one group.
+struct SfarJoin {
+    int c0, c1;
+    int lo, hi, step;               // parts lo, lo + step .. hi are joined next
+    int *counter;                   // of those that have come
+    __device__ __forceinline__ SfarJoin(const SfarAttnArgs &a, int kind, int first, int last, int me) : c0(first), c1(last)
+    {
+        // three sets of counters: of groups that begin a row tile, of others (their first CTA begins no other row
+        // tile's second group), of the groups of a row tile; index: the first CTA
+        int *set = a.arrived + kind * 3 * a.arrived_stride;
+        const int parts = c1 - c0 + 1;
+        lo = c0, hi = c1, step = 1, counter = set + c0;
+        if (parts > 8) {
+            const int radix = max(8, (int)ceilf(sqrtf((float)parts)));
+            lo = c0 + (me - c0) / radix * radix;
+            hi = min(lo + radix - 1, c1);
+            counter = lo == c0 ? set + a.arrived_stride + c0 : set + 2 * a.arrived_stride + lo;
+            up = radix;
+        }
+    }
+    int up = 0;                     // the groups' size, if there are groups to join after these
+    // by one thread, after the CTA's writes: whether this CTA is the last
+    __device__ __forceinline__ bool last() const
+    {
+        __threadfence();            // of all the CTA's writes: a barrier has ordered them before it
+        const bool is = atomicAdd(counter, 1) == (hi - lo) / step;
+        if (is)
+            *counter = 0;           // for the next call
+        __threadfence();
+        return is;
+    }
+    // on to the groups; false: these were all
+    __device__ __forceinline__ bool next(const SfarAttnArgs &a, int kind)
+    {
+        if (!up)
+            return false;
+        lo = c0, hi = c0 + (c1 - c0) / up * up, step = up, up = 0;
+        counter = a.arrived + kind * 3 * a.arrived_stride + c0;
+        return true;
+    }
+};

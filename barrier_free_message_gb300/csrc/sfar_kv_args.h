@@ -47,11 +47,11 @@ struct SfarAttnArgs {
     uint16_t *out[SFAR_MAX_R];
     const int *table, *lens, *starts;
     float *part;                            // partial results, two per CTA
-    int *arrived;                           // [2 * grid] parts of the row tile that began in a CTA; 0 between calls
+    int *arrived;                           // [6][arrived_stride] counters of parts (SfarJoin); 0 between calls
     SfarCtl *ctl;
     long long qts, qhs, ots, ohs;
     float scale;
-    int R, B, W, T, Hq, Hk, G, shift, pages, window;
+    int R, B, W, T, Hq, Hk, G, shift, pages, window, arrived_stride;
 };
 
 struct SfarQuantArgs {

@@ -160,7 +160,7 @@ sfar_kv_t *sfar_kv_create(int R, int q_heads, int kv_heads, int head_dim, int pa
             return fail(encode ? SFAR_ERR_INVALID : SFAR_ERR_UNSUPPORTED);
         }
     const size_t ctas = (size_t)sms * 3;                   // the most CTAs of any of the kernels
-    const size_t o_arrived = 256, o_part = (o_arrived + ctas * 8 + 255) / 256 * 256;
+    const size_t o_arrived = 256, o_part = (o_arrived + 6 * ctas * 4 + 255) / 256 * 256;
     const size_t few = (size_t)sms * 2 * 2 * 16, many = (size_t)sms * 2 * SFAR_PROMPT_ROWS;     // rows of partial results
     const size_t bytes = o_part + (few > many ? few : many) * ((size_t)head_dim + 4) * 4;
     if (cudaMalloc(&h->ws, bytes) != cudaSuccess) {
@@ -325,6 +325,7 @@ sfar_status sfar_kv_attention(sfar_kv_t *h, const void *const q[], void *const o
     a.ctl = h->ctl;
     a.part = h->part;
     a.arrived = h->arrived;
+    a.arrived_stride = 3 * h->sms;
     a.qts = (long long)q_token_stride;
     a.qhs = (long long)q_head_stride;
     a.ots = (long long)out_token_stride;

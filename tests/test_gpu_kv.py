@@ -327,6 +327,17 @@ def test_attention_long_context():
         check_attention(got, cpu, table, lens, starts, q, 0.09, ctx=str(lens))
 
 
+@pytest.mark.parametrize("R,H,G,D,P,lens,counts", [
+    (1, 1, 16, 128, 32, [60007], [1]), (1, 1, 3, 64, 16, [40000, 17], [1, 1]), (1, 2, 8, 64, 64, [9000], [40]),
+    (1, 1, 8, 128, 128, [20000, 300], [17, 2])])
+def test_attention_of_few_rows_joined_from_many_parts(R, H, G, D, P, lens, counts):
+    """One long context for a few rows: its parts are joined in groups, then the groups."""
+    cpu, table, starts, q = setup_attention(R, H, G, D, P, lens, counts, 71)
+    for _ in range(2):                                           # the counters of parts are clear again
+        got = run_attention(cpu, table, lens, starts, q, H * G, 0.1)
+        check_attention(got, cpu, table, lens, starts, q, 0.1, ctx=str(lens))
+
+
 def test_attention_strided_rows_and_padding():
     """q and out as slices of wider tensors; rows past the last request are zeros; a hint that is too small."""
     for counts, lens in (([1, 1, 1], [40, 7, 90]), ([30, 2, 41], [64, 2, 200])):
