@@ -876,6 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             tc::Ring<kHStages> hr;
             bool dead = false;
             uint32_t qphase[2] = {0, 0}, pphase[2] = {0, 0}, ofree[2] = {1, 1};
+            const uint64_t dv0 = tc::desc_n128(mem + L::oH, kTile * 128), dk0 = tc::desc_k<D>(mem + L::oK), dq0 = tc::desc_k<D>(mem + L::oQ);
             tc::Ring<kPieces> ps;
             for (;; ps.next()) {
                 dead = __any_sync(SFAR_FULL, dead || !tc::bar_wait(bar(kPiece + ps.slot), ps.phase, limit));
@@ -889,60 +890,74 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                     break;
                 const int tiles = min(kRows, p.count * a.G - p.rt * kRows) > 128 ? 2 : 1;
                 if (tc::elect_one()) {             // the same lane every time: the rings stay in its registers
-                    for (int k = 0; k <= p.tiles && !dead; ++k) {
+                    // the products of one tile of rows: W V of the step before, S of this one
+                    auto values = [&](int x, bool add) {
+                        const uint64_t dv = dv0 + hr.slot * (L::kH >> 4);
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            if (x >= tiles || dead)
-                                continue;
-                            const uint32_t tS = tmem + x * 256, tO = tS + 128;
-                            if (k > 0) {
-                                if (x == 0)
-                                    dead = !tc::bar_wait(bar(kHFull + hr.slot), hr.phase, limit);
-                                if (k == 1) {
-                                    dead = dead || !tc::bar_wait(bar(kOEmpty + x), ofree[x], limit);
-                                    ofree[x] ^= 1u;
-                                }
-                                dead = dead || !tc::bar_wait(bar(kPFull + x), pphase[x], limit);
-                                if (dead)
-                                    continue;
-                                pphase[x] ^= 1u;
-                                tc::fence_after();
-                                const uint64_t dv = tc::desc_n128(mem + L::oH + hr.slot * L::kH, kTile * 128);
+                        for (int i = 0; i < kTile / 16; ++i)
+                            tc::mma_f16_ts(tmem + x * 256 + 128, tmem + x * 256 + (i < 4 ? 8 * i : 32 + 8 * i), dv + 128 * i, idO, add || i > 0);
+                    };
+                    auto scores = [&](int x) {
+                        const uint64_t dk = dk0 + kr.slot * (L::kK >> 4), dq = dq0 + x * (2 * L::kQ >> 4);
 #pragma unroll
-                                for (int i = 0; i < kTile / 16; ++i)
-                                    tc::mma_f16_ts(tO, tS + (i < 4 ? 8 * i : 32 + 8 * i), dv + 128 * i, idO, k > 1 || i > 0);
-                                if (x == tiles - 1) {
-                                    tc::commit(bar(kHEmpty + hr.slot));
-                                    hr.next();
-                                }
-                                if (k == p.tiles)
-                                    tc::commit(bar(kOFull + x));
-                            }
-                            if (k < p.tiles) {
-                                if (k == 0) {
-                                    dead = !tc::bar_wait(bar(kQFull + x), qphase[x], limit);
-                                    qphase[x] ^= 1u;
-                                }
-                                if (x == 0)
-                                    dead = dead || !tc::bar_wait(bar(kKFull + kr.slot), kr.phase, limit);
-                                if (dead)
-                                    continue;
-                                tc::fence_after();
-                                const uint64_t dk = tc::desc_k<D>(mem + L::oK + kr.slot * L::kK);
-                                const uint64_t dq = tc::desc_k<D>(mem + L::oQ + x * 2 * L::kQ);
+                        for (int i = 0; i < D / 32; ++i)
+                            tc::mma_f8<1>(tmem + x * 256, dq + 2 * i, dk + 2 * i, idS, i > 0);
 #pragma unroll
-                                for (int i = 0; i < D / 32; ++i)
-                                    tc::mma_f8<1>(tS, dq + 2 * i, dk + 2 * i, idS, i > 0);
-#pragma unroll
-                                for (int i = 0; i < D / 32; ++i)
-                                    tc::mma_f8<1>(tS, dq + (L::kQ >> 4) + 2 * i, dk + 2 * i, idS, true);
-                                tc::commit(bar(kSFull + x));
-                                if (x == tiles - 1) {
-                                    tc::commit(bar(kKEmpty + kr.slot));
-                                    kr.next();
-                                }
-                            }
+                        for (int i = 0; i < D / 32; ++i)
+                            tc::mma_f8<1>(tmem + x * 256, dq + (L::kQ >> 4) + 2 * i, dk + 2 * i, idS, true);
+                        tc::commit(bar(kSFull + x));
+                    };
+                    auto wait = [&](int which, uint32_t &phase) {
+                        const bool in = tc::bar_wait(bar(which), phase, limit);
+                        phase ^= 1u;
+                        return in;
+                    };
+                    dead = !tc::bar_wait(bar(kKFull + kr.slot), kr.phase, limit);
+                    for (int x = 0; x < tiles && !dead; ++x) {
+                        dead = !wait(kQFull + x, qphase[x]);
+                        tc::fence_after();
+                        if (!dead)
+                            scores(x);
+                    }
+                    if (!dead) {
+                        tc::commit(bar(kKEmpty + kr.slot));
+                        kr.next();
+                    }
+                    // The loop that the tensor core waits for: as few instructions between a tile's weights and its
+                    // products as there can be.
+                    for (int k = 1; k < p.tiles && !dead; ++k) {
+                        dead = !tc::bar_wait(bar(kHFull + hr.slot), hr.phase, limit) || !tc::bar_wait(bar(kKFull + kr.slot), kr.phase, limit) ||
+                               (k == 1 && !wait(kOEmpty, ofree[0])) || !wait(kPFull, pphase[0]);
+                        if (dead)
+                            break;
+                        tc::fence_after();
+                        values(0, k > 1);
+                        scores(0);
+                        if (tiles == 2) {
+                            dead = (k == 1 && !wait(kOEmpty + 1, ofree[1])) || !wait(kPFull + 1, pphase[1]);
+                            if (dead)
+                                break;
+                            tc::fence_after();
+                            values(1, k > 1);
+                            scores(1);
                         }
+                        tc::commit(bar(kHEmpty + hr.slot));
+                        tc::commit(bar(kKEmpty + kr.slot));
+                        hr.next();
+                        kr.next();
+                    }
+                    dead = dead || !tc::bar_wait(bar(kHFull + hr.slot), hr.phase, limit);
+                    for (int x = 0; x < tiles && !dead; ++x) {
+                        dead = (p.tiles == 1 && !wait(kOEmpty + x, ofree[x])) || !wait(kPFull + x, pphase[x]);
+                        if (dead)
+                            break;
+                        tc::fence_after();
+                        values(x, p.tiles > 1);
+                        tc::commit(bar(kOFull + x));
+                    }
+                    if (!dead) {
+                        tc::commit(bar(kHEmpty + hr.slot));
+                        hr.next();
                     }
                 }
                 dead = __any_sync(SFAR_FULL, dead);

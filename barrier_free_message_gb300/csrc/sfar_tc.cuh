@@ -43,10 +43,10 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(bar), "r"(parity)
+        : "r"(bar), "r"(parity), "r"(20000u)        // ns that the hardware may hold the thread: a poll takes issue slots
         : "memory");
     return ok != 0;
 }
@@ -56,12 +56,10 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, unsigned
     if (bar_try(bar, parity))
         return true;
     const unsigned long long t0 = globaltimer();
-    for (uint32_t it = 1;; ++it) {
-        if (bar_try(bar, parity))
-            return true;
-        if ((it & 127u) == 0 && globaltimer() - t0 > limit_ns)
+    while (!bar_try(bar, parity))
+        if (globaltimer() - t0 > limit_ns)
             return false;
-    }
+    return true;
 }
 // A position in a ring of N barriers: slot and phase parity.
 template <int N> struct Ring {
