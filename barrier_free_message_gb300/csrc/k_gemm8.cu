@@ -255,13 +255,13 @@ namespace {
 // Warps 0-7: epilogue (0-3 the first 128 outputs, 4-7 the second); 8: TMA; 9:
 // MMA (of the pair's even CTA); 10 and 11: scales of either half.  A kernel of
 // three warpgroups starts with 168 registers a thread; the epilogue's two take
-// 224, the third keeps 56: the same 504 per lane of three, so no increase
+// 200, the third keeps 104: the same 504 per lane of three, so no increase
 // waits.
 struct Many {
     static constexpr int kThreads = 384;
     static constexpr int kA = 128 * 128, kB = 128 * 128, kStage = kA + kB, kStages = 6;
-    static constexpr int kScales = 8, kAhead = 4;           // ring of scales; blocks whose scales are loaded at once
-    static constexpr int kSmem = kStages * kStage + kScales * 2 * 128 * 4 + 1024;
+    static constexpr int kAhead = 4, kScales = 2;           // blocks whose scales are handed over at once; ring of those
+    static constexpr int kSmem = kStages * kStage + kScales * kAhead * 2 * 128 * 4 + 1024;
 };
 
 }  // namespace
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(Many::kThreads, 1) __cluster_dims__(2, 1, 1)
     pdl_wait();
 
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (warp == 8 && tc::elect_one()) {
             const uint64_t often = tc::evict_last();
             const uint32_t lead_full = tc::map_rank(full, 0);
@@ -392,27 +392,24 @@ __global__ void __launch_bounds__(Many::kThreads, 1) __cluster_dims__(2, 1, 1)
                         for (int i = 0; i < 4; ++i)
                             v[u][i] = m0 + 32 * i < a.m ? sx[b * a.m + 32 * i] * w : 0.f;
                     }
+                    if (!tc::bar_wait(sempty + 8 * (half * F::kScales + st.slot), st.phase ^ 1u, limit)) {
+                        gave_up = true;
+                        break;
+                    }
 #pragma unroll
-                    for (int u = 0; u < F::kAhead; ++u) {
-                        if (b0 + u >= kb || gave_up)
-                            break;
-                        if (!tc::bar_wait(sempty + 8 * (half * F::kScales + st.slot), st.phase ^ 1u, limit)) {
-                            gave_up = true;
-                            break;
-                        }
+                    for (int u = 0; u < F::kAhead; ++u)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            scl[(st.slot * 2 + half) * 128 + 32 * i + lane] = v[u][i];
-                        __syncwarp();
-                        if (lane == 0)
-                            tc::bar_arrive(sfull + 8 * (half * F::kScales + st.slot));
-                        st.next();
-                    }
+                            scl[((st.slot * F::kAhead + u) * 2 + half) * 128 + 32 * i + lane] = v[u][i];
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::bar_arrive(sfull + 8 * (half * F::kScales + st.slot));
+                    st.next();
                 }
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         tc::Ring<2> acc;
         tc::Ring<F::kScales> st;
         const int half = warp >> 2, lrow = (warp & 3) * 32 + lane;
@@ -428,37 +425,39 @@ __global__ void __launch_bounds__(Many::kThreads, 1) __cluster_dims__(2, 1, 1)
             for (int c = 0; c < 64; ++c)
                 y[c] = 0ull;
             for (int b = 0; b < kb; ++b) {
-                if (!tc::bar_wait(sfull + 8 * (half * F::kScales + st.slot), st.phase, limit) ||
+                const int u = b % F::kAhead;
+                if ((u == 0 && !tc::bar_wait(sfull + 8 * (half * F::kScales + st.slot), st.phase, limit)) ||
                     !tc::bar_wait(tfull + 8 * acc.slot, acc.phase, limit)) {
                     gave_up = true;
                     break;
                 }
                 tc::fence_after();
-                // the next columns are on their way while these are folded
+                // 32 columns at a time: what a spilled register costs is more than what a second set in flight saves
                 const uint32_t from = mine + acc.slot * 256;
-                uint32_t p[2][32];
-                tc::ld32(p[0], from);
-                const float s = scl[(st.slot * 2 + half) * 128 + lrow];
+                const float s = scl[((st.slot * F::kAhead + u) * 2 + half) * 128 + lrow];
+                const bool spent = u == F::kAhead - 1 || b == kb - 1;
                 const uint64_t ss = tc::pack2(s, s);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    tc::wait_ld(p[c & 1]);
-                    if (c < 3)
-                        tc::ld32(p[(c + 1) & 1], from + 32 * (c + 1));
-                    else {
+                    uint32_t p[32];
+                    tc::ld32(p, from + 32 * c);
+                    tc::wait_ld(p);
+                    if (c == 3) {
                         tc::fence_before();
                         __syncwarp();
                         if (lane == 0) {
                             tc::bar_arrive_remote(lead_empty + 8 * acc.slot);
-                            tc::bar_arrive(sempty + 8 * (half * F::kScales + st.slot));
+                            if (spent)
+                                tc::bar_arrive(sempty + 8 * (half * F::kScales + st.slot));
                         }
                     }
 #pragma unroll
                     for (int e = 0; e < 32; e += 2)
-                        y[16 * c + e / 2] = tc::fma2(tc::pack2u(p[c & 1][e], p[c & 1][e + 1]), ss, y[16 * c + e / 2]);
+                        y[16 * c + e / 2] = tc::fma2(tc::pack2u(p[e], p[e + 1]), ss, y[16 * c + e / 2]);
                 }
                 acc.next();
-                st.next();
+                if (spent)
+                    st.next();
             }
             if (gave_up)
                 break;
@@ -467,15 +466,14 @@ __global__ void __launch_bounds__(Many::kThreads, 1) __cluster_dims__(2, 1, 1)
                 const int cols = (int)min(128ll, a.n - nb * 128);
                 if (cols == 128 && a.vec) {
 #pragma unroll
-                    for (int c = 0; c < 128; c += 8) {
-                        uint4 v;
-                        uint32_t *w = &v.x;
+                    for (int c = 0; c < 128; c += 16) {
+                        uint32_t w[8];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
+                        for (int e = 0; e < 8; ++e) {
                             const float2 f = tc::unpack2(y[c / 2 + e]);
                             w[e] = tc::bf16x2(f.x, f.y);
                         }
-                        st_v4(dst + c, v);
+                        tc::st32(dst + c, w);
                     }
                 } else {
 #pragma unroll

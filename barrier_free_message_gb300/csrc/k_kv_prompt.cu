@@ -166,18 +166,6 @@ __device__ __forceinline__ void widen(unsigned char *to, int flip, const uint4 &
     *reinterpret_cast<uint4 *>(to) = flip ? hi : lo;
     *reinterpret_cast<uint4 *>((uintptr_t)to ^ 16) = flip ? lo : hi;
 }
-// 32 bytes of a row of the result: one store if they are aligned to it
-__device__ __forceinline__ void st32(uint16_t *p, const uint32_t (&v)[8])
-{
-    if (((uintptr_t)p & 31) == 0) {
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
-                     "r"(v[5]), "r"(v[6]), "r"(v[7])
-                     : "memory");
-    } else {
-        st_v4(p, make_uint4(v[0], v[1], v[2], v[3]));
-        st_v4(p + 8, make_uint4(v[4], v[5], v[6], v[7]));
-    }
-}
 // the largest of 16 values, NaN left out unless all are
 __device__ __forceinline__ float max16(const uint32_t *v)
 {
@@ -585,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             b[e] = tc::bf16x2(v[2 * e] * inv, v[2 * e + 1] * inv);
-                        st32(out + d0 + i, b);
+                        tc::st32(out + d0 + i, b);
                     }
                 }
                 tc::fence_before();
@@ -651,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
                                 b[e] = tc::bf16x2(v[2 * e] * by, v[2 * e + 1] * by);
-                            st32(out + i, b);
+                            tc::st32(out + i, b);
                         }
                     }
                     if (!more)

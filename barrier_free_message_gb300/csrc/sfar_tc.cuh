@@ -305,4 +305,17 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
     return r;
 }
 
+// 32 bytes to a 16-byte aligned place: one store if it is aligned to them
+__device__ __forceinline__ void st32(uint16_t *p, const uint32_t (&v)[8])
+{
+    if (((uintptr_t)p & 31) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+                     "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        st_v4(p, make_uint4(v[0], v[1], v[2], v[3]));
+        st_v4(p + 8, make_uint4(v[4], v[5], v[6], v[7]));
+    }
+}
+
 }  // namespace tc
