@@ -255,7 +255,7 @@ namespace {
 // Warps 0-7: epilogue (0-3 the first 128 outputs, 4-7 the second); 8: TMA; 9:
 // MMA (of the pair's even CTA); 10 and 11: scales of either half.  A kernel of
 // three warpgroups starts with 168 registers a thread; the epilogue's two take
-// 200, the third keeps 104: the same 504 per lane of three, so no increase
+// 192, the third keeps 120: the same 504 per lane of three, so no increase
 // waits.
 struct Many {
     static constexpr int kThreads = 384;
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(Many::kThreads, 1) __cluster_dims__(2, 1, 1)
     pdl_wait();
 
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
         if (warp == 8 && tc::elect_one()) {
             const uint64_t often = tc::evict_last();
             const uint32_t lead_full = tc::map_rank(full, 0);
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(Many::kThreads, 1) __cluster_dims__(2, 1, 1)
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         tc::Ring<2> acc;
         tc::Ring<F::kScales> st;
         const int half = warp >> 2, lrow = (warp & 3) * 32 + lane;
@@ -420,10 +420,10 @@ __global__ void __launch_bounds__(Many::kThreads, 1) __cluster_dims__(2, 1, 1)
             const int r = (int)(t / a.tiles_m / a.tiles_n);
             const long long nb = t / a.tiles_m % a.tiles_n * 2 + half;     // block of 128 outputs
             const bool row = m < a.m, col = nb * 128 < a.n;
-            uint64_t y[64];
+            float y[128];
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-                y[c] = 0ull;
+            for (int c = 0; c < 128; ++c)
+                y[c] = 0.f;
             for (int b = 0; b < kb; ++b) {
                 const int u = b % F::kAhead;
                 if ((u == 0 && !tc::bar_wait(sfull + 8 * (half * F::kScales + st.slot), st.phase, limit)) ||
@@ -436,7 +436,6 @@ __global__ void __launch_bounds__(Many::kThreads, 1) __cluster_dims__(2, 1, 1)
                 const uint32_t from = mine + acc.slot * 256;
                 const float s = scl[((st.slot * F::kAhead + u) * 2 + half) * 128 + lrow];
                 const bool spent = u == F::kAhead - 1 || b == kb - 1;
-                const uint64_t ss = tc::pack2(s, s);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t p[32];
@@ -452,8 +451,8 @@ __global__ void __launch_bounds__(Many::kThreads, 1) __cluster_dims__(2, 1, 1)
                         }
                     }
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        y[16 * c + e / 2] = tc::fma2(tc::pack2u(p[e], p[e + 1]), ss, y[16 * c + e / 2]);
+                    for (int e = 0; e < 32; ++e)
+                        y[32 * c + e] = fmaf(__uint_as_float(p[e]), s, y[32 * c + e]);
                 }
                 acc.next();
                 if (spent)
@@ -470,7 +469,7 @@ __global__ void __launch_bounds__(Many::kThreads, 1) __cluster_dims__(2, 1, 1)
                         uint32_t w[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            const float2 f = tc::unpack2(y[c / 2 + e]);
+                            const float2 f = make_float2(y[c + 2 * e], y[c + 2 * e + 1]);
                             w[e] = tc::bf16x2(f.x, f.y);
                         }
                         tc::st32(dst + c, w);
@@ -478,7 +477,7 @@ __global__ void __launch_bounds__(Many::kThreads, 1) __cluster_dims__(2, 1, 1)
                 } else {
 #pragma unroll
                     for (int c = 0; c < 128; c += 2) {
-                        const float2 f = tc::unpack2(y[c / 2]);
+                        const float2 f = make_float2(y[c], y[c + 1]);
                         const uint32_t w = tc::bf16x2(f.x, f.y);
                         if (c < cols)
                             dst[c] = (uint16_t)w;
