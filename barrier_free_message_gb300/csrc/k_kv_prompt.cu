@@ -157,14 +157,12 @@ struct Work {
 
 // 0xff for each byte that is a NaN of e4m3
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
-// Sixteen e4m3 as binary16 to two 16-byte chunks of a swizzled row (the second
-// one's place differs in bit 4); flip: the second half first.
-__device__ __forceinline__ void widen(unsigned char *to, int flip, const uint4 &v)
+// Sixteen e4m3 as binary16 to two 16-byte chunks of a swizzled row, whose places differ in bit 4.
+__device__ __forceinline__ void widen(unsigned char *to, const uint4 &v)
 {
-    const uint4 lo = make_uint4(cvt_f16x2_e4m3(v.x), cvt_f16x2_e4m3(v.x >> 16), cvt_f16x2_e4m3(v.y), cvt_f16x2_e4m3(v.y >> 16));
-    const uint4 hi = make_uint4(cvt_f16x2_e4m3(v.z), cvt_f16x2_e4m3(v.z >> 16), cvt_f16x2_e4m3(v.w), cvt_f16x2_e4m3(v.w >> 16));
-    *reinterpret_cast<uint4 *>(to) = flip ? hi : lo;
-    *reinterpret_cast<uint4 *>((uintptr_t)to ^ 16) = flip ? lo : hi;
+    *reinterpret_cast<uint4 *>(to) = make_uint4(cvt_f16x2_e4m3(v.x), cvt_f16x2_e4m3(v.x >> 16), cvt_f16x2_e4m3(v.y), cvt_f16x2_e4m3(v.y >> 16));
+    *reinterpret_cast<uint4 *>((uintptr_t)to ^ 16) =
+        make_uint4(cvt_f16x2_e4m3(v.z), cvt_f16x2_e4m3(v.z >> 16), cvt_f16x2_e4m3(v.w), cvt_f16x2_e4m3(v.w >> 16));
 }
 // the largest of 16 values, NaN left out unless all are
 __device__ __forceinline__ float max16(const uint32_t *v)
@@ -484,17 +482,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                     if (i < 3)
                         tc::ld16(s[(i + 1) & 1], tS + 16 * (i + 1));
                     uint32_t w[8];
-                    const uint64_t c2 = tc::pack2(c[i], c[i]), off = tc::pack2(lvs[i] - ref, lvs[i] - ref);
-                    uint64_t add = 0ull;
+                    const float off = lvs[i] - ref;
+                    float add0 = 0.f, add1 = 0.f;
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
-                        const float2 y = tc::unpack2(tc::fma2(tc::pack2u(s[i & 1][e], s[i & 1][e + 1]), c2, off));
-                        const float a0 = ex2(y.x), a1 = ex2(y.y);
-                        add = tc::add2(add, tc::pack2(a0, a1));
+                        const float a0 = ex2(fmaf(__uint_as_float(s[i & 1][e]), c[i], off)), a1 = ex2(fmaf(__uint_as_float(s[i & 1][e + 1]), c[i], off));
+                        add0 += a0;
+                        add1 += a1;
                         w[e / 2] = half2_of(a0, a1);
                     }
-                    const float2 y = tc::unpack2(add);
-                    sum = fmaf(y.x + y.y, ivs[i], sum);
+                    sum = fmaf(add0 + add1, ivs[i], sum);
                     tc::st8(tS + 8 * i, w);        // over scores that have been read
                 }
                 tc::wait_st();
@@ -668,13 +665,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             // this thread's 16-byte chunk c of tokens ct / kC, + 32 kWiden / kC, ...: the swizzle's bits of a token repeat
             constexpr int kC = D / 16, kSteps = kTile * kC / (32 * kWiden), kFrom = 32 * kWiden * 16, kTo = 32 * kWiden / kC * 128;
             static_assert((32 * kWiden / kC) % 8 == 0 && kSteps % 4 == 0, "a step keeps the swizzle");
-            const int tok0 = ct / kC, c = ct % kC;
+            // Eight neighbouring lanes take four chunks of two tokens: their stores meet in no bank (eight chunks of one
+            // token, as they lie, would go to four pairs of equal banks).
+            const int tok0 = D == 128 ? 2 * (ct >> 4) + (ct >> 2 & 1) : ct >> 2, c = D == 128 ? 4 * (ct >> 3 & 1) + (ct & 3) : ct & 3;
             const int from = tok0 * D + ((D == 128 ? c ^ (tok0 & 7) : c ^ ((tok0 >> 1) & 3)) << 4);
-            // 64 elements (128 bytes) of a token to a row, swizzled; the second 64 in a block of their own.  The two
-            // halves of a chunk go to chunks 2 (c & 3) and + 1; c & 4 takes them in the other order, so that 8 lanes
-            // meet in no bank.
-            const int at = 2 * (c & 3) + (c >> 2 & 1);
-            const int to = (c >> 2) * (kTile * 128) + tok0 * 128 + ((at ^ (tok0 & 7)) << 4), flip = c >> 2 & 1;
+            // 64 elements (128 bytes) of a token to a row, swizzled; the second 64 in a block of their own
+            const int to = (c >> 2) * (kTile * 128) + tok0 * 128 + (((2 * (c & 3)) ^ (tok0 & 7)) << 4);
             bool dead = false;
             uint32_t qphase = 0, ophase = 0;
             int before = 0, piece = 0;             // rows of the piece before
@@ -720,14 +716,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                                 v[b] = *reinterpret_cast<const uint4 *>(src + (n + b) * kFrom);
 #pragma unroll
                             for (int b = 0; b < 4; ++b)
-                                widen(dst + (n + b) * kTo, flip, v[b]);
+                                widen(dst + (n + b) * kTo, v[b]);
                         }
                     } else {
                         // some row does not see some token: places that hold none are zeros, and a NaN, which
                         // would reach every row, is taken out here and put back at the end
 #pragma unroll 1
                         for (int n = 0; n < kSteps; ++n) {
-                            const int tok = ct / kC + n * (32 * kWiden / kC);
+                            const int tok = tok0 + n * (32 * kWiden / kC);
                             uint4 v = *reinterpret_cast<const uint4 *>(src + n * kFrom);
                             const int g = tok >> 4;
                             if (j0 + tok >= p.len || ((odd | odd >> 16) >> g & 1))
@@ -740,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                                 atomicMin(&nan[0], j0 + tok);
                                 atomicMax(&nan[1], j0 + tok);
                             }
-                            widen(dst + n * kTo, flip, v);
+                            widen(dst + n * kTo, v);
                         }
                     }
                     if (k == p.tiles - 1) {
