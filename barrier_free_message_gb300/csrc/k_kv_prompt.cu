@@ -164,15 +164,20 @@ __device__ __forceinline__ void widen(unsigned char *to, const uint4 &v)
     *reinterpret_cast<uint4 *>((uintptr_t)to ^ 16) =
         make_uint4(cvt_f16x2_e4m3(v.z), cvt_f16x2_e4m3(v.z >> 16), cvt_f16x2_e4m3(v.w), cvt_f16x2_e4m3(v.w >> 16));
 }
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 // the largest of 16 values, NaN left out unless all are
 __device__ __forceinline__ float max16(const uint32_t *v)
 {
-    float m[4];
+    float m[5];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        m[i] = fmaxf(fmaxf(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])),
-                     fmaxf(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
-    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    for (int i = 0; i < 5; ++i)
+        m[i] = max3(__uint_as_float(v[3 * i]), __uint_as_float(v[3 * i + 1]), __uint_as_float(v[3 * i + 2]));
+    return fmaxf(max3(m[0], m[1], m[2]), max3(m[3], m[4], __uint_as_float(v[15])));
 }
 // The eight warps of a tile's softmax; the two warps that share 32 rows.
 __device__ __forceinline__ void tile_sync(int x) { asm volatile("bar.sync %0, 256;" ::"r"(1 + x) : "memory"); }
