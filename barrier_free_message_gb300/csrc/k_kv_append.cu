@@ -14,6 +14,8 @@
 // tokens when there are few (a decode step then has 8 warps per token and
 // plane group in flight), up to 32 for prompts, where only one token in a
 // page begins a run and a CTA per token would spend its time on launches.
+// Measured: 4 ranks of two heads of 128, 9 prompts of 1501 to 2139 tokens (102
+// MB) 21 us, 4.8 TB/s; 8 ranks of one head, 64 single tokens 2.7 us.
 #include "sfar_e4m3.cuh"
 #include "sfar_kv_args.h"
 #include "sfar_kv_device.cuh"

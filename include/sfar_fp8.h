@@ -33,7 +33,7 @@ extern "C" {
  * values independent of how they are computed.  Infinities and NaN do not
  * count for the scale and are stored as NaN.
  * HOST arrays of R DEVICE pointers; x 2-byte, sx 4-byte aligned; the outputs
- * overlap nothing.  bf16 handles only.  One kernel on stream s, capturable;
+ * overlap nothing.  bf16 handles only.  m below 2^31, k up to 2^26 - 1024.  One kernel on stream s, capturable;
  * SFAR_ERR_INVALID for a bad argument, SFAR_ERR_CUDA if the launch fails.
  */
 sfar_status sfar_quantize_fp8(sfar_t *h, const void *const x[], void *const x8[], float *const sx[], size_t m,

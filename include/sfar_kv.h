@@ -17,9 +17,8 @@
  *   sfar_kv_append     per layer: the new keys and values into the cache;
  *   sfar_kv_attention  per layer: the new tokens over their contexts.
  *
- * Every call enqueues one kernel on stream s (sfar_kv_attention: at most
- * two), allocates and synchronises nothing and can be captured in a CUDA
- * graph.  Arrays of requests and tokens are DEVICE memory, 4-byte aligned;
+ * Every call enqueues one kernel on stream s, allocates and synchronises
+ * nothing and can be captured in a CUDA graph.  Arrays of requests and tokens are DEVICE memory, 4-byte aligned;
  * lengths are read on the device, so a captured step replays with new ones.
  * Calls on one handle must not overlap on the GPU (sfar_kv_attention keeps
  * partial results in the handle); a handle may be used from one host thread
@@ -55,7 +54,7 @@ typedef struct sfar_kv sfar_kv_t;
  * pointers; caches 16-byte, scales 4-byte aligned, no two overlapping).
  * 1 <= R <= 16; head_dim 64 or 128; page_tokens 16, 32, 64 or 128; q_heads a
  * multiple of kv_heads; pages * page_tokens and pages * kv_heads below 2^31.
- * The handle holds a workspace of a few MB for partial results.  NULL on
+ * The handle holds a workspace for partial results, about 41 MB at head_dim 128.  NULL on
  * failure (reason: sfar_last_error).  The caches' contents are not touched.
  */
 sfar_kv_t *sfar_kv_create(int R, int q_heads, int kv_heads, int head_dim, int page_tokens, size_t pages,
@@ -122,7 +121,11 @@ sfar_status sfar_kv_append(sfar_kv_t *kv, const void *const k[], const void *con
  * tokens j <= p and, with window > 0, j > p - window.  A row that has none
  * (and a row past starts[requests]) is zeros.  The largest score and the sum
  * of the exponentials are held in binary32, as are the products' sums; the
- * result does not depend on what the other rows or masked tokens hold.
+ * result does not depend on what the other rows or masked tokens hold.  A
+ * page's scales may be any finite number, zero and negative ones included;
+ * the value scales of one request's context (those that are not zero) are
+ * within a factor of 2^100 of one another: beyond it tokens with the smaller
+ * scales lose their part of the sum of the exponentials.
  * max_q: the most new tokens any request has in this call (a hint that picks
  * the kernel; a request that has more is still computed).  out overlaps no
  * other argument.  1 <= requests <= SFAR_KV_MAX_REQUESTS; tokens, table_width
