@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
             work.range(len, count, begin, all);
             const int n = (int)(((long long)count * a.G + kRows - 1) / kRows);
             v = (uint32_t)n * (uint32_t)all;
-            row_tiles += n;
+            row_tiles = min(row_tiles + n, 1 << 26);       // above any step's; 32 such sums fit 32 bits
             if (blockIdx.x == 0)
                 sfar_attn_check(a, b, len, count, first);
         }
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w)
         whole += s_warp[w];
-    const long long U = (long long)carry * a.R * a.Hk;
+    const long long U = sfar_attn_many(a, whole) ? 0 : (long long)carry * a.R * a.Hk;
     const long long N = min(min((long long)gridDim.x, U), max(whole * a.R * a.Hk, U / 4));
     if (blockIdx.x >= N) {
         sfar_attn_padding<D>(a, tid, kThreads);

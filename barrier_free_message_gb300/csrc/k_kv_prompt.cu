@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             int len, count, first;
             sfar_attn_request(a, b, len, count, first);
             const int n = work.row_tiles(count);
-            row_tiles += n;
+            row_tiles = min(row_tiles + n, 1 << 26);       // above any step's
             for (int rt = lane; rt < n; rt += 32) {
                 int begin, all;
                 work.range(len, count, rt, begin, all);
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
     long long whole = 0;
     for (int w = 0; w < kThreads / 32; ++w)
         whole += s_warp[w];
-    const long long U = (long long)carry * a.R * a.Hk;
+    const long long U = sfar_attn_many(a, whole) ? 0 : (long long)carry * a.R * a.Hk;
     const long long N = min(min((long long)gridDim.x, U), max(whole * a.R * a.Hk, U / (2 * kOver)));
     const long long u0 = blockIdx.x < N ? sfar_div(blockIdx.x * U, N) : 0, u1 = blockIdx.x < N ? sfar_div((blockIdx.x + 1) * U, N) : 0;
 

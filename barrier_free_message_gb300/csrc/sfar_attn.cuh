@@ -47,6 +47,15 @@ __device__ __forceinline__ void sfar_attn_check(const SfarAttnArgs &a, int b, in
     if (first < 0 || a.starts[b + 1] - first != count)
         sfar_kv_fault(a.ctl, b, SFAR_KV_BAD_TOKENS);
 }
+// Offsets in no order can give the requests more row tiles together than the
+// step has (and the line more units than its 32-bit sums hold, which the host
+// bounds for a step's): nothing is computed then.
+__device__ __forceinline__ bool sfar_attn_many(const SfarAttnArgs &a, long long row_tiles)
+{
+    if (row_tiles > a.most && blockIdx.x == 0 && threadIdx.x == 0)
+        sfar_kv_fault(a.ctl, a.B, SFAR_KV_BAD_TOKENS);
+    return row_tiles > a.most;
+}
 // Zeros for the rows past the last request, by the whole grid; this thread is
 // `thread` of the `threads` that its CTA has for it (or of fewer than another's).
 template <int D> __device__ __forceinline__ void sfar_attn_padding(const SfarAttnArgs &a, int thread, int threads)

@@ -52,6 +52,7 @@ struct SfarAttnArgs {
     long long qts, qhs, ots, ohs;
     float scale;
     int R, B, W, T, Hq, Hk, G, shift, pages, window, arrived_stride;
+    int most;                               // row tiles of all requests, at most
 };
 
 struct SfarQuantArgs {

@@ -256,7 +256,8 @@ sfar_status sfar_kv_append(sfar_kv_t *h, const void *const k[], const void *cons
                            size_t v_head_stride, sfar_stream_t s)
 {
     if (!h || !k || !v || tokens >= (1ull << 31) || (tokens && !aligned(slots, 4)) || k_token_stride % 8 ||
-        k_head_stride % 8 || v_token_stride % 8 || v_head_stride % 8)
+        k_head_stride % 8 || v_token_stride % 8 || v_head_stride % 8 ||
+        (k_token_stride | k_head_stride | v_token_stride | v_head_stride) >> 40)
         return SFAR_ERR_INVALID;
     SfarKvAppendArgs a;
     memset(&a, 0, sizeof a);
@@ -302,7 +303,7 @@ sfar_status sfar_kv_attention(sfar_kv_t *h, const void *const q[], void *const o
     if (!h || !q || !out || requests == 0 || requests > SFAR_KV_MAX_REQUESTS || table_width == 0 ||
         table_width >= (1ull << 31) || tokens >= (1ull << 31) || !aligned(table, 4) || !aligned(lens, 4) ||
         !aligned(starts, 4) || q_token_stride % 8 || q_head_stride % 8 || out_token_stride % 8 || out_head_stride % 8 ||
-        !(scale >= 0.f) || isinf(scale))
+        !(scale >= 0.f) || isinf(scale) || (q_token_stride | q_head_stride | out_token_stride | out_head_stride) >> 40)
         return SFAR_ERR_INVALID;
     if (tokens == 0)
         return SFAR_OK;
@@ -346,12 +347,19 @@ sfar_status sfar_kv_attention(sfar_kv_t *h, const void *const q[], void *const o
     a.shift = h->shift;
     a.pages = (int)h->pages;
     a.window = window >= (1ull << 31) ? 0 : (int)window;
+    const bool many = max_q > kFewRows / (size_t)a.G && requests <= SFAR_PROMPT_REQUESTS;
+    const int rows = many ? SFAR_PROMPT_ROWS : max_q * (size_t)a.G <= 8 ? 8 : 16;
+    // the kernels' sums over the line of (row tile, tile) are of 32 bits, its row numbers of 31
+    const size_t most = tokens * (size_t)a.G / (size_t)rows + requests;
+    const size_t context = table_width << h->shift, reach = context < (1ull << 31) ? context : 1ull << 31;
+    if (tokens * (size_t)a.G >= 1ull << 29 || most * (ceil_div(reach, many ? 128 : SFAR_ATTN_TILE) + 8) >= 1ull << 32)
+        return SFAR_ERR_INVALID;
+    a.most = (int)most;
     int threads = 0, smem = 0;
-    if (max_q * (size_t)a.G > kFewRows && requests <= SFAR_PROMPT_REQUESTS) {
+    if (many) {
         const void *f = sfar_kernel_kv_prompt(h->D, &threads, &smem);
         return launch(h->dev, f, dim3((unsigned)h->sms), (unsigned)threads, (size_t)smem + (requests + 1) * 4, &a, s);
     }
-    const int rows = max_q * (size_t)a.G <= 8 ? 8 : 16;
     const void *f = sfar_kernel_kv_attn(h->D, rows, &threads, &smem);
     return launch(h->dev, f, dim3((unsigned)(h->sms * SFAR_ATTN_CTAS(rows))), (unsigned)threads, (size_t)smem + (requests + 1) * 4, &a, s);
 }

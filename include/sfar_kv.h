@@ -94,8 +94,8 @@ sfar_status sfar_kv_plan(sfar_kv_t *kv, const int32_t *lens, const int32_t *delt
 /*
  * sfar_kv_append: the keys and values of the step's tokens into the cache.
  * k[r], v[r]: bf16, element (token t, head h, d) at t * token_stride + h *
- * head_stride + d (strides in elements, multiples of 8; pointers 16-byte
- * aligned).  Token t goes to slots[t]; -1 leaves it out.  Tokens of one page
+ * head_stride + d (strides in elements, multiples of 8, below 2^40; pointers
+ * 16-byte aligned).  Token t goes to slots[t]; -1 leaves it out.  Tokens of one page
  * must be neighbours in t with consecutive slots (as sfar_kv_plan gives
  * them), and the page's offsets before the first of them are held tokens.
  * For each page, head and cache, with amax the largest magnitude of the new
@@ -129,7 +129,11 @@ sfar_status sfar_kv_append(sfar_kv_t *kv, const void *const k[], const void *con
  * max_q: the most new tokens any request has in this call (a hint that picks
  * the kernel; a request that has more is still computed).  out overlaps no
  * other argument.  1 <= requests <= SFAR_KV_MAX_REQUESTS; tokens, table_width
- * < 2^31; scale finite and at least 0.
+ * < 2^31; strides below 2^40; scale finite and at least 0.  The kernels count
+ * in 32 bits: with G = q_heads / kv_heads, tokens * G is below 2^29 and the
+ * product of tokens * G / n + requests (row tiles) and table_width *
+ * page_tokens / m + 8 (tiles of a context) below 2^32, where n = 256, m = 128,
+ * or n = 8, m = 64 if max_q * G is at most 32 or requests above 2048.
  */
 sfar_status sfar_kv_attention(sfar_kv_t *kv, const void *const q[], void *const out[], const int32_t *table,
                               const int32_t *lens, const int32_t *starts, size_t requests, size_t table_width,

@@ -401,6 +401,20 @@ def test_attention_reports_bad_pages_and_lengths():
         check_attention(out.cpu().double()[:, 1:], cpu, table[1:], lens[1:], [0, 1], q[:, 1:], 0.125)
 
 
+@pytest.mark.parametrize("max_q", [1, 512])
+def test_attention_refuses_offsets_in_no_order(max_q):
+    """Offsets that run back and forth give the requests more rows together than the step has: recorded, nothing written."""
+    T, B = 512, 9
+    cpu, table, _, q = setup_attention(1, 1, 8, 64, 64, [600] * B, [57] * 8 + [56], 53)
+    assert q.shape[1] == T
+    kv = sfar.SfarKv(*[t.cuda() for t in cpu], q_heads=8)
+    out = torch.full_like(q, 7.0).cuda()
+    args = [cuda_int(table), cuda_int([600] * B), cuda_int([0, T] * 5)]
+    kv.attention(q.cuda(), out, *args, max_q=max_q, scale=0.125)
+    ok(kv, sfar_where("tokens"))
+    assert (out == 7.0).all()
+
+
 def test_attention_side_stream_and_graph():
     """On a stream of its own, captured; replays follow lengths and caches that change between them."""
     R, H, G, D, P = 2, 1, 8, 128, 64
@@ -555,6 +569,10 @@ def test_calls_refuse_bad_arguments():
         assert L.sfar_kv_attention(kv.h, x, o, a, a, a, *args, 256, 64, 256, 64, 1, 1.0, 0, None) == bad
     for scale in (-1.0, float("inf"), float("nan")):
         assert L.sfar_kv_attention(kv.h, x, o, a, a, a, 1, 1, 4, 256, 64, 256, 64, 1, scale, 0, None) == bad
+    for width, tokens, strides, max_q in ((1, 1 << 28, 0, 1), (1, 1 << 28, 0, 64), (1 << 30, 1 << 20, 0, 1), (1 << 30, 1 << 27, 0, 64),
+                                          (1, 4, 1 << 40, 1)):           # more than the kernels' sums hold
+        assert L.sfar_kv_attention(kv.h, x, o, a, a, a, 1, width, tokens, *[strides] * 4, max_q, 1.0, 0, None) == bad, (width, tokens)
+    assert L.sfar_kv_append(kv.h, x, x, a, 4, 1 << 40, 64, 256, 64, None) == bad
     assert L.sfar_kv_attention(kv.h, x, x, a, a, a, 1, 1, 4, 256, 64, 256, 64, 1, 1.0, 0, None) == bad
     assert L.sfar_kv_attention(kv.h, x, o, a, a, a, 1, 1, 4, 256, 60, 256, 64, 1, 1.0, 0, None) == bad
     assert L.sfar_kv_attention(kv.h, x, o, a, a, a, 1, 1, 0, 256, 64, 256, 64, 1, 1.0, 0, None) == 0
