@@ -1,14 +1,21 @@
 """Build libsfar.so in-tree with nvcc for sm_103a.
 
 Each .cu file is compiled on its own (in parallel) and the objects are linked
-into ``barrier_free_message_gb300/_build/libsfar.so``.  A stamp of the
-sources and flags skips the build when nothing changed.
+into ``barrier_free_message_gb300/_build/libsfar.so``.  Beside it the host
+compiler builds ``sfar_tensors.so``, the Python module that reads the torch
+tensors of the paged cache's and the 8-bit projection's calls.  A stamp of the
+sources, flags and torch's and Python's versions skips the build when nothing
+changed.
 """
 import concurrent.futures as cf
 import hashlib
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -16,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libsfar.so")
+TENSORS = os.path.join(OUT_DIR, "sfar_tensors.so")
 
 SOURCES = ["sfar_host.cu", "k_ll.cu", "k_ll128.cu", "k_sentinel.cu", "k_db.cu", "k_twoshot.cu", "k_twoshot_sent.cu", "k_tma.cu",
            "k_atomic.cu", "k_fused.cu", "k_fused8.cu", "k_fused_ts.cu", "k_gemv.cu",
@@ -35,6 +43,7 @@ def nvcc() -> str:
 def _stamp() -> str:
     h = hashlib.sha256()
     h.update(" ".join(NVCC_FLAGS).encode())
+    h.update(f"{importlib.metadata.version('torch')} {sys.version}".encode())
     for d in (CSRC, INCLUDE):
         for name in sorted(os.listdir(d)):
             with open(os.path.join(d, name), "rb") as f:
@@ -43,11 +52,26 @@ def _stamp() -> str:
     return h.hexdigest()
 
 
+def _build_tensors(cc: str) -> None:
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    libs = os.path.join(torch, "lib")
+    inc = [INCLUDE, os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include")]
+    tmp = TENSORS + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           os.path.join(CSRC, "sfar_tensors.cpp"), "-o", tmp, *["-I" + i for i in inc], "-L" + libs, "-Wl,-rpath," + libs,
+           "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on sfar_tensors.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TENSORS)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     stamp_file = os.path.join(OUT_DIR, "stamp")
     stamp = _stamp()
-    if not force and os.path.exists(LIB) and os.path.exists(stamp_file):
+    if not force and os.path.exists(LIB) and os.path.exists(TENSORS) and os.path.exists(stamp_file):
         with open(stamp_file) as f:
             if f.read() == stamp:
                 return LIB
@@ -63,8 +87,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
+        tensors = ex.submit(_build_tensors, cc)
         results = list(ex.map(compile_one, SOURCES))
+        tensors.result()
     if verbose:
         for _, log in results:
             print(log)

@@ -9,6 +9,8 @@ torch stream).  The library must have been built (``_build.build()``);
 loading it otherwise raises, and there is no CPU fallback.
 """
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 from . import _build
@@ -149,70 +151,24 @@ def _ptr_array(ptrs):
     return (ctypes.c_void_p * len(ptrs))(*[int(p) for p in ptrs])
 
 
-_types = None
+_native = None
 
 
-def _torch_types():
-    """(bf16, fp32, int32, types of a byte), once torch is loaded."""
-    global _types
-    if _types is None:
-        import torch
-        _types = ((torch.bfloat16,), (torch.float32,), torch.int32, (torch.float8_e4m3fn, torch.uint8))
-    return _types
-
-
-_forms = {}
-
-
-def _form(dtype, shape, stride, cuda, ndim, dtypes, what):
-    """Checks one rank's shape and strides; returns them, the stride of a dimension of one entry as 0, whatever
-    torch keeps there, and whether they are a contiguous tensor's."""
-    if len(shape) != ndim or dtype not in dtypes:
-        raise ValueError(f"{what}: need {ndim} dimensions of {' or '.join(map(str, dtypes))} per rank")
-    if stride[-1] != 1 and shape[-1] > 1:
-        raise ValueError(f"{what}: the last dimension must be contiguous")
-    if not cuda:
-        raise ValueError(f"{what}: must be on the GPU")
-    n, dense = 1, True
-    for size, st in zip(reversed(shape), reversed(stride)):
-        dense = dense and (size <= 1 or st == n)
-        n *= size
-    return shape, tuple(st if n > 1 else 0 for n, st in zip(shape, stride)), dense
-
-
-def _ranks(x, R, ndim, dtypes, what):
-    """(array of a pointer per rank, shape, strides, contiguous) of R tensors on the GPU, given as a list or as one
-    tensor [R, ...] whose slices they are: the same shape, strides and type, unit stride along the last dimension."""
-    if isinstance(x, (list, tuple)):
-        if len(x) != R:
-            raise ValueError(f"{what}: need {R} tensors, one per rank")
-        t = x[0]
-        dtype, shape, stride = t.dtype, t.shape, t.stride()
-        for o in x:
-            if o.shape != shape or o.stride() != stride or o.dtype != dtype:
-                raise ValueError(f"{what}: the ranks' tensors differ in shape, strides or type")
-        ptrs = (ctypes.c_void_p * R)(*[o.data_ptr() for o in x])
-        return (ptrs, *_form(dtype, tuple(shape), stride, all(o.is_cuda for o in x), ndim, dtypes, what))
-    # what a shape and its strides come to is worked out once
-    key = (what, R, ndim, x.dtype, x.shape, x.stride(), x.is_cuda)
-    form = _forms.get(key)
-    if form is None:
-        shape, stride = tuple(x.shape), x.stride()
-        if len(shape) == 0 or shape[0] != R:
-            raise ValueError(f"{what}: need [{R}, ...], a slice per rank")
-        if len(_forms) >= 4096:
-            _forms.clear()
-        form = _forms[key] = (ctypes.c_void_p * R, stride[0] * x.element_size(),
-                              *_form(x.dtype, shape[1:], stride[1:], x.is_cuda, ndim, dtypes, what))
-    array, step, shape, stride, dense = form
-    base = x.data_ptr()
-    return array(*range(base, base + R * step, step)) if step else array(*[base] * R), shape, stride, dense
-
-
-def _int32(t, shape, what):
-    if t.dtype is not _torch_types()[2] or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{what}: need a contiguous int32 tensor of shape {list(shape)} on the GPU")
-    return t.data_ptr()
+def _tensors():
+    """The module that reads the tensors of a call and makes it (raises if it has not been built)."""
+    global _native
+    if _native is None:
+        import torch  # noqa: F401  (the libraries the module is linked with)
+        L = lib()
+        if not os.path.exists(_build.TENSORS):
+            raise RuntimeError(f"libsfar is not built ({_build.TENSORS} missing); run barrier_free_message_gb300._build.build()")
+        loader = importlib.machinery.ExtensionFileLoader("sfar_tensors", _build.TENSORS)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("sfar_tensors", loader))
+        loader.exec_module(module)
+        module.bind(*[ctypes.cast(getattr(L, n), ctypes.c_void_p).value
+                      for n in ("sfar_kv_plan", "sfar_kv_append", "sfar_kv_attention", "sfar_quantize_fp8", "sfar_rowpar_gemm_fp8")])
+        _native = module
+    return _native
 
 
 def _check(code, what):
@@ -398,38 +354,17 @@ class Sfar:
     def quantize_fp8(self, x, x8, sx, stream=None) -> None:
         """x: [m, k] bf16 per rank -> x8: [m, k] e4m3 and sx: [ceil(k / 128), m] fp32 per rank (lists of R
         tensors, or one tensor [R, ...] each; rows of x and x8 may be strided)."""
-        bf16, fp32, _, byte = _torch_types()
-        R = self.R
-        px, shape, st, _ = _ranks(x, R, 2, bf16, "x")
-        po, oshape, ost, _ = _ranks(x8, R, 2, byte, "x8")
-        ps, sshape, _, dense = _ranks(sx, R, 2, fp32, "sx")
-        m, k = shape
-        if oshape != shape or sshape != ((k + 127) // 128, m) or not dense:
-            raise ValueError("quantize_fp8: x8 must be [m, k], sx a contiguous [ceil(k / 128), m]")
-        up = (k + 15) // 16 * 16
-        _check(lib().sfar_quantize_fp8(self.h, px, po, ps, m, k, st[0] or up, ost[0] or up, _stream(stream)),
-               "sfar_quantize_fp8")
+        code = (_native or _tensors()).quantize_fp8(self.h, self.R, x, x8, sx, stream)
+        if code:
+            _check(code, "sfar_quantize_fp8")
 
     def rowpar_gemm_fp8(self, x8, sx, w8, sw, y, stream=None) -> None:
         """x8 [m, k], sx [ceil(k / 128), m] (as quantize_fp8 gives them), w8 [hidden, k] e4m3 and sw
         [ceil(hidden / 128), ceil(k / 128)] fp32 -> y [m, hidden] bf16, per rank (lists of R tensors, or one
         tensor [R, ...] each; rows of x8 and w8 may be strided by multiples of 16)."""
-        bf16, fp32, _, byte = _torch_types()
-        R = self.R
-        px, xs, xst, _ = _ranks(x8, R, 2, byte, "x8")
-        pw, ws, wst, _ = _ranks(w8, R, 2, byte, "w8")
-        py, ys, _, dense_y = _ranks(y, R, 2, bf16, "y")
-        pc, cs, _, dense_c = _ranks(sx, R, 2, fp32, "sx")
-        pd, ds, _, dense_d = _ranks(sw, R, 2, fp32, "sw")
-        m, k = xs
-        n, kb = ws[0], (k + 127) // 128
-        if ws[1] != k or ys != (m, n) or cs != (kb, m) or ds != ((n + 127) // 128, kb) or \
-                not (dense_y and dense_c and dense_d):
-            raise ValueError("rowpar_gemm_fp8: need x8 [m, k], w8 [hidden, k], contiguous sx [ceil(k / 128), m], "
-                             "sw [ceil(hidden / 128), ceil(k / 128)] and y [m, hidden]")
-        up = (k + 15) // 16 * 16
-        _check(lib().sfar_rowpar_gemm_fp8(self.h, px, pc, pw, pd, py, m, k, n, xst[0] or up, wst[0] or up,
-                                          _stream(stream)), "sfar_rowpar_gemm_fp8")
+        code = (_native or _tensors()).rowpar_gemm_fp8(self.h, self.R, x8, sx, w8, sw, y, stream)
+        if code:
+            _check(code, "sfar_rowpar_gemm_fp8")
 
     def status(self):
         return sfar_status_get(self.h)
@@ -466,12 +401,11 @@ class SfarKv:
 
     def __init__(self, k_cache, v_cache, k_scale, v_scale, q_heads: int):
         self.h = None
-        _, fp32, _, byte = _torch_types()
-        R = len(k_cache)
-        pk, k, _, dense_k = _ranks(k_cache, R, 4, byte, "k_cache")
-        pv, v, _, dense_v = _ranks(v_cache, R, 4, byte, "v_cache")
-        pks, ks, _, dense_ks = _ranks(k_scale, R, 2, fp32, "k_scale")
-        pvs, vs, _, dense_vs = _ranks(v_scale, R, 2, fp32, "v_scale")
+        native, R = _tensors(), len(k_cache)
+        pk, k, dense_k = native.ranks(k_cache, R, 4, "byte", "k_cache")
+        pv, v, dense_v = native.ranks(v_cache, R, 4, "byte", "v_cache")
+        pks, ks, dense_ks = native.ranks(k_scale, R, 2, "fp32", "k_scale")
+        pvs, vs, dense_vs = native.ranks(v_scale, R, 2, "fp32", "v_scale")
         if v != k or ks != k[:2] or vs != k[:2] or \
                 not (dense_k and dense_v and dense_ks and dense_vs):
             raise ValueError("SfarKv: need contiguous caches [pages, kv_heads, page_tokens, head_dim] and scales "
@@ -479,7 +413,8 @@ class SfarKv:
         self.R, self.q_heads = R, q_heads
         self.pages, self.kv_heads, self.page_tokens, self.head_dim = k
         self.tensors = (k_cache, v_cache, k_scale, v_scale)
-        h = lib().sfar_kv_create(R, q_heads, self.kv_heads, self.head_dim, self.page_tokens, self.pages, pk, pv, pks, pvs)
+        h = lib().sfar_kv_create(R, q_heads, self.kv_heads, self.head_dim, self.page_tokens, self.pages,
+                                 *[_ptr_array(p) for p in (pk, pv, pks, pvs)])
         if not h:
             raise SfarError(lib().sfar_last_error(), "sfar_kv_create")
         self.h = h
@@ -488,40 +423,26 @@ class SfarKv:
         """Pages, slots and offsets of a step from the requests' lengths; every tensor int32.  lens, delta,
         lens_out, taken: [requests]; table: [requests, width]; ring: [pages]; state, state_out: [2]; starts:
         [requests + 1]; slots: [tokens].  lens_out may be lens, state_out may be state."""
-        B = lens.shape[0]
-        W, T = table.shape[1], slots.shape[0]
-        code = lib().sfar_kv_plan(self.h, _int32(lens, (B,), "lens"), _int32(delta, (B,), "delta"),
-                                  _int32(table, (B, W), "table"), _int32(ring, (self.pages,), "ring"),
-                                  _int32(state, (2,), "state"), _int32(lens_out, (B,), "lens_out"),
-                                  _int32(state_out, (2,), "state_out"), _int32(starts, (B + 1,), "starts"),
-                                  _int32(slots, (T,), "slots"), _int32(taken, (B,), "taken"), B, W, T, _stream(stream))
-        _check(code, "sfar_kv_plan")
+        code = (_native or _tensors()).plan(self.h, self.pages, lens, delta, table, ring, state, lens_out, state_out, starts, slots,
+                                            taken, stream)
+        if code:
+            _check(code, "sfar_kv_plan")
 
     def append(self, k, v, slots, stream=None) -> None:
         """k, v: [tokens, kv_heads, head_dim] bf16 per rank (token and head strides multiples of 8); slots: [tokens]."""
-        bf16 = _torch_types()[0]
-        pk, ks, kst, _ = _ranks(k, self.R, 3, bf16, "k")
-        pv, vs, vst, _ = _ranks(v, self.R, 3, bf16, "v")
-        T = slots.shape[0]
-        if ks != (T, self.kv_heads, self.head_dim) or vs != ks:
-            raise ValueError(f"append: need k and v of shape {[T, self.kv_heads, self.head_dim]} per rank")
-        _check(lib().sfar_kv_append(self.h, pk, pv, _int32(slots, (T,), "slots"), T, kst[0], kst[1], vst[0], vst[1],
-                                    _stream(stream)), "sfar_kv_append")
+        code = (_native or _tensors()).append(self.h, self.R, self.kv_heads, self.head_dim, k, v, slots, stream)
+        if code:
+            _check(code, "sfar_kv_append")
 
     def attention(self, q, out, table, lens, starts, max_q: int, scale=None, window: int = 0, stream=None) -> None:
         """q, out: [tokens, q_heads, head_dim] bf16 per rank (token and head strides multiples of 8); table:
         [requests, width], lens: [requests], starts: [requests + 1].  scale: 1 / sqrt(head_dim) if None."""
-        bf16 = _torch_types()[0]
-        pq, qs, qst, _ = _ranks(q, self.R, 3, bf16, "q")
-        po, os_, ost, _ = _ranks(out, self.R, 3, bf16, "out")
-        if qs[1:] != (self.q_heads, self.head_dim) or os_ != qs:
-            raise ValueError(f"attention: need q and out of shape [tokens, {self.q_heads}, {self.head_dim}] per rank")
-        B, W = table.shape
         if scale is None:
             scale = self.head_dim ** -0.5
-        _check(lib().sfar_kv_attention(self.h, pq, po, _int32(table, (B, W), "table"), _int32(lens, (B,), "lens"),
-                                       _int32(starts, (B + 1,), "starts"), B, W, qs[0], qst[0], qst[1], ost[0], ost[1],
-                                       max_q, scale, window, _stream(stream)), "sfar_kv_attention")
+        code = (_native or _tensors()).attention(self.h, self.R, self.q_heads, self.head_dim, q, out, table, lens, starts, max_q, scale,
+                                                 window, stream)
+        if code:
+            _check(code, "sfar_kv_attention")
 
     def status(self):
         f = SfarFault()

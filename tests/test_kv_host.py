@@ -76,6 +76,25 @@ def test_python_layer_refuses_wrong_tensors():
             sfar.SfarKv(*args, q_heads=4)
 
 
+def test_calls_refuse_wrong_tensors():
+    """What the module that reads the tensors refuses before it makes the call (a closed handle would be next)."""
+    native = sfar._tensors()
+    i = torch.zeros(4, dtype=torch.int32)
+    bf, f8, f32 = torch.zeros(2, 4, 2, 64, dtype=torch.bfloat16), torch.zeros(2, 4, 64, dtype=torch.uint8), torch.zeros(2, 1, 4)
+    for args in (([bf[0]], 2, 3, "bf16"), (bf, 3, 3, "bf16"), (bf, 2, 2, "bf16"), (bf.float(), 2, 3, "bf16"), (f8, 2, 2, "fp32"),
+                 (bf, 17, 3, "bf16"), ((bf[0], bf[1, :3]), 2, 3, "bf16"), ([1, 2], 2, 3, "bf16"), (None, 2, 3, "bf16"),
+                 (bf, 2, 3, "bf16"), (f8, 2, 2, "byte"), ([f32[0], f32[1]], 2, 2, "fp32")):          # the last three: on the CPU
+        with pytest.raises(ValueError):
+            native.ranks(*args, "x")
+    for call, args in ((native.plan, (4, i, i, i.view(2, 2), i, i[:2], i, i[:2], i, i, i, 0)), (native.plan, (4, *[1] * 10, 0)),
+                       (native.append, (2, 2, 64, bf, bf, i, 0)), (native.attention, (2, 2, 64, bf, bf, i.view(2, 2), i, i, 1, 1.0, 0, 0)),
+                       (native.quantize_fp8, (2, bf[:, :, 0], f8, f32, 0)), (native.rowpar_gemm_fp8, (2, f8, f32, f8, f32, bf[:, :, 0], 0))):
+        with pytest.raises(ValueError):
+            call(None, *args)
+        with pytest.raises(TypeError):
+            call(None, *args[1:])
+
+
 def test_reference_rounds_as_the_format_does():
     """Every bf16 value of magnitude up to 448 against torch's conversion to e4m3."""
     x = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
