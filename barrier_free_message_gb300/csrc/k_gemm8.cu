@@ -71,6 +71,8 @@ __global__ void __launch_bounds__(Few<NT>::kThreads, 1) k_gemm8_few(const __grid
     float *scl = reinterpret_cast<float *>(dyn + (ring - tc::smem(dyn)) + F::kStages * F::kStage);
     const uint32_t full = tc::smem(bars), empty = full + 8 * F::kStages, tfull = empty + 8 * F::kStages, tempty = tfull + 16,
                    sfull = tempty + 16, sempty = sfull + 8 * F::kScales, drain = sempty + 8 * F::kScales;
+    if (warp == 4 && lane < 2 * a.R)
+        tc::prefetch_map(lane & 1 ? &a.xmap[lane >> 1] : &a.wmap[lane >> 1]);
     if (threadIdx.x == 0) {
         for (int s = 0; s < F::kStages; ++s) {
             tc::bar_init(full + 8 * s, 1);
@@ -286,6 +288,8 @@ __global__ void __launch_bounds__(Many::kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t full = tc::smem(bars), empty = full + 8 * F::kStages, tfull = empty + 8 * F::kStages, tempty = tfull + 16, drain = tempty + 16,
                    sfull = drain + 8, sempty = sfull + 16 * F::kScales;
     float *scl = reinterpret_cast<float *>(dyn + (ring - tc::smem(dyn)) + F::kStages * F::kStage);
+    if (warp == 8 && lane < 2 * a.R)
+        tc::prefetch_map(lane & 1 ? &a.xmap[lane >> 1] : &a.wmap[lane >> 1]);
     if (threadIdx.x == 0) {
         for (int s = 0; s < F::kStages; ++s) {
             tc::bar_init(full + 8 * s, 2);              // the two producers

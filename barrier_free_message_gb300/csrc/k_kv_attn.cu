@@ -163,6 +163,8 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
     uint32_t *upto = reinterpret_cast<uint32_t *>(mem + L::kBytes);
     const uint32_t full = tc::smem(bars), empty = full + 8 * kStages, qfull = empty + 8 * kStages, qempty = qfull + 16;
 
+    if (warp == kConsumers && lane < 2 * a.R)
+        tc::prefetch_map(lane & 1 ? &a.vmap[lane >> 1] : &a.kmap[lane >> 1]);
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             tc::bar_init(full + 8 * s, 1);

@@ -232,6 +232,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
     const uint32_t b0 = tc::smem(bars);
     auto bar = [&](int i) { return b0 + 8u * (uint32_t)i; };
 
+    if (warp == kCopyWarp && lane < 2 * a.R)
+        tc::prefetch_map(lane & 1 ? &a.vmap[lane >> 1] : &a.kmap[lane >> 1]);
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i) {
             const bool widen = (i >= kVEmpty && i < kVEmpty + kVStages) || (i >= kHFull && i < kHFull + kHStages);

@@ -39,8 +39,8 @@ struct SfarKvAppendArgs {
 struct SfarAttnArgs {
     // caches of every rank as 3-D tensor maps: head_dim bytes (innermost) by
     // page_tokens by pages * kv_heads, a box of up to SFAR_ATTN_TILE tokens
-    alignas(64) CUtensorMap kmap[SFAR_MAX_R];
-    alignas(64) CUtensorMap vmap[SFAR_MAX_R];
+    CUtensorMap kmap[SFAR_MAX_R];
+    CUtensorMap vmap[SFAR_MAX_R];
     const uint8_t *v[SFAR_MAX_R];           // the value caches
     const float *ks[SFAR_MAX_R], *vs[SFAR_MAX_R];
     const uint16_t *q[SFAR_MAX_R];
@@ -67,8 +67,8 @@ struct SfarGemm8Args {
     // x8 and w8 of every rank as 2-D tensor maps: k bytes (innermost) by rows,
     // boxes of 128 bytes x the tile's tokens (x) or 128 rows (w), 128-byte
     // swizzle, zeros outside
-    alignas(64) CUtensorMap xmap[SFAR_MAX_R];
-    alignas(64) CUtensorMap wmap[SFAR_MAX_R];
+    CUtensorMap xmap[SFAR_MAX_R];
+    CUtensorMap wmap[SFAR_MAX_R];
     const float *sx[SFAR_MAX_R], *sw[SFAR_MAX_R];
     uint16_t *y[SFAR_MAX_R];
     SfarCtl *ctl;
