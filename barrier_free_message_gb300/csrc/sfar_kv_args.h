@@ -77,7 +77,8 @@ struct SfarGemm8Args {
 };
 
 const void *sfar_kernel_kv_plan();
-const void *sfar_kernel_kv_append(int head_dim);
+// few: for a decode step; *team: warps to a run
+const void *sfar_kernel_kv_append(int head_dim, int page_tokens, int few, int *team);
 const void *sfar_kernel_kv_attn(int head_dim, int rows, int *threads, int *smem);
 const void *sfar_kernel_kv_prompt(int head_dim, int *threads, int *smem);
 const void *sfar_kernel_quantize();

@@ -284,15 +284,19 @@ sfar_status sfar_kv_append(sfar_kv_t *h, const void *const k[], const void *cons
     a.R = h->R;
     a.shift = h->shift;
     a.pages = (int)h->pages;
-    // tokens per CTA: one while the grid is below four CTAs per SM, doubling from there
-    const size_t groups = ceil_div(2 * (size_t)h->R * (size_t)h->Hk, SFAR_APPEND_WARPS);
+    // One token per CTA while that gives no more CTAs than eight per SM (few), then up to 32, doubling while there are
+    // more than four per SM.
+    const size_t planes = 2 * (size_t)h->R * (size_t)h->Hk;
+    const bool few = tokens * ceil_div(planes, SFAR_APPEND_WARPS) <= 8 * (size_t)h->sms;
+    int team = 1;
+    const void *f = sfar_kernel_kv_append(h->D, 1 << h->shift, few, &team);
+    const size_t groups = ceil_div(planes * (size_t)team, SFAR_APPEND_WARPS);
     a.window = 1;
-    while (a.window < 32 && ceil_div(tokens, (size_t)a.window) * groups > 4 * (size_t)h->sms)
+    while (!few && a.window < 32 && ceil_div(tokens, (size_t)a.window) * groups > 4 * (size_t)h->sms)
         a.window *= 2;
     if (groups > 65535)
         return SFAR_ERR_INVALID;
-    return launch(h->dev, sfar_kernel_kv_append(h->D), dim3((unsigned)ceil_div(tokens, (size_t)a.window), (unsigned)groups),
-                  32 * SFAR_APPEND_WARPS, 0, &a, s);
+    return launch(h->dev, f, dim3((unsigned)ceil_div(tokens, (size_t)a.window), (unsigned)groups), 32 * SFAR_APPEND_WARPS, 0, &a, s);
 }
 
 sfar_status sfar_kv_attention(sfar_kv_t *h, const void *const q[], void *const out[], const int32_t *table,

@@ -175,6 +175,38 @@ def test_append(R, H, D, P, runs, wide):
     check_append(cpu, dev, x, slots)
 
 
+@pytest.mark.parametrize("P", [16, 32, 64, 128])
+@pytest.mark.parametrize("D", [64, 128])
+def test_append_many_tokens(D, P):
+    """Whole pages, their parts and single tokens, enough of them that windows of many tokens are taken; zeros, infinities
+    and NaN among them, growth of held pages, slots outside the pool."""
+    R, H = 4, 3
+    g = torch.Generator().manual_seed(D + P)
+    runs = [(0, P), (0, P), (P - 1, 1), (1, P - 1), (0, P // 2 + 1), (P // 2, P // 2), (0, 1)]
+    while sum(n for _, n in runs) < 650:
+        first = int(torch.randint(0, P, (1,), generator=g))
+        runs.append((first, int(torch.randint(1, P - first + 1, (1,), generator=g))))
+    cpu, dev, kv = fresh(R=R, H=H, D=D, P=P, pages=len(runs) + 2, q_heads=H, seed=P)
+    pages = torch.randperm(len(runs) + 2, generator=g).tolist()
+    slots = []
+    for i, (p, (first, n)) in enumerate(zip(pages, runs)):
+        slots += [p * P + first + j for j in range(n)] + ([-1] * (i % 4) if i % 3 == 1 else [])
+    x = token_rows(g, R, len(slots), H, D, True)
+    for t in x:
+        t[:, P + 3] = 0.0
+        t[1, 2 * P - 1, 0, 5] = float("nan")
+        t[2, 5, 1] = float("inf")
+        t[0, :P, 2] = 0.0
+        t[3, -1, 0, 0] = -3.3e38
+    kv.append(x[0].cuda(), x[1].cuda(), cuda_int(slots))
+    ok(kv)
+    check_append(cpu, dev, x, slots)
+    before, bad = [t.cpu() for t in dev], [-1 if i % 5 else len(cpu[0][0]) * P + i for i in range(len(slots))]
+    kv.append(x[0].cuda(), x[1].cuda(), cuda_int(bad))
+    ok(kv, sfar_where("slot"))
+    check_append(before, dev, x, [-1] * len(slots))
+
+
 def test_append_strided_slices_and_lists():
     """k and v as views into one tensor on the device; ranks as a list of tensors."""
     g = torch.Generator().manual_seed(3)
