@@ -474,26 +474,21 @@ __global__ void __launch_bounds__(Many::kThreads, 1) __cluster_dims__(2, 1, 1)
             if (row && col) {
                 uint16_t *dst = a.y[r] + m * a.n + nb * 128;
                 const int cols = (int)min(128ll, a.n - nb * 128);
-                if (cols == 128 && a.vec) {
 #pragma unroll
-                    for (int c = 0; c < 128; c += 16) {
-                        uint32_t w[8];
+                for (int c = 0; c < 128; c += 16) {
+                    uint32_t w[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float2 f = make_float2(y[c + 2 * e], y[c + 2 * e + 1]);
-                            w[e] = tc::bf16x2(f.x, f.y);
-                        }
+                    for (int e = 0; e < 8; ++e)
+                        w[e] = tc::bf16x2(y[c + 2 * e], y[c + 2 * e + 1]);
+                    if (a.vec && c + 16 <= cols) {
                         tc::st32(dst + c, w);
-                    }
-                } else {
+                    } else if (a.vec && c < cols) {          // 8 outputs: their number is a multiple of 8
+                        st_v4(dst + c, make_uint4(w[0], w[1], w[2], w[3]));
+                    } else {
 #pragma unroll
-                    for (int c = 0; c < 128; c += 2) {
-                        const float2 f = make_float2(y[c], y[c + 1]);
-                        const uint32_t w = tc::bf16x2(f.x, f.y);
-                        if (c < cols)
-                            dst[c] = (uint16_t)w;
-                        if (c + 1 < cols)
-                            dst[c + 1] = (uint16_t)(w >> 16);
+                        for (int e = 0; e < 16; ++e)
+                            if (c + e < cols)
+                                dst[c + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
                     }
                 }
             }
