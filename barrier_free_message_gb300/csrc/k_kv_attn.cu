@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
     extern __shared__ __align__(1024) unsigned char dyn[];
     __shared__ __align__(8) unsigned long long bars[2 * kStages + 4];
     __shared__ Meta meta[kStages];
+    __shared__ Piece s_next[2];                    // with the query rows' buffers: what the producer has begun with
     __shared__ Piece s_piece[kConsumers];          // each warp's, out of its registers
     __shared__ float s_ml[3][kConsumers][kRows];   // running maximum, sum, weight reference
     __shared__ uint32_t s_warp[kThreads / 32];
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
             tc::bar_init(empty + 8 * s, kConsumers);
         }
         for (int s = 0; s < 2; ++s) {
-            tc::bar_init(qfull + 8 * s, 32);
+            tc::bar_init(qfull + 8 * s, 33);
             tc::bar_init(qempty + 8 * s, kConsumers);
         }
         tc::bar_fence_init();
@@ -271,6 +272,10 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
                                  : "memory");
                 }
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(qfull + 8 * qs.slot) : "memory");
+                if (lane == 0) {
+                    s_next[qs.slot] = p;
+                    tc::bar_arrive(qfull + 8 * qs.slot);
+                }
                 qs.next();
             };
             const int *row = a.table + (size_t)p.b * a.W;
@@ -339,13 +344,17 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
     bool dead = false;                             // a wait gave up: go on without waiting, so that the warps stay together
     int piece = 0;
     for (long long u = u0; u < u1;) {
-        {
+        dead = dead || !tc::bar_wait(qfull + 8 * qs.slot, qs.phase, limit);
+        __syncwarp();
+        if (__any_sync(SFAR_FULL, dead)) {
+            dead = true;
             const Piece q = work.at(u, u1);
-            __syncwarp();
             if (lane == 0)
                 s_piece[warp] = q;
-            __syncwarp();
+        } else if (lane < sizeof(Piece) / 4) {
+            reinterpret_cast<int *>(&s_piece[warp])[lane] = reinterpret_cast<const int *>(&s_next[qs.slot])[lane];
         }
+        __syncwarp();
         const Piece &p = s_piece[warp];
         const int r = p.plane / a.Hk, hk = p.plane % a.Hk;
         const int rows = min(kRows, p.count * a.G - p.rt * kRows);
@@ -354,7 +363,6 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
         uint32_t q[RH][kK][2];
         float f[RH][2];
         int lo[RH][2], hi[RH][2];
-        dead = dead || !tc::bar_wait(qfull + 8 * qs.slot, qs.phase, limit);
         const unsigned char *qrow = mem + kStages * L::kStage + L::kJoin + qs.slot * L::kQ;
 #pragma unroll
         for (int i = 0; i < RH; ++i) {
