@@ -234,20 +234,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
 
     if (warp == kCopyWarp && lane < 2 * a.R)
         tc::prefetch_map(lane & 1 ? &a.vmap[lane >> 1] : &a.kmap[lane >> 1]);
-    if (tid == 0) {
-        for (int i = 0; i < kBars; ++i) {
-            const bool widen = (i >= kVEmpty && i < kVEmpty + kVStages) || (i >= kHFull && i < kHFull + kHStages);
-            const bool eight = (i >= kPFull && i < kPFull + 2) || (i >= kOEmpty && i < kPiece);
-            tc::bar_init(bar(i), eight ? kSoft / 2 : widen ? kWiden : i >= kPieceFree && i < kDrain ? kSoft + kWiden + 1 : 1);
-        }
+    if (tid < kBars) {
+        const int i = tid;
+        const bool widen = (i >= kVEmpty && i < kVEmpty + kVStages) || (i >= kHFull && i < kHFull + kHStages);
+        const bool eight = (i >= kPFull && i < kPFull + 2) || (i >= kOEmpty && i < kPiece);
+        tc::bar_init(bar(i), eight ? kSoft / 2 : widen ? kWiden : i >= kPieceFree && i < kDrain ? kSoft + kWiden + 1 : 1);
         tc::bar_fence_init();
         tc::fence_async();
-        upto[0] = 0;
-        for (int i = 0; i < 4; ++i) {
-            s_nan[i][0] = INT_MAX;
-            s_nan[i][1] = -1;
-        }
     }
+    if (tid < 4) {
+        s_nan[tid][0] = INT_MAX;
+        s_nan[tid][1] = -1;
+    }
+    if (tid == 0)
+        upto[0] = 0;
     if (warp == kMmaWarp)
         tc::tmem_alloc<1>(tc::smem(&s_tmem), 512);
     pdl_wait();
@@ -289,7 +289,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             upto[b + 1] = before;
         __syncthreads();
     }
-    sfar_attn_padding<D>(a, tid, kThreads);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -743,21 +742,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                         // some row does not see some token: places that hold none are zeros, and a NaN, which
                         // would reach every row, is taken out here and put back at the end
 #pragma unroll 1
-                        for (int n = 0; n < kSteps; ++n) {
-                            const int tok = tok0 + n * (32 * kWiden / kC);
-                            uint4 v = *reinterpret_cast<const uint4 *>(src + n * kFrom);
-                            const int g = tok >> 4;
-                            if (j0 + tok >= p.len || ((odd | odd >> 16) >> g & 1))
-                                v = make_uint4(0, 0, 0, 0);
-                            if (odd >> (24 + g) & 1)
-                                v = make_uint4(v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u);
-                            const uint4 is = make_uint4(nan_bytes(v.x), nan_bytes(v.y), nan_bytes(v.z), nan_bytes(v.w));
-                            if (is.x | is.y | is.z | is.w) {
-                                v = make_uint4(v.x & ~is.x, v.y & ~is.y, v.z & ~is.z, v.w & ~is.w);
-                                atomicMin(&nan[0], j0 + tok);
-                                atomicMax(&nan[1], j0 + tok);
+                        for (int n = 0; n < kSteps; n += 2) {
+                            uint4 v[2];
+#pragma unroll
+                            for (int b = 0; b < 2; ++b)
+                                v[b] = *reinterpret_cast<const uint4 *>(src + (n + b) * kFrom);
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) {
+                                const int tok = tok0 + (n + b) * (32 * kWiden / kC), g = tok >> 4;
+                                const uint32_t keep = j0 + tok >= p.len || ((odd | odd >> 16) >> g & 1) ? 0u : ~0u;
+                                const uint32_t sign = odd >> (24 + g) & 1 ? 0x80808080u : 0u;
+                                uint32_t *w = &v[b].x, any = 0;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t is = nan_bytes(w[e]) & keep;
+                                    any |= is;
+                                    w[e] = (w[e] ^ sign) & keep & ~is;
+                                }
+                                if (any) {
+                                    atomicMin(&nan[0], j0 + tok);
+                                    atomicMax(&nan[1], j0 + tok);
+                                }
+                                widen(dst + (n + b) * kTo, v[b]);
                             }
-                            widen(dst + n * kTo, v);
                         }
                     }
                     if (k == p.tiles - 1) {
@@ -779,6 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                     ms.next();
                 }
             }
+            sfar_attn_padding<D>(a, ct, 32 * kWiden);
         } else if (warp == kCopyWarp) {
             // ------------------------------------------------------------ copies
             tc::Ring<kKStages> kr;
