@@ -1,5 +1,7 @@
-"""Thin ctypes binding of libsfar (``include/sfar.h``, ``include/sfar_decode.h``,
-``include/sfar_kv.h``, ``include/sfar_fp8.h``, ``include/sfar_test.h``).
+"""Thin binding of libsfar (``include/sfar.h``, ``include/sfar_decode.h``,
+``include/sfar_kv.h``, ``include/sfar_fp8.h``, ``include/sfar_test.h``): ctypes,
+and for the calls on whole tensors (``SfarKv``, ``Sfar.quantize_fp8``,
+``Sfar.rowpar_gemm_fp8``) the module built from ``csrc/sfar_tensors.cpp``.
 
 Argument marshalling only: every step of the AllReduce runs in the library's
 CUDA kernels.  The functions keep the C names; pointers are plain integers
