@@ -7,13 +7,38 @@
 // the registers between.  HBM-bound: 3 bytes per element; the warps of a CTA
 // take consecutive rows, so their scales, [block][row], share sectors.  Measured,
 // 8 ranks of 2048 rows of 3584: 30 us, 5.9 TB/s; sixteen lanes to a block and a
-// vector each took 36 (twice the shuffles and exponents), one block at a time 48.
+// vector each took 36 (twice the shuffles and exponents), one block at a time 48.  Rows of odd
+// length: 1024 of 3583, 23 us, 3.8 TB/s; element by element they ran at 1.0.
 #include "sfar_e4m3.cuh"
 #include "sfar_kv_args.h"
 
 namespace {
+
 constexpr int kGroups = 2;                      // groups of four blocks a warp has in flight
+
+// Eight elements from an address that is a multiple of 2 only, out of the two aligned vectors they lie in.
+__device__ __forceinline__ uint4 load_shifted(uintptr_t at)
+{
+    const uint16_t *base = reinterpret_cast<const uint16_t *>(at & ~(uintptr_t)15);
+    const uint4 a = ld_nc_v4(base), b = ld_nc_v4(base + 8);
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const uint32_t off = (uint32_t)at & 15u;
+    if (off & 8u) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i)
+            w[i] = w[i + 2];
+    }
+    if (off & 4u) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i)
+            w[i] = w[i + 1];
+    }
+    const uint32_t bits = 8u * (off & 2u);
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
+                      __funnelshift_r(w[3], w[4], bits));
 }
+
+}  // namespace
 
 __global__ void __launch_bounds__(256) k_quant8(const __grid_constant__ SfarQuantArgs a)
 {
@@ -28,23 +53,28 @@ __global__ void __launch_bounds__(256) k_quant8(const __grid_constant__ SfarQuan
     const uint16_t *src = a.x[r] + row * a.ldx + k0;
     uint8_t *dst = a.x8[r] + row * a.ldx8 + k0;
     float *sx = a.sx[r] + b0 * a.m + row;
-    const bool whole = a.vec && (blockIdx.y + 1ll) * (512 * kGroups) <= a.k;        // of all the warp's blocks
+    const bool inside = (blockIdx.y + 1ll) * (512 * kGroups) <= a.k;        // all the warp's blocks are
     uint4 v[kGroups][2];
-    if (whole) {
+    if (inside && a.vec) {
 #pragma unroll
         for (int i = 0; i < kGroups; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 v[i][j] = ld_nc_v4(src + 512 * i + 64 * j);
     } else {
+        // rows that begin on no 16 bytes: the vectors around eight elements are read whole where both are the tensor's
+        const uintptr_t from = (uintptr_t)a.x[r], to = from + 2 * ((a.m - 1) * a.ldx + a.k);
 #pragma unroll
         for (int i = 0; i < kGroups; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int at = 512 * i + 64 * j;
+                const uintptr_t here = (uintptr_t)(src + at), base = here & ~(uintptr_t)15;
                 v[i][j] = make_uint4(0, 0, 0, 0);
                 if (a.vec && k0 + at + 8 <= a.k) {
                     v[i][j] = ld_nc_v4(src + at);
+                } else if (k0 + at + 8 <= a.k && base >= from && base + 32 <= to) {
+                    v[i][j] = load_shifted(here);
                 } else {
                     uint32_t *w = &v[i][j].x;
 #pragma unroll
@@ -86,7 +116,7 @@ __global__ void __launch_bounds__(256) k_quant8(const __grid_constant__ SfarQuan
         for (int j = 0; j < 2; ++j) {
             const int at = 512 * i + 64 * j;
             const uint2 q = sfar_quantize8(v[i][j], by, special);
-            if (whole || (a.vec && in && k0 + at + 8 <= a.k)) {
+            if (a.vec8 && (inside || (in && k0 + at + 8 <= a.k))) {
                 st_v2u32(dst + at, q.x, q.y);
             } else {
 #pragma unroll

@@ -60,7 +60,7 @@ struct SfarQuantArgs {
     uint8_t *x8[SFAR_MAX_R];
     float *sx[SFAR_MAX_R];
     long long m, k, ldx, ldx8;
-    int R, kb, vec;                         // vec: 16-byte loads and 8-byte stores are aligned
+    int R, kb, vec, vec8;                   // 16-byte loads, 8-byte stores are aligned
 };
 
 struct SfarGemm8Args {

@@ -37,7 +37,9 @@ bool aligned(const void *p, uintptr_t a) { return p && ((uintptr_t)p & (a - 1)) 
 // Up to this many tokens the projection runs with outputs along the tensor
 // core's lanes (weights read once, HBM-bound), beyond it with tokens there.
 // R = 8, k = 3584, hidden 8192: 128 tokens 52 us that way and 64 the other, 256
-// tokens (two tiles of tokens that way) 93 and 65.
+// tokens (two tiles of tokens that way) 93 and 65.  More tokens run that way
+// too if all tiles of 128 x 128 find an SM of their own, whose blocks of k then
+// pass faster: 8 x 307 tokens, k = 2048, hidden 256: 10.1 us, 12.4 the other.
 const size_t kFewTokens = 128;
 
 // Up to this many query rows (new tokens x query heads per key head) of the
@@ -414,12 +416,14 @@ sfar_status sfar_quantize_fp8(sfar_t *h, const void *const x[], void *const x8[]
     SfarQuantArgs a;
     memset(&a, 0, sizeof a);
     a.kb = (int)ceil_div(k, SFAR_FP8_BLOCK);
-    a.vec = ldx % 8 == 0 && ldx8 % 8 == 0;
+    a.vec = ldx % 8 == 0;
+    a.vec8 = ldx8 % 8 == 0;
     const size_t xb = ((m - 1) * ldx + k) * 2, qb = (m - 1) * ldx8 + k, sb = (size_t)a.kb * m * 4;
     for (int r = 0; r < v.R; ++r) {
         if (!aligned(x[r], 2) || !x8[r] || !aligned(sx[r], 4))
             return SFAR_ERR_INVALID;
-        a.vec = a.vec && aligned(x[r], 16) && aligned(x8[r], 8);
+        a.vec = a.vec && aligned(x[r], 16);
+        a.vec8 = a.vec8 && aligned(x8[r], 8);
         a.x[r] = static_cast<const uint16_t *>(x[r]);
         a.x8[r] = static_cast<uint8_t *>(x8[r]);
         a.sx[r] = sx[r];
@@ -477,7 +481,8 @@ sfar_status sfar_rowpar_gemm_fp8(sfar_t *h, const void *const x8[], const float 
                 out.meets(Span(sw[j], nb * kb * 4)) || (i < j && out.meets(Span(y[j], yb))))
                 return SFAR_ERR_INVALID;
     }
-    const int few = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : m <= kFewTokens ? 128 : 0;
+    const bool one = (size_t)v.R * ceil_div(m, 128) * ceil_div(hidden, 128) <= (size_t)v.sms;
+    const int few = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : m <= kFewTokens || one ? 128 : 0;
     const cuuint32_t unit[2] = {1, 1}, wbox[2] = {SFAR_FP8_BLOCK, 128}, xbox[2] = {SFAR_FP8_BLOCK, few ? (cuuint32_t)few : 128u};
     auto map = [&](CUtensorMap *to, const void *p, size_t rows, size_t ld, const cuuint32_t *box) {
         const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld};

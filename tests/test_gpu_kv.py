@@ -515,6 +515,38 @@ def test_quantize_and_gemm(R, m, k, n):
     check_gemm(y.cpu(), x8.cpu(), sx.cpu(), w[:, :, :k], sw, f"{R} {m} {k} {n}")
 
 
+@pytest.mark.parametrize("R,m,k,n", [(8, 300, 200, 1000), (4, 513, 130, 1030), (2, 257, 72, 4832), (8, 260, 384, 1001),
+                                     (3, 1100, 1027, 776), (8, 256, 1536, 2048)])
+def test_quantize_and_gemm_of_many_tiles(R, m, k, n):
+    """More tiles of 128 x 128 than there are SMs; last outputs that are no multiple of 128, 16 or 8."""
+    test_quantize_and_gemm(R, m, k, n)
+
+
+def test_quantize_rows_of_every_alignment():
+    """Rows that begin on any even address, in a tensor that others' values surround; an infinity at one place."""
+    R, m, k = 2, 17, 2200
+    g = torch.Generator().manual_seed(12)
+    h = sfar.Sfar(R, 1 << 16, "bf16")
+    try:
+        for at, wide in ((0, 2200), (1, 2203), (3, 2208), (4, 2204), (6, 2207), (7, 2209)):
+            whole = torch.full((R, m + 2, wide + 8), float("nan"), dtype=torch.bfloat16, device="cuda")
+            xd = whole[:, 1:-1, at:at + k]
+            x = (torch.randn(R, m, k, generator=g) * torch.exp(2 * torch.randn(R, m, 1, generator=g))).to(torch.bfloat16)
+            x[1, m - 1, k - 1] = float("inf")
+            xd.copy_(x)
+            x8 = torch.zeros(R, m, 2208, dtype=torch.uint8, device="cuda").view(F8)[:, :, :k]
+            sx = torch.empty(R, -(-k // 128), m, device="cuda")
+            for given in (xd, [t.contiguous() for t in xd]):
+                h.quantize_fp8(given, x8, sx)
+                torch.cuda.synchronize()
+                for r in range(R):
+                    q, s = kv_ref.quantize(x[r])
+                    assert torch.equal(sx[r].cpu().double(), s), (at, r)
+                    assert torch.equal(x8[r].cpu().double().nan_to_num(1e9), q.nan_to_num(1e9)), (at, r)
+    finally:
+        h.close()
+
+
 def test_quantize_special_values_and_strides():
     x = torch.randn(2, 6, 300, generator=torch.Generator().manual_seed(8)).to(torch.bfloat16)
     x[0, 0] = 0
