@@ -127,12 +127,10 @@ struct SfarJoin {
     // by one thread, after the CTA's writes: whether this CTA is the last
     __device__ __forceinline__ bool last() const
     {
-        __threadfence();            // of all the CTA's writes: a barrier has ordered them before it
-        const bool is = atomicAdd(counter, 1) == (hi - lo) / step;
-        if (is)
-            *counter = 0;           // for the next call
-        __threadfence();
-        return is;
+        const int all = (hi - lo) / step;
+        int come;                   // releases all the CTA's writes: a barrier has ordered them before it
+        asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(come) : "l"(counter), "r"(all) : "memory");
+        return come == all;         // the last has set the counter back to 0, for the next call
     }
     // on to the groups; false: these were all
     __device__ __forceinline__ bool next(const SfarAttnArgs &a, int kind)
