@@ -25,8 +25,8 @@
 //
 // Measured, 8 ranks, k = 3584, hidden 8192: 64 tokens (235 MB of weights) 43
 // us, 5.8 TB/s or 0.85 of a copy's rate, bound by the weights' stream and the
-// last, partly filled wave of tiles; 2048 tokens 400 us, 2408 TFLOP/s, 1.22 of
-// a bf16 product's rate.  There the fold bounds it: 512 x 128 partial sums
+// last, partly filled wave of tiles; 2048 tokens 392 us, 2455 TFLOP/s, 1.24 of
+// a bf16 product's rate.  There the fold bounds it: 128 x 256 partial sums
 // pass through the registers of an SM for every block (with the fold's
 // arithmetic left out the same kernel takes 306 us).
 #include "sfar_e4m3.cuh"
