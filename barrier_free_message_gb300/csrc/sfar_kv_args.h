@@ -87,7 +87,7 @@ const void *sfar_kernel_gemm8(int tokens, int *threads, int *smem);
 int sfar_fp8_prepare();
 
 #define SFAR_PLAN_THREADS 1024
-#define SFAR_PLAN_CLUSTER 8
+#define SFAR_PLAN_CLUSTER 8                 // twice that for many requests or tokens
 #define SFAR_QUANT_COLS 1024                // columns a warp of the quantisation takes of a row
 #define SFAR_APPEND_WARPS 8
 #define SFAR_ATTN_TILE 64
