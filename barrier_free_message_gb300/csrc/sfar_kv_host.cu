@@ -266,7 +266,7 @@ sfar_status sfar_kv_plan(sfar_kv_t *h, const int32_t *lens, const int32_t *delta
     SfarKvPlanArgs a{lens,  delta, table,  ring,          state,            lens_out,    state_out, starts,
                      slots, taken, h->ctl, (int)requests, (int)table_width, (int)tokens, h->shift,  (int)h->pages};
     // Small steps need no more than a warp's worth of sums per scheduler, large ones all the CTAs that a cluster can have:
-    // their time is that of the instructions of the slots and pages (2039 requests with 62 k tokens: 13.5 us on 8 SMs, 11.1 on 16).
+    // their time is that of the instructions of the slots and pages (2039 requests with 62 k tokens: 13.5 us on 8 SMs, 11.1 on 16, with the page lists of that time).
     const bool small = requests <= 256 && tokens <= 8192;
     const unsigned cluster = small ? SFAR_PLAN_CLUSTER : h->plan_ctas;
     return launch(h->dev, sfar_kernel_kv_plan(), dim3(cluster), small ? 256 : SFAR_PLAN_THREADS, (4 * requests + 1) * 4, &a, s, false, cluster);
