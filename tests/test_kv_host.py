@@ -66,7 +66,7 @@ def test_null_handles(lib):
     lib.sfar_kv_destroy(None)
 
 
-def test_python_layer_refuses_wrong_tensors():
+def test_python_layer_refuses_wrong_tensors(lib):
     t = torch.zeros(2, 4, 2, 16, 64, dtype=torch.uint8)
     s = torch.zeros(2, 4, 2)
     for args in ((t.float(), t, s, s), (t, t[:, :, :, :8], s, s), (t, t, s[:, :3], s), (t, t, s, s.double()),
@@ -76,7 +76,7 @@ def test_python_layer_refuses_wrong_tensors():
             sfar.SfarKv(*args, q_heads=4)
 
 
-def test_calls_refuse_wrong_tensors():
+def test_calls_refuse_wrong_tensors(lib):
     """What the module that reads the tensors refuses before it makes the call (a closed handle would be next)."""
     native = sfar._tensors()
     i = torch.zeros(4, dtype=torch.int32)
