@@ -53,6 +53,11 @@ namespace {
 
 constexpr int kTile = SFAR_ATTN_TILE;              // cached tokens per stage
 constexpr int kConsumers = 4, kThreads = 32 * (kConsumers + 1);
+// A weight is exp2(score - top) times exp2(top + log2 scale - wtop).  Tokens of value scale 0 count for `top` alone, so
+// where they are the row's largest the second factor has no bound while the first underflows; a page's weights are taken
+// for 0 where it passes this, their share of the row's sum being below 2^-100.  Up to nonzero scales 2^100 apart it stays
+// below.
+constexpr float kFar = 120.f;
 
 // Shared memory of a CTA, after the prefix sums.
 template <int D, int RH> struct Lay {
@@ -490,7 +495,8 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const float ref = top[i][y] == -INFINITY ? 0.f : top[i][y];
-                    const float by = copysignf(wtop[i][y] == -INFINITY ? 0.f : ex2(ref + lvs - wtop[i][y]), vs);
+                    const float up = ref + lvs - wtop[i][y];          // inf or NaN while no token has a value scale
+                    const float by = copysignf(up <= kFar ? ex2(up) : 0.f, vs);
                     const float e0 = ex2(x[i][y] - ref), e1 = ex2(x[i][2 + y] - ref);
                     sum[i][y] += e0 + e1;
                     e4[y] = e0 * by;
