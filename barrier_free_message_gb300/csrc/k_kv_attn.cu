@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
                 Meta &m = meta[st.slot];
                 if (lane < kTile / 16) {
                     m.ks[lane] = k16;
-                    m.vs[lane] = v16;
+                    m.vs[lane] = fabsf(v16) <= kNoScale ? 0.f : v16;
                 }
                 if (lane == 0)
                     m.bad = (int)dead;

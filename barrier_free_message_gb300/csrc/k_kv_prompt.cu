@@ -16,7 +16,8 @@
 // place of the scores they come from.  One running reference serves weights
 // and sum, the weights' (score times value scale), and the sum is of weight /
 // value scale: nothing is lost while the value scales of one request are
-// within 2^100 of one another.  The accumulator is rescaled, in tensor memory,
+// within 2^100 of one another.  Tokens of value scale 0 have no weight; their
+// exponentials have a reference and a sum of their own, joined at the end.  The accumulator is rescaled, in tensor memory,
 // only when a reference moves.
 //
 // A CTA takes 256 rows as two tiles of 128, each with eight softmax warps (two
@@ -50,6 +51,7 @@ constexpr int kSoft = 16;                          // softmax warps
 constexpr int kWiden = 2, kCopyWarp = kSoft + kWiden, kMmaWarp = kCopyWarp + 1;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kOver = 6;                           // what a row tile costs beside its tiles, in tiles
+constexpr float kSumUp = 20.f, kSumDown = 0x1p-20f;    // the sum is kept 2^20 down: so it holds scales from 2^-100 to 2^100
 constexpr int kKStages = 3, kVStages = 2, kHStages = 2, kMeta = 4, kPieces = 8;
 
 template <int D> struct Lay {
@@ -58,9 +60,10 @@ template <int D> struct Lay {
     static constexpr int kBytes = oQ + 4 * kQ;     // queries: two tiles, nearest and rest
 };
 struct Meta {                                      // of a step
-    float ks[kTile / 16], lvs[kTile / 16], ivs[kTile / 16];    // each 16 tokens: key scale, log2 of the value scale and its inverse
-    // bit i: tokens 16 i .. are on no page of the pool; 8: a key scale is negative; 16 + i: tokens' value scale is 0
-    // (1 is put for it, and zeros for the values); 24 + i: it is negative (its magnitude is put, and -v for the values)
+    // each 16 tokens: key scale, log2 of the value scale (-inf for 0), kSumDown over the value scale (0 for 0)
+    float ks[kTile / 16], lvs[kTile / 16], ivs[kTile / 16];
+    // bit i: tokens 16 i .. are on no page of the pool; 8: a key scale is negative; 16 + i: tokens' value scale is 0 (they
+    // have no weight and are summed apart); 24 + i: it is negative (its magnitude is put, and -v for the values)
     uint32_t odd;
     int pad[3];
 };
@@ -422,6 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             const int all_from = __reduce_max_sync(SFAR_FULL, lo), all_to = min(p.len, __reduce_min_sync(SFAR_FULL, hi));
             // log2 reference of the row's weights; sum: of this half's weight / value scale
             float wtop = -INFINITY, sum = 0.f;
+            bool zeros = false;                    // told(0), told(2): reference and sum of the tokens of value scale 0
             const int tiles = p.tiles, j00 = p.tile0 * kTile + 64 * half;
             for (int k = 0; mine && k < tiles; ++k) {
                 const int j0 = j00 + k * kTile;
@@ -433,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                 const float lvs[4] = {lv.x, lv.y, lv.z, lv.w}, ivs[4] = {iv.x, iv.y, iv.z, iv.w};
                 const uint32_t odd = m.odd;
                 const uint32_t none = odd >> (4 * half) & 15u;
-                const bool edge = j0 < all_from || j0 + 64 > all_to || none || (odd & 0x100u);
+                const bool edge = j0 < all_from || j0 + 64 > all_to || none || (odd & 0xff0100u);
                 dead = dead || !tc::bar_wait(bar(kSFull + x), sphase, limit);
                 sphase ^= 1u;
                 tc::fence_after();
@@ -444,7 +448,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                         fetch(s_piece[next_at]);
                 }
                 if (edge) {
-                    // scaled here, -inf where the row does not see the token, and put back
+                    // scaled here, -inf where the row does not see the token, and put back; tokens of value scale 0 are summed
+                    float zt = -INFINITY, zs = 0.f;
+                    if (odd & 0xff0000u) {
+                        pair_sync(pair);           // the other half has read what the places held before
+                        if (zeros)
+                            zt = told(0), zs = told(2);
+                    }
 #pragma unroll 1
                     for (int i = 0; i < 64; i += 16) {
                         uint32_t v[16];
@@ -456,8 +466,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                         for (int e = 0; e < 16; ++e)
                             v[e] = __float_as_uint(e >= from && e < to ? __uint_as_float(v[e]) * by : -INFINITY);
                         tc::st16(tS + i, v);
+                        if (odd >> (16 + 4 * half + (i >> 4)) & 1) {
+                            const float next = fmaxf(zt, max16(v)), ref = next == -INFINITY ? 0.f : next;
+                            zs *= zt == -INFINITY ? 1.f : ex2(zt - next);
+                            zt = next;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                zs += ex2(__uint_as_float(v[e]) - ref);
+                        }
                     }
                     tc::wait_st();
+                    if (odd & 0xff0000u) {
+                        zeros = true;
+                        told(0) = zt;
+                        told(2) = zs;
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         c[i] = 1.f;
@@ -528,15 +551,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                 if (have && rows_of(s_piece[next_at]) > 0)
                     fetch(s_piece[next_at]);
             }
+            // what the sum is relative to; with tokens of value scale 0, both sums at one reference
+            float top = wtop + kSumUp;
+            if (zeros) {
+                const float zt = told(0), zs = told(2), at = fmaxf(top, zt);
+                sum = (top == -INFINITY ? sum : ex2(top - at) * sum) + (zt == -INFINITY ? zs : ex2(zt - at) * zs);
+                top = at;
+            }
             // the next queries first, so that their first scores are formed while this piece is written out
             float fnext = 0.f;
             if (have && rows_of(s_piece[next_at]) > 0)
                 fnext = split();
             // --------------------------------------------------------- epilogue
             if (mine) {
+                if (zeros) {
+                    pair_sync(pair);               // the last move's exchange has been read
+                    told(1) = top;
+                }
                 told(2) = sum;
                 pair_sync(pair);
-                sum += other(2);
+                if (zeros) {
+                    const float at = fmaxf(top, other(1));
+                    sum = (top == -INFINITY ? sum : ex2(top - at) * sum) + (other(1) == -INFINITY ? other(2) : ex2(other(1) - at) * other(2));
+                    top = at;
+                } else {
+                    sum += other(2);
+                }
                 dead = dead || !tc::bar_wait(bar(kOFull + x), ophase, limit);
                 ophase ^= 1u;
                 tc::fence_after();
@@ -549,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                 return reinterpret_cast<float4 *>(a.part) + ((size_t)cta * 2 + (cta == c0)) * (kRows * (D / 4 + 1)) + rho;
             };
             float4 *dst = slot(blockIdx.x);
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;         // 0: the row attends to nothing
+            const float inv = sum == 0.f ? 0.f : (wtop == -INFINITY ? 1.f : ex2(wtop - top)) / sum;       // 0: the row attends to nothing
             const int r = p.plane / a.Hk, hk = p.plane % a.Hk;
             uint16_t *out = a.out[r] + (long long)(p.first + tok) * a.ots + (long long)(hk * a.G + n - tok * a.G) * a.ohs;
             const int *nan = s_nan[piece++ & 3];
@@ -598,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                 if (lane == 0)
                     tc::bar_arrive(bar(kOEmpty + x));
                 if (part && row && half == 0)
-                    __stcg(dst + D / 4 * kRows, make_float4(wtop, sum, wtop, 0.f));
+                    __stcg(dst + D / 4 * kRows, make_float4(top, sum, wtop, 0.f));
             }
             if (mine && part) {
                 // the last of the row tile's CTAs joins its parts; the two tiles of rows separately
@@ -722,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                 for (int k = 0; k < p.tiles; ++k) {
                     const int j0 = (p.tile0 + k) * kTile;
                     dead = dead || !tc::bar_wait(bar(kMFull + ms.slot), ms.phase, limit);
-                    const uint32_t odd = meta[ms.slot].odd & ~0x100u;
+                    const uint32_t odd = meta[ms.slot].odd & 0xff0000ffu;
                     dead = dead || !tc::bar_wait(bar(kVFull + vs.slot), vs.phase, limit) ||
                            !tc::bar_wait(bar(kHEmpty + hs.slot), hs.phase ^ 1u, limit);
                     const unsigned char *src = gen + L::oV + vs.slot * L::kK + from;
@@ -750,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
 #pragma unroll
                             for (int b = 0; b < 2; ++b) {
                                 const int tok = tok0 + (n + b) * (32 * kWiden / kC), g = tok >> 4;
-                                const uint32_t keep = j0 + tok >= p.len || ((odd | odd >> 16) >> g & 1) ? 0u : ~0u;
+                                const uint32_t keep = j0 + tok >= p.len || (odd >> g & 1) ? 0u : ~0u;
                                 const uint32_t sign = odd >> (24 + g) & 1 ? 0x80808080u : 0u;
                                 uint32_t *w = &v[b].x, any = 0;
 #pragma unroll
@@ -841,14 +881,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                     const float k16 = __shfl_sync(SFAR_FULL, ks, of & 31), v16 = __shfl_sync(SFAR_FULL, vs, of & 31);
                     const bool sixteen = lane < kTile / 16, there = any >> (of & 31) & 1u;
                     const uint32_t none = __ballot_sync(SFAR_FULL, sixteen && !there), minus = __ballot_sync(SFAR_FULL, sixteen && v16 < 0.f);
-                    const uint32_t zero = __ballot_sync(SFAR_FULL, sixteen && there && v16 == 0.f);
+                    const bool nil = fabsf(v16) <= kNoScale;
+                    const uint32_t zero = __ballot_sync(SFAR_FULL, sixteen && there && nil);
                     const bool negative = __any_sync(SFAR_FULL, ks < 0.f);
                     Meta &m = meta[ms.slot];
                     if (sixteen) {
-                        const float v = v16 == 0.f ? 1.f : fabsf(v16);
                         m.ks[lane] = k16;
-                        m.lvs[lane] = lg2(v);
-                        m.ivs[lane] = 1.f / v;
+                        m.lvs[lane] = nil ? -INFINITY : lg2(fabsf(v16));
+                        m.ivs[lane] = nil ? 0.f : kSumDown / fabsf(v16);
                     }
                     if (lane == 0)
                         m.odd = none | (negative ? 256u : 0u) | zero << 16 | minus << 24;

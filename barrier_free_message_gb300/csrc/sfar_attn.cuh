@@ -4,6 +4,7 @@
 #include "sfar_kv_device.cuh"
 #include "sfar_tc.cuh"
 
+constexpr float kNoScale = 0x1p-100f;  // value scales up to it count as 0: what the append gives to a page of zeros
 constexpr float kAttnLift = 6.f;       // log2 by which a score or weight may pass its running reference
 
 __device__ __forceinline__ float ex2(float x)

@@ -122,10 +122,11 @@ sfar_status sfar_kv_append(sfar_kv_t *kv, const void *const k[], const void *con
  * (and a row past starts[requests]) is zeros.  The largest score and the sum
  * of the exponentials are held in binary32, as are the products' sums; the
  * result does not depend on what the other rows or masked tokens hold.  A
- * page's scales may be any finite number, zero and negative ones included;
- * the value scales of one request's context (those that are not zero) are
- * within a factor of 2^100 of one another: beyond it tokens with the smaller
- * scales lose their part of the sum of the exponentials.
+ * page's scales may be zero, and negative.  A value scale of magnitude 2^-100
+ * or less counts as zero (2^-100 is what sfar_kv_append gives to zeros); the
+ * others of one request's context are at most 2^100 and within a factor of
+ * 2^100 of one another: beyond it tokens with the smaller scales lose their
+ * part of the sum of the exponentials.
  * max_q: the most new tokens any request has in this call (a hint that picks
  * the kernel; a request that has more is still computed).  out overlaps no
  * other argument.  1 <= requests <= SFAR_KV_MAX_REQUESTS; tokens, table_width
