@@ -497,10 +497,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                 }
                 uint32_t s[2][16];                 // scores are read twice rather than held: registers that spill cost more
                 tc::ld16(s[0], tS);
-                if (pair_any(pair, now > wtop + kAttnLift)) {
+                if (pair_any(pair, now > wtop + (kAttnLift + kAttnDeep))) {
                     told(1) = now;
                     pair_sync(pair);
-                    const float next = fmaxf(wtop, fmaxf(now, other(1)));
+                    const float next = fmaxf(wtop, fmaxf(now, other(1)) - kAttnDeep);
                     const float keep = wtop == -INFINITY ? 1.f : ex2(wtop - next);   // o is 0 then, or NaN
                     sum *= keep;
                     wtop = next;

@@ -5,7 +5,9 @@
 #include "sfar_tc.cuh"
 
 constexpr float kNoScale = 0x1p-100f;  // value scales up to it count as 0: what the append gives to a page of zeros
-constexpr float kAttnLift = 6.f;       // log2 by which a score or weight may pass its running reference
+// log2 by which a score may pass its running reference.  The weights' reference stands 2^kAttnDeep lower: in binary16 they
+// reach 2^15 of its 2^16, keep all their bits down to 2^-23 of a row's largest and some down to 2^-34.
+constexpr float kAttnLift = 6.f, kAttnDeep = 9.f;
 
 __device__ __forceinline__ float ex2(float x)
 {

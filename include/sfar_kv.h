@@ -120,7 +120,9 @@ sfar_status sfar_kv_append(sfar_kv_t *kv, const void *const k[], const void *con
  * p = lens[b] - (starts[b + 1] - starts[b]) + i and attends to the cached
  * tokens j <= p and, with window > 0, j > p - window.  A row that has none
  * (and a row past starts[requests]) is zeros.  The largest score and the sum
- * of the exponentials are held in binary32, as are the products' sums; the
+ * of the exponentials are held in binary32, as are the products' sums; a
+ * weight (exponential times value scale) is rounded to 11 bits, and to a
+ * multiple of 2^-33 of the row's largest where that is coarser; the
  * result does not depend on what the other rows or masked tokens hold.  A
  * page's scales may be zero, and negative.  A value scale of magnitude 2^-100
  * or less counts as zero (2^-100 is what sfar_kv_append gives to zeros); the
