@@ -20,10 +20,10 @@
 // accumulator are binary32.  A value's weight, p times its page's scale, is
 // rounded to binary16 for the second product (2^-11, where the bf16 result has
 // 2^-8); it is taken relative to a running reference of its own, so that the
-// scales' size does not matter.  Both references move only when they are
-// passed by 2^6, so that the accumulator is seldom rescaled.  The weights'
-// stands 2^9 lower and uses binary16's range: weights are at most 2^15, and
-// lose bits only below 2^-23 of the row's largest.
+// scales' size does not matter.  A row's references move only when its scores
+// pass them by 2^7.9, so that the accumulator is seldom rescaled.  The weights'
+// stands 2^8 lower and uses binary16's range: weights are at most 2^15.9, and
+// lose bits only below 2^-22 of the row's largest.
 //
 // Work: the tiles of all (rank, key head, request, 8 or 16 rows) form one line that
 // is cut into equal pieces, one per CTA, wherever the cuts fall: a batch of
@@ -477,7 +477,9 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1)
                             now = fmaxf(now, __shfl_xor_sync(SFAR_FULL, now, d));
-                        const float next = fmaxf(top[i][y], now), wnext = fmaxf(wtop[i][y], now + lvs - kAttnDeep);
+                        // a row's references go by its own scores alone
+                        const float next = now > top[i][y] + kAttnLift ? now : top[i][y];
+                        const float wnext = now + lvs > wtop[i][y] + (kAttnLift + kAttnDeep) ? now + lvs - kAttnDeep : wtop[i][y];
                         const float keep = wtop[i][y] == -INFINITY ? 1.f : ex2(wtop[i][y] - wnext);      // o is 0 then, or NaN
                         sum[i][y] *= top[i][y] == -INFINITY ? 1.f : ex2(top[i][y] - next);
                         top[i][y] = next;

@@ -193,6 +193,9 @@ __device__ __forceinline__ float max16(const uint32_t *v)
         m[i] = max3(__uint_as_float(v[3 * i]), __uint_as_float(v[3 * i + 1]), __uint_as_float(v[3 * i + 2]));
     return fmaxf(max3(m[0], m[1], m[2]), max3(m[3], m[4], __uint_as_float(v[15])));
 }
+// What takes a product with keys of scale ks to units of log2, without its sign.  Never 0, so that a masked product of -inf
+// stays that; products are below 2^25, so 2^-60 stands for any smaller one.
+__device__ __forceinline__ float score_scale(float f, float ks) { return fmaxf(f * fabsf(ks), 0x1p-60f); }
 // The eight warps of a tile's softmax; the two warps that share 32 rows.
 __device__ __forceinline__ void tile_sync(int x) { asm volatile("bar.sync %0, 256;" ::"r"(1 + x) : "memory"); }
 __device__ __forceinline__ bool tile_any(int x, bool v)
@@ -433,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                 const Meta &m = meta[ms.slot];
                 const float4 ks = *reinterpret_cast<const float4 *>(m.ks + 4 * half), lv = *reinterpret_cast<const float4 *>(m.lvs + 4 * half),
                              iv = *reinterpret_cast<const float4 *>(m.ivs + 4 * half);
-                float c[4] = {f * ks.x, f * ks.y, f * ks.z, f * ks.w};
+                const float c[4] = {score_scale(f, ks.x), score_scale(f, ks.y), score_scale(f, ks.z), score_scale(f, ks.w)};
                 const float lvs[4] = {lv.x, lv.y, lv.z, lv.w}, ivs[4] = {iv.x, iv.y, iv.z, iv.w};
                 const uint32_t odd = m.odd;
                 const uint32_t none = odd >> (4 * half) & 15u;
@@ -448,7 +451,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                         fetch(s_piece[next_at]);
                 }
                 if (edge) {
-                    // scaled here, -inf where the row does not see the token, and put back; tokens of value scale 0 are summed
+                    // -inf where the row does not see the token, the other sign where the key scale is negative, and put back (so
+                    // that what is seen is rounded as in a tile without masks); tokens of value scale 0 are summed
                     float zt = -INFINITY, zs = 0.f;
                     if (odd & 0xff0000u) {
                         pair_sync(pair);           // the other half has read what the places held before
@@ -460,19 +464,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                         uint32_t v[16];
                         tc::ld16(v, tS + i);
                         tc::wait_ld(v);
-                        const float by = f * m.ks[4 * half + (i >> 4)];
+                        const float scale = m.ks[4 * half + (i >> 4)];
+                        const uint32_t sign = scale < 0.f ? 0x80000000u : 0u;
                         const int from = none >> (i >> 4) & 1 ? 64 : lo - j0 - i, to = min(hi, p.len) - j0 - i;
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            v[e] = __float_as_uint(e >= from && e < to ? __uint_as_float(v[e]) * by : -INFINITY);
+                            v[e] = e >= from && e < to ? v[e] ^ sign : __float_as_uint(-INFINITY);
                         tc::st16(tS + i, v);
                         if (odd >> (16 + 4 * half + (i >> 4)) & 1) {
-                            const float next = fmaxf(zt, max16(v)), ref = next == -INFINITY ? 0.f : next;
+                            const float by = score_scale(f, scale), next = fmaxf(zt, max16(v) * by), ref = next == -INFINITY ? 0.f : next;
                             zs *= zt == -INFINITY ? 1.f : ex2(zt - next);
                             zt = next;
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                zs += ex2(__uint_as_float(v[e]) - ref);
+                                zs += ex2(fmaf(__uint_as_float(v[e]), by, -ref));
                         }
                     }
                     tc::wait_st();
@@ -481,9 +486,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                         told(0) = zt;
                         told(2) = zs;
                     }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        c[i] = 1.f;
                 }
                 float now;
                 {
@@ -500,7 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                 if (pair_any(pair, now > wtop + (kAttnLift + kAttnDeep))) {
                     told(1) = now;
                     pair_sync(pair);
-                    const float next = fmaxf(wtop, fmaxf(now, other(1)) - kAttnDeep);
+                    // a row's reference goes by its own scores alone
+                    const float most = fmaxf(now, other(1)), next = most > wtop + (kAttnLift + kAttnDeep) ? most - kAttnDeep : wtop;
                     const float keep = wtop == -INFINITY ? 1.f : ex2(wtop - next);   // o is 0 then, or NaN
                     sum *= keep;
                     wtop = next;

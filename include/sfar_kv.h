@@ -122,7 +122,7 @@ sfar_status sfar_kv_append(sfar_kv_t *kv, const void *const k[], const void *con
  * (and a row past starts[requests]) is zeros.  The largest score and the sum
  * of the exponentials are held in binary32, as are the products' sums; a
  * weight (exponential times value scale) is rounded to 11 bits, and to a
- * multiple of 2^-33 of the row's largest where that is coarser; the
+ * multiple of 2^-32 of the row's largest where that is coarser; the
  * result does not depend on what the other rows or masked tokens hold.  A
  * page's scales may be zero, and negative.  A value scale of magnitude 2^-100
  * or less counts as zero (2^-100 is what sfar_kv_append gives to zeros); the

@@ -38,9 +38,9 @@ def reference(cpu, r, table, lens, starts, q, scale, window=0, lost=None):
 
 def bound(out, mag, top, n, vmax):
     """2^-8 |o| (one rounding to bf16) + 2^-10 of the weighted mean of |v| (the weights' rounding to 11 bits, and as much
-    again for the exponentials and the binary32 sums) + n times 2^-34 of the row's largest weighted value (weights below
-    2^-23 of it lie below binary16's normal range) + 2^-100 of the largest value (weights that small count as none)."""
-    return 2.0 ** -8 * out.abs() + 2.0 ** -10 * mag + n * 2.0 ** -34 * 448.0 * top + 2.0 ** -100 * 448.0 * vmax
+    again for the exponentials and the binary32 sums) + n times 2^-33 of the row's largest weighted value (weights below
+    2^-22 of it lie below binary16's normal range) + 2^-100 of the largest value (weights that small count as none)."""
+    return 2.0 ** -8 * out.abs() + 2.0 ** -10 * mag + n * 2.0 ** -33 * 448.0 * top + 2.0 ** -100 * 448.0 * vmax
 
 
 def check(got, cpu, table, lens, starts, q, scale, window=0, floor=0.0, ctx=""):
