@@ -165,13 +165,11 @@ __global__ void __launch_bounds__(SFAR_PLAN_THREADS) k_kv_plan(const __grid_cons
     }
     if (crank == 0 && tid == 0) {
         a.starts[a.B] = s_start[a.B];
-        long long left = (long long)freec - used + carry.back;
-        if (left > a.pages) {
+        const int held = a.pages - freec;       // the ring has room for no more, whatever is taken
+        if (carry.back > held)
             sfar_kv_fault(a.ctl, 0, SFAR_KV_BAD_RING);
-            left = a.pages;
-        }
         a.state_out[0] = (int)ring_at((unsigned)used);
-        a.state_out[1] = (int)left;
+        a.state_out[1] = freec - used + (int)min(carry.back, (long long)held);
     }
     // Table entries of new pages, ring entries of pages given back: a few lanes per request (most gain a page or none, a
     // large step has ones that leave with many), four pages in flight.
@@ -200,9 +198,11 @@ __global__ void __launch_bounds__(SFAR_PLAN_THREADS) k_kv_plan(const __grid_cons
             for (int i = 0; i < 4; ++i) {
                 const long long at = (long long)off + j0 + i * share - want;
                 if (j0 + i * share >= have || at >= (long long)a.pages - freec)
-                    continue;               // more than the pool has: recorded above
-                if ((unsigned)p[i] >= pages)
+                    continue;               // more than the pool has: recorded above, and not counted
+                if ((unsigned)p[i] >= pages) {
                     sfar_kv_fault(a.ctl, b, SFAR_KV_BAD_PAGE);
+                    p[i] = -1;              // its place holds no page
+                }
                 unsigned to = (unsigned)head + (unsigned)freec;
                 to = (to >= pages ? to - pages : to) + (unsigned)at;
                 a.ring[to >= pages ? to - pages : to] = p[i];

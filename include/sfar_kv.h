@@ -83,7 +83,12 @@ void sfar_kv_destroy(sfar_kv_t *kv);
  * max(delta, 0): request b's new tokens are rows starts[b] .. starts[b + 1]
  * of the step's tensors, taken or not), slots[0 .. tokens) (-1 past the last
  * new token), the table entries of new pages, the ring entries of pages given
- * back, and state_out.  Other entries stay.  table: [requests][table_width].
+ * back, and state_out.  Pages given back beyond those that the state says are
+ * held are dropped (SFAR_KV_BAD_RING); a page number outside the pool
+ * (SFAR_KV_BAD_PAGE) becomes -1, in the ring when it is given back and in the
+ * table when it is taken, and its tokens' slots are -1.  The rows of a request
+ * that was refused mean nothing to sfar_kv_attention.  Other entries stay.
+ * table: [requests][table_width].
  * lens_out may be lens and state_out may be state; nothing else overlaps.
  * 1 <= requests <= SFAR_KV_MAX_REQUESTS, 1 <= table_width, tokens < 2^31.
  */
