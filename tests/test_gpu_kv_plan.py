@@ -1,7 +1,9 @@
-"""The plan of the paged cache's steps: more pages given back than the pool holds, and bad pages given back."""
+"""The plan of the paged cache's steps: more pages given back than the pool holds, bad pages given
+back, and thousands of requests."""
 import pytest
 
-from test_gpu_kv import _built, fresh, ok, run_plan, sfar_where  # noqa: F401  (a fixture)
+import kv_ref
+from test_gpu_kv import _built, draw_plan, fresh, ok, run_plan, sfar_where  # noqa: F401  (a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +38,16 @@ def test_bad_pages_given_back_leave_the_ring():
         got = run_plan(kv, [0, 1], [48, 0], [[-1] * 3, [2, -1, -1]], got["ring"], [1, 3], 48)
         assert got["table"][0] == [0, -1, 1] and got["slots"] == list(range(16)) + [-1] * 16 + list(range(16, 32))
         ok(kv, sfar_where("page"))
+
+
+@pytest.mark.parametrize("B,P,W,most_add,spare", [(257, 32, 5, 3, 60), (1024, 16, 4, 30, 400), (2049, 64, 3, 100, 900), (4097, 16, 5, 2, 100),
+                                                  (8192, 16, 4, 40, 9000), (8192, 128, 2, 1, 3)])
+def test_thousands_of_requests(B, P, W, most_add, spare):
+    lens, delta, table, ring, state = draw_plan(B + P, B, P, W, most_add, spare)
+    tokens = sum(max(d, 0) for d in delta) + 1
+    _, _, kv = fresh(R=1, H=1, P=P, pages=len(ring), q_heads=1)
+    got = run_plan(kv, lens, delta, table, ring, state, tokens, in_place=B % 2 == 0)
+    want = kv_ref.plan(P, lens, delta, table, ring, state, tokens)
+    for name in want:
+        assert got[name] == want[name], name
+    ok(kv)
