@@ -373,7 +373,7 @@ sfar_status sfar_kv_attention(sfar_kv_t *h, const void *const q[], void *const o
     a.pages = (int)h->pages;
     a.window = window >= (1ull << 31) ? 0 : (int)window;
     const bool many = max_q > kFewRows / (size_t)a.G && requests <= SFAR_PROMPT_REQUESTS;
-    const int rows = many ? SFAR_PROMPT_ROWS : max_q * (size_t)a.G <= 8 ? 8 : 16;
+    const int rows = many ? SFAR_PROMPT_ROWS : max_q <= 8 / (size_t)a.G ? 8 : 16;
     // the kernels' sums over the line of (row tile, tile) are of 32 bits, its row numbers of 31
     const size_t most = tokens * (size_t)a.G / (size_t)rows + requests;
     const size_t context = table_width << h->shift, reach = context < (1ull << 31) ? context : 1ull << 31;

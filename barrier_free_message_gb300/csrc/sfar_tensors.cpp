@@ -166,8 +166,13 @@ long long number(PyObject *x)
         throw PythonError();
     return v;
 }
-// sizes; what is negative becomes a size that every call refuses
-size_t natural(PyObject *x) { return (size_t)number(x); }
+size_t natural(PyObject *x, const char *what)
+{
+    const long long v = number(x);
+    if (v < 0)
+        wrong(std::string(what) + ": must not be negative");
+    return (size_t)v;
+}
 
 template <class F> PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F body)
 {
@@ -232,13 +237,13 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n)
         const auto h = static_cast<sfar_kv_t *>(handle_of(a[0]));
         const int R = (int)number(a[1]);
         const int64_t H = number(a[2]), D = number(a[3]);
+        const size_t max_q = natural(a[9], "max_q"), window = natural(a[11], "window");
         const Ranks q(a[4], R, 3, kBf16, "q"), out(a[5], R, 3, kBf16, "out");
         const int64_t T = q.shape[0];
         if (!q.same({T, H, D}) || !out.same({T, H, D}))
             wrong("attention: need q and out of shape [tokens, " + std::to_string(H) + ", " + std::to_string(D) + "] per rank");
         const int64_t B = size(a[6], 2, 0, "table"), W = size(a[6], 2, 1, "table");
         const int32_t *table = ints(a[6], {B, W}, "table"), *lens = ints(a[7], {B}, "lens"), *starts = ints(a[8], {B + 1}, "starts");
-        const size_t max_q = natural(a[9]), window = natural(a[11]);
         const double scale = PyFloat_AsDouble(a[10]);
         if (PyErr_Occurred())
             throw PythonError();
