@@ -336,9 +336,9 @@ __global__ void __launch_bounds__(Many::kThreads, 1) __cluster_dims__(2, 1, 1)
                         gave_up = true;
                         break;
                     }
-                    const uint32_t at = ring + st.slot * F::kStage, bar = full + 8 * st.slot;
+                    const uint32_t at = ring + st.slot * F::kStage, bar = lead_full + 8 * st.slot;
                     // each CTA announces and copies its own half; the even CTA's barrier counts both
-                    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(lead_full + 8 * st.slot),
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar),
                                  "r"(F::kStage)
                                  : "memory");
                     tc::load_2d_pair(at, &a.xmap[r], b * 128, m * 256 + (int)rank * 128, bar, often);

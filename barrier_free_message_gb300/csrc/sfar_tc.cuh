@@ -126,13 +126,13 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap *map, in
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(pol)
         : "memory");
 }
-// the same by one CTA of a pair: completion is counted on `bar` of the pair's even CTA
+// the same by one CTA of a pair: completion is counted on `bar`, a shared::cluster address (mapa) in either
 __device__ __forceinline__ void load_2d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar, uint64_t pol)
 {
     asm volatile(
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
         " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(bar & 0xFEFFFFFFu), "l"(pol)
+        "l"(map), "r"(x), "r"(y), "r"(bar), "l"(pol)
         : "memory");
 }
 
