@@ -1,11 +1,14 @@
 """Build libsfar.so in-tree with nvcc for sm_103a.
 
 Each .cu file is compiled on its own (in parallel) and the objects are linked
-into ``barrier_free_message_gb300/_build/libsfar.so``.  Beside it the host
-compiler builds ``sfar_tensors.so``, the Python module that reads the torch
-tensors of the paged cache's and the 8-bit projection's calls.  A stamp of the
-sources, flags and torch's and Python's versions skips the build when nothing
-changed.
+into ``barrier_free_message_gb300/_build/libsfar.so``.  A stamp of the sources
+and flags skips the build when nothing changed.
+
+Beside it the host compiler builds ``sfar_tensors.so``, the Python module that
+reads the torch tensors of the paged cache's and the 8-bit projection's calls,
+with a stamp of its own (torch's and Python's versions too).  The library does
+not need it: where it cannot be built, without torch or a header of it, a
+warning says so and the calls that need it raise with the reason.
 """
 import concurrent.futures as cf
 import hashlib
@@ -16,6 +19,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -40,11 +44,10 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libsfar")
 
 
-def _stamp() -> str:
+def _stamp(flags: str, dirs) -> str:
     h = hashlib.sha256()
-    h.update(" ".join(NVCC_FLAGS).encode())
-    h.update(f"{importlib.metadata.version('torch')} {sys.version}".encode())
-    for d in (CSRC, INCLUDE):
+    h.update(flags.encode())
+    for d in dirs:
         for name in sorted(os.listdir(d)):
             with open(os.path.join(d, name), "rb") as f:
                 h.update(name.encode())
@@ -52,8 +55,23 @@ def _stamp() -> str:
     return h.hexdigest()
 
 
+def _stamped(out: str, stamp: str) -> bool:
+    if not (os.path.exists(out) and os.path.exists(out + ".stamp")):
+        return False
+    with open(out + ".stamp") as f:
+        return f.read() == stamp
+
+
+def _write(path: str, text: str) -> None:
+    with open(path, "w") as f:
+        f.write(text)
+
+
 def _build_tensors(cc: str) -> None:
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch is not installed")
+    torch = os.path.dirname(spec.origin)
     libs = os.path.join(torch, "lib")
     inc = [INCLUDE, os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include")]
@@ -61,20 +79,58 @@ def _build_tensors(cc: str) -> None:
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            os.path.join(CSRC, "sfar_tensors.cpp"), "-o", tmp, *["-I" + i for i in inc], "-L" + libs, "-Wl,-rpath," + libs,
            "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        raise RuntimeError(f"{cmd[0]}: {e}") from e
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on sfar_tensors.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, TENSORS)
 
 
+def tensors_error() -> str:
+    """Why the module that reads tensors is not there ("" if it is)."""
+    if os.path.exists(TENSORS):
+        return ""
+    if os.path.exists(TENSORS + ".err"):
+        with open(TENSORS + ".err") as f:
+            return f.read()
+    return "not built"
+
+
+def _tensors(force: bool) -> None:
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "none"
+    stamp = _stamp(f"{version} {sys.version}", (CSRC, INCLUDE))
+    if not force and _stamped(TENSORS, stamp):
+        return
+    for old in (TENSORS, TENSORS + ".stamp", TENSORS + ".err"):
+        if os.path.exists(old):
+            os.remove(old)                      # built from other sources
+    try:
+        _build_tensors(nvcc())
+    except RuntimeError as e:
+        _write(TENSORS + ".err", str(e))
+        warnings.warn(f"libsfar's Python calls on whole tensors are not available: {e}", RuntimeWarning, stacklevel=3)
+        return
+    _write(TENSORS + ".stamp", stamp)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
-    stamp_file = os.path.join(OUT_DIR, "stamp")
-    stamp = _stamp()
-    if not force and os.path.exists(LIB) and os.path.exists(TENSORS) and os.path.exists(stamp_file):
-        with open(stamp_file) as f:
-            if f.read() == stamp:
-                return LIB
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        tensors = ex.submit(_tensors, force)
+        _library(force, verbose)
+        tensors.result()
+    return LIB
+
+
+def _library(force: bool, verbose: bool) -> None:
+    stamp = _stamp(" ".join(NVCC_FLAGS), (CSRC, INCLUDE))
+    if not force and _stamped(LIB, stamp):
+        return
     cc = nvcc()
 
     def compile_one(src):
@@ -87,10 +143,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
-        tensors = ex.submit(_build_tensors, cc)
+    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
         results = list(ex.map(compile_one, SOURCES))
-        tensors.result()
     if verbose:
         for _, log in results:
             print(log)
@@ -100,11 +154,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    with open(stamp_file, "w") as f:
-        f.write(stamp)
-    return LIB
+    _write(LIB + ".stamp", stamp)
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))

@@ -163,7 +163,7 @@ def _tensors():
         import torch  # noqa: F401  (the libraries the module is linked with)
         L = lib()
         if not os.path.exists(_build.TENSORS):
-            raise RuntimeError(f"libsfar is not built ({_build.TENSORS} missing); run barrier_free_message_gb300._build.build()")
+            raise RuntimeError(f"{_build.TENSORS} is missing ({_build.tensors_error()}); run barrier_free_message_gb300._build.build()")
         loader = importlib.machinery.ExtensionFileLoader("sfar_tensors", _build.TENSORS)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("sfar_tensors", loader))
         loader.exec_module(module)
