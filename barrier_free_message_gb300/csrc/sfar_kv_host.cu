@@ -6,6 +6,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
+#include <memory>
 #include <new>
 
 #include "sfar.h"
@@ -49,6 +51,9 @@ const size_t kFewTokens = 128;
 // requests of 6003 to 10400 tokens 205 us that way and 354 the other; 32 rows, 32
 // such requests 211 and 191, 4 requests of 503 to 2400 26 and 33.
 const size_t kFewRows = 32;
+
+// Counters of parts: six sets of one for each of the most CTAs of any of the kernels (3 per SM).
+size_t arrived_bytes(int sms) { return 6 * 3 * (size_t)sms * sizeof(int); }
 
 struct Span {
     uintptr_t lo, hi;
@@ -167,8 +172,7 @@ sfar_kv_t *sfar_kv_create(int R, int q_heads, int kv_heads, int head_dim, int pa
             delete h;
             return fail(encode ? SFAR_ERR_INVALID : SFAR_ERR_UNSUPPORTED);
         }
-    const size_t ctas = (size_t)sms * 3;                   // the most CTAs of any of the kernels
-    const size_t o_arrived = 256, o_part = (o_arrived + 6 * ctas * 4 + 255) / 256 * 256;
+    const size_t o_arrived = 256, o_part = (o_arrived + arrived_bytes(sms) + 255) / 256 * 256;
     const size_t few = (size_t)sms * 2 * 2 * 16, many = (size_t)sms * 2 * SFAR_PROMPT_ROWS;     // rows of partial results
     const size_t bytes = o_part + (few > many ? few : many) * ((size_t)head_dim + 4) * 4;
     if (cudaMalloc(&h->ws, bytes) != cudaSuccess) {
@@ -415,10 +419,32 @@ sfar_status sfar_kv_reset(sfar_kv_t *h, sfar_stream_t s)
 {
     if (!h)
         return SFAR_ERR_INVALID;
-    if (cudaMemsetAsync(h->ctl, 0, 32, (cudaStream_t)s) != cudaSuccess) {
+    // the counters of parts too: a CTA that gave up has left them where they were
+    if (cudaMemsetAsync(h->ctl, 0, 32, (cudaStream_t)s) != cudaSuccess ||
+        cudaMemsetAsync(h->arrived, 0, arrived_bytes(h->sms), (cudaStream_t)s) != cudaSuccess) {
         cudaGetLastError();
         return SFAR_ERR_CUDA;
     }
+    return SFAR_OK;
+}
+
+sfar_status sfar_test_kv_record_failure(sfar_kv_t *h)
+{
+    if (!h)
+        return SFAR_ERR_INVALID;
+    SfarCtl c;
+    const size_t n = arrived_bytes(h->sms) / sizeof(int);
+    std::unique_ptr<int[]> ones(new (std::nothrow) int[n]);
+    if (!ones)
+        return SFAR_ERR_OOM;
+    std::fill_n(ones.get(), n, 1);
+    if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpy(&c, h->ctl, sizeof c, cudaMemcpyDeviceToHost) != cudaSuccess)
+        return SFAR_ERR_CUDA;
+    c.status = SFAR_ERR_TIMEOUT;
+    c.f_where = SFAR_WAIT_COPY;
+    if (cudaMemcpy(h->ctl, &c, sizeof c, cudaMemcpyHostToDevice) != cudaSuccess ||
+        cudaMemcpy(h->arrived, ones.get(), n * sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
+        return SFAR_ERR_CUDA;
     return SFAR_OK;
 }
 

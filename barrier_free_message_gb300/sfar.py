@@ -99,6 +99,7 @@ _SIGS = [
      [ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p]),
     ("sfar_kv_status_get", ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(SfarFault)]),
     ("sfar_kv_reset", ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
+    ("sfar_test_kv_record_failure", ctypes.c_int, [ctypes.c_void_p]),
     ("sfar_probe_empty", ctypes.c_int, [ctypes.c_void_p]),
     ("sfar_probe_pingpong", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                            ctypes.c_void_p, ctypes.c_void_p]),

@@ -151,7 +151,10 @@ sfar_status sfar_kv_attention(sfar_kv_t *kv, const void *const q[], void *const 
 /*
  * sfar_kv_status_get: SFAR_OK, or the first failure recorded on the device
  * (synchronise the calls' streams first).  It stays until sfar_kv_reset.
- * Calls go on computing after it.
+ * Calls go on computing after it, but after SFAR_ERR_TIMEOUT (a wait of an
+ * attention call that ran out after a second: where = SFAR_WAIT_COPY) the
+ * results of attention are undefined until sfar_kv_reset, which puts the
+ * handle's workspace in order too, on stream s.
  */
 sfar_status sfar_kv_status_get(sfar_kv_t *kv, sfar_fault *info);
 sfar_status sfar_kv_reset(sfar_kv_t *kv, sfar_stream_t s);

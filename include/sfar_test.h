@@ -13,6 +13,7 @@
 #define SFAR_TEST_H
 
 #include "sfar.h"
+#include "sfar_kv.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -132,6 +133,11 @@ sfar_status sfar_test_query_fused_path(sfar_t *h, size_t rows, size_t hidden, in
  * lost message, to test what callers of that entry point see afterwards.
  * Synchronous; sets the fixed array up first if no call has done so yet. */
 sfar_status sfar_test_noalloc_record_failure(int rank, int peer, int where);
+
+/* Leaves a paged cache's handle as an attention call whose wait for a copy ran
+ * out may leave it: SFAR_ERR_TIMEOUT at SFAR_WAIT_COPY in its status, and the
+ * counters of row tiles' parts not at 0.  Synchronous. */
+sfar_status sfar_test_kv_record_failure(sfar_kv_t *kv);
 
 /*
  * Latency floor probes.

@@ -21,3 +21,7 @@ def test_numbers_beyond_64_bits():
     i, bf = torch.zeros(4, dtype=torch.int32), torch.zeros(2, 4, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(OverflowError):
         sfar._tensors().attention(None, 2, 2, 64, bf, bf, i.view(2, 2), i, i, 1, 1.0, 1 << 64, 0)
+
+
+def test_no_handle():
+    assert sfar.lib().sfar_test_kv_record_failure(None) == sfar.SFAR_ERR_INVALID
