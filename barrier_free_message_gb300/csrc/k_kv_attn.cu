@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
             m = max(m, __shfl_xor_sync(SFAR_FULL, m, 1));
             m = max(m, __shfl_xor_sync(SFAR_FULL, m, 2));
             const int e = max((int)(m >> 7) - 127, -112);       // largest magnitude below 2^(e + 1)
-            const float up = sfar_exp2i(14 - e);
+            const float up = m >= 0x7f80u ? 0.f : sfar_exp2i(14 - e);        // an infinity becomes NaN: scores of -inf would count as masked
             const float mine = a.scale * 1.4426950408889634f * sfar_exp2i(max(e - 14, -126));
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {

@@ -1,8 +1,8 @@
-"""Rows of attention by both of its kernels: what other rows and masked tokens hold does not reach them."""
+"""Rows of attention by both of its kernels: what other rows and masked tokens hold does not reach them, infinities do."""
 import pytest
 import torch
 
-from kv_rows import cache
+from kv_rows import cache, check, offsets
 from test_gpu_kv import _built, run_attention  # noqa: F401  (a fixture)
 
 pytestmark = pytest.mark.gpu
@@ -44,3 +44,24 @@ def test_a_row_does_not_depend_on_tokens_it_does_not_see(form, D, P):
             changed[3][0, table[0][i]] = -louder
         got = run_attention(changed, table, [n], [0, count], q, G, D ** -0.5, max_q=form)
         assert torch.equal(got[:, :row + 1], whole[:, :row + 1]), row
+
+
+@pytest.mark.parametrize("form", [FEW, MANY])
+def test_infinite_and_nan_queries(form):
+    """Such a row is NaN (its largest score is infinite, or none), whatever the signs; the others are as they were."""
+    G, D, n = 4, 64, 200
+    cpu, table = cache(1, 1, D, 16, [n], lambda b, i: 0.01, lambda b, i: 0.01, 35)
+    k = cpu[0].view(torch.uint8)
+    k[0, table[0], 0, :, 3] = (k[0, table[0], 0, :, 3] & 0x7f) | 0x80         # negative in every token
+    k[0, table[0], 0, :, 3] = torch.where(k[0, table[0], 0, :, 3] == 0x80, 0x81, k[0, table[0], 0, :, 3])
+    q = (torch.randn(1, 2, G, D, generator=torch.Generator().manual_seed(36)) * 1.5).to(torch.bfloat16)
+    for value in (float("inf"), float("-inf"), float("nan")):
+        bad = q.clone()
+        bad[0, 0, 1, 3] = value
+        bad[0, 1, 2, 40] = value
+        got = run_attention(cpu, table, [n], [0, 2], bad, G, 0.125, max_q=form)
+        assert torch.isnan(got[0, 0, 1]).all() and torch.isnan(got[0, 1, 2]).all()
+        got[0, 0, 1] = got[0, 1, 2] = 0
+        clean = run_attention(cpu, table, [n], [0, 2], q, G, 0.125, max_q=form)
+        clean[0, 0, 1] = clean[0, 1, 2] = 0
+        assert torch.equal(got, clean)
