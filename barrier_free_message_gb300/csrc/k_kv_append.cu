@@ -26,6 +26,29 @@
 #include "sfar_kv_args.h"
 #include "sfar_kv_device.cuh"
 
+namespace {
+
+// Sixteen e4m3, each by `how`.
+template <class F> __device__ __forceinline__ uint4 times(uint4 w, F how)
+{
+    uint32_t *p = &w.x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 lo = e4m3x2_to_float2(p[j]), hi = e4m3x2_to_float2(p[j] >> 16);
+        p[j] = cvt_e4m3x2(how(lo.x), how(lo.y)) | cvt_e4m3x2(how(hi.x), how(hi.y)) << 16;
+    }
+    return w;
+}
+// by a ratio that is no power of two: products of more than 24 bits
+__device__ __noinline__ uint4 times_any(uint4 w, float ratio)
+{
+    return times(w, [&](float v) { return sfar_to_odd(v * ratio, fmaf(v, ratio, -(v * ratio))); });
+}
+// A vector of a run whose scale is no power of two: out of line, so that the common path's code is short.
+__device__ __noinline__ uint2 quantize8_by_any(uint4 v, float scale, bool special) { return sfar_quantize8(v, SfarInv(scale), special); }
+
+}  // namespace
+
 // Keep: vectors a lane holds between the maximum and the stores; Team: warps to
 // a run; Whole: a page has no more than Keep * Team * 32 vectors.
 template <int D, int Keep, int Team, bool Whole>
@@ -174,18 +197,16 @@ __global__ void __launch_bounds__(32 * SFAR_APPEND_WARPS, Keep > 8 ? 2 : Whole ?
         if (lane == 0 && member == 0)
             scales[at] = scale;
         if (first && scale > old) {
-            const float ratio = __fdiv_rn(old, scale);
+            const float ratio = __fdiv_rn(old, scale);       // exact: the new one is a power of two
             uint4 *held = reinterpret_cast<uint4 *>(base);
+            if (SfarInv(ratio).pow2) {
 #pragma unroll 4
-            for (int i = lane + 32 * member; i < first * (D / 16); i += 32 * Team) {
-                uint4 w = held[i];
-                uint32_t *p = &w.x;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 lo = e4m3x2_to_float2(p[j]), hi = e4m3x2_to_float2(p[j] >> 16);
-                    p[j] = cvt_e4m3x2(lo.x * ratio, lo.y * ratio) | cvt_e4m3x2(hi.x * ratio, hi.y * ratio) << 16;
-                }
-                held[i] = w;
+                for (int i = lane + 32 * member; i < first * (D / 16); i += 32 * Team)
+                    held[i] = times(held[i], [&](float v) { return v * ratio; });
+            } else {
+#pragma unroll 1
+                for (int i = lane + 32 * member; i < first * (D / 16); i += 32 * Team)
+                    held[i] = times_any(held[i], ratio);
             }
         }
         const SfarInv by(scale);
@@ -193,7 +214,7 @@ __global__ void __launch_bounds__(32 * SFAR_APPEND_WARPS, Keep > 8 ? 2 : Whole ?
         auto store = [&](auto how) {
             auto one = [&](int i, const uint4 &v) {
                 if (holds(i)) {
-                    const uint2 q = sfar_quantize8(v, how, special);
+                    const uint2 q = how(v);
                     st_v2u32(dst + i * (kTok * Team * D), q.x, q.y);
                 }
             };
@@ -203,9 +224,9 @@ __global__ void __launch_bounds__(32 * SFAR_APPEND_WARPS, Keep > 8 ? 2 : Whole ?
             rest(one);
         };
         if (by.pow2)
-            store(by.inv);
+            store([&](const uint4 &v) { return sfar_quantize8(v, by.inv, special); });
         else
-            store(by);
+            store([&](const uint4 &v) { return quantize8_by_any(v, scale, special); });
     }
 }
 

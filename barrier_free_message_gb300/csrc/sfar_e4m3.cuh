@@ -44,8 +44,22 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t v)
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
+// The binary32 result y of an operation, given what the exact result has beyond it (its sign): of the two binary32 values
+// around the exact one, that with an odd significand, so that a second rounding to far fewer bits goes as a single one would.
+__device__ __forceinline__ float sfar_to_odd(float y, float beyond)
+{
+    uint32_t b = __float_as_uint(y);
+    if (beyond < 0.f || beyond > 0.f) {
+        if ((__float_as_uint(beyond) ^ b) >> 31)
+            --b;                           // towards zero: y is beyond the exact result, and so not 0
+        b |= 1u;
+    }
+    return __uint_as_float(b);
+}
+
 // How x / scale is formed for a scale: a product with the exact reciprocal of
-// a power of two, a division otherwise (a scale that the caller brought).
+// a power of two, a division otherwise (a scale > 0 that the caller brought),
+// rounded to odd.
 struct SfarInv {
     float s, inv;
     bool pow2;
@@ -56,7 +70,13 @@ struct SfarInv {
         pow2 = (b & 0x7fffffu) == 0 && e >= -126 && e <= 126;
         inv = pow2 ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
     }
-    __device__ __forceinline__ float operator()(float x) const { return pow2 ? x * inv : __fdiv_rn(x, s); }
+    __device__ __forceinline__ float operator()(float x) const
+    {
+        if (pow2)
+            return x * inv;
+        const float y = __fdiv_rn(x, s);
+        return sfar_to_odd(y, fmaf(-y, s, x));
+    }
 };
 
 __device__ __forceinline__ float sfar_times(float by, float x) { return by * x; }
