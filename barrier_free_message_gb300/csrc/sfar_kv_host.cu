@@ -336,6 +336,15 @@ sfar_status sfar_kv_attention(sfar_kv_t *h, const void *const q[], void *const o
         return SFAR_ERR_INVALID;
     if (tokens == 0)
         return SFAR_OK;
+    // rows of out that share memory
+    const size_t row = (size_t)h->D;
+    if ((tokens > 1 && out_token_stride < row) || (h->Hq > 1 && out_head_stride < row) ||
+        (tokens > 1 && h->Hq > 1 && out_token_stride == out_head_stride))
+        return SFAR_ERR_INVALID;
+    for (int i = 1; i < h->R; ++i)
+        for (int j = 0; j < i; ++j)
+            if (out[i] == out[j])
+                return SFAR_ERR_INVALID;
     SfarAttnArgs a;
     memcpy(a.kmap, h->map[0], sizeof a.kmap);
     memcpy(a.vmap, h->map[1], sizeof a.vmap);

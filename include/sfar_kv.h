@@ -136,7 +136,7 @@ sfar_status sfar_kv_append(sfar_kv_t *kv, const void *const k[], const void *con
  * part of the sum of the exponentials.
  * max_q: the most new tokens any request has in this call (a hint that picks
  * the kernel; a request that has more is still computed).  out overlaps no
- * other argument.  1 <= requests <= SFAR_KV_MAX_REQUESTS; tokens, table_width
+ * other argument, no row of it another, and the ranks' arrays not one another.  1 <= requests <= SFAR_KV_MAX_REQUESTS; tokens, table_width
  * < 2^31; strides below 2^40; scale finite and at least 0.  The kernels count
  * in 32 bits: with G = q_heads / kv_heads, tokens * G is below 2^29 and the
  * product of tokens * G / n + requests (row tiles) and table_width *
