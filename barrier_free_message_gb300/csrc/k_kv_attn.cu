@@ -117,8 +117,7 @@ template <int kRows> struct Work {
     // tiles that some row of the request attends to (at least one: rows of nothing are written too)
     __device__ __forceinline__ void range(int len, int count, int &begin, int &all) const
     {
-        const int pos = max(0, len - count);
-        begin = (a.window ? max(0, pos - a.window + 1) : 0) / kTile;
+        begin = sfar_attn_from(a, len - count) / kTile;
         all = max(1, (len + kTile - 1) / kTile - begin);
     }
     __device__ __forceinline__ Piece at(long long u, long long end) const
@@ -397,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
                 const int rho = 8 * i + 2 * t + y, pos = p.len - p.count + (p.rt * kRows + rho) / a.G;
                 f[i][y] = __shfl_sync(SFAR_FULL, mine, 4 * (2 * t + y));
                 hi[i][y] = rho < rows ? pos + 1 : INT_MAX;
-                lo[i][y] = rho < rows && a.window ? max(0, pos - a.window + 1) : 0;
+                lo[i][y] = rho < rows ? sfar_attn_from(a, pos) : 0;
             }
         }
         __syncwarp();
@@ -406,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
         qs.next();
         // tiles that every row sees whole
         const int pos0 = p.len - p.count + p.rt * kRows / a.G, pos1 = p.len - p.count + (p.rt * kRows + rows - 1) / a.G;
-        const int all_from = a.window ? max(0, pos1 - a.window + 1) : 0, all_to = pos0 + 1;
+        const int all_from = sfar_attn_from(a, pos1), all_to = pos0 + 1;
 
         float o[RH][D / 16][4] = {};               // o[i][n][2 h + y]: row 8 i + 2 t + y, element (D / 8) g + 2 n + h
         // log2 references: of the scores (sum), of the weights (o)
@@ -606,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, RH == 1 ? 3 : 2) k_kv_attn(const __g
         const int *nan = s_nan[piece++ & 1];
         if (nan[1] >= 0 && row < rows) {
             const int n = p.rt * kRows + row, pos = p.len - p.count + n / a.G;
-            const int from = max(max(nan[0], p.tile0 * kTile), a.window ? pos - a.window + 1 : 0);
+            const int from = max(max(nan[0], p.tile0 * kTile), sfar_attn_from(a, pos));
             const int to = min(min(nan[1], pos), (p.tile0 + p.tiles) * kTile - 1);
             for (int j = from; j <= to; ++j) {
                 const int page = a.table[(size_t)p.b * a.W + (j >> a.shift)];

@@ -104,7 +104,7 @@ struct Work {
     {
         const int i0 = rt * kRows / a.G, i1 = min(count - 1, (rt * kRows + kRows - 1) / a.G);
         const int pos0 = len - count + i0, pos1 = len - count + i1;
-        begin = (a.window ? max(0, pos0 - a.window + 1) : 0) / kTile;
+        begin = sfar_attn_from(a, pos0) / kTile;
         all = max(1, (max(0, pos1 + 1) + kTile - 1) / kTile - begin);
     }
     __device__ __forceinline__ int row_tiles(int count) const { return (int)(((long long)count * a.G + kRows - 1) / kRows); }
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             const bool row = lrow < rows_of(p);
             const int tok = n / a.G;
             const int pos = p.len - p.count + tok;
-            const int hi = row ? min(p.len, pos + 1) : INT_MAX, lo = row && a.window ? max(0, pos - a.window + 1) : 0;
+            const int hi = row ? min(p.len, pos + 1) : INT_MAX, lo = row ? sfar_attn_from(a, pos) : 0;
             // tiles that every row of this warp sees whole
             const int all_from = __reduce_max_sync(SFAR_FULL, lo), all_to = min(p.len, __reduce_min_sync(SFAR_FULL, hi));
             // log2 reference of the row's weights; sum: of this half's weight / value scale
@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                 // tiles that every row of the piece sees whole
                 const int pos0 = p.len - p.count + p.rt * kRows / a.G;
                 const int pos1 = p.len - p.count + min(p.count - 1, (p.rt * kRows + kRows - 1) / a.G);
-                const int all_from = a.window ? max(0, pos1 - a.window + 1) : 0, all_to = min(p.len, pos0 + 1);
+                const int all_from = sfar_attn_from(a, pos1), all_to = min(p.len, pos0 + 1);
                 for (int k = 0; k < p.tiles; ++k) {
                     const int j0 = (p.tile0 + k) * kTile;
                     dead = dead || !tc::bar_wait(bar(kMFull + ms.slot), ms.phase, limit);

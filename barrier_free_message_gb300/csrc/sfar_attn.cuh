@@ -35,6 +35,11 @@ __device__ __forceinline__ long long sfar_div(long long a, long long b)
 {
     return (a | b) >> 32 == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
+// The first token that position `pos` attends to (below 0: a row of nothing, for which a window near 2^31 would wrap).
+__device__ __forceinline__ int sfar_attn_from(const SfarAttnArgs &a, int pos)
+{
+    return a.window ? max(0, max(pos, -1) - a.window + 1) : 0;
+}
 // Request b: its context, how many new tokens it has and the row of the first.
 __device__ __forceinline__ void sfar_attn_request(const SfarAttnArgs &a, int b, int &len, int &count, int &first)
 {
