@@ -269,9 +269,11 @@ sfar_status sfar_kv_plan(sfar_kv_t *h, const int32_t *lens, const int32_t *delta
         return SFAR_ERR_INVALID;
     SfarKvPlanArgs a{lens,  delta, table,  ring,          state,            lens_out,    state_out, starts,
                      slots, taken, h->ctl, (int)requests, (int)table_width, (int)tokens, h->shift,  (int)h->pages};
-    // Small steps need no more than a warp's worth of sums per scheduler, large ones all the CTAs that a cluster can have:
-    // their time is that of the instructions of the slots and pages (2039 requests with 62 k tokens: 13.5 us on 8 SMs, 11.1 on 16, with the page lists of that time).
-    const bool small = requests <= 256 && tokens <= 8192;
+    // Small steps run on 8 CTAs of 256 threads, a request to a thread; large ones on all the CTAs that a cluster can have, of
+    // 1024: their time is that of the instructions of the slots and pages.  Small and large form, us: requests of one token,
+    // 64: 3.2, 4.0; 256: 3.5, 4.2; 257: 4.2, 4.2; 512: 4.6, 4.6; 1024: 6.3, 5.4; 8192: 32, 18.  16 requests with 1412 tokens
+    // 4.5, 4.7; 128 with 2533 4.6, 4.9; 256 with 1767 5.7, 4.9, with 3088 4.9, 4.8, with 7118 6.6, 4.9; 64 with 7156 4.6, 4.6.
+    const bool small = requests <= 256 && tokens <= 4096;
     const unsigned cluster = small ? SFAR_PLAN_CLUSTER : h->plan_ctas;
     return launch(h->dev, sfar_kernel_kv_plan(), dim3(cluster), small ? 256 : SFAR_PLAN_THREADS, (4 * requests + 1) * 4, &a, s, false, cluster);
 }
