@@ -255,7 +255,9 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
-size_t padded(int64_t k) { return (size_t)(k + 15) / 16 * 16; }        // the row stride of a single row, which has none
+// The row stride of a matrix of rows of k.  A single row has none, and gets one that every call takes; that of an expanded
+// matrix, 0, is passed on and refused.
+size_t row_stride(const Ranks &x) { return x.shape[0] == 1 ? (size_t)(x.shape[1] + 15) / 16 * 16 : (size_t)x.stride[0]; }
 
 // (handle, R, x, x8, sx, stream)
 PyObject *quantize(PyObject *, PyObject *const *a, Py_ssize_t n)
@@ -270,7 +272,7 @@ PyObject *quantize(PyObject *, PyObject *const *a, Py_ssize_t n)
         const sfar_stream_t s = stream_of(a[5]);
         return released([&] {
             return c_quantize(h, x.ptr, const_cast<void *const *>(x8.ptr), reinterpret_cast<float *const *>(sx.ptr), m, k,
-                              x.stride[0] ? (size_t)x.stride[0] : padded(k), x8.stride[0] ? (size_t)x8.stride[0] : padded(k), s);
+                              row_stride(x), row_stride(x8), s);
         });
     });
 }
@@ -290,8 +292,7 @@ PyObject *gemm(PyObject *, PyObject *const *a, Py_ssize_t n)
         const sfar_stream_t s = stream_of(a[7]);
         return released([&] {
             return c_gemm(h, x8.ptr, reinterpret_cast<const float *const *>(sx.ptr), w8.ptr, reinterpret_cast<const float *const *>(sw.ptr),
-                          const_cast<void *const *>(y.ptr), m, k, N, x8.stride[0] ? (size_t)x8.stride[0] : padded(k),
-                          w8.stride[0] ? (size_t)w8.stride[0] : padded(k), s);
+                          const_cast<void *const *>(y.ptr), m, k, N, row_stride(x8), row_stride(w8), s);
         });
     });
 }
