@@ -15,12 +15,13 @@
 //    is read once, and a short page holds no registers it does not use.
 //  few tokens: windows of one token, so that a decode step has a warp per token
 //    and plane in flight, 8 vectors kept per lane; what a longer run has beyond
-//    is read twice, in batches.
+//    is read twice, in batches (80 registers, 80 bytes of them spilled: three
+//    CTAs per SM).
 //
 // Measured: 4 ranks of two heads of 128, pages of 32, 9 prompts of 1501 to 2139
-// tokens (102 MB) 20.8 us, 4.9 TB/s; 8 ranks, 16 prompts of 500 to 1000: 4.4
+// tokens (102 MB) 20.9 us, 4.9 TB/s; 8 ranks, 16 prompts of 500 to 1000: 4.4
 // TB/s with pages of 64 and 4.8 with 16 (3.2 and 3.6 with one warp and 16
-// vectors for every page); 64 single tokens 2.5 us; 128 single tokens of 8 ranks
+// vectors for every page); 64 single tokens 2.7 us; 128 single tokens of 8 ranks
 // of four heads 6.3 us (in windows of two tokens 8.9).
 #include "sfar_e4m3.cuh"
 #include "sfar_kv_args.h"

@@ -40,12 +40,13 @@
 // tiles hide a CTA's first page lookups and its joins.
 //
 // Measured: 8 ranks, one key head of 128, 8 query heads: 64 requests of 6003 to
-// 10400 tokens, 1.08 GB in 161 us, 6.7 TB/s or 0.99 of a copy's rate; 16
+// 10400 tokens, 1.08 GB in 162 us, 6.7 TB/s or 0.98 of a copy's rate; 16
 // requests of 301 to 4096, 72 MB in 22 us, of which about 8 pass outside the
 // stream of tiles (launch, prefix sums and first page lookups, partial results
 // and their join, unequal ends).  4 ranks of two key heads with 5 query heads
 // each, one context of 131071 tokens: 269 MB in 49 us, 5.5 TB/s.  99 tokens of
-// one request: 5.8 us, the latency of the chain; 2112 row tiles of 5 tokens 24.
+// one request: 5.9 us, the latency of the chain; 2112 row tiles of 5 tokens 24.
+// 8 rows fit 128 registers; 16 rows of 128 elements spill 44 bytes at 168.
 #include "sfar_e4m3.cuh"
 #include "sfar_attn.cuh"
 #include "sfar_tc.cuh"

@@ -14,8 +14,8 @@
 // CTAs exchange nothing, and takes its share of the outputs.  The one cluster
 // barrier, between the reads of the lengths and the ring's state and the
 // writes of the new ones, lets both be updated in place.  Measured: 256
-// requests of one new token each 3.2 us (4.7 with four slots to every thread),
-// 2039 requests of mixed changes (0 to 61 new tokens, every 7th leaving) 9.7.
+// requests of one new token each 3.3 us (4.7 with four slots to every thread),
+// 2039 requests of mixed changes (0 to 61 new tokens, every 7th leaving) 9.6.
 #include <cooperative_groups.h>
 
 #include "sfar_kv_args.h"

@@ -32,13 +32,14 @@
 // are joined by the last of their CTAs, in order.
 //
 // Measured, 8 ranks of 8 query heads and one key head of 128, three chunks of
-// 700 to 1024 new tokens at the ends of contexts of 1100 to 4099: 203 us, 1080
-// TFLOP/s, 0.55 of a bf16 product's rate; the tensor core is busy 0.49 of the
+// 700 to 1024 new tokens at the ends of contexts of 1100 to 4099: 204 us, 1075
+// TFLOP/s, 0.54 of a bf16 product's rate; the tensor core is busy 0.49 of the
 // time.  A tile's chain is what bounds it: about 2000 clocks from scores to
 // weights (maxima 400, the warps' agreement on the reference 300, exponentials
 // 930, masks and stores the rest) against 1088 of products, which two tiles in
 // flight only just cover.  One thread per row took 288 us, scores kept in
-// registers over the agreement spilled and took 771.
+// registers over the agreement spilled and took 771 (what is left spills 24 to 32
+// bytes of 96 registers a thread).
 #include "sfar_e4m3.cuh"
 #include "sfar_attn.cuh"
 #include "sfar_tc.cuh"

@@ -47,9 +47,17 @@ const size_t kFewTokens = 128;
 
 // Up to this many query rows (new tokens x query heads per key head) of the
 // longest request the attention runs 8 or 16 rows at a time (every 16 rows read
-// the cache once), beyond it 256.  8 ranks, one key head of 128: 16 rows, 64
-// requests of 6003 to 10400 tokens 205 us that way and 354 the other; 32 rows, 32
-// such requests 211 and 191, 4 requests of 503 to 2400 26 and 33.
+// the cache once), beyond it 256.  The host does not know the contexts' lengths,
+// on which it depends between 17 and 48 rows which is faster.  us that way and
+// the other, 8 ranks, one key head of 128 (64), requests of so many tokens each:
+//   rows  requests x tokens:  4 x 1000     16 x 1000    64 x 1000    64 x 3000      64 x 10000
+//   32, 8 query heads of 128  17.1, 21.6   29.5, 32.1   78.1, 84.8   166.5, 161.4   480, 434
+//   48                        22.9, 22.1   39.2, 33.3  106.6, 85.7   239, 162       709, 436
+//   24, 4 query heads of 64   10.9, 17.8   21.2, 25.7   60.3, 70.3   150, 143       467, 405
+//   32                        13.5, 17.8   26.7, 25.9   76.9, 70.1   196, 143       622, 406
+// so up to 32 rows the first is ahead for contexts of about 1000 tokens and less
+// and behind for long ones.  16 rows read the cache once: 32 requests of 6003 to
+// 10400 tokens 111 and 192.
 const size_t kFewRows = 32;
 
 // Counters of parts: six sets of one for each of the most CTAs of any of the kernels (3 per SM).

@@ -127,17 +127,21 @@ sfar_status sfar_kv_append(sfar_kv_t *kv, const void *const k[], const void *con
  * (and a row past starts[requests]) is zeros.  The largest score and the sum
  * of the exponentials are held in binary32, as are the products' sums; a
  * weight (exponential times value scale) is rounded to 11 bits, and to a
- * multiple of 2^-32 of the row's largest where that is coarser; the
- * result does not depend on what the other rows or masked tokens hold.  A
- * page's scales may be zero, and negative.  A value scale of magnitude 2^-100
+ * multiple of 2^-32 of the row's largest where that is coarser.  A query's
+ * elements are taken exactly down to 2^-29 of its row's largest (2^-9 by the
+ * kernel for many rows, see max_q), smaller ones to within 2^-39 (2^-17) of
+ * that.  The result does not depend on what the other rows or masked tokens
+ * hold; a row with an infinity or NaN among its queries, or among what it
+ * attends to (NaN, cached), is NaN there.  A page's scales may be zero, and negative.  A value scale of magnitude 2^-100
  * or less counts as zero (2^-100 is what sfar_kv_append gives to zeros); the
  * others of one request's context are at most 2^100 and within a factor of
  * 2^100 of one another: beyond it tokens with the smaller scales lose their
  * part of the sum of the exponentials.
  * max_q: the most new tokens any request has in this call (a hint that picks
  * the kernel; a request that has more is still computed).  out overlaps no
- * other argument, no row of it another, and the ranks' arrays not one another.  1 <= requests <= SFAR_KV_MAX_REQUESTS; tokens, table_width
- * < 2^31; strides below 2^40; scale finite and at least 0.  The kernels count
+ * other argument, no row of it another, and the ranks' arrays not one another.
+ * 1 <= requests <= SFAR_KV_MAX_REQUESTS; tokens, table_width < 2^31; strides
+ * below 2^40; scale finite and at least 0.  The kernels count
  * in 32 bits: with G = q_heads / kv_heads, tokens * G is below 2^29 and the
  * product of tokens * G / n + requests (row tiles) and table_width *
  * page_tokens / m + 8 (tiles of a context) below 2^32, where n = 256, m = 128,
