@@ -38,7 +38,7 @@
 // weights (maxima 400, the warps' agreement on the reference 300, exponentials
 // 930, masks and stores the rest) against 1088 of products, which two tiles in
 // flight only just cover.  One thread per row took 288 us, scores kept in
-// registers over the agreement spilled and took 771 (what is left spills 24 to 32
+// registers over the agreement spilled and took 771 (what is left spills 20 to 24
 // bytes of 96 registers a thread).
 #include "sfar_e4m3.cuh"
 #include "sfar_attn.cuh"
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
             const int all_from = __reduce_max_sync(SFAR_FULL, lo), all_to = min(p.len, __reduce_min_sync(SFAR_FULL, hi));
             // log2 reference of the row's weights; sum: of this half's weight / value scale
             float wtop = -INFINITY, sum = 0.f;
-            bool zeros = false;                    // told(0), told(2): reference and sum of the tokens of value scale 0
+            float zt = -INFINITY, zs = 0.f;        // reference and sum of this half's tokens of value scale 0
             const int tiles = p.tiles, j00 = p.tile0 * kTile + 64 * half;
             for (int k = 0; mine && k < tiles; ++k) {
                 const int j0 = j00 + k * kTile;
@@ -454,12 +454,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                 if (edge) {
                     // -inf where the row does not see the token, the other sign where the key scale is negative, and put back (so
                     // that what is seen is rounded as in a tile without masks); tokens of value scale 0 are summed
-                    float zt = -INFINITY, zs = 0.f;
-                    if (odd & 0xff0000u) {
-                        pair_sync(pair);           // the other half has read what the places held before
-                        if (zeros)
-                            zt = told(0), zs = told(2);
-                    }
 #pragma unroll 1
                     for (int i = 0; i < 64; i += 16) {
                         uint32_t v[16];
@@ -482,11 +476,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                         }
                     }
                     tc::wait_st();
-                    if (odd & 0xff0000u) {
-                        zeros = true;
-                        told(0) = zt;
-                        told(2) = zs;
-                    }
                 }
                 float now;
                 {
@@ -555,32 +544,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                 if (have && rows_of(s_piece[next_at]) > 0)
                     fetch(s_piece[next_at]);
             }
-            // what the sum is relative to; with tokens of value scale 0, both sums at one reference
-            float top = wtop + kSumUp;
-            if (zeros) {
-                const float zt = told(0), zs = told(2), at = fmaxf(top, zt);
-                sum = (top == -INFINITY ? sum : ex2(top - at) * sum) + (zt == -INFINITY ? zs : ex2(zt - at) * zs);
-                top = at;
-            }
+            // both sums at one reference
+            float top = fmaxf(wtop + kSumUp, zt);
+            sum = (wtop == -INFINITY ? sum : ex2(wtop + kSumUp - top) * sum) + (zt == -INFINITY ? zs : ex2(zt - top) * zs);
             // the next queries first, so that their first scores are formed while this piece is written out
             float fnext = 0.f;
             if (have && rows_of(s_piece[next_at]) > 0)
                 fnext = split();
             // --------------------------------------------------------- epilogue
             if (mine) {
-                if (zeros) {
-                    pair_sync(pair);               // the last move's exchange has been read
-                    told(1) = top;
-                }
+                pair_sync(pair);                   // the last move's exchange has been read
+                told(1) = top;
                 told(2) = sum;
                 pair_sync(pair);
-                if (zeros) {
-                    const float at = fmaxf(top, other(1));
-                    sum = (top == -INFINITY ? sum : ex2(top - at) * sum) + (other(1) == -INFINITY ? other(2) : ex2(other(1) - at) * other(2));
-                    top = at;
-                } else {
-                    sum += other(2);
-                }
+                const float at = fmaxf(top, other(1));
+                sum = (top == -INFINITY ? sum : ex2(top - at) * sum) + (other(1) == -INFINITY ? other(2) : ex2(other(1) - at) * other(2));
+                top = at;
                 dead = dead || !tc::bar_wait(bar(kOFull + x), ophase, limit);
                 ophase ^= 1u;
                 tc::fence_after();
