@@ -32,13 +32,13 @@
 // are joined by the last of their CTAs, in order.
 //
 // Measured, 8 ranks of 8 query heads and one key head of 128, three chunks of
-// 700 to 1024 new tokens at the ends of contexts of 1100 to 4099: 204 us, 1075
-// TFLOP/s, 0.54 of a bf16 product's rate; the tensor core is busy 0.49 of the
+// 700 to 1024 new tokens at the ends of contexts of 1100 to 4099: 203 us, 1080
+// TFLOP/s, 0.55 of a bf16 product's rate; the tensor core is busy 0.49 of the
 // time.  A tile's chain is what bounds it: about 2000 clocks from scores to
 // weights (maxima 400, the warps' agreement on the reference 300, exponentials
 // 930, masks and stores the rest) against 1088 of products, which two tiles in
 // flight only just cover.  One thread per row took 288 us, scores kept in
-// registers over the agreement spilled and took 771 (what is left spills 20 to 24
+// registers over the agreement spilled and took 771 (what is left spills 8 to 12
 // bytes of 96 registers a thread).
 #include "sfar_e4m3.cuh"
 #include "sfar_attn.cuh"
@@ -452,30 +452,48 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                         fetch(s_piece[next_at]);
                 }
                 if (edge) {
-                    // -inf where the row does not see the token, the other sign where the key scale is negative, and put back (so
-                    // that what is seen is rounded as in a tile without masks); tokens of value scale 0 are summed
+                    // -inf where the row does not see the token (products, not scores, so that what is seen is rounded as in a
+                    // tile without masks)
 #pragma unroll 1
                     for (int i = 0; i < 64; i += 16) {
                         uint32_t v[16];
                         tc::ld16(v, tS + i);
                         tc::wait_ld(v);
-                        const float scale = m.ks[4 * half + (i >> 4)];
-                        const uint32_t sign = scale < 0.f ? 0x80000000u : 0u;
                         const int from = none >> (i >> 4) & 1 ? 64 : lo - j0 - i, to = min(hi, p.len) - j0 - i;
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            v[e] = e >= from && e < to ? v[e] ^ sign : __float_as_uint(-INFINITY);
+                            v[e] = e >= from && e < to ? v[e] : __float_as_uint(-INFINITY);
                         tc::st16(tS + i, v);
-                        if (odd >> (16 + 4 * half + (i >> 4)) & 1) {
-                            const float by = score_scale(f, scale), next = fmaxf(zt, max16(v) * by), ref = next == -INFINITY ? 0.f : next;
-                            zs *= zt == -INFINITY ? 1.f : ex2(zt - next);
-                            zt = next;
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                zs += ex2(fmaf(__uint_as_float(v[e]), by, -ref));
-                        }
                     }
                     tc::wait_st();
+                    if (odd & 0xff0100u) {
+                        // rare, and in a loop of its own: the other sign where a key scale is negative, sums where a value scale is 0
+#pragma unroll 1
+                        for (int i = 0; i < 4; ++i) {
+                            const float scale = m.ks[4 * half + i];
+                            const bool zero = odd >> (16 + 4 * half + i) & 1;
+                            if (!zero && !(scale < 0.f))
+                                continue;
+                            uint32_t v[16];
+                            tc::ld16(v, tS + 16 * i);
+                            tc::wait_ld(v);
+                            if (scale < 0.f) {
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    v[e] ^= v[e] == __float_as_uint(-INFINITY) ? 0u : 0x80000000u;
+                                tc::st16(tS + 16 * i, v);
+                            }
+                            if (zero) {
+                                const float by = score_scale(f, scale), next = fmaxf(zt, max16(v) * by), ref = next == -INFINITY ? 0.f : next;
+                                zs *= zt == -INFINITY ? 1.f : ex2(zt - next);
+                                zt = next;
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    zs += ex2(fmaf(__uint_as_float(v[e]), by, -ref));
+                            }
+                        }
+                        tc::wait_st();
+                    }
                 }
                 float now;
                 {
@@ -871,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const __grid_constant
                     if (sixteen) {
                         m.ks[lane] = k16;
                         m.lvs[lane] = nil ? -INFINITY : lg2(fabsf(v16));
-                        m.ivs[lane] = nil ? 0.f : kSumDown / fabsf(v16);
+                        m.ivs[lane] = nil ? 0.f : kSumDown * (1.f / fabsf(v16));
                     }
                     if (lane == 0)
                         m.odd = none | (negative ? 256u : 0u) | zero << 16 | minus << 24;
