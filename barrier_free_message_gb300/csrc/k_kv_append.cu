@@ -15,13 +15,13 @@
 //    is read once, and a short page holds no registers it does not use.
 //  few tokens: windows of one token, so that a decode step has a warp per token
 //    and plane in flight, 8 vectors kept per lane; what a longer run has beyond
-//    is read twice, in batches (80 registers, 80 bytes of them spilled: three
+//    is read twice, in batches (80 registers, 52 bytes of them spilled: three
 //    CTAs per SM).
 //
 // Measured: 4 ranks of two heads of 128, pages of 32, 9 prompts of 1501 to 2139
 // tokens (102 MB) 20.9 us, 4.9 TB/s; 8 ranks, 16 prompts of 500 to 1000: 4.4
 // TB/s with pages of 64 and 4.8 with 16 (3.2 and 3.6 with one warp and 16
-// vectors for every page); 64 single tokens 2.7 us; 128 single tokens of 8 ranks
+// vectors for every page); 64 single tokens 2.4 us; 128 single tokens of 8 ranks
 // of four heads 6.3 us (in windows of two tokens 8.9).
 #include "sfar_e4m3.cuh"
 #include "sfar_kv_args.h"
@@ -40,13 +40,27 @@ template <class F> __device__ __forceinline__ uint4 times(uint4 w, F how)
     }
     return w;
 }
-// by a ratio that is no power of two: products of more than 24 bits
-__device__ __noinline__ uint4 times_any(uint4 w, float ratio)
+// A run beside a scale that is no power of two (the caller's): what the kernel does with the others, its values read again.
+// Held values take products of more than 24 bits, new ones a division, both rounded to odd.  Out of line: inside, its code
+// and registers cost a decode step of 64 tokens 0.3 us of 2.4.
+template <int D>
+__device__ __noinline__ void append_any(const uint16_t *x, long long ts, uint8_t *page, int first, int n, float old, float scale, bool special,
+                                        int member, int team)
 {
-    return times(w, [&](float v) { return sfar_to_odd(v * ratio, fmaf(v, ratio, -(v * ratio))); });
+    constexpr int kVec = D / 8, kTok = 32 / kVec;
+    const int lane = threadIdx.x & 31;
+    if (first && scale > old) {
+        const float ratio = __fdiv_rn(old, scale);           // exact: the new scale is a power of two
+        uint4 *held = reinterpret_cast<uint4 *>(page);
+        for (int i = lane + 32 * member; i < first * (D / 16); i += 32 * team)
+            held[i] = times(held[i], [&](float v) { return sfar_to_odd(v * ratio, fmaf(v, ratio, -(v * ratio))); });
+    }
+    const SfarInv by(scale);
+    for (int t = member * kTok + lane / kVec; t < n; t += kTok * team) {
+        const uint2 q = sfar_quantize8(ld_nc_v4(x + t * ts + (lane % kVec) * 8), by, special);
+        st_v2u32(page + (first + t) * D + (lane % kVec) * 8, q.x, q.y);
+    }
 }
-// A vector of a run whose scale is no power of two: out of line, so that the common path's code is short.
-__device__ __noinline__ uint2 quantize8_by_any(uint4 v, float scale, bool special) { return sfar_quantize8(v, SfarInv(scale), special); }
 
 }  // namespace
 
@@ -197,37 +211,30 @@ __global__ void __launch_bounds__(32 * SFAR_APPEND_WARPS, Keep > 8 ? 2 : Whole ?
         __syncwarp();                      // every lane (with a team, every warp) has read the old one
         if (lane == 0 && member == 0)
             scales[at] = scale;
-        if (first && scale > old) {
-            const float ratio = __fdiv_rn(old, scale);       // exact: the new one is a power of two
-            uint4 *held = reinterpret_cast<uint4 *>(base);
-            if (SfarInv(ratio).pow2) {
-#pragma unroll 4
-                for (int i = lane + 32 * member; i < first * (D / 16); i += 32 * Team)
-                    held[i] = times(held[i], [&](float v) { return v * ratio; });
-            } else {
-#pragma unroll 1
-                for (int i = lane + 32 * member; i < first * (D / 16); i += 32 * Team)
-                    held[i] = times_any(held[i], ratio);
-            }
-        }
+        const bool grows = first && scale > old;
         const SfarInv by(scale);
+        if (!by.pow2 || (grows && !SfarInv(old).pow2)) {
+            append_any<D>(src + (long long)t0 * ts, ts, base, first, n, old, scale, special, member, Team);
+            continue;
+        }
+        if (grows) {
+            const float ratio = old * by.inv;
+            uint4 *held = reinterpret_cast<uint4 *>(base);
+#pragma unroll 4
+            for (int i = lane + 32 * member; i < first * (D / 16); i += 32 * Team)
+                held[i] = times(held[i], [&](float v) { return v * ratio; });
+        }
         uint8_t *dst = base + (long long)(first + member * kTok + tok) * D + (lane % kVec) * 8;
-        auto store = [&](auto how) {
-            auto one = [&](int i, const uint4 &v) {
-                if (holds(i)) {
-                    const uint2 q = how(v);
-                    st_v2u32(dst + i * (kTok * Team * D), q.x, q.y);
-                }
-            };
-#pragma unroll
-            for (int i = 0; i < Keep; ++i)
-                one(i, keep[i]);
-            rest(one);
+        auto one = [&](int i, const uint4 &v) {
+            if (holds(i)) {
+                const uint2 q = sfar_quantize8(v, by.inv, special);
+                st_v2u32(dst + i * (kTok * Team * D), q.x, q.y);
+            }
         };
-        if (by.pow2)
-            store([&](const uint4 &v) { return sfar_quantize8(v, by.inv, special); });
-        else
-            store([&](const uint4 &v) { return quantize8_by_any(v, scale, special); });
+#pragma unroll
+        for (int i = 0; i < Keep; ++i)
+            one(i, keep[i]);
+        rest(one);
     }
 }
 
