@@ -17,8 +17,8 @@
 // and sum, the weights' (score times value scale), and the sum is of weight /
 // value scale: nothing is lost while the value scales of one request are
 // within 2^100 of one another.  Tokens of value scale 0 have no weight; their
-// exponentials have a reference and a sum of their own, joined at the end.  The accumulator is rescaled, in tensor memory,
-// only when a reference moves.
+// exponentials have a reference and a sum of their own, joined at the end.  The
+// accumulator is rescaled, in tensor memory, only when a reference moves.
 //
 // A CTA takes 256 rows as two tiles of 128, each with eight softmax warps (two
 // threads per row, a half of its columns each: the row's maximum needs one
