@@ -33,7 +33,7 @@
 //
 // Measured, 8 ranks of 8 query heads and one key head of 128, three chunks of
 // 700 to 1024 new tokens at the ends of contexts of 1100 to 4099: 203 us, 1080
-// TFLOP/s, 0.55 of a bf16 product's rate; the tensor core is busy 0.49 of the
+// TFLOP/s, 0.55 of a bf16 product's rate; the tensor core is busy 0.50 of the
 // time.  A tile's chain is what bounds it: about 2000 clocks from scores to
 // weights (maxima 400, the warps' agreement on the reference 300, exponentials
 // 930, masks and stores the rest) against 1088 of products, which two tiles in
