@@ -1,0 +1,673 @@
+// k_latent_attn.cu -- attention of the step's tokens over the paged latent
+// cache, absorbed form (include/sfar_latent.h).
+//
+// A request's new tokens times all query heads are the rows of one matrix,
+// taken 16 or 32 at a time; a cached row serves them all, as key (all its
+// numbers) and as value (the latent).  One pass with the running maximum and
+// sum of the softmax; per tile of 128 cached tokens, on the tensor cores,
+//   S^T = C Q^T   (tokens x rows, contraction over latent + key)
+//   O^T += L^T P^T (latent x rows, contraction over the tokens).
+// Transposed, because the few rows then are the short side: an MMA takes 128
+// of the other, and both products read the tile from shared memory as TMA
+// wrote it, once as the K-major and once as the M-major operand.
+// HBM-bound: 2 (latent + key) bytes a token against 2 NR (2 latent + key)
+// flops, 32 flops a byte at 16 rows.
+//
+// Softmax: a thread holds one token's scores of all rows.  A row's reference
+// moves only when a score passes it by 2^7.9 (a vote of the CTA's softmax
+// threads, no maxima otherwise), and the accumulator is rescaled in tensor
+// memory only then.  Weights go to shared memory as bf16, the type that an
+// MMA with these values takes; sums are of the unrounded ones.
+//
+// Shared memory holds one tile and a little more: a ring of 128-element pairs
+// of 64-element boxes (32 KB) and one of key boxes (16 KB).  A pair is free
+// again when its part of the second product is done, so the next tile streams
+// in while this one is multiplied.
+//
+// Work: as in k_kv_attn.cu the tiles of all (rank, request, row tile) form one
+// line that is cut into equal pieces, one per CTA; row tiles cut apart are
+// joined by the last of their CTAs, in order.  Prefix sums of 32 requests at a
+// time are kept, so that shared memory is the tiles'.
+// Warps 0-3: softmax; 4: copies and pieces; 5: the MMAs.
+#include "sfar_attn.cuh"
+#include "sfar_latent_args.h"
+
+namespace {
+
+constexpr int kTile = SFAR_LATENT_TILE, kGroup = SFAR_LATENT_GROUP;
+constexpr int kSoft = 4, kCopyWarp = kSoft, kMmaWarp = kSoft + 1, kThreads = 32 * (kMmaWarp + 1);
+constexpr int kBox = kTile * 128, kPair = 2 * kBox;                // bytes of 64 elements of every token, of 128
+constexpr int kMeta = 4, kPieces = 4, kParts = 16;                 // kParts: joined at once, at most
+
+template <int L, int NR> struct Lay {
+    static constexpr int kBlocks = L / 128, kChunks = L / 64 + 1;
+    static constexpr int kPairs = 5, kKeys = L == 512 && NR == 32 ? 1 : 2;     // slots of the rings
+    static constexpr int kQ = kChunks * NR * 128, kP = 2 * NR * 128;
+    static constexpr int oKey = kPairs * kPair, oQ = oKey + kKeys * kBox, oP = oQ + kQ;
+    static constexpr int kBytes = oP + kP;
+    static constexpr int kNeed = NR + kBlocks * NR, kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : 256;    // tensor memory
+    static constexpr int kPart = NR * (L + 2);                     // floats of a partial result
+};
+
+// One piece: NR rows of a request and a run of its tiles.
+struct Piece {
+    int r, b, rt;               // rank; request; row tile
+    int tile0, tiles;           // first tile, how many are on the line
+    int run;                    // of these, the ones that some row attends to
+    int all;                    // tiles of the whole row tile
+    int len, count, first;      // context, new tokens, row of the first new token
+    long long at;               // place of the piece's first tile on the line
+};
+
+template <int NR, class A> struct Work {
+    const uint32_t *upto;       // [groups + 1] prefix sums of the units of 32 requests, per rank
+    const A &a;
+    __device__ __forceinline__ int tiles(int len) const { return max(1, (len + kTile - 1) / kTile); }
+    __device__ __forceinline__ int row_tiles(int count) const { return (int)(((long long)count * a.Hq + NR - 1) / NR); }
+    // by a whole warp
+    __device__ __forceinline__ Piece at(long long u, long long end) const
+    {
+        const int lane = threadIdx.x & 31, groups = (a.B + kGroup - 1) / kGroup;
+        Piece p;
+        p.at = u;
+        const uint32_t S = upto[groups];
+        p.r = (int)sfar_div(u, S);
+        uint32_t v = (uint32_t)(u - (long long)p.r * S);
+        int lo = 0, hi = groups;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (upto[mid] <= v)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        v -= upto[lo];
+        const int b = lo * kGroup + lane;
+        int len = 0, count = 0, first = 0;
+        uint32_t sum = 0;
+        if (b < a.B) {
+            sfar_attn_request(a, b, len, count, first);
+            sum = (uint32_t)row_tiles(count) * (uint32_t)tiles(len);
+        }
+        const uint32_t mine = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t o = __shfl_up_sync(SFAR_FULL, sum, d);
+            if (lane >= d)
+                sum += o;
+        }
+        const unsigned past = __ballot_sync(SFAR_FULL, sum > v);
+        const int l = past ? __ffs(past) - 1 : 0;
+        p.b = lo * kGroup + l;
+        p.len = __shfl_sync(SFAR_FULL, len, l);
+        p.count = __shfl_sync(SFAR_FULL, count, l);
+        p.first = __shfl_sync(SFAR_FULL, first, l);
+        const uint32_t w = v - __shfl_sync(SFAR_FULL, sum - mine, l);
+        p.all = tiles(p.len);
+        p.rt = (int)(w / (uint32_t)p.all);
+        p.tile0 = (int)(w - (uint32_t)p.rt * (uint32_t)p.all);
+        p.tiles = (int)min((long long)(p.all - p.tile0), end - u);
+        const long long last = min((long long)p.count * a.Hq, ((long long)p.rt + 1) * NR) - 1;       // the row tile's last row
+        const int to = p.len - p.count + (int)(last / a.Hq) + 1;                                     // tokens it attends to
+        p.run = max(0, min(p.tiles, (max(0, to) + kTile - 1) / kTile - p.tile0));
+        return p;
+    }
+};
+
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool soft_any(bool v)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"((uint32_t)v)
+                 : "memory");
+    return r != 0;
+}
+// binary32 as integers in the same order, and back
+__device__ __forceinline__ int ordered(float x)
+{
+    const int i = __float_as_int(x);
+    return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float disordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+// whether one of the two bf16 is an infinity or NaN
+__device__ __forceinline__ bool odd2(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
+
+}  // namespace
+
+template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(const __grid_constant__ SfarLatentAttnArgs a)
+{
+    using Y = Lay<L, NR>;
+    extern __shared__ __align__(1024) unsigned char dyn[];
+    __shared__ __align__(8) unsigned long long bars[2 * Y::kPairs + 2 * Y::kKeys + 2 * kPieces + 5];
+    __shared__ Piece s_piece[kPieces];             // what the copying warp has begun with; no tiles: the end
+    __shared__ uint32_t s_live[kMeta];             // of a tile: which 16 tokens are on a page of the pool
+    __shared__ uint32_t upto[SFAR_KV_MAX_REQUESTS / kGroup + 1];
+    __shared__ uint32_t s_warp[kThreads / 32], s_tmem;
+    __shared__ int s_hi[NR], s_last;
+    __shared__ float s_max[kSoft][NR], s_sum[NR], s_ref[NR], s_inv[NR], s_w[kParts][NR];
+    __shared__ uint16_t *s_out[NR];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t mem = (tc::smem(dyn) + 1023u) & ~1023u;
+    unsigned char *gen = dyn + (mem - tc::smem(dyn));
+    const uint32_t full = tc::smem(bars), empty = full + 8 * Y::kPairs, kfull = empty + 8 * Y::kPairs, kempty = kfull + 8 * Y::kKeys,
+                   pfull = kempty + 8 * Y::kKeys, pempty = pfull + 8 * kPieces, qbar = pempty + 8 * kPieces, sbar = qbar + 8, wbar = qbar + 16,
+                   obar = qbar + 24, drain = qbar + 32;
+
+    if (warp == kCopyWarp && lane < a.R)
+        tc::prefetch_map(&a.map[lane]);
+    if (tid == 0) {
+        for (uint32_t b = full; b <= drain; b += 8)
+            tc::bar_init(b, b >= pempty && b < qbar ? kSoft + 1 : b == qbar || b == wbar ? kSoft : 1);
+        tc::bar_fence_init();
+        tc::fence_async();
+        upto[0] = 0;
+    }
+    if (warp == kMmaWarp)
+        tc::tmem_alloc<1>(tc::smem(&s_tmem), Y::kCols);
+    pdl_wait();
+    const unsigned long long limit = ld_relaxed_u64(&a.ctl->timeout_ns);
+
+    // prefix sums of the requests' units: row tiles x tiles, 32 requests to a warp
+    const Work<NR, SfarLatentAttnArgs> work{upto, a};
+    uint32_t carry = 0;
+    int row_tiles = 0;                             // of this thread's requests
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        const int b = b0 + tid;
+        uint32_t v = 0;
+        if (b < a.B) {
+            int len, count, first;
+            sfar_attn_request(a, b, len, count, first);
+            const int n = work.row_tiles(count);
+            v = (uint32_t)n * (uint32_t)work.tiles(len);
+            row_tiles = min(row_tiles + n, 1 << 26);       // above any step's; 32 such sums fit 32 bits
+            if (blockIdx.x == 0)
+                sfar_attn_check(a, b, len, count, first);
+        }
+        v = __reduce_add_sync(SFAR_FULL, v);
+        if (lane == 0)
+            s_warp[warp] = v;
+        __syncthreads();
+        uint32_t before = carry;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            carry += s_warp[w];
+            if (w <= warp)
+                before += s_warp[w];
+        }
+        if (lane == 0 && b < a.B)
+            upto[b / kGroup + 1] = before;
+        __syncthreads();
+    }
+    row_tiles = __reduce_add_sync(SFAR_FULL, row_tiles);
+    if (lane == 0)
+        s_warp[warp] = (uint32_t)row_tiles;
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = s_tmem;
+    long long whole = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w)
+        whole += s_warp[w];
+    // short row tiles are left whole, or in cuts of two tiles
+    const long long U = sfar_attn_many(a, whole) ? 0 : (long long)carry * a.R;
+    const long long N = min(min((long long)gridDim.x, U), max(whole * a.R, U / 2));
+    const long long u0 = blockIdx.x < N ? sfar_div(blockIdx.x * U, N) : 0, u1 = blockIdx.x < N ? sfar_div((blockIdx.x + 1) * U, N) : 0;
+
+    if (warp < kSoft) {
+        // -------------------------------------------------------------- softmax
+        bool dead = false;                         // a wait gave up: go on without waiting
+        const uint32_t lanes = (uint32_t)warp * 32u << 16, tS = tmem + lanes, tO = tmem + NR + lanes;
+        const int tok = warp * 32 + lane;          // of a tile, this thread's; of a block of the latent, its element
+        const float f = a.scale * 1.4426950408889634f;
+        // where this thread's weight of row n goes: P[half][row][64 tokens], 128-byte swizzle
+        unsigned char *const pw = gen + Y::oP + (tok >> 6) * (NR * 128) + (tok & 7) * 2;
+        const int unit = (tok & 63) >> 3;
+        tc::Ring<kPieces> ps;
+        tc::Ring<Y::kPairs> st;                    // the first pair of the tile
+        uint32_t sphase = 0, ophase = 0, tile = 0;
+        for (;;) {
+            dead = dead || !tc::bar_wait(pfull + 8 * ps.slot, ps.phase, limit);
+            if (soft_any(dead)) {
+                dead = true;
+                break;
+            }
+            const Piece p = s_piece[ps.slot];
+            __syncwarp();
+            if (lane == 0)
+                tc::bar_arrive(pempty + 8 * ps.slot);
+            ps.next();
+            if (p.tiles == 0)
+                break;
+            const int row0 = p.rt * NR, rows = (int)min((long long)NR, (long long)p.count * a.Hq - row0);
+            if (tid < NR) {
+                const int n = row0 + min(tid, rows - 1), i = n / a.Hq, h = n - i * a.Hq;
+                s_hi[tid] = p.len - p.count + i + 1;
+                s_out[tid] = a.out[p.r] + (long long)(p.first + i) * a.ots + h * a.ohs;
+            }
+            // the query rows: [chunk][row][64 elements], 128-byte swizzle; zeros past the rows and past a short key
+            const uint16_t *q = a.q[p.r];
+            for (int i = tid; i < NR * Y::kChunks * 8 && p.run; i += 32 * kSoft) {
+                const int n = i / (Y::kChunks * 8), c = i % (Y::kChunks * 8), row = row0 + n, t = row / a.Hq;
+                const bool in = n < rows && c * 8 < L + a.rope;
+                const uint16_t *src = q;
+                if (in)
+                    src += (long long)(p.first + t) * a.qts + (long long)(row - t * a.Hq) * a.qhs + c * 8;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(mem + Y::oQ + (c >> 3) * (NR * 128) + n * 128 +
+                                                                                  (((c & 7) ^ (n & 7)) << 4)),
+                             "l"(src), "r"(in ? 16u : 0u)
+                             : "memory");
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            tc::fence_async();
+            soft_sync();                           // s_hi, s_out
+            if (lane == 0 && p.run)
+                tc::bar_arrive(qbar);
+            const int all_to = s_hi[0];            // every row sees the tokens before it
+            float ref[NR], sum[NR];
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                ref[n] = -INFINITY;
+                sum[n] = 0.f;
+            }
+            for (int k = 0; k < p.run; ++k, ++tile) {
+                const int j0 = (p.tile0 + k) * kTile, j = j0 + tok;
+                dead = dead || !tc::bar_wait(sbar, sphase, limit) || !tc::bar_wait(full + 8 * st.slot, st.phase, limit);
+                sphase ^= 1u;
+                tc::fence_after();
+                uint32_t raw[NR];
+                tc::ld(raw, tS);
+                tc::wait_ld(raw);
+                const uint32_t live = s_live[tile % kMeta];
+                const bool edge = j0 + kTile > all_to || live != 0xffu;
+                const bool there = j < p.len && (live >> (tok >> 4) & 1u);
+                bool odd = false;
+                if (edge) {
+                    // A place that holds no token becomes zeros, whatever lies there; so does a token with an infinity or
+                    // NaN that not every row sees, and the rows that do see it get a NaN for its weight.
+                    tc::Ring<Y::kPairs> it = st;
+                    for (int c = 0; c < Y::kBlocks; ++c, it.next()) {
+                        dead = dead || !tc::bar_wait(full + 8 * it.slot, it.phase, limit);
+                        if (there && j >= all_to) {
+                            const unsigned char *at = gen + it.slot * kPair + tok * 128;
+                            for (int i = 0; i < 16; ++i) {
+                                const uint4 v = *reinterpret_cast<const uint4 *>(at + (i >> 3) * kBox + ((i & 7) << 4));
+                                odd = odd || odd2(v.x) || odd2(v.y) || odd2(v.z) || odd2(v.w);
+                            }
+                        }
+                    }
+                    it = st;
+                    for (int c = 0; c < Y::kBlocks; ++c, it.next())
+                        if (!there || odd) {
+                            unsigned char *at = gen + it.slot * kPair + tok * 128;
+                            for (int i = 0; i < 16; ++i)
+                                *reinterpret_cast<uint4 *>(at + (i >> 3) * kBox + ((i & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                        }
+                }
+                for (int c = 0; c < Y::kBlocks; ++c)
+                    st.next();
+                // scores in units of log2, relative to the references
+                float x[NR];
+                bool move = false;
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    x[n] = __uint_as_float(raw[n]) * f;
+                    if (edge && (!there || j >= s_hi[n]))
+                        x[n] = -INFINITY;
+                    move = move || x[n] - ref[n] > kAttnLift;
+                }
+                if (soft_any(move)) {
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) {
+                        const int m = __reduce_max_sync(SFAR_FULL, ordered(x[n]));
+                        if (lane == 0)
+                            s_max[warp][n] = disordered(m);
+                    }
+                    soft_sync();
+                    float keep[NR];
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) {
+                        const float now = fmaxf(fmaxf(s_max[0][n], s_max[1][n]), fmaxf(s_max[2][n], s_max[3][n]));
+                        const float next = now - ref[n] > kAttnLift ? now : ref[n];
+                        keep[n] = ref[n] == -INFINITY ? 1.f : ex2(ref[n] - next);          // all is 0 then, or NaN
+                        ref[n] = next;
+                        sum[n] *= keep[n];
+                    }
+                    if (k) {
+#pragma unroll
+                        for (int c = 0; c < Y::kBlocks; ++c)
+#pragma unroll
+                            for (int n0 = 0; n0 < NR; n0 += 16) {
+                                uint32_t o[16];
+                                tc::ld16(o, tO + c * NR + n0);
+                                tc::wait_ld(o);
+#pragma unroll
+                                for (int n = 0; n < 16; ++n)
+                                    o[n] = __float_as_uint(__uint_as_float(o[n]) * keep[n0 + n]);
+                                tc::st16(tO + c * NR + n0, o);
+                            }
+                        tc::wait_st();
+                    }
+                    soft_sync();                   // s_max has been read
+                }
+#pragma unroll
+                for (int n = 0; n < NR; n += 2) {
+                    float w[2];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        w[y] = x[n + y] == -INFINITY ? 0.f : ex2(x[n + y] - ref[n + y]);
+                        if (odd && j < s_hi[n + y])
+                            w[y] = NAN;
+                        sum[n + y] += w[y];
+                    }
+                    const uint32_t b = tc::bf16x2(w[0], w[1]);
+                    *reinterpret_cast<uint16_t *>(pw + n * 128 + ((unit ^ (n & 7)) << 4)) = (uint16_t)b;
+                    *reinterpret_cast<uint16_t *>(pw + (n + 1) * 128 + ((unit ^ ((n + 1) & 7)) << 4)) = (uint16_t)(b >> 16);
+                }
+                tc::fence_async();
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    tc::bar_arrive(wbar);
+            }
+            // the rows' sums
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                float v = sum[n];
+#pragma unroll
+                for (int d = 16; d; d >>= 1)
+                    v += __shfl_xor_sync(SFAR_FULL, v, d);
+                if (lane == 0)
+                    s_max[warp][n] = v;
+                if (tid == 0)
+                    s_ref[n] = ref[n];
+            }
+            soft_sync();
+            if (tid < NR) {
+                const float v = (s_max[0][tid] + s_max[1][tid]) + (s_max[2][tid] + s_max[3][tid]);
+                s_sum[tid] = v;
+                s_inv[tid] = v == 0.f ? 0.f : 1.f / v;
+            }
+            soft_sync();
+            if (p.run) {
+                dead = dead || !tc::bar_wait(obar, ophase, limit);
+                ophase ^= 1u;
+                tc::fence_after();
+            }
+            // the accumulator, element `tok` of each 128 of the latent, a column at a time
+            auto each = [&](auto what) {
+#pragma unroll
+                for (int c = 0; c < Y::kBlocks; ++c) {
+                    uint32_t o[NR];
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+                        o[n] = 0;
+                    if (p.run) {
+                        tc::ld(o, tO + c * NR);
+                        tc::wait_ld(o);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+                        if (n < rows)
+                            what(n, c * 128 + tok, __uint_as_float(o[n]));
+                }
+            };
+            if (p.tiles == p.all) {
+                each([&](int n, int d, float v) { s_out[n][d] = (uint16_t)tc::bf16x2(v * s_inv[n], 0.f); });
+            } else {
+                // a part: leave it in the workspace, for the last of the row tile's CTAs
+                const long long from = p.at - p.tile0, to = from + p.all;
+                const int c0 = (int)sfar_div((from + 1) * N - 1, U), c1 = (int)sfar_div(to * N - 1, U);
+                SfarJoin join(a, 0, c0, c1, blockIdx.x);
+                auto slot = [&](int c) { return a.part + ((size_t)c * 2 + (c == c0)) * Y::kPart; };
+                float *dst = slot(blockIdx.x);
+                each([&](int n, int d, float v) { __stcg(dst + n * L + d, v); });
+                if (tid < rows)
+                    __stcg(reinterpret_cast<float2 *>(dst + NR * L) + tid, make_float2(s_ref[tid], s_sum[tid]));
+                for (;;) {
+                    soft_sync();
+                    if (tid == 0)
+                        s_last = join.last();
+                    soft_sync();
+                    if (!s_last)
+                        break;
+                    const int parts = (join.hi - join.lo) / join.step + 1;
+                    float top = -INFINITY, total = 0.f;
+                    if (tid < rows) {
+                        for (int c = 0; c < parts; ++c)
+                            top = fmaxf(top, __ldcg(reinterpret_cast<const float2 *>(slot(join.lo + c * join.step) + NR * L) + tid).x);
+                        for (int c = 0; c < parts; ++c) {
+                            const float2 m = __ldcg(reinterpret_cast<const float2 *>(slot(join.lo + c * join.step) + NR * L) + tid);
+                            const float w = m.x == -INFINITY ? 0.f : ex2(m.x - top);
+                            s_w[c][tid] = w;
+                            total += m.x == -INFINITY ? m.y : w * m.y;        // its sum is 0 then, or NaN
+                        }
+                        s_inv[tid] = total == 0.f ? 0.f : 1.f / total;
+                    }
+                    soft_sync();
+                    float *group = slot(join.lo);
+                    const bool more = join.up != 0;
+                    constexpr int kPer = L / 4;    // threads of a row
+                    for (int n = tid / kPer; n < rows; n += 32 * kSoft / kPer) {
+                        const int d = tid % kPer * 4;
+                        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                        for (int c = 0; c < parts; ++c) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(slot(join.lo + c * join.step) + n * L + d));
+                            const float w = s_w[c][n];
+                            o.x += w * v.x;
+                            o.y += w * v.y;
+                            o.z += w * v.z;
+                            o.w += w * v.w;
+                        }
+                        if (more) {
+                            __stcg(reinterpret_cast<float4 *>(group + n * L + d), o);
+                        } else {
+                            const float by = s_inv[n];
+                            st_v2u32(s_out[n] + d, tc::bf16x2(o.x * by, o.y * by), tc::bf16x2(o.z * by, o.w * by));
+                        }
+                    }
+                    if (more && tid < rows)
+                        __stcg(reinterpret_cast<float2 *>(group + NR * L) + tid, make_float2(top, total));
+                    if (!join.next(a, 0))
+                        break;
+                }
+            }
+            tc::fence_before();                    // before the MMAs that the next weights allow
+            soft_sync();                           // the tables in shared memory have been read
+        }
+        sfar_attn_padding<L>(a, tid, 32 * kSoft);
+        if (dead && lane == 0)
+            sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
+    } else if (warp == kCopyWarp) {
+        // --------------------------------------------------------------- copies
+        const uint64_t once = tc::evict_first(), often = tc::evict_last();
+        // by all lanes alike
+        auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(SFAR_FULL, tc::bar_wait(bar, parity, limit)); };
+        tc::Ring<Y::kPairs> st;
+        tc::Ring<Y::kKeys> ks;
+        tc::Ring<kPieces> ps;
+        bool dead = false;
+        uint32_t pairs = 0, keys = 0, tile = 0;    // issued
+        const int per = 1 << a.shift, boxes = kTile / per;     // tokens of one copy, copies of a tile's 64 elements
+        for (long long u = u0; !dead;) {
+            Piece p;
+            const bool end = u >= u1;
+            if (!end)
+                p = work.at(u, u1);
+            else
+                p.tiles = 0;
+            if (!wait(pempty + 8 * ps.slot, ps.phase ^ 1u)) {
+                dead = true;
+                break;
+            }
+            if (lane == 0) {
+                s_piece[ps.slot] = p;
+                tc::bar_arrive(pfull + 8 * ps.slot);
+            }
+            ps.next();
+            if (end)
+                break;
+            u += p.tiles;
+            const int *row = a.table + (size_t)p.b * a.W;
+            const CUtensorMap *map = &a.map[p.r];
+            const uint64_t pol = (long long)p.count * a.Hq <= NR ? once : often;     // other row tiles read it again
+            // lane i: the page of copy i, of 32 copies from token `base` on
+            auto pages = [&](int base) {
+                const unsigned j = (unsigned)base + (unsigned)(lane * per);      // may pass 2^31
+                int page = 0;
+                if (j < (unsigned)p.len && j < (unsigned)(p.tile0 + p.run) * (unsigned)kTile)
+                    page = row[j >> a.shift];
+                return page;
+            };
+            const int stretch = 32 * per;
+            int base = p.tile0 * kTile, page = pages(base), next = pages(base + stretch);
+            for (int k = 0; k < p.run && !dead; ++k) {
+                const int j0 = (p.tile0 + k) * kTile;
+                if (j0 - base >= stretch) {
+                    base += stretch;
+                    page = next;
+                    next = pages(base + stretch);
+                }
+                // lane i: copy i % 8 of the tile, of the first or second 64 elements of a pair
+                const int box = lane & 7, at = (j0 - base) / per + box, j = j0 + box * per;
+                const int mine = __shfl_sync(SFAR_FULL, page, at & 31);
+                const bool live = box < boxes && j < p.len, bad = live && (unsigned)mine >= (unsigned)a.pages, go = live && !bad;
+                if (bad && lane < 8)
+                    sfar_kv_fault(a.ctl, p.b, SFAR_KV_BAD_PAGE);
+                const unsigned any = __ballot_sync(SFAR_FULL, go) & 0xffu;
+                const unsigned held = __ballot_sync(SFAR_FULL, lane < 8 && (any >> (lane * 16 / per) & 1u));
+                if (lane == 0)
+                    s_live[tile % kMeta] = held;
+                __syncwarp();
+                ++tile;
+                const uint32_t bytes = (uint32_t)__popc(any) * per * 128;
+                for (int c = 0; c < Y::kBlocks; ++c) {
+                    if (!wait(empty + 8 * st.slot, st.phase ^ 1u)) {
+                        dead = true;
+                        break;
+                    }
+                    const uint32_t bar = full + 8 * st.slot;
+                    if (go && lane < 16)
+                        tc::load_3d(mem + st.slot * kPair + (lane >> 3) * kBox + box * per * 128, map, c * 128 + (lane >> 3) * 64, 0, mine, bar, pol);
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::bar_expect(bar, 2 * bytes);
+                    ++pairs;
+                    st.next();
+                }
+                if (dead)
+                    break;
+                if (!wait(kempty + 8 * ks.slot, ks.phase ^ 1u)) {
+                    dead = true;
+                    break;
+                }
+                const uint32_t bar = kfull + 8 * ks.slot;
+                if (go && lane < 8)
+                    tc::load_3d(mem + Y::oKey + ks.slot * kBox + box * per * 128, map, L, 0, mine, bar, pol);
+                __syncwarp();
+                if (lane == 0)
+                    tc::bar_expect(bar, bytes);
+                ++keys;
+                ks.next();
+            }
+        }
+        if (dead && lane == 0) {
+            sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
+            // the copies in flight land before the shared memory is released
+            for (uint32_t i = pairs - min(pairs, (uint32_t)Y::kPairs); i < pairs; ++i)
+                tc::bar_wait(full + 8 * (i % Y::kPairs), (i / Y::kPairs) & 1u, limit);
+            for (uint32_t i = keys - min(keys, (uint32_t)Y::kKeys); i < keys; ++i)
+                tc::bar_wait(kfull + 8 * (i % Y::kKeys), (i / Y::kKeys) & 1u, limit);
+        }
+    } else {
+        // ----------------------------------------------------------------- MMAs
+        constexpr uint32_t idS = tc::idesc_bf16(128, NR), idO = idS | tc::kTransposeA;
+        const uint64_t dq = tc::desc_k128(mem + Y::oQ), dp = tc::desc_k128(mem + Y::oP), dk = tc::desc_k128(mem), dv = tc::desc_n128(mem, kBox),
+                       dr = tc::desc_k128(mem + Y::oKey);
+        tc::Ring<Y::kPairs> st;
+        tc::Ring<Y::kKeys> ks;
+        tc::Ring<kPieces> ps;
+        uint32_t qphase = 0, wphase = 0;
+        bool dead = false;
+        for (;;) {
+            dead = __any_sync(SFAR_FULL, dead || !tc::bar_wait(pfull + 8 * ps.slot, ps.phase, limit));
+            if (dead)
+                break;
+            const int run = s_piece[ps.slot].run, tiles = s_piece[ps.slot].tiles;
+            __syncwarp();
+            if (lane == 0)
+                tc::bar_arrive(pempty + 8 * ps.slot);
+            ps.next();
+            if (tiles == 0)
+                break;
+            if (tc::elect_one() && run) {
+                dead = !tc::bar_wait(qbar, qphase, limit);
+                qphase ^= 1u;
+                for (int k = 0; k < run && !dead; ++k) {
+                    tc::Ring<Y::kPairs> it = st;
+#pragma unroll
+                    for (int c = 0; c < Y::kBlocks; ++c, it.next()) {
+                        dead = dead || !tc::bar_wait(full + 8 * it.slot, it.phase, limit);
+                        if (dead)
+                            break;
+                        tc::fence_after();
+                        const uint64_t d = dk + it.slot * (kPair >> 4);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            tc::mma_f16_ss(tmem, d + (i >> 2) * (kBox >> 4) + 2 * (i & 3), dq + (2 * c + (i >> 2)) * (NR * 128 >> 4) + 2 * (i & 3), idS,
+                                           c + i > 0);
+                    }
+                    dead = dead || !tc::bar_wait(kfull + 8 * ks.slot, ks.phase, limit);
+                    if (dead)
+                        break;
+                    for (int i = 0; i < a.rope / 16; ++i)
+                        tc::mma_f16_ss(tmem, dr + ks.slot * (kBox >> 4) + 2 * i, dq + (L / 64) * (NR * 128 >> 4) + 2 * i, idS, true);
+                    tc::commit(kempty + 8 * ks.slot);
+                    tc::commit(sbar);
+                    ks.next();
+                    dead = !tc::bar_wait(wbar, wphase, limit);
+                    wphase ^= 1u;
+                    if (dead)
+                        break;
+                    tc::fence_after();
+#pragma unroll
+                    for (int c = 0; c < Y::kBlocks; ++c, st.next()) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            tc::mma_f16_ss(tmem + NR + c * NR, dv + st.slot * (kPair >> 4) + 128 * i, dp + (i >> 2) * (NR * 128 >> 4) + 2 * (i & 3), idO,
+                                           k + i > 0);
+                        tc::commit(empty + 8 * st.slot);
+                    }
+                }
+                if (!dead)
+                    tc::commit(obar);
+            }
+            dead = __any_sync(SFAR_FULL, dead);
+        }
+        if (tc::elect_one()) {
+            if (dead)
+                sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
+            // every MMA and every arrival it causes is done before the CTA leaves
+            tc::commit(drain);
+            tc::bar_wait(drain, 0, limit);
+        }
+    }
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp)
+        tc::tmem_free<1>(tmem, Y::kCols);
+}
+
+const void *sfar_kernel_latent_attn(int latent, int rows, int *threads, int *smem)
+{
+#define SFAR_LATENT(L, NR) (*smem = Lay<L, NR>::kBytes + 1024, (const void *)k_latent_attn<L, NR>)
+    *threads = kThreads;
+    if (rows == 16)
+        return latent == 256 ? SFAR_LATENT(256, 16) : SFAR_LATENT(512, 16);
+    return latent == 256 ? SFAR_LATENT(256, 32) : SFAR_LATENT(512, 32);
+#undef SFAR_LATENT
+}

@@ -1,0 +1,557 @@
+// k_latent_prompt.cu -- attention of prompts over expanded keys and values,
+// the rotated part of the keys shared by the heads (include/sfar_latent.h).
+//
+// Per 128 new tokens of one head and 128 context tokens, on the tensor cores,
+// both accumulated in tensor memory:
+//   S = Q K^T + Qr Kr^T, O += P V.
+// Compute-bound: 2 (2 D + rope) flops per visible pair, D = 128, rope = 64:
+// 1280 clocks of products a tile, against 1024 of exponentials.
+//
+// A CTA takes 256 rows as two tiles, so that while one tile's softmax works
+// the tensor core has the other's products; keys and values are then read once
+// for both.  A thread owns a row: its maximum and sum need no exchange, its
+// 128 scores stay in registers.  Weights go back to tensor memory as bf16, in
+// the place of the scores; the accumulator is rescaled, there, only when a
+// row's reference moves (kAttnLift).
+//
+// Keys (three boxes of 64 elements x 128 tokens, 16 KB) and values (two) pass
+// through one ring in the order of their use.
+//
+// Work: row tiles are taken from a counter, one (rank, head)'s row tiles
+// after another, the longest first: they share keys and values in L2.
+// Warps 0-3, 4-7: the tiles' softmax; 8: copies and pieces; 9: the MMAs.
+#include "sfar_attn.cuh"
+#include "sfar_latent_args.h"
+
+namespace {
+
+constexpr int kTile = 128, kGroup = SFAR_LATENT_GROUP, kBox = kTile * 128;     // bytes of 64 elements of 128 tokens
+constexpr int kPieces = 4;
+constexpr int kRegsSoft = 216, kRegsRest = 72;     // 8 warps, 4 warps: together the launch's 12 x 168
+
+template <int D, int TILES> struct Lay {
+    static constexpr int kV = D / 64, kK = kV + 1;                 // boxes of a step's values, keys
+    static constexpr int kQ = TILES * kK * kBox;
+    static constexpr int kSlots = TILES == 2 && D == 128 ? 8 : 10;
+    static constexpr int kBytes = kQ + kSlots * kBox;
+};
+enum { kSoftWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kThreads = 384 };
+
+// 128 or 256 rows of one head of a request.
+struct Piece {
+    int r, h, b, rt;            // rank, head, request, row tile; b < 0: the end
+    int len, count, first, kfirst;      // context, new tokens, rows of the first new and of the first context token
+    int steps[2];               // tiles of the context that each tile of rows attends to
+};
+
+__device__ __forceinline__ bool odd2(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Request b's rows, none if its offsets are out of order or beyond the tensors.
+__device__ __forceinline__ bool request(const SfarLatentPromptArgs &a, int b, int &len, int &count, int &first, int &kfirst)
+{
+    first = a.starts[b];
+    kfirst = a.kstarts[b];
+    const int e = a.starts[b + 1], ke = a.kstarts[b + 1];
+    const bool ok = first >= 0 && e >= first && e <= a.T && kfirst >= 0 && ke >= kfirst && ke <= a.S;
+    count = ok ? e - first : 0;
+    len = ok ? ke - kfirst : 0;
+    return ok;
+}
+
+}  // namespace
+
+template <int D, int TILES> __global__ void __launch_bounds__(kThreads, 1) k_latent_prompt(const __grid_constant__ SfarLatentPromptArgs a)
+{
+    using Y = Lay<D, TILES>;
+    constexpr int kRows = 128 * TILES;
+    extern __shared__ __align__(1024) unsigned char dyn[];
+    __shared__ __align__(8) unsigned long long bars[2 * Y::kSlots + 2 * kPieces + 11];
+    __shared__ Piece s_piece[kPieces];
+    __shared__ uint32_t upto[SFAR_KV_MAX_REQUESTS / kGroup + 1];
+    __shared__ uint32_t s_warp[kThreads / 32], s_tmem;
+    __shared__ int s_odd[4];                       // by the piece: the first context token that is not finite, of those that were checked
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t mem = (tc::smem(dyn) + 1023u) & ~1023u, ring = mem + Y::kQ;
+    unsigned char *gen = dyn + (mem - tc::smem(dyn));
+    const uint32_t full = tc::smem(bars), empty = full + 8 * Y::kSlots, pfull = empty + 8 * Y::kSlots, pempty = pfull + 8 * kPieces,
+                   qfull = pempty + 8 * kPieces, qempty = qfull + 16, sbar = qempty + 16, wbar = sbar + 16, obar = wbar + 16, drain = obar + 16;
+
+    if (warp == kCopyWarp && lane < a.R) {
+        tc::prefetch_map(&a.qmap[lane]);
+        tc::prefetch_map(&a.kmap[lane]);
+        tc::prefetch_map(&a.vmap[lane]);
+        tc::prefetch_map(&a.krmap[lane]);
+    }
+    if (tid == 0) {
+        for (uint32_t b = full; b <= drain; b += 8)
+            tc::bar_init(b, b >= pempty && b < qfull ? 4 * TILES + 1 : b >= wbar && b < obar ? 4 : 1);
+        tc::bar_fence_init();
+        tc::fence_async();
+        upto[0] = 0;
+    }
+    if (tid < 4)
+        s_odd[tid] = INT_MAX;
+    if (warp == kMmaWarp)
+        tc::tmem_alloc<1>(tc::smem(&s_tmem), 256 * TILES);
+    pdl_wait();
+    const unsigned long long limit = ld_relaxed_u64(&a.ctl->timeout_ns);
+
+    // prefix sums of the requests' row tiles, 32 requests to a warp
+    uint32_t carry = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        const int b = b0 + tid;
+        uint32_t v = 0;
+        if (b < a.B) {
+            int len, count, first, kfirst;
+            if (!request(a, b, len, count, first, kfirst) && blockIdx.x == 0)
+                sfar_kv_fault(a.ctl, b, SFAR_KV_BAD_TOKENS);
+            v = min((uint32_t)(count + kRows - 1) / kRows, 1u << 26);     // offsets in no order: 32 such sums fit 32 bits
+        }
+        v = __reduce_add_sync(SFAR_FULL, v);
+        if (lane == 0)
+            s_warp[warp] = v;
+        __syncthreads();
+        uint32_t before = carry;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            carry = min(carry + min(s_warp[w], 1u << 30), 1u << 30);
+            if (w <= warp)
+                before = carry;
+        }
+        if (lane == 0 && b < a.B)
+            upto[b / kGroup + 1] = before;
+        __syncthreads();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = s_tmem;
+    const bool many = carry > (uint32_t)a.most;    // more than the step has: offsets in no order, nothing is computed
+    if (many && blockIdx.x == 0 && tid == 0)
+        sfar_kv_fault(a.ctl, a.B, SFAR_KV_BAD_TOKENS);
+    const uint32_t items = many ? 0 : carry * (uint32_t)(a.R * a.Hq);
+
+    if (warp < kSoftWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+        const int x = warp >> 2;                   // tile
+        if (x < TILES) {
+            // ---------------------------------------------------------- softmax
+            bool dead = false;                     // a wait gave up: go on without waiting
+            const int lrow = (warp & 3) * 32 + lane;
+            const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16, tS = tmem + x * 256 + lanes, tO = tS + 128;
+            // never 0, so that a masked score of -inf stays that
+            const float f = fmaxf(a.scale * 1.4426950408889634f, 1e-37f);
+            tc::Ring<kPieces> ps;
+            uint32_t sphase = 0, ophase = 0, slot = 0;     // slot: boxes that came before this step's keys
+            for (int piece = 0;; ++piece) {
+                dead = dead || !tc::bar_wait(pfull + 8 * ps.slot, ps.phase, limit);
+                dead = __any_sync(SFAR_FULL, dead);
+                if (dead)
+                    break;
+                const Piece p = s_piece[ps.slot];
+                __syncwarp();
+                if (lane == 0)
+                    tc::bar_arrive(pempty + 8 * ps.slot);
+                ps.next();
+                if (p.b < 0)
+                    break;
+                if (tid == 0)
+                    s_odd[(piece + 2) & 3] = INT_MAX;
+                const int i = p.rt * kRows + x * 128 + lrow, pos = p.len - p.count + i;
+                const int all_to = min(p.len, p.len - p.count + p.rt * kRows + 1);     // every row of both tiles sees the tokens before it
+                const bool row = i < p.count;
+                const int hi = row ? pos + 1 : INT_MAX;
+                const int mine_to = p.len - p.count + p.rt * kRows + x * 128 + 1;      // every row of this tile
+                float ref = -INFINITY, sum = 0.f;
+                const int steps = p.steps[x], whole = max(p.steps[0], p.steps[1]);
+                for (int k = 0; k < steps; ++k) {
+                    const int j0 = k * kTile;
+                    dead = dead || !tc::bar_wait(sbar + 8 * x, sphase, limit);
+                    sphase ^= 1u;
+                    tc::fence_after();
+                    uint32_t s[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        tc::ld32(s[c], tS + 32 * c);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        tc::wait_ld(s[c]);
+                    if (j0 + kTile > all_to && (x == 0 || k >= p.steps[0])) {
+                        // Values of tokens that not every row sees, a token to a thread: one past the context, or with an
+                        // infinity or NaN, becomes zeros (0 times it would reach the rows that do not see it); the rows that
+                        // see the latter become NaN at the end.
+                        const int j = j0 + lrow;
+                        uint32_t at = slot + k * (Y::kK + Y::kV) + Y::kK;
+#pragma unroll
+                        for (int c = 0; c < Y::kV; ++c)
+                            dead = dead || !tc::bar_wait(full + 8 * ((at + c) % Y::kSlots), (at + c) / Y::kSlots & 1u, limit);
+                        if (j >= all_to) {
+                            bool odd = false;
+#pragma unroll
+                            for (int c = 0; c < Y::kV; ++c) {
+                                const unsigned char *v = gen + Y::kQ + (at + c) % Y::kSlots * kBox + lrow * 128;
+                                for (int e = 0; e < 8; ++e) {
+                                    const uint4 w = *reinterpret_cast<const uint4 *>(v + ((e ^ (lrow & 7)) << 4));
+                                    odd = odd || odd2(w.x) || odd2(w.y) || odd2(w.z) || odd2(w.w);
+                                }
+                            }
+                            if (odd) {
+                                if (j < p.len)
+                                    atomicMin(&s_odd[piece & 3], j);
+#pragma unroll
+                                for (int c = 0; c < Y::kV; ++c) {
+                                    unsigned char *v = gen + Y::kQ + (at + c) % Y::kSlots * kBox + lrow * 128;
+                                    for (int e = 0; e < 8; ++e)
+                                        *reinterpret_cast<uint4 *>(v + (e << 4)) = make_uint4(0, 0, 0, 0);
+                                }
+                            }
+                        }
+                        tc::fence_async();
+                    }
+                    if (j0 + kTile > mine_to) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (j0 + 32 * c + e >= hi)
+                                    s[c][e] = 0xff800000u;
+                    }
+                    float m[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        m[c] = max3(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]), __uint_as_float(s[c][2]));
+#pragma unroll
+                        for (int e = 3; e < 31; e += 2)
+                            m[c] = max3(m[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+                        m[c] = fmaxf(m[c], __uint_as_float(s[c][31]));
+                    }
+                    const float now = fmaxf(max3(m[0], m[1], m[2]), m[3]) * f;
+                    const bool move = now - ref > kAttnLift;
+                    if (__any_sync(SFAR_FULL, move)) {
+                        const float next = move ? now : ref;
+                        const float keep = ref == -INFINITY ? 1.f : ex2(ref - next);      // all is 0 then, or NaN
+                        ref = next;
+                        sum *= keep;
+                        if (k) {
+#pragma unroll
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t o[16];
+                                tc::ld16(o, tO + c);
+                                tc::wait_ld(o);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                                tc::st16(tO + c, o);
+                            }
+                        }
+                    }
+                    // a row that has seen nothing: any finite reference, weights 0
+                    const float base = ref == -INFINITY ? 0.f : ref;
+                    const uint64_t f2 = tc::pack2(f, f), b2 = tc::pack2(-base, -base);
+                    float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float2 y = tc::unpack2(tc::fma2(tc::pack2u(s[c][e], s[c][e + 1]), f2, b2));
+                            const float u = ex2(y.x), v = ex2(y.y);
+                            part[e >> 1 & 3] += u + v;
+                            w[e >> 1] = tc::bf16x2(u, v);
+                        }
+                        tc::st16(tS + 16 * c, w);
+                    }
+                    sum += (part[0] + part[1]) + (part[2] + part[3]);
+                    tc::wait_st();
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::bar_arrive(wbar + 8 * x);
+                }
+                slot += whole * (Y::kK + Y::kV);
+                slot = slot % (2 * Y::kSlots);     // its parity counts, too
+                if (steps) {
+                    dead = dead || !tc::bar_wait(obar + 8 * x, ophase, limit);
+                    ophase ^= 1u;
+                    tc::fence_after();
+                }
+                const bool nan = row && *(volatile int *)&s_odd[piece & 3] < hi;
+                const float by = nan ? NAN : sum == 0.f ? 0.f : 1.f / sum;
+                uint16_t *dst = a.out[p.r] + (long long)(p.first + min(i, p.count - 1)) * a.ots + (long long)p.h * a.ohs;
+#pragma unroll
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t o[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        o[e] = 0;
+                    if (steps) {
+                        tc::ld16(o, tO + c);
+                        tc::wait_ld(o);
+                    }
+                    uint32_t y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        y[e] = tc::bf16x2(__uint_as_float(o[2 * e]) * by, __uint_as_float(o[2 * e + 1]) * by);
+                    if (row)
+                        tc::st32(dst + c, y);
+                }
+                tc::fence_before();
+                __syncwarp();
+            }
+            if (dead && lane == 0)
+                sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
+        }
+        sfar_attn_padding<D>(a, tid, 32 * kSoftWarps);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+        if (warp == kCopyWarp) {
+            // ------------------------------------------------------------ copies
+            const uint64_t often = tc::evict_last(), once = tc::evict_first();
+            auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(SFAR_FULL, tc::bar_wait(bar, parity, limit)); };
+            tc::Ring<Y::kSlots> st;
+            tc::Ring<kPieces> ps;
+            bool dead = false;
+            uint32_t boxes = 0, taken = blockIdx.x, qphase[2] = {1, 1}, queries[2] = {0, 0};     // queries: asked for
+            const int groups = (a.B + kGroup - 1) / kGroup;
+            const uint32_t planes = (uint32_t)(a.R * a.Hq), wrap = items - 1;
+            for (; !dead;) {
+                Piece p;
+                p.b = -1;
+                const bool end = taken >= items;
+                // the next one is asked for early: one question for each row tile, so the counter is back at 0 when all are taken
+                uint32_t after = 0;
+                if (!end && lane == 0)
+                    asm volatile("atom.relaxed.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(after) : "l"(a.next), "r"(wrap) : "memory");
+                if (!end) {
+                    int lo = 0, hi = groups;
+                    while (hi - lo > 1) {
+                        const int mid = (lo + hi) >> 1;
+                        if (upto[mid] * planes <= taken)
+                            lo = mid;
+                        else
+                            hi = mid;
+                    }
+                    uint32_t v = taken - upto[lo] * planes;
+                    const int b = lo * kGroup + lane;
+                    int len = 0, count = 0, first = 0, kfirst = 0;
+                    if (b < a.B)
+                        request(a, b, len, count, first, kfirst);
+                    const uint32_t n = (uint32_t)(count + kRows - 1) / kRows;
+                    uint32_t sum = n;
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const uint32_t o = __shfl_up_sync(SFAR_FULL, sum, d);
+                        if (lane >= d)
+                            sum += o;
+                    }
+                    const unsigned past = __ballot_sync(SFAR_FULL, sum * planes > v);
+                    const int l = past ? __ffs(past) - 1 : 0;
+                    p.b = lo * kGroup + l;
+                    p.len = __shfl_sync(SFAR_FULL, len, l);
+                    p.count = __shfl_sync(SFAR_FULL, count, l);
+                    p.first = __shfl_sync(SFAR_FULL, first, l);
+                    p.kfirst = __shfl_sync(SFAR_FULL, kfirst, l);
+                    const uint32_t tiles = max(1u, __shfl_sync(SFAR_FULL, n, l));
+                    v -= __shfl_sync(SFAR_FULL, sum - n, l) * planes;
+                    const uint32_t plane = v / tiles;
+                    p.rt = (int)(tiles - 1 - (v - plane * tiles));
+                    p.r = (int)(plane / (uint32_t)a.Hq);
+                    p.h = (int)(plane - (uint32_t)p.r * (uint32_t)a.Hq);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int from = p.rt * kRows + x * 128, last = min(p.count, from + 128) - 1;      // tile's last row
+                        p.steps[x] = x < TILES && from < p.count ? (max(0, p.len - p.count + last + 1) + kTile - 1) / kTile : 0;
+                    }
+                }
+                if (!wait(pempty + 8 * ps.slot, ps.phase ^ 1u)) {
+                    dead = true;
+                    break;
+                }
+                if (lane == 0) {
+                    s_piece[ps.slot] = p;
+                    tc::bar_arrive(pfull + 8 * ps.slot);
+                }
+                ps.next();
+                if (end)
+                    break;
+                const int steps = max(p.steps[0], p.steps[1]);
+                for (int k = 0; k < steps && !dead; ++k)
+                    for (int c = 0; c < Y::kK + Y::kV; ++c) {
+                        if (!wait(empty + 8 * st.slot, st.phase ^ 1u)) {
+                            dead = true;
+                            break;
+                        }
+                        if (lane == 0) {
+                            const uint32_t bar = full + 8 * st.slot, dst = ring + st.slot * kBox;
+                            const int y = p.kfirst + k * kTile;
+                            tc::bar_expect(bar, kBox);
+                            if (c < Y::kV)
+                                tc::load_3d(dst, &a.kmap[p.r], 64 * c, p.h, y, bar, often);
+                            else if (c == Y::kV)
+                                tc::load_2d(dst, &a.krmap[p.r], 0, y, bar, often);
+                            else
+                                tc::load_3d(dst, &a.vmap[p.r], 64 * (c - Y::kK), p.h, y, bar, often);
+                        }
+                        ++boxes;
+                        st.next();
+                        if (k == 0 && c == Y::kV) {
+                            // the queries, once the last piece's scores are done with theirs
+                            for (int x = 0; x < TILES && !dead; ++x)
+                                if (p.steps[x]) {
+                                    if (!wait(qempty + 8 * x, qphase[x])) {
+                                        dead = true;
+                                        break;
+                                    }
+                                    qphase[x] ^= 1u;
+                                    ++queries[x];
+                                    if (lane == 0) {
+                                        tc::bar_expect(qfull + 8 * x, Y::kK * kBox);
+                                        for (int i = 0; i < Y::kK; ++i)
+                                            tc::load_3d(mem + (x * Y::kK + i) * kBox, &a.qmap[p.r], 64 * i, p.h, p.first + p.rt * kRows + x * 128,
+                                                        qfull + 8 * x, once);
+                                    }
+                                }
+                            if (dead)
+                                break;
+                        }
+                    }
+                taken = gridDim.x + __shfl_sync(SFAR_FULL, after, 0);
+            }
+            if (dead && lane == 0) {
+                sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
+                // the copies in flight land before the shared memory is released
+                for (uint32_t i = boxes - min(boxes, (uint32_t)Y::kSlots); i < boxes; ++i)
+                    tc::bar_wait(full + 8 * (i % Y::kSlots), (i / Y::kSlots) & 1u, limit);
+                for (int x = 0; x < TILES; ++x)
+                    if (queries[x])
+                        tc::bar_wait(qfull + 8 * x, (queries[x] - 1) & 1u, limit);
+            }
+        } else if (warp == kMmaWarp) {
+            // -------------------------------------------------------------- MMAs
+            constexpr uint32_t idS = tc::idesc_bf16(128, 128), idO = tc::idesc_bf16(128, D) | tc::kTransposeB;
+            const uint64_t dq = tc::desc_k128(mem), dk = tc::desc_k128(ring);
+            tc::Ring<kPieces> ps;
+            uint32_t qphase[2] = {0, 0}, wphase[2] = {0, 0}, slot = 0;     // slot: boxes before this step's keys, modulo 2 kSlots
+            bool dead = false;
+            for (;;) {
+                dead = __any_sync(SFAR_FULL, dead || !tc::bar_wait(pfull + 8 * ps.slot, ps.phase, limit));
+                if (dead)
+                    break;
+                const int n[2] = {s_piece[ps.slot].steps[0], s_piece[ps.slot].steps[1]}, b = s_piece[ps.slot].b;
+                __syncwarp();
+                if (lane == 0)
+                    tc::bar_arrive(pempty + 8 * ps.slot);
+                ps.next();
+                if (b < 0)
+                    break;
+                if (tc::elect_one()) {             // the same lane every time: the phases stay in its registers
+                    const int most = max(n[0], n[1]);
+                    auto there = [&](uint32_t at) { return tc::bar_wait(full + 8 * (at % Y::kSlots), at / Y::kSlots & 1u, limit); };
+                    auto wait = [&](uint32_t bar, uint32_t &phase) {
+                        const bool in = tc::bar_wait(bar, phase, limit);
+                        phase ^= 1u;
+                        return in;
+                    };
+                    uint32_t keys = slot, values = 0;              // boxes before step k's keys, before the values of the one before
+                    for (int k = 0; k <= most && !dead; ++k) {
+#pragma unroll
+                        for (int x = 0; x < TILES; ++x) {
+                            const uint32_t tS = tmem + x * 256;
+                            if (k && k <= n[x]) {
+                                // O += P V of the step before
+                                dead = dead || !wait(wbar + 8 * x, wphase[x]);
+#pragma unroll
+                                for (int c = 0; c < Y::kV; ++c)
+                                    dead = dead || !there(values + c);
+                                if (dead)
+                                    break;
+                                tc::fence_after();
+                                const uint32_t v0 = values % Y::kSlots, v1 = (values + 1) % Y::kSlots;
+                                if (D == 64 || v1 == v0 + 1) {
+                                    // both boxes side by side: one product for all the head
+                                    const uint64_t dv = tc::desc_n128(ring + v0 * kBox, kBox);
+#pragma unroll
+                                    for (int i = 0; i < kTile / 16; ++i)
+                                        tc::mma_f16_ts(tS + 128, tS + 8 * i, dv + 128 * i, idO, k > 1 || i > 0);
+                                } else {
+                                    constexpr uint32_t idH = tc::idesc_bf16(128, 64) | tc::kTransposeB;
+#pragma unroll
+                                    for (int c = 0; c < 2; ++c) {
+                                        const uint64_t dv = tc::desc_n128(ring + (c ? v1 : v0) * kBox, kBox);
+#pragma unroll
+                                        for (int i = 0; i < kTile / 16; ++i)
+                                            tc::mma_f16_ts(tS + 128 + 64 * c, tS + 8 * i, dv + 128 * i, idH, k > 1 || i > 0);
+                                    }
+                                }
+                                if (k == n[x])
+                                    tc::commit(obar + 8 * x);
+                            }
+                            if (k < n[x]) {
+                                // S = Q K^T + Qr Kr^T
+                                dead = dead || (k == 0 && !wait(qfull + 8 * x, qphase[x]));
+#pragma unroll
+                                for (int c = 0; c < Y::kK; ++c) {
+                                    dead = dead || !there(keys + c);
+                                    if (dead)
+                                        break;
+                                    tc::fence_after();
+                                    const uint64_t d = dk + (keys + c) % Y::kSlots * (kBox >> 4), q = dq + (x * Y::kK + c) * (kBox >> 4);
+                                    const int parts = c < Y::kV ? 4 : a.rope / 16;
+                                    for (int i = 0; i < parts; ++i)
+                                        tc::mma_f16_ss(tS, q + 2 * i, d + 2 * i, idS, c + i > 0);
+                                }
+                                if (dead)
+                                    break;
+                                tc::commit(sbar + 8 * x);
+                                if (k == n[x] - 1)
+                                    tc::commit(qempty + 8 * x);
+                            }
+                        }
+                        if (dead)
+                            break;
+                        if (k)
+#pragma unroll
+                            for (int c = 0; c < Y::kV; ++c)
+                                tc::commit(empty + 8 * ((values + c) % Y::kSlots));
+                        if (k < most)
+#pragma unroll
+                            for (int c = 0; c < Y::kK; ++c)
+                                tc::commit(empty + 8 * ((keys + c) % Y::kSlots));
+                        values = keys + Y::kK;
+                        keys += Y::kK + Y::kV;
+                    }
+                    slot = (slot + (uint32_t)most * (Y::kK + Y::kV)) % (2 * Y::kSlots);
+                }
+                dead = __any_sync(SFAR_FULL, dead);
+            }
+            if (tc::elect_one()) {
+                if (dead)
+                    sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
+                // every MMA and every arrival it causes is done before the CTA leaves
+                tc::commit(drain);
+                tc::bar_wait(drain, 0, limit);
+            }
+        }
+    }
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp)
+        tc::tmem_free<1>(tmem, 256 * TILES);
+}
+
+const void *sfar_kernel_latent_prompt(int head_dim, int tiles, int *threads, int *smem)
+{
+#define SFAR_PROMPT(D, N) (*smem = Lay<D, N>::kBytes + 1024, (const void *)k_latent_prompt<D, N>)
+    *threads = kThreads;
+    if (tiles == 1)
+        return head_dim == 64 ? SFAR_PROMPT(64, 1) : SFAR_PROMPT(128, 1);
+    return head_dim == 64 ? SFAR_PROMPT(64, 2) : SFAR_PROMPT(128, 2);
+#undef SFAR_PROMPT
+}

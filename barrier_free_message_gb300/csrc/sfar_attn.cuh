@@ -1,4 +1,4 @@
-// sfar_attn.cuh -- what the two attention kernels share.
+// sfar_attn.cuh -- what the attention kernels share.  A: a kernel's parameters.
 #pragma once
 #include "sfar_kv_args.h"
 #include "sfar_kv_device.cuh"
@@ -41,7 +41,7 @@ __device__ __forceinline__ int sfar_attn_from(const SfarAttnArgs &a, int pos)
     return a.window ? max(0, max(pos, -1) - a.window + 1) : 0;
 }
 // Request b: its context, how many new tokens it has and the row of the first.
-__device__ __forceinline__ void sfar_attn_request(const SfarAttnArgs &a, int b, int &len, int &count, int &first)
+template <class A> __device__ __forceinline__ void sfar_attn_request(const A &a, int b, int &len, int &count, int &first)
 {
     const long long most = min((long long)a.W << a.shift, (long long)INT_MAX - 1024);
     len = (int)max(0ll, min((long long)a.lens[b], most));
@@ -50,7 +50,7 @@ __device__ __forceinline__ void sfar_attn_request(const SfarAttnArgs &a, int b, 
     count = s < 0 || e < s || e > a.T ? 0 : e - s;
 }
 // Records what sfar_attn_request had to correct.
-__device__ __forceinline__ void sfar_attn_check(const SfarAttnArgs &a, int b, int len, int count, int first)
+template <class A> __device__ __forceinline__ void sfar_attn_check(const A &a, int b, int len, int count, int first)
 {
     if (a.lens[b] != len)
         sfar_kv_fault(a.ctl, b, SFAR_KV_BAD_LENGTH);
@@ -60,7 +60,7 @@ __device__ __forceinline__ void sfar_attn_check(const SfarAttnArgs &a, int b, in
 // Offsets in no order can give the requests more row tiles together than the
 // step has (and the line more units than its 32-bit sums hold, which the host
 // bounds for a step's): nothing is computed then.
-__device__ __forceinline__ bool sfar_attn_many(const SfarAttnArgs &a, long long row_tiles)
+template <class A> __device__ __forceinline__ bool sfar_attn_many(const A &a, long long row_tiles)
 {
     if (row_tiles > a.most && blockIdx.x == 0 && threadIdx.x == 0)
         sfar_kv_fault(a.ctl, a.B, SFAR_KV_BAD_TOKENS);
@@ -68,7 +68,7 @@ __device__ __forceinline__ bool sfar_attn_many(const SfarAttnArgs &a, long long 
 }
 // Zeros for the rows past the last request, by the whole grid; this thread is
 // `thread` of the `threads` that its CTA has for it (or of fewer than another's).
-template <int D> __device__ __forceinline__ void sfar_attn_padding(const SfarAttnArgs &a, int thread, int threads)
+template <int D, class A> __device__ __forceinline__ void sfar_attn_padding(const A &a, int thread, int threads)
 {
     const long long rows = (long long)(a.T - max(0, min(a.starts[a.B], a.T))) * a.Hq * a.R;
     for (long long i = blockIdx.x + (long long)thread * gridDim.x; i < rows; i += (long long)gridDim.x * threads) {
@@ -118,7 +118,7 @@ struct SfarJoin {
     int c0, c1;
     int lo, hi, step;               // parts lo, lo + step .. hi are joined next
     int *counter;                   // of those that have come
-    __device__ __forceinline__ SfarJoin(const SfarAttnArgs &a, int kind, int first, int last, int me) : c0(first), c1(last)
+    template <class A> __device__ __forceinline__ SfarJoin(const A &a, int kind, int first, int last, int me) : c0(first), c1(last)
     {
         // three sets of counters: of groups that begin a row tile, of others (their first CTA begins no other row
         // tile's second group), of the groups of a row tile; index: the first CTA
@@ -143,7 +143,7 @@ struct SfarJoin {
         return come == all;         // the last has set the counter back to 0, for the next call
     }
     // on to the groups; false: these were all
-    __device__ __forceinline__ bool next(const SfarAttnArgs &a, int kind)
+    template <class A> __device__ __forceinline__ bool next(const A &a, int kind)
     {
         if (!up)
             return false;

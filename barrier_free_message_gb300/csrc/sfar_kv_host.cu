@@ -14,6 +14,7 @@
 #include "sfar_fp8.h"
 #include "sfar_kv.h"
 #include "sfar_kv_args.h"
+#include "sfar_launch.h"
 #include "sfar_test.h"
 
 struct sfar_kv {
@@ -33,9 +34,6 @@ struct sfar_kv {
 };
 
 namespace {
-
-size_t ceil_div(size_t x, size_t a) { return (x + a - 1) / a; }
-bool aligned(const void *p, uintptr_t a) { return p && ((uintptr_t)p & (a - 1)) == 0; }
 
 // Up to this many tokens the projection runs with outputs along the tensor
 // core's lanes (weights read once, HBM-bound), beyond it with tokens there.
@@ -63,52 +61,65 @@ const size_t kFewRows = 32;
 // Counters of parts: six sets of one for each of the most CTAs of any of the kernels (3 per SM).
 size_t arrived_bytes(int sms) { return 6 * 3 * (size_t)sms * sizeof(int); }
 
-struct Span {
-    uintptr_t lo, hi;
-    Span(const void *p, size_t bytes) : lo((uintptr_t)p), hi((uintptr_t)p + bytes) {}
-    bool meets(const Span &o) const { return lo < o.hi && o.lo < hi; }
-};
+}  // namespace
 
-// Launches f as a programmatic dependent of the kernel before it on the
-// stream (every kernel here begins with griddepcontrol.wait); plain: without.
-sfar_status launch(int dev, const void *f, dim3 grid, unsigned threads, size_t smem, void *args, sfar_stream_t s, bool plain = false,
-                   unsigned cluster = 1)
+bool sfar_pool_prepare(unsigned *plan_ctas)
 {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = (cudaStream_t)s;
-    cudaLaunchAttribute attr[2];
-    unsigned n = 0;
-    if (!plain) {
-        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[n++].val.programmaticStreamSerializationAllowed = 1;
-    }
-    if (cluster > 1) {
-        attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = cluster;
-        attr[n].val.clusterDim.y = 1;
-        attr[n++].val.clusterDim.z = 1;
-    }
-    cfg.attrs = attr;
-    cfg.numAttrs = n;
-    void *params[] = {args};
-    int cur = -1;
-    cudaGetDevice(&cur);
-    if (cur != dev)
-        cudaSetDevice(dev);
-    const cudaError_t err = cudaLaunchKernelExC(&cfg, f, params);
-    if (cur != dev && cur >= 0)
-        cudaSetDevice(cur);
-    if (err != cudaSuccess) {
+    if (cudaFuncSetAttribute(sfar_kernel_kv_plan(), cudaFuncAttributeMaxDynamicSharedMemorySize, (4 * SFAR_KV_MAX_REQUESTS + 1) * 4) !=
+        cudaSuccess) {
         cudaGetLastError();
-        return SFAR_ERR_CUDA;
+        return false;
     }
-    return SFAR_OK;
+    // a large plan takes a cluster of 16 where the device can place one
+    if (cudaFuncSetAttribute(sfar_kernel_kv_plan(), cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2 * SFAR_PLAN_CLUSTER;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(2 * SFAR_PLAN_CLUSTER);
+        cfg.blockDim = dim3(SFAR_PLAN_THREADS);
+        cfg.dynamicSmemBytes = (4 * SFAR_KV_MAX_REQUESTS + 1) * 4;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, sfar_kernel_kv_plan(), &cfg) == cudaSuccess && clusters > 0)
+            *plan_ctas = 2 * SFAR_PLAN_CLUSTER;
+    }
+    cudaGetLastError();
+    return true;
 }
 
-}  // namespace
+sfar_status sfar_pool_plan(const SfarPool &h, const int32_t *lens, const int32_t *delta, int32_t *table, int32_t *ring,
+                           const int32_t *state, int32_t *lens_out, int32_t *state_out, int32_t *starts, int32_t *slots,
+                           int32_t *taken, size_t requests, size_t table_width, size_t tokens, sfar_stream_t s)
+{
+    if (requests == 0 || requests > SFAR_KV_MAX_REQUESTS || table_width == 0 || table_width >= (1ull << 31) ||
+        tokens >= (1ull << 31) || (tokens && !aligned(slots, 4)))
+        return SFAR_ERR_INVALID;
+    const Span spans[] = {Span(lens, requests * 4), Span(delta, requests * 4), Span(table, requests * table_width * 4),
+                          Span(ring, h.pages * 4), Span(state, 8), Span(lens_out, requests * 4), Span(state_out, 8),
+                          Span(starts, requests * 4 + 4), Span(slots, tokens * 4), Span(taken, requests * 4)};
+    const int n = (int)(sizeof spans / sizeof spans[0]);
+    for (int i = 0; i < n; ++i) {
+        if (i != 8 && !aligned((const void *)spans[i].lo, 4))
+            return SFAR_ERR_INVALID;
+        for (int j = 0; j < i; ++j)
+            if (spans[i].meets(spans[j]) && !((i == 5 && j == 0) || (i == 6 && j == 4)))
+                return SFAR_ERR_INVALID;
+    }
+    if ((lens_out != lens && spans[5].meets(spans[0])) || (state_out != state && spans[6].meets(spans[4])))
+        return SFAR_ERR_INVALID;
+    SfarKvPlanArgs a{lens,  delta, table,  ring,          state,            lens_out,    state_out, starts,
+                     slots, taken, h.ctl, (int)requests, (int)table_width, (int)tokens, h.shift,  (int)h.pages};
+    // Small steps run on 8 CTAs of 256 threads, a request to a thread; large ones on all the CTAs that a cluster can have, of
+    // 1024: their time is that of the instructions of the slots and pages.  Small and large form, us: requests of one token,
+    // 64: 3.2, 4.0; 256: 3.5, 4.2; 257: 4.2, 4.2; 512: 4.6, 4.6; 1024: 6.3, 5.4; 8192: 32, 18.  16 requests with 1412 tokens
+    // 4.5, 4.7; 128 with 2533 4.6, 4.9; 256 with 1767 5.7, 4.9, with 3088 4.9, 4.8, with 7118 6.6, 4.9; 64 with 7156 4.6, 4.6.
+    const bool small = requests <= 256 && tokens <= 4096;
+    const unsigned cluster = small ? SFAR_PLAN_CLUSTER : h.plan_ctas;
+    return launch(h.dev, sfar_kernel_kv_plan(), dim3(cluster), small ? 256 : SFAR_PLAN_THREADS, (4 * requests + 1) * 4, &a, s, false, cluster);
+}
 
 extern "C" {
 
@@ -191,11 +202,7 @@ sfar_kv_t *sfar_kv_create(int R, int q_heads, int kv_heads, int head_dim, int pa
     h->ctl = reinterpret_cast<SfarCtl *>(h->ws);
     h->arrived = reinterpret_cast<int *>(h->ws + o_arrived);
     h->part = reinterpret_cast<float *>(h->ws + o_part);
-    SfarCtl init;
-    memset(&init, 0, sizeof init);
-    init.timeout_ns = 1000000000ull;
-    init.strag_rank = init.drop_rank = -1;
-    init.f_rank = init.f_cta = init.f_peer = -1;
+    const SfarCtl init = fresh_ctl();
     int threads = 0, smem = 0;
     int pthreads = 0, psmem = 0;
     const void *prompt = sfar_kernel_kv_prompt(head_dim, &pthreads, &psmem);
@@ -207,30 +214,11 @@ sfar_kv_t *sfar_kv_create(int R, int q_heads, int kv_heads, int head_dim, int pa
         cudaFuncSetAttribute(sfar_kernel_kv_attn(head_dim, 16, &threads, &smem), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem + (SFAR_KV_MAX_REQUESTS + 1) * 4) != cudaSuccess ||
         cudaStreamCreateWithFlags(&h->priv, cudaStreamNonBlocking) != cudaSuccess ||
-        cudaMallocHost(&h->host_ctl, sizeof(SfarCtl)) != cudaSuccess ||
-        cudaFuncSetAttribute(sfar_kernel_kv_plan(), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (4 * SFAR_KV_MAX_REQUESTS + 1) * 4) != cudaSuccess) {
+        cudaMallocHost(&h->host_ctl, sizeof(SfarCtl)) != cudaSuccess || !sfar_pool_prepare(&h->plan_ctas)) {
         cudaGetLastError();
         sfar_kv_destroy(h);
         return fail(SFAR_ERR_CUDA);
     }
-    // a large plan takes a cluster of 16 where the device can place one
-    if (cudaFuncSetAttribute(sfar_kernel_kv_plan(), cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
-        cudaLaunchAttribute attr;
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = 2 * SFAR_PLAN_CLUSTER;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(2 * SFAR_PLAN_CLUSTER);
-        cfg.blockDim = dim3(SFAR_PLAN_THREADS);
-        cfg.dynamicSmemBytes = (4 * SFAR_KV_MAX_REQUESTS + 1) * 4;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        int clusters = 0;
-        if (cudaOccupancyMaxActiveClusters(&clusters, sfar_kernel_kv_plan(), &cfg) == cudaSuccess && clusters > 0)
-            h->plan_ctas = 2 * SFAR_PLAN_CLUSTER;
-    }
-    cudaGetLastError();
     sfar_set_last_error(SFAR_OK);
     return h;
 }
@@ -259,31 +247,10 @@ sfar_status sfar_kv_plan(sfar_kv_t *h, const int32_t *lens, const int32_t *delta
                          const int32_t *state, int32_t *lens_out, int32_t *state_out, int32_t *starts, int32_t *slots,
                          int32_t *taken, size_t requests, size_t table_width, size_t tokens, sfar_stream_t s)
 {
-    if (!h || requests == 0 || requests > SFAR_KV_MAX_REQUESTS || table_width == 0 || table_width >= (1ull << 31) ||
-        tokens >= (1ull << 31) || (tokens && !aligned(slots, 4)))
+    if (!h)
         return SFAR_ERR_INVALID;
-    const Span spans[] = {Span(lens, requests * 4), Span(delta, requests * 4), Span(table, requests * table_width * 4),
-                          Span(ring, h->pages * 4), Span(state, 8), Span(lens_out, requests * 4), Span(state_out, 8),
-                          Span(starts, requests * 4 + 4), Span(slots, tokens * 4), Span(taken, requests * 4)};
-    const int n = (int)(sizeof spans / sizeof spans[0]);
-    for (int i = 0; i < n; ++i) {
-        if (i != 8 && !aligned((const void *)spans[i].lo, 4))
-            return SFAR_ERR_INVALID;
-        for (int j = 0; j < i; ++j)
-            if (spans[i].meets(spans[j]) && !((i == 5 && j == 0) || (i == 6 && j == 4)))
-                return SFAR_ERR_INVALID;
-    }
-    if ((lens_out != lens && spans[5].meets(spans[0])) || (state_out != state && spans[6].meets(spans[4])))
-        return SFAR_ERR_INVALID;
-    SfarKvPlanArgs a{lens,  delta, table,  ring,          state,            lens_out,    state_out, starts,
-                     slots, taken, h->ctl, (int)requests, (int)table_width, (int)tokens, h->shift,  (int)h->pages};
-    // Small steps run on 8 CTAs of 256 threads, a request to a thread; large ones on all the CTAs that a cluster can have, of
-    // 1024: their time is that of the instructions of the slots and pages.  Small and large form, us: requests of one token,
-    // 64: 3.2, 4.0; 256: 3.5, 4.2; 257: 4.2, 4.2; 512: 4.6, 4.6; 1024: 6.3, 5.4; 8192: 32, 18.  16 requests with 1412 tokens
-    // 4.5, 4.7; 128 with 2533 4.6, 4.9; 256 with 1767 5.7, 4.9, with 3088 4.9, 4.8, with 7118 6.6, 4.9; 64 with 7156 4.6, 4.6.
-    const bool small = requests <= 256 && tokens <= 4096;
-    const unsigned cluster = small ? SFAR_PLAN_CLUSTER : h->plan_ctas;
-    return launch(h->dev, sfar_kernel_kv_plan(), dim3(cluster), small ? 256 : SFAR_PLAN_THREADS, (4 * requests + 1) * 4, &a, s, false, cluster);
+    return sfar_pool_plan(SfarPool{h->dev, h->shift, h->pages, h->ctl, h->plan_ctas}, lens, delta, table, ring, state, lens_out,
+                          state_out, starts, slots, taken, requests, table_width, tokens, s);
 }
 
 sfar_status sfar_kv_append(sfar_kv_t *h, const void *const k[], const void *const v[], const int32_t *slots,
@@ -416,22 +383,7 @@ sfar_status sfar_kv_status_get(sfar_kv_t *h, sfar_fault *info)
 {
     if (!h)
         return SFAR_ERR_INVALID;
-    if (cudaMemcpyAsync(h->host_ctl, h->ctl, 32, cudaMemcpyDeviceToHost, h->priv) != cudaSuccess ||
-        cudaStreamSynchronize(h->priv) != cudaSuccess) {
-        cudaGetLastError();
-        return SFAR_ERR_CUDA;
-    }
-    const SfarCtl *c = h->host_ctl;
-    const sfar_status code = (sfar_status)c->status;
-    if (info) {
-        info->code = code;
-        info->rank = code ? c->f_rank : -1;
-        info->cta = code ? c->f_cta : -1;
-        info->peer = code ? c->f_peer : -1;
-        info->epoch = code ? c->f_epoch : 0;
-        info->where = code ? c->f_where : 0;
-    }
-    return code;
+    return read_ctl(h->ctl, h->host_ctl, h->priv, info);
 }
 
 sfar_status sfar_kv_reset(sfar_kv_t *h, sfar_stream_t s)

@@ -186,6 +186,8 @@ __device__ __forceinline__ void ld32(uint32_t (&v)[32], uint32_t addr)
         : "r"(addr));
 }
 #undef SFAR_R4
+__device__ __forceinline__ void ld(uint32_t (&v)[16], uint32_t addr) { ld16(v, addr); }
+__device__ __forceinline__ void ld(uint32_t (&v)[32], uint32_t addr) { ld32(v, addr); }
 __device__ __forceinline__ void st16(uint32_t addr, const uint32_t (&v)[16])
 {
     asm volatile(
@@ -247,6 +249,20 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
                  "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
                  : "memory");
 }
+// the same with both operands in shared memory
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+                 : "memory");
+}
+// Instruction descriptor: binary32 accumulator, both operands K-major bf16; kTransposeA, kTransposeB: M- or N-major.
+__host__ __device__ constexpr uint32_t idesc_bf16(int m, int n)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+constexpr uint32_t kTransposeA = 1u << 15, kTransposeB = 1u << 16;
 // arrives on bar when every MMA issued so far by this thread is complete
 __device__ __forceinline__ void commit(uint32_t bar)
 {

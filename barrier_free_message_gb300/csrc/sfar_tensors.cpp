@@ -1,4 +1,5 @@
-// sfar_tensors.cpp -- the Python calls of include/sfar_kv.h and sfar_fp8.h:
+// sfar_tensors.cpp -- the Python calls of include/sfar_kv.h, sfar_fp8.h,
+// sfar_rope.h and sfar_latent.h:
 // checks torch tensors, takes their pointers, sizes and strides, and makes the
 // C call on the stream.
 //
@@ -20,9 +21,12 @@
 #include <initializer_list>
 #include <stdexcept>
 #include <string>
+#include <type_traits>
 
 #include "sfar_fp8.h"
 #include "sfar_kv.h"
+#include "sfar_latent.h"
+#include "sfar_rope.h"
 
 namespace {
 
@@ -33,6 +37,12 @@ decltype(&sfar_kv_append) c_append;
 decltype(&sfar_kv_attention) c_attention;
 decltype(&sfar_quantize_fp8) c_quantize;
 decltype(&sfar_rowpar_gemm_fp8) c_gemm;
+decltype(&sfar_rope) c_rope;
+decltype(&sfar_latent_plan) c_latent_plan;
+decltype(&sfar_latent_append) c_latent_append;
+decltype(&sfar_latent_gather) c_latent_gather;
+decltype(&sfar_latent_attention) c_latent_attention;
+decltype(&sfar_latent_prompt) c_latent_prompt;
 
 struct PythonError {};                  // an exception is set already
 
@@ -200,19 +210,21 @@ template <class F> sfar_status released(F call)
 }
 
 // (handle, pages, lens, delta, table, ring, state, lens_out, state_out, starts, slots, taken, stream)
-PyObject *plan(PyObject *, PyObject *const *a, Py_ssize_t n)
+template <class H, class F> PyObject *plan_of(F *const &call, PyObject *const *a, Py_ssize_t n)
 {
     return guarded(n, 13, [&] {
-        const auto h = static_cast<sfar_kv_t *>(handle_of(a[0]));
+        const auto h = static_cast<H *>(handle_of(a[0]));
         const int64_t pages = number(a[1]), B = size(a[2], 1, 0, "lens"), W = size(a[4], 2, 1, "table"), T = size(a[10], 1, 0, "slots");
         int32_t *lens = ints(a[2], {B}, "lens"), *delta = ints(a[3], {B}, "delta"), *table = ints(a[4], {B, W}, "table"),
                 *ring = ints(a[5], {pages}, "ring"), *state = ints(a[6], {2}, "state"), *lens_out = ints(a[7], {B}, "lens_out"),
                 *state_out = ints(a[8], {2}, "state_out"), *starts = ints(a[9], {B + 1}, "starts"), *slots = ints(a[10], {T}, "slots"),
                 *taken = ints(a[11], {B}, "taken");
         const sfar_stream_t s = stream_of(a[12]);
-        return released([&] { return c_plan(h, lens, delta, table, ring, state, lens_out, state_out, starts, slots, taken, B, W, T, s); });
+        return released([&] { return call(h, lens, delta, table, ring, state, lens_out, state_out, starts, slots, taken, B, W, T, s); });
     });
 }
+PyObject *plan(PyObject *, PyObject *const *a, Py_ssize_t n) { return plan_of<sfar_kv_t>(c_plan, a, n); }
+PyObject *latent_plan(PyObject *, PyObject *const *a, Py_ssize_t n) { return plan_of<sfar_latent_t>(c_latent_plan, a, n); }
 
 // (handle, R, kv_heads, head_dim, k, v, slots, stream)
 PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n)
@@ -297,6 +309,144 @@ PyObject *gemm(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
+// a contiguous fp32 or bf16 vector of this length
+const void *vector_of(PyObject *x, at::ScalarType type, int64_t n, const char *what)
+{
+    const at::Tensor &t = tensor(x, what);
+    if (t.scalar_type() != type || t.dim() != 1 || t.size(0) != n || !t.is_contiguous() || !t.is_cuda())
+        wrong(std::string(what) + ": need a contiguous " + (type == at::kFloat ? "float32" : "bfloat16") + " tensor of shape [" +
+              std::to_string(n) + "] on the GPU");
+    return t.data_ptr();
+}
+float real(PyObject *x)
+{
+    const double v = PyFloat_AsDouble(x);
+    if (PyErr_Occurred())
+        throw PythonError();
+    return (float)v;
+}
+
+// (handle, R, fp32, q, q_out, k or None, k_out or None, pos, freq, layout, scale, stream)
+PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 12, [&] {
+        const auto h = static_cast<sfar_t *>(handle_of(a[0]));
+        const int R = (int)number(a[1]);
+        const Type type = number(a[2]) ? kF32 : kBf16;
+        const Ranks q(a[3], R, 3, type, "q"), qo(a[4], R, 3, type, "q_out");
+        const int64_t T = q.shape[0], rot = q.shape[2];
+        if (!qo.same({T, q.shape[1], rot}))
+            wrong("rope: q_out must have the shape of q, [tokens, heads, rotated part] per rank");
+        const bool keys = a[5] != Py_None;
+        if (keys != (a[6] != Py_None))
+            wrong("rope: need both of k and k_out, or none");
+        const Ranks k(keys ? a[5] : a[3], R, 3, type, "k"), ko(keys ? a[6] : a[4], R, 3, type, "k_out");
+        const int64_t K = keys ? k.shape[1] : 0;
+        if (keys && (!k.same({T, K, rot}) || !ko.same({T, K, rot})))
+            wrong("rope: need k and k_out of shape [" + std::to_string(T) + ", heads, " + std::to_string(rot) + "] per rank");
+        const int32_t *pos = ints(a[7], {T}, "pos");
+        const auto freq = static_cast<const float *>(vector_of(a[8], at::kFloat, rot / 2, "freq"));
+        const int layout = (int)number(a[9]);
+        const float scale = real(a[10]);
+        const sfar_stream_t s = stream_of(a[11]);
+        return released([&] {
+            return c_rope(h, q.ptr, const_cast<void *const *>(qo.ptr), k.ptr, const_cast<void *const *>(ko.ptr), pos, freq, T, q.shape[1], K,
+                          rot, q.stride[0], q.stride[1], qo.stride[0], qo.stride[1], k.stride[0], k.stride[1], ko.stride[0], ko.stride[1],
+                          layout, scale, s);
+        });
+    });
+}
+
+// (handle, R, latent_dim, rope_dim, x, weight, pos, freq, slots, eps, layout, scale, stream)
+PyObject *latent_append(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 13, [&] {
+        const auto h = static_cast<sfar_latent_t *>(handle_of(a[0]));
+        const int R = (int)number(a[1]);
+        const int64_t L = number(a[2]), rope = number(a[3]), T = size(a[8], 1, 0, "slots");
+        const Ranks x(a[4], R, 2, kBf16, "x");
+        if (!x.same({T, L + rope}))
+            wrong("append: need x of shape [" + std::to_string(T) + ", " + std::to_string(L + rope) + "] per rank");
+        const void *weight = vector_of(a[5], at::kBFloat16, L, "weight");
+        const int32_t *pos = ints(a[6], {T}, "pos"), *slots = ints(a[8], {T}, "slots");
+        const auto freq = static_cast<const float *>(vector_of(a[7], at::kFloat, rope / 2, "freq"));
+        const float eps = real(a[9]), scale = real(a[11]);
+        const int layout = (int)number(a[10]);
+        const sfar_stream_t s = stream_of(a[12]);
+        return released([&] { return c_latent_append(h, x.ptr, weight, pos, freq, slots, T, x.stride[0], eps, layout, scale, s); });
+    });
+}
+
+// (handle, R, row, out, table, lens, starts, stream)
+PyObject *latent_gather(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 8, [&] {
+        const auto h = static_cast<sfar_latent_t *>(handle_of(a[0]));
+        const int R = (int)number(a[1]);
+        const int64_t W = number(a[2]);
+        const Ranks out(a[3], R, 2, kBf16, "out");
+        const int64_t T = out.shape[0];
+        if (!out.same({T, W}))
+            wrong("gather: need out of shape [tokens, " + std::to_string(W) + "] per rank");
+        const int64_t B = size(a[4], 2, 0, "table"), width = size(a[4], 2, 1, "table");
+        const int32_t *table = ints(a[4], {B, width}, "table"), *lens = ints(a[5], {B}, "lens"), *starts = ints(a[6], {B + 1}, "starts");
+        const sfar_stream_t s = stream_of(a[7]);
+        return released([&] { return c_latent_gather(h, const_cast<void *const *>(out.ptr), table, lens, starts, B, width, T, out.stride[0], s); });
+    });
+}
+
+// (handle, R, q_heads, latent_dim, rope_dim, q, out, table, lens, starts, max_q, scale, stream)
+PyObject *latent_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 13, [&] {
+        const auto h = static_cast<sfar_latent_t *>(handle_of(a[0]));
+        const int R = (int)number(a[1]);
+        const int64_t H = number(a[2]), L = number(a[3]), rope = number(a[4]);
+        const Ranks q(a[5], R, 3, kBf16, "q"), out(a[6], R, 3, kBf16, "out");
+        const int64_t T = q.shape[0];
+        if (!q.same({T, H, L + rope}) || !out.same({T, H, L}))
+            wrong("attention: need q of shape [tokens, " + std::to_string(H) + ", " + std::to_string(L + rope) + "] and out of [tokens, " +
+                  std::to_string(H) + ", " + std::to_string(L) + "] per rank");
+        const int64_t B = size(a[7], 2, 0, "table"), W = size(a[7], 2, 1, "table");
+        const int32_t *table = ints(a[7], {B, W}, "table"), *lens = ints(a[8], {B}, "lens"), *starts = ints(a[9], {B + 1}, "starts");
+        const size_t max_q = natural(a[10], "max_q");
+        const float scale = real(a[11]);
+        const sfar_stream_t s = stream_of(a[12]);
+        return released([&] {
+            return c_latent_attention(h, q.ptr, const_cast<void *const *>(out.ptr), table, lens, starts, B, W, T, q.stride[0], q.stride[1],
+                                      out.stride[0], out.stride[1], max_q, scale, s);
+        });
+    });
+}
+
+// (handle, R, q_heads, rope_dim, q, k, v, kr, out, starts, k_starts, max_q, scale, stream)
+PyObject *latent_prompt(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 14, [&] {
+        const auto h = static_cast<sfar_latent_t *>(handle_of(a[0]));
+        const int R = (int)number(a[1]);
+        const int64_t H = number(a[2]), rope = number(a[3]);
+        const Ranks q(a[4], R, 3, kBf16, "q"), k(a[5], R, 3, kBf16, "k"), v(a[6], R, 3, kBf16, "v"), kr(a[7], R, 2, kBf16, "kr"),
+            out(a[8], R, 3, kBf16, "out");
+        const int64_t T = q.shape[0], S = k.shape[0], D = k.shape[2], B = size(a[9], 1, 0, "starts") - 1;
+        if (!q.same({T, H, D + rope}) || !k.same({S, H, D}) || !v.same({S, H, D}) || !kr.same({S, rope}) || !out.same({T, H, D}))
+            wrong("prompt: need q [tokens, heads, head_dim + rope_dim], k and v [context rows, heads, head_dim], kr [context rows, rope_dim] "
+                  "and out [tokens, heads, head_dim] per rank, with " +
+                  std::to_string(H) + " heads and rope_dim " + std::to_string(rope));
+        if (B < 1)
+            wrong("prompt: need starts of at least two numbers");
+        const int32_t *starts = ints(a[9], {B + 1}, "starts"), *k_starts = ints(a[10], {B + 1}, "k_starts");
+        const size_t max_q = natural(a[11], "max_q");
+        const float scale = real(a[12]);
+        const sfar_stream_t s = stream_of(a[13]);
+        return released([&] {
+            return c_latent_prompt(h, q.ptr, k.ptr, v.ptr, kr.ptr, const_cast<void *const *>(out.ptr), starts, k_starts, B, T, S, D, q.stride[0],
+                                   q.stride[1], k.stride[0], k.stride[1], v.stride[0], v.stride[1], kr.stride[0], out.stride[0], out.stride[1],
+                                   max_q, scale, s);
+        });
+    });
+}
+
 // (tensors, R, dimensions, "bf16" | "fp32" | "byte", what) -> (pointers, shape, contiguous)
 PyObject *ranks(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
@@ -325,15 +475,23 @@ PyObject *ranks(PyObject *, PyObject *const *a, Py_ssize_t n)
     return result;
 }
 
-// the addresses of the five C functions
+// the addresses of the C functions
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    return guarded(n, 5, [&] {
-        c_plan = reinterpret_cast<decltype(c_plan)>(handle_of(a[0]));
-        c_append = reinterpret_cast<decltype(c_append)>(handle_of(a[1]));
-        c_attention = reinterpret_cast<decltype(c_attention)>(handle_of(a[2]));
-        c_quantize = reinterpret_cast<decltype(c_quantize)>(handle_of(a[3]));
-        c_gemm = reinterpret_cast<decltype(c_gemm)>(handle_of(a[4]));
+    return guarded(n, 11, [&] {
+        int i = 0;
+        auto next = [&](auto &to) { to = reinterpret_cast<std::decay_t<decltype(to)>>(handle_of(a[i++])); };
+        next(c_plan);
+        next(c_append);
+        next(c_attention);
+        next(c_quantize);
+        next(c_gemm);
+        next(c_rope);
+        next(c_latent_plan);
+        next(c_latent_append);
+        next(c_latent_gather);
+        next(c_latent_attention);
+        next(c_latent_prompt);
         return 0;
     });
 }
@@ -347,6 +505,12 @@ PyMethodDef methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
                          {"attention", fast(attention), METH_FASTCALL, nullptr},
                          {"quantize_fp8", fast(quantize), METH_FASTCALL, nullptr},
                          {"rowpar_gemm_fp8", fast(gemm), METH_FASTCALL, nullptr},
+                         {"rope", fast(rope), METH_FASTCALL, nullptr},
+                         {"latent_plan", fast(latent_plan), METH_FASTCALL, nullptr},
+                         {"latent_append", fast(latent_append), METH_FASTCALL, nullptr},
+                         {"latent_gather", fast(latent_gather), METH_FASTCALL, nullptr},
+                         {"latent_attention", fast(latent_attention), METH_FASTCALL, nullptr},
+                         {"latent_prompt", fast(latent_prompt), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "sfar_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,7 +1,8 @@
 """Thin binding of libsfar (``include/sfar.h``, ``include/sfar_decode.h``,
-``include/sfar_kv.h``, ``include/sfar_fp8.h``, ``include/sfar_test.h``): ctypes,
-and for the calls on whole tensors (``SfarKv``, ``Sfar.quantize_fp8``,
-``Sfar.rowpar_gemm_fp8``) the module built from ``csrc/sfar_tensors.cpp``.
+``include/sfar_kv.h``, ``include/sfar_fp8.h``, ``include/sfar_rope.h``,
+``include/sfar_latent.h``, ``include/sfar_test.h``): ctypes, and for the calls
+on whole tensors (``SfarKv``, ``SfarLatent``, ``Sfar.quantize_fp8``,
+``Sfar.rowpar_gemm_fp8``, ``Sfar.rope``) the module built from ``csrc/sfar_tensors.cpp``.
 
 Argument marshalling only: every step of the AllReduce runs in the library's
 CUDA kernels.  The functions keep the C names; pointers are plain integers
@@ -29,6 +30,9 @@ DTYPES = {"bf16": SFAR_BF16, "fp32": SFAR_FP32}
 SFAR_OK, SFAR_ERR_INVALID, SFAR_ERR_CUDA, SFAR_ERR_OOM, SFAR_ERR_TIMEOUT, SFAR_ERR_UNSUPPORTED, \
     SFAR_ERR_POISONED = range(7)
 SFAR_LAUNCH_SERIAL, SFAR_LAUNCH_OVERLAP, SFAR_LAUNCH_PLAIN, SFAR_LAUNCH_COOPERATIVE = 0, 1, 2, 3
+SFAR_ROPE_HALF, SFAR_ROPE_INTERLEAVED = 0, 1
+ROPE_LAYOUTS = {"half": SFAR_ROPE_HALF, "interleaved": SFAR_ROPE_INTERLEAVED}
+ROPE_SCALINGS = {None: 0, "linear": 1, "wavelength": 2, "ramp": 3}
 MODES = {"serial": SFAR_LAUNCH_SERIAL, "overlap": SFAR_LAUNCH_OVERLAP, "plain": SFAR_LAUNCH_PLAIN,
          "cooperative": SFAR_LAUNCH_COOPERATIVE}
 WAIT_NAMES = {1: "done", 2: "ll", 3: "sentinel", 4: "ready", 5: "bottom", 6: "ll128", 7: "rs", 8: "ag",
@@ -99,6 +103,19 @@ _SIGS = [
      [ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p]),
     ("sfar_kv_status_get", ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(SfarFault)]),
     ("sfar_kv_reset", ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
+    ("sfar_rope", ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_size_t] * 12 + [ctypes.c_int, ctypes.c_float, ctypes.c_void_p]),
+    ("sfar_rope_frequencies", ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_double, ctypes.c_int] +
+     [ctypes.c_double] * 4),
+    ("sfar_latent_create", ctypes.c_void_p, [ctypes.c_int] * 5 + [ctypes.c_size_t, ctypes.c_void_p]),
+    ("sfar_latent_destroy", None, [ctypes.c_void_p]),
+    ("sfar_latent_plan", ctypes.c_int, [ctypes.c_void_p] * 11 + [ctypes.c_size_t] * 3 + [ctypes.c_void_p]),
+    ("sfar_latent_append", ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_size_t] * 2 +
+     [ctypes.c_float, ctypes.c_int, ctypes.c_float, ctypes.c_void_p]),
+    ("sfar_latent_gather", ctypes.c_int, [ctypes.c_void_p] * 5 + [ctypes.c_size_t] * 4 + [ctypes.c_void_p]),
+    ("sfar_latent_attention", ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_size_t] * 8 + [ctypes.c_float, ctypes.c_void_p]),
+    ("sfar_latent_prompt", ctypes.c_int, [ctypes.c_void_p] * 8 + [ctypes.c_size_t] * 14 + [ctypes.c_float, ctypes.c_void_p]),
+    ("sfar_latent_status_get", ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(SfarFault)]),
+    ("sfar_latent_reset", ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     ("sfar_test_kv_record_failure", ctypes.c_int, [ctypes.c_void_p]),
     ("sfar_probe_empty", ctypes.c_int, [ctypes.c_void_p]),
     ("sfar_probe_pingpong", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int,
@@ -169,7 +186,9 @@ def _tensors():
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("sfar_tensors", loader))
         loader.exec_module(module)
         module.bind(*[ctypes.cast(getattr(L, n), ctypes.c_void_p).value
-                      for n in ("sfar_kv_plan", "sfar_kv_append", "sfar_kv_attention", "sfar_quantize_fp8", "sfar_rowpar_gemm_fp8")])
+                      for n in ("sfar_kv_plan", "sfar_kv_append", "sfar_kv_attention", "sfar_quantize_fp8", "sfar_rowpar_gemm_fp8",
+                                "sfar_rope", "sfar_latent_plan", "sfar_latent_append", "sfar_latent_gather", "sfar_latent_attention",
+                                "sfar_latent_prompt")])
         _native = module
     return _native
 
@@ -177,6 +196,27 @@ def _tensors():
 def _check(code, what):
     if code != SFAR_OK:
         raise SfarError(code, what)
+
+
+def _layout(layout):
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout: need one of {', '.join(ROPE_LAYOUTS)}, not {layout!r}")
+    return ROPE_LAYOUTS[layout]
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling=None, factor: float = 1.0, trained: float = 4096.0, low: float = 1.0,
+                     high: float = 32.0, device="cuda"):
+    """(frequencies, scale) of ``Sfar.rope`` and ``SfarLatent.append``: a float32 tensor [rot / 2] on ``device`` and a
+    float.  scaling: None, "linear", "wavelength" or "ramp" (``include/sfar_rope.h`` has the formulas)."""
+    import torch
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling: need None, \"linear\", \"wavelength\" or \"ramp\", not {scaling!r}")
+    if rot < 2:
+        raise ValueError(f"rot: need an even number of at least 2, not {rot}")
+    freq, scale = (ctypes.c_float * (rot // 2))(), ctypes.c_float()
+    _check(lib().sfar_rope_frequencies(freq, ctypes.byref(scale), rot, base, ROPE_SCALINGS[scaling], factor, trained, low, high),
+           "sfar_rope_frequencies")
+    return torch.tensor(list(freq), dtype=torch.float32, device=device), scale.value
 
 
 # ------------------------------------------------------------- C-named calls
@@ -369,6 +409,15 @@ class Sfar:
         if code:
             _check(code, "sfar_rowpar_gemm_fp8")
 
+    def rope(self, q, q_out, pos, freq, k=None, k_out=None, layout="half", scale: float = 1.0, stream=None) -> None:
+        """Rotary positions: q, q_out: [tokens, heads, rotated part] of the handle's type per rank, views of whole heads
+        or tensors of their own; k, k_out the same with their own heads (lists of R tensors, or one tensor [R, ...]
+        each).  An output may be its input.  pos: [tokens] int32, freq: [rotated part / 2] fp32 (``rope_frequencies``);
+        layout "half" or "interleaved"; rows of a negative position are left as they are."""
+        code = (_native or _tensors()).rope(self.h, self.R, self.dtype == "fp32", q, q_out, k, k_out, pos, freq, _layout(layout), scale, stream)
+        if code:
+            _check(code, "sfar_rope")
+
     def status(self):
         return sfar_status_get(self.h)
 
@@ -458,6 +507,90 @@ class SfarKv:
     def close(self) -> None:
         if self.h:
             lib().sfar_kv_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class SfarLatent:
+    """A paged cache of latents and rotated keys in bf16, for R simulated ranks (``include/sfar_latent.h``).
+
+    ``cache``: [pages, page_tokens, latent_dim + rope_dim] bf16 per rank -- a list of R contiguous tensors, or one
+    tensor [R, ...].  The tensors stay the caller's and are kept alive by this object.
+    """
+
+    def __init__(self, cache, q_heads: int, rope_dim: int = 64):
+        self.h = None
+        R = len(cache)
+        pointers, shape, dense = _tensors().ranks(cache, R, 3, "bf16", "cache")
+        if not dense:
+            raise ValueError("SfarLatent: need contiguous caches [pages, page_tokens, latent_dim + rope_dim]")
+        self.R, self.q_heads, self.rope_dim = R, q_heads, rope_dim
+        self.pages, self.page_tokens, self.row = shape
+        self.latent_dim = self.row - rope_dim
+        self.tensors = cache
+        h = lib().sfar_latent_create(R, q_heads, self.latent_dim, rope_dim, self.page_tokens, self.pages, _ptr_array(pointers))
+        if not h:
+            raise SfarError(lib().sfar_last_error(), "sfar_latent_create")
+        self.h = h
+
+    def plan(self, lens, delta, table, ring, state, lens_out, state_out, starts, slots, taken, stream=None) -> None:
+        """As ``SfarKv.plan``, for this cache's pages."""
+        code = (_native or _tensors()).latent_plan(self.h, self.pages, lens, delta, table, ring, state, lens_out, state_out, starts, slots,
+                                                   taken, stream)
+        if code:
+            _check(code, "sfar_latent_plan")
+
+    def append(self, x, weight, pos, freq, slots, eps: float = 1e-6, layout="interleaved", scale: float = 1.0, stream=None) -> None:
+        """x: [tokens, latent_dim + rope_dim] bf16 per rank (token stride a multiple of 8): latents, which are normalised
+        (weight: [latent_dim] bf16), and keys, which are turned (pos: [tokens] int32, freq: [rope_dim / 2] fp32, layout
+        and scale as in ``Sfar.rope``); slots: [tokens] int32."""
+        code = (_native or _tensors()).latent_append(self.h, self.R, self.latent_dim, self.rope_dim, x, weight, pos, freq, slots, eps,
+                                                     _layout(layout), scale, stream)
+        if code:
+            _check(code, "sfar_latent_append")
+
+    def gather(self, out, table, lens, starts, stream=None) -> None:
+        """out: [rows, latent_dim + rope_dim] bf16 per rank: row starts[b] + i becomes token i of request b; table:
+        [requests, width], lens: [requests], starts: [requests + 1] int32."""
+        code = (_native or _tensors()).latent_gather(self.h, self.R, self.row, out, table, lens, starts, stream)
+        if code:
+            _check(code, "sfar_latent_gather")
+
+    def attention(self, q, out, table, lens, starts, max_q: int, scale: float, stream=None) -> None:
+        """Absorbed form.  q: [tokens, q_heads, latent_dim + rope_dim], out: [tokens, q_heads, latent_dim] bf16 per rank
+        (token and head strides multiples of 8); table: [requests, width], lens: [requests], starts: [requests + 1]."""
+        code = (_native or _tensors()).latent_attention(self.h, self.R, self.q_heads, self.latent_dim, self.rope_dim, q, out, table, lens,
+                                                        starts, max_q, scale, stream)
+        if code:
+            _check(code, "sfar_latent_attention")
+
+    def prompt(self, q, k, v, kr, out, starts, k_starts, max_q: int, scale=None, stream=None) -> None:
+        """Expanded form.  q: [tokens, q_heads, head_dim + rope_dim], k, v: [context rows, q_heads, head_dim], kr:
+        [context rows, rope_dim], out: [tokens, q_heads, head_dim] bf16 per rank (strides multiples of 8); starts,
+        k_starts: [requests + 1].  scale: 1 / sqrt(head_dim + rope_dim) if None."""
+        if scale is None:
+            scale = q[0].shape[-1] ** -0.5
+        code = (_native or _tensors()).latent_prompt(self.h, self.R, self.q_heads, self.rope_dim, q, k, v, kr, out, starts, k_starts, max_q,
+                                                     scale, stream)
+        if code:
+            _check(code, "sfar_latent_prompt")
+
+    def status(self):
+        f = SfarFault()
+        code = lib().sfar_latent_status_get(self.h, ctypes.byref(f))
+        return code, f
+
+    def reset(self, stream=None) -> None:
+        _check(lib().sfar_latent_reset(self.h, _stream(stream)), "sfar_latent_reset")
+
+    def close(self) -> None:
+        if self.h:
+            lib().sfar_latent_destroy(self.h)
             self.h = None
 
     def __del__(self):
