@@ -2,27 +2,29 @@
 // cache, absorbed form (include/sfar_latent.h).
 //
 // A request's new tokens times all query heads are the rows of one matrix,
-// taken 16 or 32 at a time; a cached row serves them all, as key (all its
+// taken 16, 32 or 64 at a time; a cached row serves them all, as key (all its
 // numbers) and as value (the latent).  One pass with the running maximum and
-// sum of the softmax; per tile of 128 cached tokens, on the tensor cores,
+// sum of the softmax; per tile of 64 cached tokens, on the tensor cores,
 //   S^T = C Q^T   (tokens x rows, contraction over latent + key)
 //   O^T += L^T P^T (latent x rows, contraction over the tokens).
-// Transposed, because the few rows then are the short side: an MMA takes 128
-// of the other, and both products read the tile from shared memory as TMA
-// wrote it, once as the K-major and once as the M-major operand.
+// Transposed, because the few rows then are the short side: an MMA takes 64
+// tokens or 128 elements of the latent, and both products read the tile from
+// shared memory as TMA wrote it, once as the K-major and once as the M-major
+// operand.
 // HBM-bound: 2 (latent + key) bytes a token against 2 NR (2 latent + key)
 // flops, 32 flops a byte at 16 rows.
 //
-// Softmax: a thread holds one token's scores of all rows.  A row's reference
+// Softmax: a warp holds 16 tokens' scores, spread as an accumulator's fragment
+// (a thread 2 tokens of a quarter of the rows).  A row's reference
 // moves only when a score passes it by 2^7.9 (a vote of the CTA's softmax
 // threads, no maxima otherwise), and the accumulator is rescaled in tensor
 // memory only then.  Weights go to shared memory as bf16, the type that an
 // MMA with these values takes; sums are of the unrounded ones.
 //
-// Shared memory holds one tile and a little more: a ring of 128-element pairs
-// of 64-element boxes (32 KB) and one of key boxes (16 KB).  A pair is free
-// again when its part of the second product is done, so the next tile streams
-// in while this one is multiplied.
+// Shared memory holds two tiles and more: a ring of pairs of 64-element boxes
+// (16 KB) and one of key boxes (8 KB).  A pair is free again when its part of
+// the second product is done, so the next tiles stream in while this one is
+// multiplied.
 //
 // Work: as in k_kv_attn.cu the tiles of all (rank, request, row tile) form one
 // line that is cut into equal pieces, one per CTA; row tiles cut apart are
@@ -37,15 +39,16 @@ namespace {
 constexpr int kTile = SFAR_LATENT_TILE, kGroup = SFAR_LATENT_GROUP;
 constexpr int kSoft = 4, kCopyWarp = kSoft, kMmaWarp = kSoft + 1, kThreads = 32 * (kMmaWarp + 1);
 constexpr int kBox = kTile * 128, kPair = 2 * kBox;                // bytes of 64 elements of every token, of 128
-constexpr int kMeta = 4, kPieces = 4, kParts = 16;                 // kParts: joined at once, at most
+constexpr int kMeta = 8, kPieces = 4, kParts = 16;                 // kMeta: above the tiles in flight; kParts: joined at once, at most
 
 template <int L, int NR> struct Lay {
     static constexpr int kBlocks = L / 128, kChunks = L / 64 + 1;
-    static constexpr int kPairs = 5, kKeys = L == 512 && NR == 32 ? 1 : 2;     // slots of the rings
-    static constexpr int kQ = kChunks * NR * 128, kP = 2 * NR * 128;
+    // slots of the rings: what fits
+    static constexpr int kPairs = L == 256 ? 9 : NR == 64 ? 7 : 10, kKeys = L == 256 || NR == 16 ? 3 : 2;
+    static constexpr int kQ = kChunks * NR * 128, kP = NR * 128;
     static constexpr int oKey = kPairs * kPair, oQ = oKey + kKeys * kBox, oP = oQ + kQ;
     static constexpr int kBytes = oP + kP;
-    static constexpr int kNeed = NR + kBlocks * NR, kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : 256;    // tensor memory
+    static constexpr int kNeed = NR + kBlocks * NR, kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;    // tensor memory
     static constexpr int kPart = NR * (L + 2);                     // floats of a partial result
 };
 
@@ -124,13 +127,12 @@ __device__ __forceinline__ bool soft_any(bool v)
                  : "memory");
     return r != 0;
 }
-// binary32 as integers in the same order, and back
-__device__ __forceinline__ int ordered(float x)
+// Four 8 x 8 matrices of 16-bit values, in fragments, transposed to rows of 16 bytes: lanes 8 i .. 8 i + 7 give the i-th's.
+__device__ __forceinline__ void store_transposed(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
-    const int i = __float_as_int(x);
-    return i ^ ((i >> 31) & 0x7fffffff);
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
 }
-__device__ __forceinline__ float disordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 // whether one of the two bf16 is an infinity or NaN
 __device__ __forceinline__ bool odd2(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
 
@@ -146,7 +148,7 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
     __shared__ uint32_t upto[SFAR_KV_MAX_REQUESTS / kGroup + 1];
     __shared__ uint32_t s_warp[kThreads / 32], s_tmem;
     __shared__ int s_hi[NR], s_last;
-    __shared__ float s_max[kSoft][NR], s_sum[NR], s_ref[NR], s_inv[NR], s_w[kParts][NR];
+    __shared__ float s_max[kSoft][NR], s_sum[NR], s_ref[NR], s_keep[NR], s_inv[NR], s_w[kParts][NR];
     __shared__ uint16_t *s_out[NR];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t mem = (tc::smem(dyn) + 1023u) & ~1023u;
@@ -211,20 +213,21 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w)
         whole += s_warp[w];
-    // short row tiles are left whole, or in cuts of two tiles
+    // short row tiles are left whole, or in cuts of four tiles
     const long long U = sfar_attn_many(a, whole) ? 0 : (long long)carry * a.R;
-    const long long N = min(min((long long)gridDim.x, U), max(whole * a.R, U / 2));
+    const long long N = min(min((long long)gridDim.x, U), max(whole * a.R, U / 4));
     const long long u0 = blockIdx.x < N ? sfar_div(blockIdx.x * U, N) : 0, u1 = blockIdx.x < N ? sfar_div((blockIdx.x + 1) * U, N) : 0;
 
     if (warp < kSoft) {
         // -------------------------------------------------------------- softmax
         bool dead = false;                         // a wait gave up: go on without waiting
         const uint32_t lanes = (uint32_t)warp * 32u << 16, tS = tmem + lanes, tO = tmem + NR + lanes;
-        const int tok = warp * 32 + lane;          // of a tile, this thread's; of a block of the latent, its element
+        // of a tile, token 16 warp + g + 8 h of rows 8 i + 2 t + y is x[4 i + 2 h + y]; of a block of the latent, element tid
+        const int g = lane >> 2, t = lane & 3;
+        constexpr int kI = NR / 8;
         const float f = a.scale * 1.4426950408889634f;
-        // where this thread's weight of row n goes: P[half][row][64 tokens], 128-byte swizzle
-        unsigned char *const pw = gen + Y::oP + (tok >> 6) * (NR * 128) + (tok & 7) * 2;
-        const int unit = (tok & 63) >> 3;
+        // where a lane's row of the transposed weights goes: P[row][64 tokens], 128-byte swizzle; matrices (i, h) of two i at once
+        const uint32_t pw = mem + Y::oP + ((lane >> 4) * 8 + (lane & 7)) * 128 + (((2 * warp + (lane >> 3 & 1)) ^ (lane & 7)) << 4);
         tc::Ring<kPieces> ps;
         tc::Ring<Y::kPairs> st;                    // the first pair of the tile
         uint32_t sphase = 0, ophase = 0, tile = 0;
@@ -266,75 +269,107 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
             if (lane == 0 && p.run)
                 tc::bar_arrive(qbar);
             const int all_to = s_hi[0];            // every row sees the tokens before it
-            float ref[NR], sum[NR];
+            float ref[2 * kI], sum[2 * kI];        // of rows 8 i + 2 t + y
 #pragma unroll
-            for (int n = 0; n < NR; ++n) {
+            for (int n = 0; n < 2 * kI; ++n) {
                 ref[n] = -INFINITY;
                 sum[n] = 0.f;
             }
             for (int k = 0; k < p.run; ++k, ++tile) {
-                const int j0 = (p.tile0 + k) * kTile, j = j0 + tok;
+                const int j0 = (p.tile0 + k) * kTile, j = j0 + 16 * warp + g;
                 dead = dead || !tc::bar_wait(sbar, sphase, limit) || !tc::bar_wait(full + 8 * st.slot, st.phase, limit);
                 sphase ^= 1u;
                 tc::fence_after();
-                uint32_t raw[NR];
-                tc::ld(raw, tS);
+                uint32_t raw[4 * kI];
+                tc::ld_rows(raw, tS);
                 tc::wait_ld(raw);
                 const uint32_t live = s_live[tile % kMeta];
-                const bool edge = j0 + kTile > all_to || live != 0xffu;
-                const bool there = j < p.len && (live >> (tok >> 4) & 1u);
-                bool odd = false;
+                const bool edge = j0 + kTile > all_to || live != 0xfu;
+                bool there[2] = {true, true}, odd[2] = {false, false};
                 if (edge) {
                     // A place that holds no token becomes zeros, whatever lies there; so does a token with an infinity or
-                    // NaN that not every row sees, and the rows that do see it get a NaN for its weight.
+                    // NaN that not every row sees, and the rows that do see it get a NaN for its weight.  Two threads to a
+                    // token of the warp's 16, a box of every pair each.
+                    const int mine = 16 * warp + (lane >> 1);
+                    const bool on = live >> warp & 1u, here = on && j0 + mine < p.len;
+                    bool bad = false;
                     tc::Ring<Y::kPairs> it = st;
                     for (int c = 0; c < Y::kBlocks; ++c, it.next()) {
                         dead = dead || !tc::bar_wait(full + 8 * it.slot, it.phase, limit);
-                        if (there && j >= all_to) {
-                            const unsigned char *at = gen + it.slot * kPair + tok * 128;
-                            for (int i = 0; i < 16; ++i) {
-                                const uint4 v = *reinterpret_cast<const uint4 *>(at + (i >> 3) * kBox + ((i & 7) << 4));
-                                odd = odd || odd2(v.x) || odd2(v.y) || odd2(v.z) || odd2(v.w);
+                        if (here && j0 + mine >= all_to) {
+                            const unsigned char *at = gen + it.slot * kPair + (lane & 1) * kBox + mine * 128;
+                            for (int i = 0; i < 8; ++i) {
+                                const uint4 v = *reinterpret_cast<const uint4 *>(at + ((i ^ (mine & 7)) << 4));
+                                bad = bad || odd2(v.x) || odd2(v.y) || odd2(v.z) || odd2(v.w);
                             }
                         }
                     }
+                    const uint32_t bads = __ballot_sync(SFAR_FULL, bad);
                     it = st;
                     for (int c = 0; c < Y::kBlocks; ++c, it.next())
-                        if (!there || odd) {
-                            unsigned char *at = gen + it.slot * kPair + tok * 128;
-                            for (int i = 0; i < 16; ++i)
-                                *reinterpret_cast<uint4 *>(at + (i >> 3) * kBox + ((i & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                        if (!here || (bads >> (lane & 30) & 3u)) {
+                            unsigned char *at = gen + it.slot * kPair + (lane & 1) * kBox + mine * 128;
+                            for (int i = 0; i < 8; ++i)
+                                *reinterpret_cast<uint4 *>(at + ((i ^ (mine & 7)) << 4)) = make_uint4(0, 0, 0, 0);
                         }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        there[h] = on && j + 8 * h < p.len;
+                        odd[h] = bads >> (2 * (g + 8 * h)) & 3u;
+                    }
                 }
                 for (int c = 0; c < Y::kBlocks; ++c)
                     st.next();
-                // scores in units of log2, relative to the references
-                float x[NR];
+                // scores in units of log2
+                float x[4 * kI];
                 bool move = false;
 #pragma unroll
-                for (int n = 0; n < NR; ++n) {
+                for (int n = 0; n < 4 * kI; ++n)
                     x[n] = __uint_as_float(raw[n]) * f;
-                    if (edge && (!there || j >= s_hi[n]))
-                        x[n] = -INFINITY;
-                    move = move || x[n] - ref[n] > kAttnLift;
+                if (edge) {
+#pragma unroll
+                    for (int i = 0; i < kI; ++i)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int hi = s_hi[8 * i + 2 * t + y];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                if (!there[h] || j + 8 * h >= hi)
+                                    x[4 * i + 2 * h + y] = -INFINITY;
+                        }
                 }
+#pragma unroll
+                for (int i = 0; i < kI; ++i)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        move = move || fmaxf(x[4 * i + y], x[4 * i + 2 + y]) - ref[2 * i + y] > kAttnLift;
                 if (soft_any(move)) {
 #pragma unroll
-                    for (int n = 0; n < NR; ++n) {
-                        const int m = __reduce_max_sync(SFAR_FULL, ordered(x[n]));
-                        if (lane == 0)
-                            s_max[warp][n] = disordered(m);
-                    }
-                    soft_sync();
-                    float keep[NR];
+                    for (int i = 0; i < kI; ++i)
 #pragma unroll
-                    for (int n = 0; n < NR; ++n) {
-                        const float now = fmaxf(fmaxf(s_max[0][n], s_max[1][n]), fmaxf(s_max[2][n], s_max[3][n]));
-                        const float next = now - ref[n] > kAttnLift ? now : ref[n];
-                        keep[n] = ref[n] == -INFINITY ? 1.f : ex2(ref[n] - next);          // all is 0 then, or NaN
-                        ref[n] = next;
-                        sum[n] *= keep[n];
-                    }
+                        for (int y = 0; y < 2; ++y) {
+                            float m = fmaxf(x[4 * i + y], x[4 * i + 2 + y]);
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1)
+                                m = fmaxf(m, __shfl_xor_sync(SFAR_FULL, m, d));
+                            if (g == 0)
+                                s_max[warp][8 * i + 2 * t + y] = m;
+                        }
+                    soft_sync();
+#pragma unroll
+                    for (int i = 0; i < kI; ++i)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int n = 8 * i + 2 * t + y, e = 2 * i + y;
+                            const float now = fmaxf(fmaxf(s_max[0][n], s_max[1][n]), fmaxf(s_max[2][n], s_max[3][n]));
+                            const float next = now - ref[e] > kAttnLift ? now : ref[e];
+                            const float keep = ref[e] == -INFINITY ? 1.f : ex2(ref[e] - next);     // all is 0 then, or NaN
+                            ref[e] = next;
+                            sum[e] *= keep;
+                            if (warp == 0 && g == 0)
+                                s_keep[n] = keep;
+                        }
+                    soft_sync();                   // s_max has been read, s_keep is there until the next move's first barrier
                     if (k) {
 #pragma unroll
                         for (int c = 0; c < Y::kBlocks; ++c)
@@ -345,27 +380,34 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                                 tc::wait_ld(o);
 #pragma unroll
                                 for (int n = 0; n < 16; ++n)
-                                    o[n] = __float_as_uint(__uint_as_float(o[n]) * keep[n0 + n]);
+                                    o[n] = __float_as_uint(__uint_as_float(o[n]) * s_keep[n0 + n]);
                                 tc::st16(tO + c * NR + n0, o);
                             }
                         tc::wait_st();
                     }
-                    soft_sync();                   // s_max has been read
                 }
+                uint32_t w[2 * kI];                // weights of rows 8 i + 2 t and + 1: w[2 i + h]
 #pragma unroll
-                for (int n = 0; n < NR; n += 2) {
-                    float w[2];
+                for (int i = 0; i < kI; ++i)
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        w[y] = x[n + y] == -INFINITY ? 0.f : ex2(x[n + y] - ref[n + y]);
-                        if (odd && j < s_hi[n + y])
-                            w[y] = NAN;
-                        sum[n + y] += w[y];
+                    for (int h = 0; h < 2; ++h) {
+                        float e[2];
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const float v = x[4 * i + 2 * h + y];
+                            e[y] = ex2(v - ref[2 * i + y]);
+                            if (edge) {
+                                e[y] = v == -INFINITY ? 0.f : e[y];
+                                if (odd[h] && j + 8 * h < s_hi[8 * i + 2 * t + y])
+                                    e[y] = NAN;
+                            }
+                            sum[2 * i + y] += e[y];
+                        }
+                        w[2 * i + h] = tc::bf16x2(e[0], e[1]);
                     }
-                    const uint32_t b = tc::bf16x2(w[0], w[1]);
-                    *reinterpret_cast<uint16_t *>(pw + n * 128 + ((unit ^ (n & 7)) << 4)) = (uint16_t)b;
-                    *reinterpret_cast<uint16_t *>(pw + (n + 1) * 128 + ((unit ^ ((n + 1) & 7)) << 4)) = (uint16_t)(b >> 16);
-                }
+#pragma unroll
+                for (int i = 0; i < kI; i += 2)
+                    store_transposed(pw + i * 1024, w[2 * i], w[2 * i + 1], w[2 * i + 2], w[2 * i + 3]);
                 tc::fence_async();
                 tc::fence_before();
                 __syncwarp();
@@ -374,16 +416,19 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
             }
             // the rows' sums
 #pragma unroll
-            for (int n = 0; n < NR; ++n) {
-                float v = sum[n];
+            for (int i = 0; i < kI; ++i)
 #pragma unroll
-                for (int d = 16; d; d >>= 1)
-                    v += __shfl_xor_sync(SFAR_FULL, v, d);
-                if (lane == 0)
-                    s_max[warp][n] = v;
-                if (tid == 0)
-                    s_ref[n] = ref[n];
-            }
+                for (int y = 0; y < 2; ++y) {
+                    float v = sum[2 * i + y];
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1)
+                        v += __shfl_xor_sync(SFAR_FULL, v, d);
+                    if (g == 0) {
+                        s_max[warp][8 * i + 2 * t + y] = v;
+                        if (warp == 0)
+                            s_ref[8 * i + 2 * t + y] = ref[2 * i + y];
+                    }
+                }
             soft_sync();
             if (tid < NR) {
                 const float v = (s_max[0][tid] + s_max[1][tid]) + (s_max[2][tid] + s_max[3][tid]);
@@ -396,22 +441,25 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                 ophase ^= 1u;
                 tc::fence_after();
             }
-            // the accumulator, element `tok` of each 128 of the latent, a column at a time
+            // the accumulator, element tid of each 128 of the latent, a row at a time
             auto each = [&](auto what) {
 #pragma unroll
                 for (int c = 0; c < Y::kBlocks; ++c) {
-                    uint32_t o[NR];
 #pragma unroll
-                    for (int n = 0; n < NR; ++n)
-                        o[n] = 0;
-                    if (p.run) {
-                        tc::ld(o, tO + c * NR);
-                        tc::wait_ld(o);
+                    for (int n0 = 0; n0 < NR; n0 += 16) {
+                        uint32_t o[16];
+#pragma unroll
+                        for (int n = 0; n < 16; ++n)
+                            o[n] = 0;
+                        if (p.run) {
+                            tc::ld16(o, tO + c * NR + n0);
+                            tc::wait_ld(o);
+                        }
+#pragma unroll
+                        for (int n = 0; n < 16; ++n)
+                            if (n0 + n < rows)
+                                what(n0 + n, c * 128 + tid, __uint_as_float(o[n]));
                     }
-#pragma unroll
-                    for (int n = 0; n < NR; ++n)
-                        if (n < rows)
-                            what(n, c * 128 + tok, __uint_as_float(o[n]));
                 }
             };
             if (p.tiles == p.all) {
@@ -491,7 +539,7 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
         tc::Ring<kPieces> ps;
         bool dead = false;
         uint32_t pairs = 0, keys = 0, tile = 0;    // issued
-        const int per = 1 << a.shift, boxes = kTile / per;     // tokens of one copy, copies of a tile's 64 elements
+        const int per = min(1 << a.shift, kTile), boxes = kTile / per;     // tokens of one copy, copies of a tile's 64 elements
         for (long long u = u0; !dead;) {
             Piece p;
             const bool end = u >= u1;
@@ -531,14 +579,14 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                     page = next;
                     next = pages(base + stretch);
                 }
-                // lane i: copy i % 8 of the tile, of the first or second 64 elements of a pair
-                const int box = lane & 7, at = (j0 - base) / per + box, j = j0 + box * per;
-                const int mine = __shfl_sync(SFAR_FULL, page, at & 31);
+                // lane i: copy i % 4 of the tile, of the first or second 64 elements of a pair
+                const int box = lane & 3, at = (j0 - base) / per + box, j = j0 + box * per;
+                const int mine = __shfl_sync(SFAR_FULL, page, at & 31), y = j & ((1 << a.shift) - 1);
                 const bool live = box < boxes && j < p.len, bad = live && (unsigned)mine >= (unsigned)a.pages, go = live && !bad;
-                if (bad && lane < 8)
+                if (bad && lane < 4)
                     sfar_kv_fault(a.ctl, p.b, SFAR_KV_BAD_PAGE);
-                const unsigned any = __ballot_sync(SFAR_FULL, go) & 0xffu;
-                const unsigned held = __ballot_sync(SFAR_FULL, lane < 8 && (any >> (lane * 16 / per) & 1u));
+                const unsigned any = __ballot_sync(SFAR_FULL, go) & 0xfu;
+                const unsigned held = __ballot_sync(SFAR_FULL, lane < 4 && (any >> (lane * 16 / per) & 1u));
                 if (lane == 0)
                     s_live[tile % kMeta] = held;
                 __syncwarp();
@@ -550,8 +598,8 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                         break;
                     }
                     const uint32_t bar = full + 8 * st.slot;
-                    if (go && lane < 16)
-                        tc::load_3d(mem + st.slot * kPair + (lane >> 3) * kBox + box * per * 128, map, c * 128 + (lane >> 3) * 64, 0, mine, bar, pol);
+                    if (go && lane < 8)
+                        tc::load_3d(mem + st.slot * kPair + (lane >> 2) * kBox + box * per * 128, map, c * 128 + (lane >> 2) * 64, y, mine, bar, pol);
                     __syncwarp();
                     if (lane == 0)
                         tc::bar_expect(bar, 2 * bytes);
@@ -565,8 +613,8 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                     break;
                 }
                 const uint32_t bar = kfull + 8 * ks.slot;
-                if (go && lane < 8)
-                    tc::load_3d(mem + Y::oKey + ks.slot * kBox + box * per * 128, map, L, 0, mine, bar, pol);
+                if (go && lane < 4)
+                    tc::load_3d(mem + Y::oKey + ks.slot * kBox + box * per * 128, map, L, y, mine, bar, pol);
                 __syncwarp();
                 if (lane == 0)
                     tc::bar_expect(bar, bytes);
@@ -584,7 +632,7 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
         }
     } else {
         // ----------------------------------------------------------------- MMAs
-        constexpr uint32_t idS = tc::idesc_bf16(128, NR), idO = idS | tc::kTransposeA;
+        constexpr uint32_t idS = tc::idesc_bf16(64, NR), idO = tc::idesc_bf16(128, NR) | tc::kTransposeA;
         const uint64_t dq = tc::desc_k128(mem + Y::oQ), dp = tc::desc_k128(mem + Y::oP), dk = tc::desc_k128(mem), dv = tc::desc_n128(mem, kBox),
                        dr = tc::desc_k128(mem + Y::oKey);
         tc::Ring<Y::kPairs> st;
@@ -636,9 +684,8 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
 #pragma unroll
                     for (int c = 0; c < Y::kBlocks; ++c, st.next()) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            tc::mma_f16_ss(tmem + NR + c * NR, dv + st.slot * (kPair >> 4) + 128 * i, dp + (i >> 2) * (NR * 128 >> 4) + 2 * (i & 3), idO,
-                                           k + i > 0);
+                        for (int i = 0; i < kTile / 16; ++i)
+                            tc::mma_f16_ss(tmem + NR + c * NR, dv + st.slot * (kPair >> 4) + 128 * i, dp + 2 * i, idO, k + i > 0);
                         tc::commit(empty + 8 * st.slot);
                     }
                 }
@@ -668,6 +715,8 @@ const void *sfar_kernel_latent_attn(int latent, int rows, int *threads, int *sme
     *threads = kThreads;
     if (rows == 16)
         return latent == 256 ? SFAR_LATENT(256, 16) : SFAR_LATENT(512, 16);
-    return latent == 256 ? SFAR_LATENT(256, 32) : SFAR_LATENT(512, 32);
+    if (rows == 32)
+        return latent == 256 ? SFAR_LATENT(256, 32) : SFAR_LATENT(512, 32);
+    return latent == 256 ? SFAR_LATENT(256, 64) : SFAR_LATENT(512, 64);
 #undef SFAR_LATENT
 }

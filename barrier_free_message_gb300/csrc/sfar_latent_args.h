@@ -40,7 +40,7 @@ struct SfarLatentGatherArgs {
 
 struct SfarLatentAttnArgs {
     // caches of every rank as 3-D tensor maps: a row's numbers (innermost) by
-    // page_tokens by pages; boxes of 64 numbers by up to 128 tokens, 128-byte swizzle
+    // page_tokens by pages; boxes of 64 numbers by up to 64 tokens, 128-byte swizzle
     CUtensorMap map[SFAR_MAX_R];
     const uint16_t *q[SFAR_MAX_R];
     uint16_t *out[SFAR_MAX_R];
@@ -72,7 +72,7 @@ struct SfarLatentPromptArgs {
 const void *sfar_kernel_rope(int dt, int interleaved);
 const void *sfar_kernel_latent_append(int latent);
 const void *sfar_kernel_latent_gather();
-// rows: 16 or 32 at a time
+// rows: 16, 32 or 64 at a time
 const void *sfar_kernel_latent_attn(int latent, int rows, int *threads, int *smem);
 // tiles: 128 query rows at a time, or twice that
 const void *sfar_kernel_latent_prompt(int head_dim, int tiles, int *threads, int *smem);
@@ -80,7 +80,7 @@ const void *sfar_kernel_latent_prompt(int head_dim, int tiles, int *threads, int
 #define SFAR_ROPE_THREADS 256
 #define SFAR_LATENT_APPEND_WARPS 8
 #define SFAR_GATHER_WARPS 8
-#define SFAR_LATENT_TILE 128                // cached tokens of a step of the attention
-#define SFAR_LATENT_ROWS 32                 // query rows at a time, at most
+#define SFAR_LATENT_TILE 64                // cached tokens of a step of the attention
+#define SFAR_LATENT_ROWS 64                 // query rows at a time, at most
 #define SFAR_LATENT_GROUP 32                // requests to a prefix sum
 #define SFAR_GATHER_ROWS 4                  // rows of a warp

@@ -232,7 +232,7 @@ sfar_latent_t *sfar_latent_create(int R, int q_heads, int latent_dim, int rope_d
     h->sms = sms;
     const cuuint64_t dims[3] = {(cuuint64_t)row, (cuuint64_t)page_tokens, (cuuint64_t)pages};
     const cuuint64_t strides[2] = {(cuuint64_t)row * 2, (cuuint64_t)row * 2 * (cuuint64_t)page_tokens};
-    const cuuint32_t unit[3] = {1, 1, 1}, box[3] = {64, (cuuint32_t)page_tokens, 1};
+    const cuuint32_t unit[3] = {1, 1, 1}, box[3] = {64, (cuuint32_t)std::min(page_tokens, SFAR_LATENT_TILE), 1};
     for (int r = 0; r < R; ++r) {
         h->cache[r] = cache[r];
         if (encode(&h->map[r], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, cache[r], dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -256,15 +256,17 @@ sfar_latent_t *sfar_latent_create(int R, int q_heads, int latent_dim, int rope_d
     bool ok = cudaMemset(h->ws, 0, ws) == cudaSuccess && cudaMemcpy(h->ctl, &init, sizeof init, cudaMemcpyHostToDevice) == cudaSuccess &&
               cudaStreamCreateWithFlags(&h->priv, cudaStreamNonBlocking) == cudaSuccess &&
               cudaMallocHost(&h->host_ctl, sizeof(SfarCtl)) == cudaSuccess && sfar_pool_prepare(&h->plan_ctas);
-    for (int two = 0; two < 2 && ok; ++two) {
-        int threads = 0, smem = 0;
-        const void *f = sfar_kernel_latent_attn(latent_dim, two ? 32 : 16, &threads, &smem);
-        ok = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
-        for (int dim : {64, 128}) {
-            f = sfar_kernel_latent_prompt(dim, 1 + two, &threads, &smem);
-            ok = ok && cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
-        }
+    auto room = [&](const void *f, int smem) { ok = ok && cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess; };
+    int threads = 0, smem = 0;
+    for (int rows : {16, 32, 64}) {
+        const void *f = sfar_kernel_latent_attn(latent_dim, rows, &threads, &smem);
+        room(f, smem);
     }
+    for (int tiles : {1, 2})
+        for (int dim : {64, 128}) {
+            const void *f = sfar_kernel_latent_prompt(dim, tiles, &threads, &smem);
+            room(f, smem);
+        }
     if (!ok) {
         cudaGetLastError();
         sfar_latent_destroy(h);
@@ -438,7 +440,7 @@ sfar_status sfar_latent_attention(sfar_latent_t *h, const void *const q[], void 
     a.shift = h->shift;
     a.pages = (int)h->pages;
     a.rope = h->rope;
-    const int rows = max_q <= 16 / H ? 16 : SFAR_LATENT_ROWS;
+    const int rows = max_q <= 16 / H ? 16 : max_q <= 32 / H ? 32 : 64;
     // the kernel's sums over the line of (row tile, tile) are of 32 bits, its row numbers of 31
     const size_t context = table_width << h->shift, reach = context < (1ull << 31) ? context : 1ull << 31;
     if (tokens * H >= 1ull << 29 || (tokens * H / 16 + requests) * (ceil_div(reach, SFAR_LATENT_TILE) + 8) >= 1ull << 32)

@@ -185,9 +185,29 @@ __device__ __forceinline__ void ld32(uint32_t (&v)[32], uint32_t addr)
           SFAR_R4(v, 28)
         : "r"(addr));
 }
+// 16 lanes x 16, 32 or 64 columns, as products' fragments lie: v[4 i + 2 h + y] = lane g + 8 h, column 8 i + 2 t + y, for
+// thread 4 g + t
+__device__ __forceinline__ void ld_rows(uint32_t (&v)[8], uint32_t addr)
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : SFAR_R4(v, 0), SFAR_R4(v, 4) : "r"(addr));
+}
+__device__ __forceinline__ void ld_rows(uint32_t (&v)[16], uint32_t addr)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : SFAR_R4(v, 0), SFAR_R4(v, 4), SFAR_R4(v, 8), SFAR_R4(v, 12)
+        : "r"(addr));
+}
+__device__ __forceinline__ void ld_rows(uint32_t (&v)[32], uint32_t addr)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : SFAR_R4(v, 0), SFAR_R4(v, 4), SFAR_R4(v, 8), SFAR_R4(v, 12), SFAR_R4(v, 16), SFAR_R4(v, 20), SFAR_R4(v, 24),
+          SFAR_R4(v, 28)
+        : "r"(addr));
+}
 #undef SFAR_R4
-__device__ __forceinline__ void ld(uint32_t (&v)[16], uint32_t addr) { ld16(v, addr); }
-__device__ __forceinline__ void ld(uint32_t (&v)[32], uint32_t addr) { ld32(v, addr); }
 __device__ __forceinline__ void st16(uint32_t addr, const uint32_t (&v)[16])
 {
     asm volatile(

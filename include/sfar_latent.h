@@ -41,7 +41,7 @@ typedef struct sfar_latent sfar_latent_t;
  * pointers, 16-byte aligned, no two overlapping).  1 <= R <= 16; latent_dim
  * 256 or 512; rope_dim 32 or 64; page_tokens 16, 32, 64 or 128;
  * 1 <= q_heads <= 65535; pages * page_tokens below 2^31.  The handle holds a
- * workspace for partial results, about 20 MB at latent_dim 512.  NULL on
+ * workspace for partial results, about 40 MB at latent_dim 512.  NULL on
  * failure (reason: sfar_last_error).  The caches' contents are not touched.
  */
 sfar_latent_t *sfar_latent_create(int R, int q_heads, int latent_dim, int rope_dim, int page_tokens, size_t pages,
@@ -104,7 +104,7 @@ sfar_status sfar_latent_gather(sfar_latent_t *h, void *const out[], const int32_
  * table_width < 2^31; strides below 2^40; scale finite and at least 0.  The
  * kernel counts in 32 bits: tokens * q_heads is below 2^29, and the product of
  * tokens * q_heads / 16 + requests (row tiles) and table_width * page_tokens
- * / 128 + 8 (tiles of a context) below 2^32.
+ * / 64 + 8 (tiles of a context) below 2^32.
  */
 sfar_status sfar_latent_attention(sfar_latent_t *h, const void *const q[], void *const out[], const int32_t *table,
                                   const int32_t *lens, const int32_t *starts, size_t requests, size_t table_width,
