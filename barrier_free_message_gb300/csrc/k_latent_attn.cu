@@ -44,7 +44,7 @@ constexpr int kMeta = 8, kPieces = 4, kParts = 16;                 // kMeta: abo
 template <int L, int NR> struct Lay {
     static constexpr int kBlocks = L / 128, kChunks = L / 64 + 1;
     // slots of the rings: what fits
-    static constexpr int kPairs = L == 256 ? 9 : NR == 64 ? 7 : 10, kKeys = L == 256 || NR == 16 ? 3 : 2;
+    static constexpr int kPairs = L == 256 ? NR == 64 ? 8 : 9 : NR == 64 ? 7 : 10, kKeys = L == 256 || NR == 16 ? 3 : 2;
     static constexpr int kQ = kChunks * NR * 128, kP = NR * 128;
     static constexpr int oKey = kPairs * kPair, oQ = oKey + kKeys * kBox, oP = oQ + kQ;
     static constexpr int kBytes = oP + kP;
@@ -148,7 +148,7 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
     __shared__ uint32_t upto[SFAR_KV_MAX_REQUESTS / kGroup + 1];
     __shared__ uint32_t s_warp[kThreads / 32], s_tmem;
     __shared__ int s_hi[NR], s_last;
-    __shared__ float s_max[kSoft][NR], s_sum[NR], s_ref[NR], s_keep[NR], s_inv[NR], s_w[kParts][NR];
+    __shared__ float s_max[kSoft][NR], s_sum[NR], s_ref[NR], s_keep[NR], s_inv[NR], s_w[kParts][NR], s_m[kParts][NR];
     __shared__ uint16_t *s_out[NR];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t mem = (tc::smem(dyn) + 1023u) & ~1023u;
@@ -482,39 +482,70 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                     if (!s_last)
                         break;
                     const int parts = (join.hi - join.lo) / join.step + 1;
+                    // references and sums of all parts at once, then what each part's rows are multiplied by
+                    for (int i = tid; i < parts * NR; i += 32 * kSoft) {
+                        const int c = i / NR, n = i % NR;
+                        const float2 m = n < rows ? __ldcg(reinterpret_cast<const float2 *>(slot(join.lo + c * join.step) + NR * L) + n)
+                                                  : make_float2(-INFINITY, 0.f);
+                        s_w[c][n] = m.x;
+                        s_m[c][n] = m.y;
+                    }
+                    soft_sync();
                     float top = -INFINITY, total = 0.f;
-                    if (tid < rows) {
+                    if (tid < NR) {
                         for (int c = 0; c < parts; ++c)
-                            top = fmaxf(top, __ldcg(reinterpret_cast<const float2 *>(slot(join.lo + c * join.step) + NR * L) + tid).x);
+                            top = fmaxf(top, s_w[c][tid]);
                         for (int c = 0; c < parts; ++c) {
-                            const float2 m = __ldcg(reinterpret_cast<const float2 *>(slot(join.lo + c * join.step) + NR * L) + tid);
-                            const float w = m.x == -INFINITY ? 0.f : ex2(m.x - top);
+                            const float m = s_w[c][tid], w = m == -INFINITY ? 0.f : ex2(m - top);
                             s_w[c][tid] = w;
-                            total += m.x == -INFINITY ? m.y : w * m.y;        // its sum is 0 then, or NaN
+                            total += m == -INFINITY ? s_m[c][tid] : w * s_m[c][tid];        // its sum is 0 then, or NaN
                         }
                         s_inv[tid] = total == 0.f ? 0.f : 1.f / total;
                     }
                     soft_sync();
                     float *group = slot(join.lo);
                     const bool more = join.up != 0;
-                    constexpr int kPer = L / 4;    // threads of a row
-                    for (int n = tid / kPer; n < rows; n += 32 * kSoft / kPer) {
-                        const int d = tid % kPer * 4;
-                        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                        for (int c = 0; c < parts; ++c) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(slot(join.lo + c * join.step) + n * L + d));
-                            const float w = s_w[c][n];
-                            o.x += w * v.x;
-                            o.y += w * v.y;
-                            o.z += w * v.z;
-                            o.w += w * v.w;
+                    // Three rows of eight parts in flight to a thread.
+                    constexpr int kPer = L / 4, kStep = 32 * kSoft / kPer, kBatch = 8, kY = 3;     // threads of a row, rows at once
+                    const int d = tid % kPer * 4;
+                    for (int n0 = tid / kPer; n0 < rows; n0 += kY * kStep) {
+                        float4 o[kY];
+#pragma unroll
+                        for (int y = 0; y < kY; ++y)
+                            o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int c0 = 0; c0 < parts; c0 += kBatch) {
+                            float4 v[kBatch][kY];
+#pragma unroll
+                            for (int c = 0; c < kBatch; ++c) {
+                                const float *src = slot(join.lo + min(c0 + c, parts - 1) * join.step) + d;
+#pragma unroll
+                                for (int y = 0; y < kY; ++y)
+                                    if (c0 + c < parts && n0 + y * kStep < rows)
+                                        v[c][y] = __ldcg(reinterpret_cast<const float4 *>(src + (n0 + y * kStep) * L));
+                            }
+#pragma unroll
+                            for (int c = 0; c < kBatch; ++c)
+#pragma unroll
+                                for (int y = 0; y < kY; ++y)
+                                    if (c0 + c < parts && n0 + y * kStep < rows) {
+                                        const float w = s_w[c0 + c][n0 + y * kStep];
+                                        o[y].x += w * v[c][y].x;
+                                        o[y].y += w * v[c][y].y;
+                                        o[y].z += w * v[c][y].z;
+                                        o[y].w += w * v[c][y].w;
+                                    }
                         }
-                        if (more) {
-                            __stcg(reinterpret_cast<float4 *>(group + n * L + d), o);
-                        } else {
-                            const float by = s_inv[n];
-                            st_v2u32(s_out[n] + d, tc::bf16x2(o.x * by, o.y * by), tc::bf16x2(o.z * by, o.w * by));
+#pragma unroll
+                        for (int y = 0; y < kY; ++y) {
+                            const int n = n0 + y * kStep;
+                            if (n >= rows)
+                                break;
+                            if (more) {
+                                __stcg(reinterpret_cast<float4 *>(group + n * L + d), o[y]);
+                            } else {
+                                const float by = s_inv[n];
+                                st_v2u32(s_out[n] + d, tc::bf16x2(o[y].x * by, o[y].y * by), tc::bf16x2(o[y].z * by, o[y].w * by));
+                            }
                         }
                     }
                     if (more && tid < rows)
