@@ -30,16 +30,16 @@
 // line that is cut into equal pieces, one per CTA; row tiles cut apart are
 // joined by the last of their CTAs, in order.  Prefix sums of 32 requests at a
 // time are kept, so that shared memory is the tiles'.
-// Warps 0-3: softmax; 4: copies and pieces; 5: the MMAs.
+// Warps 0-3: softmax; 4: copies and pieces; 5: the MMAs; 6: query rows.
 #include "sfar_attn.cuh"
 #include "sfar_latent_args.h"
 
 namespace {
 
 constexpr int kTile = SFAR_LATENT_TILE, kGroup = SFAR_LATENT_GROUP;
-constexpr int kSoft = 4, kCopyWarp = kSoft, kMmaWarp = kSoft + 1, kThreads = 32 * (kMmaWarp + 1);
+constexpr int kSoft = 4, kCopyWarp = kSoft, kMmaWarp = kSoft + 1, kQueryWarp = kSoft + 2, kThreads = 32 * (kQueryWarp + 1);
 constexpr int kBox = kTile * 128, kPair = 2 * kBox;                // bytes of 64 elements of every token, of 128
-constexpr int kMeta = 8, kPieces = 4, kParts = 16;                 // kMeta: above the tiles in flight; kParts: joined at once, at most
+constexpr int kMeta = 8, kPieces = 4, kParts = 16, kKept = 64;     // kMeta: above the tiles in flight; kParts: joined at once, at most
 
 template <int L, int NR> struct Lay {
     static constexpr int kBlocks = L / 128, kChunks = L / 64 + 1;
@@ -62,8 +62,12 @@ struct Piece {
     long long at;               // place of the piece's first tile on the line
 };
 
+struct Request {
+    int len, count, first;
+};
 template <int NR, class A> struct Work {
     const uint32_t *upto;       // [groups + 1] prefix sums of the units of 32 requests, per rank
+    const Request *kept;        // the first kKept requests, read once
     const A &a;
     __device__ __forceinline__ int tiles(int len) const { return max(1, (len + kTile - 1) / kTile); }
     __device__ __forceinline__ int row_tiles(int count) const { return (int)(((long long)count * a.Hq + NR - 1) / NR); }
@@ -89,7 +93,11 @@ template <int NR, class A> struct Work {
         int len = 0, count = 0, first = 0;
         uint32_t sum = 0;
         if (b < a.B) {
-            sfar_attn_request(a, b, len, count, first);
+            if (b < kKept) {
+                len = kept[b].len, count = kept[b].count, first = kept[b].first;
+            } else {
+                sfar_attn_request(a, b, len, count, first);
+            }
             sum = (uint32_t)row_tiles(count) * (uint32_t)tiles(len);
         }
         const uint32_t mine = sum;
@@ -136,16 +144,74 @@ __device__ __forceinline__ void store_transposed(uint32_t addr, uint32_t a, uint
 // whether one of the two bf16 is an infinity or NaN
 __device__ __forceinline__ bool odd2(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
 
+// Adds up `parts` partial results, the first at p0, the second at p1 and the others `step` floats on from it, each times
+// its row's weight w[part][row], by the 128 threads of the softmax: into the first one, or, where out is given, times by[row]
+// to the rows of the result.  Four rows of eight parts are in flight to a thread; out of line, so that the kernel's loops
+// keep their registers.
+template <int L, int NR>
+__device__ __noinline__ void add_parts(float *p0, const float *p1, size_t step, int parts, int rows, const float *w, uint16_t *const *out,
+                                       const float *by)
+{
+    constexpr int kPer = L / 4, kStep = 32 * kSoft / kPer, kBatch = 8, kY = 4;     // threads of a row, rows at once
+    const int d = threadIdx.x % kPer * 4;
+    for (int n0 = threadIdx.x / kPer; n0 < rows; n0 += kY * kStep) {
+        float4 o[kY];
+#pragma unroll
+        for (int y = 0; y < kY; ++y)
+            o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+        int at[kY];                                // rows past the last: the last again
+#pragma unroll
+        for (int y = 0; y < kY; ++y)
+            at[y] = min(n0 + y * kStep, rows - 1);
+#pragma unroll 1
+        for (int c0 = 0; c0 < parts; c0 += kBatch) {
+            float4 v[kBatch][kY];
+#pragma unroll
+            for (int c = 0; c < kBatch; ++c) {
+                const int part = min(c0 + c, parts - 1);           // parts past the last: the last again, not added
+                const float *src = (part == 0 ? p0 : p1 + (size_t)(part - 1) * step) + d;
+#pragma unroll
+                for (int y = 0; y < kY; ++y)
+                    v[c][y] = __ldcg(reinterpret_cast<const float4 *>(src + at[y] * L));
+            }
+#pragma unroll
+            for (int c = 0; c < kBatch; ++c)
+                if (c0 + c < parts)
+#pragma unroll
+                    for (int y = 0; y < kY; ++y) {
+                        const float f = w[(c0 + c) * NR + at[y]];
+                        o[y].x += f * v[c][y].x;
+                        o[y].y += f * v[c][y].y;
+                        o[y].z += f * v[c][y].z;
+                        o[y].w += f * v[c][y].w;
+                    }
+        }
+#pragma unroll
+        for (int y = 0; y < kY; ++y) {
+            const int n = n0 + y * kStep;
+            if (n >= rows)
+                break;
+            if (out) {
+                const float f = by[n];
+                st_v2u32(out[n] + d, tc::bf16x2(o[y].x * f, o[y].y * f), tc::bf16x2(o[y].z * f, o[y].w * f));
+            } else {
+                __stcg(reinterpret_cast<float4 *>(p0 + n * L + d), o[y]);
+            }
+        }
+    }
+}
+
 }  // namespace
 
 template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(const __grid_constant__ SfarLatentAttnArgs a)
 {
     using Y = Lay<L, NR>;
     extern __shared__ __align__(1024) unsigned char dyn[];
-    __shared__ __align__(8) unsigned long long bars[2 * Y::kPairs + 2 * Y::kKeys + 2 * kPieces + 5];
+    __shared__ __align__(8) unsigned long long bars[2 * Y::kPairs + 2 * Y::kKeys + 2 * kPieces + 6];
     __shared__ Piece s_piece[kPieces];             // what the copying warp has begun with; no tiles: the end
-    __shared__ uint32_t s_live[kMeta];             // of a tile: which 16 tokens are on a page of the pool
+    __shared__ uint32_t s_live[kMeta];             // of a tile: which 16 places hold a token on a page of the pool
     __shared__ uint32_t upto[SFAR_KV_MAX_REQUESTS / kGroup + 1];
+    __shared__ Request s_kept[kKept];
     __shared__ uint32_t s_warp[kThreads / 32], s_tmem;
     __shared__ int s_hi[NR], s_last;
     __shared__ float s_max[kSoft][NR], s_sum[NR], s_ref[NR], s_keep[NR], s_inv[NR], s_w[kParts][NR], s_m[kParts][NR];
@@ -155,13 +221,13 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
     unsigned char *gen = dyn + (mem - tc::smem(dyn));
     const uint32_t full = tc::smem(bars), empty = full + 8 * Y::kPairs, kfull = empty + 8 * Y::kPairs, kempty = kfull + 8 * Y::kKeys,
                    pfull = kempty + 8 * Y::kKeys, pempty = pfull + 8 * kPieces, qbar = pempty + 8 * kPieces, sbar = qbar + 8, wbar = qbar + 16,
-                   obar = qbar + 24, drain = qbar + 32;
+                   obar = qbar + 24, qempty = qbar + 32, drain = qbar + 40;
 
     if (warp == kCopyWarp && lane < a.R)
         tc::prefetch_map(&a.map[lane]);
     if (tid == 0) {
         for (uint32_t b = full; b <= drain; b += 8)
-            tc::bar_init(b, b >= pempty && b < qbar ? kSoft + 1 : b == qbar || b == wbar ? kSoft : 1);
+            tc::bar_init(b, b >= pempty && b < qbar ? kSoft + 2 : b == qbar ? 32 : b == wbar ? kSoft : 1);
         tc::bar_fence_init();
         tc::fence_async();
         upto[0] = 0;
@@ -172,7 +238,7 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
     const unsigned long long limit = ld_relaxed_u64(&a.ctl->timeout_ns);
 
     // prefix sums of the requests' units: row tiles x tiles, 32 requests to a warp
-    const Work<NR, SfarLatentAttnArgs> work{upto, a};
+    const Work<NR, SfarLatentAttnArgs> work{upto, s_kept, a};
     uint32_t carry = 0;
     int row_tiles = 0;                             // of this thread's requests
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
@@ -181,6 +247,8 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
         if (b < a.B) {
             int len, count, first;
             sfar_attn_request(a, b, len, count, first);
+            if (b < kKept)
+                s_kept[b] = Request{len, count, first};
             const int n = work.row_tiles(count);
             v = (uint32_t)n * (uint32_t)work.tiles(len);
             row_tiles = min(row_tiles + n, 1 << 26);       // above any step's; 32 such sums fit 32 bits
@@ -231,43 +299,28 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
         tc::Ring<kPieces> ps;
         tc::Ring<Y::kPairs> st;                    // the first pair of the tile
         uint32_t sphase = 0, ophase = 0, tile = 0;
-        for (;;) {
+        // The next piece, by all softmax warps alike; false: the end, or a wait that gave up.  It is read where the copying
+        // warp has put it, and given back when it has been written out.
+        auto take = [&](int &at) {
             dead = dead || !tc::bar_wait(pfull + 8 * ps.slot, ps.phase, limit);
             if (soft_any(dead)) {
                 dead = true;
-                break;
+                return false;
             }
-            const Piece p = s_piece[ps.slot];
-            __syncwarp();
-            if (lane == 0)
-                tc::bar_arrive(pempty + 8 * ps.slot);
+            at = (int)ps.slot;
             ps.next();
-            if (p.tiles == 0)
-                break;
+            return s_piece[at].tiles != 0;
+        };
+        int now_at = 0;
+        while (take(now_at)) {
+            const Piece &p = s_piece[now_at];
             const int row0 = p.rt * NR, rows = (int)min((long long)NR, (long long)p.count * a.Hq - row0);
             if (tid < NR) {
                 const int n = row0 + min(tid, rows - 1), i = n / a.Hq, h = n - i * a.Hq;
                 s_hi[tid] = p.len - p.count + i + 1;
                 s_out[tid] = a.out[p.r] + (long long)(p.first + i) * a.ots + h * a.ohs;
             }
-            // the query rows: [chunk][row][64 elements], 128-byte swizzle; zeros past the rows and past a short key
-            const uint16_t *q = a.q[p.r];
-            for (int i = tid; i < NR * Y::kChunks * 8 && p.run; i += 32 * kSoft) {
-                const int n = i / (Y::kChunks * 8), c = i % (Y::kChunks * 8), row = row0 + n, t = row / a.Hq;
-                const bool in = n < rows && c * 8 < L + a.rope;
-                const uint16_t *src = q;
-                if (in)
-                    src += (long long)(p.first + t) * a.qts + (long long)(row - t * a.Hq) * a.qhs + c * 8;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(mem + Y::oQ + (c >> 3) * (NR * 128) + n * 128 +
-                                                                                  (((c & 7) ^ (n & 7)) << 4)),
-                             "l"(src), "r"(in ? 16u : 0u)
-                             : "memory");
-            }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            tc::fence_async();
             soft_sync();                           // s_hi, s_out
-            if (lane == 0 && p.run)
-                tc::bar_arrive(qbar);
             const int all_to = s_hi[0];            // every row sees the tokens before it
             float ref[2 * kI], sum[2 * kI];        // of rows 8 i + 2 t + y
 #pragma unroll
@@ -275,8 +328,9 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                 ref[n] = -INFINITY;
                 sum[n] = 0.f;
             }
-            for (int k = 0; k < p.run; ++k, ++tile) {
-                const int j0 = (p.tile0 + k) * kTile, j = j0 + 16 * warp + g;
+            const int run = p.run, j00 = p.tile0 * kTile, len = p.len;
+            for (int k = 0; k < run; ++k, ++tile) {
+                const int j0 = j00 + k * kTile, j = j0 + 16 * warp + g;
                 dead = dead || !tc::bar_wait(sbar, sphase, limit) || !tc::bar_wait(full + 8 * st.slot, st.phase, limit);
                 sphase ^= 1u;
                 tc::fence_after();
@@ -284,14 +338,15 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                 tc::ld_rows(raw, tS);
                 tc::wait_ld(raw);
                 const uint32_t live = s_live[tile % kMeta];
-                const bool edge = j0 + kTile > all_to || live != 0xfu;
+                const bool edge = j0 + kTile > all_to || live != 0xfu, none = warp && !(live >> warp & 1u);
                 bool there[2] = {true, true}, odd[2] = {false, false};
                 if (edge) {
-                    // A place that holds no token becomes zeros, whatever lies there; so does a token with an infinity or
-                    // NaN that not every row sees, and the rows that do see it get a NaN for its weight.  Two threads to a
-                    // token of the warp's 16, a box of every pair each.
+                    // A place that holds no token becomes zeros, whatever lies there (16 without one are left out of the
+                    // product, but for the first); so does a token with an infinity or NaN that not every row sees, and the
+                    // rows that do see it get a NaN for its weight.  Two threads to a token of the warp's 16, a box of every
+                    // pair each.
                     const int mine = 16 * warp + (lane >> 1);
-                    const bool on = live >> warp & 1u, here = on && j0 + mine < p.len;
+                    const bool on = live >> warp & 1u, here = on && j0 + mine < len;
                     bool bad = false;
                     tc::Ring<Y::kPairs> it = st;
                     for (int c = 0; c < Y::kBlocks; ++c, it.next()) {
@@ -307,14 +362,14 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                     const uint32_t bads = __ballot_sync(SFAR_FULL, bad);
                     it = st;
                     for (int c = 0; c < Y::kBlocks; ++c, it.next())
-                        if (!here || (bads >> (lane & 30) & 3u)) {
+                        if (!none && (!here || (bads >> (lane & 30) & 3u))) {
                             unsigned char *at = gen + it.slot * kPair + (lane & 1) * kBox + mine * 128;
                             for (int i = 0; i < 8; ++i)
                                 *reinterpret_cast<uint4 *>(at + ((i ^ (mine & 7)) << 4)) = make_uint4(0, 0, 0, 0);
                         }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        there[h] = on && j + 8 * h < p.len;
+                        there[h] = on && j + 8 * h < len;
                         odd[h] = bads >> (2 * (g + 8 * h)) & 3u;
                     }
                 }
@@ -441,29 +496,46 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                 ophase ^= 1u;
                 tc::fence_after();
             }
-            // the accumulator, element tid of each 128 of the latent, a row at a time
-            auto each = [&](auto what) {
+            // The accumulator, element tid of each 128 of the latent, a row at a time.  begin(n): what is read once for a row.
+            auto each = [&](auto begin, auto what) {
 #pragma unroll
-                for (int c = 0; c < Y::kBlocks; ++c) {
+                for (int n0 = 0; n0 < NR; n0 += 8) {
+                    if (n0 >= rows)
+                        break;
+                    decltype(begin(0)) of[8];
 #pragma unroll
-                    for (int n0 = 0; n0 < NR; n0 += 16) {
-                        uint32_t o[16];
+                    for (int n = 0; n < 8; ++n)
+                        of[n] = begin(n0 + n);
+                    uint32_t o[Y::kBlocks][8];
 #pragma unroll
-                        for (int n = 0; n < 16; ++n)
-                            o[n] = 0;
-                        if (p.run) {
-                            tc::ld16(o, tO + c * NR + n0);
-                            tc::wait_ld(o);
-                        }
+                    for (int c = 0; c < Y::kBlocks; ++c)
 #pragma unroll
-                        for (int n = 0; n < 16; ++n)
-                            if (n0 + n < rows)
-                                what(n0 + n, c * 128 + tid, __uint_as_float(o[n]));
+                        for (int n = 0; n < 8; ++n)
+                            o[c][n] = 0;
+                    if (run) {
+#pragma unroll
+                        for (int c = 0; c < Y::kBlocks; ++c)
+                            tc::ld8(o[c], tO + c * NR + n0);
+#pragma unroll
+                        for (int c = 0; c < Y::kBlocks; ++c)
+                            tc::wait_ld(o[c]);
                     }
+#pragma unroll
+                    for (int n = 0; n < 8; ++n)
+                        if (n0 + n < rows) {
+#pragma unroll
+                            for (int c = 0; c < Y::kBlocks; ++c)
+                                what(of[n], n0 + n, c * 128 + tid, __uint_as_float(o[c][n]));
+                        }
                 }
             };
             if (p.tiles == p.all) {
-                each([&](int n, int d, float v) { s_out[n][d] = (uint16_t)tc::bf16x2(v * s_inv[n], 0.f); });
+                struct Row {
+                    uint16_t *out;
+                    float by;
+                };
+                each([&](int n) { return Row{s_out[n], s_inv[n]}; },
+                     [&](const Row &r, int, int d, float v) { r.out[d] = (uint16_t)tc::bf16x2(v * r.by, 0.f); });
             } else {
                 // a part: leave it in the workspace, for the last of the row tile's CTAs
                 const long long from = p.at - p.tile0, to = from + p.all;
@@ -471,7 +543,7 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                 SfarJoin join(a, 0, c0, c1, blockIdx.x);
                 auto slot = [&](int c) { return a.part + ((size_t)c * 2 + (c == c0)) * Y::kPart; };
                 float *dst = slot(blockIdx.x);
-                each([&](int n, int d, float v) { __stcg(dst + n * L + d, v); });
+                each([](int) { return 0; }, [&](int, int n, int d, float v) { __stcg(dst + n * L + d, v); });
                 if (tid < rows)
                     __stcg(reinterpret_cast<float2 *>(dst + NR * L) + tid, make_float2(s_ref[tid], s_sum[tid]));
                 for (;;) {
@@ -505,49 +577,8 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                     soft_sync();
                     float *group = slot(join.lo);
                     const bool more = join.up != 0;
-                    // Three rows of eight parts in flight to a thread.
-                    constexpr int kPer = L / 4, kStep = 32 * kSoft / kPer, kBatch = 8, kY = 3;     // threads of a row, rows at once
-                    const int d = tid % kPer * 4;
-                    for (int n0 = tid / kPer; n0 < rows; n0 += kY * kStep) {
-                        float4 o[kY];
-#pragma unroll
-                        for (int y = 0; y < kY; ++y)
-                            o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (int c0 = 0; c0 < parts; c0 += kBatch) {
-                            float4 v[kBatch][kY];
-#pragma unroll
-                            for (int c = 0; c < kBatch; ++c) {
-                                const float *src = slot(join.lo + min(c0 + c, parts - 1) * join.step) + d;
-#pragma unroll
-                                for (int y = 0; y < kY; ++y)
-                                    if (c0 + c < parts && n0 + y * kStep < rows)
-                                        v[c][y] = __ldcg(reinterpret_cast<const float4 *>(src + (n0 + y * kStep) * L));
-                            }
-#pragma unroll
-                            for (int c = 0; c < kBatch; ++c)
-#pragma unroll
-                                for (int y = 0; y < kY; ++y)
-                                    if (c0 + c < parts && n0 + y * kStep < rows) {
-                                        const float w = s_w[c0 + c][n0 + y * kStep];
-                                        o[y].x += w * v[c][y].x;
-                                        o[y].y += w * v[c][y].y;
-                                        o[y].z += w * v[c][y].z;
-                                        o[y].w += w * v[c][y].w;
-                                    }
-                        }
-#pragma unroll
-                        for (int y = 0; y < kY; ++y) {
-                            const int n = n0 + y * kStep;
-                            if (n >= rows)
-                                break;
-                            if (more) {
-                                __stcg(reinterpret_cast<float4 *>(group + n * L + d), o[y]);
-                            } else {
-                                const float by = s_inv[n];
-                                st_v2u32(s_out[n] + d, tc::bf16x2(o[y].x * by, o[y].y * by), tc::bf16x2(o[y].z * by, o[y].w * by));
-                            }
-                        }
-                    }
+                    add_parts<L, NR>(slot(join.lo), slot(join.lo + join.step), (size_t)join.step * 2 * Y::kPart, parts, rows, &s_w[0][0],
+                                     more ? nullptr : s_out, s_inv);
                     if (more && tid < rows)
                         __stcg(reinterpret_cast<float2 *>(group + NR * L) + tid, make_float2(top, total));
                     if (!join.next(a, 0))
@@ -556,6 +587,8 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
             }
             tc::fence_before();                    // before the MMAs that the next weights allow
             soft_sync();                           // the tables in shared memory have been read
+            if (lane == 0)
+                tc::bar_arrive(pempty + 8 * now_at);
         }
         sfar_attn_padding<L>(a, tid, 32 * kSoft);
         if (dead && lane == 0)
@@ -617,7 +650,7 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                 if (bad && lane < 4)
                     sfar_kv_fault(a.ctl, p.b, SFAR_KV_BAD_PAGE);
                 const unsigned any = __ballot_sync(SFAR_FULL, go) & 0xfu;
-                const unsigned held = __ballot_sync(SFAR_FULL, lane < 4 && (any >> (lane * 16 / per) & 1u));
+                const unsigned held = __ballot_sync(SFAR_FULL, lane < 4 && (any >> (lane * 16 / per) & 1u) && j0 + lane * 16 < p.len);
                 if (lane == 0)
                     s_live[tile % kMeta] = held;
                 __syncwarp();
@@ -661,6 +694,51 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
             for (uint32_t i = keys - min(keys, (uint32_t)Y::kKeys); i < keys; ++i)
                 tc::bar_wait(kfull + 8 * (i % Y::kKeys), (i / Y::kKeys) & 1u, limit);
         }
+    } else if (warp == kQueryWarp) {
+        // -------------------------------------------------------------- queries
+        // A piece's query rows: [chunk][row][64 elements], 128-byte swizzle; zeros past the rows and past a short key.
+        tc::Ring<kPieces> ps;
+        uint32_t phase = 1;
+        bool dead = false;
+        for (;;) {
+            dead = !__all_sync(SFAR_FULL, tc::bar_wait(pfull + 8 * ps.slot, ps.phase, limit));
+            if (dead || s_piece[ps.slot].tiles == 0)
+                break;
+            const Piece &p = s_piece[ps.slot];
+            if (p.run) {
+                // the last piece's scores have been formed
+                dead = !__all_sync(SFAR_FULL, tc::bar_wait(qempty, phase, limit));
+                phase ^= 1u;
+                if (dead)
+                    break;
+                constexpr int kVecs = Y::kChunks * 8, kEach = NR < 32 ? NR : 32;
+                const int row0 = p.rt * NR, rows = (int)min((long long)NR, (long long)p.count * a.Hq - row0);
+                for (int m = 0; m < NR; m += kEach) {
+                    // lane i: where row m + i comes from
+                    const int row = row0 + min(m + lane, rows - 1), i = row / a.Hq;
+                    const uint16_t *src = a.q[p.r] + (long long)(p.first + i) * a.qts + (long long)(row - i * a.Hq) * a.qhs;
+#pragma unroll 4
+                    for (int e = lane; e < kEach * kVecs; e += 32) {
+                        const int y = e / kVecs, c = e - y * kVecs, n = m + y;
+                        const uint16_t *from = reinterpret_cast<const uint16_t *>(__shfl_sync(SFAR_FULL, (unsigned long long)src, y));
+                        const bool in = n < rows && c * 8 < L + a.rope;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(mem + Y::oQ + (c >> 3) * (NR * 128) + n * 128 +
+                                                                                          (((c & 7) ^ (n & 7)) << 4)),
+                                     "l"(in ? from + c * 8 : from), "r"(in ? 16u : 0u)
+                                     : "memory");
+                    }
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                tc::fence_async();
+                tc::bar_arrive(qbar);
+            }
+            __syncwarp();
+            if (lane == 0)
+                tc::bar_arrive(pempty + 8 * ps.slot);
+            ps.next();
+        }
+        if (dead && lane == 0)
+            sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
     } else {
         // ----------------------------------------------------------------- MMAs
         constexpr uint32_t idS = tc::idesc_bf16(64, NR), idO = tc::idesc_bf16(128, NR) | tc::kTransposeA;
@@ -669,7 +747,7 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
         tc::Ring<Y::kPairs> st;
         tc::Ring<Y::kKeys> ks;
         tc::Ring<kPieces> ps;
-        uint32_t qphase = 0, wphase = 0;
+        uint32_t qphase = 0, wphase = 0, tile = 0;
         bool dead = false;
         for (;;) {
             dead = __any_sync(SFAR_FULL, dead || !tc::bar_wait(pfull + 8 * ps.slot, ps.phase, limit));
@@ -706,17 +784,21 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                         tc::mma_f16_ss(tmem, dr + ks.slot * (kBox >> 4) + 2 * i, dq + (L / 64) * (NR * 128 >> 4) + 2 * i, idS, true);
                     tc::commit(kempty + 8 * ks.slot);
                     tc::commit(sbar);
+                    if (k == run - 1)
+                        tc::commit(qempty);
                     ks.next();
                     dead = !tc::bar_wait(wbar, wphase, limit);
                     wphase ^= 1u;
                     if (dead)
                         break;
                     tc::fence_after();
+                    const uint32_t live = s_live[tile++ % kMeta] | 1u;
 #pragma unroll
                     for (int c = 0; c < Y::kBlocks; ++c, st.next()) {
 #pragma unroll
                         for (int i = 0; i < kTile / 16; ++i)
-                            tc::mma_f16_ss(tmem + NR + c * NR, dv + st.slot * (kPair >> 4) + 128 * i, dp + 2 * i, idO, k + i > 0);
+                            if (live >> i & 1u)
+                                tc::mma_f16_ss(tmem + NR + c * NR, dv + st.slot * (kPair >> 4) + 128 * i, dp + 2 * i, idO, k + i > 0);
                         tc::commit(empty + 8 * st.slot);
                     }
                 }

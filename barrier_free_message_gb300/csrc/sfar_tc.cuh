@@ -168,7 +168,11 @@ template <int N> __device__ __forceinline__ void wait_ld(uint32_t (&v)[N])
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 #define SFAR_R4(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3])
-// 32 lanes x 16 or 32 columns of 32 bits: lane = the warp's TMEM lane, v[c] = column c
+// 32 lanes x 8, 16 or 32 columns of 32 bits: lane = the warp's TMEM lane, v[c] = column c
+__device__ __forceinline__ void ld8(uint32_t (&v)[8], uint32_t addr)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : SFAR_R4(v, 0), SFAR_R4(v, 4) : "r"(addr));
+}
 __device__ __forceinline__ void ld16(uint32_t (&v)[16], uint32_t addr)
 {
     asm volatile(
