@@ -146,23 +146,23 @@ __device__ __forceinline__ bool odd2(uint32_t w) { return (w & 0x7f80u) == 0x7f8
 
 // Adds up `parts` partial results, the first at p0, the second at p1 and the others `step` floats on from it, each times
 // its row's weight w[part][row], by the 128 threads of the softmax: into the first one, or, where out is given, times by[row]
-// to the rows of the result.  Four rows of eight parts are in flight to a thread; out of line, so that the kernel's loops
-// keep their registers.
-template <int L, int NR>
-__device__ __noinline__ void add_parts(float *p0, const float *p1, size_t step, int parts, int rows, const float *w, uint16_t *const *out,
-                                       const float *by)
+// to the rows of the result.  A thread has kBatch parts of kY rows in flight: time passes by round trips (1.2 us), so few
+// parts are taken with more rows.
+template <int L, int NR, int kBatch, int kY>
+__device__ __forceinline__ void add_parts(float *p0, const float *p1, size_t step, int parts, int rows, const float *w, uint16_t *const *out,
+                                          const float *by)
 {
-    constexpr int kPer = L / 4, kStep = 32 * kSoft / kPer, kBatch = 8, kY = 4;     // threads of a row, rows at once
+    constexpr int kPer = L / 4, kStep = 32 * kSoft / kPer;         // threads of a row, rows at once
     const int d = threadIdx.x % kPer * 4;
+#pragma unroll 1
     for (int n0 = threadIdx.x / kPer; n0 < rows; n0 += kY * kStep) {
         float4 o[kY];
-#pragma unroll
-        for (int y = 0; y < kY; ++y)
-            o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
         int at[kY];                                // rows past the last: the last again
 #pragma unroll
-        for (int y = 0; y < kY; ++y)
+        for (int y = 0; y < kY; ++y) {
+            o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
             at[y] = min(n0 + y * kStep, rows - 1);
+        }
 #pragma unroll 1
         for (int c0 = 0; c0 < parts; c0 += kBatch) {
             float4 v[kBatch][kY];
@@ -199,6 +199,18 @@ __device__ __noinline__ void add_parts(float *p0, const float *p1, size_t step, 
             }
         }
     }
+}
+// out of line, so that the kernel's loops keep their registers
+template <int L, int NR>
+__device__ __noinline__ void add_parts(float *p0, const float *p1, size_t step, int parts, int rows, const float *w, uint16_t *const *out,
+                                       const float *by)
+{
+    if (parts <= 2)
+        add_parts<L, NR, 2, 12>(p0, p1, step, parts, rows, w, out, by);
+    else if (parts <= 4)
+        add_parts<L, NR, 4, 7>(p0, p1, step, parts, rows, w, out, by);
+    else
+        add_parts<L, NR, 8, 4>(p0, p1, step, parts, rows, w, out, by);
 }
 
 }  // namespace
