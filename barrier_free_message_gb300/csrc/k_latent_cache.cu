@@ -2,8 +2,10 @@
 // (include/sfar_latent.h).
 //
 // Append: a warp takes a token's row of one rank: latents of 8 or 16 a lane,
-// their sum of squares by shuffles, the rotated key's pairs an angle to a
-// lane.  Read once, written once, nothing shared between warps.
+// their sum of squares by shuffles, the rotated key's pairs an angle to a lane.
+// The row is asked for before its slot is known; 40 registers, so that 48 warps
+// are in flight on an SM.  (Rows of two or four ranks to a warp, with the angle
+// in common: 30 and 37 us where this takes 26.)
 //
 // Gather: a warp takes four neighbouring rows, finds the first one's request
 // by a search of 32 places at a time and the others by walking on, and copies
@@ -14,6 +16,7 @@
 #include "sfar_angle.cuh"
 #include "sfar_kv_device.cuh"
 #include "sfar_latent_args.h"
+#include "sfar_tc.cuh"
 
 namespace {
 
@@ -28,23 +31,17 @@ __device__ __forceinline__ uint32_t pack(float l, float h)
 
 }  // namespace
 
-template <int L> __global__ void __launch_bounds__(32 * SFAR_LATENT_APPEND_WARPS) k_latent_append(const __grid_constant__ SfarLatentAppendArgs a)
+template <int L>
+__global__ void __launch_bounds__(32 * SFAR_LATENT_APPEND_WARPS, 6) k_latent_append(const __grid_constant__ SfarLatentAppendArgs a)
 {
     constexpr int kV = L / 256;                    // 16-byte vectors of latents per lane
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     const long long item = (long long)blockIdx.x * SFAR_LATENT_APPEND_WARPS + warp;
-    const int r = (int)(item % a.R), t = (int)(item / a.R);
+    const int t = (int)(item / a.R), r = (int)(item - (long long)t * a.R);
     if (t >= a.T)
         return;
     const int slot = a.slots[t], n = a.pos[t];
-    if (slot < -1 || slot >= a.slot_end) {
-        if (lane == 0)
-            sfar_kv_fault(a.ctl, t, SFAR_KV_BAD_SLOT);
-        return;
-    }
-    if (slot < 0 || n < 0)
-        return;
     const uint16_t *x = a.x[r] + t * a.ts;
     uint4 v[kV], w[kV];
 #pragma unroll
@@ -55,38 +52,55 @@ template <int L> __global__ void __launch_bounds__(32 * SFAR_LATENT_APPEND_WARPS
     // the key: pair `lane` of rope / 2
     const int half = a.rope / 2, first = a.inter ? 2 * lane : lane, second = a.inter ? first + 1 : lane + half;
     const bool pair = lane < half;
-    const float p = pair ? lo(x[L + first]) : 0.f, q = pair ? lo(x[L + second]) : 0.f;
-    float2 cs = make_float2(0.f, 0.f);
-    if (pair)
-        cs = sfar_cos_sin(n, a.freq[lane]);
-    float s = 0.f;
+    uint32_t k = 0;
+    float freq = 0.f;
+    if (pair) {
+        freq = a.freq[lane];
+        k = a.inter ? *reinterpret_cast<const uint32_t *>(x + L + first) : x[L + first] | (uint32_t)x[L + second] << 16;
+    }
+    if (slot < -1 || slot >= a.slot_end) {
+        if (lane == 0)
+            sfar_kv_fault(a.ctl, t, SFAR_KV_BAD_SLOT);
+        return;
+    }
+    if (slot < 0 || n < 0)
+        return;
+    const float2 cs = sfar_cos_sin(n, freq);
+    uint64_t two = 0;                              // two sums at once
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
         const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            s = fmaf(hi(u[j]), hi(u[j]), fmaf(lo(u[j]), lo(u[j]), s));
+        for (int j = 0; j < 4; ++j) {
+            const uint64_t y = tc::pack2(lo(u[j]), hi(u[j]));
+            two = tc::fma2(y, y, two);
+        }
     }
+    const float2 both = tc::unpack2(two);
+    float s = both.x + both.y;
 #pragma unroll
-    for (int d = 16; d; d >>= 1)
-        s += __shfl_xor_sync(SFAR_FULL, s, d);
-    const float by = 1.f / sqrtf(s * (1.f / L) + a.eps);
+    for (int e = 16; e; e >>= 1)
+        s += __shfl_xor_sync(SFAR_FULL, s, e);
+    const float by = rsqrtf(fmaf(s, 1.f / L, a.eps));
+    const uint64_t by2 = tc::pack2(by, by);
     uint16_t *to = a.cache[r] + (long long)slot * (L + a.rope);
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
         const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w}, g[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
         uint32_t y[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            y[j] = pack(lo(u[j]) * by * lo(g[j]), hi(u[j]) * by * hi(g[j]));
+        for (int j = 0; j < 4; ++j) {
+            const float2 z = tc::unpack2(tc::mul2(tc::mul2(tc::pack2(lo(u[j]), hi(u[j])), by2), tc::pack2(lo(g[j]), hi(g[j]))));
+            y[j] = pack(z.x, z.y);
+        }
         st_v4(to + 256 * i + 8 * lane, make_uint4(y[0], y[1], y[2], y[3]));
     }
     if (pair) {
-        const float c = cs.x * a.scale, d = cs.y * a.scale;
+        const float c = cs.x * a.scale, d = cs.y * a.scale, p = lo(k), q = hi(k);
         const uint32_t y = pack(p * c - q * d, q * c + p * d);
-        if (a.inter)
+        if (a.inter) {
             *reinterpret_cast<uint32_t *>(to + L + first) = y;
-        else {
+        } else {
             to[L + first] = (uint16_t)y;
             to[L + second] = (uint16_t)(y >> 16);
         }

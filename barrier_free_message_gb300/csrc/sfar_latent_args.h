@@ -14,7 +14,7 @@ struct SfarRopeArgs {
     long long its[2], ihs[2], ots[2], ohs[2];   // strides of a token and of a head, elements
     float scale;
     int T, R, H[2], half;                   // half: pairs of a row
-    int span;                               // work items (rank, head, 8 pairs) of a token that a CTA takes
+    int span;                               // (rank, head) rows of a token that a CTA takes
 };
 
 struct SfarLatentAppendArgs {

@@ -91,7 +91,7 @@ sfar_status sfar_rope(sfar_t *h, const void *const q[], void *const q_out[], con
                       int layout, float scale, sfar_stream_t s)
 {
     if (!h || (q_heads && (!q || !q_out)) || (k_heads && (!k || !k_out)) || q_heads + k_heads == 0 || q_heads > 65535 || k_heads > 65535 ||
-        rot == 0 || rot % 16 || rot > 1024 || tokens >= (1ull << 31) || (layout != SFAR_ROPE_HALF && layout != SFAR_ROPE_INTERLEAVED) ||
+        rot == 0 || rot % 16 || rot > 1024 || (q_heads + k_heads) * rot >= 1u << 22 || tokens >= (1ull << 31) || (layout != SFAR_ROPE_HALF && layout != SFAR_ROPE_INTERLEAVED) ||
         !isfinite(scale))
         return SFAR_ERR_INVALID;
     if (tokens == 0)
@@ -146,12 +146,13 @@ sfar_status sfar_rope(sfar_t *h, const void *const q[], void *const q_out[], con
     a.T = (int)tokens;
     a.R = v.R;
     a.half = (int)(rot / 2);
-    // a CTA a token, or several where that would leave SMs without one
-    const size_t all = (size_t)v.R * (q_heads + k_heads) * (rot / 16);
-    const size_t cuts = std::min(std::min(ceil_div(all, SFAR_ROPE_THREADS), ceil_div(2 * (size_t)v.sms, tokens)), (size_t)64);
-    a.span = (int)ceil_div(all, cuts);
+    // a thread to 8 pairs, whole rows to a CTA, equally many to each
+    const size_t rows = (size_t)v.R * (q_heads + k_heads), chunks = rot / 16;
+    const size_t cuts = ceil_div(rows, SFAR_ROPE_THREADS / chunks);
+    a.span = (int)ceil_div(rows, cuts);
+    const unsigned threads = (unsigned)(ceil_div((size_t)a.span * chunks, 32) * 32);
     return launch(v.dev, sfar_kernel_rope(v.dt == SFAR_BF16 ? 0 : 1, layout == SFAR_ROPE_INTERLEAVED), dim3((unsigned)tokens, (unsigned)cuts),
-                  SFAR_ROPE_THREADS, rot * 4, &a, s, v.mode == SFAR_LAUNCH_PLAIN);
+                  threads, chunks * 80, &a, s, v.mode == SFAR_LAUNCH_PLAIN);
 }
 
 sfar_status sfar_rope_frequencies(float *freq, float *scale, size_t rot, double base, int scaling, double factor, double trained,
