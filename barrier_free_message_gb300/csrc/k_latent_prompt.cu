@@ -27,15 +27,15 @@ namespace {
 
 constexpr int kTile = 128, kGroup = SFAR_LATENT_GROUP, kBox = kTile * 128;     // bytes of 64 elements of 128 tokens
 constexpr int kPieces = 4;
-constexpr int kRegsSoft = 216, kRegsRest = 72;     // 8 warps, 4 warps: together the launch's 12 x 168
+constexpr int kRegsSoft = 104, kRegsRest = 64;     // with two tiles, 16 warps and 4: together the launch's 20 x 96
 
 template <int D, int TILES> struct Lay {
     static constexpr int kV = D / 64, kK = kV + 1;                 // boxes of a step's values, keys
     static constexpr int kQ = TILES * kK * kBox;
     static constexpr int kSlots = TILES == 2 && D == 128 ? 8 : 10;
     static constexpr int kBytes = kQ + kSlots * kBox;
+    static constexpr int kSoftWarps = 8 * TILES, kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kThreads = 32 * (kSoftWarps + 4);
 };
-enum { kSoftWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kThreads = 384 };
 
 // 128 or 256 rows of one head of a request.
 struct Piece {
@@ -44,6 +44,17 @@ struct Piece {
     int steps[2];               // tiles of the context that each tile of rows attends to
 };
 
+// The two warps that share 32 rows.
+__device__ __forceinline__ void pair_sync(int pair) { asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory"); }
+__device__ __forceinline__ bool pair_any(int pair, bool v)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\tbar.red.or.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"(1 + pair), "r"((uint32_t)v)
+                 : "memory");
+    return r != 0;
+}
 __device__ __forceinline__ bool odd2(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
@@ -66,10 +77,11 @@ __device__ __forceinline__ bool request(const SfarLatentPromptArgs &a, int b, in
 
 }  // namespace
 
-template <int D, int TILES> __global__ void __launch_bounds__(kThreads, 1) k_latent_prompt(const __grid_constant__ SfarLatentPromptArgs a)
+template <int D, int TILES>
+__global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(const __grid_constant__ SfarLatentPromptArgs a)
 {
     using Y = Lay<D, TILES>;
-    constexpr int kRows = 128 * TILES;
+    constexpr int kRows = 128 * TILES, kThreads = Y::kThreads, kSoftWarps = Y::kSoftWarps, kCopyWarp = Y::kCopyWarp, kMmaWarp = Y::kMmaWarp;
     extern __shared__ __align__(1024) unsigned char dyn[];
     __shared__ __align__(8) unsigned long long bars[2 * Y::kSlots + 2 * kPieces + 11];
     __shared__ Piece s_piece[kPieces];
@@ -90,7 +102,7 @@ template <int D, int TILES> __global__ void __launch_bounds__(kThreads, 1) k_lat
     }
     if (tid == 0) {
         for (uint32_t b = full; b <= drain; b += 8)
-            tc::bar_init(b, b >= pempty && b < qfull ? 4 * TILES + 1 : b >= wbar && b < obar ? 4 : 1);
+            tc::bar_init(b, b >= pempty && b < qfull ? kSoftWarps + 1 : b >= wbar && b < obar ? 8 : 1);
         tc::bar_fence_init();
         tc::fence_async();
         upto[0] = 0;
@@ -138,178 +150,184 @@ template <int D, int TILES> __global__ void __launch_bounds__(kThreads, 1) k_lat
     const uint32_t items = many ? 0 : carry * (uint32_t)(a.R * a.Hq);
 
     if (warp < kSoftWarps) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-        const int x = warp >> 2;                   // tile
-        if (x < TILES) {
-            // ---------------------------------------------------------- softmax
-            bool dead = false;                     // a wait gave up: go on without waiting
-            const int lrow = (warp & 3) * 32 + lane;
-            const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16, tS = tmem + x * 256 + lanes, tO = tS + 128;
-            // never 0, so that a masked score of -inf stays that
-            const float f = fmaxf(a.scale * 1.4426950408889634f, 1e-37f);
-            tc::Ring<kPieces> ps;
-            uint32_t sphase = 0, ophase = 0, slot = 0;     // slot: boxes that came before this step's keys
-            for (int piece = 0;; ++piece) {
-                dead = dead || !tc::bar_wait(pfull + 8 * ps.slot, ps.phase, limit);
-                dead = __any_sync(SFAR_FULL, dead);
-                if (dead)
-                    break;
-                const Piece p = s_piece[ps.slot];
-                __syncwarp();
-                if (lane == 0)
-                    tc::bar_arrive(pempty + 8 * ps.slot);
-                ps.next();
-                if (p.b < 0)
-                    break;
-                if (tid == 0)
-                    s_odd[(piece + 2) & 3] = INT_MAX;
-                const int i = p.rt * kRows + x * 128 + lrow, pos = p.len - p.count + i;
-                const int all_to = min(p.len, p.len - p.count + p.rt * kRows + 1);     // every row of both tiles sees the tokens before it
-                const bool row = i < p.count;
-                const int hi = row ? pos + 1 : INT_MAX;
-                const int mine_to = p.len - p.count + p.rt * kRows + x * 128 + 1;      // every row of this tile
-                float ref = -INFINITY, sum = 0.f;
-                const int steps = p.steps[x], whole = max(p.steps[0], p.steps[1]);
-                for (int k = 0; k < steps; ++k) {
-                    const int j0 = k * kTile;
-                    dead = dead || !tc::bar_wait(sbar + 8 * x, sphase, limit);
-                    sphase ^= 1u;
-                    tc::fence_after();
-                    uint32_t s[4][32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        tc::ld32(s[c], tS + 32 * c);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        tc::wait_ld(s[c]);
-                    if (j0 + kTile > all_to && (x == 0 || k >= p.steps[0])) {
-                        // Values of tokens that not every row sees, a token to a thread: one past the context, or with an
-                        // infinity or NaN, becomes zeros (0 times it would reach the rows that do not see it); the rows that
-                        // see the latter become NaN at the end.
-                        const int j = j0 + lrow;
-                        uint32_t at = slot + k * (Y::kK + Y::kV) + Y::kK;
-#pragma unroll
-                        for (int c = 0; c < Y::kV; ++c)
-                            dead = dead || !tc::bar_wait(full + 8 * ((at + c) % Y::kSlots), (at + c) / Y::kSlots & 1u, limit);
-                        if (j >= all_to) {
-                            bool odd = false;
-#pragma unroll
-                            for (int c = 0; c < Y::kV; ++c) {
-                                const unsigned char *v = gen + Y::kQ + (at + c) % Y::kSlots * kBox + lrow * 128;
-                                for (int e = 0; e < 8; ++e) {
-                                    const uint4 w = *reinterpret_cast<const uint4 *>(v + ((e ^ (lrow & 7)) << 4));
-                                    odd = odd || odd2(w.x) || odd2(w.y) || odd2(w.z) || odd2(w.w);
-                                }
-                            }
-                            if (odd) {
-                                if (j < p.len)
-                                    atomicMin(&s_odd[piece & 3], j);
-#pragma unroll
-                                for (int c = 0; c < Y::kV; ++c) {
-                                    unsigned char *v = gen + Y::kQ + (at + c) % Y::kSlots * kBox + lrow * 128;
-                                    for (int e = 0; e < 8; ++e)
-                                        *reinterpret_cast<uint4 *>(v + (e << 4)) = make_uint4(0, 0, 0, 0);
-                                }
-                            }
+        // -------------------------------------------------------------- softmax
+        if constexpr (TILES == 2)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+        bool dead = false;                         // a wait gave up: go on without waiting
+        // two threads to a row of scores, and of the accumulator: the first half of the columns and the second
+        const int x = warp >> 3, half = warp >> 2 & 1, pair = x * 4 + (warp & 3), lrow = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16, tS = tmem + x * 256 + 64 * half + lanes, tO = tmem + x * 256 + 128 + D / 2 * half + lanes;
+        // What the two threads of a row tell each other, in a column of the scores that have been read (shared memory is full).
+        auto swap = [&](float v) {
+            tc::st1(tS + 63, __float_as_uint(v));
+            tc::wait_st();
+            tc::fence_before();
+            pair_sync(pair);
+            tc::fence_after();
+            uint32_t r[1];
+            tc::ld1(r, tS + 63 + (half ? -64 : 64));
+            tc::wait_ld(r);
+            return __uint_as_float(r[0]);
+        };
+        // never 0, so that a masked score of -inf stays that
+        const float f = fmaxf(a.scale * 1.4426950408889634f, 1e-37f);
+        const uint64_t f2 = tc::pack2(f, f);
+        tc::Ring<kPieces> ps;
+        uint32_t sphase = 0, ophase = 0, slot = 0;         // slot: boxes that came before this step's keys
+        for (int piece = 0;; ++piece) {
+            dead = dead || !tc::bar_wait(pfull + 8 * ps.slot, ps.phase, limit);
+            dead = pair_any(pair, dead);
+            if (dead)
+                break;
+            const Piece &p = s_piece[ps.slot];
+            if (p.b < 0)
+                break;
+            if (tid == 0)
+                s_odd[(piece + 2) & 3] = INT_MAX;
+            const int i = p.rt * kRows + x * 128 + lrow, pos = p.len - p.count + i, len = p.len;
+            const int all_to = min(len, len - p.count + p.rt * kRows + 1);         // every row of both tiles sees the tokens before it
+            const bool row = i < p.count;
+            const int hi = (row ? pos + 1 : INT_MAX) - 64 * half;                   // of this thread's columns
+            const int mine_to = len - p.count + p.rt * kRows + x * 128 + (warp & 3) * 32 + 1 - 64 * half;   // every row of this warp
+            float ref = -INFINITY, sum = 0.f;      // of the row; of this half
+            const int steps = p.steps[x], before = p.steps[0];
+            for (int k = 0; k < steps; ++k) {
+                const int j0 = k * kTile;
+                dead = dead || !tc::bar_wait(sbar + 8 * x, sphase, limit);
+                sphase ^= 1u;
+                tc::fence_after();
+                uint32_t s[2][32];
+                tc::ld32(s[0], tS);
+                tc::ld32(s[1], tS + 32);
+                tc::wait_ld(s[0]);
+                tc::wait_ld(s[1]);
+                if (j0 + kTile > all_to && (x == 0 || k >= before) && half < Y::kV) {
+                    // Values of tokens that not every row sees, a token's 64 to a thread: with an infinity or NaN they become
+                    // zeros (0 times it would reach the rows that do not see it); the rows that see them become NaN at the end.
+                    const int j = j0 + lrow;
+                    const uint32_t at = slot + k * (Y::kK + Y::kV) + Y::kK + half;
+                    dead = dead || !tc::bar_wait(full + 8 * (at % Y::kSlots), at / Y::kSlots & 1u, limit);
+                    if (j >= all_to) {
+                        unsigned char *v = gen + Y::kQ + at % Y::kSlots * kBox + lrow * 128;
+                        bool odd = false;
+#pragma unroll 4
+                        for (int e = 0; e < 8; ++e) {
+                            const uint4 w = *reinterpret_cast<const uint4 *>(v + ((e ^ (lrow & 7)) << 4));
+                            odd = odd || odd2(w.x) || odd2(w.y) || odd2(w.z) || odd2(w.w);
                         }
-                        tc::fence_async();
-                    }
-                    if (j0 + kTile > mine_to) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (j0 + 32 * c + e >= hi)
-                                    s[c][e] = 0xff800000u;
-                    }
-                    float m[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        m[c] = max3(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]), __uint_as_float(s[c][2]));
-#pragma unroll
-                        for (int e = 3; e < 31; e += 2)
-                            m[c] = max3(m[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
-                        m[c] = fmaxf(m[c], __uint_as_float(s[c][31]));
-                    }
-                    const float now = fmaxf(max3(m[0], m[1], m[2]), m[3]) * f;
-                    const bool move = now - ref > kAttnLift;
-                    if (__any_sync(SFAR_FULL, move)) {
-                        const float next = move ? now : ref;
-                        const float keep = ref == -INFINITY ? 1.f : ex2(ref - next);      // all is 0 then, or NaN
-                        ref = next;
-                        sum *= keep;
-                        if (k) {
-#pragma unroll
-                            for (int c = 0; c < D; c += 16) {
-                                uint32_t o[16];
-                                tc::ld16(o, tO + c);
-                                tc::wait_ld(o);
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-                                tc::st16(tO + c, o);
-                            }
+                        if (odd) {
+                            if (j < len)
+                                atomicMin(&s_odd[piece & 3], j);
+                            for (int e = 0; e < 8; ++e)
+                                *reinterpret_cast<uint4 *>(v + (e << 4)) = make_uint4(0, 0, 0, 0);
                         }
                     }
-                    // a row that has seen nothing: any finite reference, weights 0
-                    const float base = ref == -INFINITY ? 0.f : ref;
-                    const uint64_t f2 = tc::pack2(f, f), b2 = tc::pack2(-base, -base);
-                    float part[4] = {0.f, 0.f, 0.f, 0.f};
+                    tc::fence_async();
+                }
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t w[16];
+                for (int c = 0; c < 2; ++c)
+                    if (j0 + 32 * c + 32 > mine_to) {
+                        const int n = hi - j0 - 32 * c;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float2 y = tc::unpack2(tc::fma2(tc::pack2u(s[c][e], s[c][e + 1]), f2, b2));
-                            const float u = ex2(y.x), v = ex2(y.y);
-                            part[e >> 1 & 3] += u + v;
-                            w[e >> 1] = tc::bf16x2(u, v);
-                        }
-                        tc::st16(tS + 16 * c, w);
+                        for (int e = 0; e < 32; ++e)
+                            if (e >= n)
+                                s[c][e] = 0xff800000u;
                     }
-                    sum += (part[0] + part[1]) + (part[2] + part[3]);
+                float m[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    m[c] = max3(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]), __uint_as_float(s[c][2]));
+#pragma unroll
+                    for (int e = 3; e < 31; e += 2)
+                        m[c] = max3(m[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+                }
+                float now = fmaxf(max3(m[0], m[1], __uint_as_float(s[0][31])), __uint_as_float(s[1][31])) * f;
+                if (pair_any(pair, now - ref > kAttnLift)) {
+                    now = fmaxf(now, swap(now));
+                    const float next = now - ref > kAttnLift ? now : ref;
+                    const float keep = ref == -INFINITY ? 1.f : ex2(ref - next);           // all is 0 then, or NaN
+                    ref = next;
+                    sum *= keep;
+                    if (k) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 2; c += 16) {
+                            uint32_t o[16];
+                            tc::ld16(o, tO + c);
+                            tc::wait_ld(o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                            tc::st16(tO + c, o);
+                        }
+                    }
                     tc::wait_st();
                     tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        tc::bar_arrive(wbar + 8 * x);
+                    pair_sync(pair);               // the other's has been read
                 }
-                slot += whole * (Y::kK + Y::kV);
-                slot = slot % (2 * Y::kSlots);     // its parity counts, too
-                if (steps) {
-                    dead = dead || !tc::bar_wait(obar + 8 * x, ophase, limit);
-                    ophase ^= 1u;
-                    tc::fence_after();
-                }
-                const bool nan = row && *(volatile int *)&s_odd[piece & 3] < hi;
-                const float by = nan ? NAN : sum == 0.f ? 0.f : 1.f / sum;
-                uint16_t *dst = a.out[p.r] + (long long)(p.first + min(i, p.count - 1)) * a.ots + (long long)p.h * a.ohs;
+                // a row that has seen nothing: any finite reference, weights 0
+                const float base = ref == -INFINITY ? 0.f : ref;
+                const uint64_t b2 = tc::pack2(-base, -base);
+                uint64_t part = 0;
 #pragma unroll
-                for (int c = 0; c < D; c += 16) {
-                    uint32_t o[16];
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t w[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        o[e] = 0;
-                    if (steps) {
-                        tc::ld16(o, tO + c);
-                        tc::wait_ld(o);
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 y = tc::unpack2(tc::fma2(tc::pack2u(s[c][e], s[c][e + 1]), f2, b2));
+                        const float u = ex2(y.x), v = ex2(y.y);
+                        part = tc::add2(part, tc::pack2(u, v));
+                        w[e >> 1] = tc::bf16x2(u, v);
                     }
-                    uint32_t y[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        y[e] = tc::bf16x2(__uint_as_float(o[2 * e]) * by, __uint_as_float(o[2 * e + 1]) * by);
-                    if (row)
-                        tc::st32(dst + c, y);
+                    tc::st16(tS + 16 * c, w);
                 }
+                const float2 both = tc::unpack2(part);
+                sum += both.x + both.y;
+                if (k == steps - 1)
+                    sum += swap(sum);              // of the row, from here on
+                tc::wait_st();
                 tc::fence_before();
                 __syncwarp();
+                if (lane == 0)
+                    tc::bar_arrive(wbar + 8 * x);
             }
-            if (dead && lane == 0)
-                sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
+            slot = (slot + max(before, p.steps[1]) * (Y::kK + Y::kV)) % (2 * Y::kSlots);       // its parity counts, too
+            if (steps) {
+                dead = dead || !tc::bar_wait(obar + 8 * x, ophase, limit);
+                ophase ^= 1u;
+                tc::fence_after();
+            }
+            const bool nan = row && *(volatile int *)&s_odd[piece & 3] < hi + 64 * half;
+            const float by = nan ? NAN : sum == 0.f ? 0.f : 1.f / sum;
+            uint16_t *dst = a.out[p.r] + (long long)(p.first + min(i, p.count - 1)) * a.ots + (long long)p.h * a.ohs + D / 2 * half;
+#pragma unroll
+            for (int c = 0; c < D / 2; c += 16) {
+                uint32_t o[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    o[e] = 0;
+                if (steps) {
+                    tc::ld16(o, tO + c);
+                    tc::wait_ld(o);
+                }
+                uint32_t y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    y[e] = tc::bf16x2(__uint_as_float(o[2 * e]) * by, __uint_as_float(o[2 * e + 1]) * by);
+                if (row)
+                    tc::st32(dst + c, y);
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0)
+                tc::bar_arrive(pempty + 8 * ps.slot);
+            ps.next();
         }
+        if (dead && lane == 0)
+            sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
         sfar_attn_padding<D>(a, tid, 32 * kSoftWarps);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+        if constexpr (TILES == 2)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
         if (warp == kCopyWarp) {
             // ------------------------------------------------------------ copies
             const uint64_t often = tc::evict_last(), once = tc::evict_first();
@@ -478,7 +496,7 @@ template <int D, int TILES> __global__ void __launch_bounds__(kThreads, 1) k_lat
                                     const uint64_t dv = tc::desc_n128(ring + v0 * kBox, kBox);
 #pragma unroll
                                     for (int i = 0; i < kTile / 16; ++i)
-                                        tc::mma_f16_ts(tS + 128, tS + 8 * i, dv + 128 * i, idO, k > 1 || i > 0);
+                                        tc::mma_f16_ts(tS + 128, tS + (i < 4 ? 8 * i : 32 + 8 * i), dv + 128 * i, idO, k > 1 || i > 0);
                                 } else {
                                     constexpr uint32_t idH = tc::idesc_bf16(128, 64) | tc::kTransposeB;
 #pragma unroll
@@ -486,7 +504,7 @@ template <int D, int TILES> __global__ void __launch_bounds__(kThreads, 1) k_lat
                                         const uint64_t dv = tc::desc_n128(ring + (c ? v1 : v0) * kBox, kBox);
 #pragma unroll
                                         for (int i = 0; i < kTile / 16; ++i)
-                                            tc::mma_f16_ts(tS + 128 + 64 * c, tS + 8 * i, dv + 128 * i, idH, k > 1 || i > 0);
+                                            tc::mma_f16_ts(tS + 128 + 64 * c, tS + (i < 4 ? 8 * i : 32 + 8 * i), dv + 128 * i, idH, k > 1 || i > 0);
                                     }
                                 }
                                 if (k == n[x])
@@ -549,7 +567,7 @@ template <int D, int TILES> __global__ void __launch_bounds__(kThreads, 1) k_lat
 const void *sfar_kernel_latent_prompt(int head_dim, int tiles, int *threads, int *smem)
 {
 #define SFAR_PROMPT(D, N) (*smem = Lay<D, N>::kBytes + 1024, (const void *)k_latent_prompt<D, N>)
-    *threads = kThreads;
+    *threads = tiles == 1 ? Lay<64, 1>::kThreads : Lay<64, 2>::kThreads;
     if (tiles == 1)
         return head_dim == 64 ? SFAR_PROMPT(64, 1) : SFAR_PROMPT(128, 1);
     return head_dim == 64 ? SFAR_PROMPT(64, 2) : SFAR_PROMPT(128, 2);

@@ -168,7 +168,11 @@ template <int N> __device__ __forceinline__ void wait_ld(uint32_t (&v)[N])
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 #define SFAR_R4(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3])
-// 32 lanes x 8, 16 or 32 columns of 32 bits: lane = the warp's TMEM lane, v[c] = column c
+// 32 lanes x 1, 8, 16 or 32 columns of 32 bits: lane = the warp's TMEM lane, v[c] = column c
+__device__ __forceinline__ void ld1(uint32_t (&v)[1], uint32_t addr)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v[0]) : "r"(addr));
+}
 __device__ __forceinline__ void ld8(uint32_t (&v)[8], uint32_t addr)
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : SFAR_R4(v, 0), SFAR_R4(v, 4) : "r"(addr));
@@ -221,6 +225,10 @@ __device__ __forceinline__ void st16(uint32_t addr, const uint32_t (&v)[16])
         : "memory");
 }
 
+__device__ __forceinline__ void st1(uint32_t addr, uint32_t v)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void st8(uint32_t addr, const uint32_t (&v)[8])
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -323,6 +331,12 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
 {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
