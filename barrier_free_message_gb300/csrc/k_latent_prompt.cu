@@ -26,7 +26,7 @@
 namespace {
 
 constexpr int kTile = 128, kGroup = SFAR_LATENT_GROUP, kBox = kTile * 128;     // bytes of 64 elements of 128 tokens
-constexpr int kPieces = 4;
+constexpr int kPieces = 4, kAhead = 0;              // kAhead: steps between a tile's way to L2 and its copy
 constexpr int kRegsSoft = 104, kRegsRest = 64;     // with two tiles, 16 warps and 4: together the launch's 20 x 96
 
 template <int D, int TILES> struct Lay {
@@ -335,58 +335,74 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
             tc::Ring<Y::kSlots> st;
             tc::Ring<kPieces> ps;
             bool dead = false;
-            uint32_t boxes = 0, taken = blockIdx.x, qphase[2] = {1, 1}, queries[2] = {0, 0};     // queries: asked for
+            uint32_t boxes = 0, qphase[2] = {1, 1}, queries[2] = {0, 0};     // queries: asked for
             const int groups = (a.B + kGroup - 1) / kGroup;
-            const uint32_t planes = (uint32_t)(a.R * a.Hq), wrap = items - 1;
-            for (; !dead;) {
+            const uint32_t planes = (uint32_t)(a.R * a.Hq);
+            // row tile number `taken`, by the whole warp
+            auto piece = [&](uint32_t taken) {
                 Piece p;
                 p.b = -1;
-                const bool end = taken >= items;
-                // the next one is asked for early: one question for each row tile, so the counter is back at 0 when all are taken
-                uint32_t after = 0;
-                if (!end && lane == 0)
-                    asm volatile("atom.relaxed.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(after) : "l"(a.next), "r"(wrap) : "memory");
-                if (!end) {
-                    int lo = 0, hi = groups;
-                    while (hi - lo > 1) {
-                        const int mid = (lo + hi) >> 1;
-                        if (upto[mid] * planes <= taken)
-                            lo = mid;
-                        else
-                            hi = mid;
-                    }
-                    uint32_t v = taken - upto[lo] * planes;
-                    const int b = lo * kGroup + lane;
-                    int len = 0, count = 0, first = 0, kfirst = 0;
-                    if (b < a.B)
-                        request(a, b, len, count, first, kfirst);
-                    const uint32_t n = (uint32_t)(count + kRows - 1) / kRows;
-                    uint32_t sum = n;
-#pragma unroll
-                    for (int d = 1; d < 32; d <<= 1) {
-                        const uint32_t o = __shfl_up_sync(SFAR_FULL, sum, d);
-                        if (lane >= d)
-                            sum += o;
-                    }
-                    const unsigned past = __ballot_sync(SFAR_FULL, sum * planes > v);
-                    const int l = past ? __ffs(past) - 1 : 0;
-                    p.b = lo * kGroup + l;
-                    p.len = __shfl_sync(SFAR_FULL, len, l);
-                    p.count = __shfl_sync(SFAR_FULL, count, l);
-                    p.first = __shfl_sync(SFAR_FULL, first, l);
-                    p.kfirst = __shfl_sync(SFAR_FULL, kfirst, l);
-                    const uint32_t tiles = max(1u, __shfl_sync(SFAR_FULL, n, l));
-                    v -= __shfl_sync(SFAR_FULL, sum - n, l) * planes;
-                    const uint32_t plane = v / tiles;
-                    p.rt = (int)(tiles - 1 - (v - plane * tiles));
-                    p.r = (int)(plane / (uint32_t)a.Hq);
-                    p.h = (int)(plane - (uint32_t)p.r * (uint32_t)a.Hq);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int from = p.rt * kRows + x * 128, last = min(p.count, from + 128) - 1;      // tile's last row
-                        p.steps[x] = x < TILES && from < p.count ? (max(0, p.len - p.count + last + 1) + kTile - 1) / kTile : 0;
-                    }
+                p.steps[0] = p.steps[1] = 0;
+                if (taken >= items)
+                    return p;
+                int lo = 0, hi = groups;
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (upto[mid] * planes <= taken)
+                        lo = mid;
+                    else
+                        hi = mid;
                 }
+                uint32_t v = taken - upto[lo] * planes;
+                const int b = lo * kGroup + lane;
+                int len = 0, count = 0, first = 0, kfirst = 0;
+                if (b < a.B)
+                    request(a, b, len, count, first, kfirst);
+                const uint32_t n = (uint32_t)(count + kRows - 1) / kRows;
+                uint32_t sum = n;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const uint32_t o = __shfl_up_sync(SFAR_FULL, sum, d);
+                    if (lane >= d)
+                        sum += o;
+                }
+                const unsigned past = __ballot_sync(SFAR_FULL, sum * planes > v);
+                const int l = past ? __ffs(past) - 1 : 0;
+                p.b = lo * kGroup + l;
+                p.len = __shfl_sync(SFAR_FULL, len, l);
+                p.count = __shfl_sync(SFAR_FULL, count, l);
+                p.first = __shfl_sync(SFAR_FULL, first, l);
+                p.kfirst = __shfl_sync(SFAR_FULL, kfirst, l);
+                const uint32_t tiles = max(1u, __shfl_sync(SFAR_FULL, n, l));
+                v -= __shfl_sync(SFAR_FULL, sum - n, l) * planes;
+                const uint32_t plane = v / tiles;
+                p.rt = (int)(tiles - 1 - (v - plane * tiles));
+                p.r = (int)(plane / (uint32_t)a.Hq);
+                p.h = (int)(plane - (uint32_t)p.r * (uint32_t)a.Hq);
+#pragma unroll
+                for (int x = 0; x < TILES; ++x) {
+                    const int from = p.rt * kRows + x * 128, last = min(p.count, from + 128) - 1;      // tile's last row
+                    if (from < p.count)
+                        p.steps[x] = (max(0, p.len - p.count + last + 1) + kTile - 1) / kTile;
+                }
+                return p;
+            };
+            // Keys and values of step k on their way to L2, by one lane: a ring of a step and a half hides L2's latency, not HBM's.
+            auto ahead = [&](const Piece &p, int k) {
+                const int y = p.kfirst + k * kTile;
+#pragma unroll
+                for (int c = 0; c < Y::kV; ++c) {
+                    tc::prefetch_3d(&a.kmap[p.r], 64 * c, p.h, y);
+                    tc::prefetch_3d(&a.vmap[p.r], 64 * c, p.h, y);
+                }
+                tc::prefetch_2d(&a.krmap[p.r], 0, y);
+            };
+            Piece p = piece(blockIdx.x);
+            for (;;) {
+                // The next one is asked for early: one question for each row tile, so the counter is back at 0 when all are taken.
+                uint32_t after = 0;
+                if (p.b >= 0 && lane == 0)
+                    asm volatile("atom.relaxed.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(after) : "l"(a.next), "r"(items - 1) : "memory");
                 if (!wait(pempty + 8 * ps.slot, ps.phase ^ 1u)) {
                     dead = true;
                     break;
@@ -396,10 +412,13 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                     tc::bar_arrive(pfull + 8 * ps.slot);
                 }
                 ps.next();
-                if (end)
+                if (p.b < 0)
                     break;
+                Piece next;
                 const int steps = max(p.steps[0], p.steps[1]);
-                for (int k = 0; k < steps && !dead; ++k)
+                if (steps == 0)
+                    next = piece(gridDim.x + __shfl_sync(SFAR_FULL, after, 0));
+                for (int k = 0; k < steps && !dead; ++k) {
                     for (int c = 0; c < Y::kK + Y::kV; ++c) {
                         if (!wait(empty + 8 * st.slot, st.phase ^ 1u)) {
                             dead = true;
@@ -439,7 +458,19 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                                 break;
                         }
                     }
-                taken = gridDim.x + __shfl_sync(SFAR_FULL, after, 0);
+                    if (k == 0)
+                        next = piece(gridDim.x + __shfl_sync(SFAR_FULL, after, 0));
+                    const int far = k + kAhead, more = max(next.steps[0], next.steps[1]);
+                    if (kAhead && lane == 0 && far < steps)
+                        ahead(p, far);
+                    else if (kAhead && lane == 0 && far - steps < more)
+                        ahead(next, far - steps);
+                    if (k == max(0, steps - 2) && lane < TILES * Y::kK && next.steps[lane / Y::kK])
+                        tc::prefetch_3d(&a.qmap[next.r], 64 * (lane % Y::kK), next.h, next.first + next.rt * kRows + lane / Y::kK * 128);
+                }
+                if (dead)
+                    break;
+                p = next;
             }
             if (dead && lane == 0) {
                 sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
@@ -469,7 +500,7 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                 if (b < 0)
                     break;
                 if (tc::elect_one()) {             // the same lane every time: the phases stay in its registers
-                    const int most = max(n[0], n[1]);
+                    const int most = max(n[0], n[1]), last = TILES == 2 && n[1] ? 1 : 0;       // last: the tile that a box is used by last
                     auto there = [&](uint32_t at) { return tc::bar_wait(full + 8 * (at % Y::kSlots), at / Y::kSlots & 1u, limit); };
                     auto wait = [&](uint32_t bar, uint32_t &phase) {
                         const bool in = tc::bar_wait(bar, phase, limit);
@@ -484,9 +515,10 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                             if (k && k <= n[x]) {
                                 // O += P V of the step before
                                 dead = dead || !wait(wbar + 8 * x, wphase[x]);
+                                if (x == 0 || k > n[0])
 #pragma unroll
-                                for (int c = 0; c < Y::kV; ++c)
-                                    dead = dead || !there(values + c);
+                                    for (int c = 0; c < Y::kV; ++c)
+                                        dead = dead || !there(values + c);
                                 if (dead)
                                     break;
                                 tc::fence_after();
@@ -507,6 +539,10 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                                             tc::mma_f16_ts(tS + 128 + 64 * c, tS + (i < 4 ? 8 * i : 32 + 8 * i), dv + 128 * i, idH, k > 1 || i > 0);
                                     }
                                 }
+                                if (x == last)
+#pragma unroll
+                                    for (int c = 0; c < Y::kV; ++c)
+                                        tc::commit(empty + 8 * ((values + c) % Y::kSlots));
                                 if (k == n[x])
                                     tc::commit(obar + 8 * x);
                             }
@@ -515,7 +551,8 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                                 dead = dead || (k == 0 && !wait(qfull + 8 * x, qphase[x]));
 #pragma unroll
                                 for (int c = 0; c < Y::kK; ++c) {
-                                    dead = dead || !there(keys + c);
+                                    if (x == 0 || k >= n[0])
+                                        dead = dead || !there(keys + c);
                                     if (dead)
                                         break;
                                     tc::fence_after();
@@ -523,6 +560,8 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                                     const int parts = c < Y::kV ? 4 : a.rope / 16;
                                     for (int i = 0; i < parts; ++i)
                                         tc::mma_f16_ss(tS, q + 2 * i, d + 2 * i, idS, c + i > 0);
+                                    if (x == last)
+                                        tc::commit(empty + 8 * ((keys + c) % Y::kSlots));
                                 }
                                 if (dead)
                                     break;
@@ -533,14 +572,6 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                         }
                         if (dead)
                             break;
-                        if (k)
-#pragma unroll
-                            for (int c = 0; c < Y::kV; ++c)
-                                tc::commit(empty + 8 * ((values + c) % Y::kSlots));
-                        if (k < most)
-#pragma unroll
-                            for (int c = 0; c < Y::kK; ++c)
-                                tc::commit(empty + 8 * ((keys + c) % Y::kSlots));
                         values = keys + Y::kK;
                         keys += Y::kK + Y::kV;
                     }

@@ -126,7 +126,16 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap *map, in
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(pol)
         : "memory");
 }
-// the same by one CTA of a pair: completion is counted on `bar`, a shared::cluster address (mapa) in either
+// boxes into L2
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap *map, int x, int y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void prefetch_3d(const CUtensorMap *map, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z) : "memory");
+}
+// load_2d by one CTA of a pair: completion is counted on `bar`, a shared::cluster address (mapa) in either
 __device__ __forceinline__ void load_2d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar, uint64_t pol)
 {
     asm volatile(
