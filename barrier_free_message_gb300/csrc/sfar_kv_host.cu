@@ -6,8 +6,6 @@
 #include <math.h>
 #include <string.h>
 
-#include <algorithm>
-#include <memory>
 #include <new>
 
 #include "sfar.h"
@@ -401,22 +399,7 @@ sfar_status sfar_kv_reset(sfar_kv_t *h, sfar_stream_t s)
 
 sfar_status sfar_test_kv_record_failure(sfar_kv_t *h)
 {
-    if (!h)
-        return SFAR_ERR_INVALID;
-    SfarCtl c;
-    const size_t n = arrived_bytes(h->sms) / sizeof(int);
-    std::unique_ptr<int[]> ones(new (std::nothrow) int[n]);
-    if (!ones)
-        return SFAR_ERR_OOM;
-    std::fill_n(ones.get(), n, 1);
-    if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpy(&c, h->ctl, sizeof c, cudaMemcpyDeviceToHost) != cudaSuccess)
-        return SFAR_ERR_CUDA;
-    c.status = SFAR_ERR_TIMEOUT;
-    c.f_where = SFAR_WAIT_COPY;
-    if (cudaMemcpy(h->ctl, &c, sizeof c, cudaMemcpyHostToDevice) != cudaSuccess ||
-        cudaMemcpy(h->arrived, ones.get(), n * sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
-        return SFAR_ERR_CUDA;
-    return SFAR_OK;
+    return h ? record_failure(h->ctl, h->arrived, arrived_bytes(h->sms) / sizeof(int)) : SFAR_ERR_INVALID;
 }
 
 // ---------------------------------------------------------- 8-bit projection

@@ -558,4 +558,9 @@ sfar_status sfar_latent_reset(sfar_latent_t *h, sfar_stream_t s)
     return SFAR_OK;
 }
 
+sfar_status sfar_test_latent_record_failure(sfar_latent_t *h)
+{
+    return h ? record_failure(h->ctl, h->arrived, counter_bytes(h->sms) / sizeof(int)) : SFAR_ERR_INVALID;
+}
+
 }  // extern "C"

@@ -5,6 +5,10 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <algorithm>
+#include <memory>
+#include <new>
+
 #include "sfar.h"
 #include "sfar_internal.h"
 
@@ -83,6 +87,24 @@ static inline sfar_status read_ctl(const SfarCtl *ctl, SfarCtl *host, cudaStream
         info->where = code ? host->f_where : 0;
     }
     return code;
+}
+
+// Puts a timeout into a handle's status and 1 into its n counters, as a call that gave up may leave them.
+static inline sfar_status record_failure(SfarCtl *ctl, int *counters, size_t n)
+{
+    SfarCtl c;
+    std::unique_ptr<int[]> ones(new (std::nothrow) int[n]);
+    if (!ones)
+        return SFAR_ERR_OOM;
+    std::fill_n(ones.get(), n, 1);
+    if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpy(&c, ctl, sizeof c, cudaMemcpyDeviceToHost) != cudaSuccess)
+        return SFAR_ERR_CUDA;
+    c.status = SFAR_ERR_TIMEOUT;
+    c.f_where = SFAR_WAIT_COPY;
+    if (cudaMemcpy(ctl, &c, sizeof c, cudaMemcpyHostToDevice) != cudaSuccess ||
+        cudaMemcpy(counters, ones.get(), n * sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
+        return SFAR_ERR_CUDA;
+    return SFAR_OK;
 }
 
 // The plan of a step over a pool of pages, for any handle that has one (sfar_kv_host.cu).

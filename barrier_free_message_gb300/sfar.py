@@ -117,6 +117,7 @@ _SIGS = [
     ("sfar_latent_status_get", ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(SfarFault)]),
     ("sfar_latent_reset", ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     ("sfar_test_kv_record_failure", ctypes.c_int, [ctypes.c_void_p]),
+    ("sfar_test_latent_record_failure", ctypes.c_int, [ctypes.c_void_p]),
     ("sfar_probe_empty", ctypes.c_int, [ctypes.c_void_p]),
     ("sfar_probe_pingpong", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                            ctypes.c_void_p, ctypes.c_void_p]),

@@ -14,6 +14,7 @@
 
 #include "sfar.h"
 #include "sfar_kv.h"
+#include "sfar_latent.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -138,6 +139,8 @@ sfar_status sfar_test_noalloc_record_failure(int rank, int peer, int where);
  * out may leave it: SFAR_ERR_TIMEOUT at SFAR_WAIT_COPY in its status, and the
  * counters of row tiles' parts not at 0.  Synchronous. */
 sfar_status sfar_test_kv_record_failure(sfar_kv_t *kv);
+/* The same for a latent cache's handle, and the counter of its prompts' row tiles not at 0. */
+sfar_status sfar_test_latent_record_failure(sfar_latent_t *h);
 
 /*
  * Latency floor probes.
