@@ -19,14 +19,15 @@
 //
 // Work: row tiles are taken from a counter, one (rank, head)'s row tiles
 // after another, the longest first: they share keys and values in L2.
-// Warps 0-3, 4-7: the tiles' softmax; 8: copies and pieces; 9: the MMAs.
+// Warps 0-7, 8-15: the tiles' softmax; then copies and pieces, the MMAs, and two
+// that look at values beyond the rows' sight.
 #include "sfar_attn.cuh"
 #include "sfar_latent_args.h"
 
 namespace {
 
 constexpr int kTile = 128, kGroup = SFAR_LATENT_GROUP, kBox = kTile * 128;     // bytes of 64 elements of 128 tokens
-constexpr int kPieces = 4, kAhead = 0;              // kAhead: steps between a tile's way to L2 and its copy
+constexpr int kPieces = 4, kLeast = 4, kKept = 64;
 constexpr int kRegsSoft = 104, kRegsRest = 64;     // with two tiles, 16 warps and 4: together the launch's 20 x 96
 
 template <int D, int TILES> struct Lay {
@@ -41,7 +42,10 @@ template <int D, int TILES> struct Lay {
 struct Piece {
     int r, h, b, rt;            // rank, head, request, row tile; b < 0: the end
     int len, count, first, kfirst;      // context, new tokens, rows of the first new and of the first context token
-    int steps[2];               // tiles of the context that each tile of rows attends to
+    int steps[2];               // of this piece, the tiles of the context that each tile of rows attends to
+    int from;                   // the first tile of the piece
+    int part, c0, c1;           // this part of the row tile, its first and its last
+    int odd;                    // the first context token that is not finite, of those that were looked at
 };
 
 // The two warps that share 32 rows.
@@ -55,6 +59,12 @@ __device__ __forceinline__ bool pair_any(int pair, bool v)
                  : "memory");
     return r != 0;
 }
+__device__ __forceinline__ uint32_t times0(uint32_t w, uint32_t sum)
+{
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(0u), "r"(sum));
+    return r;
+}
 __device__ __forceinline__ bool odd2(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
@@ -63,16 +73,125 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 
+struct Request {
+    int len, count, first, kfirst;
+};
 // Request b's rows, none if its offsets are out of order or beyond the tensors.
-__device__ __forceinline__ bool request(const SfarLatentPromptArgs &a, int b, int &len, int &count, int &first, int &kfirst)
+__device__ __forceinline__ bool request(const SfarLatentPromptArgs &a, int b, Request &q)
 {
-    first = a.starts[b];
-    kfirst = a.kstarts[b];
+    q.first = a.starts[b];
+    q.kfirst = a.kstarts[b];
     const int e = a.starts[b + 1], ke = a.kstarts[b + 1];
-    const bool ok = first >= 0 && e >= first && e <= a.T && kfirst >= 0 && ke >= kfirst && ke <= a.S;
-    count = ok ? e - first : 0;
-    len = ok ? ke - kfirst : 0;
+    const bool ok = q.first >= 0 && e >= q.first && e <= a.T && q.kfirst >= 0 && ke >= q.kfirst && ke <= a.S;
+    q.count = ok ? e - q.first : 0;
+    q.len = ok ? ke - q.kfirst : 0;
     return ok;
+}
+
+// Every row of the piece sees the tokens before all_see; its first whole_steps steps have no others.
+__device__ __forceinline__ int all_see(const Piece &p, int rows) { return min(p.len, p.len - p.count + p.rt * rows + 1); }
+__device__ __forceinline__ int whole_steps(const Piece &p, int rows) { return max(0, max(0, all_see(p, rows)) / kTile - p.from); }
+
+template <int D> __device__ __noinline__ void padding(const SfarLatentPromptArgs &a, int lane)
+{
+    if (a.starts[a.B] < a.T)
+        sfar_attn_padding<D>(a, lane, 32);
+}
+
+// All softmax threads, after their parts: joins the row tile's parts if this CTA is the last of them.  A warp takes a row;
+// lane i keeps what part i is multiplied by.
+template <int D, int TILES> __device__ __noinline__ void join(const SfarLatentPromptArgs &a, const Piece &p, int warp, int *s_last)
+{
+    constexpr int kRows = 128 * TILES, kWarps = 8 * TILES, kPart = kRows * (D + 2), kVec = D / 32, kBatch = 3, kY = 4;
+    const int lane = threadIdx.x & 31, rows = min(kRows, p.count - p.rt * kRows);
+    SfarJoin j(a, 0, p.c0, p.c1, p.part);
+    for (;;) {
+        asm volatile("bar.sync 9, %0;" ::"n"(32 * kWarps) : "memory");
+        if (threadIdx.x == 0)
+            *s_last = j.last();
+        asm volatile("bar.sync 9, %0;" ::"n"(32 * kWarps) : "memory");
+        if (!*s_last)
+            return;
+        const int parts = (j.hi - j.lo) / j.step + 1;
+        const bool more = j.up != 0;
+        auto slot = [&](int c) { return a.part + (size_t)(j.lo + c * j.step) * kPart; };
+        // four rows at a time: time passes by round trips
+        for (int n0 = warp; n0 < rows; n0 += kY * kWarps) {
+            float2 m[kY];
+            int n[kY];                             // rows past the last: the last again
+#pragma unroll
+            for (int y = 0; y < kY; ++y) {
+                n[y] = min(n0 + y * kWarps, rows - 1);
+                m[y] = make_float2(-INFINITY, 0.f);
+                if (lane < parts)
+                    m[y] = __ldcg(reinterpret_cast<const float2 *>(slot(lane) + kRows * D) + n[y]);
+            }
+            float w[kY], top[kY], total[kY], o[kY][kVec];
+#pragma unroll
+            for (int y = 0; y < kY; ++y) {
+                top[y] = m[y].x;
+#pragma unroll
+                for (int d = 16; d; d >>= 1)
+                    top[y] = fmaxf(top[y], __shfl_xor_sync(SFAR_FULL, top[y], d));
+                w[y] = m[y].x == -INFINITY ? 0.f : ex2(m[y].x - top[y]);
+                total[y] = m[y].x == -INFINITY ? m[y].y : w[y] * m[y].y;           // its sum is 0 then, or NaN
+#pragma unroll
+                for (int d = 16; d; d >>= 1)
+                    total[y] += __shfl_xor_sync(SFAR_FULL, total[y], d);
+#pragma unroll
+                for (int e = 0; e < kVec; ++e)
+                    o[y][e] = 0.f;
+            }
+#pragma unroll 1
+            for (int c0 = 0; c0 < parts; c0 += kBatch) {
+                float v[kBatch][kY][kVec];
+#pragma unroll
+                for (int c = 0; c < kBatch; ++c)
+#pragma unroll
+                    for (int y = 0; y < kY; ++y) {
+                        const float *src = slot(min(c0 + c, parts - 1)) + n[y] * D + lane * kVec;
+                        if constexpr (kVec == 4) {
+                            const float4 u = __ldcg(reinterpret_cast<const float4 *>(src));
+                            v[c][y][0] = u.x, v[c][y][1] = u.y, v[c][y][2] = u.z, v[c][y][3] = u.w;
+                        } else {
+                            const float2 u = __ldcg(reinterpret_cast<const float2 *>(src));
+                            v[c][y][0] = u.x, v[c][y][1] = u.y;
+                        }
+                    }
+#pragma unroll
+                for (int c = 0; c < kBatch; ++c)
+#pragma unroll
+                    for (int y = 0; y < kY; ++y) {
+                        const float f = __shfl_sync(SFAR_FULL, w[y], (c0 + c) & 31);
+                        if (c0 + c < parts)
+#pragma unroll
+                            for (int e = 0; e < kVec; ++e)
+                                o[y][e] += f * v[c][y][e];
+                    }
+            }
+#pragma unroll
+            for (int y = 0; y < kY; ++y) {
+                if (n0 + y * kWarps >= rows)
+                    break;
+                if (more) {
+                    float *to = slot(0) + n[y] * D + lane * kVec;
+#pragma unroll
+                    for (int e = 0; e < kVec; e += 2)
+                        __stcg(reinterpret_cast<float2 *>(to + e), make_float2(o[y][e], o[y][e + 1]));
+                    if (lane == 0)
+                        __stcg(reinterpret_cast<float2 *>(slot(0) + kRows * D) + n[y], make_float2(top[y], total[y]));
+                } else {
+                    const float by = total[y] == 0.f ? 0.f : 1.f / total[y];
+                    uint16_t *dst = a.out[p.r] + (long long)(p.first + p.rt * kRows + n[y]) * a.ots + (long long)p.h * a.ohs + lane * kVec;
+#pragma unroll
+                    for (int e = 0; e < kVec; e += 2)
+                        *reinterpret_cast<uint32_t *>(dst + e) = tc::bf16x2(o[y][e] * by, o[y][e + 1] * by);
+                }
+            }
+        }
+        if (!j.next(a, 0))
+            return;
+    }
 }
 
 }  // namespace
@@ -81,18 +200,19 @@ template <int D, int TILES>
 __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(const __grid_constant__ SfarLatentPromptArgs a)
 {
     using Y = Lay<D, TILES>;
-    constexpr int kRows = 128 * TILES, kThreads = Y::kThreads, kSoftWarps = Y::kSoftWarps, kCopyWarp = Y::kCopyWarp, kMmaWarp = Y::kMmaWarp;
+    constexpr int kRows = 128 * TILES, kPart = kRows * (D + 2), kThreads = Y::kThreads, kSoftWarps = Y::kSoftWarps, kCopyWarp = Y::kCopyWarp, kMmaWarp = Y::kMmaWarp;
     extern __shared__ __align__(1024) unsigned char dyn[];
-    __shared__ __align__(8) unsigned long long bars[2 * Y::kSlots + 2 * kPieces + 11];
+    __shared__ __align__(8) unsigned long long bars[2 * Y::kSlots + 2 * kPieces + 13];
     __shared__ Piece s_piece[kPieces];
-    __shared__ uint32_t upto[SFAR_KV_MAX_REQUESTS / kGroup + 1];
+    __shared__ __align__(16) uint32_t upto[SFAR_KV_MAX_REQUESTS / kGroup + 4];
+    Request *const kept = reinterpret_cast<Request *>(upto + 4);    // of up to kKept requests (two sums), read once
     __shared__ uint32_t s_warp[kThreads / 32], s_tmem;
-    __shared__ int s_odd[4];                       // by the piece: the first context token that is not finite, of those that were checked
+    __shared__ int s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t mem = (tc::smem(dyn) + 1023u) & ~1023u, ring = mem + Y::kQ;
     unsigned char *gen = dyn + (mem - tc::smem(dyn));
     const uint32_t full = tc::smem(bars), empty = full + 8 * Y::kSlots, pfull = empty + 8 * Y::kSlots, pempty = pfull + 8 * kPieces,
-                   qfull = pempty + 8 * kPieces, qempty = qfull + 16, sbar = qempty + 16, wbar = sbar + 16, obar = wbar + 16, drain = obar + 16;
+                   qfull = pempty + 8 * kPieces, qempty = qfull + 16, sbar = qempty + 16, wbar = sbar + 16, obar = wbar + 16, look = obar + 16, clean = look + 8, drain = clean + 8;
 
     if (warp == kCopyWarp && lane < a.R) {
         tc::prefetch_map(&a.qmap[lane]);
@@ -102,13 +222,11 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
     }
     if (tid == 0) {
         for (uint32_t b = full; b <= drain; b += 8)
-            tc::bar_init(b, b >= pempty && b < qfull ? kSoftWarps + 1 : b >= wbar && b < obar ? 8 : 1);
+            tc::bar_init(b, b >= pempty && b < qfull ? kSoftWarps + 1 + Y::kV : b >= wbar && b < obar ? 8 : b == clean ? Y::kV : 1);
         tc::bar_fence_init();
         tc::fence_async();
         upto[0] = 0;
     }
-    if (tid < 4)
-        s_odd[tid] = INT_MAX;
     if (warp == kMmaWarp)
         tc::tmem_alloc<1>(tc::smem(&s_tmem), 256 * TILES);
     pdl_wait();
@@ -120,10 +238,12 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
         const int b = b0 + tid;
         uint32_t v = 0;
         if (b < a.B) {
-            int len, count, first, kfirst;
-            if (!request(a, b, len, count, first, kfirst) && blockIdx.x == 0)
+            Request q;
+            if (!request(a, b, q) && blockIdx.x == 0)
                 sfar_kv_fault(a.ctl, b, SFAR_KV_BAD_TOKENS);
-            v = min((uint32_t)(count + kRows - 1) / kRows, 1u << 26);     // offsets in no order: 32 such sums fit 32 bits
+            if (a.B <= kKept)
+                kept[b] = q;
+            v = min((uint32_t)(q.count + kRows - 1) / kRows, 1u << 26);     // offsets in no order: 32 such sums fit 32 bits
         }
         v = __reduce_add_sync(SFAR_FULL, v);
         if (lane == 0)
@@ -147,7 +267,10 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
     const bool many = carry > (uint32_t)a.most;    // more than the step has: offsets in no order, nothing is computed
     if (many && blockIdx.x == 0 && tid == 0)
         sfar_kv_fault(a.ctl, a.B, SFAR_KV_BAD_TOKENS);
-    const uint32_t items = many ? 0 : carry * (uint32_t)(a.R * a.Hq);
+    // Fewer row tiles than CTAs are cut along the context, into at most two parts for each CTA and of no less than kLeast
+    // tiles; the last of a row tile's parts to finish joins them, in their order.
+    const uint32_t whole = many ? 0 : carry * (uint32_t)(a.R * a.Hq);
+    const uint32_t cuts = whole && whole < gridDim.x ? 2 * gridDim.x / whole : 1, items = whole * cuts;
 
     if (warp < kSoftWarps) {
         // -------------------------------------------------------------- softmax
@@ -173,8 +296,8 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
         const float f = fmaxf(a.scale * 1.4426950408889634f, 1e-37f);
         const uint64_t f2 = tc::pack2(f, f);
         tc::Ring<kPieces> ps;
-        uint32_t sphase = 0, ophase = 0, slot = 0;         // slot: boxes that came before this step's keys
-        for (int piece = 0;; ++piece) {
+        uint32_t sphase = 0, ophase = 0;
+        for (;;) {
             dead = dead || !tc::bar_wait(pfull + 8 * ps.slot, ps.phase, limit);
             dead = pair_any(pair, dead);
             if (dead)
@@ -182,17 +305,14 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
             const Piece &p = s_piece[ps.slot];
             if (p.b < 0)
                 break;
-            if (tid == 0)
-                s_odd[(piece + 2) & 3] = INT_MAX;
-            const int i = p.rt * kRows + x * 128 + lrow, pos = p.len - p.count + i, len = p.len;
-            const int all_to = min(len, len - p.count + p.rt * kRows + 1);         // every row of both tiles sees the tokens before it
+            const int i = p.rt * kRows + x * 128 + lrow, pos = p.len - p.count + i;
             const bool row = i < p.count;
             const int hi = (row ? pos + 1 : INT_MAX) - 64 * half;                   // of this thread's columns
-            const int mine_to = len - p.count + p.rt * kRows + x * 128 + (warp & 3) * 32 + 1 - 64 * half;   // every row of this warp
+            const int mine_to = p.len - p.count + p.rt * kRows + x * 128 + (warp & 3) * 32 + 1 - 64 * half;   // every row of this warp
             float ref = -INFINITY, sum = 0.f;      // of the row; of this half
-            const int steps = p.steps[x], before = p.steps[0];
+            const int steps = p.steps[x];
             for (int k = 0; k < steps; ++k) {
-                const int j0 = k * kTile;
+                const int j0 = (p.from + k) * kTile;
                 dead = dead || !tc::bar_wait(sbar + 8 * x, sphase, limit);
                 sphase ^= 1u;
                 tc::fence_after();
@@ -201,29 +321,6 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                 tc::ld32(s[1], tS + 32);
                 tc::wait_ld(s[0]);
                 tc::wait_ld(s[1]);
-                if (j0 + kTile > all_to && (x == 0 || k >= before) && half < Y::kV) {
-                    // Values of tokens that not every row sees, a token's 64 to a thread: with an infinity or NaN they become
-                    // zeros (0 times it would reach the rows that do not see it); the rows that see them become NaN at the end.
-                    const int j = j0 + lrow;
-                    const uint32_t at = slot + k * (Y::kK + Y::kV) + Y::kK + half;
-                    dead = dead || !tc::bar_wait(full + 8 * (at % Y::kSlots), at / Y::kSlots & 1u, limit);
-                    if (j >= all_to) {
-                        unsigned char *v = gen + Y::kQ + at % Y::kSlots * kBox + lrow * 128;
-                        bool odd = false;
-#pragma unroll 4
-                        for (int e = 0; e < 8; ++e) {
-                            const uint4 w = *reinterpret_cast<const uint4 *>(v + ((e ^ (lrow & 7)) << 4));
-                            odd = odd || odd2(w.x) || odd2(w.y) || odd2(w.z) || odd2(w.w);
-                        }
-                        if (odd) {
-                            if (j < len)
-                                atomicMin(&s_odd[piece & 3], j);
-                            for (int e = 0; e < 8; ++e)
-                                *reinterpret_cast<uint4 *>(v + (e << 4)) = make_uint4(0, 0, 0, 0);
-                        }
-                    }
-                    tc::fence_async();
-                }
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
                     if (j0 + 32 * c + 32 > mine_to) {
@@ -290,16 +387,18 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                 if (lane == 0)
                     tc::bar_arrive(wbar + 8 * x);
             }
-            slot = (slot + max(before, p.steps[1]) * (Y::kK + Y::kV)) % (2 * Y::kSlots);       // its parity counts, too
             if (steps) {
                 dead = dead || !tc::bar_wait(obar + 8 * x, ophase, limit);
                 ophase ^= 1u;
                 tc::fence_after();
             }
-            const bool nan = row && *(volatile int *)&s_odd[piece & 3] < hi + 64 * half;
-            const float by = nan ? NAN : sum == 0.f ? 0.f : 1.f / sum;
+            if (row && *(volatile const int *)&p.odd < hi + 64 * half)
+                sum = NAN;
+            const bool parts = p.c0 != p.c1;
+            const float by = parts ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
             uint16_t *dst = a.out[p.r] + (long long)(p.first + min(i, p.count - 1)) * a.ots + (long long)p.h * a.ohs + D / 2 * half;
-#pragma unroll
+            float *part = a.part + (size_t)p.part * kPart + (x * 128 + lrow) * D + D / 2 * half;
+#pragma unroll 1
             for (int c = 0; c < D / 2; c += 16) {
                 uint32_t o[16];
 #pragma unroll
@@ -309,12 +408,24 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                     tc::ld16(o, tO + c);
                     tc::wait_ld(o);
                 }
+                if (parts) {
+                    if (row)
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            __stcg(reinterpret_cast<uint4 *>(part + c + e), make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+                    continue;
+                }
                 uint32_t y[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     y[e] = tc::bf16x2(__uint_as_float(o[2 * e]) * by, __uint_as_float(o[2 * e + 1]) * by);
                 if (row)
                     tc::st32(dst + c, y);
+            }
+            if (parts) {
+                if (row && half == 0)
+                    __stcg(reinterpret_cast<float2 *>(a.part + (size_t)p.part * kPart + kRows * D) + x * 128 + lrow, make_float2(ref, sum));
+                join<D, TILES>(a, p, warp, &s_last);
             }
             tc::fence_before();
             __syncwarp();
@@ -324,7 +435,6 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
         }
         if (dead && lane == 0)
             sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
-        sfar_attn_padding<D>(a, tid, 32 * kSoftWarps);
     } else {
         if constexpr (TILES == 2)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
@@ -342,9 +452,13 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
             auto piece = [&](uint32_t taken) {
                 Piece p;
                 p.b = -1;
+                p.odd = INT_MAX;
                 p.steps[0] = p.steps[1] = 0;
                 if (taken >= items)
                     return p;
+                const int part = (int)(taken % cuts);
+                p.part = (int)taken;
+                taken /= cuts;
                 int lo = 0, hi = groups;
                 while (hi - lo > 1) {
                     const int mid = (lo + hi) >> 1;
@@ -355,10 +469,14 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                 }
                 uint32_t v = taken - upto[lo] * planes;
                 const int b = lo * kGroup + lane;
-                int len = 0, count = 0, first = 0, kfirst = 0;
-                if (b < a.B)
-                    request(a, b, len, count, first, kfirst);
-                const uint32_t n = (uint32_t)(count + kRows - 1) / kRows;
+                Request q{0, 0, 0, 0};
+                if (b < a.B) {
+                    if (a.B <= kKept)
+                        q = kept[b];
+                    else
+                        request(a, b, q);
+                }
+                const uint32_t n = (uint32_t)(q.count + kRows - 1) / kRows;
                 uint32_t sum = n;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
@@ -369,10 +487,10 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                 const unsigned past = __ballot_sync(SFAR_FULL, sum * planes > v);
                 const int l = past ? __ffs(past) - 1 : 0;
                 p.b = lo * kGroup + l;
-                p.len = __shfl_sync(SFAR_FULL, len, l);
-                p.count = __shfl_sync(SFAR_FULL, count, l);
-                p.first = __shfl_sync(SFAR_FULL, first, l);
-                p.kfirst = __shfl_sync(SFAR_FULL, kfirst, l);
+                p.len = __shfl_sync(SFAR_FULL, q.len, l);
+                p.count = __shfl_sync(SFAR_FULL, q.count, l);
+                p.first = __shfl_sync(SFAR_FULL, q.first, l);
+                p.kfirst = __shfl_sync(SFAR_FULL, q.kfirst, l);
                 const uint32_t tiles = max(1u, __shfl_sync(SFAR_FULL, n, l));
                 v -= __shfl_sync(SFAR_FULL, sum - n, l) * planes;
                 const uint32_t plane = v / tiles;
@@ -385,91 +503,94 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                     if (from < p.count)
                         p.steps[x] = (max(0, p.len - p.count + last + 1) + kTile - 1) / kTile;
                 }
+                // this part of the row tile's: p.c1 < p.c0 if it is none
+                const int all = max(p.steps[0], p.steps[1]), parts = min((int)cuts, max(1, (all + kLeast - 1) / kLeast));
+                p.c0 = p.part - part;
+                p.c1 = part < parts ? p.c0 + parts - 1 : -1;
+                const int each = all / parts, rest = all - each * parts;            // the first `rest` have one more
+                p.from = each * part + min(part, rest);
+                const int to = p.from + each + (part < rest);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    p.steps[x] = max(0, min(p.steps[x], to) - p.from);
                 return p;
             };
-            // Keys and values of step k on their way to L2, by one lane: a ring of a step and a half hides L2's latency, not HBM's.
-            auto ahead = [&](const Piece &p, int k) {
-                const int y = p.kfirst + k * kTile;
-#pragma unroll
-                for (int c = 0; c < Y::kV; ++c) {
-                    tc::prefetch_3d(&a.kmap[p.r], 64 * c, p.h, y);
-                    tc::prefetch_3d(&a.vmap[p.r], 64 * c, p.h, y);
-                }
-                tc::prefetch_2d(&a.krmap[p.r], 0, y);
-            };
-            Piece p = piece(blockIdx.x);
-            for (;;) {
-                // The next one is asked for early: one question for each row tile, so the counter is back at 0 when all are taken.
+            uint32_t taken = blockIdx.x;
+            Piece p = piece(taken), next;
+#pragma unroll 1
+            while (!dead) {
+                const bool end = p.b < 0;
+                // The next one is asked for early: one question for each row tile's part, so the counter is back at 0 when all
+                // are taken.
                 uint32_t after = 0;
-                if (p.b >= 0 && lane == 0)
+                if (!end && lane == 0)
                     asm volatile("atom.relaxed.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(after) : "l"(a.next), "r"(items - 1) : "memory");
-                if (!wait(pempty + 8 * ps.slot, ps.phase ^ 1u)) {
-                    dead = true;
-                    break;
-                }
-                if (lane == 0) {
-                    s_piece[ps.slot] = p;
-                    tc::bar_arrive(pfull + 8 * ps.slot);
-                }
-                ps.next();
-                if (p.b < 0)
-                    break;
-                Piece next;
-                const int steps = max(p.steps[0], p.steps[1]);
-                if (steps == 0)
+                if (!end && (p.c1 < 0 || max(p.steps[0], p.steps[1]) == 0))
                     next = piece(gridDim.x + __shfl_sync(SFAR_FULL, after, 0));
-                for (int k = 0; k < steps && !dead; ++k) {
-                    for (int c = 0; c < Y::kK + Y::kV; ++c) {
-                        if (!wait(empty + 8 * st.slot, st.phase ^ 1u)) {
-                            dead = true;
-                            break;
-                        }
-                        if (lane == 0) {
-                            const uint32_t bar = full + 8 * st.slot, dst = ring + st.slot * kBox;
-                            const int y = p.kfirst + k * kTile;
-                            tc::bar_expect(bar, kBox);
-                            if (c < Y::kV)
-                                tc::load_3d(dst, &a.kmap[p.r], 64 * c, p.h, y, bar, often);
-                            else if (c == Y::kV)
-                                tc::load_2d(dst, &a.krmap[p.r], 0, y, bar, often);
-                            else
-                                tc::load_3d(dst, &a.vmap[p.r], 64 * (c - Y::kK), p.h, y, bar, often);
-                        }
-                        ++boxes;
-                        st.next();
-                        if (k == 0 && c == Y::kV) {
-                            // the queries, once the last piece's scores are done with theirs
-                            for (int x = 0; x < TILES && !dead; ++x)
-                                if (p.steps[x]) {
-                                    if (!wait(qempty + 8 * x, qphase[x])) {
-                                        dead = true;
-                                        break;
-                                    }
-                                    qphase[x] ^= 1u;
-                                    ++queries[x];
-                                    if (lane == 0) {
-                                        tc::bar_expect(qfull + 8 * x, Y::kK * kBox);
-                                        for (int i = 0; i < Y::kK; ++i)
-                                            tc::load_3d(mem + (x * Y::kK + i) * kBox, &a.qmap[p.r], 64 * i, p.h, p.first + p.rt * kRows + x * 128,
-                                                        qfull + 8 * x, once);
-                                    }
-                                }
-                            if (dead)
+                if (end || p.c1 >= 0) {
+                    if (!wait(pempty + 8 * ps.slot, ps.phase ^ 1u)) {
+                        dead = true;
+                        break;
+                    }
+                    if (lane == 0) {
+                        s_piece[ps.slot] = p;
+                        tc::bar_arrive(pfull + 8 * ps.slot);
+                    }
+                    ps.next();
+                    if (end)
+                        break;
+                    const int steps = max(p.steps[0], p.steps[1]);
+#pragma unroll 1
+                    for (int k = 0; k < steps && !dead; ++k) {
+#pragma unroll
+                        for (int c = 0; c < Y::kK + Y::kV; ++c) {
+                            if (!wait(empty + 8 * st.slot, st.phase ^ 1u)) {
+                                dead = true;
                                 break;
+                            }
+                            if (lane == 0) {
+                                const uint32_t bar = full + 8 * st.slot, dst = ring + st.slot * kBox;
+                                const int y = p.kfirst + (p.from + k) * kTile;
+                                tc::bar_expect(bar, kBox);
+                                if (c == Y::kV)
+                                    tc::load_2d(dst, &a.krmap[p.r], 0, y, bar, often);
+                                else
+                                    tc::load_3d(dst, c < Y::kV ? &a.kmap[p.r] : &a.vmap[p.r], c < Y::kV ? 64 * c : 64 * (c - Y::kK), p.h, y, bar, often);
+                            }
+                            ++boxes;
+                            st.next();
+                            if (k == 0 && c == Y::kV) {
+                                // the queries, once the last piece's scores are done with theirs
+#pragma unroll 1
+                                for (int x = 0; x < TILES; ++x)
+                                    if (p.steps[x]) {
+                                        if (!wait(qempty + 8 * x, x ? qphase[1] : qphase[0])) {
+                                            dead = true;
+                                            break;
+                                        }
+                                        (x ? qphase[1] : qphase[0]) ^= 1u;
+                                        ++(x ? queries[1] : queries[0]);
+                                        if (lane == 0)
+                                            tc::bar_expect(qfull + 8 * x, Y::kK * kBox);
+                                        __syncwarp();
+                                        if (lane < Y::kK)
+                                            tc::load_3d(mem + (x * Y::kK + lane) * kBox, &a.qmap[p.r], 64 * lane, p.h,
+                                                        p.first + p.rt * kRows + x * 128, qfull + 8 * x, once);
+                                    }
+                                if (dead)
+                                    break;
+                            }
+                        }
+                        if (k == max(0, steps - 2)) {
+                            next = piece(gridDim.x + __shfl_sync(SFAR_FULL, after, 0));
+                            // its queries on their way to L2
+                            if (lane < TILES * Y::kK && next.steps[lane / Y::kK])
+                                tc::prefetch_3d(&a.qmap[next.r], 64 * (lane % Y::kK), next.h, next.first + next.rt * kRows + lane / Y::kK * 128);
                         }
                     }
-                    if (k == 0)
-                        next = piece(gridDim.x + __shfl_sync(SFAR_FULL, after, 0));
-                    const int far = k + kAhead, more = max(next.steps[0], next.steps[1]);
-                    if (kAhead && lane == 0 && far < steps)
-                        ahead(p, far);
-                    else if (kAhead && lane == 0 && far - steps < more)
-                        ahead(next, far - steps);
-                    if (k == max(0, steps - 2) && lane < TILES * Y::kK && next.steps[lane / Y::kK])
-                        tc::prefetch_3d(&a.qmap[next.r], 64 * (lane % Y::kK), next.h, next.first + next.rt * kRows + lane / Y::kK * 128);
+                    if (dead)
+                        break;
                 }
-                if (dead)
-                    break;
                 p = next;
             }
             if (dead && lane == 0) {
@@ -486,13 +607,13 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
             constexpr uint32_t idS = tc::idesc_bf16(128, 128), idO = tc::idesc_bf16(128, D) | tc::kTransposeB;
             const uint64_t dq = tc::desc_k128(mem), dk = tc::desc_k128(ring);
             tc::Ring<kPieces> ps;
-            uint32_t qphase[2] = {0, 0}, wphase[2] = {0, 0}, slot = 0;     // slot: boxes before this step's keys, modulo 2 kSlots
+            uint32_t qphase[2] = {0, 0}, wphase[2] = {0, 0}, cphase = 0, slot = 0;     // slot: boxes before this step's keys, modulo 2 kSlots
             bool dead = false;
             for (;;) {
                 dead = __any_sync(SFAR_FULL, dead || !tc::bar_wait(pfull + 8 * ps.slot, ps.phase, limit));
                 if (dead)
                     break;
-                const int n[2] = {s_piece[ps.slot].steps[0], s_piece[ps.slot].steps[1]}, b = s_piece[ps.slot].b;
+                const int n[2] = {s_piece[ps.slot].steps[0], s_piece[ps.slot].steps[1]}, b = s_piece[ps.slot].b, whole = whole_steps(s_piece[ps.slot], kRows);
                 __syncwarp();
                 if (lane == 0)
                     tc::bar_arrive(pempty + 8 * ps.slot);
@@ -508,6 +629,7 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                         return in;
                     };
                     uint32_t keys = slot, values = 0;              // boxes before step k's keys, before the values of the one before
+#pragma unroll 1
                     for (int k = 0; k <= most && !dead; ++k) {
 #pragma unroll
                         for (int x = 0; x < TILES; ++x) {
@@ -515,10 +637,13 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                             if (k && k <= n[x]) {
                                 // O += P V of the step before
                                 dead = dead || !wait(wbar + 8 * x, wphase[x]);
-                                if (x == 0 || k > n[0])
-#pragma unroll
+                                if (x == 0 || k > n[0]) {
+#pragma unroll 1
                                     for (int c = 0; c < Y::kV; ++c)
                                         dead = dead || !there(values + c);
+                                    if (k > whole)
+                                        dead = dead || !wait(clean, cphase);
+                                }
                                 if (dead)
                                     break;
                                 tc::fence_after();
@@ -556,10 +681,15 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                                     if (dead)
                                         break;
                                     tc::fence_after();
+                                    // these keys are here, so what the values' place held before them was: it may be looked at when they are
+                                    if (c == Y::kV && k >= whole && (x == 0 || k >= n[0]))
+                                        tc::bar_arrive(look);
                                     const uint64_t d = dk + (keys + c) % Y::kSlots * (kBox >> 4), q = dq + (x * Y::kK + c) * (kBox >> 4);
                                     const int parts = c < Y::kV ? 4 : a.rope / 16;
-                                    for (int i = 0; i < parts; ++i)
-                                        tc::mma_f16_ss(tS, q + 2 * i, d + 2 * i, idS, c + i > 0);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        if (i < parts)
+                                            tc::mma_f16_ss(tS, q + 2 * i, d + 2 * i, idS, c + i > 0);
                                     if (x == last)
                                         tc::commit(empty + 8 * ((keys + c) % Y::kSlots));
                                 }
@@ -586,6 +716,64 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                 tc::commit(drain);
                 tc::bar_wait(drain, 0, limit);
             }
+        } else {
+            // -------------------------------------------------------- values
+            // Values of tokens that not every row of the piece sees: 64 with an infinity or NaN among them become zeros (0 times
+            // it would reach the rows that do not see it), and the rows that do see the token become NaN at the end.  A warp to
+            // each box of a step; it has the time that the softmax takes.
+            const int c = warp - kMmaWarp - 1;
+            tc::Ring<kPieces> ps;
+            uint32_t slot = 0, phase = 0;
+            bool dead = false;
+            while (c < Y::kV) {
+                dead = !__all_sync(SFAR_FULL, tc::bar_wait(pfull + 8 * ps.slot, ps.phase, limit));
+                if (dead || s_piece[ps.slot].b < 0)
+                    break;
+                Piece &p = s_piece[ps.slot];
+                const int most = max(p.steps[0], p.steps[1]), all_to = all_see(p, kRows);
+                for (int k = whole_steps(p, kRows); k < most && !dead; ++k) {
+                    const uint32_t at = slot + k * (Y::kK + Y::kV) + Y::kK + c;
+                    dead = !__all_sync(SFAR_FULL, tc::bar_wait(look, phase, limit) && tc::bar_wait(full + 8 * (at % Y::kSlots), at / Y::kSlots & 1u, limit));
+                    phase ^= 1u;
+                    if (dead)
+                        break;
+                    unsigned char *v = gen + Y::kQ + at % Y::kSlots * kBox;
+                    // times 0, whatever is not finite gives a NaN
+#pragma unroll 2
+                    for (int row = lane; row < kTile; row += 32) {
+                        uint32_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const uint4 w = *reinterpret_cast<const uint4 *>(v + row * 128 + ((e ^ (row & 7)) << 4));
+                            sum[0] = times0(w.x, sum[0]);
+                            sum[1] = times0(w.y, sum[1]);
+                            sum[2] = times0(w.z, sum[2]);
+                            sum[3] = times0(w.w, sum[3]);
+                        }
+                        const int j = (p.from + k) * kTile + row;
+                        if (j >= all_to && odd2(sum[0] | sum[1] | sum[2] | sum[3])) {
+                            if (j < p.len)
+                                atomicMin(&p.odd, j);
+#pragma unroll 1
+                            for (int e = 0; e < 8; ++e)
+                                *reinterpret_cast<uint4 *>(v + row * 128 + (e << 4)) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    tc::fence_async();
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::bar_arrive(clean);
+                }
+                slot = (slot + (uint32_t)most * (Y::kK + Y::kV)) % (2 * Y::kSlots);        // its parity counts, too
+                __syncwarp();
+                if (lane == 0)
+                    tc::bar_arrive(pempty + 8 * ps.slot);
+                ps.next();
+            }
+            if (dead && lane == 0)
+                sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
+            if (c == Y::kV - 1)
+                padding<D>(a, lane);
         }
     }
     __syncwarp();

@@ -61,6 +61,9 @@ struct SfarLatentPromptArgs {
     uint16_t *out[SFAR_MAX_R];
     const int *starts, *kstarts;
     unsigned *next;                         // counter of row tiles taken; 0 between calls
+    float *part;                            // partial results, SFAR_PROMPT_PARTS for each SM
+    int *arrived;                           // [3][arrived_stride] counters of parts (SfarJoin); 0 between calls
+    int arrived_stride;
     SfarCtl *ctl;
     long long ots, ohs;
     float scale;
@@ -82,5 +85,6 @@ const void *sfar_kernel_latent_prompt(int head_dim, int tiles, int *threads, int
 #define SFAR_GATHER_WARPS 8
 #define SFAR_LATENT_TILE 64                // cached tokens of a step of the attention
 #define SFAR_LATENT_ROWS 64                 // query rows at a time, at most
+#define SFAR_PROMPT_PARTS 2                 // parts of row tiles that the expanded attention makes, for each SM
 #define SFAR_LATENT_GROUP 32                // requests to a prefix sum
 #define SFAR_GATHER_ROWS 4                  // rows of a warp

@@ -35,8 +35,10 @@ struct sfar_latent {
 
 namespace {
 
-// Counters: three sets of one for each CTA (of the parts of row tiles), and one of the prompt's row tiles.
-size_t counter_bytes(int sms) { return (3 * (size_t)sms + 1) * sizeof(int); }
+// Counters: three sets of one for each part of a row tile (the absorbed form has one to a CTA), and one of the prompt's row
+// tiles.
+size_t counter_stride(int sms) { return SFAR_PROMPT_PARTS * (size_t)sms; }
+size_t counter_bytes(int sms) { return (3 * counter_stride(sms) + 1) * sizeof(int); }
 
 // A tensor [tokens][heads][numbers] in memory, in bytes; strides of dimensions of one entry do not count.
 struct Rows {
@@ -243,7 +245,8 @@ sfar_latent_t *sfar_latent_create(int R, int q_heads, int latent_dim, int rope_d
         }
     }
     const size_t o_arrived = 256, o_part = (o_arrived + counter_bytes(sms) + 255) / 256 * 256;
-    const size_t ws = o_part + 2 * (size_t)sms * SFAR_LATENT_ROWS * ((size_t)latent_dim + 2) * 4;
+    const size_t absorbed = 2 * SFAR_LATENT_ROWS * ((size_t)latent_dim + 2), expanded = SFAR_PROMPT_PARTS * 256 * (size_t)(128 + 2);
+    const size_t ws = o_part + (size_t)sms * std::max(absorbed, expanded) * 4;
     if (cudaMalloc(&h->ws, ws) != cudaSuccess) {
         cudaGetLastError();
         delete h;
@@ -251,7 +254,7 @@ sfar_latent_t *sfar_latent_create(int R, int q_heads, int latent_dim, int rope_d
     }
     h->ctl = reinterpret_cast<SfarCtl *>(h->ws);
     h->arrived = reinterpret_cast<int *>(h->ws + o_arrived);
-    h->next = reinterpret_cast<unsigned *>(h->arrived + 3 * sms);
+    h->next = reinterpret_cast<unsigned *>(h->arrived + 3 * counter_stride(sms));
     h->part = reinterpret_cast<float *>(h->ws + o_part);
     const SfarCtl init = fresh_ctl();
     bool ok = cudaMemset(h->ws, 0, ws) == cudaSuccess && cudaMemcpy(h->ctl, &init, sizeof init, cudaMemcpyHostToDevice) == cudaSuccess &&
@@ -426,7 +429,7 @@ sfar_status sfar_latent_attention(sfar_latent_t *h, const void *const q[], void 
     a.starts = starts;
     a.part = h->part;
     a.arrived = h->arrived;
-    a.arrived_stride = h->sms;
+    a.arrived_stride = (int)counter_stride(h->sms);
     a.ctl = h->ctl;
     a.qts = (long long)q_token_stride;
     a.qhs = (long long)q_head_stride;
@@ -519,6 +522,9 @@ sfar_status sfar_latent_prompt(sfar_latent_t *h, const void *const q[], const vo
     a.starts = starts;
     a.kstarts = k_starts;
     a.next = h->next;
+    a.part = h->part;
+    a.arrived = h->arrived;
+    a.arrived_stride = (int)counter_stride(h->sms);
     a.ctl = h->ctl;
     a.ots = (long long)out_token_stride;
     a.ohs = (long long)out_head_stride;
@@ -536,7 +542,8 @@ sfar_status sfar_latent_prompt(sfar_latent_t *h, const void *const q[], const vo
     a.most = (int)most;
     int threads = 0, smem = 0;
     const void *f = sfar_kernel_latent_prompt((int)D, tiles, &threads, &smem);
-    const size_t grid = std::min((size_t)h->sms, most * H * (size_t)h->R);
+    // no more CTAs than there can be row tiles and, where these are few, parts of theirs
+    const size_t grid = std::min((size_t)h->sms, most * H * (size_t)h->R * (S / 512 + 1));
     return launch(h->dev, f, dim3((unsigned)grid), (unsigned)threads, (size_t)smem, &a, s);
 }
 
