@@ -30,7 +30,8 @@
 // line that is cut into equal pieces, one per CTA; row tiles cut apart are
 // joined by the last of their CTAs, in order.  Prefix sums of 32 requests at a
 // time are kept, so that shared memory is the tiles'.
-// Warps 0-3: softmax; 4: copies and pieces; 5: the MMAs; 6: query rows.
+// Warps 0-3: softmax; 4: copies and pieces; 5: the MMAs; 6: query rows, and the
+// zeros past the last request.
 #include "sfar_attn.cuh"
 #include "sfar_latent_args.h"
 
@@ -143,6 +144,13 @@ __device__ __forceinline__ void store_transposed(uint32_t addr, uint32_t a, uint
 }
 // whether one of the two bf16 is an infinity or NaN
 __device__ __forceinline__ bool odd2(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
+
+// Zeros for the rows past the last request, by a warp of each CTA.
+template <int L> __device__ __noinline__ void padding(const SfarLatentAttnArgs &a, int lane)
+{
+    if (a.starts[a.B] < a.T)
+        sfar_attn_padding<L>(a, lane, 32);
+}
 
 // Adds up `parts` partial results, the first at p0, the second at p1 and the others `step` floats on from it, each times
 // its row's weight w[part][row], by the 128 threads of the softmax: into the first one, or, where out is given, times by[row]
@@ -438,18 +446,16 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                         }
                     soft_sync();                   // s_max has been read, s_keep is there until the next move's first barrier
                     if (k) {
+#pragma unroll 1
+                        for (int n = 0; n < Y::kBlocks * NR; n += 16) {
+                            uint32_t o[16];
+                            tc::ld16(o, tO + n);
+                            tc::wait_ld(o);
 #pragma unroll
-                        for (int c = 0; c < Y::kBlocks; ++c)
-#pragma unroll
-                            for (int n0 = 0; n0 < NR; n0 += 16) {
-                                uint32_t o[16];
-                                tc::ld16(o, tO + c * NR + n0);
-                                tc::wait_ld(o);
-#pragma unroll
-                                for (int n = 0; n < 16; ++n)
-                                    o[n] = __float_as_uint(__uint_as_float(o[n]) * s_keep[n0 + n]);
-                                tc::st16(tO + c * NR + n0, o);
-                            }
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * s_keep[n % NR + e]);
+                            tc::st16(tO + n, o);
+                        }
                         tc::wait_st();
                     }
                 }
@@ -510,10 +516,8 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
             }
             // The accumulator, element tid of each 128 of the latent, a row at a time.  begin(n): what is read once for a row.
             auto each = [&](auto begin, auto what) {
-#pragma unroll
-                for (int n0 = 0; n0 < NR; n0 += 8) {
-                    if (n0 >= rows)
-                        break;
+#pragma unroll 1
+                for (int n0 = 0; n0 < rows; n0 += 8) {
                     decltype(begin(0)) of[8];
 #pragma unroll
                     for (int n = 0; n < 8; ++n)
@@ -602,7 +606,6 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
             if (lane == 0)
                 tc::bar_arrive(pempty + 8 * now_at);
         }
-        sfar_attn_padding<L>(a, tid, 32 * kSoft);
         if (dead && lane == 0)
             sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
     } else if (warp == kCopyWarp) {
@@ -751,6 +754,7 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
         }
         if (dead && lane == 0)
             sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
+        padding<L>(a, lane);
     } else {
         // ----------------------------------------------------------------- MMAs
         constexpr uint32_t idS = tc::idesc_bf16(64, NR), idO = tc::idesc_bf16(128, NR) | tc::kTransposeA;
