@@ -40,7 +40,7 @@ namespace {
 constexpr int kTile = SFAR_LATENT_TILE, kGroup = SFAR_LATENT_GROUP;
 constexpr int kSoft = 4, kCopyWarp = kSoft, kMmaWarp = kSoft + 1, kQueryWarp = kSoft + 2, kThreads = 32 * (kQueryWarp + 1);
 constexpr int kBox = kTile * 128, kPair = 2 * kBox;                // bytes of 64 elements of every token, of 128
-constexpr int kMeta = 8, kPieces = 4, kParts = 16, kKept = 64;     // kMeta: above the tiles in flight; kParts: joined at once, at most
+constexpr int kMeta = 8, kPieces = 4, kParts = 16, kKept = 64, kWhole = 8;     // kMeta: above the tiles in flight; kParts: joined at once, at most
 
 template <int L, int NR> struct Lay {
     static constexpr int kBlocks = L / 128, kChunks = L / 64 + 1;
@@ -118,7 +118,7 @@ template <int NR, class A> struct Work {
         p.all = tiles(p.len);
         p.rt = (int)(w / (uint32_t)p.all);
         p.tile0 = (int)(w - (uint32_t)p.rt * (uint32_t)p.all);
-        p.tiles = (int)min((long long)(p.all - p.tile0), end - u);
+        p.tiles = p.all <= kWhole ? p.all - p.tile0 : (int)min((long long)(p.all - p.tile0), end - u);
         const long long last = min((long long)p.count * a.Hq, ((long long)p.rt + 1) * NR) - 1;       // the row tile's last row
         const int to = p.len - p.count + (int)(last / a.Hq) + 1;                                     // tokens it attends to
         p.run = max(0, min(p.tiles, (max(0, to) + kTile - 1) / kTile - p.tile0));
@@ -245,6 +245,8 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
 
     if (warp == kCopyWarp && lane < a.R)
         tc::prefetch_map(&a.map[lane]);
+    if (warp == kQueryWarp && lane < a.R && a.q_flat)
+        tc::prefetch_map(&a.qmap[lane]);
     if (tid == 0) {
         for (uint32_t b = full; b <= drain; b += 8)
             tc::bar_init(b, b >= pempty && b < qbar ? kSoft + 2 : b == qbar ? 32 : b == wbar ? kSoft : 1);
@@ -301,7 +303,8 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w)
         whole += s_warp[w];
-    // short row tiles are left whole, or in cuts of four tiles
+    // Row tiles of up to 8 tiles are left whole (34 requests of 127 tokens, 22 heads, 8 ranks: 28 us cut in equal pieces, XX so:
+    // joining two parts costs what four tiles do), longer ones in cuts of no less than four.
     const long long U = sfar_attn_many(a, whole) ? 0 : (long long)carry * a.R;
     const long long N = min(min((long long)gridDim.x, U), max(whole * a.R, U / 4));
     const long long u0 = blockIdx.x < N ? sfar_div(blockIdx.x * U, N) : 0, u1 = blockIdx.x < N ? sfar_div((blockIdx.x + 1) * U, N) : 0;
@@ -621,11 +624,15 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
         const int per = min(1 << a.shift, kTile), boxes = kTile / per;     // tokens of one copy, copies of a tile's 64 elements
         for (long long u = u0; !dead;) {
             Piece p;
+            p.tiles = 0;
             const bool end = u >= u1;
-            if (!end)
+            if (!end) {
                 p = work.at(u, u1);
-            else
-                p.tiles = 0;
+                if (p.tile0 && p.all <= kWhole) {
+                    u += p.tiles;                  // a short row tile is the CTA's that has its first tile
+                    continue;
+                }
+            }
             if (!wait(pempty + 8 * ps.slot, ps.phase ^ 1u)) {
                 dead = true;
                 break;
@@ -712,8 +719,9 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
     } else if (warp == kQueryWarp) {
         // -------------------------------------------------------------- queries
         // A piece's query rows: [chunk][row][64 elements], 128-byte swizzle; zeros past the rows and past a short key.
+        const uint64_t once = tc::evict_first();
         tc::Ring<kPieces> ps;
-        uint32_t phase = 1;
+        uint32_t phase = 1, asked = 0;
         bool dead = false;
         for (;;) {
             dead = !__all_sync(SFAR_FULL, tc::bar_wait(pfull + 8 * ps.slot, ps.phase, limit));
@@ -726,25 +734,36 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                 phase ^= 1u;
                 if (dead)
                     break;
-                constexpr int kVecs = Y::kChunks * 8, kEach = NR < 32 ? NR : 32;
-                const int row0 = p.rt * NR, rows = (int)min((long long)NR, (long long)p.count * a.Hq - row0);
-                for (int m = 0; m < NR; m += kEach) {
-                    // lane i: where row m + i comes from
-                    const int row = row0 + min(m + lane, rows - 1), i = row / a.Hq;
-                    const uint16_t *src = a.q[p.r] + (long long)(p.first + i) * a.qts + (long long)(row - i * a.Hq) * a.qhs;
+                const int row0 = p.rt * NR;
+                ++asked;
+                if (a.q_flat) {
+                    // rows one stride apart: a copy to 64 elements of all (those past the request's are others', and not written out)
+                    if (lane == 0)
+                        tc::bar_expect_only(qbar, Y::kQ);
+                    __syncwarp();
+                    if (lane < Y::kChunks)
+                        tc::load_2d(mem + Y::oQ + lane * (NR * 128), &a.qmap[p.r], 64 * lane, p.first * a.Hq + row0, qbar, once);
+                } else {
+                    constexpr int kVecs = Y::kChunks * 8, kEach = NR < 32 ? NR : 32;
+                    const int rows = (int)min((long long)NR, (long long)p.count * a.Hq - row0);
+                    for (int m = 0; m < NR; m += kEach) {
+                        // lane i: where row m + i comes from
+                        const int row = row0 + min(m + lane, rows - 1), i = row / a.Hq;
+                        const uint16_t *src = a.q[p.r] + (long long)(p.first + i) * a.qts + (long long)(row - i * a.Hq) * a.qhs;
 #pragma unroll 4
-                    for (int e = lane; e < kEach * kVecs; e += 32) {
-                        const int y = e / kVecs, c = e - y * kVecs, n = m + y;
-                        const uint16_t *from = reinterpret_cast<const uint16_t *>(__shfl_sync(SFAR_FULL, (unsigned long long)src, y));
-                        const bool in = n < rows && c * 8 < L + a.rope;
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(mem + Y::oQ + (c >> 3) * (NR * 128) + n * 128 +
-                                                                                          (((c & 7) ^ (n & 7)) << 4)),
-                                     "l"(in ? from + c * 8 : from), "r"(in ? 16u : 0u)
-                                     : "memory");
+                        for (int e = lane; e < kEach * kVecs; e += 32) {
+                            const int y = e / kVecs, c = e - y * kVecs, n = m + y;
+                            const uint16_t *from = reinterpret_cast<const uint16_t *>(__shfl_sync(SFAR_FULL, (unsigned long long)src, y));
+                            const bool in = n < rows && c * 8 < L + a.rope;
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(mem + Y::oQ + (c >> 3) * (NR * 128) + n * 128 +
+                                                                                              (((c & 7) ^ (n & 7)) << 4)),
+                                         "l"(in ? from + c * 8 : from), "r"(in ? 16u : 0u)
+                                         : "memory");
+                        }
                     }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    tc::fence_async();
                 }
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                tc::fence_async();
                 tc::bar_arrive(qbar);
             }
             __syncwarp();
@@ -752,8 +771,11 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                 tc::bar_arrive(pempty + 8 * ps.slot);
             ps.next();
         }
-        if (dead && lane == 0)
+        if (dead && lane == 0) {
             sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
+            if (asked)                             // the copies in flight land before the shared memory is released
+                tc::bar_wait(qbar, (asked - 1) & 1u, limit);
+        }
         padding<L>(a, lane);
     } else {
         // ----------------------------------------------------------------- MMAs

@@ -42,6 +42,9 @@ struct SfarLatentAttnArgs {
     // caches of every rank as 3-D tensor maps: a row's numbers (innermost) by
     // page_tokens by pages; boxes of 64 numbers by up to 64 tokens, 128-byte swizzle
     CUtensorMap map[SFAR_MAX_R];
+    // q_flat: query rows (tokens, their heads) lie one stride apart, and are 2-D tensor maps too; boxes of 64 numbers by a row
+    // tile, zeros past the last row
+    CUtensorMap qmap[SFAR_MAX_R];
     const uint16_t *q[SFAR_MAX_R];
     uint16_t *out[SFAR_MAX_R];
     const int *table, *lens, *starts;
@@ -50,7 +53,7 @@ struct SfarLatentAttnArgs {
     SfarCtl *ctl;
     long long qts, qhs, ots, ohs;
     float scale;
-    int R, B, W, T, Hq, shift, pages, rope, arrived_stride;
+    int R, B, W, T, Hq, shift, pages, rope, arrived_stride, q_flat;
     int most;                               // row tiles of all requests, at most
 };
 

@@ -450,6 +450,18 @@ sfar_status sfar_latent_attention(sfar_latent_t *h, const void *const q[], void 
     if (tokens * H >= 1ull << 29 || (tokens * H / 16 + requests) * (ceil_div(reach, SFAR_LATENT_TILE) + 8) >= 1ull << 32)
         return SFAR_ERR_INVALID;
     a.most = (int)(tokens * H / (size_t)rows + requests);
+    const size_t step = H > 1 ? q_head_stride : q_token_stride;        // of a row
+    a.q_flat = tokens * H == 1 || (step >= row && (H == 1 || tokens == 1 || q_token_stride == H * q_head_stride));
+    if (a.q_flat) {
+        const cuuint64_t dims[2] = {(cuuint64_t)row, (cuuint64_t)(tokens * H)}, strides[1] = {(cuuint64_t)(tokens * H == 1 ? row : step) * 2};
+        const cuuint32_t unit[2] = {1, 1}, box[2] = {64, (cuuint32_t)rows};
+        const PFN_cuTensorMapEncodeTiled_v12000 encode = encoder();
+        for (int r = 0; r < h->R; ++r)
+            if (!encode || encode(&a.qmap[r], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(q[r]), dims, strides, box, unit,
+                                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+                return encode ? SFAR_ERR_INVALID : SFAR_ERR_UNSUPPORTED;
+    }
     int threads = 0, smem = 0;
     const void *f = sfar_kernel_latent_attn(h->L, rows, &threads, &smem);
     return launch(h->dev, f, dim3((unsigned)h->sms), (unsigned)threads, (size_t)smem, &a, s);
