@@ -303,7 +303,7 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w)
         whole += s_warp[w];
-    // Row tiles of up to 8 tiles are left whole (34 requests of 127 tokens, 22 heads, 8 ranks: 28 us cut in equal pieces, XX so:
+    // Row tiles of up to 8 tiles are left whole (34 requests of 127 tokens, 22 heads, 8 ranks: 28 us cut in equal pieces, 19 so:
     // joining two parts costs what four tiles do), longer ones in cuts of no less than four.
     const long long U = sfar_attn_many(a, whole) ? 0 : (long long)carry * a.R;
     const long long N = min(min((long long)gridDim.x, U), max(whole * a.R, U / 4));

@@ -74,7 +74,7 @@ bool apart(size_t tokens, size_t heads, size_t row, size_t ts, size_t hs)
 bool strides_fit(std::initializer_list<size_t> s, size_t of)
 {
     for (size_t v : s)
-        if (v % of || v >> 40)
+        if (v % of || v >> 39)
             return false;
     return true;
 }

@@ -63,7 +63,7 @@ sfar_status sfar_latent_plan(sfar_latent_t *h, const int32_t *lens, const int32_
  * whose position is negative is left out; the slots of a call are distinct.
  * weight: [latent_dim] bf16.  Pointers 16-byte aligned (pos, freq, slots 4),
  * token_stride a multiple of 8, at least a row (with more than one token) and
- * below 2^40; tokens < 2^31; eps >= 0, scale finite.
+ * below 2^39; tokens < 2^31; eps >= 0, scale finite.
  */
 sfar_status sfar_latent_append(sfar_latent_t *h, const void *const x[], const void *weight, const int32_t *pos,
                                const float *freq, const int32_t *slots, size_t tokens, size_t token_stride, float eps,
@@ -76,7 +76,7 @@ sfar_status sfar_latent_append(sfar_latent_t *h, const void *const x[], const vo
  * SFAR_KV_BAD_TOKENS) or that are on no page of the pool (SFAR_KV_BAD_PAGE),
  * and rows past starts[requests], are left as they are.  out[r]: bf16, rows of
  * latent_dim + rope_dim, token_stride a multiple of 8, at least a row, below
- * 2^40; pointers 16-byte aligned; out overlaps no other argument nor the
+ * 2^39; pointers 16-byte aligned; out overlaps no other argument nor the
  * caches.  1 <= requests <= SFAR_KV_MAX_REQUESTS; tokens, table_width < 2^31.
  */
 sfar_status sfar_latent_gather(sfar_latent_t *h, void *const out[], const int32_t *table, const int32_t *lens,
@@ -101,8 +101,12 @@ sfar_status sfar_latent_gather(sfar_latent_t *h, void *const out[], const int32_
  * the kernel; a request that has more is still computed).  out overlaps no
  * other argument nor the caches, no row of it another, and the ranks' arrays
  * not one another.  1 <= requests <= SFAR_KV_MAX_REQUESTS; tokens,
- * table_width < 2^31; strides below 2^40; scale finite and at least 0.  The
- * kernel counts in 32 bits: tokens * q_heads is below 2^29, and the product of
+ * table_width < 2^31; strides below 2^39; scale finite and at least 0.  (Two
+ * tensors that lie in one another's memory without meeting are taken if they
+ * are beside one another in rows of one length, as slices of one tensor's
+ * last dimensions are, and refused otherwise; a strided out whose rows along
+ * one dimension do not fit the other's stride is refused too.)  The kernel
+ * counts in 32 bits: tokens * q_heads is below 2^29, and the product of
  * tokens * q_heads / 16 + requests (row tiles) and table_width * page_tokens
  * / 64 + 8 (tiles of a context) below 2^32.
  */
@@ -122,9 +126,10 @@ sfar_status sfar_latent_attention(sfar_latent_t *h, const void *const q[], void 
  * (new tokens) + i and attends to context rows j <= p, with score
  * scale * (q[:head_dim] . k_j + q[head_dim:] . kr_j).  Softmax, numbers, rows
  * of nothing and rows past starts[requests] as in sfar_latent_attention.  All
- * bf16, strides in elements, multiples of 8 and below 2^40 (those of k, v, kr
- * below 2^32), pointers 16-byte aligned; head_dim 64 or 128.  out overlaps no
- * other argument, no row of it another, and the ranks' arrays not one another.
+ * bf16, strides in elements, multiples of 8 and below 2^39 (those of q, k, v
+ * and kr above 0 for a dimension of more than one entry), pointers 16-byte
+ * aligned; head_dim 64 or 128.  out overlaps no other argument, no row of it
+ * another, and the ranks' arrays not one another.
  * 1 <= requests <= SFAR_KV_MAX_REQUESTS; tokens, k_tokens < 2^31 - 1024;
  * tokens / 128 + requests, times q_heads and R, below 2^31; scale finite and
  * at least 0.  Offsets out of order or beyond the tensors' rows:

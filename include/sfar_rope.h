@@ -32,7 +32,7 @@ extern "C" {
  * one token stride.  pos: [tokens], freq: [rot / 2] binary32, DEVICE memory.
  * A row whose position is negative is left as it is.
  * Types: the handle's (bf16 or fp32).  rot a multiple of 16, at most 1024;
- * pointers 16-byte aligned, strides multiples of 16 bytes and below 2^40,
+ * pointers 16-byte aligned, strides multiples of 16 bytes and below 2^39,
  * tokens < 2^31, heads < 65536, (q_heads + k_heads) * rot < 2^22; scale finite.  tokens = 0 does nothing.
  * One kernel on stream s; allocates and synchronises nothing.
  */

@@ -280,6 +280,42 @@ def test_attention(R, H, L, rot, P, lens, count):
     check_attention(out, q, cache, table, lens, starts, rot)
 
 
+LAYOUTS = ["slices of wider rows", "padded tokens", "heads outside", "one row for all tokens"]
+
+
+def laid_out(layout, R, T, H, W, g):
+    """A random [R, T, H, W] with the strides of a layout, on memory that holds NaN elsewhere."""
+    shape = {"slices of wider rows": (R, T, H, W + 24), "padded tokens": (R, T, H * W + 8), "heads outside": (R, H, T + 1, W),
+             "one row for all tokens": (R, 1, H, W)}[layout]
+    wide = torch.full(shape, float("nan"), dtype=BF, device="cuda")
+    x = {"slices of wider rows": lambda: wide[..., 16:16 + W], "padded tokens": lambda: wide[..., :H * W].unflatten(-1, (H, W)),
+         "heads outside": lambda: wide[:, :, :T].transpose(1, 2), "one row for all tokens": lambda: wide.expand(R, T, H, W)}[layout]()
+    if layout == "one row for all tokens":
+        wide.copy_(torch.randn(shape, generator=g, device="cuda"))
+    else:
+        x.copy_(torch.randn(R, T, H, W, generator=g, device="cuda"))
+    return x, wide
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("H,L,rot,lens,count", [(1, 256, 32, [70, 9], [1, 1]), (5, 512, 64, [300, 1000], [1, 3]), (30, 512, 32, [130], [2]),
+                                                (70, 256, 64, [65, 500], [1, 2])])
+def test_attention_strides(layout, H, L, rot, lens, count):
+    cache, table = cached(2, L, rot, 32, lens, seed=H)
+    g, T, starts = gen(H), sum(count) + 2, ref.offsets(count)
+    q, _ = laid_out(layout, 2, T, H, L + rot, g)
+    out, wide = laid_out(layout if layout != LAYOUTS[3] else LAYOUTS[0], 2, T, H, L, g)
+    out.fill_(0)
+    rest = torch.isnan(wide)
+    kv = sfar.SfarLatent(cache, q_heads=H, rope_dim=rot)
+    kv.attention(q, out, ints(table), ints(lens), ints(starts), max_q=max(count), scale=0.07)
+    torch.cuda.synchronize()
+    fine(kv)
+    check_attention(out, q, cache, table, lens, starts, rot)
+    assert torch.equal(torch.isnan(wide), rest)
+    kv.close()
+
+
 @pytest.mark.parametrize("max_q", [0, 1, 100])
 def test_attention_any_hint(max_q):
     cache, table = cached(2, 512, 64, 32, [400, 90], seed=2)
@@ -426,6 +462,22 @@ def test_prompt(R, H, D, rot, lens, count):
     x[4].fill_(float("nan"))
     prompt(kv, x, lens, count)
     assert torch.equal(x[4], first)                         # the same bits again
+    kv.close()
+
+
+@pytest.mark.parametrize("layout", LAYOUTS[:3])
+@pytest.mark.parametrize("H,D,rot,lens,count", [(1, 64, 32, [130, 9], [129, 9]), (5, 128, 64, [300, 500], [290, 3]), (9, 128, 32, [700], [40])])
+def test_prompt_strides(layout, H, D, rot, lens, count):
+    g, S, T = gen(H), sum(lens), sum(count) + 2
+    (q, _), (k, _), (v, _) = [laid_out(layout, 2, n, H, w, g) for n, w in ((T, D + rot), (S, D), (S, D))]
+    kr = laid_out("slices of wider rows", 2, S, 1, rot, g)[0][:, :, 0]
+    out, wide = laid_out(layout, 2, T, H, D, g)
+    out.fill_(0)
+    rest = torch.isnan(wide)
+    kv = plain_handle(2, H, rot)
+    prompt(kv, (q, k, v, kr, out), lens, count)
+    check_prompt((q, k, v, kr, out), lens, count)
+    assert torch.equal(torch.isnan(wide), rest)
     kv.close()
 
 
