@@ -415,7 +415,7 @@ class Sfar:
         or tensors of their own; k, k_out the same with their own heads (lists of R tensors, or one tensor [R, ...]
         each).  An output may be its input.  pos: [tokens] int32, freq: [rotated part / 2] fp32 (``rope_frequencies``);
         layout "half" or "interleaved"; rows of a negative position are left as they are."""
-        code = (_native or _tensors()).rope(self.h, self.R, self.dtype == "fp32", q, q_out, k, k_out, pos, freq, _layout(layout), scale, stream)
+        code = (_native or _tensors()).rope(self.h, self.R, DTYPES.get(self.dtype, self.dtype) == SFAR_FP32, q, q_out, k, k_out, pos, freq, _layout(layout), scale, stream)
         if code:
             _check(code, "sfar_rope")
 

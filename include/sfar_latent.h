@@ -41,8 +41,8 @@ typedef struct sfar_latent sfar_latent_t;
  * pointers, 16-byte aligned, no two overlapping).  1 <= R <= 16; latent_dim
  * 256 or 512; rope_dim 32 or 64; page_tokens 16, 32, 64 or 128;
  * 1 <= q_heads <= 65535; pages * page_tokens below 2^31.  The handle holds a
- * workspace for partial results, about 40 MB at latent_dim 512.  NULL on
- * failure (reason: sfar_last_error).  The caches' contents are not touched.
+ * workspace for partial results, about 40 MB.  NULL on failure (reason:
+ * sfar_last_error).  The caches' contents are not touched.
  */
 sfar_latent_t *sfar_latent_create(int R, int q_heads, int latent_dim, int rope_dim, int page_tokens, size_t pages,
                                   void *const cache[]);
@@ -59,7 +59,8 @@ sfar_status sfar_latent_plan(sfar_latent_t *h, const int32_t *lens, const int32_
  *   c_i = l_i * weight_i / sqrt(mean of l^2 + eps),
  *   kr  = k turned by pos[t] as sfar_rope does (freq: [rope_dim / 2]
  *         binary32, layout, scale),
- * in binary32, rounded once to bf16, to slots[t].  A token whose slot is -1 or
+ * in binary32 (a row whose sum of squares passes its range has zeros for its
+ * finite latents), rounded once to bf16, to slots[t].  A token whose slot is -1 or
  * whose position is negative is left out; the slots of a call are distinct.
  * weight: [latent_dim] bf16.  Pointers 16-byte aligned (pos, freq, slots 4),
  * token_stride a multiple of 8, at least a row (with more than one token) and
@@ -125,7 +126,8 @@ sfar_status sfar_latent_attention(sfar_latent_t *h, const void *const q[], void 
  * of them: row starts[b] + i stands at position p = (rows of the context) -
  * (new tokens) + i and attends to context rows j <= p, with score
  * scale * (q[:head_dim] . k_j + q[head_dim:] . kr_j).  Softmax, numbers, rows
- * of nothing and rows past starts[requests] as in sfar_latent_attention.  All
+ * of nothing and rows past starts[requests] as in sfar_latent_attention; a
+ * scale below 2^-123 counts as about that.  All
  * bf16, strides in elements, multiples of 8 and below 2^39 (those of q, k, v
  * and kr above 0 for a dimension of more than one entry), pointers 16-byte
  * aligned; head_dim 64 or 128.  out overlaps no other argument, no row of it

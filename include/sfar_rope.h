@@ -33,8 +33,9 @@ extern "C" {
  * A row whose position is negative is left as it is.
  * Types: the handle's (bf16 or fp32).  rot a multiple of 16, at most 1024;
  * pointers 16-byte aligned, strides multiples of 16 bytes and below 2^39,
- * tokens < 2^31, heads < 65536, (q_heads + k_heads) * rot < 2^22; scale finite.  tokens = 0 does nothing.
- * One kernel on stream s; allocates and synchronises nothing.
+ * tokens < 2^31, heads < 65536, (q_heads + k_heads) * rot < 2^22; scale
+ * finite.  tokens = 0 does nothing.  One kernel on stream s; allocates and
+ * synchronises nothing.
  */
 sfar_status sfar_rope(sfar_t *h, const void *const q[], void *const q_out[], const void *const k[], void *const k_out[],
                       const int32_t *pos, const float *freq, size_t tokens, size_t q_heads, size_t k_heads, size_t rot,

@@ -76,6 +76,20 @@ def test_rope_no_position_turns_nothing():
     h.close()
 
 
+@pytest.mark.parametrize("dtype", [sfar.SFAR_BF16, sfar.SFAR_FP32])
+def test_rope_of_a_handle_with_the_c_type(dtype):
+    mine, other = (BF, torch.float32) if dtype == sfar.SFAR_BF16 else (torch.float32, BF)
+    h = sfar.Sfar(2, 1 << 16, dtype)
+    x, freq = torch.randn(2, 3, 2, 32, generator=gen(2), device="cuda").to(mine), torch.ones(16, device="cuda")
+    out = torch.empty_like(x)
+    h.rope(x, out, ints([0, 0, 0]), freq)
+    torch.cuda.synchronize()
+    assert torch.equal(out, x)
+    with pytest.raises(ValueError):
+        h.rope(x.to(other), out.to(other), ints([0, 0, 0]), freq)
+    h.close()
+
+
 def test_rope_refuses():
     h = sfar.Sfar(2, 1 << 16, "bf16")
     x, pos, freq = torch.zeros(2, 4, 3, 64, dtype=BF, device="cuda"), ints([0] * 4), torch.ones(32, device="cuda")
@@ -478,6 +492,18 @@ def test_prompt_strides(layout, H, D, rot, lens, count):
     prompt(kv, (q, k, v, kr, out), lens, count)
     check_prompt((q, k, v, kr, out), lens, count)
     assert torch.equal(torch.isnan(wide), rest)
+    kv.close()
+
+
+@pytest.mark.parametrize("B", [64, 65, 100])
+def test_prompt_many_requests(B):
+    count = [(7 * i) % 5 for i in range(B)]
+    count[B // 2] = 150
+    lens = [n + (11 * i) % 40 for i, n in enumerate(count)]
+    x = expanded(1, 2, 64, 32, lens, count, seed=B, pad=1)
+    kv = plain_handle(1, 2, 32)
+    prompt(kv, x, lens, count)
+    check_prompt(x, lens, count)
     kv.close()
 
 
