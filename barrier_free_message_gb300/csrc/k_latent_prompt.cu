@@ -98,96 +98,104 @@ template <int D> __device__ __noinline__ void padding(const SfarLatentPromptArgs
         sfar_attn_padding<D>(a, lane, 32);
 }
 
-// All softmax threads, after their parts: joins the row tile's parts if this CTA is the last of them.  A warp takes a row;
-// lane i keeps what part i is multiplied by.
-template <int D, int TILES> __device__ __noinline__ void join(const SfarLatentPromptArgs &a, const Piece &p, int warp, int *s_last)
+// Joins `parts` parts, the first at p0, the others `step` floats on from it each: 8 elements of a row to a thread, rows next to
+// one another as they lie in a part, kItems of them with kBatch parts each in flight (time passes by round trips).  Into the
+// result, or into the first part; then a thread's first item's reference and sum are given back.
+template <int D, int TILES, int kBatch, int kItems>
+__device__ __forceinline__ float2 join_parts(float *p0, uint32_t step, int parts, int rows, uint16_t *out, long long ots)
 {
-    constexpr int kRows = 128 * TILES, kWarps = 8 * TILES, kPart = kRows * (D + 2), kVec = D / 32, kBatch = 3, kY = 4;
-    const int lane = threadIdx.x & 31, rows = min(kRows, p.count - p.rt * kRows);
+    constexpr int kRows = 128 * TILES, kThreads = 256 * TILES;
+    float2 kept = make_float2(-INFINITY, 0.f);
+#pragma unroll 1
+    for (int i0 = threadIdx.x; i0 < rows * (D / 8); i0 += kItems * kThreads) {
+        uint32_t at[kItems], n[kItems];            // items past the last: the last again
+        float top[kItems], total[kItems], o[kItems][8];
+#pragma unroll
+        for (int y = 0; y < kItems; ++y) {
+            const int i = min(i0 + y * kThreads, rows * (D / 8) - 1);
+            n[y] = (uint32_t)i % (uint32_t)rows;
+            at[y] = 8u * (uint32_t)i - 7u * n[y];  // of the item's first element, 8 (i / rows), in a part
+            top[y] = -INFINITY;
+            total[y] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                o[y][e] = 0.f;
+        }
+#pragma unroll 1
+        for (int c0 = 0; c0 < parts; c0 += kBatch) {
+            float2 m[kItems][kBatch];
+            float v[kItems][kBatch][8];
+#pragma unroll
+            for (int y = 0; y < kItems; ++y)
+#pragma unroll
+                for (int c = 0; c < kBatch; ++c) {
+                    const uint32_t from = min(c0 + c, parts - 1) * step;           // parts past the last: the last again, not added
+                    m[y][c] = __ldcg(reinterpret_cast<const float2 *>(p0 + (from + kRows * D + 2 * n[y])));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[y][c][e] = __ldcg(p0 + (from + at[y] + e * rows));
+                }
+#pragma unroll
+            for (int y = 0; y < kItems; ++y)
+#pragma unroll
+                for (int c = 0; c < kBatch; ++c)
+                    if (c0 + c < parts) {
+                        const float now = fmaxf(top[y], m[y][c].x);
+                        const float keep = top[y] == now ? 1.f : ex2(top[y] - now), w = m[y][c].x == -INFINITY ? 0.f : ex2(m[y][c].x - now);
+                        top[y] = now;
+                        // a part that has seen nothing: its sum is 0, or NaN
+                        total[y] = total[y] * keep + (m[y][c].x == -INFINITY ? m[y][c].y : w * m[y][c].y);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            o[y][e] = o[y][e] * keep + w * v[y][c][e];
+                    }
+        }
+#pragma unroll
+        for (int y = 0; y < kItems; ++y) {
+            if (i0 + y * kThreads >= rows * (D / 8))
+                break;
+            if (out) {
+                const float by = total[y] == 0.f ? 0.f : 1.f / total[y];
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = tc::bf16x2(o[y][2 * e] * by, o[y][2 * e + 1] * by);
+                st_v4(out + n[y] * ots + (at[y] - n[y]) / (uint32_t)rows, make_uint4(w[0], w[1], w[2], w[3]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    __stcg(p0 + (at[y] + e * rows), o[y][e]);
+            }
+        }
+        if (i0 == (int)threadIdx.x)
+            kept = make_float2(top[0], total[0]);
+    }
+    return kept;
+}
+// All softmax threads, after their parts: joins the row tile's parts if this CTA is the last of them.
+template <int D, int TILES> __device__ __noinline__ void join(const SfarLatentPromptArgs &a, const Piece &p, int *s_last)
+{
+    constexpr int kRows = 128 * TILES, kThreads = 256 * TILES, kPart = kRows * (D + 2);
+    const int rows = min(kRows, p.count - p.rt * kRows);
     SfarJoin j(a, 0, p.c0, p.c1, p.part);
     for (;;) {
-        asm volatile("bar.sync 9, %0;" ::"n"(32 * kWarps) : "memory");
+        asm volatile("bar.sync 9, %0;" ::"n"(kThreads) : "memory");
         if (threadIdx.x == 0)
             *s_last = j.last();
-        asm volatile("bar.sync 9, %0;" ::"n"(32 * kWarps) : "memory");
+        asm volatile("bar.sync 9, %0;" ::"n"(kThreads) : "memory");
         if (!*s_last)
             return;
         const int parts = (j.hi - j.lo) / j.step + 1;
         const bool more = j.up != 0;
-        auto slot = [&](int c) { return a.part + (size_t)(j.lo + c * j.step) * kPart; };
-        // four rows at a time: time passes by round trips
-        for (int n0 = warp; n0 < rows; n0 += kY * kWarps) {
-            float2 m[kY];
-            int n[kY];                             // rows past the last: the last again
-#pragma unroll
-            for (int y = 0; y < kY; ++y) {
-                n[y] = min(n0 + y * kWarps, rows - 1);
-                m[y] = make_float2(-INFINITY, 0.f);
-                if (lane < parts)
-                    m[y] = __ldcg(reinterpret_cast<const float2 *>(slot(lane) + kRows * D) + n[y]);
-            }
-            float w[kY], top[kY], total[kY], o[kY][kVec];
-#pragma unroll
-            for (int y = 0; y < kY; ++y) {
-                top[y] = m[y].x;
-#pragma unroll
-                for (int d = 16; d; d >>= 1)
-                    top[y] = fmaxf(top[y], __shfl_xor_sync(SFAR_FULL, top[y], d));
-                w[y] = m[y].x == -INFINITY ? 0.f : ex2(m[y].x - top[y]);
-                total[y] = m[y].x == -INFINITY ? m[y].y : w[y] * m[y].y;           // its sum is 0 then, or NaN
-#pragma unroll
-                for (int d = 16; d; d >>= 1)
-                    total[y] += __shfl_xor_sync(SFAR_FULL, total[y], d);
-#pragma unroll
-                for (int e = 0; e < kVec; ++e)
-                    o[y][e] = 0.f;
-            }
-#pragma unroll 1
-            for (int c0 = 0; c0 < parts; c0 += kBatch) {
-                float v[kBatch][kY][kVec];
-#pragma unroll
-                for (int c = 0; c < kBatch; ++c)
-#pragma unroll
-                    for (int y = 0; y < kY; ++y) {
-                        const float *src = slot(min(c0 + c, parts - 1)) + n[y] * D + lane * kVec;
-                        if constexpr (kVec == 4) {
-                            const float4 u = __ldcg(reinterpret_cast<const float4 *>(src));
-                            v[c][y][0] = u.x, v[c][y][1] = u.y, v[c][y][2] = u.z, v[c][y][3] = u.w;
-                        } else {
-                            const float2 u = __ldcg(reinterpret_cast<const float2 *>(src));
-                            v[c][y][0] = u.x, v[c][y][1] = u.y;
-                        }
-                    }
-#pragma unroll
-                for (int c = 0; c < kBatch; ++c)
-#pragma unroll
-                    for (int y = 0; y < kY; ++y) {
-                        const float f = __shfl_sync(SFAR_FULL, w[y], (c0 + c) & 31);
-                        if (c0 + c < parts)
-#pragma unroll
-                            for (int e = 0; e < kVec; ++e)
-                                o[y][e] += f * v[c][y][e];
-                    }
-            }
-#pragma unroll
-            for (int y = 0; y < kY; ++y) {
-                if (n0 + y * kWarps >= rows)
-                    break;
-                if (more) {
-                    float *to = slot(0) + n[y] * D + lane * kVec;
-#pragma unroll
-                    for (int e = 0; e < kVec; e += 2)
-                        __stcg(reinterpret_cast<float2 *>(to + e), make_float2(o[y][e], o[y][e + 1]));
-                    if (lane == 0)
-                        __stcg(reinterpret_cast<float2 *>(slot(0) + kRows * D) + n[y], make_float2(top[y], total[y]));
-                } else {
-                    const float by = total[y] == 0.f ? 0.f : 1.f / total[y];
-                    uint16_t *dst = a.out[p.r] + (long long)(p.first + p.rt * kRows + n[y]) * a.ots + (long long)p.h * a.ohs + lane * kVec;
-#pragma unroll
-                    for (int e = 0; e < kVec; e += 2)
-                        *reinterpret_cast<uint32_t *>(dst + e) = tc::bf16x2(o[y][e] * by, o[y][e + 1] * by);
-                }
-            }
+        float *const p0 = a.part + (size_t)j.lo * kPart;
+        uint16_t *const out = more ? nullptr : a.out[p.r] + (long long)(p.first + p.rt * kRows) * a.ots + (long long)p.h * a.ohs;
+        const uint32_t step = (uint32_t)(j.step * kPart);
+        const float2 m = parts <= 2 ? join_parts<D, TILES, 2, 2>(p0, step, parts, rows, out, a.ots)
+                                    : join_parts<D, TILES, 4, 1>(p0, step, parts, rows, out, a.ots);
+        if (more) {
+            asm volatile("bar.sync 9, %0;" ::"n"(kThreads) : "memory");       // the first part's references have been read
+            if ((int)threadIdx.x < rows)
+                __stcg(reinterpret_cast<float2 *>(p0 + kRows * D) + threadIdx.x, m);
         }
         if (!j.next(a, 0))
             return;
@@ -268,7 +276,9 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
     if (many && blockIdx.x == 0 && tid == 0)
         sfar_kv_fault(a.ctl, a.B, SFAR_KV_BAD_TOKENS);
     // Fewer row tiles than CTAs are cut along the context, into at most two parts for each CTA and of no less than kLeast
-    // tiles; the last of a row tile's parts to finish joins them, in their order.
+    // tiles, twice that for more than 32 rows, whose parts are longer to write and read (one request, 4 heads, 1000 tokens: 31 us
+    // so, 38 with kLeast; 4 new tokens after 16384 gain 3 us by it); the last of a row tile's parts to finish joins them, in
+    // their order.
     const uint32_t whole = many ? 0 : carry * (uint32_t)(a.R * a.Hq);
     const uint32_t cuts = whole && whole < gridDim.x ? 2 * gridDim.x / whole : 1, items = whole * cuts;
 
@@ -397,7 +407,8 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
             const bool parts = p.c0 != p.c1;
             const float by = parts ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
             uint16_t *dst = a.out[p.r] + (long long)(p.first + min(i, p.count - 1)) * a.ots + (long long)p.h * a.ohs + D / 2 * half;
-            float *part = a.part + (size_t)p.part * kPart + (x * 128 + lrow) * D + D / 2 * half;
+            const int rows = min(kRows, p.count - p.rt * kRows);       // of the row tile: a part's stride
+            float *part = a.part + (size_t)p.part * kPart + D / 2 * half * rows + x * 128 + lrow;      // [element][row]
 #pragma unroll 1
             for (int c = 0; c < D / 2; c += 16) {
                 uint32_t o[16];
@@ -411,8 +422,8 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                 if (parts) {
                     if (row)
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4)
-                            __stcg(reinterpret_cast<uint4 *>(part + c + e), make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+                        for (int e = 0; e < 16; ++e)
+                            __stcg(part + (c + e) * rows, __uint_as_float(o[e]));
                     continue;
                 }
                 uint32_t y[8];
@@ -425,7 +436,7 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
             if (parts) {
                 if (row && half == 0)
                     __stcg(reinterpret_cast<float2 *>(a.part + (size_t)p.part * kPart + kRows * D) + x * 128 + lrow, make_float2(ref, sum));
-                join<D, TILES>(a, p, warp, &s_last);
+                join<D, TILES>(a, p, &s_last);
             }
             tc::fence_before();
             __syncwarp();
@@ -504,7 +515,8 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                         p.steps[x] = (max(0, p.len - p.count + last + 1) + kTile - 1) / kTile;
                 }
                 // this part of the row tile's: p.c1 < p.c0 if it is none
-                const int all = max(p.steps[0], p.steps[1]), parts = min((int)cuts, max(1, (all + kLeast - 1) / kLeast));
+                const int least = p.count - p.rt * kRows <= 32 ? kLeast : 2 * kLeast;
+                const int all = max(p.steps[0], p.steps[1]), parts = min((int)cuts, max(1, (all + least - 1) / least));
                 p.c0 = p.part - part;
                 p.c1 = part < parts ? p.c0 + parts - 1 : -1;
                 const int each = all / parts, rest = all - each * parts;            // the first `rest` have one more
