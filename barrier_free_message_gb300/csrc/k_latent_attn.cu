@@ -559,7 +559,7 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                 // a part: leave it in the workspace, for the last of the row tile's CTAs
                 const long long from = p.at - p.tile0, to = from + p.all;
                 const int c0 = (int)sfar_div((from + 1) * N - 1, U), c1 = (int)sfar_div(to * N - 1, U);
-                SfarJoin join(a, 0, c0, c1, blockIdx.x);
+                SfarJoin join(a, 0, c0, c1, blockIdx.x, kParts);
                 auto slot = [&](int c) { return a.part + ((size_t)c * 2 + (c == c0)) * Y::kPart; };
                 float *dst = slot(blockIdx.x);
                 each([](int) { return 0; }, [&](int, int n, int d, float v) { __stcg(dst + n * L + d, v); });

@@ -118,14 +118,14 @@ struct SfarJoin {
     int c0, c1;
     int lo, hi, step;               // parts lo, lo + step .. hi are joined next
     int *counter;                   // of those that have come
-    template <class A> __device__ __forceinline__ SfarJoin(const A &a, int kind, int first, int last, int me) : c0(first), c1(last)
+    template <class A> __device__ __forceinline__ SfarJoin(const A &a, int kind, int first, int last, int me, int flat = 8) : c0(first), c1(last)
     {
         // three sets of counters: of groups that begin a row tile, of others (their first CTA begins no other row
         // tile's second group), of the groups of a row tile; index: the first CTA
         int *set = a.arrived + kind * 3 * a.arrived_stride;
         const int parts = c1 - c0 + 1;
         lo = c0, hi = c1, step = 1, counter = set + c0;
-        if (parts > 8) {
+        if (parts > flat) {        // flat: joined at once
             const int radix = max(8, (int)ceilf(sqrtf((float)parts)));
             lo = c0 + (me - c0) / radix * radix;
             hi = min(lo + radix - 1, c1);
