@@ -113,7 +113,7 @@ template <int E> struct SfarAttnState {
 // the order of the CTAs, by whichever of them comes last -- of a group of
 // `radix` neighbours, which leaves its result in the place of its first, and
 // then of the groups (one CTA would read 76 parts of 16 rows for 40 us; two
-// levels of 9 take 5).  Up to 8 parts are one group.
+// levels of 9 take 5).  Up to `flat` parts are one group.
 struct SfarJoin {
     int c0, c1;
     int lo, hi, step;               // parts lo, lo + step .. hi are joined next
@@ -125,7 +125,7 @@ struct SfarJoin {
         int *set = a.arrived + kind * 3 * a.arrived_stride;
         const int parts = c1 - c0 + 1;
         lo = c0, hi = c1, step = 1, counter = set + c0;
-        if (parts > flat) {        // flat: joined at once
+        if (parts > flat) {
             const int radix = max(8, (int)ceilf(sqrtf((float)parts)));
             lo = c0 + (me - c0) / radix * radix;
             hi = min(lo + radix - 1, c1);
