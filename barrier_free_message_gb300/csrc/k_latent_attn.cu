@@ -799,21 +799,27 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
         tc::Ring<kPieces> ps;
         uint32_t qphase = 0, wphase = 0, tile = 0;
         bool dead = false;
-        for (;;) {
-            dead = __any_sync(SFAR_FULL, dead || !tc::bar_wait(pfull + 8 * ps.slot, ps.phase, limit));
-            if (dead)
-                break;
-            const int run = s_piece[ps.slot].run, tiles = s_piece[ps.slot].tiles;
-            __syncwarp();
-            if (lane == 0)
-                tc::bar_arrive(pempty + 8 * ps.slot);
-            ps.next();
-            if (tiles == 0)
-                break;
-            if (tc::elect_one() && run) {
+        if (tc::elect_one()) {                     // all by one lane
+            int run = 0, tiles = 0;
+            auto take = [&]() {
+                dead = !tc::bar_wait(pfull + 8 * ps.slot, ps.phase, limit);
+                if (!dead) {
+                    run = s_piece[ps.slot].run;
+                    tiles = s_piece[ps.slot].tiles;
+                    tc::bar_arrive(pempty + 8 * ps.slot);
+                    ps.next();
+                }
+            };
+            take();
+            while (!dead && tiles) {
+                if (run == 0) {
+                    take();
+                    continue;
+                }
                 dead = !tc::bar_wait(qbar, qphase, limit);
                 qphase ^= 1u;
-                for (int k = 0; k < run && !dead; ++k) {
+                const int now = run;
+                for (int k = 0; k < now && !dead; ++k) {
                     tc::Ring<Y::kPairs> it = st;
 #pragma unroll
                     for (int c = 0; c < Y::kBlocks; ++c, it.next()) {
@@ -834,10 +840,12 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                         tc::mma_f16_ss(tmem, dr + ks.slot * (kBox >> 4) + 2 * i, dq + (L / 64) * (NR * 128 >> 4) + 2 * i, idS, true);
                     tc::commit(kempty + 8 * ks.slot);
                     tc::commit(sbar);
-                    if (k == run - 1)
-                        tc::commit(qempty);
                     ks.next();
-                    dead = !tc::bar_wait(wbar, wphase, limit);
+                    if (k == now - 1) {
+                        tc::commit(qempty);
+                        take();                    // the next piece, beside the softmax
+                    }
+                    dead = dead || !tc::bar_wait(wbar, wphase, limit);
                     wphase ^= 1u;
                     if (dead)
                         break;
@@ -855,8 +863,9 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                 if (!dead)
                     tc::commit(obar);
             }
-            dead = __any_sync(SFAR_FULL, dead);
         }
+        __syncwarp();
+        dead = __any_sync(SFAR_FULL, dead);
         if (tc::elect_one()) {
             if (dead)
                 sfar_record_fault(a.ctl, 0, blockIdx.x, -1, 0, SFAR_WAIT_COPY);
