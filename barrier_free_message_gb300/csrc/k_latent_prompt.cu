@@ -224,7 +224,8 @@ template <int D, int TILES>
 __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(const __grid_constant__ SfarLatentPromptArgs a)
 {
     using Y = Lay<D, TILES>;
-    constexpr int kRows = 128 * TILES, kPart = kRows * (D + 2), kThreads = Y::kThreads, kSoftWarps = Y::kSoftWarps, kCopyWarp = Y::kCopyWarp, kMmaWarp = Y::kMmaWarp;
+    constexpr int kRows = 128 * TILES, kPart = kRows * (D + 2), kThreads = Y::kThreads, kSoftWarps = Y::kSoftWarps,
+                  kCopyWarp = Y::kCopyWarp, kMmaWarp = Y::kMmaWarp;
     extern __shared__ __align__(1024) unsigned char dyn[];
     __shared__ __align__(8) unsigned long long bars[2 * Y::kSlots + 2 * kPieces + 13];
     __shared__ Piece s_piece[kPieces];
@@ -236,7 +237,8 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
     const uint32_t mem = (tc::smem(dyn) + 1023u) & ~1023u, ring = mem + Y::kQ;
     unsigned char *gen = dyn + (mem - tc::smem(dyn));
     const uint32_t full = tc::smem(bars), empty = full + 8 * Y::kSlots, pfull = empty + 8 * Y::kSlots, pempty = pfull + 8 * kPieces,
-                   qfull = pempty + 8 * kPieces, qempty = qfull + 16, sbar = qempty + 16, wbar = sbar + 16, obar = wbar + 16, look = obar + 16, clean = look + 8, drain = clean + 8;
+                   qfull = pempty + 8 * kPieces, qempty = qfull + 16, sbar = qempty + 16, wbar = sbar + 16, obar = wbar + 16, look = obar + 16,
+                   clean = look + 8, drain = clean + 8;
 
     if (warp == kCopyWarp && lane < a.R) {
         tc::prefetch_map(&a.qmap[lane]);
