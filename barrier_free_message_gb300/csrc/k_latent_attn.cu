@@ -52,6 +52,7 @@ namespace {
 constexpr int kTile = SFAR_LATENT_TILE, kGroup = SFAR_LATENT_GROUP;
 constexpr int kSoft = 4, kCopyWarp = kSoft, kMmaWarp = kSoft + 1, kQueryWarp = kSoft + 2, kThreads = 32 * (kQueryWarp + 1);
 constexpr int kBox = kTile * 128, kPair = 2 * kBox;                // bytes of 64 elements of every token, of 128
+constexpr float kLeast = -3.4028234663852886e38f;                  // the least finite number
 constexpr int kMeta = 8, kPieces = 4, kParts = 16, kKept = 64, kWhole = 8;     // kMeta: above the tiles in flight; kParts: joined at once, at most
 
 template <int L, int NR> struct Lay {
@@ -156,6 +157,9 @@ __device__ __forceinline__ void store_transposed(uint32_t addr, uint32_t a, uint
 }
 // whether one of the two bf16 is an infinity or NaN
 __device__ __forceinline__ bool odd2(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
+
+// What a row's accumulator is multiplied by: 0 if it attends to nothing, NaN if all its scores are -inf.
+__device__ __forceinline__ float factor(float ref, float sum) { return ref == kLeast ? NAN : sum == 0.f ? 0.f : 1.f / sum; }
 
 // Zeros for the rows past the last request, by a warp of each CTA.
 template <int L> __device__ __noinline__ void padding(const SfarLatentAttnArgs &a, int lane)
@@ -410,9 +414,11 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                 }
                 for (int c = 0; c < Y::kBlocks; ++c)
                     st.next();
-                // scores in units of log2
+                // Scores in units of log2; -inf: not attended to.  A score of -inf that is attended to has weight 0, too, but a
+                // row that has such scores alone is NaN: they count as the least finite number for its reference.
                 float x[4 * kI];
                 bool move = false;
+                const float least = edge ? -INFINITY : kLeast;
 #pragma unroll
                 for (int n = 0; n < 4 * kI; ++n)
                     x[n] = __uint_as_float(raw[n]) * f;
@@ -423,22 +429,26 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                         for (int y = 0; y < 2; ++y) {
                             const int hi = s_hi[8 * i + 2 * t + y];
 #pragma unroll
-                            for (int h = 0; h < 2; ++h)
+                            for (int h = 0; h < 2; ++h) {
+                                float &v = x[4 * i + 2 * h + y];
                                 if (!there[h] || j + 8 * h >= hi)
-                                    x[4 * i + 2 * h + y] = -INFINITY;
+                                    v = -INFINITY;
+                                else if (v == -INFINITY)
+                                    v = kLeast;
+                            }
                         }
                 }
 #pragma unroll
                 for (int i = 0; i < kI; ++i)
 #pragma unroll
                     for (int y = 0; y < 2; ++y)
-                        move = move || fmaxf(x[4 * i + y], x[4 * i + 2 + y]) - ref[2 * i + y] > kAttnLift;
+                        move = move || fmaxf(fmaxf(x[4 * i + y], x[4 * i + 2 + y]), least) - ref[2 * i + y] > kAttnLift;
                 if (soft_any(move)) {
 #pragma unroll
                     for (int i = 0; i < kI; ++i)
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
-                            float m = fmaxf(x[4 * i + y], x[4 * i + 2 + y]);
+                            float m = fmaxf(fmaxf(x[4 * i + y], x[4 * i + 2 + y]), least);
 #pragma unroll
                             for (int d = 4; d < 32; d <<= 1)
                                 m = fmaxf(m, __shfl_xor_sync(SFAR_FULL, m, d));
@@ -521,7 +531,7 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
             if (tid < NR) {
                 const float v = (s_max[0][tid] + s_max[1][tid]) + (s_max[2][tid] + s_max[3][tid]);
                 s_sum[tid] = v;
-                s_inv[tid] = v == 0.f ? 0.f : 1.f / v;
+                s_inv[tid] = factor(s_ref[tid], v);
             }
             soft_sync();
             if (p.run) {
@@ -603,7 +613,7 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                             s_w[c][tid] = w;
                             total += m == -INFINITY ? s_m[c][tid] : w * s_m[c][tid];        // its sum is 0 then, or NaN
                         }
-                        s_inv[tid] = total == 0.f ? 0.f : 1.f / total;
+                        s_inv[tid] = factor(top, total);
                     }
                     soft_sync();
                     float *group = slot(join.lo);
