@@ -161,6 +161,29 @@ __device__ __forceinline__ bool odd2(uint32_t w) { return (w & 0x7f80u) == 0x7f8
 // What a row's accumulator is multiplied by: 0 if it attends to nothing, NaN if all its scores are -inf.
 __device__ __forceinline__ float factor(float ref, float sum) { return ref == kLeast ? NAN : sum == 0.f ? 0.f : 1.f / sum; }
 
+// The rows whose accumulator holds an infinity or NaN, by the softmax threads: NaN for their sums, and for their results if
+// these have been written.
+template <int L, int NR> __device__ __noinline__ void odd_rows(uint32_t tO, int rows, float *sum, uint16_t *const *out)
+{
+    for (int again = 0; again < (out ? 2 : 1); ++again) {
+        for (int n0 = 0; n0 < rows; n0 += 8)
+            for (int c = 0; c < L / 128; ++c) {
+                uint32_t o[8];
+                tc::ld8(o, tO + c * NR + n0);
+                tc::wait_ld(o);
+#pragma unroll
+                for (int n = 0; n < 8; ++n)
+                    if (n0 + n < rows) {
+                        if (again == 0 && (o[n] & 0x7f800000u) == 0x7f800000u)
+                            sum[n0 + n] = NAN;
+                        if (again && isnan(sum[n0 + n]))
+                            out[n0 + n][c * 128 + threadIdx.x] = 0x7fff;
+                    }
+            }
+        soft_sync();
+    }
+}
+
 // Zeros for the rows past the last request, by a warp of each CTA.
 template <int L> __device__ __noinline__ void padding(const SfarLatentAttnArgs &a, int lane)
 {
@@ -539,6 +562,9 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                 ophase ^= 1u;
                 tc::fence_after();
             }
+            // A row that attends to a latent that is not finite is NaN.  Where the token's weight is 0, only the accumulator's
+            // element says so.
+            float odd[Y::kBlocks] = {};            // NaN: some element is not finite
             // The accumulator, element tid of each 128 of the latent, a row at a time.  begin(n): what is read once for a row.
             auto each = [&](auto begin, auto what) {
 #pragma unroll 1
@@ -565,10 +591,19 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                     for (int n = 0; n < 8; ++n)
                         if (n0 + n < rows) {
 #pragma unroll
-                            for (int c = 0; c < Y::kBlocks; ++c)
+                            for (int c = 0; c < Y::kBlocks; ++c) {
+                                odd[c] = fmaf(__uint_as_float(o[c][n]), 0.f, odd[c]);
                                 what(of[n], n0 + n, c * 128 + tid, __uint_as_float(o[c][n]));
+                            }
                         }
                 }
+            };
+            auto any_odd = [&] {
+                float all = 0.f;
+#pragma unroll
+                for (int c = 0; c < Y::kBlocks; ++c)
+                    all += odd[c];
+                return soft_any(all != 0.f);
             };
             if (p.tiles == p.all) {
                 struct Row {
@@ -577,6 +612,8 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                 };
                 each([&](int n) { return Row{s_out[n], s_inv[n]}; },
                      [&](const Row &r, int, int d, float v) { r.out[d] = (uint16_t)tc::bf16x2(v * r.by, 0.f); });
+                if (any_odd())                     // the tables in shared memory have been read
+                    odd_rows<L, NR>(tO, rows, s_sum, s_out);
             } else {
                 // a part: leave it in the workspace, for the last of the row tile's CTAs
                 const long long from = p.at - p.tile0, to = from + p.all;
@@ -585,10 +622,17 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                 auto slot = [&](int c) { return a.part + ((size_t)c * 2 + (c == c0)) * Y::kPart; };
                 float *dst = slot(blockIdx.x);
                 each([](int) { return 0; }, [&](int, int n, int d, float v) { __stcg(dst + n * L + d, v); });
-                if (tid < rows)
-                    __stcg(reinterpret_cast<float2 *>(dst + NR * L) + tid, make_float2(s_ref[tid], s_sum[tid]));
-                for (;;) {
+                auto leave = [&] {
+                    if (tid < rows)
+                        __stcg(reinterpret_cast<float2 *>(dst + NR * L) + tid, make_float2(s_ref[tid], s_sum[tid]));
+                };
+                leave();
+                if (any_odd()) {
+                    odd_rows<L, NR>(tO, rows, s_sum, nullptr);
+                    leave();
                     soft_sync();
+                }
+                for (;;) {
                     if (tid == 0)
                         s_last = join.last();
                     soft_sync();
@@ -624,10 +668,11 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                         __stcg(reinterpret_cast<float2 *>(group + NR * L) + tid, make_float2(top, total));
                     if (!join.next(a, 0))
                         break;
+                    soft_sync();
                 }
+                soft_sync();                       // the tables in shared memory have been read
             }
             tc::fence_before();                    // before the MMAs that the next weights allow
-            soft_sync();                           // the tables in shared memory have been read
             if (lane == 0)
                 tc::bar_arrive(pempty + 8 * now_at);
         }

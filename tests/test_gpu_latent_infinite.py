@@ -75,3 +75,22 @@ def test_absorbed_infinite_keys(n, value):
         rows = ref.held_rows(clean[0], table[0], n, P)
         want, off = without(heads, rows, rows[:, :L], list(gone), 0.07)
         ref.check(down, want, off, f"without {gone[:3]}..")
+
+
+@pytest.mark.parametrize("H,L", [(2, 512), (12, 256), (33, 512)])
+@pytest.mark.parametrize("n", LENGTHS)
+def test_absorbed_infinite_latents(n, H, L):
+    """A row that attends to a latent with an infinity is NaN, though that token's weight is 0 and whatever tile it is in."""
+    rot, P, count = 64, 16, min(n, 3)
+    clean, table = cached(1, L, rot, P, [n], seed=n + 2)
+    q = torch.randn(1, count, H, L + rot, generator=torch.Generator("cuda").manual_seed(3), device="cuda").to(BF)
+    q[..., 7] = -q[..., 7].abs().clamp_min(0.1)             # times +inf: a score of -inf
+    want, _, _ = attend(clean, table, [n], [count], H, rot, q=q)
+    assert torch.isfinite(want).all()
+    for at in {0, n // 2, n - 1, max(0, n - 2), max(0, n - 70)}:
+        cache = clean.clone()
+        cache[0, place(table[0], P, at)[0], place(table[0], P, at)[1], 7] = INF
+        got, _, _ = attend(cache, table, [n], [count], H, rot, q=q)
+        first = max(0, at - (n - count))                    # the first row at or past that token
+        assert torch.isnan(got[:, first:]).all(), at
+        assert torch.equal(got[:, :first], want[:, :first]), at
