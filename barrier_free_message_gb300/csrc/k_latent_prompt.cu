@@ -114,11 +114,16 @@ template <int D> __device__ __noinline__ void padding(const SfarLatentPromptArgs
         sfar_attn_padding<D>(a, lane, 32);
 }
 
+// What a row's accumulator is multiplied by.  A sum is 0 if a row attends to nothing, then so is its result, or if all its
+// scores are -inf: NaN.
+__device__ __forceinline__ float factor(float sum, bool sees) { return sum == 0.f ? sees ? NAN : 0.f : 1.f / sum; }
+
 // Joins `parts` parts, the first at p0, the others `step` floats on from it each: 8 elements of a row to a thread, rows next to
 // one another as they lie in a part, kItems of them with kBatch parts each in flight (time passes by round trips).  Into the
-// result, or into the first part; then a thread's first item's reference and sum are given back.
+// result, or into the first part; then a thread's first item's reference and sum are given back.  The first `blind` rows
+// attend to nothing.
 template <int D, int TILES, int kBatch, int kItems>
-__device__ __forceinline__ float2 join_parts(float *p0, uint32_t step, int parts, int rows, uint16_t *out, long long ots)
+__device__ __forceinline__ float2 join_parts(float *p0, uint32_t step, int parts, int rows, int blind, uint16_t *out, long long ots)
 {
     constexpr int kRows = 128 * TILES, kThreads = 256 * TILES;
     float2 kept = make_float2(-INFINITY, 0.f);
@@ -171,7 +176,7 @@ __device__ __forceinline__ float2 join_parts(float *p0, uint32_t step, int parts
             if (i0 + y * kThreads >= rows * (D / 8))
                 break;
             if (out) {
-                const float by = total[y] == 0.f ? 0.f : 1.f / total[y];
+                const float by = factor(total[y], (int)n[y] >= blind);
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -206,8 +211,9 @@ template <int D, int TILES> __device__ __noinline__ void join(const SfarLatentPr
         float *const p0 = a.part + (size_t)j.lo * kPart;
         uint16_t *const out = more ? nullptr : a.out[p.r] + (long long)(p.first + p.rt * kRows) * a.ots + (long long)p.h * a.ohs;
         const uint32_t step = (uint32_t)(j.step * kPart);
-        const float2 m = parts <= 2 ? join_parts<D, TILES, 2, 2>(p0, step, parts, rows, out, a.ots)
-                                    : join_parts<D, TILES, 4, 1>(p0, step, parts, rows, out, a.ots);
+        const int blind = p.count - p.len - p.rt * kRows;
+        const float2 m = parts <= 2 ? join_parts<D, TILES, 2, 2>(p0, step, parts, rows, blind, out, a.ots)
+                                    : join_parts<D, TILES, 4, 1>(p0, step, parts, rows, blind, out, a.ots);
         if (more) {
             asm volatile("bar.sync 9, %0;" ::"n"(kThreads) : "memory");       // the first part's references have been read
             if ((int)threadIdx.x < rows)
@@ -389,7 +395,7 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                     tc::fence_before();
                     pair_sync(pair);               // the other's has been read
                 }
-                // a row that has seen nothing: any finite reference, weights 0
+                // a row that has seen nothing, or scores of -inf alone: any finite reference, weights 0
                 const float base = ref == -INFINITY ? 0.f : ref;
                 const uint64_t b2 = tc::pack2(-base, -base);
                 uint64_t part = 0;
@@ -423,7 +429,7 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
             if (row && *(volatile const int *)&p.odd < hi + 64 * half)
                 sum = NAN;
             const bool parts = p.c0 != p.c1;
-            const float by = parts ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+            const float by = parts ? 1.f : factor(sum, pos >= 0);
             uint16_t *dst = a.out[p.r] + (long long)(p.first + min(i, p.count - 1)) * a.ots + (long long)p.h * a.ohs + D / 2 * half;
             const int rows = min(kRows, p.count - p.rt * kRows);       // of the row tile: a part's stride
             float *part = a.part + (size_t)p.part * kPart + D / 2 * half * rows + x * 128 + lrow;      // [element][row]

@@ -94,3 +94,78 @@ def test_absorbed_infinite_latents(n, H, L):
         first = max(0, at - (n - count))                    # the first row at or past that token
         assert torch.isnan(got[:, first:]).all(), at
         assert torch.equal(got[:, :first], want[:, :first]), at
+
+
+# -------------------------------------------------------------- expanded form
+def prompt_of(H, D, rot, lens, count, seed):
+    """q, k, v, kr of contexts `lens` whose last `count` are new, and a call that gives the results."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    S, T = sum(lens), sum(count)
+    q, k, v, kr = [torch.randn(s, generator=g, device="cuda").to(BF) for s in ((1, T, H, D + rot), (1, S, H, D), (1, S, H, D), (1, S, rot))]
+
+    def run(q, k, v, kr, max_q):
+        out = torch.full((1, T, H, D), 7.0, dtype=BF, device="cuda")
+        kv = sfar.SfarLatent(torch.zeros(1, 1, 16, 256 + rot, dtype=BF, device="cuda"), q_heads=H, rope_dim=rot)
+        kv.prompt(q, k, v, kr, out, ints(ref.offsets(count)), ints(ref.offsets(lens)), max_q=max_q, scale=0.09)
+        torch.cuda.synchronize()
+        assert kv.status()[0] == sfar.SFAR_OK
+        kv.close()
+        return out
+    return q, k, v, kr, run
+
+
+# contexts and new tokens: one step and less, whole steps ahead, row tiles in one part and in many, two tiles at a time
+PROMPTS = [([1], [1], 2), ([5], [3], 2), ([63], [63], 2), ([64], [2], 2), ([200], [131], 3), ([300], [300], 2), ([1500], [20], 2), ([2200], [300], 9),
+           ([9000], [1], 2), ([700, 400], [400, 300], 40)]
+
+
+@pytest.mark.parametrize("D,rot", [(128, 64), (64, 32)])
+@pytest.mark.parametrize("lens,count,H", PROMPTS)
+def test_expanded_infinite_query(lens, count, H, D, rot):
+    """Such a row is NaN whatever the sign of its scores; the others are as they were."""
+    q, k, v, kr, run = prompt_of(H, D, rot, lens, count, seed=sum(lens))
+    k[..., 3] = -k[..., 3].abs().clamp_min(0.01)
+    kr[..., 5] = kr[..., 5].abs().clamp_min(0.01)
+    for max_q in {max(count), 1000}:
+        clean = run(q, k, v, kr, max_q)
+        assert torch.isfinite(clean).all()
+        for value in (INF, -INF, float("nan")):
+            bad = q.clone()
+            bad[0, 0, 1, 3] = value
+            bad[0, -1, 0, D + 5] = value
+            got = run(bad, k, v, kr, max_q)
+            assert torch.isnan(got[0, 0, 1]).all() and torch.isnan(got[0, -1, 0]).all(), value
+            got[0, 0, 1], got[0, -1, 0] = clean[0, 0, 1], clean[0, -1, 0]
+            assert torch.equal(got, clean)
+
+
+@pytest.mark.parametrize("value", [INF, -INF, torch.finfo(BF).min])
+@pytest.mark.parametrize("n,count", [(1, 1), (5, 1), (63, 1), (64, 1), (200, 1), (200, 100), (1500, 1), (1500, 140), (9000, 3)])
+def test_expanded_infinite_keys(n, count, value):
+    """A key, or rotated key, with an infinity, or so large that its products pass binary32: rows for which that is +inf are
+    NaN, the others leave the token out, wherever it lies."""
+    D, rot, H = 128, 64, 2
+    q, k, v, kr, run = prompt_of(H, D, rot, [n], [count], seed=n)
+    q[:, :, 0, D + 9], q[:, :, 1, D + 9] = 40.0, -40.0
+    q[:, :, 0, 9], q[:, :, 1, 9] = 40.0, -40.0
+    for gone in {(0,), (n - 1,), (n // 2,), tuple(range(min(n, 64))), tuple(range(min(n, 130))), tuple(range(max(0, n - 140), n)), tuple(range(n))}:
+        at = torch.tensor(gone, device="cuda")
+        for rotated in (True, False):
+            bad, bad_r = k.clone(), kr.clone()
+            if rotated:
+                bad_r[0, at, 9] = value
+            else:
+                bad[0, at, :, 9] = value
+            got = run(q, bad, v, bad_r, count)
+            seen = ref.causal(count, n, "cuda")
+            kept = seen.clone()
+            kept[:, at] = False
+            up = 0 if value > 0 else 1
+            if math.isinf(value):
+                assert torch.isnan(got[0, seen[:, at].any(1), up]).all(), gone
+                assert torch.isnan(got[0, ~kept.any(1), 1 - up]).all(), gone
+            some = kept.any(1)
+            keys = torch.cat([k[0, :, 1 - up], kr[0]], -1)
+            if some.any():
+                want, off = ref.rows(q[0, :, 1 - up], keys, v[0, :, 1 - up], kept, 0.09)
+                ref.check(got[0, some, 1 - up], want[some], off[some], f"without {gone[:3]}..")
