@@ -61,7 +61,7 @@ struct Piece {
     int steps[2];               // of this piece, the tiles of the context that each tile of rows attends to
     int from;                   // the first tile of the piece
     int part, c0, c1;           // this part of the row tile, its first and its last
-    int odd;                    // the first context token that is not finite, of those that were looked at
+    int odd;                    // the first context token with a value that is not finite, of those that were looked at
 };
 
 // The two warps that share 32 rows.
@@ -82,6 +82,11 @@ __device__ __forceinline__ uint32_t times0(uint32_t w, uint32_t sum)
     return r;
 }
 __device__ __forceinline__ bool odd2(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
+// the same with zeros in place of infinities and NaN
+__device__ __forceinline__ uint32_t finite2(uint32_t w)
+{
+    return w & ((w & 0x7f80u) == 0x7f80u ? 0xffff0000u : ~0u) & ((w & 0x7f800000u) == 0x7f800000u ? 0xffffu : ~0u);
+}
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float r;
@@ -107,6 +112,26 @@ __device__ __forceinline__ bool request(const SfarLatentPromptArgs &a, int b, Re
 // Every row of the piece sees the tokens before all_see; its first whole_steps steps have no others.
 __device__ __forceinline__ int all_see(const Piece &p, int rows) { return min(p.len, p.len - p.count + p.rt * rows + 1); }
 __device__ __forceinline__ int whole_steps(const Piece &p, int rows) { return max(0, max(0, all_see(p, rows)) / kTile - p.from); }
+
+// Infinities and NaN of `tokens` values from v on that the products had zeros for, into `dim` elements of a row's result, or of
+// its part (`rows` floats from one to the next).
+__device__ __noinline__ void add_odd(const uint16_t *v, long long vts, int tokens, int dim, uint16_t *out, float *part, int rows)
+{
+    for (int d = 0; d < dim; ++d) {
+        float sum = 0.f;
+        for (int j = 0; j < tokens; ++j) {
+            const uint32_t w = v[j * vts + d];
+            if ((w & 0x7f80u) == 0x7f80u)
+                sum += __uint_as_float(w << 16);
+        }
+        if (sum == 0.f)
+            continue;
+        if (part)
+            __stcg(part + d * rows, __ldcg(part + d * rows) + sum);
+        else
+            out[d] = (uint16_t)tc::bf16x2(__uint_as_float((uint32_t)out[d] << 16) + sum, 0.f);
+    }
+}
 
 template <int D> __device__ __noinline__ void padding(const SfarLatentPromptArgs &a, int lane)
 {
@@ -426,8 +451,6 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                 ophase ^= 1u;
                 tc::fence_after();
             }
-            if (row && *(volatile const int *)&p.odd < hi + 64 * half)
-                sum = NAN;
             const bool parts = p.c0 != p.c1;
             const float by = parts ? 1.f : factor(sum, pos >= 0);
             uint16_t *dst = a.out[p.r] + (long long)(p.first + min(i, p.count - 1)) * a.ots + (long long)p.h * a.ohs + D / 2 * half;
@@ -457,6 +480,10 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                 if (row)
                     tc::st32(dst + c, y);
             }
+            const int odd = *(volatile const int *)&p.odd;
+            if (row && odd <= pos)
+                add_odd(a.v[p.r] + (long long)(p.kfirst + odd) * a.vts + (long long)p.h * a.vhs + D / 2 * half, a.vts,
+                        min(pos + 1, (p.from + steps) * kTile) - odd, D / 2, dst, parts ? part : nullptr, rows);
             if (parts) {
                 if (row && half == 0)
                     __stcg(reinterpret_cast<float2 *>(a.part + (size_t)p.part * kPart + kRows * D) + x * 128 + lrow, make_float2(ref, sum));
@@ -754,9 +781,9 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
             }
         } else {
             // -------------------------------------------------------- values
-            // Values of tokens that not every row of the piece sees: 64 with an infinity or NaN among them become zeros (0 times
-            // it would reach the rows that do not see it), and the rows that do see the token become NaN at the end.  A warp to
-            // each box of a step; it has the time that the softmax takes.
+            // Values of tokens that not every row of the piece sees: infinities and NaN become zeros (0 times them would reach
+            // the rows that do not see them), and are added to the results of the rows that do see the token at the end.  A
+            // warp to each box of a step; it has the time that the softmax takes.
             const int c = warp - kMmaWarp - 1;
             tc::Ring<kPieces> ps;
             uint32_t slot = 0, phase = 0;
@@ -791,8 +818,10 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                             if (j < p.len)
                                 atomicMin(&p.odd, j);
 #pragma unroll 1
-                            for (int e = 0; e < 8; ++e)
-                                *reinterpret_cast<uint4 *>(v + row * 128 + (e << 4)) = make_uint4(0, 0, 0, 0);
+                            for (int e = 0; e < 8; ++e) {
+                                uint4 &w = *reinterpret_cast<uint4 *>(v + row * 128 + (e << 4));
+                                w = make_uint4(finite2(w.x), finite2(w.y), finite2(w.z), finite2(w.w));
+                            }
                         }
                     }
                     tc::fence_async();

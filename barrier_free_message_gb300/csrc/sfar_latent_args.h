@@ -61,6 +61,7 @@ struct SfarLatentPromptArgs {
     // per rank, 3-D tensor maps: numbers of a head (innermost) by heads by tokens, boxes of 64 numbers of one head of 128 tokens,
     // 128-byte swizzle, zeros outside; kr 2-D
     CUtensorMap qmap[SFAR_MAX_R], kmap[SFAR_MAX_R], vmap[SFAR_MAX_R], krmap[SFAR_MAX_R];
+    const uint16_t *v[SFAR_MAX_R];          // values that are not finite are read again
     uint16_t *out[SFAR_MAX_R];
     const int *starts, *kstarts;
     unsigned *next;                         // counter of row tiles taken; 0 between calls
@@ -68,7 +69,7 @@ struct SfarLatentPromptArgs {
     int *arrived;                           // [3][arrived_stride] counters of parts (SfarJoin); 0 between calls
     int arrived_stride;
     SfarCtl *ctl;
-    long long ots, ohs;
+    long long vts, vhs, ots, ohs;
     float scale;
     int R, B, T, S, Hq, rope;               // T, S: rows of q, of k
     int most;                               // row tiles of all requests, at most

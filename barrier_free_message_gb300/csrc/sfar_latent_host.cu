@@ -506,6 +506,7 @@ sfar_status sfar_latent_prompt(sfar_latent_t *h, const void *const q[], const vo
     for (int r = 0; r < h->R; ++r) {
         if (!aligned(q[r], 16) || !aligned(out[r], 16) || (S && (!aligned(k[r], 16) || !aligned(v[r], 16) || !aligned(kr[r], 16))))
             return SFAR_ERR_INVALID;
+        a.v[r] = S ? static_cast<const uint16_t *>(v[r]) : nullptr;
         a.out[r] = static_cast<uint16_t *>(out[r]);
     }
     for (int i = 0; i < h->R; ++i) {
@@ -541,6 +542,8 @@ sfar_status sfar_latent_prompt(sfar_latent_t *h, const void *const q[], const vo
     a.arrived = h->arrived;
     a.arrived_stride = (int)counter_stride(h->sms);
     a.ctl = h->ctl;
+    a.vts = (long long)v_token_stride;
+    a.vhs = (long long)v_head_stride;
     a.ots = (long long)out_token_stride;
     a.ohs = (long long)out_head_stride;
     a.scale = scale;

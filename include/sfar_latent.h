@@ -130,7 +130,9 @@ sfar_status sfar_latent_attention(sfar_latent_t *h, const void *const q[], void 
  * of them: row starts[b] + i stands at position p = (rows of the context) -
  * (new tokens) + i and attends to context rows j <= p, with score
  * scale * (q[:head_dim] . k_j + q[head_dim:] . kr_j).  Softmax, numbers, rows
- * of nothing and rows past starts[requests] as in sfar_latent_attention; a
+ * of nothing, infinite scores and rows past starts[requests] as in
+ * sfar_latent_attention; a value that is not finite leaves the rows that attend
+ * to it an infinity or NaN in its own element and nothing in the others.  A
  * scale below 2^-123 counts as about that.  All
  * bf16, strides in elements, multiples of 8 and below 2^39 (those of q, k, v
  * and kr above 0 for a dimension of more than one entry), pointers 16-byte

@@ -169,3 +169,32 @@ def test_expanded_infinite_keys(n, count, value):
             if some.any():
                 want, off = ref.rows(q[0, :, 1 - up], keys, v[0, :, 1 - up], kept, 0.09)
                 ref.check(got[0, some, 1 - up], want[some], off[some], f"without {gone[:3]}..")
+
+
+@pytest.mark.parametrize("D,rot", [(128, 64), (64, 32)])
+@pytest.mark.parametrize("lens,count,H", PROMPTS)
+def test_expanded_infinite_values(lens, count, H, D, rot):
+    """An infinite value is one in its own element of the rows that attend to it, whatever tile it is in."""
+    q, k, v, kr, run = prompt_of(H, D, rot, lens, count, seed=sum(lens) + 1)
+    n, m, h = lens[0], count[0], H - 1
+    clean = {max_q: run(q, k, v, kr, max_q) for max_q in {max(count), 1000}}
+    for i, at in enumerate(sorted({0, n // 2, n - m, n - m // 2 - 1, n - 1, max(0, n - 129)})):
+        bad, values = v.clone(), [(D - 1, INF), (3, -INF), (D // 2, float("nan"))]
+        for d, value in values:
+            bad[0, at, h, d] = value
+        if at:
+            bad[0, at - 1, h, 3] = INF                      # of both signs: NaN where a row attends to both
+        for max_q, before in clean.items():
+            got = run(q, k, bad, kr, max_q)
+            first, lone = max(0, at - (n - m)), bool(at) and at - 1 >= n - m       # lone: a row that attends to at - 1 only
+            for d, value in values:
+                mine = got[0, first:m, h, d]
+                want = float("nan") if math.isnan(value) or (d == 3 and at) else value
+                assert (mine.isnan() if math.isnan(want) else mine == want).all(), (at, d, max_q)
+            if lone:
+                assert (got[0, first - 1, h, 3] == INF).all(), (at, max_q)
+            rest = torch.ones_like(got, dtype=torch.bool)
+            rest[0, first:m, h, [d for d, _ in values]] = False
+            if at:
+                rest[0, max(0, first - 1):m, h, 3] = False
+            assert torch.equal(got[rest], before[rest]), (at, max_q)
