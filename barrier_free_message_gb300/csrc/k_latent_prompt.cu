@@ -75,6 +75,17 @@ __device__ __forceinline__ bool pair_any(int pair, bool v)
                  : "memory");
     return r != 0;
 }
+// All the softmax warps.
+template <int TILES> __device__ __forceinline__ void all_sync() { asm volatile("bar.sync 9, %0;" ::"n"(256 * TILES) : "memory"); }
+template <int TILES> __device__ __forceinline__ bool all_any(bool v)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, 9, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"((uint32_t)v), "n"(256 * TILES)
+                 : "memory");
+    return r != 0;
+}
 __device__ __forceinline__ uint32_t times0(uint32_t w, uint32_t sum)
 {
     uint32_t r;
@@ -221,14 +232,14 @@ __device__ __forceinline__ float2 join_parts(float *p0, uint32_t step, int parts
 // All softmax threads, after their parts: joins the row tile's parts if this CTA is the last of them.
 template <int D, int TILES> __device__ __noinline__ void join(const SfarLatentPromptArgs &a, const Piece &p, int *s_last)
 {
-    constexpr int kRows = 128 * TILES, kThreads = 256 * TILES, kPart = kRows * (D + 2);
+    constexpr int kRows = 128 * TILES, kPart = kRows * (D + 2);
     const int rows = min(kRows, p.count - p.rt * kRows);
     SfarJoin j(a, 0, p.c0, p.c1, p.part);
     for (;;) {
-        asm volatile("bar.sync 9, %0;" ::"n"(kThreads) : "memory");
+        all_sync<TILES>();
         if (threadIdx.x == 0)
             *s_last = j.last();
-        asm volatile("bar.sync 9, %0;" ::"n"(kThreads) : "memory");
+        all_sync<TILES>();
         if (!*s_last)
             return;
         const int parts = (j.hi - j.lo) / j.step + 1;
@@ -240,7 +251,7 @@ template <int D, int TILES> __device__ __noinline__ void join(const SfarLatentPr
         const float2 m = parts <= 2 ? join_parts<D, TILES, 2, 2>(p0, step, parts, rows, blind, out, a.ots)
                                     : join_parts<D, TILES, 4, 1>(p0, step, parts, rows, blind, out, a.ots);
         if (more) {
-            asm volatile("bar.sync 9, %0;" ::"n"(kThreads) : "memory");       // the first part's references have been read
+            all_sync<TILES>();                     // the first part's references have been read
             if ((int)threadIdx.x < rows)
                 __stcg(reinterpret_cast<float2 *>(p0 + kRows * D) + threadIdx.x, m);
         }
@@ -358,7 +369,8 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
         uint32_t sphase = 0, ophase = 0;
         for (;;) {
             dead = dead || !tc::bar_wait(pfull + 8 * ps.slot, ps.phase, limit);
-            dead = pair_any(pair, dead);
+            // Those that speak to one another leave together: two warps, or where row tiles are cut all of them (join()).
+            dead = cuts > 1 ? all_any<TILES>(dead) : pair_any(pair, dead);
             if (dead)
                 break;
             const Piece &p = s_piece[ps.slot];
