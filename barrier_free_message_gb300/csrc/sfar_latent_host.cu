@@ -324,8 +324,16 @@ sfar_status sfar_latent_append(sfar_latent_t *h, const void *const x[], const vo
         return SFAR_ERR_INVALID;
     SfarLatentAppendArgs a;
     memset(&a, 0, sizeof a);
+    const size_t bytes = 2 * ((tokens - 1) * token_stride + row), cached = (h->pages << h->shift) * row * 2;
     for (int r = 0; r < h->R; ++r) {
         if (!aligned(x[r], 16))
+            return SFAR_ERR_INVALID;
+        const Span cache(h->cache[r], cached);
+        for (int j = 0; j < h->R; ++j)
+            if (cache.meets(Span(x[j], bytes)))
+                return SFAR_ERR_INVALID;
+        if (cache.meets(Span(weight, 2 * (size_t)h->L)) || cache.meets(Span(pos, 4 * tokens)) || cache.meets(Span(slots, 4 * tokens)) ||
+            cache.meets(Span(freq, 2 * (size_t)h->rope)))
             return SFAR_ERR_INVALID;
         a.x[r] = static_cast<const uint16_t *>(x[r]);
         a.cache[r] = static_cast<uint16_t *>(h->cache[r]);

@@ -64,7 +64,8 @@ sfar_status sfar_latent_plan(sfar_latent_t *h, const int32_t *lens, const int32_
  * whose position is negative is left out; the slots of a call are distinct.
  * weight: [latent_dim] bf16.  Pointers 16-byte aligned (pos, freq, slots 4),
  * token_stride a multiple of 8, at least a row (with more than one token) and
- * below 2^39; tokens < 2^31; eps >= 0, scale finite.
+ * below 2^39; tokens < 2^31; eps >= 0, scale finite.  Nothing overlaps the
+ * caches.
  */
 sfar_status sfar_latent_append(sfar_latent_t *h, const void *const x[], const void *weight, const int32_t *pos,
                                const float *freq, const int32_t *slots, size_t tokens, size_t token_stride, float eps,
