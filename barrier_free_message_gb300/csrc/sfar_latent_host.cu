@@ -43,16 +43,25 @@ size_t counter_bytes(int sms) { return (3 * counter_stride(sms) + 1) * sizeof(in
 // A tensor [tokens][heads][numbers] in memory, in bytes; strides of dimensions of one entry do not count.
 struct Rows {
     uintptr_t p;
-    size_t ts, ext, tokens;             // stride of a token, what lies between its first and last byte
+    size_t ts, hs, row, ext, tokens, heads;     // ext: what lies between a token's first and last byte
     size_t whole;                       // from the first byte to past the last
     Rows(const void *ptr, size_t tokens, size_t heads, size_t row, size_t ts, size_t hs)
-        : p((uintptr_t)ptr), ts(ts), ext((heads - 1) * hs + row), tokens(tokens), whole((tokens - 1) * ts + ext)
+        : p((uintptr_t)ptr), ts(ts), hs(hs), row(row), ext((heads - 1) * hs + row), tokens(tokens), heads(heads), whole((tokens - 1) * ts + ext)
     {
     }
+    bool every(size_t m) const { return (tokens == 1 || ts % m == 0) && (heads == 1 || hs % m == 0); }
     bool meets(const Rows &o) const
     {
         if (p >= o.p + o.whole || o.p >= p + whole)
             return false;
+        // Slices of one tensor's last dimension: rows at places of one period that all strides are multiples of, where those
+        // of the one lie beside those of the other.
+        for (size_t m : {tokens > 1 ? ts : 0, heads > 1 ? hs : 0})
+            if (m && every(m) && o.every(m)) {
+                const size_t d = (o.p % m + m - p % m) % m;
+                if (d >= row && d + o.row <= m)
+                    return false;
+            }
         // beside one another in rows of one length
         if (tokens > 1 && o.tokens > 1 && ts == o.ts && ext <= ts && o.ext <= ts) {
             const size_t d = (o.p >= p ? o.p - p : ts - (p - o.p) % ts) % ts;

@@ -62,3 +62,66 @@ def test_gather_of_requests_without_rows(B, held):
                 assert torch.equal(out[r, starts[b]:starts[b + 1]], ref.held_rows(cache[r], table[b].tolist(), m, P))
         assert (out[:, starts[-1]:] == 5).all()
     kv.close()
+
+
+def beside(layout, shape, widths, g):
+    """Tensors of these widths beside one another in the last dimension of one tensor, a gap of 8 between them."""
+    R, T, H = shape
+    wide = torch.randn(R, *((T, H) if layout == "tokens outside" else (H, T)), sum(widths) + 8 * len(widths), generator=g, device="cuda").to(BF)
+    out, at = [], 0
+    for w in widths:
+        x = wide[..., at:at + w]
+        out.append(x if layout == "tokens outside" else x.transpose(1, 2))
+        at += w + 8
+    return wide, out
+
+
+@pytest.mark.parametrize("layout", ["tokens outside", "heads outside"])
+@pytest.mark.parametrize("T,H", [(1, 1), (1, 3), (5, 1), (5, 3)])
+def test_results_beside_their_inputs(layout, T, H):
+    """Slices of one tensor's last dimension do not meet: the results of slices are those of tensors of their own."""
+    g, rot = gen(T + H), 32
+    freq, pos = sfar.rope_frequencies(rot)[0], ints(list(range(T)))
+    h = sfar.Sfar(2, 1 << 16, "bf16")
+    for first in (0, 1):                                    # the output before the input, and after it
+        wide, xs = beside(layout, (2, T, H), [rot, rot], g)
+        before, own = wide.clone(), torch.empty(2, T, H, rot, dtype=BF, device="cuda")
+        h.rope(xs[first].clone(), own, pos, freq)
+        h.rope(xs[first], xs[1 - first], pos, freq)
+        torch.cuda.synchronize()
+        assert torch.equal(xs[1 - first], own) and torch.equal(xs[first].clone(), before[..., 40 * first:40 * first + rot] if
+                                                               layout == "tokens outside" else before[..., 40 * first:40 * first + rot].transpose(1, 2))
+    L, D = 256, 64
+    cache = torch.randn(2, 4, 16, L + rot, generator=g, device="cuda").to(BF)
+    kv = sfar.SfarLatent(cache, q_heads=H, rope_dim=rot)
+    table, lens, starts = ints([[2, 0, 3, 1]]), ints([50]), ints([0, T])
+    for order in (0, 1):
+        _, xs = beside(layout, (2, T, H), [L + rot, L] if order else [L, L + rot], g)
+        out, q = xs if not order else xs[::-1]
+        own = torch.empty(2, T, H, L, dtype=BF, device="cuda")
+        kv.attention(q.clone(), own, table, lens, starts, max_q=T, scale=0.07)
+        kv.attention(q, out, table, lens, starts, max_q=T, scale=0.07)
+        torch.cuda.synchronize()
+        assert torch.equal(out, own)
+        _, (k, out, q, v) = beside(layout, (2, T, H), [D, D, D + rot, D], g)
+        kr, own = cache[:, 0, :T, L:], torch.empty(2, T, H, D, dtype=BF, device="cuda")
+        kv.prompt(q.clone(), k.clone(), v.clone(), kr, own, starts, starts, max_q=T)
+        kv.prompt(q, k, v, kr, out, starts, starts, max_q=T)
+        torch.cuda.synchronize()
+        assert torch.equal(out, own)
+    fine(kv)
+    # by 8 numbers too near, or of a period that the other's rows do not keep
+    wide = torch.zeros(2, T, H, L + L + rot, dtype=BF, device="cuda")
+    if layout == "heads outside":
+        wide = torch.zeros(2, H, T, L + L + rot, dtype=BF, device="cuda").transpose(1, 2)
+    with pytest.raises(sfar.SfarError):
+        kv.attention(wide[..., :L + rot], wide[..., L + rot - 8:-8], table, lens, starts, max_q=T, scale=0.07)
+    with pytest.raises(sfar.SfarError):
+        h.rope(wide[..., :rot], wide[..., rot - 8:2 * rot - 8], pos, freq)
+    if T * H > 1:
+        flat = torch.zeros(2 * 4096, dtype=BF, device="cuda")
+        a, b = [flat[at:].as_strided((2, T, H, rot), (4096, H * step, step, 1)) for at, step in ((0, 64), (32, 80))]
+        with pytest.raises(sfar.SfarError):
+            h.rope(a, b, pos, freq)
+    kv.close()
+    h.close()
