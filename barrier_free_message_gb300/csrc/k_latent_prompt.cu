@@ -61,7 +61,6 @@ struct Piece {
     int steps[2];               // of this piece, the tiles of the context that each tile of rows attends to
     int from;                   // the first tile of the piece
     int part, c0, c1;           // this part of the row tile, its first and its last
-    int odd;                    // the first context token with a value that is not finite, of those that were looked at
 };
 
 // The two warps that share 32 rows.
@@ -124,23 +123,46 @@ __device__ __forceinline__ bool request(const SfarLatentPromptArgs &a, int b, Re
 __device__ __forceinline__ int all_see(const Piece &p, int rows) { return min(p.len, p.len - p.count + p.rt * rows + 1); }
 __device__ __forceinline__ int whole_steps(const Piece &p, int rows) { return max(0, max(0, all_see(p, rows)) / kTile - p.from); }
 
-// Infinities and NaN of `tokens` values from v on that the products had zeros for, into `dim` elements of a row's result, or of
-// its part (`rows` floats from one to the next).
-__device__ __noinline__ void add_odd(const uint16_t *v, long long vts, int tokens, int dim, uint16_t *out, float *part, int rows)
+// the lowest n bits, n > 0
+__device__ __forceinline__ uint32_t low_bits(int n) { return n < 32 ? (1u << n) - 1 : ~0u; }
+// Infinities and NaN of values that the products had zeros for, into `dim` elements of a row's result, or of its part (`rows`
+// floats from one to the next).  odd: a bit for each of the `tokens` that the row attends to of those from v on, set if it has
+// such a value.
+__device__ __noinline__ void add_odd(const uint32_t *odd, int tokens, const uint16_t *v, long long vts, int dim, uint16_t *out, float *part, int rows)
 {
-    for (int d = 0; d < dim; ++d) {
-        float sum = 0.f;
-        for (int j = 0; j < tokens; ++j) {
-            const uint32_t w = v[j * vts + d];
-            if ((w & 0x7f80u) == 0x7f80u)
-                sum += __uint_as_float(w << 16);
+    for (int d = 0; d < dim; d += 8) {
+        float sum[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            sum[e] = -0.f;                         // adds nothing, to -0 either
+        bool open = true;                          // some element is not NaN yet
+        for (int at = 0; open && at < tokens; at += 32)
+            for (uint32_t m = odd[at >> 5] & low_bits(tokens - at); open && m; m &= m - 1) {
+                const uint4 x = ld_nc_v4(v + (at + __ffs(m) - 1) * vts + d);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                open = false;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t one = e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16;
+                    if ((one & 0x7f800000u) == 0x7f800000u)
+                        sum[e] += __uint_as_float(one);
+                    open = open || !isnan(sum[e]);
+                }
+            }
+        if (part) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (sum[e] != 0.f)
+                    __stcg(part + (d + e) * rows, __ldcg(part + (d + e) * rows) + sum[e]);
+        } else {
+            uint4 x = *reinterpret_cast<const uint4 *>(out + d);
+            auto plus = [](uint32_t &w, float l, float h) { w = tc::bf16x2(__uint_as_float(w << 16) + l, __uint_as_float(w & 0xffff0000u) + h); };
+            plus(x.x, sum[0], sum[1]);
+            plus(x.y, sum[2], sum[3]);
+            plus(x.z, sum[4], sum[5]);
+            plus(x.w, sum[6], sum[7]);
+            st_v4(out + d, x);
         }
-        if (sum == 0.f)
-            continue;
-        if (part)
-            __stcg(part + d * rows, __ldcg(part + d * rows) + sum);
-        else
-            out[d] = (uint16_t)tc::bf16x2(__uint_as_float((uint32_t)out[d] << 16) + sum, 0.f);
     }
 }
 
@@ -271,10 +293,10 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
     extern __shared__ __align__(1024) unsigned char dyn[];
     __shared__ __align__(8) unsigned long long bars[2 * Y::kSlots + 2 * kPieces + 13];
     __shared__ Piece s_piece[kPieces];
+    __shared__ __align__(16) uint32_t s_odd[kPieces][Y::kV][(TILES + 1) * kTile / 32];     // tokens with values that are not finite, of each box
     __shared__ __align__(16) uint32_t upto[SFAR_KV_MAX_REQUESTS / kGroup + 4];
     Request *const kept = reinterpret_cast<Request *>(upto + 4);    // of up to kKept requests (two sums), read once
     __shared__ uint32_t s_warp[kThreads / 32], s_tmem;
-    __shared__ int s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t mem = (tc::smem(dyn) + 1023u) & ~1023u, ring = mem + Y::kQ;
     unsigned char *gen = dyn + (mem - tc::smem(dyn));
@@ -295,6 +317,8 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
         tc::fence_async();
         upto[0] = 0;
     }
+    for (int i = tid; i < kPieces * Y::kV * (TILES + 1) * kTile / 32; i += kThreads)
+        (&s_odd[0][0][0])[i] = 0;
     if (warp == kMmaWarp)
         tc::tmem_alloc<1>(tc::smem(&s_tmem), 256 * TILES);
     pdl_wait();
@@ -492,14 +516,24 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                 if (row)
                     tc::st32(dst + c, y);
             }
-            const int odd = *(volatile const int *)&p.odd;
-            if (row && odd <= pos)
-                add_odd(a.v[p.r] + (long long)(p.kfirst + odd) * a.vts + (long long)p.h * a.vhs + D / 2 * half, a.vts,
-                        min(pos + 1, (p.from + steps) * kTile) - odd, D / 2, dst, parts ? part : nullptr, rows);
+            if (row) {
+                const int from = p.from + whole_steps(p, kRows);       // where the values have been looked at
+                const int tokens = min(pos + 1, (p.from + steps) * kTile) - from * kTile;
+                const uint32_t *odd = s_odd[ps.slot][D == 128 ? half : 0];
+                uint32_t any = 0;                  // of steps that were not looked at, an earlier piece's
+#pragma unroll
+                for (int i = 0; i <= TILES; ++i) {
+                    const uint4 w = reinterpret_cast<const uint4 *>(odd)[i];
+                    any |= w.x | w.y | w.z | w.w;
+                }
+                if (any)
+                    add_odd(odd, tokens, a.v[p.r] + (p.kfirst + (long long)from * kTile) * a.vts + (long long)p.h * a.vhs + D / 2 * half, a.vts,
+                            D / 2, dst, parts ? part : nullptr, rows);
+            }
             if (parts) {
                 if (row && half == 0)
                     __stcg(reinterpret_cast<float2 *>(a.part + (size_t)p.part * kPart + kRows * D) + x * 128 + lrow, make_float2(ref, sum));
-                join<D, TILES>(a, p, &s_last);
+                join<D, TILES>(a, p, reinterpret_cast<int *>(s_warp));
             }
             tc::fence_before();
             __syncwarp();
@@ -526,7 +560,6 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
             auto piece = [&](uint32_t taken) {
                 Piece p;
                 p.b = -1;
-                p.odd = INT_MAX;
                 p.steps[0] = p.steps[1] = 0;
                 if (taken >= items)
                     return p;
@@ -804,9 +837,9 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                 dead = !__all_sync(SFAR_FULL, tc::bar_wait(pfull + 8 * ps.slot, ps.phase, limit));
                 if (dead || s_piece[ps.slot].b < 0)
                     break;
-                Piece &p = s_piece[ps.slot];
-                const int most = max(p.steps[0], p.steps[1]), all_to = all_see(p, kRows);
-                for (int k = whole_steps(p, kRows); k < most && !dead; ++k) {
+                const Piece &p = s_piece[ps.slot];
+                const int most = max(p.steps[0], p.steps[1]), all_to = all_see(p, kRows), whole = whole_steps(p, kRows);
+                for (int k = whole; k < most && !dead; ++k) {
                     const uint32_t at = slot + k * (Y::kK + Y::kV) + Y::kK + c;
                     dead = !__all_sync(SFAR_FULL, tc::bar_wait(look, phase, limit) && tc::bar_wait(full + 8 * (at % Y::kSlots), at / Y::kSlots & 1u, limit));
                     phase ^= 1u;
@@ -826,15 +859,17 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                             sum[3] = times0(w.w, sum[3]);
                         }
                         const int j = (p.from + k) * kTile + row;
-                        if (j >= all_to && odd2(sum[0] | sum[1] | sum[2] | sum[3])) {
-                            if (j < p.len)
-                                atomicMin(&p.odd, j);
+                        const bool found = j >= all_to && odd2(sum[0] | sum[1] | sum[2] | sum[3]);
+                        if (found) {
 #pragma unroll 1
                             for (int e = 0; e < 8; ++e) {
                                 uint4 &w = *reinterpret_cast<uint4 *>(v + row * 128 + (e << 4));
                                 w = make_uint4(finite2(w.x), finite2(w.y), finite2(w.z), finite2(w.w));
                             }
                         }
+                        const uint32_t bits = __ballot_sync(SFAR_FULL, found);
+                        if (lane == 0)
+                            s_odd[ps.slot][c][((k - whole) * kTile + row) >> 5] = bits;
                     }
                     tc::fence_async();
                     __syncwarp();
