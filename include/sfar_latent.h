@@ -60,9 +60,10 @@ sfar_status sfar_latent_plan(sfar_latent_t *h, const int32_t *lens, const int32_
  *   kr  = k turned by pos[t] as sfar_rope does (freq: [rope_dim / 2]
  *         binary32, layout, scale),
  * in binary32 (a row whose sum of squares passes its range has zeros for its
- * finite latents), rounded once to bf16, to slots[t].  A token whose slot is -1 or
- * whose position is negative is left out; the slots of a call are distinct.
- * weight: [latent_dim] bf16.  Pointers 16-byte aligned (pos, freq, slots 4),
+ * finite latents; squares below it are 0, so that with eps = 0 a row of numbers
+ * below 2^-75 has infinities or NaN), rounded once to bf16, to slots[t].  A
+ * token whose slot is -1 or whose position is negative is left out; the slots
+ * of a call are distinct.  weight: [latent_dim] bf16.  Pointers 16-byte aligned (pos, freq, slots 4),
  * token_stride a multiple of 8, at least a row (with more than one token) and
  * below 2^39; tokens < 2^31; eps >= 0, scale finite.  Nothing overlaps the
  * caches.

@@ -125,3 +125,87 @@ def test_results_beside_their_inputs(layout, T, H):
             h.rope(a, b, pos, freq)
     kv.close()
     h.close()
+
+
+def test_sixteen_ranks():
+    R, H, L, rot, D, P, n, count = 16, 2, 256, 32, 64, 16, 70, 40
+    g = gen(0)
+    cache = torch.full((R, 6, P, L + rot), float("nan"), dtype=BF, device="cuda")
+    kv, h = sfar.SfarLatent(cache, q_heads=H, rope_dim=rot), sfar.Sfar(R, 1 << 16, "bf16")
+    new = lambda *s: torch.randn(R, *s, generator=g, device="cuda").to(BF)                # noqa: E731
+    pages = [4, 1, 5, 0, 2]
+    table, pos = ints([pages]), ints(list(range(n)))
+    slots = ints([pages[i // P] * P + i % P for i in range(n)])
+    freq, weight = sfar.rope_frequencies(rot)[0], torch.ones(L, dtype=BF, device="cuda")
+    x, rows, q, k, v = new(n, L + rot), new(n, L + rot), new(count, H, D + rot), new(n, H, D), new(n, H, D)
+    kv.append(x, weight, pos, freq, slots, layout="half")
+    kv.gather(rows, table, ints([n]), ints([0, n]))
+    raw = q.clone()
+    h.rope(q[..., D:], q[..., D:], pos[n - count:].clone(), freq)
+    qa = new(count, H, L + rot)
+    oa, op = [torch.empty(R, count, H, w, dtype=BF, device="cuda") for w in (L, D)]
+    kv.attention(qa, oa, table, ints([n]), ints([0, count]), max_q=count, scale=0.07)
+    kv.prompt(q, k, v, rows[..., L:], op, ints([0, count]), ints([0, n]), max_q=count, scale=0.09)
+    torch.cuda.synchronize()
+    fine(kv)
+    seen = ref.causal(count, n, "cuda")
+    for r in range(R):
+        want, off = ref.append(x[r], weight, pos, freq, "half", 1.0, 1e-6, L)
+        ref.check(rows[r], want, off * 1.01 + want.abs() * ref.HALF[BF], "append")
+        want, off = ref.rope(raw[r, ..., D:], pos[n - count:], freq, "half", 1.0)
+        ref.check(q[r, ..., D:], want, off * 1.01 + want.abs() * ref.HALF[BF], "rope")
+        for i in range(H):
+            ref.check(oa[r, :, i], *ref.rows(qa[r, :, i], rows[r], rows[r, :, :L], seen, 0.07), f"absorbed {r} {i}")
+            ref.check(op[r, :, i], *ref.rows(q[r, :, i], torch.cat([k[r, :, i], rows[r, :, L:]], -1), v[r, :, i], seen, 0.09), f"expanded {r} {i}")
+    kv.close()
+    h.close()
+
+
+def test_requests_that_share_pages():
+    """Two requests with the same first pages, and one whose table names a page twice."""
+    L, rot, P, H = 256, 64, 32, 3
+    cache = torch.randn(1, 6, P, L + rot, generator=gen(1), device="cuda").to(BF)
+    table, lens = [[3, 0, 1, -1], [3, 0, 5, 2], [4, 4, 3, -1]], [70, 128, 96]
+    kv = sfar.SfarLatent(cache, q_heads=H, rope_dim=rot)
+    q = torch.randn(1, 3, H, L + rot, generator=gen(2), device="cuda").to(BF)
+    out = torch.empty(1, 3, H, L, dtype=BF, device="cuda")
+    rows = torch.empty(1, sum(lens), L + rot, dtype=BF, device="cuda")
+    kv.attention(q, out, ints(table), ints(lens), ints([0, 1, 2, 3]), max_q=1, scale=0.07)
+    kv.gather(rows, ints(table), ints(lens), ints(ref.offsets(lens)))
+    torch.cuda.synchronize()
+    fine(kv)
+    for b, n in enumerate(lens):
+        held = ref.held_rows(cache[0], table[b], n, P)
+        assert torch.equal(rows[0, ref.offsets(lens)[b]:][:n], held)
+        ref.check(out[0, b], *ref.rows(q[0, b], held, held[:, :L], torch.ones(H, n, dtype=torch.bool, device="cuda"), 0.07), f"request {b}")
+    kv.close()
+
+
+def test_captured_prompts_replay_with_new_lengths():
+    """A prompt's step captured once: row tiles that are cut, whole ones, none at all, and rows of padding."""
+    H, D, rot, T, S, B = 5, 128, 64, 700, 2200, 3
+    g = gen(3)
+    q, k, v, kr = [torch.randn(s, generator=g, device="cuda").to(BF) for s in ((1, T, H, D + rot), (1, S, H, D), (1, S, H, D), (1, S, rot))]
+    out, starts, ks = torch.empty(1, T, H, D, dtype=BF, device="cuda"), ints([0] * (B + 1)), ints([0] * (B + 1))
+    kv = sfar.SfarLatent(torch.zeros(1, 1, 16, 256 + rot, dtype=BF, device="cuda"), q_heads=H, rope_dim=rot)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kv.prompt(q, k, v, kr, out, starts, ks, max_q=T, scale=0.09)
+    for lens, count in (([2000, 0, 1], [3, 0, 1]), ([700, 700, 700], [400, 100, 200]), ([0, 0, 0], [0, 0, 0]), ([5, 9, 2100], [5, 0, 300]), ([2200, 0, 0], [1, 0, 0])):
+        starts.copy_(ints(ref.offsets(count)))
+        ks.copy_(ints(ref.offsets(lens)))
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        fine(kv)
+        first = out.clone()
+        for b, n in enumerate(lens):
+            a, z, s = ref.offsets(count)[b], ref.offsets(count)[b + 1], slice(ref.offsets(lens)[b], ref.offsets(lens)[b + 1])
+            for h in range(H if z > a else 0):
+                want, off = ref.rows(q[0, a:z, h], torch.cat([k[0, s, h], kr[0, s]], -1), v[0, s, h], ref.causal(z - a, n, "cuda"), 0.09)
+                ref.check(out[0, a:z, h], want, off, f"{lens} {count} request {b} head {h}")
+        assert (out[:, sum(count):] == 0).all()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+    kv.close()
