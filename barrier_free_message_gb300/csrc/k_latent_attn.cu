@@ -158,12 +158,19 @@ __device__ __forceinline__ void store_transposed(uint32_t addr, uint32_t a, uint
 // whether one of the two bf16 is an infinity or NaN
 __device__ __forceinline__ bool odd2(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
 
+// the larger one, NaN if one is
+__device__ __forceinline__ float at_least(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 // What a row's accumulator is multiplied by: 0 if it attends to nothing, NaN if all its scores are -inf.
 __device__ __forceinline__ float factor(float ref, float sum) { return ref == kLeast ? NAN : sum == 0.f ? 0.f : 1.f / sum; }
 
 // The rows whose accumulator holds an infinity or NaN, by the softmax threads: NaN for their sums, and for their results if
-// these have been written.
-template <int L, int NR> __device__ __noinline__ void odd_rows(uint32_t tO, int rows, float *sum, uint16_t *const *out)
+// these have been written.  Puts the flag that brought them here back.
+template <int L, int NR> __device__ __noinline__ void odd_rows(uint32_t tO, int rows, float *sum, uint16_t *const *out, int *flag)
 {
     for (int again = 0; again < (out ? 2 : 1); ++again) {
         for (int n0 = 0; n0 < rows; n0 += 8)
@@ -181,6 +188,8 @@ template <int L, int NR> __device__ __noinline__ void odd_rows(uint32_t tO, int 
                     }
             }
         soft_sync();
+        if (threadIdx.x == 0)
+            *flag = 0;                             // all have read it; set no sooner than after another barrier
     }
 }
 
@@ -272,7 +281,7 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
     __shared__ uint32_t upto[SFAR_KV_MAX_REQUESTS / kGroup + 1];
     __shared__ Request s_kept[kKept];
     __shared__ uint32_t s_warp[kThreads / 32], s_tmem;
-    __shared__ int s_hi[NR], s_last;
+    __shared__ int s_hi[NR], s_last, s_odd;
     __shared__ float s_max[kSoft][NR], s_sum[NR], s_ref[NR], s_keep[NR], s_inv[NR], s_w[kParts][NR], s_m[kParts][NR];
     __shared__ uint16_t *s_out[NR];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -292,6 +301,7 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
         tc::bar_fence_init();
         tc::fence_async();
         upto[0] = 0;
+        s_odd = 0;
     }
     if (warp == kMmaWarp)
         tc::tmem_alloc<1>(tc::smem(&s_tmem), Y::kCols);
@@ -454,10 +464,7 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 float &v = x[4 * i + 2 * h + y];
-                                if (!there[h] || j + 8 * h >= hi)
-                                    v = -INFINITY;
-                                else if (v == -INFINITY)
-                                    v = kLeast;
+                                v = !there[h] || j + 8 * h >= hi ? -INFINITY : at_least(v, kLeast);
                             }
                         }
                 }
@@ -465,7 +472,7 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                 for (int i = 0; i < kI; ++i)
 #pragma unroll
                     for (int y = 0; y < 2; ++y)
-                        move = move || fmaxf(fmaxf(x[4 * i + y], x[4 * i + 2 + y]), least) - ref[2 * i + y] > kAttnLift;
+                        move |= fmaxf(fmaxf(x[4 * i + y], x[4 * i + 2 + y]), least) - ref[2 * i + y] > kAttnLift;
                 if (soft_any(move)) {
 #pragma unroll
                     for (int i = 0; i < kI; ++i)
@@ -564,7 +571,7 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
             }
             // A row that attends to a latent that is not finite is NaN.  Where the token's weight is 0, only the accumulator's
             // element says so.
-            float odd[Y::kBlocks] = {};            // NaN: some element is not finite
+            uint64_t odd[Y::kBlocks] = {};         // NaN: some element is not finite, maybe of a row past the request's
             // The accumulator, element tid of each 128 of the latent, a row at a time.  begin(n): what is read once for a row.
             auto each = [&](auto begin, auto what) {
 #pragma unroll 1
@@ -588,22 +595,30 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                             tc::wait_ld(o[c]);
                     }
 #pragma unroll
+                    for (int n = 0; n < 8; n += 2)
+#pragma unroll
+                        for (int c = 0; c < Y::kBlocks; ++c)
+                            odd[c] = tc::fma2(tc::pack2u(o[c][n], o[c][n + 1]), 0ull, odd[c]);
+#pragma unroll
                     for (int n = 0; n < 8; ++n)
                         if (n0 + n < rows) {
 #pragma unroll
                             for (int c = 0; c < Y::kBlocks; ++c) {
-                                odd[c] = fmaf(__uint_as_float(o[c][n]), 0.f, odd[c]);
                                 what(of[n], n0 + n, c * 128 + tid, __uint_as_float(o[c][n]));
                             }
                         }
                 }
             };
+            // a barrier, too (a flag in shared memory beside one takes less than a vote)
             auto any_odd = [&] {
                 float all = 0.f;
 #pragma unroll
                 for (int c = 0; c < Y::kBlocks; ++c)
-                    all += odd[c];
-                return soft_any(all != 0.f);
+                    all += tc::unpack2(odd[c]).x + tc::unpack2(odd[c]).y;
+                if (all != 0.f)
+                    s_odd = 1;
+                soft_sync();
+                return s_odd != 0;
             };
             if (p.tiles == p.all) {
                 struct Row {
@@ -613,7 +628,7 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                 each([&](int n) { return Row{s_out[n], s_inv[n]}; },
                      [&](const Row &r, int, int d, float v) { r.out[d] = (uint16_t)tc::bf16x2(v * r.by, 0.f); });
                 if (any_odd())                     // the tables in shared memory have been read
-                    odd_rows<L, NR>(tO, rows, s_sum, s_out);
+                    odd_rows<L, NR>(tO, rows, s_sum, s_out, &s_odd);
             } else {
                 // a part: leave it in the workspace, for the last of the row tile's CTAs
                 const long long from = p.at - p.tile0, to = from + p.all;
@@ -628,7 +643,7 @@ template <int L, int NR> __global__ void __launch_bounds__(kThreads, 1) k_latent
                 };
                 leave();
                 if (any_odd()) {
-                    odd_rows<L, NR>(tO, rows, s_sum, nullptr);
+                    odd_rows<L, NR>(tO, rows, s_sum, nullptr, &s_odd);
                     leave();
                     soft_sync();
                 }
