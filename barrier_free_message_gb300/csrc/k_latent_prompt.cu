@@ -97,6 +97,10 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w)
 {
     return w & ((w & 0x7f80u) == 0x7f80u ? 0xffff0000u : ~0u) & ((w & 0x7f800000u) == 0x7f800000u ? 0xffffu : ~0u);
 }
+// What a row's scores are multiplied by in its weights 2^(f s - ref), taken with one rounding, that of ref: all of the row's have
+// it in common, but beyond 2^32 it moves them out of binary32.  There f s is shrunk to 2^30, where it moves them by 2^64 and
+// neighbouring numbers are 64 apart, so that the largest score has all the weight, as it has in full size.
+__device__ __forceinline__ float row_factor(float ref, float f) { return fabsf(ref) > 0x1p30f ? f * (0x1p30f / fabsf(ref)) : f; }
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float r;
@@ -388,7 +392,6 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
         };
         // never 0, so that a masked score of -inf stays that
         const float f = fmaxf(a.scale * 1.4426950408889634f, 1e-37f);
-        const uint64_t f2 = tc::pack2(f, f);
         tc::Ring<kPieces> ps;
         uint32_t sphase = 0, ophase = 0;
         for (;;) {
@@ -405,6 +408,8 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
             const int hi = (row ? pos + 1 : INT_MAX) - 64 * half;                   // of this thread's columns
             const int mine_to = p.len - p.count + p.rt * kRows + x * 128 + (warp & 3) * 32 + 1 - 64 * half;   // every row of this warp
             float ref = -INFINITY, sum = 0.f;      // of the row; of this half
+            // Weights are 2^(by_score s - less).  A row that has seen nothing, or scores of -inf alone: any finite numbers, weights 0.
+            float by_score = f, less = 0.f;
             const int steps = p.steps[x];
             for (int k = 0; k < steps; ++k) {
                 const int j0 = (p.from + k) * kTile;
@@ -433,11 +438,15 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                     for (int e = 3; e < 31; e += 2)
                         m[c] = max3(m[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
                 }
-                float now = fmaxf(max3(m[0], m[1], __uint_as_float(s[0][31])), __uint_as_float(s[1][31])) * f;
-                if (pair_any(pair, now - ref > kAttnLift)) {
+                float now = fmaxf(max3(m[0], m[1], __uint_as_float(s[0][31])), __uint_as_float(s[1][31]));
+                if (pair_any(pair, now * f - ref > kAttnLift)) {
                     now = fmaxf(now, swap(now));
-                    const float next = now - ref > kAttnLift ? now : ref;
+                    const float next = now * f - ref > kAttnLift ? now * f : ref;
                     const float keep = ref == -INFINITY ? 1.f : ex2(ref - next);           // all is 0 then, or NaN
+                    if (next != ref) {
+                        by_score = row_factor(next, f);
+                        less = now * by_score;
+                    }
                     ref = next;
                     sum *= keep;
                     if (k) {
@@ -456,9 +465,7 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                     tc::fence_before();
                     pair_sync(pair);               // the other's has been read
                 }
-                // a row that has seen nothing, or scores of -inf alone: any finite reference, weights 0
-                const float base = ref == -INFINITY ? 0.f : ref;
-                const uint64_t b2 = tc::pack2(-base, -base);
+                const uint64_t f2 = tc::pack2(by_score, by_score), b2 = tc::pack2(-less, -less);
                 uint64_t part = 0;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {

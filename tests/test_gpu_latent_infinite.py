@@ -198,3 +198,47 @@ def test_expanded_infinite_values(lens, count, H, D, rot):
             if at:
                 rest[0, max(0, first - 1):m, h, 3] = False
             assert torch.equal(got[rest], before[rest]), (at, max_q)
+
+
+# ------------------------------------------------------------- scores far from 0
+def far_scores(n, power):
+    """Multiples of 2^power, the largest at one place: numbers of 8 bits, exact in bf16, for keys; times the like for a query."""
+    order = torch.randperm(n, generator=torch.Generator().manual_seed(n + power)).cuda() % 200
+    order[n // 3] = 201
+    return (order + 32).double() * 2.0 ** (power // 2), 2.0 ** (power - power // 2)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("power", [20, 32, 40, 60, 100])
+@pytest.mark.parametrize("n", [1, 5, 64, 200, 1500, 5000])
+def test_scores_far_from_zero(n, power, sign):
+    """Both forms, scores up to 2^108: weights stay in their range, and beyond 2^32 the largest score has them all."""
+    H, D, L, rot, P = 2, 64, 256, 32, 32
+    at, times = far_scores(n, power)
+    if sign < 0:
+        at, times = at.flip(0), -times
+    clean, table = cached(1, L, rot, P, [n], seed=n)
+    rows = ref.held_rows(clean[0], table[0], n, P).clone()
+    rows[:, L + 1] = at.to(BF)
+    cache = clean.clone()
+    for i in range(n):
+        cache[0, place(table[0], P, i)[0], place(table[0], P, i)[1], L + 1] = rows[i, L + 1]
+    q = torch.randn(1, 1, H, L + rot, generator=torch.Generator("cuda").manual_seed(4), device="cuda").to(BF)
+    q[..., L + 1] = times
+    best = torch.nonzero(at == (at.max() if sign > 0 else at.min())).flatten()
+    got, _, _ = attend(cache, table, [n], [1], H, rot, q=q)
+    if len(best) == 1 and (power > 30 or n == 1):           # steps of 2^power * 0.07 in the exponent
+        assert torch.equal(got[0, 0], rows[best[0], :L].expand(H, L))
+    assert torch.isfinite(got).all()
+    count = min(n, 3)
+    x = prompt_of(H, D, rot, [n], [count], seed=n + 5)
+    x[3][0, :, 1] = at.to(BF)
+    x[0][..., D + 1] = times
+    for max_q in (count, 1000):
+        out = x[4](*x[:4], max_q)
+        assert torch.isfinite(out).all()
+        for i in range(count if power > 30 else 0):
+            seen = at[:n - count + 1 + i]
+            best = torch.nonzero(seen == (seen.max() if sign > 0 else seen.min())).flatten()
+            if len(best) == 1:
+                assert torch.equal(out[0, i], x[2][0, best[0]]), (i, max_q)
