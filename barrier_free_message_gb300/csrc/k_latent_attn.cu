@@ -18,7 +18,8 @@
 // (a thread 2 tokens of a quarter of the rows).  A row's reference
 // moves only when a score passes it by 2^7.9 (a vote of the CTA's softmax
 // threads, no maxima otherwise), and the accumulator is rescaled in tensor
-// memory only then.  Weights go to shared memory as bf16, the type that an
+// memory only then.  What a row does not attend to is masked by its place: a
+// score of -inf is not that.  Weights go to shared memory as bf16, the type that an
 // MMA with these values takes; sums are of the unrounded ones.
 //
 // Shared memory holds two tiles and more: a ring of pairs of 64-element boxes
@@ -35,7 +36,7 @@
 //
 // Measured, latent 512, key 64: 8 ranks, 32 requests of 301 to 6100 tokens, 20
 // heads: 964 MB in 165 us, 5.8 TB/s or 0.86 of a copy's rate; 64 requests of 2000,
-// 16 heads: 6.1 TB/s; 131071 tokens, 4 ranks, 20 rows: 604 MB in 116 us, 10 of
+// 16 heads: 6.0 TB/s; 131071 tokens, 4 ranks, 20 rows: 604 MB in 117 us, 10 of
 // them before the first tile and in joins.  Per tile at 32 rows 3400 clocks:
 // 1300 of scores, 1260 of softmax and handing over, 600 of products (shared
 // memory's rate: both read the whole tile), against 3130 that its bytes take

@@ -10,30 +10,35 @@
 // A CTA takes 256 rows as two tiles, so that while one tile's softmax works
 // the tensor core has the other's products; keys and values are then read once
 // for both.  Two threads own a row, half of its columns each: 16 softmax
-// warps keep their scores in registers, and speak to one another only when a
-// reference moves (kAttnLift) and at the end (one thread to a row, 8 warps:
-// 431 us where this takes 362).  Weights go back to tensor memory as bf16, in
-// the place of the scores; the accumulator is rescaled, there, only when a
-// row's reference moves.
+// warps keep their scores in registers.  The two warps of 32 rows vote at every
+// tile, by a barrier of their own and before any exponential, whether a
+// reference moves (kAttnLift), tell each other maxima if one does and sums at
+// the end (one thread to a row, 8 warps: 431 us where this took 362).  Weights
+// go back to tensor memory as bf16, in the place of the scores; the accumulator
+// is rescaled, there, only when a row's reference moves.
 //
 // Keys (three boxes of 64 elements x 128 tokens, 16 KB) and values (two) pass
 // through one ring of 8 boxes in the order of their use; a box is given back
 // by the last product that reads it.  Values that some rows of the piece do not
-// see are looked at by two warps of their own, in the time of the softmax.
+// see are looked at by two warps of their own, in the time of the softmax:
+// infinities and NaN become zeros for the products, and the rows that do see
+// them add them to their results.
 //
-// Work: row tiles are taken from a counter, one (rank, head)'s row tiles
-// after another, the longest first: they share keys and values in L2.  Fewer
-// than CTAs are cut along the context and joined, in the parts' order.
+// Work: row tiles are taken from a counter, one (rank, head) of a request after
+// another, of its row tiles the one with the longest context first: they share
+// keys and values in L2.  Fewer than CTAs are cut along the context and joined,
+// in the parts' order.
 // Warps 0-7, 8-15: the tiles' softmax; then copies and pieces, the MMAs, and two
 // that look at values.
 //
 // Measured: 8 ranks, 12 heads, 3 prompts of 0.7 to 1 thousand tokens over
-// contexts of 1.1 to 4.1 thousand, D = 128, rope = 64: 362 to 371 us, 1110 to
-// 1140 TFLOP/s of visible pairs, 0.6 of the measured rate; tensor pipes active
-// 53%.  What bounds it is a tile's chain, scores -> softmax -> product, of which
+// contexts of 1.1 to 4.1 thousand, D = 128, rope = 64: 371 to 378 us, 1090 to
+// 1110 TFLOP/s of visible pairs, 0.58 of the measured rate; tensor pipes active
+// 52%.  With two tiles the last four warps' 64 registers do not hold all that
+// they need: 216 bytes of stack a thread (232 with D = 64), none with one tile.  What bounds it is a tile's chain, scores -> softmax -> product, of which
 // two run beside one another (tensor memory holds no third), while shared
 // memory gives a product of 128 x 128 its operands in just the 64 clocks that
-// it takes.  Not L2: with half the bytes of keys and values it takes 2% less.
+// it takes.  Not L2: with half the bytes of keys and values it took 2% less.
 // Slower: weights handed over in two halves, so that the second product starts
 // earlier (378 us); loops of products not unrolled (513); copies announced to L2
 // ahead (418).

@@ -462,8 +462,8 @@ sfar_status sfar_latent_attention(sfar_latent_t *h, const void *const q[], void 
     a.pages = (int)h->pages;
     a.rope = h->rope;
     // As few rows as hold a request's: their products and softmax are what a tile costs beside its bytes (64 requests of 2000
-    // tokens, 16 heads, 8 ranks: 192 us with 16 rows, 198 with 32, 259 with 64; 300 of 60 tokens 64, 75 and 95; 32 of 3000, 32
-    // heads: 150 with 32, 194 with 64).
+    // tokens, 16 heads, 8 ranks: 200 us with 16 rows, 204 with 32, 258 with 64; 300 of 60 tokens 67, 75 and 101; 32 of 3000, 32
+    // heads: 159 with 32, 197 with 64; 16 of 2000, 40 heads: 113 and 85).
     const int rows = max_q <= 16 / H ? 16 : max_q <= 32 / H ? 32 : 64;
     // the kernel's sums over the line of (row tile, tile) are of 32 bits, its row numbers of 31
     const size_t context = table_width << h->shift, reach = context < (1ull << 31) ? context : 1ull << 31;
