@@ -35,7 +35,8 @@
 // contexts of 1.1 to 4.1 thousand, D = 128, rope = 64: 371 to 378 us, 1090 to
 // 1110 TFLOP/s of visible pairs, 0.58 of the measured rate; tensor pipes active
 // 52%.  With two tiles the last four warps' 64 registers do not hold all that
-// they need: 216 bytes of stack a thread (232 with D = 64), none with one tile.  What bounds it is a tile's chain, scores -> softmax -> product, of which
+// they need: 216 bytes of stack a thread (232 with D = 64), none with one tile.
+// What bounds it is a tile's chain, scores -> softmax -> product, of which
 // two run beside one another (tensor memory holds no third), while shared
 // memory gives a product of 128 x 128 its operands in just the 64 clocks that
 // it takes.  Not L2: with half the bytes of keys and values it took 2% less.
@@ -102,10 +103,10 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w)
 {
     return w & ((w & 0x7f80u) == 0x7f80u ? 0xffff0000u : ~0u) & ((w & 0x7f800000u) == 0x7f800000u ? 0xffffu : ~0u);
 }
-// What a row's scores are multiplied by in its weights 2^(f s - ref), taken with one rounding, that of ref: all of the row's have
-// it in common, but beyond 2^32 it moves them out of binary32.  There f s is shrunk to 2^30, where it moves them by 2^64 and
-// neighbouring numbers are 64 apart, so that the largest score has all the weight, as it has in full size.
-__device__ __forceinline__ float row_factor(float ref, float f) { return fabsf(ref) > 0x1p30f ? f * (0x1p30f / fabsf(ref)) : f; }
+// What a row's scores are multiplied by in its weights 2^(f s - ref), taken with one rounding, that of ref = f top: all of the
+// row's have it in common, but beyond 2^32 it moves them out of binary32.  There f top is shrunk to 2^30, where it moves them by
+// 2^64 and neighbouring numbers are 64 apart, so that the largest score has all the weight, as it has in full size.
+__device__ __forceinline__ float row_factor(float top, float f) { return fabsf(top) * f > 0x1p30f ? 0x1p30f / fabsf(top) : f; }
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float r;
@@ -449,8 +450,8 @@ __global__ void __launch_bounds__(Lay<D, TILES>::kThreads, 1) k_latent_prompt(co
                     const float next = now * f - ref > kAttnLift ? now * f : ref;
                     const float keep = ref == -INFINITY ? 1.f : ex2(ref - next);           // all is 0 then, or NaN
                     if (next != ref) {
-                        by_score = row_factor(next, f);
-                        less = now * by_score;
+                        by_score = row_factor(now, f);
+                        less = now * by_score + (next - next);                             // NaN for a score of +inf
                     }
                     ref = next;
                     sum *= keep;

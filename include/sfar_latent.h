@@ -99,11 +99,11 @@ sfar_status sfar_latent_gather(sfar_latent_t *h, void *const out[], const int32_
  * the products' sums are binary32, a weight is rounded to bf16 (8 bits,
  * relative to itself) before the second product.  A row's result does not
  * depend on what the other rows hold, nor on tokens it does not see.
- * Infinities: a token whose score is -inf has weight 0; a row that attends to
- * tokens and has no other scores, or a score of +inf or NaN, is NaN (so is a
- * row with an infinity or NaN among its queries, whatever the signs), and so is
- * one that attends to a latent that is not finite (or whose sum of weights, up
- * to 2^7.9 each, times latents passes binary32).
+ * Infinities (a score that passes binary32 is one): a token whose score is -inf
+ * has weight 0; a row that attends to tokens and has no other scores, or a score
+ * of +inf or NaN, is NaN (so is a row with an infinity or NaN among its queries,
+ * whatever the signs), and so is one that attends to a latent that is not finite
+ * (or whose sum of weights, up to 2^7.9 each, times latents passes binary32).
  * max_q: the most new tokens any request has in this call (a hint that picks
  * the kernel; a request that has more is still computed).  out overlaps no
  * other argument nor the caches, no row of it another, and the ranks' arrays

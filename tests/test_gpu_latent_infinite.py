@@ -242,3 +242,35 @@ def test_scores_far_from_zero(n, power, sign):
             best = torch.nonzero(seen == (seen.max() if sign > 0 else seen.min())).flatten()
             if len(best) == 1:
                 assert torch.equal(out[0, i], x[2][0, best[0]]), (i, max_q)
+
+
+@pytest.mark.parametrize("n", [1, 100, 200, 1500])
+def test_scores_past_binary32(n):
+    """Products that are finite, scores that pass binary32 once scaled: +inf, so NaN, or -inf, weight 0; alike in both forms."""
+    D, L, rot = 64, 256, 32
+    clean, table = cached(1, L, rot, 32, [n], seed=n)
+    q = torch.randn(1, 1, 2, L + rot, generator=torch.Generator("cuda").manual_seed(5), device="cuda").to(BF)
+    q[0, 0, 0, L + 1], q[0, 0, 1, L + 1] = 2.0 ** 63, -(2.0 ** 63)
+    for at in {0, n // 2, n - 1}:
+        cache = clean.clone()
+        cache[..., L + 1] = 0
+        cache[0, place(table[0], 32, at)[0], place(table[0], 32, at)[1], L + 1] = 2.0 ** 63
+        out = torch.empty(1, 1, 2, L, dtype=BF, device="cuda")
+        kv = sfar.SfarLatent(cache, q_heads=2, rope_dim=rot)
+        rows = ref.held_rows(cache[0], table[0], n, 32)
+        kv.attention(q, out, ints(table), ints([n]), ints([0, 1]), max_q=1, scale=8.0)
+        k, v = rows[:, None, :D].expand(n, 2, D).contiguous()[None], rows[:, None, D:2 * D].expand(n, 2, D).contiguous()[None]
+        qp, op = torch.cat([q[..., :D], q[..., L:]], -1).contiguous(), torch.empty(1, 1, 2, D, dtype=BF, device="cuda")
+        kv.prompt(qp, k, v, rows[None, :, L:].contiguous(), op, ints([0, 1]), ints([0, n]), max_q=1, scale=8.0)
+        torch.cuda.synchronize()
+        assert torch.isnan(out[0, 0, 0]).all() and torch.isnan(op[0, 0, 0]).all(), at
+        if n == 1:
+            assert torch.isnan(out[0, 0, 1]).all() and torch.isnan(op[0, 0, 1]).all()
+        else:
+            rows = rows.clone()
+            rows[at, L + 1] = 0
+            want, off = without(q[0, 0, 1:], rows, rows[:, :L], [at], 8.0)
+            ref.check(out[0, 0, 1:], want, off, f"absorbed without {at}")
+            want, off = without(qp[0, 0, 1:], torch.cat([rows[:, :D], rows[:, L:]], -1), rows[:, D:2 * D], [at], 8.0)
+            ref.check(op[0, 0, 1:], want, off, f"expanded without {at}")
+        kv.close()
